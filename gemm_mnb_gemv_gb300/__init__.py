@@ -12,6 +12,8 @@ The names match the C entry points: ``mnb_dequant``, ``mnb_repacked_bytes``,
 ``mnb_dequant_gidx``,
 ``mnb_act_order_plan``, ``mnb_act_order_prepare``, ``mnb_act_order_gather``,
 ``mnb_act_order_workspace_bytes``, ``mnb_gemm_act_order``, ``mnb_gemm_act_order_noalloc``,
+``mnb_kv4_cache_bytes``, ``mnb_kv4_append``, ``mnb_kv4_read``, ``mnb_kv4_attention_workspace_bytes``,
+``mnb_kv4_attention`` (with ``MnbKv4Cache``, the handle of a cache, and ``mnb_kv4_cache_alloc``),
 ``mnb_set_programmatic_launch``,
 ``mnb_check_device_status``,
 ``mnb_last_error``,
@@ -44,6 +46,16 @@ class MnbWeight(ctypes.Structure):
                 ("scales_dtype", ctypes.c_int32), ("zero_points", ctypes.c_void_p)]
 
 
+class MnbKv4CacheArg(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("group_size", ctypes.c_int32)]
+
+
+class MnbRope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -56,7 +68,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is missing: build it with `python -m gemm_mnb_gemv_gb300._build` "
                           "(there is no fallback implementation)")
     lib = ctypes.CDLL(path)
-    c_int, c_size, vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    c_int, c_size, vp, i64 = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64
     sigs = {
         "mnb_dequant": (c_int, [MnbWeight, c_int, c_int, c_int, vp, vp]),
         "mnb_repacked_bytes": (c_size, [c_int, c_int, c_int]),
@@ -77,6 +89,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                        c_size, vp, vp]),
         "mnb_gemm_act_order_noalloc": (c_int, [vp, c_int, MnbWeight, vp, vp, c_int, c_int, c_int, c_int, vp,
                                                c_int, vp, vp]),
+        "mnb_kv4_cache_bytes": (c_size, [c_int, c_int, c_int, c_int, c_int]),
+        "mnb_kv4_append": (c_int, [vp, vp, vp, c_int, c_int, c_int, i64, i64, i64, vp, MnbRope, vp, MnbKv4CacheArg,
+                                   vp, vp]),
+        "mnb_kv4_read": (c_int, [MnbKv4CacheArg, vp, c_int, c_int, vp, vp, vp]),
+        "mnb_kv4_attention_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int, c_int, c_int]),
+        "mnb_kv4_attention": (c_int, [vp, c_int, c_int, c_int, i64, MnbKv4CacheArg, vp, vp, vp, c_int, c_int,
+                                      ctypes.c_float, c_int, c_int, vp, c_size, vp, vp, vp]),
         "mnb_set_programmatic_launch": (None, [c_int]),
         "mnb_check_device_status": (c_int, []),
         "mnb_selftest_wait_timeout": (c_int, [ctypes.c_uint, vp]),
@@ -431,4 +450,171 @@ def mnb_gemm_act_order_noalloc(A, packed, scales, zero_points, perm, K: int, K_p
     _check_dev("out", out, torch.float16)
     _raise(lib.mnb_gemm_act_order_noalloc(_ptr(A), M, w, _ptr(repacked), _ptr(perm), K, K_prepared, N,
                                           block_size, _ptr(bias), bias_mode, _ptr(out), _stream_handle(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Paged 4-bit key/value cache and attention
+# ---------------------------------------------------------------------------
+
+
+def mnb_kv4_cache_bytes(num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int) -> int:
+    return int(load_library().mnb_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim, group_size))
+
+
+class MnbKv4Cache:
+    """Handle of a paged 4-bit key/value cache: ``pages`` is uint8 ``[num_pages, kv_heads, record bytes]``."""
+
+    def __init__(self, pages, page_size: int, head_dim: int, group_size: int):
+        torch = _torch()
+        _check_dev("pages", pages, torch.uint8)
+        if pages.dim() != 3:
+            raise ValueError("pages must be [num_pages, kv_heads, record bytes]")
+        num_pages, kv_heads, record = pages.shape
+        need = mnb_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim, group_size)
+        if need == 0:
+            raise MnbError(MNB_ERR_INVALID_ARG, f"MnbKv4Cache: num_pages={num_pages} page_size={page_size} "
+                           f"kv_heads={kv_heads} head_dim={head_dim} group_size={group_size}")
+        if need != num_pages * kv_heads * record:
+            raise ValueError(f"pages has records of {record} bytes, {need // (num_pages * kv_heads)} needed")
+        self.pages, self.page_size, self.head_dim, self.group_size = pages, page_size, head_dim, group_size
+        self.num_pages, self.kv_heads = num_pages, kv_heads
+        self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
+
+
+def mnb_kv4_cache_alloc(num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int,
+                        device="cuda") -> MnbKv4Cache:
+    """A new cache, zeroed (every element reads as 0)."""
+    nbytes = mnb_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim, group_size)
+    if nbytes == 0:
+        raise MnbError(MNB_ERR_INVALID_ARG, f"mnb_kv4_cache_alloc: num_pages={num_pages} page_size={page_size} "
+                       f"kv_heads={kv_heads} head_dim={head_dim} group_size={group_size}")
+    torch = _torch()
+    pages = torch.zeros((num_pages, kv_heads, nbytes // (num_pages * kv_heads)), dtype=torch.uint8, device=device)
+    return MnbKv4Cache(pages, page_size, head_dim, group_size)
+
+
+def _act_dtype(name, t):
+    torch = _torch()
+    if t.dtype == torch.float16:
+        return MNB_F16
+    if t.dtype == torch.float32:
+        return MNB_F32
+    raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
+
+
+def _token_rows(name, t, heads, D, dtype):
+    """Elements between the tokens of ``[T, heads, D]``, whose heads must lie one after the other."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
+        raise ValueError(f"{name}: the heads of a token must lie one after the other")
+    return s0 if t.shape[0] > 1 else heads * D
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor of ``stream``'s own pool (the current stream's when None), so that it outlives the kernels on it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _index(name, t, dtype, shape):
+    _check_dev(name, t, dtype)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=None, sin=None,
+                   interleaved: bool = False, q_out=None, stream=None):
+    """Rotates, quantises and stores ``k`` and ``v`` (``[T, kv_heads, head_dim]``) at ``slots``; returns the rotated
+    ``q`` (or None).  ``cos`` and ``sin`` are fp32 ``[rows, rot_dim / 2]``, None for no rotation."""
+    torch = _torch()
+    dtype = k.dtype
+    dt, T, Hk, D = _act_dtype("k", k), k.shape[0], cache.kv_heads, cache.head_dim
+    ks, vs = _token_rows("k", k, Hk, D, dtype), _token_rows("v", v, Hk, D, dtype)
+    if v.shape[0] != T:
+        raise ValueError(f"v has {v.shape[0]} tokens, k has {T}")
+    qs = Hq = 0
+    qp = op = None
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError(f"q must be [{T}, q_heads, {D}], got {list(q.shape)}")
+        Hq = q.shape[1]
+        qs = _token_rows("q", q, Hq, D, dtype)
+        if q_out is None:
+            q_out = _new((T, Hq, D), dtype, q.device, stream)
+        qp, op = q.data_ptr(), _index("q_out", q_out, dtype, (T, Hq, D))
+    rope = MnbRope(None, None, 0, 0, 0)
+    pp = None
+    if cos is not None:
+        rows, half = cos.shape
+        rope = MnbRope(_index("cos", cos, torch.float32, (rows, half)), _index("sin", sin, torch.float32, (rows, half)),
+                       rows, 2 * half, 1 if interleaved else 0)
+        pp = _index("positions", positions, torch.int32, (T,))
+    sp = _index("slots", slots, torch.int64, (T,))
+    _raise(load_library().mnb_kv4_append(qp, k.data_ptr(), v.data_ptr(), dt, T, Hq, qs, ks, vs, pp, rope, sp, cache.arg,
+                                         op, _stream_handle(stream)))
+    return q_out
+
+
+def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, stream=None):
+    """``(k, v)``, ``[T, kv_heads, head_dim]`` of ``dtype`` (float16 by default): what ``slots`` hold."""
+    torch = _torch()
+    T = slots.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else torch.float16
+    if k_out is None:
+        k_out = _new(shape, dtype, slots.device, stream)
+    if v_out is None:
+        v_out = _new(shape, dtype, slots.device, stream)
+    kp, vp = _index("k_out", k_out, dtype, shape), _index("v_out", v_out, dtype, shape)
+    _raise(load_library().mnb_kv4_read(cache.arg, _index("slots", slots, torch.int64, (T,)), T,
+                                       _act_dtype("k_out", k_out), kp, vp, _stream_handle(stream)))
+    return k_out, v_out
+
+
+def mnb_kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                      dtype: int = MNB_F16) -> int:
+    return int(load_library().mnb_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, dtype))
+
+
+def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale: float, causal: bool = True,
+                      window: int = 0, workspace=None, out=None, lse=None, stream=None):
+    """``[T, q_heads, head_dim]``: attention of ``q`` over the cached keys of ``batch`` sequences.
+
+    ``q_start`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]``, ``page_table`` int32 ``[batch, pages]``.
+    """
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, q_heads, head_dim], got {list(q.shape)}")
+    T, Hq, D = q.shape
+    dtype, dt = q.dtype, _act_dtype("q", q)
+    qs = _token_rows("q", q, Hq, cache.head_dim, dtype)
+    B = kv_len.shape[0]
+    need = mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
+    if workspace is None and need > 0:
+        workspace = _new(need, torch.uint8, q.device, stream)
+    _check_dev("workspace", workspace)
+    if out is None:
+        out = _new((T, Hq, D), dtype, q.device, stream)
+    op = _index("out", out, dtype, (T, Hq, D))
+    lp = None if lse is None else _index("lse", lse, torch.float32, (T, Hq))
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [{B}, pages], got {list(page_table.shape)}")
+    stride = page_table.shape[1]
+    _raise(load_library().mnb_kv4_attention(
+        q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
+        _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
+        stride, scale, 1 if causal else 0, window, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), op, lp, _stream_handle(stream)))
     return out

@@ -149,7 +149,8 @@ mnb_status mnb_check_device_status(void) {
                 "2 = slot wait, 4 = tensor-core pipeline wait, 8 = index out of range); outputs of that "
                 "call are NaN", fn, v);
   return fail(MNB_ERR_INVALID_ARG, "%s: an index input was out of range (status bits 0x%x: a g_idx, perm "
-              "or block_group entry outside its range; that element was written as 0)", fn, v);
+              "or block_group entry outside its range; that element was written as 0; or a slot, position, page "
+              "or kv_len of a key/value cache call: see the call)", fn, v);
 }
 
 mnb_status mnb_selftest_wait_timeout(unsigned int limit_us, mnb_stream stream) {
@@ -630,6 +631,170 @@ mnb_status mnb_gemm_act_order_noalloc(const void* A, int M, mnb_weight w, const 
                         static_cast<uint8_t*>(scratch) + head, kNoAllocScratchBytes - head);
   }
   return finish(fn, e, ctx);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------
+// Paged 4-bit key/value cache and attention.
+// ------------------------------------------------------------------------------------
+
+namespace {
+
+bool kv4_geometry_ok(int num_pages, int page_size, int kv_heads, int head_dim, int group) {
+  return num_pages >= 1 && page_size >= 16 && page_size <= 4096 && page_size % 16 == 0 && kv_heads >= 1 &&
+         kv_heads <= 1024 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+         (group == 32 || group == 64 || group == 128) && group <= head_dim;
+}
+
+mnb_status check_kv4(const char* fn, const mnb_kv4_cache& c, mnb::Kv4Cache* out) {
+  if (!kv4_geometry_ok(c.num_pages, c.page_size, c.kv_heads, c.head_dim, c.group_size))
+    return fail(MNB_ERR_INVALID_ARG, "%s: cache of num_pages=%d page_size=%d kv_heads=%d head_dim=%d group_size=%d "
+                "(num_pages >= 1, page_size a multiple of 16 up to 4096, kv_heads 1..1024, head_dim 64, 128 or 256, "
+                "group_size 32, 64 or 128 up to head_dim)", fn, c.num_pages, c.page_size, c.kv_heads, c.head_dim,
+                c.group_size);
+  mnb_status st = check_ptr(fn, "pages", c.pages);
+  if (st != MNB_OK) return st;
+  *out = {c.pages, c.num_pages, c.page_size, c.kv_heads, c.head_dim, c.group_size};
+  return MNB_OK;
+}
+
+mnb_status check_dtype(const char* fn, int dtype) {
+  if (dtype == MNB_F16 || dtype == MNB_F32) return MNB_OK;
+  return fail(MNB_ERR_INVALID_ARG, "%s: dtype %d must be MNB_F16 or MNB_F32", fn, dtype);
+}
+
+mnb_status check_stride(const char* fn, const char* name, int64_t stride, int heads, int D, int dtype) {
+  const int64_t e = dtype == MNB_F16 ? 2 : 4;
+  if (stride < (int64_t)heads * D || stride > (int64_t)1 << 40)
+    return fail(MNB_ERR_INVALID_ARG, "%s: %s=%lld is below %d heads of %d elements", fn, name, (long long)stride,
+                heads, D);
+  if (stride * e % 16 != 0)
+    return fail(MNB_ERR_MISALIGNED, "%s: %s=%lld elements is not a multiple of 16 bytes", fn, name,
+                (long long)stride);
+  return MNB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mnb_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim, int group_size) {
+  if (!kv4_geometry_ok(num_pages, page_size, kv_heads, head_dim, group_size)) return 0;
+  const mnb::Kv4Cache c = {nullptr, num_pages, page_size, kv_heads, head_dim, group_size};
+  return (size_t)num_pages * kv_heads * (page_size / 16) * c.block_bytes();
+}
+
+mnb_status mnb_kv4_append(const void* q, const void* k, const void* v, int dtype, int T, int q_heads,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                          mnb_rope rope, const int64_t* slots, mnb_kv4_cache cache, void* q_out, mnb_stream stream) {
+  const char* fn = "mnb_kv4_append";
+  mnb_status st;
+  mnb::Kv4Cache c;
+  if ((st = check_kv4(fn, cache, &c)) != MNB_OK) return st;
+  if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
+  if (T < 0 || T > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: T=%d must be in [0, 2^20]", fn, T);
+  if (q_heads < 0 || q_heads > 16384 || (q == nullptr) != (q_heads == 0))
+    return fail(MNB_ERR_INVALID_ARG, "%s: q_heads=%d must be in [1, 16384] with q, or 0 without", fn, q_heads);
+  if (rope.rot_dim < 0 || rope.rot_dim > c.head_dim || rope.rot_dim % 16 != 0)
+    return fail(MNB_ERR_INVALID_ARG, "%s: rot_dim=%d must be a multiple of 16 in [0, head_dim]", fn, rope.rot_dim);
+  if (T == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  if (q) {
+    if ((st = check_ptr(fn, "q", q)) != MNB_OK) return st;
+    if ((st = check_ptr(fn, "q_out", q_out)) != MNB_OK) return st;
+    if ((st = check_stride(fn, "q_stride", q_stride, q_heads, c.head_dim, dtype)) != MNB_OK) return st;
+  }
+  if ((st = check_ptr(fn, "k", k)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "v", v)) != MNB_OK) return st;
+  if ((st = check_stride(fn, "k_stride", k_stride, c.kv_heads, c.head_dim, dtype)) != MNB_OK) return st;
+  if ((st = check_stride(fn, "v_stride", v_stride, c.kv_heads, c.head_dim, dtype)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "slots", slots)) != MNB_OK) return st;
+  if (rope.rot_dim) {
+    if (rope.rows < 1) return fail(MNB_ERR_INVALID_ARG, "%s: rope.rows=%d must be at least 1", fn, rope.rows);
+    if ((st = check_ptr(fn, "cos", rope.cos)) != MNB_OK) return st;
+    if ((st = check_ptr(fn, "sin", rope.sin)) != MNB_OK) return st;
+    if ((st = check_ptr(fn, "positions", positions)) != MNB_OK) return st;
+  }
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  const mnb::Kv4Append a = {q,         k,        v,        dtype == MNB_F32, T,           q_heads,
+                            q_stride,  k_stride, v_stride, positions,        rope.cos,    rope.sin,
+                            rope.rows, rope.rot_dim, rope.interleaved != 0, slots, q_out};
+  return finish(fn, mnb::launch_kv4_append(ctx, c, a), ctx);
+}
+
+mnb_status mnb_kv4_read(mnb_kv4_cache cache, const int64_t* slots, int T, int dtype, void* k_out, void* v_out,
+                        mnb_stream stream) {
+  const char* fn = "mnb_kv4_read";
+  mnb_status st;
+  mnb::Kv4Cache c;
+  if ((st = check_kv4(fn, cache, &c)) != MNB_OK) return st;
+  if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
+  if (T < 0 || T > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: T=%d must be in [0, 2^20]", fn, T);
+  if (T == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  if ((st = check_ptr(fn, "slots", slots)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "k_out", k_out)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "v_out", v_out)) != MNB_OK) return st;
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  return finish(fn, mnb::launch_kv4_read(ctx, c, slots, T, dtype == MNB_F32, k_out, v_out), ctx);
+}
+
+size_t mnb_kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim, int dtype) {
+  if (T < 1 || T > kMaxM || batch < 1 || batch > kMaxM || kv_heads < 1 || kv_heads > 1024 || q_heads < kv_heads ||
+      q_heads > 16384 || q_heads % kv_heads != 0 || !(head_dim == 64 || head_dim == 128 || head_dim == 256) ||
+      (dtype != MNB_F16 && dtype != MNB_F32))
+    return 0;
+  return mnb::kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, dtype == MNB_F32);
+}
+
+mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64_t q_stride, mnb_kv4_cache cache,
+                             const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table, int batch,
+                             int table_stride, float scale, int causal, int window, void* workspace, size_t ws_bytes,
+                             void* out, float* lse, mnb_stream stream) {
+  const char* fn = "mnb_kv4_attention";
+  mnb_status st;
+  mnb::Kv4Cache c;
+  if ((st = check_kv4(fn, cache, &c)) != MNB_OK) return st;
+  if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
+  if (T < 0 || T > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: T=%d must be in [0, 2^20]", fn, T);
+  if (batch < 0 || batch > kMaxM || (T > 0 && batch == 0))
+    return fail(MNB_ERR_INVALID_ARG, "%s: batch=%d must be in [1, 2^20]", fn, batch);
+  if (q_heads < 1 || q_heads > 16384 || q_heads % c.kv_heads != 0)
+    return fail(MNB_ERR_INVALID_ARG, "%s: q_heads=%d must be a multiple of kv_heads=%d in [1, 16384]", fn, q_heads,
+                c.kv_heads);
+  if (table_stride < 1 || (int64_t)table_stride * c.page_size > (int64_t)1 << 30)
+    return fail(MNB_ERR_INVALID_ARG, "%s: table_stride=%d pages of %d tokens must be in [1, 2^30] tokens", fn,
+                table_stride, c.page_size);
+  if (!(scale == scale) || scale - scale != 0.0f)
+    return fail(MNB_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+  if (window < 0) return fail(MNB_ERR_INVALID_ARG, "%s: window=%d must be 0 (none) or positive", fn, window);
+  if (T == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  if ((st = check_ptr(fn, "q", q)) != MNB_OK) return st;
+  if ((st = check_stride(fn, "q_stride", q_stride, q_heads, c.head_dim, dtype)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "q_start", q_start)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "kv_len", kv_len)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "page_table", page_table)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
+  if (lse && !aligned16(lse)) return fail(MNB_ERR_MISALIGNED, "%s: lse is not 16-byte aligned", fn);
+  const size_t need = mnb_kv4_attention_workspace_bytes(T, batch, q_heads, c.kv_heads, c.head_dim, dtype);
+  if (ws_bytes < need)
+    return fail(MNB_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  if (need > 0 && (st = check_ptr(fn, "workspace", workspace)) != MNB_OK) return st;
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  const mnb::Kv4Attention a = {q,     dtype == MNB_F32, T,           q_heads, q_stride,  q_start,  kv_len, page_table, batch,
+                               table_stride, scale, causal != 0, window, workspace, ws_bytes, out,   lse};
+  return finish(fn, mnb::launch_kv4_attention(ctx, c, a), ctx);
 }
 
 }  // extern "C"

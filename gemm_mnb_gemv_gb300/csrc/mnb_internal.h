@@ -104,6 +104,42 @@ cudaError_t launch_generic(LaunchCtx& ctx, const void* A, int M, const QWeight& 
 cudaError_t launch_generic_pair_swiglu(LaunchCtx& ctx, const void* A, const QWeight& gate,
                                        const QWeight& up, int K, int N, int bs, void* out);
 
+// Paged 4-bit key/value cache (mnb.h): geometry of a cache and of its 16-token blocks.
+struct Kv4Cache {
+  uint8_t* pages;
+  int num_pages, page_size, kv_heads, head_dim, group;
+  __host__ __device__ int ng() const { return head_dim / group; }
+  __host__ __device__ int block_bytes() const { return 16 * head_dim + 128 * ng(); }
+};
+struct Kv4Append {
+  const void *q, *k, *v;
+  int f32, T, q_heads;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* positions;
+  const float *cos, *sin;
+  int rows, rot, interleaved;
+  const int64_t* slots;
+  void* q_out;
+};
+struct Kv4Attention {
+  const void* q;
+  int f32, T, q_heads;
+  int64_t q_stride;
+  const int32_t *q_start, *kv_len, *page_table;
+  int batch, table_stride;
+  float scale;
+  int causal, window;
+  void* workspace;
+  size_t ws_bytes;
+  void* out;
+  float* lse;
+};
+cudaError_t launch_kv4_append(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Append& a);
+cudaError_t launch_kv4_read(LaunchCtx& ctx, const Kv4Cache& c, const int64_t* slots, int T, int f32, void* k_out,
+                            void* v_out);
+cudaError_t launch_kv4_attention(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a);
+size_t kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim, int f32);
+
 // Launch helper: cudaLaunchKernelEx with the programmatic-serialisation attribute when
 // ctx.pdl is set.
 template <typename Kern, typename... Args>

@@ -319,6 +319,115 @@ MNB_API mnb_status mnb_gemm_act_order_noalloc(const void *A, int M, mnb_weight w
                                               mnb_stream stream);
 
 /*
+ * ---- Paged 4-bit key/value cache and attention ----
+ *
+ * What a decoder layer needs between its qkv product and its output product, with the
+ * cache held in 4 bits as the weights are. The pages have no counterpart: formats and
+ * entry points are this library's own.
+ *
+ * Cache: `pages` holds num_pages x kv_heads records; a record holds the page_size tokens
+ * of one page and one key/value head as page_size / 16 blocks of 16 tokens. With
+ * D = head_dim (64, 128 or 256), ng = D / group_size (group_size 32, 64 or 128, at most D)
+ * a block is 16 D + 128 ng bytes:
+ *   K codes  16 rows of D/2 bytes; row r is 32-bit words in the order (t, w), t in 0..3, w in
+ *            0..D/32-1; nibble n (bits 4n..4n+3) of word (t, w) is element 32 w + 8 t + n. For
+ *            D = 256 the word is stored at w ^ 4 in odd rows.
+ *   V codes  words in the order (g, r', w), g in 0..7, r' in 0..15, w in 0..D/64-1; nibble
+ *            4 h + n (h in 0..1, n in 0..3) of word (g, r', w) is element 64 w + 32 h + 4 g + n
+ *            of row r' ^ x(g), x(g) = 8 (g/2 % 2) for D = 64, 8 (g % 2) for 128, g % 2 for 256.
+ *   K, then V parameters: fp16 pairs (scale, offset) in the order (group, row).
+ * An element is offset + code * scale (fp32, one rounding). Slot s is row s % 16 of block
+ * (s % page_size) / 16 of page s / page_size. The orders are those in which the attention
+ * kernel's lanes read a block: whole vectors, no bank conflicts, one bulk copy per block.
+ */
+typedef struct {
+    uint8_t *pages;     /* num_pages * kv_heads * (page_size / 16) blocks, 16-byte aligned   */
+    int32_t num_pages;  /* >= 1                                                              */
+    int32_t page_size;  /* tokens in a page: a multiple of 16, at most 4096                  */
+    int32_t kv_heads;   /* 1 .. 1024                                                         */
+    int32_t head_dim;   /* 64, 128 or 256                                                    */
+    int32_t group_size; /* 32, 64 or 128, at most head_dim                                   */
+} mnb_kv4_cache;
+
+/* Rotation tables: cos and sin are fp32 [rows, rot_dim / 2]; rot_dim is 0 (no rotation, the
+ * pointers are not read) or a multiple of 16 up to head_dim: the first rot_dim elements of
+ * each head turn, the others stay. Pair i is the elements (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * when `interleaved` is not 0. */
+typedef struct {
+    const float *cos;
+    const float *sin;
+    int32_t rows;
+    int32_t rot_dim;
+    int32_t interleaved;
+} mnb_rope;
+
+/* Bytes of a cache's `pages` (0 for arguments outside the ranges above). */
+MNB_API size_t mnb_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim, int group_size);
+
+/*
+ * Append T tokens: rotate q and k by their positions, quantise k and v, store them at their
+ * slots, write the rotated q.
+ * q [T, q_heads, D], k and v [T, kv_heads, D] are of `dtype` (MNB_F16 or MNB_F32); a token's
+ * heads lie one after the other and tokens are *_stride elements apart (views of one fused
+ * qkv product do), each stride a multiple of 16 bytes (else MNB_ERR_MISALIGNED). q may be
+ * NULL (q_heads 0): then q_out is not written. q_out is [T, q_heads, D] of `dtype`, contiguous,
+ * and may be q itself where q is contiguous. positions is int32 [T] (not read when rot_dim is 0), slots
+ * int64 [T]; the non-negative slots of a call are distinct.
+ * Arithmetic, fp32, each operation rounded once and none fused:
+ *   a' = a cos - b sin, b' = b cos + a sin; q_out rounds them to dtype, k goes on unrounded.
+ *   A group with least element lo and largest hi: offset = fp16(lo) and scale =
+ *   fp16((hi - lo) * fp32(1/15)), both held within +-65504; code = rint((x - offset) * (1 / scale)) within
+ *   0..15, and 0 where scale is 0. A group with an inf or NaN element holds NaN.
+ * A negative slot: the token is not stored (padding), its q is still written. A slot beyond
+ * the cache: not stored. A position outside 0..rows-1: not stored, and its q_out row is 0.
+ * The last two set the index bit of the device status word. T = 0 is valid and does nothing.
+ */
+MNB_API mnb_status mnb_kv4_append(const void *q, const void *k, const void *v, int dtype, int T, int q_heads,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                                  mnb_rope rope, const int64_t *slots, mnb_kv4_cache cache, void *q_out,
+                                  mnb_stream stream);
+
+/*
+ * The values that T slots hold: k_out and v_out [T, kv_heads, D] of `dtype`, element
+ * offset + code * scale in fp32, rounded once more for MNB_F16. A negative slot reads as
+ * zeros; one beyond the cache too, and it sets the index bit of the device status word.
+ */
+MNB_API mnb_status mnb_kv4_read(mnb_kv4_cache cache, const int64_t *slots, int T, int dtype, void *k_out,
+                                void *v_out, mnb_stream stream);
+
+/*
+ * Scratch bytes of mnb_kv4_attention for these shapes (0 for arguments outside its ranges).
+ * The size covers GPUs of up to 160 SMs; contents need no initialisation, each call
+ * overwrites them, so calls sharing one workspace must be ordered on one stream.
+ */
+MNB_API size_t mnb_kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim,
+                                                 int dtype);
+
+/*
+ * Attention of T query tokens of `batch` sequences over the cache, one token a sequence
+ * (decode), a few (speculative verify) or many (prefill). Sequence b has the query tokens
+ * q_start[b] .. q_start[b+1]-1 (int32 [batch + 1], not decreasing, from 0 to T) and kv_len[b]
+ * keys (int32 [batch], its query tokens' own included): key j is in page
+ * page_table[b * table_stride + j / page_size] (int32). Query token i of n is at position
+ * kv_len[b] - n + i; it sees the keys j of 0..kv_len[b]-1 with, if `causal`, j <= its position
+ * and, if window > 0, j > its position - window. Query head h reads key/value head
+ * h / (q_heads / kv_heads); q_heads is a multiple of kv_heads.
+ *   out[i, h] = sum_j softmax_j(scale * q[i, h] . k_j) v_j;  lse[i, h] = log sum_j e^(scale * q . k_j)
+ * (natural log; lse may be NULL). A token that sees no key gets out = 0 and lse = -inf.
+ * q [T, q_heads, D] of `dtype`, tokens q_stride elements apart (a multiple of 16 bytes); out
+ * [T, q_heads, D] of `dtype`, contiguous; lse fp32 [T, q_heads]. Sums and softmax statistics are fp32.
+ * A page index outside the cache: its keys are left out; a kv_len beyond
+ * table_stride * page_size: cut to it. Both set the index bit of the device status word.
+ * Rows of q_start's range are clamped to 0..T. Launch geometry depends on the shape
+ * arguments alone: the lengths are read on the device, so a captured call follows them.
+ */
+MNB_API mnb_status mnb_kv4_attention(const void *q, int dtype, int T, int q_heads, int64_t q_stride,
+                                     mnb_kv4_cache cache, const int32_t *q_start, const int32_t *kv_len,
+                                     const int32_t *page_table, int batch, int table_stride, float scale,
+                                     int causal, int window, void *workspace, size_t ws_bytes, void *out,
+                                     float *lse, mnb_stream stream);
+
+/*
  * Programmatic dependent launch. With `enable` != 0, later calls on this host thread
  * launch their kernels with programmatic stream serialisation: a kernel may start while
  * the previous kernel on the stream is still running, and it streams its weight, scale
@@ -332,8 +441,8 @@ MNB_API void mnb_set_programmatic_launch(int enable);
 /*
  * Reads and clears the device status word. Kernels that wait on shared-memory barriers
  * bound every wait; one that gives up sets a bit in this word, writes NaN outputs and
- * returns instead of hanging. The act-order kernels set another bit for an index input
- * out of range. Returns MNB_ERR_TIMEOUT (with the bits in the message) if a wait gave
+ * returns instead of hanging. The act-order and key/value cache kernels set another bit for
+ * an index input out of range. Returns MNB_ERR_TIMEOUT (with the bits in the message) if a wait gave
  * up, MNB_ERR_INVALID_ARG if only the index bit is set, else MNB_OK. Synchronises the
  * current device, so it must not be called while a stream is being captured.
  */
