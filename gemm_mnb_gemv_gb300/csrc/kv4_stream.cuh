@@ -1,0 +1,912 @@
+// Streaming attention over the paged 4-bit key/value cache (decode, verify, fp32 activations).
+//
+// Rows are (query token, head of the key head's group) pairs, 8 NT of them in a row tile, and are the N side
+// of mma.sync m16n8k16; 16 keys (one block of the cache) are the M side of S = K Q^T and the
+// K side of O^T = V^T P^T.  The cache's codes go into the products as small integers:
+//   * K: the nibbles as they lie are fp16 subnormals (code * 2^-24, or * 2^-20 for the upper one of
+//     a byte, undone in q), so one AND makes two operand elements and q . code is exact; a group's
+//     scale multiplies its 32..128-element dot after it is formed, and the offsets join as one
+//     more MMA: sum_g offset_g * sum_{d in g} q_d, the row sums of q split into two fp16.
+//   * V: codes become c - 8 (exact), probabilities become fp16(p * scale_g * 2^x) per group, and one more
+//     MMA adds sum_j p_j (offset + 8 scale), split into two fp16.  Centring keeps the rounding
+//     of p * scale from being multiplied by |offset| / |v|.  The power 2^x follows the largest scale seen, so
+//     values of any size use fp16's whole range.
+// A row's reference m moves only when a score passes it by 14 (in powers of two; one vote a
+// block instead of shuffles) and is then set 8 below the largest: p = 2^(s - m) <= 2^14, so
+// fp16 keeps probabilities down to 2^-22 of the largest normal.
+// fp32 activations: q and p are split into two fp16 (2^-22 together), products run once for each.
+//
+// Work: tiles of 64 keys of every (sequence, row tile, key head) in one list, cut into equal ranges, one
+// per resident CTA, on the device from the lengths (ragged batches balance, graphs
+// follow new lengths).  Each of a CTA's four warps takes one 16-key block of a tile through its own
+// ring of bulk copies (one copy of 16 D + 128 ng bytes a block) that runs ahead across the ends of sequences; the
+// warps meet only at a sequence's end.  Pieces of a sequence cut by a range's end go to the workspace
+// as (m, l, o) and a second, dependent launch joins them in order.
+#pragma once
+
+#include <float.h>
+
+#include "kv4.cuh"
+#include "mma_sync.cuh"
+#include "mnb_device.cuh"
+#include "mnb_internal.h"
+
+namespace mnb {
+namespace kv4 {
+
+constexpr int kWarps = 4;           // warps of a CTA
+constexpr int kTile = 16 * kWarps;  // keys of a work unit
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLift = 8.0f;       // a row's reference is set this far below its largest score (log2)
+constexpr float kRise = 14.0f;      // and moves when a score passes it by this much
+
+// Largest number of CTAs a launch may have: the workspace's sizing.
+constexpr int kMaxCtas = 160 * 4;
+
+struct Piece {  // what the joining kernel needs of a cut sequence, written by the CTA of its last piece
+  int first;    // CTA of the first piece, -1: this CTA ends no cut sequence
+  int q0, row0, rows, kvh;
+};
+
+// 8 x 8 transpose of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// Two V code pairs to fp16 c - 8: the lower and the upper nibble of each byte pair position.
+__device__ __forceinline__ uint32_t v_lower(uint32_t x) {
+  uint32_t r = lop3_and_or(x, 0x000f000fu, 0x64006400u);  // 1024 + c
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0xE408E408u));
+  return r;
+}
+__device__ __forceinline__ uint32_t v_upper(uint32_t x) {
+  uint32_t r = lop3_and_or(x, 0x00f000f0u, 0x64006400u);  // 1024 + 16 c
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(r), "r"(0x2C002C00u), "r"(0xD480D480u));
+  return r;
+}
+
+// One sequence's place in the work list.
+struct Cursor {
+  int b, rt, kvh, tile;
+  int q0, qlen, n;    // query rows and keys of sequence b
+  int R;              // row tiles of sequence b
+  int t0, t1;         // key tiles of row tile rt
+};
+
+template <int RT>
+struct Walk {
+  const Kv4Attention& a;
+  const Kv4Cache& c;
+  int G, capacity;
+
+  __device__ __forceinline__ void load(Cursor& s) const {
+    const int lo = min(max(a.q_start[s.b], 0), a.T), hi = min(max(a.q_start[s.b + 1], lo), a.T);
+    s.q0 = lo;
+    s.qlen = hi - lo;
+    s.n = min(max(a.kv_len[s.b], 0), capacity);
+    s.R = (int)(((int64_t)s.qlen * G + RT - 1) / RT);
+  }
+  // key tiles that some row of row tile rt sees
+  __device__ __forceinline__ void range(Cursor& s) const {
+    const int first = s.rt * RT / G, last = min(s.qlen - 1, (s.rt * RT + RT - 1) / G);
+    const int64_t pos0 = (int64_t)s.n - s.qlen + first, pos1 = (int64_t)s.n - s.qlen + last;
+    const int64_t hi = a.causal ? min((int64_t)s.n, pos1 + 1) : s.n;
+    const int64_t lo = a.window > 0 ? max((int64_t)0, pos0 - a.window + 1) : 0;
+    s.t0 = (int)(lo / kTile);
+    s.t1 = max(s.t0 + 1, (int)((max(hi, (int64_t)0) + kTile - 1) / kTile));  // a row tile without keys still has a unit: it writes zeros
+  }
+  __device__ __forceinline__ int64_t units(Cursor s) const {  // of sequence s.b, loaded
+    int64_t u = 0;
+    for (s.rt = 0; s.rt < s.R; ++s.rt) {
+      range(s);
+      u += s.t1 - s.t0;
+    }
+    return u * c.kv_heads;
+  }
+  __device__ __forceinline__ void next_part(Cursor& s) const {  // to the first tile of the next row tile or key head
+    if (++s.kvh == c.kv_heads) {
+      s.kvh = 0;
+      if (++s.rt == s.R) {
+        s.rt = 0;
+        do {
+          ++s.b;
+          if (s.b >= a.batch) return;  // past the end: not used
+          load(s);
+        } while (s.R == 0);
+      }
+      range(s);
+    }
+    s.tile = s.t0;
+  }
+};
+
+// Shared memory of a CTA.
+template <int D, int NT, bool F32>
+struct Layout {
+  static constexpr int kQ = (D / 16) * NT * 32 * 8 * (F32 ? 2 : 1);  // q fragments
+  static constexpr int kQs = NT * 32 * 8;                            // row sums of q
+  static constexpr int kCol = NT * 8 * 4;                            // score factors
+  static constexpr int kEx = kWarps * 8 * 64 * 4;                    // exchange of 64 columns of o
+  static constexpr int kMl = kWarps * NT * 8 * 8;                    // m, l of each warp
+  static constexpr int kFixed = kQ + kQs + kCol + kEx + kMl + 1024;  // + barriers, flags, scan
+  static int stages(int block_bytes, int budget) {
+    const int s = (budget - kFixed) / (kWarps * block_bytes);
+    return s < 2 ? 2 : s > 16 ? 16 : s;
+  }
+};
+
+template <int D, int NT, bool F32, int kMinCtas>
+__global__ void __launch_bounds__(kWarps * 32, kMinCtas)
+    kv4_stream_kernel(const Kv4Cache c, const Kv4Attention a, int stages, uint32_t* status) {
+  constexpr int RT = 8 * NT;
+  constexpr int KW = D / 32;  // 32-element granules
+  constexpr int VW = D / 64;  // V words of a lane's chunk
+  using L = Layout<D, NT, F32>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
+  const int block_bytes = c.block_bytes(), ng = c.ng(), gran = c.group / 32;
+  uint8_t* ring = smem + warp * stages * block_bytes;
+  uint8_t* fixed = smem + kWarps * stages * block_bytes;
+  uint2* qf = reinterpret_cast<uint2*>(fixed);
+  uint2* qsf = reinterpret_cast<uint2*>(fixed + L::kQ);
+  float* colf = reinterpret_cast<float*>(fixed + L::kQ + L::kQs);
+  float* exch = reinterpret_cast<float*>(fixed + L::kQ + L::kQs + L::kCol);
+  float2* ml = reinterpret_cast<float2*>(fixed + L::kQ + L::kQs + L::kCol + L::kEx);
+  uint8_t* misc = fixed + L::kQ + L::kQs + L::kCol + L::kEx + L::kMl;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc) + warp * 16;        // [stage]
+  int* flags = reinterpret_cast<int*>(misc + 512) + warp * 16;           // [stage] block is in the cache
+  int64_t* scan = reinterpret_cast<int64_t*>(misc + 768);                // [8]
+
+  if (lane < stages) mbar_init(&full[lane], 1);
+  fence_mbar_init();
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- the range of this CTA ----
+  Walk<RT> walk{a, c, a.q_heads / c.kv_heads, a.table_stride * c.page_size};
+  const int G = walk.G;
+  Cursor cur = {};
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
+    if (b0 + tid < a.batch) {
+      cur.b = b0 + tid;
+      walk.load(cur);
+      total += walk.units(cur);
+      if (blockIdx.x == 0 && a.kv_len[cur.b] > walk.capacity) report_status(status, kStatusBadIndex);
+    }
+  }
+  const int64_t mine = total;
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+  if (lane == 0) scan[warp] = total;
+  __syncthreads();
+  total = scan[0] + scan[1] + scan[2] + scan[3];
+  __syncthreads();
+  const int64_t ncta = min((int64_t)gridDim.x, total);
+  Piece* pieces = reinterpret_cast<Piece*>(a.workspace);
+  constexpr int kSlot = RT * (D + 2);  // floats of one partial result
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
+  if ((int64_t)blockIdx.x >= ncta) {
+    if (tid == 0) pieces[blockIdx.x].first = -1;
+    return;
+  }
+  const int64_t u0 = blockIdx.x * total / ncta, u1 = (blockIdx.x + 1) * total / ncta;
+  // the sequence that holds unit u0: 128 sequences a turn, prefix sums
+  {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
+      int64_t own = 0;
+      if (a.batch <= kWarps * 32) {
+        own = mine;
+      } else if (b0 + tid < a.batch) {
+        cur.b = b0 + tid;
+        walk.load(cur);
+        own = walk.units(cur);
+      }
+      int64_t inc = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      int64_t base = before;
+      for (int w = 0; w < warp; ++w) base += scan[w];
+      const int64_t hi = base + inc, lo = hi - own;
+      if (u0 >= lo && u0 < hi) {
+        scan[4] = b0 + tid;
+        scan[5] = u0 - lo;
+      }
+      before += scan[0] + scan[1] + scan[2] + scan[3];
+      __syncthreads();
+      if (before > u0) break;
+    }
+  }
+  cur.b = (int)scan[4];
+  int64_t off = scan[5];
+  walk.load(cur);
+  for (cur.rt = 0;; ++cur.rt) {
+    walk.range(cur);
+    const int64_t len = (int64_t)(cur.t1 - cur.t0) * c.kv_heads;
+    if (off < len) break;
+    off -= len;
+  }
+  cur.kvh = (int)(off / (cur.t1 - cur.t0));
+  cur.tile = cur.t0 + (int)(off % (cur.t1 - cur.t0));
+
+  // ---- the producer: runs ahead of the consumer by up to `stages` blocks ----
+  Cursor pro = cur;
+  int64_t pro_left = u1 - u0;
+  int pro_stage = 0;
+  int pro_page = 0;
+  // moves pro to the next unit whose block this warp has to read, and starts the load of its page index
+  auto seek = [&](bool step) {
+    while (true) {
+      if (step) {
+        if (--pro_left <= 0) return;
+        if (++pro.tile == pro.t1) walk.next_part(pro);
+      }
+      step = true;
+      if (pro_left <= 0) return;
+      const int base = pro.tile * kTile + warp * 16;
+      if (base < pro.n) {
+        pro_page = a.page_table[(int64_t)pro.b * a.table_stride + base / c.page_size];
+        return;
+      }
+    }
+  };
+  auto produce = [&]() {
+    if (pro_left <= 0) return;
+    const int base = pro.tile * kTile + warp * 16;
+    const bool ok = pro_page >= 0 && pro_page < c.num_pages;
+    if (lane == 0) {
+      flags[pro_stage] = ok;
+      if (ok) {
+        const uint8_t* src = c.pages + (((int64_t)pro_page * c.kv_heads + pro.kvh) * (c.page_size / 16) +
+                                        base % c.page_size / 16) * block_bytes;
+        mbar_arrive_expect_tx(&full[pro_stage], block_bytes);
+        bulk_g2s(ring + pro_stage * block_bytes, src, block_bytes, &full[pro_stage]);
+      } else {
+        report_status(status, kStatusBadIndex);
+        mbar_arrive(&full[pro_stage]);
+      }
+    }
+    if (++pro_stage == stages) pro_stage = 0;
+    seek(true);
+  };
+  __syncwarp();
+  seek(false);
+  for (int i = 0; i < stages; ++i) produce();
+
+  // ---- the consumer ----
+  int stage = 0;
+  uint32_t parity = 0;
+  bool gave_up = false;
+  int64_t left = u1 - u0;
+  if (tid == 0) pieces[blockIdx.x].first = -1;
+  while (left > 0) {
+    const bool from_start = cur.tile == cur.t0;
+    const int row0 = cur.rt * RT, rows = cur.qlen * G;
+    // q fragments of the row tile: warp w prepares the column groups w, w + 4, ..
+    for (int nt = warp; nt < NT; nt += kWarps) {
+      const int r = row0 + nt * 8 + g;
+      const bool live = r < rows;
+      float q[KW][8], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const int64_t at = (int64_t)(cur.q0 + (live ? r / G : 0)) * a.q_stride +
+                           ((int64_t)cur.kvh * G + (live ? r % G : 0)) * D + 32 * i + 8 * t;
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        if (live) {
+          if constexpr (F32) {
+            v0 = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
+            v1 = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at + 4);
+          } else {
+            v0 = *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at);
+          }
+        }
+        if constexpr (F32) {
+          const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[i][j] = __uint_as_float(u[j]);
+        } else {
+          const uint32_t u[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack_half2(u[j]);
+            q[i][2 * j] = f.x, q[i][2 * j + 1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(q[i][j]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      // rows are scaled by a power of two to [2^13, 2^14): the parts of q, its sums and the division
+      // by 16 then stay inside fp16
+      const int e = top > 0.0f && top < INFINITY ? min(max(ilogbf(top), -110), 127) - 13 : 0;
+      const float down = scalbnf(1.0f, -e);
+      float sums[2] = {0.0f, 0.0f};  // of groups t and t + 4
+      float acc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          q[i][j] *= down;
+          acc += q[i][j];
+        }
+        if ((i + 1) % gran == 0) {
+          acc += __shfl_xor_sync(kFull, acc, 1);
+          acc += __shfl_xor_sync(kFull, acc, 2);
+          const int gi = i / gran;
+          if (gi == t) sums[0] = acc;
+          if (gi == t + 4) sums[1] = acc;
+          acc = 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const float x0 = q[i][2 * s], x1 = q[i][2 * s + 4];
+          const float y0 = q[i][2 * s + 1] * 0.0625f, y1 = q[i][2 * s + 5] * 0.0625f;
+          const uint2 hi = make_uint2(pack_half2(x0, x1), pack_half2(y0, y1));
+          qf[((2 * i + s) * NT + nt) * 32 + lane] = hi;
+          if constexpr (F32) {
+            const float2 hx = unpack_half2(hi.x), hy = unpack_half2(hi.y);
+            qf[((D / 16 + 2 * i + s) * NT + nt) * 32 + lane] =
+                make_uint2(pack_half2(x0 - hx.x, x1 - hx.y), pack_half2(y0 - hy.x, y1 - hy.y));
+          }
+        }
+      }
+      uint32_t sp[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float s = sums[j] * 0.00390625f;  // up to 2^21 * 2^-8
+        const float hi = __half2float(__float2half_rn(s));
+        sp[j] = pack_half2(hi, s - hi);
+      }
+      qsf[nt * 32 + lane] = make_uint2(sp[0], sp[1]);
+      if (t == 0) colf[nt * 8 + g] = scalbnf(a.scale * kLog2e, e + 24);
+    }
+    __syncthreads();
+
+    float cf[NT][2];
+    int lim_lo[NT][2], lim_hi[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = nt * 8 + 2 * t + j;
+        cf[nt][j] = colf[col];
+        const int pos = cur.n - cur.qlen + (row0 + col) / G;
+        lim_hi[nt][j] = a.causal ? min(cur.n, pos + 1) : cur.n;
+        lim_lo[nt][j] = a.window > 0 ? pos - a.window + 1 : 0;
+      }
+    // keys in [all_lo, all_hi) are seen by every row of the tile
+    const int pos_a = cur.n - cur.qlen + row0 / G, pos_z = cur.n - cur.qlen + (row0 + RT - 1) / G;
+    const int all_hi = a.causal ? min(cur.n, pos_a + 1) : cur.n;
+    const int all_lo = a.window > 0 ? pos_z - a.window + 1 : 0;
+    uint2 qreg[NT == 1 ? D / 16 : 1];
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) qreg[i] = qf[i * 32 + lane];
+    }
+
+    float m[NT][2], l[NT][2], o[D / 16][NT][4], oo[NT][4];
+    float vmul = 1.0f, vinv = 1.0f;
+    uint32_t vlim = 0;  // fp16 bits that V scales stay below
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) m[nt][j] = -FLT_MAX, l[nt][j] = gave_up ? NAN : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) oo[nt][j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
+    }
+
+    const int64_t here = min(left, (int64_t)(cur.t1 - cur.tile));
+    const int tile_end = cur.tile + (int)here;
+    for (int tile = cur.tile; tile < tile_end; ++tile) {
+      const int base = tile * kTile + warp * 16;
+      if (base >= cur.n) continue;
+      if (!__all_sync(kFull, gave_up || mbar_wait_bounded(&full[stage], parity))) {
+        // give up: no more copies, a last bounded wait for those in flight, NaN results
+        if (lane == 0) report_status(status, kStatusFullWait);
+        gave_up = true;
+        pro_left = 0;
+        int st = stage;
+        uint32_t ph = parity;
+        do {
+          if (!__all_sync(kFull, mbar_wait_bounded(&full[st], ph))) break;
+          if (++st == stages) st = 0, ph ^= 1u;
+        } while (st != pro_stage);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
+      }
+      const uint8_t* blk = ring + stage * block_bytes;
+      if (flags[stage] && !gave_up) {
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 16 * D);
+        // ---- scores ----
+        float s[NT][4];
+        {
+          uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0;  // offsets of groups t, t + 4 for rows g, g + 8
+          if (t < ng) {
+            a0 = __byte_perm(par[t * 16 + g], 0, 0x3232);
+            a1 = __byte_perm(par[t * 16 + g + 8], 0, 0x3232);
+          }
+          if (t + 4 < ng) {
+            a2 = __byte_perm(par[(t + 4) * 16 + g], 0, 0x3232);
+            a3 = __byte_perm(par[(t + 4) * 16 + g + 8], 0, 0x3232);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = qsf[nt * 32 + lane];
+            mma16816_zero(s[nt], a0, a1, a2, a3, b.x, b.y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[nt][j] *= 1.52587890625e-5f;  // 2^8 / 2^24
+          }
+        }
+        uint32_t kw[2][KW];
+        {
+          const uint32_t at = smem_u32(blk);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            if constexpr (D == 64) {
+              const uint2 v = lds_u64_a(at + r * 32 + t * 8);
+              kw[h][0] = v.x, kw[h][1] = v.y;
+            } else {
+#pragma unroll
+              for (int p = 0; p < KW / 4; ++p) {
+                const uint4 v = lds128_a(at + k_word_byte<D>(r, t, 4 * p));
+                kw[h][4 * p] = v.x, kw[h][4 * p + 1] = v.y, kw[h][4 * p + 2] = v.z, kw[h][4 * p + 3] = v.w;
+              }
+            }
+          }
+        }
+        {
+          // fp32: a scale after every 32 elements and the low parts first, as the tensor cores cut sums off at
+          // fp32 and every further step would add an error of one last place of the running sum
+          float acc[NT][4];
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {
+            const bool first = F32 || i % gran == 0;
+            if (first) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[nt][j] = 0.0f;
+            }
+#pragma unroll
+            for (int part = F32 ? 1 : 0; part >= 0; --part)
+#pragma unroll
+              for (int st = 0; st < 2; ++st) {
+                const uint32_t x = kw[0][i] >> (8 * st), y = kw[1][i] >> (8 * st);
+                const uint32_t a0 = x & 0x000f000fu, a2 = x & 0x00f000f0u, a1 = y & 0x000f000fu, a3 = y & 0x00f000f0u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint2 b;
+                  if (NT == 1 && part == 0) b = qreg[NT == 1 ? 2 * i + st : 0];
+                  else b = qf[((part * (D / 16) + 2 * i + st) * NT + nt) * 32 + lane];
+                  mma16816(acc[nt], a0, a1, a2, a3, b.x, b.y);
+                }
+              }
+            if (F32 || (i + 1) % gran == 0) {
+              const int gi = i / gran;
+              const float s0 = half_bits_to_float(par[gi * 16 + g] & 0xffffu);
+              const float s1 = half_bits_to_float(par[gi * 16 + g + 8] & 0xffffu);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                s[nt][0] = fmaf(acc[nt][0], s0, s[nt][0]);
+                s[nt][1] = fmaf(acc[nt][1], s0, s[nt][1]);
+                s[nt][2] = fmaf(acc[nt][2], s1, s[nt][2]);
+                s[nt][3] = fmaf(acc[nt][3], s1, s[nt][3]);
+              }
+            }
+          }
+        }
+        const int j0 = base + g, j1 = base + g + 8;
+        const bool masked = base < all_lo || base + 16 > all_hi;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[nt][j] *= cf[nt][j & 1];
+            if (masked) {
+              const int key = j < 2 ? j0 : j1;
+              if (key < lim_lo[nt][j & 1] || key >= lim_hi[nt][j & 1]) s[nt][j] = -INFINITY;
+            }
+          }
+        // ---- V scales; keys past the end hold anything ----
+        const bool in0 = j0 < cur.n, in1 = j1 < cur.n;
+        const uint32_t* vpar = par + ng * 16;
+        uint32_t vscale = 0, voff = 0;  // largest magnitudes, as fp16 bits
+        for (int gi = 0; gi < ng; ++gi) {
+          const uint32_t p0 = in0 ? vpar[gi * 16 + g] : 0u, p1 = in1 ? vpar[gi * 16 + g + 8] : 0u;
+          vscale = max(vscale, max(p0 & 0x7fffu, p1 & 0x7fffu));
+          voff = max(voff, max((p0 >> 16) & 0x7fffu, (p1 >> 16) & 0x7fffu));
+        }
+        const bool odd = max(vscale, voff) >= 0x7c00u;  // an inf or NaN among the V parameters
+        uint32_t vtop = max(vscale, voff > 0x0c00u ? voff - 0x0c00u : 0u);  // max(scale, |offset| / 8)
+        bool rise = vtop > vlim;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rise |= s[nt][j] > m[nt][j & 1] + kRise;
+        bool any_odd = false;
+        if (__any_sync(kFull, rise || odd)) {
+          any_odd = __any_sync(kFull, odd);
+          vtop = __reduce_max_sync(kFull, odd ? 0u : vtop);
+          float grow = 1.0f;
+          if (vtop > vlim) {
+            const int ex = vtop ? (int)(__float_as_uint(half_bits_to_float(vtop)) >> 23) - 127 : -24;
+            const float mul = __uint_as_float((uint32_t)(127 - 2 - ex) << 23);  // scales up to vlim become at most 1
+            grow = vinv * mul;
+            vmul = mul;
+            vinv = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
+            vlim = ex + 2 > 15 ? 0x7bffu : (uint32_t)__half_as_ushort(__float2half_rn(scalbnf(1.0f, ex + 2)));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(s[nt][j], s[nt][j + 2]);
+#pragma unroll
+              for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, sh));
+              top = top > m[nt][j] + kRise ? top - kLift : m[nt][j];  // a row's arithmetic hangs on its own scores alone
+              const float al = ex2(m[nt][j] - top);
+              m[nt][j] = top;
+              l[nt][j] *= al;
+              const float ag = al * grow;
+              oo[nt][j] *= ag, oo[nt][j + 2] *= ag;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) o[i][nt][j] *= ag, o[i][nt][j + 2] *= ag;
+            }
+        }
+        // ---- probabilities ----
+        uint32_t ph[NT][2], pl[F32 ? NT : 1][2];  // p as B fragments
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[nt][j] = ex2(s[nt][j] - m[nt][j & 1]);
+            l[nt][j & 1] += s[nt][j];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u = pack_half2(s[nt][2 * h], s[nt][2 * h + 1]);
+            ph[nt][h] = movmatrix(u);
+            if constexpr (F32) {
+              const float2 f = unpack_half2(u);
+              pl[nt][h] = movmatrix(pack_half2(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+            }
+          }
+        }
+        // ---- sum_j p_j (offset + 8 scale): row g of this product is group g ----
+        {
+          uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0, bad0 = 0, bad1 = 0;
+          if (g < ng) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = 2 * t + (k & 1) + (k >> 1) * 8;
+              const uint32_t p = base + r < cur.n ? vpar[g * 16 + r] : 0u;
+              const bool nf = (p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u;
+              const float2 so = unpack_half2(nf ? 0u : p);
+              const float x = fmaf(so.x, 8.0f, so.y) * vmul * 1024.0f;  // |offset| <= 8, scale <= 1 in units of vinv
+              const __half h = __float2half_rn(x);
+              hi[k] = __half_as_ushort(h);
+              lo[k] = __half_as_ushort(__float2half_rn(x - __half2float(h)));
+              if (nf) {
+                if (k < 2) bad0 |= 0x3c00u << (16 * (k & 1));
+                else bad1 |= 0x3c00u << (16 * (k & 1));
+              }
+            }
+            a0 = hi[0] | hi[1] << 16, a2 = hi[2] | hi[3] << 16;
+            a1 = lo[0] | lo[1] << 16, a3 = lo[2] | lo[3] << 16;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (F32) {
+              float acc[4];
+              mma16816_zero(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              mma16816(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) oo[nt][k] += acc[k];
+            } else {
+              mma16816(oo[nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+            }
+          }
+          if (any_odd) {
+            // which rows see a key whose group is not finite: a product of two 0 / 1 matrices
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t see[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int key = base + g + 8 * h;
+                uint32_t u = 0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (key >= lim_lo[nt][j] && key < lim_hi[nt][j]) u |= 0x3c00u << (16 * j);
+                see[h] = movmatrix(u);
+              }
+              float hit[4];
+              mma16816_zero(hit, bad0, 0u, bad1, 0u, see[0], see[1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (hit[j] > 0.0f) oo[nt][j] = __uint_as_float(0x7fffffffu);
+            }
+          }
+        }
+        // ---- sum_j p_j scale_j (c_j - 8) ----
+        {
+          uint32_t vw[4][VW];  // words of keys 2t, 2t + 1, 2t + 8, 2t + 9
+          const uint32_t at = smem_u32(blk) + 8 * D;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = 2 * t + 8 * h;
+            if constexpr (D == 64) {
+              const uint2 v = lds_u64_a(at + v_word_byte<D>(g, r, 0));
+              vw[2 * h][0] = v.x, vw[2 * h + 1][0] = v.y;
+            } else if constexpr (D == 128) {
+              const uint4 v = lds128_a(at + v_word_byte<D>(g, r, 0));
+              vw[2 * h][0] = v.x, vw[2 * h][1] = v.y, vw[2 * h + 1][0] = v.z, vw[2 * h + 1][1] = v.w;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4 v = lds128_a(at + v_word_byte<D>(g, r + k, 0));
+                vw[2 * h + k][0] = v.x, vw[2 * h + k][1] = v.y, vw[2 * h + k][2] = v.z, vw[2 * h + k][3] = v.w;
+              }
+            }
+          }
+          uint32_t bh[NT][2], bl[F32 ? NT : 1][2];
+#pragma unroll
+          for (int i = 0; i < KW; ++i) {  // granule of 32 elements: word i / 2, half i % 2
+            if (i % gran == 0) {
+              const int gi = i / gran;
+              uint32_t p0 = in0 ? vpar[gi * 16 + g] & 0xffffu : 0u, p1 = in1 ? vpar[gi * 16 + g + 8] & 0xffffu : 0u;
+              if (any_odd) {
+                const uint32_t q0 = in0 ? vpar[gi * 16 + g] : 0u, q1 = in1 ? vpar[gi * 16 + g + 8] : 0u;
+                if ((q0 & 0x7c00u) == 0x7c00u || (q0 & 0x7c000000u) == 0x7c000000u) p0 = 0u;
+                if ((q1 & 0x7c00u) == 0x7c00u || (q1 & 0x7c000000u) == 0x7c000000u) p1 = 0u;
+              }
+              const float f0 = half_bits_to_float(p0) * vmul, f1 = half_bits_to_float(p1) * vmul;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float f = h ? f1 : f0;
+                  const float x = s[nt][2 * h] * f, y = s[nt][2 * h + 1] * f;
+                  const uint32_t u = pack_half2(x, y);
+                  bh[nt][h] = movmatrix(u);
+                  if constexpr (F32) {
+                    const float2 w = unpack_half2(u);
+                    bl[nt][h] = movmatrix(pack_half2(x - w.x, y - w.y));
+                  }
+                }
+            }
+            const uint32_t sel = i % 2 ? 0x7632u : 0x5410u;
+            uint32_t x = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel), y = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a0 = v_lower(x), a1 = v_upper(x), a2 = v_lower(y), a3 = v_upper(y);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (F32) {  // added outside the tensor cores, with rounding
+                  float acc[4];
+                  mma16816_zero(acc, a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+                  mma16816(acc, a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) o[2 * i + j][nt][k] += acc[k];
+                } else {
+                  mma16816(o[2 * i + j][nt], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
+                }
+              }
+              x >>= 8, y >>= 8;
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (++stage == stages) stage = 0, parity ^= 1u;
+      produce();
+    }
+
+    // ---- the end of this piece: join the four warps ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], sh);
+        if (g == 0) ml[warp * RT + nt * 8 + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
+      }
+    __syncthreads();
+    const bool ends = tile_end == cur.t1;
+    const bool whole = from_start && ends;
+    float* slot = slots + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kSlot;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float fac[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float top = -FLT_MAX;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * RT + nt * 8 + 2 * t + j].x);
+        fac[j] = ex2(m[nt][j] - top);
+        // the two fp16 parts of the offset sums: rows g and g + 8 of their product
+        oo[nt][j] = (oo[nt][j] + oo[nt][j + 2]) * 0.0009765625f;
+      }
+#pragma unroll
+      for (int w64 = 0; w64 < VW; ++w64) {
+#pragma unroll
+        for (int i = 4 * w64; i < 4 * w64 + 4; ++i) {
+          const int gi = i / 2 / gran;  // granule i / 2's group, whose offset sums lie in lanes 4 gi + t
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float base_sum = __shfl_sync(kFull, oo[nt][j], gi * 4 + t);
+            const int d = (i % 4 / 2) * 32 + 4 * g + (i % 2) * 2;  // within the 64 elements
+            const int col = 2 * t + j;
+            float2 v;
+            v.x = (o[i][nt][j] + base_sum) * (vinv * fac[j]);
+            v.y = (o[i][nt][j + 2] + base_sum) * (vinv * fac[j]);
+            *reinterpret_cast<float2*>(&exch[(warp * 8 + col) * 64 + d]) = v;
+          }
+        }
+        __syncthreads();
+        // 128 threads: column tid / 16, four elements each
+        const int col = tid / 16, d4 = tid % 16 * 4;
+        float4 sum = make_float4(0, 0, 0, 0);
+        float top = -FLT_MAX, den = 0.0f;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * RT + nt * 8 + col].x);
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 x = ml[w * RT + nt * 8 + col];
+          den = fmaf(x.y, ex2(x.x - top), den);
+          const float4 v = *reinterpret_cast<const float4*>(&exch[(w * 8 + col) * 64 + d4]);
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const int r = row0 + nt * 8 + col;
+        if (r < rows) {
+          if (whole) {
+            const bool none = den == 0.0f;
+            const float inv = none ? 0.0f : 1.0f / den;
+            const int64_t row = (int64_t)(cur.q0 + r / G) * a.q_heads + (int64_t)cur.kvh * G + r % G;
+            const int64_t at = row * D + 64 * w64 + d4;
+            sum.x *= inv, sum.y *= inv, sum.z *= inv, sum.w *= inv;
+            if (none) sum = make_float4(0, 0, 0, 0);
+            if constexpr (F32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = sum;
+            else
+              *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) =
+                  make_uint2(pack_half2(sum.x, sum.y), pack_half2(sum.z, sum.w));
+            if (a.lse && w64 == 0 && tid % 16 == 0)
+              a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
+          } else {
+            *reinterpret_cast<float4*>(slot + (nt * 8 + col) * D + 64 * w64 + d4) = sum;
+            if (w64 == 0 && tid % 16 == 0)
+              *reinterpret_cast<float2*>(slot + RT * D + (nt * 8 + col) * 2) = make_float2(top, den);
+          }
+        }
+        __syncthreads();
+      }
+    }
+    if (!from_start && ends && tid == 0) {
+      // the CTA that holds the sequence's first unit
+      const int64_t s0 = u0 + (u1 - u0 - left) - (cur.tile - cur.t0);
+      int64_t f = s0 * ncta / total;
+      while (f > 0 && f * total / ncta > s0) --f;
+      while ((f + 1) * total / ncta <= s0) ++f;
+      pieces[blockIdx.x] = {(int)f, cur.q0, row0, rows, cur.kvh};
+    }
+    left -= here;
+    cur.tile = tile_end;
+    if (left > 0 && ends) walk.next_part(cur);
+  }
+}
+
+// Joins the pieces of cut sequences: block x ends one (or returns); warp w takes column w / 4 of column
+// group y and every fourth piece.  o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order.
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(1024) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a) {
+  pdl_wait();
+  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32;
+  __shared__ float part[32][D + 2];
+  const Piece p = reinterpret_cast<const Piece*>(a.workspace)[blockIdx.x];
+  if (p.first < 0) return;
+  const float* slots = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int col = blockIdx.y * 8 + warp / 4, sub = warp % 4;
+  const int r = p.row0 + col;
+  const bool live = r < p.rows;
+  const int n = (int)blockIdx.x - p.first + 1;
+  auto slot_of = [&](int i) { return slots + ((int64_t)(p.first + i) * 2 + (i == 0 ? 1 : 0)) * kSlot; };
+  float top = -FLT_MAX;
+  if (live)
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, slot_of(i)[RT * D + col * 2]);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+  float acc[E] = {}, den = 0.0f;
+  if (live) {
+#pragma unroll 4
+    for (int i = sub; i < n; i += 4) {
+      const float* s = slot_of(i);
+      const float2 ml = *reinterpret_cast<const float2*>(s + RT * D + col * 2);
+      const float f = ex2(ml.x - top);
+      den = fmaf(ml.y, f, den);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(s + col * D + e * 32 + lane * 2);
+        acc[e] = fmaf(v.x, f, acc[e]);
+        acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[warp][(e / 2 * 32 + lane) * 2 + e % 2] = acc[e];
+  if (lane == 0) part[warp][D] = den;
+  __syncthreads();
+  if (!live || sub != 0) return;
+  den = (part[warp][D] + part[warp + 1][D]) + (part[warp + 2][D] + part[warp + 3][D]);
+  const int G = a.q_heads / c.kv_heads;
+  const int64_t row = (int64_t)(p.q0 + r / G) * a.q_heads + (int64_t)p.kvh * G + r % G;
+  const bool none = den == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / den;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = (e / 2 * 32 + lane) * 2 + e % 2;
+    float v = ((part[warp][d] + part[warp + 1][d]) + (part[warp + 2][d] + part[warp + 3][d])) * inv;
+    if (none) v = 0.0f;
+    if constexpr (F32) static_cast<float*>(a.out)[row * D + d] = v;
+    else static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(v);
+  }
+  if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
+}
+
+// CTAs an SM holds of the streaming kernel: by registers (128, 168 or 255 a thread).
+template <int D, int NT, bool F32>
+constexpr int stream_ctas() {
+  constexpr int o_regs = D / 4 * NT;
+  return o_regs <= 32 ? (F32 ? 3 : 4) : o_regs <= 64 ? 3 : 2;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a) {
+  constexpr int per_sm = stream_ctas<D, NT, F32>();
+  using L = Layout<D, NT, F32>;
+  const int budget = 227 * 1024 / per_sm - 1024;
+  const int stages = L::stages(c.block_bytes(), budget);
+  const int smem = L::kFixed + kWarps * stages * c.block_bytes();
+  auto kern = kv4_stream_kernel<D, NT, F32, per_sm>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = per_sm * (ctx.num_sms < 160 ? ctx.num_sms : 160);
+  e = launch_kernel(ctx, kern, dim3(grid), dim3(kWarps * 32), smem, c, a, stages, ctx.status);
+  if (e != cudaSuccess) return e;
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;  // the joining kernel waits for the streaming kernel on the device
+  e = launch_kernel(ctx, kv4_join_kernel<D, NT, F32>, dim3(grid, NT), dim3(1024), 0, c, a);
+  ctx.pdl = pdl;
+  return e;
+}
+
+}  // namespace kv4
+
+cudaError_t launch_kv4_stream_f16(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt);
+cudaError_t launch_kv4_stream_f32(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt);
+
+}  // namespace mnb
