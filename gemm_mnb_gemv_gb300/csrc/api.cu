@@ -644,7 +644,8 @@ namespace {
 bool kv4_geometry_ok(int num_pages, int page_size, int kv_heads, int head_dim, int group) {
   return num_pages >= 1 && page_size >= 16 && page_size <= 4096 && page_size % 16 == 0 && kv_heads >= 1 &&
          kv_heads <= 1024 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
-         (group == 32 || group == 64 || group == 128) && group <= head_dim;
+         (group == 32 || group == 64 || group == 128) && group <= head_dim &&
+         (uint64_t)num_pages * kv_heads * (page_size / 16) < 0xffffffffull;  // blocks have 32-bit numbers
 }
 
 mnb_status check_kv4(const char* fn, const mnb_kv4_cache& c, mnb::Kv4Cache* out) {

@@ -24,7 +24,10 @@ cudaError_t launch_kv4_attention(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Att
   static const char* names[2][3] = {{"kv4_stream_f16_rows8", "kv4_stream_f16_rows16", "kv4_stream_f16_rows32"},
                                     {"kv4_stream_f32_rows8", "kv4_stream_f32_rows16", ""}};
   ctx.variant = names[a.f32 ? 1 : 0][nt == 4 ? 2 : nt - 1];
-  return a.f32 ? launch_kv4_stream_f32(ctx, c, a, nt) : launch_kv4_stream_f16(ctx, c, a, nt);
+  if (c.head_dim == 64) return a.f32 ? launch_kv4_stream_d64_f32(ctx, c, a, nt) : launch_kv4_stream_d64_f16(ctx, c, a, nt);
+  if (c.head_dim == 128)
+    return a.f32 ? launch_kv4_stream_d128_f32(ctx, c, a, nt) : launch_kv4_stream_d128_f16(ctx, c, a, nt);
+  return a.f32 ? launch_kv4_stream_d256_f32(ctx, c, a, nt) : launch_kv4_stream_d256_f16(ctx, c, a, nt);
 }
 
 }  // namespace mnb

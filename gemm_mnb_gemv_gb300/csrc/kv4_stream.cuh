@@ -5,26 +5,28 @@
 // K side of O^T = V^T P^T.  The cache's codes go into the products as small integers:
 //   * K: the nibbles as they lie are fp16 subnormals (code * 2^-24, or * 2^-20 for the upper one of
 //     a byte, undone in q), so one AND makes two operand elements and q . code is exact; a group's
-//     scale multiplies its 32..128-element dot after it is formed, and the offsets join as one
-//     more MMA: sum_g offset_g * sum_{d in g} q_d, the row sums of q split into two fp16.
-//   * V: codes become c - 8 (exact), probabilities become fp16(p * scale_g * 2^x) per group, and one more
-//     MMA adds sum_j p_j (offset + 8 scale), split into two fp16.  Centring keeps the rounding
-//     of p * scale from being multiplied by |offset| / |v|.  The power 2^x follows the largest scale seen, so
-//     values of any size use fp16's whole range.
+//     scale multiplies its 32..128-element dot after it is formed, and offset_g * sum_{d in g} q_d is
+//     added in fp32.
+//   * V: codes become c - 8 (exact), probabilities become fp16(p * scale_g * 2^x) per group, and
+//     sum_j p_j (offset + 8 scale) is kept in fp32.  Centring keeps the rounding of p * scale from being
+//     multiplied by |offset| / |v|.  The power 2^x follows the largest scale seen, so values of any size use
+//     fp16's whole range.
 // A row's reference m moves only when a score passes it by 14 (in powers of two; one vote a
 // block instead of shuffles) and is then set 8 below the largest: p = 2^(s - m) <= 2^14, so
 // fp16 keeps probabilities down to 2^-22 of the largest normal.
 // fp32 activations: q and p are split into two fp16 (2^-22 together), products run once for each.
 //
-// Work: tiles of 64 keys of every (sequence, row tile, key head) in one list, cut into equal ranges, one
+// Work: tiles of 64 or 128 keys of every (sequence, row tile, key head) in one list, cut into equal ranges, one
 // per resident CTA, on the device from the lengths (ragged batches balance, graphs
-// follow new lengths).  Each of a CTA's four warps takes one 16-key block of a tile through its own
-// ring of bulk copies (one copy of 16 D + 128 ng bytes a block) that runs ahead across the ends of sequences; the
+// follow new lengths).  Each of a CTA's four warps takes one or two 16-key blocks of a tile through its own
+// ring of bulk copies (16 D + 128 ng bytes a block) that runs ahead across the ends of sequences; the
 // warps meet only at a sequence's end.  Pieces of a sequence cut by a range's end go to the workspace
 // as (m, l, o) and a second, dependent launch joins them in order.
 #pragma once
 
 #include <float.h>
+
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "mma_sync.cuh"
@@ -35,7 +37,9 @@ namespace mnb {
 namespace kv4 {
 
 constexpr int kWarps = 4;           // warps of a CTA
-constexpr int kTile = 16 * kWarps;  // keys of a work unit
+// What starting and ending a piece of a sequence costs, in tiles: counted where the work is cut, so
+// that a CTA with many short sequences gets fewer keys.
+constexpr int kPieceCost = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 8.0f;       // a row's reference is set this far below its largest score (log2)
 constexpr float kRise = 14.0f;      // and moves when a score passes it by this much
@@ -89,7 +93,7 @@ struct Cursor {
   int t0, t1;         // key tiles of row tile rt
 };
 
-template <int RT>
+template <int RT, int kTile>
 struct Walk {
   const Kv4Attention& a;
   const Kv4Cache& c;
@@ -115,7 +119,7 @@ struct Walk {
     int64_t u = 0;
     for (s.rt = 0; s.rt < s.R; ++s.rt) {
       range(s);
-      u += s.t1 - s.t0;
+      u += s.t1 - s.t0 + kPieceCost;
     }
     return u * c.kv_heads;
   }
@@ -137,41 +141,60 @@ struct Walk {
 };
 
 // Shared memory of a CTA.
-template <int D, int NT, bool F32>
+template <int D, int NG, int NT, int PB, bool F32>
 struct Layout {
+  static constexpr int kBlock = 16 * D + 128 * NG;                   // bytes of a cache block
   static constexpr int kQ = (D / 16) * NT * 32 * 8 * (F32 ? 2 : 1);  // q fragments
-  static constexpr int kQs = NT * 32 * 8;                            // row sums of q
+  static constexpr int kQs = NG * NT * 8 * 4;                        // row sums of q per group
   static constexpr int kCol = NT * 8 * 4;                            // score factors
   static constexpr int kEx = kWarps * 8 * 64 * 4;                    // exchange of 64 columns of o
   static constexpr int kMl = kWarps * NT * 8 * 8;                    // m, l of each warp
   static constexpr int kFixed = kQ + kQs + kCol + kEx + kMl + 1024;  // + barriers, flags, scan
-  static int stages(int block_bytes, int budget) {
-    const int s = (budget - kFixed) / (kWarps * block_bytes);
+  static constexpr int stages(int budget) {
+    const int s = (budget - kFixed) / (kWarps * PB * kBlock);
     return s < 2 ? 2 : s > 16 ? 16 : s;
   }
 };
 
-template <int D, int NT, bool F32, int kMinCtas>
-__global__ void __launch_bounds__(kWarps * 32, kMinCtas)
-    kv4_stream_kernel(const Kv4Cache c, const Kv4Attention a, int stages, uint32_t* status) {
+// CTAs an SM holds: by registers (128, 168 or 255 a thread).
+template <int D, int NT, bool F32>
+constexpr int stream_ctas() {
+  constexpr int o_regs = D / 4 * NT;
+  return o_regs <= 32 ? (F32 ? 3 : 4) : o_regs <= 64 ? 3 : 2;
+}
+
+// Cache blocks (of 16 keys) that a warp takes at a time: two where registers hold their scores, for
+// more independent chains and half the loop's own instructions.
+template <int D, int NT>
+constexpr int step_blocks() {
+  return D / 4 * NT <= 64 && NT <= 2 ? 2 : 1;
+}
+
+template <int D, int NG, int NT, bool F32>
+__global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
+    kv4_stream_kernel(const Kv4Cache c, const Kv4Attention a, uint64_t page_magic, uint32_t* status) {
   constexpr int RT = 8 * NT;
-  constexpr int KW = D / 32;  // 32-element granules
-  constexpr int VW = D / 64;  // V words of a lane's chunk
-  using L = Layout<D, NT, F32>;
+  constexpr int KW = D / 32;    // 32-element granules
+  constexpr int VW = D / 64;    // V words of a lane's chunk
+  constexpr int GR = KW / NG;   // granules of a group
+  constexpr int PB = step_blocks<D, NT>();
+  constexpr int kTile = 16 * PB * kWarps;  // keys of a work unit
+  using L = Layout<D, NG, NT, PB, F32>;
+  constexpr int block_bytes = L::kBlock, stage_bytes = PB * block_bytes;
+  constexpr int stages = L::stages(227 * 1024 / stream_ctas<D, NT, F32>() - 1024);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
-  const int block_bytes = c.block_bytes(), ng = c.ng(), gran = c.group / 32;
-  uint8_t* ring = smem + warp * stages * block_bytes;
-  uint8_t* fixed = smem + kWarps * stages * block_bytes;
+  uint8_t* ring = smem + warp * stages * stage_bytes;
+  uint8_t* fixed = smem + kWarps * stages * stage_bytes;
   uint2* qf = reinterpret_cast<uint2*>(fixed);
-  uint2* qsf = reinterpret_cast<uint2*>(fixed + L::kQ);
+  float* qsf = reinterpret_cast<float*>(fixed + L::kQ);
   float* colf = reinterpret_cast<float*>(fixed + L::kQ + L::kQs);
   float* exch = reinterpret_cast<float*>(fixed + L::kQ + L::kQs + L::kCol);
   float2* ml = reinterpret_cast<float2*>(fixed + L::kQ + L::kQs + L::kCol + L::kEx);
   uint8_t* misc = fixed + L::kQ + L::kQs + L::kCol + L::kEx + L::kMl;
-  uint64_t* full = reinterpret_cast<uint64_t*>(misc) + warp * 16;        // [stage]
-  int* flags = reinterpret_cast<int*>(misc + 512) + warp * 16;           // [stage] block is in the cache
-  int64_t* scan = reinterpret_cast<int64_t*>(misc + 768);                // [8]
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc) + warp * 16;  // [stage]
+  int* flags = reinterpret_cast<int*>(misc + 512) + warp * 16;     // [stage] bit i: block i was read
+  int64_t* scan = reinterpret_cast<int64_t*>(misc + 768);          // [8]
 
   if (lane < stages) mbar_init(&full[lane], 1);
   fence_mbar_init();
@@ -179,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
   pdl_wait();
 
   // ---- the range of this CTA ----
-  Walk<RT> walk{a, c, a.q_heads / c.kv_heads, a.table_stride * c.page_size};
+  Walk<RT, kTile> walk{a, c, a.q_heads / c.kv_heads, a.table_stride * c.page_size};
   const int G = walk.G;
   Cursor cur = {};
   int64_t total = 0;
@@ -238,68 +261,106 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
     }
   }
   cur.b = (int)scan[4];
-  int64_t off = scan[5];
-  walk.load(cur);
-  for (cur.rt = 0;; ++cur.rt) {
-    walk.range(cur);
-    const int64_t len = (int64_t)(cur.t1 - cur.t0) * c.kv_heads;
-    if (off < len) break;
-    off -= len;
+  int skipped;  // of the first piece's cost units, those of the CTA before
+  {
+    int64_t off = scan[5];
+    walk.load(cur);
+    for (cur.rt = 0;; ++cur.rt) {
+      walk.range(cur);
+      const int64_t len = (int64_t)(cur.t1 - cur.t0 + kPieceCost) * c.kv_heads;
+      if (off < len) break;
+      off -= len;
+    }
+    const int each = cur.t1 - cur.t0 + kPieceCost;
+    cur.kvh = (int)(off / each);
+    cur.tile = cur.t0 + max(0, (int)(off % each) - kPieceCost);
+    skipped = min((int)(off % each), kPieceCost);
   }
-  cur.kvh = (int)(off / (cur.t1 - cur.t0));
-  cur.tile = cur.t0 + (int)(off % (cur.t1 - cur.t0));
 
-  // ---- the producer: runs ahead of the consumer by up to `stages` blocks ----
+  // ---- the producer side of each warp: runs ahead of its consumer side by up to `stages` steps ----
+  // Block numbers come in batches, lane i holding the i-th next; the page indices of the batch
+  // after are on their way meanwhile.
+  constexpr uint32_t kNone = 0xfffffffeu;  // nothing to read: past the end, or not in the cache
+  const int ppb = c.page_size / 16;
   Cursor pro = cur;
-  int64_t pro_left = u1 - u0;
-  int pro_stage = 0;
-  int pro_page = 0;
-  // moves pro to the next unit whose block this warp has to read, and starts the load of its page index
-  auto seek = [&](bool step) {
-    while (true) {
-      if (step) {
-        if (--pro_left <= 0) return;
-        if (++pro.tile == pro.t1) walk.next_part(pro);
-      }
-      step = true;
+  int64_t pro_left = u1 - u0 + skipped;  // units, those of pro's piece cost included
+  int pro_stage = 0, issued = 0;         // issued: steps of the batch that are used up
+  int batch_n = 0, next_n = 0;           // steps of the batches
+  uint32_t batch_at = 0, next_in = 0;    // this lane's block number, and block within its page
+  int next_page = 0, next_kvh = 0;
+  bool pro_new = true;                   // the piece cost of pro's part is still to be taken off
+  auto fetch = [&]() {  // starts the next batch: tiles of one sequence and key head
+    next_n = 0;
+    while (next_n == 0) {
+      if (pro_new) pro_left -= kPieceCost, pro_new = false;
       if (pro_left <= 0) return;
-      const int base = pro.tile * kTile + warp * 16;
-      if (base < pro.n) {
-        pro_page = a.page_table[(int64_t)pro.b * a.table_stride + base / c.page_size];
-        return;
+      const int tiles = (int)min((int64_t)min(32 / PB, pro.t1 - pro.tile), pro_left);
+      const int first = pro.tile * kTile + warp * (16 * PB);  // this warp's first key
+      next_n = min(tiles, max(0, (pro.n - first + kTile - 1) / kTile));
+      const int key = first + lane / PB * kTile + lane % PB * 16;
+      next_page = -2;
+      if (lane < next_n * PB && key < pro.n) {
+        const uint32_t blk = (uint32_t)key / 16;
+        const uint32_t at = (uint32_t)((uint64_t)blk * page_magic >> 36);  // blk / ppb
+        next_in = blk - at * ppb;
+        next_page = max(a.page_table[(int64_t)pro.b * a.table_stride + at], -1);
       }
+      next_kvh = pro.kvh;
+      pro_left -= tiles;
+      pro.tile += tiles;
+      if (pro.tile == pro.t1 && pro_left > 0) walk.next_part(pro), pro_new = true;
     }
   };
   auto produce = [&]() {
-    if (pro_left <= 0) return;
-    const int base = pro.tile * kTile + warp * 16;
-    const bool ok = pro_page >= 0 && pro_page < c.num_pages;
+    if (issued == batch_n) {
+      if (next_n == 0) return;
+      batch_n = next_n;
+      issued = 0;
+      const bool ok = next_page >= 0 && next_page < c.num_pages;
+      if (next_page != -2 && !ok) report_status(status, kStatusBadIndex);
+      batch_at = ok ? ((uint32_t)next_page * c.kv_heads + next_kvh) * ppb + next_in : kNone;
+      fetch();
+    }
+    uint32_t at[PB];
+#pragma unroll
+    for (int i = 0; i < PB; ++i) at[i] = __shfl_sync(kFull, batch_at, issued * PB + i);
+    ++issued;
     if (lane == 0) {
-      flags[pro_stage] = ok;
-      if (ok) {
-        const uint8_t* src = c.pages + (((int64_t)pro_page * c.kv_heads + pro.kvh) * (c.page_size / 16) +
-                                        base % c.page_size / 16) * block_bytes;
-        mbar_arrive_expect_tx(&full[pro_stage], block_bytes);
-        bulk_g2s(ring + pro_stage * block_bytes, src, block_bytes, &full[pro_stage]);
+      uint64_t* bar = &full[pro_stage];
+      uint8_t* dst = ring + pro_stage * stage_bytes;
+      int have = 0;
+#pragma unroll
+      for (int i = 0; i < PB; ++i) have |= (at[i] != kNone) << i;
+      flags[pro_stage] = have;
+      if (have == 0) {
+        mbar_arrive(bar);
       } else {
-        report_status(status, kStatusBadIndex);
-        mbar_arrive(&full[pro_stage]);
+        mbar_arrive_expect_tx(bar, (have == 3 ? 2 : 1) * block_bytes);
+        if (PB == 2 && have == 3 && at[PB - 1] == at[0] + 1) {
+          bulk_g2s(dst, c.pages + (uint64_t)at[0] * block_bytes, 2 * block_bytes, bar);
+        } else {
+#pragma unroll
+          for (int i = 0; i < PB; ++i)
+            if (at[i] != kNone)
+              bulk_g2s(dst + i * block_bytes, c.pages + (uint64_t)at[i] * block_bytes, block_bytes, bar);
+        }
       }
     }
     if (++pro_stage == stages) pro_stage = 0;
-    seek(true);
   };
   __syncwarp();
-  seek(false);
+  fetch();
   for (int i = 0; i < stages; ++i) produce();
 
-  // ---- the consumer ----
+  // ---- the consumer side ----
   int stage = 0;
   uint32_t parity = 0;
   bool gave_up = false;
-  int64_t left = u1 - u0;
+  int64_t left = u1 - u0 + skipped;
   if (tid == 0) pieces[blockIdx.x].first = -1;
-  while (left > 0) {
+  while (true) {
+    left -= kPieceCost;
+    if (left <= 0) break;
     const bool from_start = cur.tile == cur.t0;
     const int row0 = cur.rt * RT, rows = cur.qlen * G;
     // q fragments of the row tile: warp w prepares the column groups w, w + 4, ..
@@ -337,11 +398,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
       }
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-      // rows are scaled by a power of two to [2^13, 2^14): the parts of q, its sums and the division
-      // by 16 then stay inside fp16
+      // rows are scaled by a power of two to [2^13, 2^14): the parts of q and its division by 16
+      // then stay inside fp16
       const int e = top > 0.0f && top < INFINITY ? min(max(ilogbf(top), -110), 127) - 13 : 0;
       const float down = scalbnf(1.0f, -e);
-      float sums[2] = {0.0f, 0.0f};  // of groups t and t + 4
       float acc = 0.0f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -350,12 +410,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
           q[i][j] *= down;
           acc += q[i][j];
         }
-        if ((i + 1) % gran == 0) {
+        if ((i + 1) % GR == 0) {
           acc += __shfl_xor_sync(kFull, acc, 1);
           acc += __shfl_xor_sync(kFull, acc, 2);
-          const int gi = i / gran;
-          if (gi == t) sums[0] = acc;
-          if (gi == t + 4) sums[1] = acc;
+          if (t == 0) qsf[(i / GR * NT + nt) * 8 + g] = acc * 5.9604644775390625e-8f;  // 2^-24, as the codes
           acc = 0.0f;
         }
 #pragma unroll
@@ -371,65 +429,61 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
           }
         }
       }
-      uint32_t sp[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float s = sums[j] * 0.00390625f;  // up to 2^21 * 2^-8
-        const float hi = __half2float(__float2half_rn(s));
-        sp[j] = pack_half2(hi, s - hi);
-      }
-      qsf[nt * 32 + lane] = make_uint2(sp[0], sp[1]);
       if (t == 0) colf[nt * 8 + g] = scalbnf(a.scale * kLog2e, e + 24);
     }
     __syncthreads();
 
     float cf[NT][2];
-    int lim_lo[NT][2], lim_hi[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = nt * 8 + 2 * t + j;
-        cf[nt][j] = colf[col];
-        const int pos = cur.n - cur.qlen + (row0 + col) / G;
-        lim_hi[nt][j] = a.causal ? min(cur.n, pos + 1) : cur.n;
-        lim_lo[nt][j] = a.window > 0 ? pos - a.window + 1 : 0;
-      }
+      for (int j = 0; j < 2; ++j) cf[nt][j] = colf[nt * 8 + 2 * t + j];
     // keys in [all_lo, all_hi) are seen by every row of the tile
     const int pos_a = cur.n - cur.qlen + row0 / G, pos_z = cur.n - cur.qlen + (row0 + RT - 1) / G;
     const int all_hi = a.causal ? min(cur.n, pos_a + 1) : cur.n;
     const int all_lo = a.window > 0 ? pos_z - a.window + 1 : 0;
-    uint2 qreg[NT == 1 ? D / 16 : 1];
-    if constexpr (NT == 1) {
+    auto sees = [&](int key, int col) {
+      const int pos = cur.n - cur.qlen + (row0 + col) / G;
+      return key < cur.n && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+    };
+    constexpr bool kQreg = NT == 1;
+    uint2 qreg[kQreg ? D / 16 : 1];
+    if constexpr (kQreg) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) qreg[i] = qf[i * 32 + lane];
     }
+    constexpr bool kQsReg = NG * NT <= 2;
+    float2 qsreg[kQsReg ? NG * NT : 1];
+    if constexpr (kQsReg) {
+#pragma unroll
+      for (int i = 0; i < NG * NT; ++i) qsreg[i] = *reinterpret_cast<const float2*>(&qsf[i * 8 + 2 * t]);
+    }
 
-    float m[NT][2], l[NT][2], o[D / 16][NT][4], oo[NT][4];
+    float m[NT][2], l[NT][2], o[D / 16][NT][4], oo[NG][NT][2];
     float vmul = 1.0f, vinv = 1.0f;
-    uint32_t vlim = 0;  // fp16 bits that V scales stay below
+    uint32_t vlim = 0x7bff0000u;  // fp16 pair: V scales stay up to this (offsets: any finite)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) m[nt][j] = -FLT_MAX, l[nt][j] = gave_up ? NAN : 0.0f;
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = -FLT_MAX, l[nt][j] = gave_up ? NAN : 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) oo[nt][j] = 0.0f;
+        for (int gi = 0; gi < NG; ++gi) oo[gi][nt][j] = 0.0f;
+      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][nt][j] = 0.0f;
     }
 
-    const int64_t here = min(left, (int64_t)(cur.t1 - cur.tile));
-    const int tile_end = cur.tile + (int)here;
-    for (int tile = cur.tile; tile < tile_end; ++tile) {
-      const int base = tile * kTile + warp * 16;
-      if (base >= cur.n) continue;
+    const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
+    const int tile_end = cur.tile + here;
+    for (int base = cur.tile * kTile + warp * (16 * PB); base < min(tile_end * kTile, cur.n); base += kTile) {
       if (!__all_sync(kFull, gave_up || mbar_wait_bounded(&full[stage], parity))) {
         // give up: no more copies, a last bounded wait for those in flight, NaN results
         if (lane == 0) report_status(status, kStatusFullWait);
         gave_up = true;
-        pro_left = 0;
+        pro_left = 0, next_n = 0, issued = batch_n;
         int st = stage;
         uint32_t ph = parity;
         do {
@@ -439,239 +493,219 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
       }
-      const uint8_t* blk = ring + stage * block_bytes;
-      if (flags[stage] && !gave_up) {
-        const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + 16 * D);
-        // ---- scores ----
-        float s[NT][4];
-        {
-          uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0;  // offsets of groups t, t + 4 for rows g, g + 8
-          if (t < ng) {
-            a0 = __byte_perm(par[t * 16 + g], 0, 0x3232);
-            a1 = __byte_perm(par[t * 16 + g + 8], 0, 0x3232);
-          }
-          if (t + 4 < ng) {
-            a2 = __byte_perm(par[(t + 4) * 16 + g], 0, 0x3232);
-            a3 = __byte_perm(par[(t + 4) * 16 + g + 8], 0, 0x3232);
-          }
+      const int have = flags[stage];
+      if (have && !gave_up) {
+        const uint32_t at = smem_u32(ring + stage * stage_bytes);
+        // ---- scores, in units of 1 / cf ----
+        float s[PB][NT][4];
+        uint32_t kw[PB][2][KW];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 b = qsf[nt * 32 + lane];
-            mma16816_zero(s[nt], a0, a1, a2, a3, b.x, b.y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[nt][j] *= 1.52587890625e-5f;  // 2^8 / 2^24
-          }
-        }
-        uint32_t kw[2][KW];
-        {
-          const uint32_t at = smem_u32(blk);
+        for (int p = 0; p < PB; ++p)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = g + 8 * h;
             if constexpr (D == 64) {
-              const uint2 v = lds_u64_a(at + r * 32 + t * 8);
-              kw[h][0] = v.x, kw[h][1] = v.y;
+              const uint2 v = lds_u64_a(at + p * block_bytes + r * 32 + t * 8);
+              kw[p][h][0] = v.x, kw[p][h][1] = v.y;
             } else {
 #pragma unroll
-              for (int p = 0; p < KW / 4; ++p) {
-                const uint4 v = lds128_a(at + k_word_byte<D>(r, t, 4 * p));
-                kw[h][4 * p] = v.x, kw[h][4 * p + 1] = v.y, kw[h][4 * p + 2] = v.z, kw[h][4 * p + 3] = v.w;
+              for (int k = 0; k < KW / 4; ++k) {
+                const uint4 v = lds128_a(at + p * block_bytes + k_word_byte<D>(r, t, 4 * k));
+                kw[p][h][4 * k] = v.x, kw[p][h][4 * k + 1] = v.y, kw[p][h][4 * k + 2] = v.z, kw[p][h][4 * k + 3] = v.w;
               }
             }
           }
-        }
         {
           // fp32: a scale after every 32 elements and the low parts first, as the tensor cores cut sums off at
           // fp32 and every further step would add an error of one last place of the running sum
-          float acc[NT][4];
+          constexpr int SG = F32 ? 1 : GR;
 #pragma unroll
-          for (int i = 0; i < KW; ++i) {
-            const bool first = F32 || i % gran == 0;
-            if (first) {
+          for (int gi = 0; gi < KW / SG; ++gi) {
+            float acc[PB][NT][4];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+            for (int i = gi * SG; i < (gi + 1) * SG; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[nt][j] = 0.0f;
+              for (int part = F32 ? 1 : 0; part >= 0; --part)
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+#pragma unroll
+                  for (int p = 0; p < PB; ++p) {
+                    const uint32_t x = kw[p][0][i] >> (8 * st), y = kw[p][1][i] >> (8 * st);
+                    const uint32_t a0 = x & 0x000f000fu, a2 = x & 0x00f000f0u, a1 = y & 0x000f000fu, a3 = y & 0x00f000f0u;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                      uint2 b;
+                      if (kQreg && part == 0) b = qreg[kQreg ? 2 * i + st : 0];
+                      else b = qf[((part * (D / 16) + 2 * i + st) * NT + nt) * 32 + lane];
+                      if (i == gi * SG && st == 0 && part == (F32 ? 1 : 0))
+                        mma16816_zero(acc[p][nt], a0, a1, a2, a3, b.x, b.y);
+                      else
+                        mma16816(acc[p][nt], a0, a1, a2, a3, b.x, b.y);
+                    }
+                  }
             }
+            const int grp = gi * SG / GR;
 #pragma unroll
-            for (int part = F32 ? 1 : 0; part >= 0; --part)
-#pragma unroll
-              for (int st = 0; st < 2; ++st) {
-                const uint32_t x = kw[0][i] >> (8 * st), y = kw[1][i] >> (8 * st);
-                const uint32_t a0 = x & 0x000f000fu, a2 = x & 0x00f000f0u, a1 = y & 0x000f000fu, a3 = y & 0x00f000f0u;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  uint2 b;
-                  if (NT == 1 && part == 0) b = qreg[NT == 1 ? 2 * i + st : 0];
-                  else b = qf[((part * (D / 16) + 2 * i + st) * NT + nt) * 32 + lane];
-                  mma16816(acc[nt], a0, a1, a2, a3, b.x, b.y);
-                }
-              }
-            if (F32 || (i + 1) % gran == 0) {
-              const int gi = i / gran;
-              const float s0 = half_bits_to_float(par[gi * 16 + g] & 0xffffu);
-              const float s1 = half_bits_to_float(par[gi * 16 + g + 8] & 0xffffu);
+            for (int p = 0; p < PB; ++p) {
+              const uint32_t kpar = at + p * block_bytes + 16 * D + g * 4 + grp * 64;  // rows g; g + 8 is 32 bytes on
+              const float2 p0 = unpack_half2(lds_u32_a(kpar)), p1 = unpack_half2(lds_u32_a(kpar + 32));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] = fmaf(acc[nt][0], s0, s[nt][0]);
-                s[nt][1] = fmaf(acc[nt][1], s0, s[nt][1]);
-                s[nt][2] = fmaf(acc[nt][2], s1, s[nt][2]);
-                s[nt][3] = fmaf(acc[nt][3], s1, s[nt][3]);
+                float* sp = s[p][nt];
+                if (gi * SG % GR == 0) {
+                  float2 qs;
+                  if constexpr (kQsReg) qs = qsreg[grp * NT + nt];
+                  else qs = *reinterpret_cast<const float2*>(&qsf[(grp * NT + nt) * 8 + 2 * t]);
+                  if (gi == 0) {
+                    sp[0] = p0.y * qs.x, sp[1] = p0.y * qs.y;
+                    sp[2] = p1.y * qs.x, sp[3] = p1.y * qs.y;
+                  } else {
+                    sp[0] = fmaf(p0.y, qs.x, sp[0]), sp[1] = fmaf(p0.y, qs.y, sp[1]);
+                    sp[2] = fmaf(p1.y, qs.x, sp[2]), sp[3] = fmaf(p1.y, qs.y, sp[3]);
+                  }
+                }
+                sp[0] = fmaf(acc[p][nt][0], p0.x, sp[0]), sp[1] = fmaf(acc[p][nt][1], p0.x, sp[1]);
+                sp[2] = fmaf(acc[p][nt][2], p1.x, sp[2]), sp[3] = fmaf(acc[p][nt][3], p1.x, sp[3]);
               }
             }
           }
         }
-        const int j0 = base + g, j1 = base + g + 8;
-        const bool masked = base < all_lo || base + 16 > all_hi;
+        const bool masked = base < all_lo || base + 16 * PB > all_hi || have != (1 << PB) - 1;
+        uint32_t vp[PB][NG][2];  // V parameters of rows g, g + 8
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int p = 0; p < PB; ++p) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[nt][j] *= cf[nt][j & 1];
-            if (masked) {
-              const int key = j < 2 ? j0 : j1;
-              if (key < lim_lo[nt][j & 1] || key >= lim_hi[nt][j & 1]) s[nt][j] = -INFINITY;
-            }
-          }
-        // ---- V scales; keys past the end hold anything ----
-        const bool in0 = j0 < cur.n, in1 = j1 < cur.n;
-        const uint32_t* vpar = par + ng * 16;
-        uint32_t vscale = 0, voff = 0;  // largest magnitudes, as fp16 bits
-        for (int gi = 0; gi < ng; ++gi) {
-          const uint32_t p0 = in0 ? vpar[gi * 16 + g] : 0u, p1 = in1 ? vpar[gi * 16 + g + 8] : 0u;
-          vscale = max(vscale, max(p0 & 0x7fffu, p1 & 0x7fffu));
-          voff = max(voff, max((p0 >> 16) & 0x7fffu, (p1 >> 16) & 0x7fffu));
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[p][nt][j] *= cf[nt][j & 1];
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              vp[p][gi][h] = lds_u32_a(at + p * block_bytes + 16 * D + NG * 64 + gi * 64 + h * 32 + g * 4);
         }
-        const bool odd = max(vscale, voff) >= 0x7c00u;  // an inf or NaN among the V parameters
-        uint32_t vtop = max(vscale, voff > 0x0c00u ? voff - 0x0c00u : 0u);  // max(scale, |offset| / 8)
-        bool rise = vtop > vlim;
+        if (masked) {
+#pragma unroll
+          for (int p = 0; p < PB; ++p) {
+            const int key = base + 16 * p + g;
+            const bool read = (have >> p & 1) != 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!read || !sees(key + (j >> 1) * 8, nt * 8 + 2 * t + (j & 1))) s[p][nt][j] = -INFINITY;
+            // keys past the end hold anything
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!read || key + 8 * h >= cur.n) vp[p][gi][h] = 0u;
+          }
+        }
+        // ---- references: rise when a score passes its row's, or a V scale its limit ----
+        uint32_t vtop = 0;  // fp16 pair of largest magnitudes, NaN if there is one
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t v = vp[p][gi][h] & 0x7fff7fffu;
+              if (p == 0 && gi == 0 && h == 0) vtop = v;
+              else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(vtop) : "r"(vtop), "r"(v));
+            }
+        bool rise = !__hble2(*reinterpret_cast<const __half2*>(&vtop), *reinterpret_cast<const __half2*>(&vlim));
+        float tops[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) rise |= s[nt][j] > m[nt][j & 1] + kRise;
-        bool any_odd = false;
-        if (__any_sync(kFull, rise || odd)) {
-          any_odd = __any_sync(kFull, odd);
-          vtop = __reduce_max_sync(kFull, odd ? 0u : vtop);
+          for (int j = 0; j < 2; ++j) {
+            tops[nt][j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+            if constexpr (PB == 2) tops[nt][j] = fmaxf(tops[nt][j], fmaxf(s[PB - 1][nt][j], s[PB - 1][nt][j + 2]));
+            rise |= tops[nt][j] > m[nt][j] + kRise;
+          }
+        if (__any_sync(kFull, rise)) {
+          // inf or NaN among the V parameters: rows that see such a key get NaN in its group, the others
+          // go on without the key's value (0 * NaN would reach them in the products)
+          const bool odd = (vtop & 0x7c00u) == 0x7c00u || (vtop & 0x7c000000u) == 0x7c000000u;
+          if (__any_sync(kFull, odd)) {
+            vtop = 0;
+#pragma unroll
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+              for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t v = vp[p][gi][h];
+                  if ((v & 0x7c00u) == 0x7c00u || (v & 0x7c000000u) == 0x7c000000u) {
+                    vp[p][gi][h] = 0u;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                      for (int j = 0; j < 2; ++j)
+                        if (sees(base + 16 * p + g + 8 * h, nt * 8 + 2 * t + j)) oo[gi][nt][j] = NAN;
+                  } else {
+                    vtop = __vmaxu2(vtop, v & 0x7fff7fffu);
+                  }
+                }
+          }
+          const uint32_t need = __reduce_max_sync(kFull, vtop & 0xffffu);
           float grow = 1.0f;
-          if (vtop > vlim) {
-            const int ex = vtop ? (int)(__float_as_uint(half_bits_to_float(vtop)) >> 23) - 127 : -24;
+          if (need > (vlim & 0xffffu)) {
+            const int ex = (int)(__float_as_uint(half_bits_to_float(need)) >> 23) - 127;
             const float mul = __uint_as_float((uint32_t)(127 - 2 - ex) << 23);  // scales up to vlim become at most 1
             grow = vinv * mul;
             vmul = mul;
             vinv = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
-            vlim = ex + 2 > 15 ? 0x7bffu : (uint32_t)__half_as_ushort(__float2half_rn(scalbnf(1.0f, ex + 2)));
+            const __half lim = __float2half_rn(fminf(scalbnf(1.0f, ex + 2), 65504.0f));
+            vlim = (uint32_t)__half_as_ushort(lim) | 0x7bff0000u;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(s[nt][j], s[nt][j + 2]);
+              float top = tops[nt][j];
 #pragma unroll
               for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, sh));
               top = top > m[nt][j] + kRise ? top - kLift : m[nt][j];  // a row's arithmetic hangs on its own scores alone
               const float al = ex2(m[nt][j] - top);
               m[nt][j] = top;
               l[nt][j] *= al;
+#pragma unroll
+              for (int gi = 0; gi < NG; ++gi) oo[gi][nt][j] *= al;
               const float ag = al * grow;
-              oo[nt][j] *= ag, oo[nt][j + 2] *= ag;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) o[i][nt][j] *= ag, o[i][nt][j + 2] *= ag;
             }
         }
         // ---- probabilities ----
-        uint32_t ph[NT][2], pl[F32 ? NT : 1][2];  // p as B fragments
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int p = 0; p < PB; ++p)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[nt][j] = ex2(s[nt][j] - m[nt][j & 1]);
-            l[nt][j & 1] += s[nt][j];
-          }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u = pack_half2(s[nt][2 * h], s[nt][2 * h + 1]);
-            ph[nt][h] = movmatrix(u);
-            if constexpr (F32) {
-              const float2 f = unpack_half2(u);
-              pl[nt][h] = movmatrix(pack_half2(s[nt][2 * h] - f.x, s[nt][2 * h + 1] - f.y));
+            for (int j = 0; j < 4; ++j) {
+              s[p][nt][j] = ex2(s[p][nt][j] - m[nt][j & 1]);
+              l[nt][j & 1] += s[p][nt][j];
             }
-          }
-        }
-        // ---- sum_j p_j (offset + 8 scale): row g of this product is group g ----
-        {
-          uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0, bad0 = 0, bad1 = 0;
-          if (g < ng) {
-            uint32_t hi[4], lo[4];
+        // ---- sum_j p_j scale_j (c_j - 8), and sum_j p_j (offset + 8 scale) per lane ----
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = 2 * t + (k & 1) + (k >> 1) * 8;
-              const uint32_t p = base + r < cur.n ? vpar[g * 16 + r] : 0u;
-              const bool nf = (p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u;
-              const float2 so = unpack_half2(nf ? 0u : p);
-              const float x = fmaf(so.x, 8.0f, so.y) * vmul * 1024.0f;  // |offset| <= 8, scale <= 1 in units of vinv
-              const __half h = __float2half_rn(x);
-              hi[k] = __half_as_ushort(h);
-              lo[k] = __half_as_ushort(__float2half_rn(x - __half2float(h)));
-              if (nf) {
-                if (k < 2) bad0 |= 0x3c00u << (16 * (k & 1));
-                else bad1 |= 0x3c00u << (16 * (k & 1));
-              }
-            }
-            a0 = hi[0] | hi[1] << 16, a2 = hi[2] | hi[3] << 16;
-            a1 = lo[0] | lo[1] << 16, a3 = lo[2] | lo[3] << 16;
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (F32) {
-              float acc[4];
-              mma16816_zero(acc, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-              mma16816(acc, a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) oo[nt][k] += acc[k];
-            } else {
-              mma16816(oo[nt], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-            }
-          }
-          if (any_odd) {
-            // which rows see a key whose group is not finite: a product of two 0 / 1 matrices
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t see[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int key = base + g + 8 * h;
-                uint32_t u = 0;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  if (key >= lim_lo[nt][j] && key < lim_hi[nt][j]) u |= 0x3c00u << (16 * j);
-                see[h] = movmatrix(u);
-              }
-              float hit[4];
-              mma16816_zero(hit, bad0, 0u, bad1, 0u, see[0], see[1]);
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (hit[j] > 0.0f) oo[nt][j] = __uint_as_float(0x7fffffffu);
-            }
-          }
-        }
-        // ---- sum_j p_j scale_j (c_j - 8) ----
-        {
+        for (int p = 0; p < PB; ++p) {
           uint32_t vw[4][VW];  // words of keys 2t, 2t + 1, 2t + 8, 2t + 9
-          const uint32_t at = smem_u32(blk) + 8 * D;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = 2 * t + 8 * h;
+            const uint32_t vat = at + p * block_bytes + 8 * D;
             if constexpr (D == 64) {
-              const uint2 v = lds_u64_a(at + v_word_byte<D>(g, r, 0));
+              const uint2 v = lds_u64_a(vat + v_word_byte<D>(g, r, 0));
               vw[2 * h][0] = v.x, vw[2 * h + 1][0] = v.y;
             } else if constexpr (D == 128) {
-              const uint4 v = lds128_a(at + v_word_byte<D>(g, r, 0));
+              const uint4 v = lds128_a(vat + v_word_byte<D>(g, r, 0));
               vw[2 * h][0] = v.x, vw[2 * h][1] = v.y, vw[2 * h + 1][0] = v.z, vw[2 * h + 1][1] = v.w;
             } else {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint4 v = lds128_a(at + v_word_byte<D>(g, r + k, 0));
+                const uint4 v = lds128_a(vat + v_word_byte<D>(g, r + k, 0));
                 vw[2 * h + k][0] = v.x, vw[2 * h + k][1] = v.y, vw[2 * h + k][2] = v.z, vw[2 * h + k][3] = v.w;
               }
             }
@@ -679,21 +713,20 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
           uint32_t bh[NT][2], bl[F32 ? NT : 1][2];
 #pragma unroll
           for (int i = 0; i < KW; ++i) {  // granule of 32 elements: word i / 2, half i % 2
-            if (i % gran == 0) {
-              const int gi = i / gran;
-              uint32_t p0 = in0 ? vpar[gi * 16 + g] & 0xffffu : 0u, p1 = in1 ? vpar[gi * 16 + g + 8] & 0xffffu : 0u;
-              if (any_odd) {
-                const uint32_t q0 = in0 ? vpar[gi * 16 + g] : 0u, q1 = in1 ? vpar[gi * 16 + g + 8] : 0u;
-                if ((q0 & 0x7c00u) == 0x7c00u || (q0 & 0x7c000000u) == 0x7c000000u) p0 = 0u;
-                if ((q1 & 0x7c00u) == 0x7c00u || (q1 & 0x7c000000u) == 0x7c000000u) p1 = 0u;
-              }
-              const float f0 = half_bits_to_float(p0) * vmul, f1 = half_bits_to_float(p1) * vmul;
+            if (i % GR == 0) {
+              const int gi = i / GR;
+              const float2 p0 = unpack_half2(vp[p][gi][0]), p1 = unpack_half2(vp[p][gi][1]);
+              const float x0 = fmaf(p0.x, 8.0f, p0.y), x1 = fmaf(p1.x, 8.0f, p1.y);
+              const float f0 = p0.x * vmul, f1 = p1.x * vmul;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt) {
+                const float* sp = s[p][nt];
+                oo[gi][nt][0] = fmaf(sp[0], x0, fmaf(sp[2], x1, oo[gi][nt][0]));
+                oo[gi][nt][1] = fmaf(sp[1], x0, fmaf(sp[3], x1, oo[gi][nt][1]));
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float f = h ? f1 : f0;
-                  const float x = s[nt][2 * h] * f, y = s[nt][2 * h + 1] * f;
+                  const float x = sp[2 * h] * f, y = sp[2 * h + 1] * f;
                   const uint32_t u = pack_half2(x, y);
                   bh[nt][h] = movmatrix(u);
                   if constexpr (F32) {
@@ -701,6 +734,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
                     bl[nt][h] = movmatrix(pack_half2(x - w.x, y - w.y));
                   }
                 }
+              }
             }
             const uint32_t sel = i % 2 ? 0x7632u : 0x5410u;
             uint32_t x = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel), y = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
@@ -735,7 +769,11 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], sh);
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], sh);
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) oo[gi][nt][j] += __shfl_xor_sync(kFull, oo[gi][nt][j], sh);
+        }
         if (g == 0) ml[warp * RT + nt * 8 + 2 * t + j] = make_float2(m[nt][j], l[nt][j]);
       }
     __syncthreads();
@@ -750,22 +788,19 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
         float top = -FLT_MAX;
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * RT + nt * 8 + 2 * t + j].x);
         fac[j] = ex2(m[nt][j] - top);
-        // the two fp16 parts of the offset sums: rows g and g + 8 of their product
-        oo[nt][j] = (oo[nt][j] + oo[nt][j + 2]) * 0.0009765625f;
       }
 #pragma unroll
       for (int w64 = 0; w64 < VW; ++w64) {
 #pragma unroll
         for (int i = 4 * w64; i < 4 * w64 + 4; ++i) {
-          const int gi = i / 2 / gran;  // granule i / 2's group, whose offset sums lie in lanes 4 gi + t
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float base_sum = __shfl_sync(kFull, oo[nt][j], gi * 4 + t);
+            const float base_sum = oo[i / 2 / GR][nt][j];
             const int d = (i % 4 / 2) * 32 + 4 * g + (i % 2) * 2;  // within the 64 elements
             const int col = 2 * t + j;
             float2 v;
-            v.x = (o[i][nt][j] + base_sum) * (vinv * fac[j]);
-            v.y = (o[i][nt][j + 2] + base_sum) * (vinv * fac[j]);
+            v.x = fmaf(o[i][nt][j], vinv, base_sum) * fac[j];
+            v.y = fmaf(o[i][nt][j + 2], vinv, base_sum) * fac[j];
             *reinterpret_cast<float2*>(&exch[(warp * 8 + col) * 64 + d]) = v;
           }
         }
@@ -808,7 +843,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
     }
     if (!from_start && ends && tid == 0) {
       // the CTA that holds the sequence's first unit
-      const int64_t s0 = u0 + (u1 - u0 - left) - (cur.tile - cur.t0);
+      const int64_t s0 = u1 - left - (cur.tile - cur.t0);
       int64_t f = s0 * ncta / total;
       while (f > 0 && f * total / ncta > s0) --f;
       while ((f + 1) * total / ncta <= s0) ++f;
@@ -816,7 +851,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
     }
     left -= here;
     cur.tile = tile_end;
-    if (left > 0 && ends) walk.next_part(cur);
+    if (left <= 0) break;
+    walk.next_part(cur);
   }
 }
 
@@ -877,25 +913,19 @@ __global__ void __launch_bounds__(1024) kv4_join_kernel(const Kv4Cache c, const 
   if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
 }
 
-// CTAs an SM holds of the streaming kernel: by registers (128, 168 or 255 a thread).
-template <int D, int NT, bool F32>
-constexpr int stream_ctas() {
-  constexpr int o_regs = D / 4 * NT;
-  return o_regs <= 32 ? (F32 ? 3 : 4) : o_regs <= 64 ? 3 : 2;
-}
-
-template <int D, int NT, bool F32>
+template <int D, int NG, int NT, bool F32>
 cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a) {
   constexpr int per_sm = stream_ctas<D, NT, F32>();
-  using L = Layout<D, NT, F32>;
-  const int budget = 227 * 1024 / per_sm - 1024;
-  const int stages = L::stages(c.block_bytes(), budget);
-  const int smem = L::kFixed + kWarps * stages * c.block_bytes();
-  auto kern = kv4_stream_kernel<D, NT, F32, per_sm>;
+  constexpr int PB = step_blocks<D, NT>();
+  using L = Layout<D, NG, NT, PB, F32>;
+  constexpr int smem = L::kFixed + kWarps * L::stages(227 * 1024 / per_sm - 1024) * PB * L::kBlock;
+  auto kern = kv4_stream_kernel<D, NG, NT, F32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int grid = per_sm * (ctx.num_sms < 160 ? ctx.num_sms : 160);
-  e = launch_kernel(ctx, kern, dim3(grid), dim3(kWarps * 32), smem, c, a, stages, ctx.status);
+  // n / ppb = n * magic >> 36 for n < 2^26 (2^30 tokens), ppb <= 256: n * ppb < 2^36
+  const uint64_t ppb = (uint64_t)(c.page_size / 16), magic = ((1ull << 36) + ppb - 1) / ppb;
+  e = launch_kernel(ctx, kern, dim3(grid), dim3(kWarps * 32), smem, c, a, magic, ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the joining kernel waits for the streaming kernel on the device
@@ -904,9 +934,31 @@ cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention&
   return e;
 }
 
+template <int D, bool F32>
+cudaError_t launch_stream_d(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt) {
+  constexpr bool kFour = D <= 128 && !F32;  // 32 rows: only where registers hold the accumulators
+  auto go = [&](auto ng) -> cudaError_t {
+    constexpr int NG = decltype(ng)::value;
+    if (nt == 1) return launch_stream<D, NG, 1, F32>(ctx, c, a);
+    if (nt == 2) return launch_stream<D, NG, 2, F32>(ctx, c, a);
+    if constexpr (kFour) return launch_stream<D, NG, 4, F32>(ctx, c, a);
+    return cudaErrorInvalidValue;
+  };
+  if (c.group == 32) return go(std::integral_constant<int, D / 32>{});
+  if (c.group == 64) return go(std::integral_constant<int, D / 64>{});
+  if constexpr (D >= 128) return go(std::integral_constant<int, D / 128>{});
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace kv4
 
-cudaError_t launch_kv4_stream_f16(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt);
-cudaError_t launch_kv4_stream_f32(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt);
+// One translation unit for each head size and activation type.
+#define MNB_KV4_STREAM(name) cudaError_t launch_kv4_stream_##name(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a, int nt)
+MNB_KV4_STREAM(d64_f16);
+MNB_KV4_STREAM(d64_f32);
+MNB_KV4_STREAM(d128_f16);
+MNB_KV4_STREAM(d128_f32);
+MNB_KV4_STREAM(d256_f16);
+MNB_KV4_STREAM(d256_f32);
 
 }  // namespace mnb

@@ -342,7 +342,7 @@ MNB_API mnb_status mnb_gemm_act_order_noalloc(const void *A, int M, mnb_weight w
  */
 typedef struct {
     uint8_t *pages;     /* num_pages * kv_heads * (page_size / 16) blocks, 16-byte aligned   */
-    int32_t num_pages;  /* >= 1                                                              */
+    int32_t num_pages;  /* >= 1, and fewer than 2^32 - 1 blocks in all                       */
     int32_t page_size;  /* tokens in a page: a multiple of 16, at most 4096                  */
     int32_t kv_heads;   /* 1 .. 1024                                                         */
     int32_t head_dim;   /* 64, 128 or 256                                                    */
