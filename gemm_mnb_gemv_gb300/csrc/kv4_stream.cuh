@@ -39,7 +39,7 @@ namespace kv4 {
 constexpr int kWarps = 4;           // warps of a CTA
 // What starting and ending a piece of a sequence costs, in tiles: counted where the work is cut, so
 // that a CTA with many short sequences gets fewer keys.
-constexpr int kPieceCost = 2;
+constexpr int kPieceCost = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 8.0f;       // a row's reference is set this far below its largest score (log2)
 constexpr float kRise = 14.0f;      // and moves when a score passes it by this much
@@ -50,6 +50,25 @@ constexpr int kMaxCtas = 160 * 4;
 struct Piece {  // what the joining kernel needs of a cut sequence, written by the CTA of its last piece
   int first;    // CTA of the first piece, -1: this CTA ends no cut sequence
   int q0, row0, rows, kvh;
+};
+
+// a / b for a, b >= 0: 32 bits where they are enough (a 64-bit division is a subroutine).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// `total` units over `parts` CTAs: each gets `each` or, the first `extra` of them, one more.
+struct Cut {
+  int64_t each, extra;
+  __device__ __forceinline__ Cut(int64_t total, int64_t parts) {
+    each = quotient(total, parts);
+    extra = total - each * parts;
+  }
+  __device__ __forceinline__ int64_t start(int64_t part) const { return part * each + min(part, extra); }
+  __device__ __forceinline__ int64_t part_of(int64_t unit) const {
+    const int64_t head = extra * (each + 1);
+    return unit < head ? quotient(unit, each + 1) : extra + quotient(unit - head, each);
+  }
 };
 
 // 8 x 8 transpose of 16-bit elements across the warp.
@@ -194,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
   uint8_t* misc = fixed + L::kQ + L::kQs + L::kCol + L::kEx + L::kMl;
   uint64_t* full = reinterpret_cast<uint64_t*>(misc) + warp * 16;  // [stage]
   int* flags = reinterpret_cast<int*>(misc + 512) + warp * 16;     // [stage] bit i: block i was read
-  int64_t* scan = reinterpret_cast<int64_t*>(misc + 768);          // [8]
+  int64_t* scan = reinterpret_cast<int64_t*>(misc + 768);          // [10]
 
   if (lane < stages) mbar_init(&full[lane], 1);
   fence_mbar_init();
@@ -228,7 +247,8 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
     if (tid == 0) pieces[blockIdx.x].first = -1;
     return;
   }
-  const int64_t u0 = blockIdx.x * total / ncta, u1 = (blockIdx.x + 1) * total / ncta;
+  const Cut cut(total, ncta);
+  const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
   // the sequence that holds unit u0: 128 sequences a turn, prefix sums
   {
     int64_t before = 0;
@@ -254,6 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       if (u0 >= lo && u0 < hi) {
         scan[4] = b0 + tid;
         scan[5] = u0 - lo;
+        scan[6] = cur.q0, scan[7] = cur.qlen, scan[8] = cur.n, scan[9] = cur.R;
       }
       before += scan[0] + scan[1] + scan[2] + scan[3];
       __syncthreads();
@@ -264,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
   int skipped;  // of the first piece's cost units, those of the CTA before
   {
     int64_t off = scan[5];
-    walk.load(cur);
+    cur.q0 = (int)scan[6], cur.qlen = (int)scan[7], cur.n = (int)scan[8], cur.R = (int)scan[9];
     for (cur.rt = 0;; ++cur.rt) {
       walk.range(cur);
       const int64_t len = (int64_t)(cur.t1 - cur.t0 + kPieceCost) * c.kv_heads;
@@ -272,9 +293,10 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       off -= len;
     }
     const int each = cur.t1 - cur.t0 + kPieceCost;
-    cur.kvh = (int)(off / each);
-    cur.tile = cur.t0 + max(0, (int)(off % each) - kPieceCost);
-    skipped = min((int)(off % each), kPieceCost);
+    cur.kvh = (int)quotient(off, each);
+    const int rest = (int)(off - (int64_t)cur.kvh * each);
+    cur.tile = cur.t0 + max(0, rest - kPieceCost);
+    skipped = min(rest, kPieceCost);
   }
 
   // ---- the producer side of each warp: runs ahead of its consumer side by up to `stages` steps ----
@@ -348,6 +370,27 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
     }
     if (++pro_stage == stages) pro_stage = 0;
   };
+  // q rows of one column group as they lie: all warps the same one (NT = 1), or warp w group w
+  constexpr int kRaw = KW * (F32 ? 2 : 1);
+  const int my_nt = NT == 1 ? 0 : warp;
+  uint4 raw[kRaw];
+  auto load_q = [&](const Cursor& s) {
+    const int r = s.rt * RT + my_nt * 8 + g;
+    const bool live = my_nt < NT && r < s.qlen * G;
+    const int tok = live ? r / G : 0, head = live ? r - tok * G : 0;
+    const int64_t at = (int64_t)(s.q0 + tok) * a.q_stride + ((int64_t)s.kvh * G + head) * D + 8 * t;
+#pragma unroll
+    for (int i = 0; i < kRaw; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (live) {
+        if constexpr (F32)
+          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at + 32 * (i / 2) + 4 * (i % 2));
+        else
+          raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at + 32 * i);
+      }
+    }
+  };
+  load_q(cur);
   __syncwarp();
   fetch();
   for (int i = 0; i < stages; ++i) produce();
@@ -358,35 +401,26 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
   bool gave_up = false;
   int64_t left = u1 - u0 + skipped;
   if (tid == 0) pieces[blockIdx.x].first = -1;
-  while (true) {
-    left -= kPieceCost;
-    if (left <= 0) break;
+  left -= kPieceCost;
+  while (left > 0) {
     const bool from_start = cur.tile == cur.t0;
     const int row0 = cur.rt * RT, rows = cur.qlen * G;
-    // q fragments of the row tile: warp w prepares the column groups w, w + 4, ..
-    for (int nt = warp; nt < NT; nt += kWarps) {
-      const int r = row0 + nt * 8 + g;
-      const bool live = r < rows;
+    constexpr bool kQreg = NT == 1;  // one column group: its fragments stay in registers, no CTA barrier
+    uint2 qreg[kQreg ? D / 16 : 1];
+    float cf[NT][2];
+    constexpr bool kQsReg = NG * NT <= 2 || NT == 1;
+    float2 qsreg[kQsReg ? NG * NT : 1];
+    if (my_nt < NT) {
       float q[KW][8], top = 0.0f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
-        const int64_t at = (int64_t)(cur.q0 + (live ? r / G : 0)) * a.q_stride +
-                           ((int64_t)cur.kvh * G + (live ? r % G : 0)) * D + 32 * i + 8 * t;
-        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-        if (live) {
-          if constexpr (F32) {
-            v0 = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
-            v1 = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at + 4);
-          } else {
-            v0 = *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at);
-          }
-        }
         if constexpr (F32) {
+          const uint4 v0 = raw[2 * i], v1 = raw[2 * i + 1];
           const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) q[i][j] = __uint_as_float(u[j]);
         } else {
-          const uint32_t u[4] = {v0.x, v0.y, v0.z, v0.w};
+          const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 f = unpack_half2(u[j]);
@@ -400,8 +434,9 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
       // rows are scaled by a power of two to [2^13, 2^14): the parts of q and its division by 16
       // then stay inside fp16
-      const int e = top > 0.0f && top < INFINITY ? min(max(ilogbf(top), -110), 127) - 13 : 0;
-      const float down = scalbnf(1.0f, -e);
+      const int ex = (int)(__float_as_uint(top) >> 23) - 127;  // subnormal rows count as 2^-127
+      const int e = top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       float acc = 0.0f;
 #pragma unroll
       for (int i = 0; i < KW; ++i) {
@@ -413,7 +448,11 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
         if ((i + 1) % GR == 0) {
           acc += __shfl_xor_sync(kFull, acc, 1);
           acc += __shfl_xor_sync(kFull, acc, 2);
-          if (t == 0) qsf[(i / GR * NT + nt) * 8 + g] = acc * 5.9604644775390625e-8f;  // 2^-24, as the codes
+          acc *= 5.9604644775390625e-8f;  // 2^-24, as the codes
+          if constexpr (NT == 1)
+            qsreg[i / GR] = make_float2(__shfl_sync(kFull, acc, 8 * t), __shfl_sync(kFull, acc, 8 * t + 4));
+          else if (t == 0)
+            qsf[(i / GR * NT + my_nt) * 8 + g] = acc;
           acc = 0.0f;
         }
 #pragma unroll
@@ -421,23 +460,35 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
           const float x0 = q[i][2 * s], x1 = q[i][2 * s + 4];
           const float y0 = q[i][2 * s + 1] * 0.0625f, y1 = q[i][2 * s + 5] * 0.0625f;
           const uint2 hi = make_uint2(pack_half2(x0, x1), pack_half2(y0, y1));
-          qf[((2 * i + s) * NT + nt) * 32 + lane] = hi;
-          if constexpr (F32) {
+          if constexpr (kQreg) qreg[2 * i + s] = hi;
+          else qf[((2 * i + s) * NT + my_nt) * 32 + lane] = hi;
+          if constexpr (F32) {  // NT = 1: every warp writes, and reads, the same values
             const float2 hx = unpack_half2(hi.x), hy = unpack_half2(hi.y);
-            qf[((D / 16 + 2 * i + s) * NT + nt) * 32 + lane] =
+            qf[((D / 16 + 2 * i + s) * NT + my_nt) * 32 + lane] =
                 make_uint2(pack_half2(x0 - hx.x, x1 - hx.y), pack_half2(y0 - hy.x, y1 - hy.y));
           }
         }
       }
-      if (t == 0) colf[nt * 8 + g] = scalbnf(a.scale * kLog2e, e + 24);
+      const float fac = scalbnf(a.scale * kLog2e, e + 24);
+      if constexpr (NT == 1)
+        cf[0][0] = __shfl_sync(kFull, fac, 8 * t), cf[0][1] = __shfl_sync(kFull, fac, 8 * t + 4);
+      else if (t == 0)
+        colf[my_nt * 8 + g] = fac;
     }
-    __syncthreads();
+    if constexpr (NT == 1) {
+      __syncwarp();
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) cf[nt][j] = colf[nt * 8 + 2 * t + j];
+      if constexpr (kQsReg) {
+#pragma unroll
+        for (int i = 0; i < NG * NT; ++i) qsreg[i] = *reinterpret_cast<const float2*>(&qsf[i * 8 + 2 * t]);
+      }
+    }
 
-    float cf[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) cf[nt][j] = colf[nt * 8 + 2 * t + j];
     // keys in [all_lo, all_hi) are seen by every row of the tile
     const int pos_a = cur.n - cur.qlen + row0 / G, pos_z = cur.n - cur.qlen + (row0 + RT - 1) / G;
     const int all_hi = a.causal ? min(cur.n, pos_a + 1) : cur.n;
@@ -446,19 +497,6 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       const int pos = cur.n - cur.qlen + (row0 + col) / G;
       return key < cur.n && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
     };
-    constexpr bool kQreg = NT == 1;
-    uint2 qreg[kQreg ? D / 16 : 1];
-    if constexpr (kQreg) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) qreg[i] = qf[i * 32 + lane];
-    }
-    constexpr bool kQsReg = NG * NT <= 2;
-    float2 qsreg[kQsReg ? NG * NT : 1];
-    if constexpr (kQsReg) {
-#pragma unroll
-      for (int i = 0; i < NG * NT; ++i) qsreg[i] = *reinterpret_cast<const float2*>(&qsf[i * 8 + 2 * t]);
-    }
-
     float m[NT][2], l[NT][2], o[D / 16][NT][4], oo[NG][NT][2];
     float vmul = 1.0f, vinv = 1.0f;
     uint32_t vlim = 0x7bff0000u;  // fp16 pair: V scales stay up to this (offsets: any finite)
@@ -763,6 +801,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       produce();
     }
 
+    left -= here;
     // ---- the end of this piece: join the four warps ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -843,74 +882,120 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
     }
     if (!from_start && ends && tid == 0) {
       // the CTA that holds the sequence's first unit
-      const int64_t s0 = u1 - left - (cur.tile - cur.t0);
-      int64_t f = s0 * ncta / total;
-      while (f > 0 && f * total / ncta > s0) --f;
-      while ((f + 1) * total / ncta <= s0) ++f;
-      pieces[blockIdx.x] = {(int)f, cur.q0, row0, rows, cur.kvh};
+      const int64_t s0 = u1 - left - here - (cur.tile - cur.t0);
+      pieces[blockIdx.x] = {(int)cut.part_of(s0), cur.q0, row0, rows, cur.kvh};
     }
-    left -= here;
-    cur.tile = tile_end;
-    if (left <= 0) break;
+    if (left <= kPieceCost) break;
+    left -= kPieceCost;
     walk.next_part(cur);
+    load_q(cur);
   }
 }
 
-// Joins the pieces of cut sequences: block x ends one (or returns); warp w takes column w / 4 of column
-// group y and every fourth piece.  o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order.
+// Joins the pieces of cut sequences: o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order. Each
+// block lists the cut sequences from the CTAs' entries; teams of four warps take their rows
+// in turn, each warp every fourth piece, ten of them in flight.
+constexpr int kJoinWarps = 16, kTeam = 4;
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(1024) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a, int ctas) {
+  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = 10;
+  __shared__ float part[kJoinWarps][D + 4];  // o, then l and m
+  __shared__ int list[kMaxCtas];
+  __shared__ int count[kJoinWarps + 1];
   pdl_wait();
-  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32;
-  __shared__ float part[32][D + 2];
-  const Piece p = reinterpret_cast<const Piece*>(a.workspace)[blockIdx.x];
-  if (p.first < 0) return;
+  const Piece* pieces = reinterpret_cast<const Piece*>(a.workspace);
   const float* slots = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int col = blockIdx.y * 8 + warp / 4, sub = warp % 4;
-  const int r = p.row0 + col;
-  const bool live = r < p.rows;
-  const int n = (int)blockIdx.x - p.first + 1;
-  auto slot_of = [&](int i) { return slots + ((int64_t)(p.first + i) * 2 + (i == 0 ? 1 : 0)) * kSlot; };
-  float top = -FLT_MAX;
-  if (live)
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, slot_of(i)[RT * D + col * 2]);
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  float acc[E] = {}, den = 0.0f;
-  if (live) {
-#pragma unroll 4
-    for (int i = sub; i < n; i += 4) {
-      const float* s = slot_of(i);
-      const float2 ml = *reinterpret_cast<const float2*>(s + RT * D + col * 2);
-      const float f = ex2(ml.x - top);
-      den = fmaf(ml.y, f, den);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kTeam;
+  int n_list = 0;
+  for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
+    const int i = i0 + threadIdx.x;
+    const bool has = i < ctas && pieces[i].first >= 0;
+    const uint32_t vote = __ballot_sync(kFull, has);
+    if (lane == 0) count[warp] = __popc(vote);
+    __syncthreads();
+    int at = n_list, all = 0;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) at += count[w];
+      all += count[w];
+    }
+    if (has) list[at + __popc(vote & ((1u << lane) - 1))] = i;
+    n_list += all;
+    __syncthreads();
+  }
+  const int G = a.q_heads / c.kv_heads;
+  const int teams = kJoinWarps / kTeam;
+  const int items = n_list * RT;
+  for (int item0 = blockIdx.x * teams; item0 < items; item0 += gridDim.x * teams) {
+    const int item = item0 + warp / kTeam;
+    const int last = item < items ? list[item / RT] : 0, col = item % RT;
+    Piece p = {};
+    if (item < items) p = pieces[last];
+    const bool live = item < items && p.row0 + col < p.rows;
+    const int n = live ? last - p.first + 1 : 0;
+    float m = -FLT_MAX, l = 0.0f, acc[E] = {};
+    for (int i0 = sub; i0 < n; i0 += kTeam * kFlight) {
+      float2 ml[kFlight];
+      float v[kFlight][E];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(s + col * D + e * 32 + lane * 2);
-        acc[e] = fmaf(v.x, f, acc[e]);
-        acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
+      for (int k = 0; k < kFlight; ++k) {
+        const int i = i0 + k * kTeam;
+        ml[k] = make_float2(-FLT_MAX, 0.0f);
+        if (i < n) {
+          const float* s = slots + ((int64_t)(p.first + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
+          ml[k] = *reinterpret_cast<const float2*>(s + RT * D + col * 2);
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(s + col * D + e * 32 + lane * 2);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) top = fmaxf(top, ml[k].x);
+      const float al = ex2(m - top);
+      m = top;
+      l *= al;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= al;
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        if (i0 + k * kTeam < n) {
+          const float f = ex2(ml[k].x - top);
+          l = fmaf(ml[k].y, f, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], f, acc[e]);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) part[warp][(e / 2 * 32 + lane) * 2 + e % 2] = acc[e];
-  if (lane == 0) part[warp][D] = den;
-  __syncthreads();
-  if (!live || sub != 0) return;
-  den = (part[warp][D] + part[warp + 1][D]) + (part[warp + 2][D] + part[warp + 3][D]);
-  const int G = a.q_heads / c.kv_heads;
-  const int64_t row = (int64_t)(p.q0 + r / G) * a.q_heads + (int64_t)p.kvh * G + r % G;
-  const bool none = den == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / den;
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&part[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
+    if (lane == 0) part[warp][D] = l, part[warp][D + 1] = m;
+    __syncthreads();
+    if (live && sub == 0) {
+      float top = part[warp][D + 1];
+      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, part[warp + w][D + 1]);
+      float den = 0.0f, f[kTeam];
+      for (int w = 0; w < kTeam; ++w) {
+        f[w] = ex2(part[warp + w][D + 1] - top);
+        den = fmaf(part[warp + w][D], f[w], den);
+      }
+      const int r = p.row0 + col;
+      const int64_t row = (int64_t)(p.q0 + r / G) * a.q_heads + (int64_t)p.kvh * G + r % G;
+      const bool none = den == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / den;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int d = (e / 2 * 32 + lane) * 2 + e % 2;
-    float v = ((part[warp][d] + part[warp + 1][d]) + (part[warp + 2][d] + part[warp + 3][d])) * inv;
-    if (none) v = 0.0f;
-    if constexpr (F32) static_cast<float*>(a.out)[row * D + d] = v;
-    else static_cast<__half*>(a.out)[row * D + d] = __float2half_rn(v);
+      for (int e = 0; e < E; e += 2) {
+        const int d = e * 32 + lane * 2;
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int w = 0; w < kTeam; ++w) v.x = fmaf(part[warp + w][d], f[w], v.x), v.y = fmaf(part[warp + w][d + 1], f[w], v.y);
+        v.x *= inv, v.y *= inv;
+        if (none) v = make_float2(0.0f, 0.0f);
+        if constexpr (F32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + d) = v;
+        else *reinterpret_cast<uint32_t*>(static_cast<__half*>(a.out) + row * D + d) = pack_half2(v.x, v.y);
+      }
+      if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
+    }
+    __syncthreads();
   }
-  if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
 }
 
 template <int D, int NG, int NT, bool F32>
@@ -929,7 +1014,7 @@ cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention&
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the joining kernel waits for the streaming kernel on the device
-  e = launch_kernel(ctx, kv4_join_kernel<D, NT, F32>, dim3(grid, NT), dim3(1024), 0, c, a);
+  e = launch_kernel(ctx, kv4_join_kernel<D, NT, F32>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
   ctx.pdl = pdl;
   return e;
 }
