@@ -24,72 +24,22 @@
 // as (m, l, o) and a second, dependent launch joins them in order.
 #pragma once
 
-#include <float.h>
-
 #include <type_traits>
 
-#include "kv4.cuh"
+#include "kv4_work.cuh"
 #include "mma_sync.cuh"
-#include "mnb_device.cuh"
-#include "mnb_internal.h"
 
 namespace mnb {
 namespace kv4 {
 
-constexpr int kWarps = 4;           // warps of a CTA
-// What starting and ending a piece of a sequence costs, in tiles: counted where the work is cut, so
-// that a CTA with many short sequences gets fewer keys.
-constexpr int kPieceCost = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLift = 8.0f;       // a row's reference is set this far below its largest score (log2)
-constexpr float kRise = 14.0f;      // and moves when a score passes it by this much
-
-// Largest number of CTAs a launch may have: the workspace's sizing.
-constexpr int kMaxCtas = 160 * 4;
-
-struct Piece {  // what the joining kernel needs of a cut sequence, written by the CTA of its last piece
-  int first;    // CTA of the first piece, -1: this CTA ends no cut sequence
-  int q0, row0, rows, kvh;
-};
-
-// a / b for a, b >= 0: 32 bits where they are enough (a 64-bit division is a subroutine).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// `total` units over `parts` CTAs: each gets `each` or, the first `extra` of them, one more.
-struct Cut {
-  int64_t each, extra;
-  __device__ __forceinline__ Cut(int64_t total, int64_t parts) {
-    each = quotient(total, parts);
-    extra = total - each * parts;
-  }
-  __device__ __forceinline__ int64_t start(int64_t part) const { return part * each + min(part, extra); }
-  __device__ __forceinline__ int64_t part_of(int64_t unit) const {
-    const int64_t head = extra * (each + 1);
-    return unit < head ? quotient(unit, each + 1) : extra + quotient(unit - head, each);
-  }
-};
+constexpr int kWarps = 4;      // warps of a CTA
+constexpr int kPieceCost = 4;  // 2: 85.9 us for 64 ragged contexts, 1: 97.0, 4: 81.6
 
 // 8 x 8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t u) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
 // Two V code pairs to fp16 c - 8: the lower and the upper nibble of each byte pair position.
@@ -104,66 +54,11 @@ __device__ __forceinline__ uint32_t v_upper(uint32_t x) {
   return r;
 }
 
-// One sequence's place in the work list.
-struct Cursor {
-  int b, rt, kvh, tile;
-  int q0, qlen, n;    // query rows and keys of sequence b
-  int R;              // row tiles of sequence b
-  int t0, t1;         // key tiles of row tile rt
-};
-
-template <int RT, int kTile>
-struct Walk {
-  const Kv4Attention& a;
-  const Kv4Cache& c;
-  int G, capacity;
-
-  __device__ __forceinline__ void load(Cursor& s) const {
-    const int lo = min(max(a.q_start[s.b], 0), a.T), hi = min(max(a.q_start[s.b + 1], lo), a.T);
-    s.q0 = lo;
-    s.qlen = hi - lo;
-    s.n = min(max(a.kv_len[s.b], 0), capacity);
-    s.R = (int)(((int64_t)s.qlen * G + RT - 1) / RT);
-  }
-  // key tiles that some row of row tile rt sees
-  __device__ __forceinline__ void range(Cursor& s) const {
-    const int first = s.rt * RT / G, last = min(s.qlen - 1, (s.rt * RT + RT - 1) / G);
-    const int64_t pos0 = (int64_t)s.n - s.qlen + first, pos1 = (int64_t)s.n - s.qlen + last;
-    const int64_t hi = a.causal ? min((int64_t)s.n, pos1 + 1) : s.n;
-    const int64_t lo = a.window > 0 ? max((int64_t)0, pos0 - a.window + 1) : 0;
-    s.t0 = (int)(lo / kTile);
-    s.t1 = max(s.t0 + 1, (int)((max(hi, (int64_t)0) + kTile - 1) / kTile));  // a row tile without keys still has a unit: it writes zeros
-  }
-  __device__ __forceinline__ int64_t units(Cursor s) const {  // of sequence s.b, loaded
-    int64_t u = 0;
-    for (s.rt = 0; s.rt < s.R; ++s.rt) {
-      range(s);
-      u += s.t1 - s.t0 + kPieceCost;
-    }
-    return u * c.kv_heads;
-  }
-  __device__ __forceinline__ void next_part(Cursor& s) const {  // to the first tile of the next row tile or key head
-    if (++s.kvh == c.kv_heads) {
-      s.kvh = 0;
-      if (++s.rt == s.R) {
-        s.rt = 0;
-        do {
-          ++s.b;
-          if (s.b >= a.batch) return;  // past the end: not used
-          load(s);
-        } while (s.R == 0);
-      }
-      range(s);
-    }
-    s.tile = s.t0;
-  }
-};
-
 // Shared memory of a CTA.
 template <int D, int NG, int NT, int PB, bool F32>
 struct Layout {
   static constexpr int kBlock = 16 * D + 128 * NG;                   // bytes of a cache block
-  static constexpr int kQ = (D / 16) * NT * 32 * 8 * (F32 ? 2 : 1);  // q fragments
+  static constexpr int kQ = (D / 16) * NT * 32 * 8 * (F32 ? 2 : NT > 1 ? 1 : 0);  // q fragments
   static constexpr int kQs = NG * NT * 8 * 4;                        // row sums of q per group
   static constexpr int kCol = NT * 8 * 4;                            // score factors
   static constexpr int kEx = kWarps * 8 * 64 * 4;                    // exchange of 64 columns of o
@@ -221,83 +116,20 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
   pdl_wait();
 
   // ---- the range of this CTA ----
-  Walk<RT, kTile> walk{a, c, a.q_heads / c.kv_heads, a.table_stride * c.page_size};
+  const Walk<RT, kTile, kPieceCost> walk(a, c);
   const int G = walk.G;
-  Cursor cur = {};
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
-    if (b0 + tid < a.batch) {
-      cur.b = b0 + tid;
-      walk.load(cur);
-      total += walk.units(cur);
-      if (blockIdx.x == 0 && a.kv_len[cur.b] > walk.capacity) report_status(status, kStatusBadIndex);
-    }
-  }
-  const int64_t mine = total;
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
-  if (lane == 0) scan[warp] = total;
-  __syncthreads();
-  total = scan[0] + scan[1] + scan[2] + scan[3];
-  __syncthreads();
-  const int64_t ncta = min((int64_t)gridDim.x, total);
   Piece* pieces = reinterpret_cast<Piece*>(a.workspace);
   constexpr int kSlot = RT * (D + 2);  // floats of one partial result
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
-  if ((int64_t)blockIdx.x >= ncta) {
+  Range range;
+  Cursor cur;
+  if (!find_range(walk, status, scan, range, cur)) {
     if (tid == 0) pieces[blockIdx.x].first = -1;
     return;
   }
-  const Cut cut(total, ncta);
-  const int64_t u0 = cut.start(blockIdx.x), u1 = cut.start(blockIdx.x + 1);
-  // the sequence that holds unit u0: 128 sequences a turn, prefix sums
-  {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kWarps * 32) {
-      int64_t own = 0;
-      if (a.batch <= kWarps * 32) {
-        own = mine;
-      } else if (b0 + tid < a.batch) {
-        cur.b = b0 + tid;
-        walk.load(cur);
-        own = walk.units(cur);
-      }
-      int64_t inc = own;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) scan[warp] = inc;
-      __syncthreads();
-      int64_t base = before;
-      for (int w = 0; w < warp; ++w) base += scan[w];
-      const int64_t hi = base + inc, lo = hi - own;
-      if (u0 >= lo && u0 < hi) {
-        scan[4] = b0 + tid;
-        scan[5] = u0 - lo;
-        scan[6] = cur.q0, scan[7] = cur.qlen, scan[8] = cur.n, scan[9] = cur.R;
-      }
-      before += scan[0] + scan[1] + scan[2] + scan[3];
-      __syncthreads();
-      if (before > u0) break;
-    }
-  }
-  cur.b = (int)scan[4];
-  int skipped;  // of the first piece's cost units, those of the CTA before
-  {
-    int64_t off = scan[5];
-    cur.q0 = (int)scan[6], cur.qlen = (int)scan[7], cur.n = (int)scan[8], cur.R = (int)scan[9];
-    for (cur.rt = 0;; ++cur.rt) {
-      walk.range(cur);
-      const int64_t len = (int64_t)(cur.t1 - cur.t0 + kPieceCost) * c.kv_heads;
-      if (off < len) break;
-      off -= len;
-    }
-    const int each = cur.t1 - cur.t0 + kPieceCost;
-    cur.kvh = (int)quotient(off, each);
-    const int rest = (int)(off - (int64_t)cur.kvh * each);
-    cur.tile = cur.t0 + max(0, rest - kPieceCost);
-    skipped = min(rest, kPieceCost);
-  }
+  const int64_t u0 = range.u0, u1 = range.u1;
+  const int skipped = range.skipped;
+  const Cut& cut = range.cut;
 
   // ---- the producer side of each warp: runs ahead of its consumer side by up to `stages` steps ----
   // Block numbers come in batches, lane i holding the i-th next; the page indices of the batch
@@ -889,112 +721,6 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
     left -= kPieceCost;
     walk.next_part(cur);
     load_q(cur);
-  }
-}
-
-// Joins the pieces of cut sequences: o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order. Each
-// block lists the cut sequences from the CTAs' entries; teams of four warps take their rows
-// in turn, each warp every fourth piece, ten of them in flight.
-constexpr int kJoinWarps = 16, kTeam = 4;
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a, int ctas) {
-  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = 10;
-  __shared__ float part[kJoinWarps][D + 4];  // o, then l and m
-  __shared__ int list[kMaxCtas];
-  __shared__ int count[kJoinWarps + 1];
-  pdl_wait();
-  const Piece* pieces = reinterpret_cast<const Piece*>(a.workspace);
-  const float* slots = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kTeam;
-  int n_list = 0;
-  for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
-    const int i = i0 + threadIdx.x;
-    const bool has = i < ctas && pieces[i].first >= 0;
-    const uint32_t vote = __ballot_sync(kFull, has);
-    if (lane == 0) count[warp] = __popc(vote);
-    __syncthreads();
-    int at = n_list, all = 0;
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) at += count[w];
-      all += count[w];
-    }
-    if (has) list[at + __popc(vote & ((1u << lane) - 1))] = i;
-    n_list += all;
-    __syncthreads();
-  }
-  const int G = a.q_heads / c.kv_heads;
-  const int teams = kJoinWarps / kTeam;
-  const int items = n_list * RT;
-  for (int item0 = blockIdx.x * teams; item0 < items; item0 += gridDim.x * teams) {
-    const int item = item0 + warp / kTeam;
-    const int last = item < items ? list[item / RT] : 0, col = item % RT;
-    Piece p = {};
-    if (item < items) p = pieces[last];
-    const bool live = item < items && p.row0 + col < p.rows;
-    const int n = live ? last - p.first + 1 : 0;
-    float m = -FLT_MAX, l = 0.0f, acc[E] = {};
-    for (int i0 = sub; i0 < n; i0 += kTeam * kFlight) {
-      float2 ml[kFlight];
-      float v[kFlight][E];
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        const int i = i0 + k * kTeam;
-        ml[k] = make_float2(-FLT_MAX, 0.0f);
-        if (i < n) {
-          const float* s = slots + ((int64_t)(p.first + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
-          ml[k] = *reinterpret_cast<const float2*>(s + RT * D + col * 2);
-#pragma unroll
-          for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(s + col * D + e * 32 + lane * 2);
-        }
-      }
-      float top = m;
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) top = fmaxf(top, ml[k].x);
-      const float al = ex2(m - top);
-      m = top;
-      l *= al;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= al;
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        if (i0 + k * kTeam < n) {
-          const float f = ex2(ml[k].x - top);
-          l = fmaf(ml[k].y, f, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(v[k][e], f, acc[e]);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&part[warp][e * 32 + lane * 2]) = make_float2(acc[e], acc[e + 1]);
-    if (lane == 0) part[warp][D] = l, part[warp][D + 1] = m;
-    __syncthreads();
-    if (live && sub == 0) {
-      float top = part[warp][D + 1];
-      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, part[warp + w][D + 1]);
-      float den = 0.0f, f[kTeam];
-      for (int w = 0; w < kTeam; ++w) {
-        f[w] = ex2(part[warp + w][D + 1] - top);
-        den = fmaf(part[warp + w][D], f[w], den);
-      }
-      const int r = p.row0 + col;
-      const int64_t row = (int64_t)(p.q0 + r / G) * a.q_heads + (int64_t)p.kvh * G + r % G;
-      const bool none = den == 0.0f;
-      const float inv = none ? 0.0f : 1.0f / den;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const int d = e * 32 + lane * 2;
-        float2 v = make_float2(0.0f, 0.0f);
-        for (int w = 0; w < kTeam; ++w) v.x = fmaf(part[warp + w][d], f[w], v.x), v.y = fmaf(part[warp + w][d + 1], f[w], v.y);
-        v.x *= inv, v.y *= inv;
-        if (none) v = make_float2(0.0f, 0.0f);
-        if constexpr (F32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + d) = v;
-        else *reinterpret_cast<uint32_t*>(static_cast<__half*>(a.out) + row * D + d) = pack_half2(v.x, v.y);
-      }
-      if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (top + log2f(den)) * 0.6931471805599453f;
-    }
-    __syncthreads();
   }
 }
 

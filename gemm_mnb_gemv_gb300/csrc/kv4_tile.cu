@@ -1,0 +1,653 @@
+// Attention of many query rows over the paged 4-bit key/value cache on the tcgen05 tensor cores
+// (prefill, chunks of a prompt, long drafts): fp16 activations, heads of 64 and 128.
+//
+// A CTA (one per SM) takes row tiles of 2 x 128 rows (query token, head of the group) and key tiles of 128:
+//   S = Q K^T (M 128, N 128 keys, Q and K in shared memory), P = 2^(c S - m) in fp16 back to tensor
+//   memory over S, O += P V (P from tensor memory, V in shared memory).
+// Roles in 512 threads:
+//   warp 0       producer: per key tile eight 16-key blocks of the cache as they lie, by bulk copies;
+//   warp 1       MMA issuer (one lane) and tensor memory (512 columns: S and O of both row tiles);
+//   warps 4-7    dequantisers: codes -> fp16 offset + code * scale in the 128-byte-swizzled operand layouts,
+//                one key a thread, K rows K-major and V rows N-major, into a ring of three buffers (K, V, K, ..);
+//                both row tiles read a buffer, which halves the conversion per product;
+//   warps 8-11, 12-15  softmax of row tile A, B: a row a thread, no shuffles.
+// The issuer alternates S_A, P_B V, S_B, P_A V, so each softmax has the other tile's products to hide behind.
+// K is held at half and V at a quarter of its value, so that offset + 15 scale of any cache filled from
+// fp16 stays inside fp16; both factors are undone in fp32. A key tile whose values are all below 2^-7 has
+// V at 2^12 times its value and P at 2^-14 times, or V's scales would be fp16 subnormals.  A row's reference m moves as in the
+// streaming kernel, and only then is O rescaled in tensor memory.
+// A non-finite V value enters as 0 and is kept as a flag of its key: rows that see the key get NaN in
+// its group at the end (0 * NaN would reach every row of the tile).
+// Element order: the nibbles of a word convert to elements (n0, n4), (n1, n5), ..; q is permuted
+// alike, and O's columns are put back when they are stored.
+// Work is cut and joined as in the streaming kernel (kv4_work.cuh), so a few rows over a long context
+// use every SM too.
+#include <type_traits>
+
+#include "kv4_work.cuh"
+#include "tcgen05.cuh"
+
+namespace mnb {
+namespace {
+
+using namespace kv4;
+
+constexpr int kRows = 256, kKeys = 128, kCost = 2, kThreads = 512;
+constexpr int kBufs = 3;   // K / V operand buffers
+constexpr int kMeta = 4;   // tiles whose flags are kept
+constexpr int kTinySize = 0x2000;  // fp16 bits of 2^-7
+
+template <int D, int NG>
+struct TileSmem {
+  static constexpr int kBlock = 16 * D + 128 * NG;
+  static constexpr int kRaw = 8 * kBlock;                // one key tile of the cache
+  static constexpr int kOperand = kKeys * D * 2;         // K or V of a tile in fp16
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kFree = 227 * 1024 - 2048 - kQ - kBufs * kOperand;
+  static constexpr int kStages = kFree / kRaw < 4 ? kFree / kRaw : 4;
+  static constexpr int kBytes = kQ + kBufs * kOperand + kStages * kRaw + 1024;
+  static_assert(kStages >= 2, "two raw tiles in flight");
+};
+
+// max over 3 values
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// (x0, x1) = (x0, x1) * (c, c) + (d, d)
+__device__ __forceinline__ void fma2(float& x0, float& x1, float c, float d) {
+  asm("{\n\t.reg .b64 a, b, e;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 e, {%3, %3};\n\t"
+      "fma.rn.f32x2 a, a, b, e;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+
+__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// A word's 8 codes to offset + code * scale, in the order (n0, n4), (n1, n5), (n2, n6), (n3, n7).
+__device__ __forceinline__ uint4 convert(uint32_t w, uint32_t scale2, uint32_t offset2) {
+  uint32_t d[4];
+  nibbles_to_centered_half2(w, zp_lo_const(0), zp_hi_const(0), d);
+  return make_uint4(hfma2_bits(d[0], scale2, offset2), hfma2_bits(d[1], scale2, offset2),
+                    hfma2_bits(d[2], scale2, offset2), hfma2_bits(d[3], scale2, offset2));
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_tile_kernel(const Kv4Cache c, const Kv4Attention a, uint64_t page_magic, uint32_t* status) {
+  using L = TileSmem<D, NG>;
+  constexpr int KW = D / 32, VW = D / 64;
+  constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory columns: S_A, S_B, O_A, O_B
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t raw_full[4], raw_empty[4], kv_full[kBufs], kv_empty[kBufs], q_full[2], s_full[2], p_full[2], o_full;
+  __shared__ int64_t scan[10];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ int raw_have[4];                 // blocks of a raw tile that were read
+  __shared__ int tile_have[kMeta];            // the same, for the softmax
+  __shared__ int v_size[kMeta][4];            // fp16 bits of the largest V parameters, by dequantiser warp
+  __shared__ int odd_any[kMeta][4];           // a dequantiser warp saw a V value that is not finite
+  __shared__ uint8_t odd[kMeta][kKeys];       // its groups, by key
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t q_at = smem_u32(smem), buf_at = q_at + L::kQ;
+  uint8_t* raw_ring = smem + L::kQ + kBufs * L::kOperand;
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
+    for (int i = 0; i < kBufs; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    mbar_init(&o_full, 1);
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const Walk<kRows, kKeys, kCost> walk(a, c);
+  const int G = walk.G;
+  Piece* pieces = reinterpret_cast<Piece*>(a.workspace);
+  constexpr int kSlot = kRows * (D + 2);
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
+  Range range;
+  Cursor cur;
+  if (!find_range(walk, status, scan, range, cur)) {
+    if (tid == 0) pieces[blockIdx.x].first = -1;
+    return;
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base;
+  // every role walks the same pieces
+  int64_t left = range.u1 - range.u0 + range.skipped - kCost;
+  auto next_piece = [&](int done) {  // false: that was the last
+    left -= done;
+    if (left <= kCost) return false;
+    left -= kCost;
+    walk.next_part(cur);
+    return true;
+  };
+  auto give_up = [&](uint32_t what) {
+    report_status(status, what);
+    atomicExch(&abort_flag, 1);
+  };
+
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    tc::setmaxnreg_dec<72>();
+    if (warp == 0) {
+      // ------------------------------ producer ------------------------------------
+      const int ppb = c.page_size / 16;
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      while (left > 0 && ok) {
+        const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
+        for (int tile = cur.tile; tile < cur.tile + here; ++tile) {
+          // lane i < 8: block i of the tile
+          const int key = tile * kKeys + (lane & 7) * 16;
+          uint32_t at = 0xffffffffu;
+          if (lane < 8 && key < cur.n) {
+            const uint32_t blk = (uint32_t)key / 16;
+            const uint32_t pi = (uint32_t)((uint64_t)blk * page_magic >> 36);
+            const int page = a.page_table[(int64_t)cur.b * a.table_stride + pi];
+            if (page >= 0 && page < c.num_pages)
+              at = ((uint32_t)page * c.kv_heads + cur.kvh) * ppb + (blk - pi * ppb);
+            else
+              report_status(status, kStatusBadIndex);
+          }
+          const uint32_t have = __ballot_sync(kFull, at != 0xffffffffu);
+          if (issued >= L::kStages && !__all_sync(kFull, mbar_wait_bounded(&raw_empty[stage], phase ^ 1u))) {
+            if (lane == 0) give_up(kStatusEmptyWait);
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            raw_have[stage] = (int)have;
+            if (have) mbar_arrive_expect_tx(&raw_full[stage], __popc(have) * L::kBlock);
+            else mbar_arrive(&raw_full[stage]);
+          }
+          __syncwarp();
+          if (at != 0xffffffffu)
+            bulk_g2s(raw_ring + stage * L::kRaw + lane * L::kBlock, c.pages + (uint64_t)at * L::kBlock, L::kBlock,
+                     &raw_full[stage]);
+          ++issued;
+          if (++stage == L::kStages) stage = 0, phase ^= 1u;
+        }
+        if (!next_piece(here)) break;
+      }
+      // every copy lands before the CTA can retire
+      for (int i = max(0, issued - L::kStages); i < issued; ++i)
+        (void)mbar_wait_bounded(&raw_full[i % L::kStages], (uint32_t)(i / L::kStages) & 1u);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------ MMA issuer ----------------------------------
+      const uint32_t idesc_s = tc::idesc_f16_f32(128, 128);
+      const uint32_t idesc_o = tc::idesc_f16_f32(128, D) | tc::kIdescBMajorN;
+      int item = 0;                       // K and V operands in order
+      uint32_t kv_phase = 0, p_phase = 0, q_phase = 0;  // a bit for each barrier
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t ph) {
+        if (mbar_spin_bounded(bar, ph)) return true;
+        give_up(kStatusMmaWait);
+        ok = false;
+        return false;
+      };
+      auto wait_kv = [&](int buf) {
+        const bool r = wait(&kv_full[buf], kv_phase >> buf & 1u);
+        kv_phase ^= 1u << buf;
+        tc::fence_after_sync();
+        return r;
+      };
+      auto mma_s = [&](int x, int buf) {
+        const uint64_t dq = tc::smem_desc_k_sw128(q_at + x * (L::kQ / 2));
+        const uint64_t dk = tc::smem_desc_k_sw128(buf_at + buf * L::kOperand);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (uint64_t)((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
+          tc::mma_f16(tmem + kColS + x * 128, dq + step, dk + step, idesc_s, kk > 0);
+        }
+        tc::mma_commit(&s_full[x]);
+      };
+      auto mma_o = [&](int x, int buf, bool first) {
+        const uint64_t dv = tc::smem_desc_mn_sw128(buf_at + buf * L::kOperand, kKeys * 128);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc::mma_f16_ts(tmem + kColO + x * 128, tmem + kColS + x * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), idesc_o,
+                         !(first && kk == 0));
+      };
+      while (left > 0 && ok) {
+        const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
+        if (!wait(&q_full[0], q_phase) || !wait(&q_full[1], q_phase)) break;
+        q_phase ^= 1u;
+        tc::fence_after_sync();
+        int vbuf = 0;  // V of the tile before
+        for (int j = 0; j < here; ++j) {
+          const int kb = item % kBufs, vb = (item + 1) % kBufs;
+          if (!wait_kv(kb)) break;
+          mma_s(0, kb);
+          if (j > 0) {
+            if (!wait(&p_full[1], p_phase >> 1)) break;
+            p_phase ^= 2u;
+            tc::fence_after_sync();
+            mma_o(1, vbuf, j == 1);
+            tc::mma_commit(&kv_empty[vbuf]);
+          }
+          mma_s(1, kb);
+          tc::mma_commit(&kv_empty[kb]);
+          if (!wait_kv(vb)) break;
+          if (!wait(&p_full[0], p_phase & 1u)) break;
+          p_phase ^= 1u;
+          tc::fence_after_sync();
+          mma_o(0, vb, j == 0);
+          vbuf = vb;
+          item += 2;
+        }
+        if (!ok) break;
+        if (!wait(&p_full[1], p_phase >> 1)) break;
+        p_phase ^= 2u;
+        tc::fence_after_sync();
+        mma_o(1, vbuf, here == 1);
+        tc::mma_commit(&kv_empty[vbuf]);
+        tc::mma_commit(&o_full);
+        if (!next_piece(here)) break;
+      }
+      if (!ok) {
+        // the tensor memory is given back only after the products in flight are done
+        tc::mma_commit(&o_full);
+        (void)mbar_wait_bounded(&o_full, 0);
+        (void)mbar_wait_bounded(&o_full, 1);
+      }
+    }
+  } else if (wg == 1) {
+    tc::setmaxnreg_dec<104>();
+    // ------------------------------ dequantisers -------------------------------------
+    const int r = tid - 128;  // key of the tile
+    const int row = r & 15;   // in its block
+    int stage = 0, item = 0, tiles = 0;
+    uint32_t phase = 0, e_phase = 0;  // e_phase: a bit for each buffer
+    bool ok = true;
+    while (left > 0 && ok) {
+      const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
+      for (int tile = cur.tile; tile < cur.tile + here; ++tile) {
+        if (!__all_sync(kFull, mbar_wait_bounded(&raw_full[stage], phase))) {
+          ok = false;
+          break;
+        }
+        const int have = raw_have[stage];
+        const uint32_t blk = smem_u32(raw_ring + stage * L::kRaw + (r >> 4) * L::kBlock);
+        const uint32_t par = blk + 16 * D + row * 4;
+        // ---- K: halves of the values; keys that are not there hold anything, their scores are masked ----
+        int buf = item % kBufs;
+        if (item >= kBufs) {
+          if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
+            ok = false;
+            break;
+          }
+          e_phase ^= 1u << buf;
+        }
+        {
+          uint32_t scale2[NG], offset2[NG];
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) {
+            const uint32_t p = lds_u32_a(par + gi * 64);
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&p), __half2half2(__ushort_as_half(0x3800)));  // 1/2
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+            scale2[gi] = __byte_perm(u, 0, 0x1010), offset2[gi] = __byte_perm(u, 0, 0x3232);
+          }
+          const uint32_t dst = buf_at + buf * L::kOperand + r * 128;
+#pragma unroll
+          for (int j = 0; j < KW; ++j) {
+            // 16 bytes: words p = 4 ch .. of the row, word (t, w) = p / KW, p % KW; the starting chunk follows the
+            // lane, so that eight rows are read from distinct banks
+            const int ch = KW == 8 ? j : (j + (lane >> 1)) & (KW - 1);
+            const uint4 v = lds128_a(blk + row * (D / 2) + ch * 16);
+            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = KW == 4 ? ch : ch * 2 + i / 2, w = KW == 4 ? i : i % 2;
+              const int gi = w * NG / KW;
+              const uint4 y = convert(w4[i], scale2[gi], offset2[gi]);
+              const int chunk = 4 * w + t;  // 16-byte chunk of the row
+              sts128(dst + (chunk >> 3) * (kKeys * 128) + (((chunk & 7) ^ (r & 7)) << 4), y);
+            }
+          }
+        }
+        uint32_t vpar[NG], bad = 0, size = 0;  // V parameters; size: the larger of |offset| and 16 |scale|
+        {
+          const bool there = tile * kKeys + r < cur.n && (have >> (r >> 4) & 1);
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) {
+            uint32_t p = there ? lds_u32_a(par + (NG + gi) * 64) : 0u;
+            if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) bad |= 1u << gi, p = 0u;
+            vpar[gi] = p;
+            size = max(size, max((p & 0x7fffu) + 0x1000u, p >> 16 & 0x7fffu));
+          }
+          size = __reduce_max_sync(kFull, size);
+        }
+        if (r == 0) tile_have[tiles % kMeta] = have;
+        if (lane == 0) v_size[tiles % kMeta][warp - 4] = (int)size;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[buf]);
+        ++item;
+        // ---- V: quarters of the values, zeros for keys that are not there ----
+        buf = item % kBufs;
+        if (item >= kBufs) {
+          if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
+            ok = false;
+            break;
+          }
+          e_phase ^= 1u << buf;
+        }
+        {
+          // the four warps agree on the tile's factor
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          const int* vs = v_size[tiles % kMeta];
+          const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
+          const __half2 factor = __half2half2(__ushort_as_half(tiny ? 0x6c00 : 0x3400));  // 2^12 or 1/4
+          uint32_t scale2[NG], offset2[NG];
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) {
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&vpar[gi]), factor);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+            scale2[gi] = __byte_perm(u, 0, 0x1010), offset2[gi] = __byte_perm(u, 0, 0x3232);
+          }
+          const uint32_t dst = buf_at + buf * L::kOperand + r * 128;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            uint32_t w4[VW];
+            const uint32_t at = blk + 8 * D + v_word_byte<D>(g, row, 0);
+            if constexpr (VW == 1) {
+              w4[0] = lds_u32_a(at);
+            } else {
+              const uint2 v = lds_u64_a(at);
+              w4[0] = v.x, w4[1] = v.y;
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              // nibbles (n, n + 4): elements 32 apart, of two groups when groups have 32
+              const int g0 = 2 * w * NG / KW, g1 = (2 * w + 1) * NG / KW;
+              const uint32_t s2 = g0 == g1 ? scale2[g0] : __byte_perm(scale2[g0], scale2[g1], 0x5410);
+              const uint32_t o2 = g0 == g1 ? offset2[g0] : __byte_perm(offset2[g0], offset2[g1], 0x5410);
+              sts128(dst + w * (kKeys * 128) + ((g ^ (r & 7)) << 4), convert(w4[w], s2, o2));
+            }
+          }
+          const bool any = __any_sync(kFull, bad != 0);
+          if (lane == 0) odd_any[tiles % kMeta][warp - 4] = any;
+          if (any) odd[tiles % kMeta][r] = (uint8_t)bad;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&kv_full[buf]);
+          mbar_arrive(&raw_empty[stage]);
+        }
+        ++item;
+        ++tiles;
+        if (++stage == L::kStages) stage = 0, phase ^= 1u;
+      }
+      if (!ok || !next_piece(here)) break;
+    }
+    if (!ok && lane == 0) give_up(kStatusFullWait);
+  } else {
+    tc::setmaxnreg_inc<168>();
+    // ------------------------------ softmax -------------------------------------
+    const int x = wg - 2;
+    const int r = tid & 127;  // row of the row tile, tensor memory lane
+    const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_at = lane_at + kColS + x * 128, o_at = lane_at + kColO + x * 128;
+    const float c1 = fmaxf(fabsf(a.scale) * (2.0f * kLog2e), FLT_MIN);  // K holds half values
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    uint32_t s_phase = 0, o_phase = 0;
+    int tiles = 0;
+    bool ok = true;
+    if (tid == 256) pieces[blockIdx.x].first = -1;
+    while (left > 0) {
+      const bool from_start = cur.tile == cur.t0;
+      const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
+      const int rows = cur.qlen * G, row = cur.rt * kRows + x * 128 + r;
+      const bool live = row < rows;
+      const int tok = live ? row / G : 0, head = live ? row - tok * G : 0;
+      {
+        const __half* q = static_cast<const __half*>(a.q) + (int64_t)(cur.q0 + tok) * a.q_stride +
+                          ((int64_t)cur.kvh * G + head) * D;
+        const uint32_t dst = q_at + x * (L::kQ / 2) + r * 128;
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch) {
+          uint4 v = live ? *reinterpret_cast<const uint4*>(q + ch * 8) : make_uint4(0, 0, 0, 0);
+          uint32_t p[4];
+          pair_halves_stride4(v, p);
+          sts128(dst + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (r & 7)) << 4),
+                 make_uint4(p[0] ^ flip, p[1] ^ flip, p[2] ^ flip, p[3] ^ flip));
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[x]);
+      }
+      const int pos = cur.n - cur.qlen + tok;
+      const int lim_hi = a.causal ? min(cur.n, pos + 1) : cur.n;
+      const int lim_lo = a.window > 0 ? pos - a.window + 1 : 0;
+      float m = -FLT_MAX, l0 = 0.0f, l1 = 0.0f;
+      uint32_t nan_groups = 0;
+      // V values that are not finite, seen by this row: of the tile before, whose flags the products waited for
+      auto odd_keys = [&](int t, int base) {
+        const int* any = odd_any[t % kMeta];
+        if ((any[0] | any[1] | any[2] | any[3]) == 0) return;
+        for (int w = 0; w < 4; ++w) {
+          if (!any[w]) continue;
+          for (int k = 32 * w; k < 32 * w + 32; ++k)
+            if (base + k >= lim_lo && base + k < lim_hi) nan_groups |= odd[t % kMeta][k];
+        }
+      };
+      for (int j = 0; j < here; ++j) {
+        const int base = (cur.tile + j) * kKeys;
+        if (ok && !__all_sync(kFull, mbar_wait_bounded(&s_full[x], s_phase))) {
+          if (lane == 0) give_up(kStatusMmaWait);
+          ok = false;
+        }
+        s_phase ^= 1u;
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (j > 0) odd_keys(tiles - 1, base - kKeys);
+        // The second half of the scores is read twice, for its maximum and for its probabilities: the whole row
+        // would not leave registers for the rest.
+        float v[64];
+        auto load_half = [&](int half) {
+          tc::tmem_ld32(s_at + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]));
+          tc::tmem_ld32(s_at + 64 * half + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+          tc::tmem_wait_ld();
+        };
+        const int have = tile_have[tiles % kMeta];
+        const int* vs = v_size[tiles % kMeta];
+        const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
+        ++tiles;
+        const bool masked = __any_sync(kFull, base < lim_lo || base + kKeys > lim_hi || have != 0xff);
+        auto mask_half = [&](int half) {
+          const int lo = lim_lo - base - 64 * half, hi = lim_hi - base - 64 * half, in = have >> (4 * half);
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo || i >= hi || !(in >> (i >> 4) & 1)) v[i] = -INFINITY;
+        };
+        auto top_half = [&]() {
+          float t0 = v[0], t1 = v[1];
+#pragma unroll
+          for (int i = 2; i < 62; i += 4) t0 = max3(t0, v[i], v[i + 1]), t1 = max3(t1, v[i + 2], v[i + 3]);
+          return fmaxf(max3(t0, v[62], v[63]), t1);
+        };
+        load_half(1);
+        if (masked) mask_half(1);
+        float top = top_half();
+        load_half(0);
+        if (masked) mask_half(0);
+        top = fmaxf(top, top_half()) * c1;
+        if (__any_sync(kFull, top > m + kRise)) {
+          const float m2 = top > m + kRise ? top - kLift : m;
+          const float al = ex2(m - m2);
+          m = m2;
+          l0 *= al, l1 *= al;
+          if (j > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tc::tmem_ld32(o_at + 32 * i, o);
+              tc::tmem_wait_ld();
+              uint32_t u[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * al);
+              tc::tmem_st32(o_at + 32 * i, u);
+            }
+          }
+        }
+        const float shift = -m - (tiny ? 14.0f : 0.0f);
+        float t0 = 0.0f, t1 = 0.0f;
+        // P overlays S: keys 64 h .. 64 h + 63 go to columns 32 h .. 32 h + 31, whose scores are in registers
+        // or used up
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) {
+            load_half(1);
+            if (masked) mask_half(1);
+          }
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            fma2(v[i], v[i + 1], c1, shift);
+            v[i] = ex2(v[i]), v[i + 1] = ex2(v[i + 1]);
+            add2(t0, t1, v[i], v[i + 1]);
+            p[i / 2] = pack_half2(v[i], v[i + 1]);
+          }
+          tc::tmem_st32(s_at + 32 * half, p);
+        }
+        l0 = fmaf(t0, tiny ? 16384.0f : 1.0f, l0), l1 = fmaf(t1, tiny ? 16384.0f : 1.0f, l1);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      // ---- the end of this piece ----
+      if (ok && !__all_sync(kFull, mbar_wait_bounded(&o_full, o_phase))) {
+        if (lane == 0) give_up(kStatusMmaWait);
+        ok = false;
+      }
+      o_phase ^= 1u;
+      tc::fence_after_sync();
+      if (ok) odd_keys(tiles - 1, (cur.tile + here - 1) * kKeys);
+      const bool ends = cur.tile + here == cur.t1;
+      const bool whole = from_start && ends;
+      const float l = ok ? l0 + l1 : NAN;
+      const bool none = l == 0.0f;
+      const float f = whole ? (none ? 0.0f : 4.0f / l) : 4.0f;  // V holds quarters
+      float* slot = slots + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kSlot;
+      const int64_t out_row = (int64_t)(cur.q0 + tok) * a.q_heads + (int64_t)cur.kvh * G + head;
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        // columns 64 w + 8 g + i hold element 64 w + 32 (i & 1) + 4 g + i / 2
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // g of 4 half ..
+          float o[32];
+          if (ok) {
+            tc::tmem_ld32(o_at + 64 * w + 32 * half, o);
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int gi = (2 * w + (i & 1)) * NG / KW;
+            o[i] = none && whole ? 0.0f : o[i] * f;
+            if ((nan_groups >> gi & 1) || !ok) o[i] = NAN;
+          }
+          if (live) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int g2 = 0; g2 < 4; g2 += 2) {  // elements 64 w + 32 h + 16 half + 4 g2 .. + 7
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 2 * (k % 4) + h];
+                const int d = 64 * w + 32 * h + 16 * half + 4 * g2;
+                if (whole) {
+                  *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + out_row * D + d) = make_uint4(
+                      pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+                } else {
+                  float4* s4 = reinterpret_cast<float4*>(slot + (x * 128 + r) * D + d);
+                  s4[0] = make_float4(y[0], y[1], y[2], y[3]);
+                  s4[1] = make_float4(y[4], y[5], y[6], y[7]);
+                }
+              }
+            }
+          }
+        }
+      }
+      if (live) {
+        if (whole) {
+          if (a.lse) a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float2*>(slot + kRows * D + (x * 128 + r) * 2) = make_float2(m, l);
+        }
+      }
+      if (tid == 256 && !from_start && ends) {
+        const int64_t s0 = range.u1 - left - (cur.tile - cur.t0);
+        pieces[blockIdx.x] = {(int)range.cut.part_of(s0), cur.q0, cur.rt * kRows, rows, cur.kvh};
+      }
+      tc::fence_before_sync();
+      if (!next_piece(here)) break;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D, int NG>
+cudaError_t launch_tile(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a) {
+  auto kern = kv4_tile_kernel<D, NG>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D, NG>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = ctx.num_sms < 160 ? ctx.num_sms : 160;
+  const uint64_t ppb = (uint64_t)(c.page_size / 16), magic = ((1ull << 36) + ppb - 1) / ppb;
+  e = launch_kernel(ctx, kern, dim3(grid), dim3(kThreads), TileSmem<D, NG>::kBytes, c, a, magic, ctx.status);
+  if (e != cudaSuccess) return e;
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;  // the joining kernel waits for this one on the device
+  e = launch_kernel(ctx, kv4_join_kernel<D, kRows / 8, false>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
+  ctx.pdl = pdl;
+  return e;
+}
+
+}  // namespace
+
+size_t kv4_tile_workspace_bytes(int D) {
+  return (size_t)kMaxCtas * sizeof(Piece) + (size_t)160 * 2 * kRows * (D + 2) * 4;
+}
+
+cudaError_t launch_kv4_tile(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a) {
+  if (c.head_dim == 64) return c.group == 32 ? launch_tile<64, 2>(ctx, c, a) : launch_tile<64, 1>(ctx, c, a);
+  if (c.group == 32) return launch_tile<128, 4>(ctx, c, a);
+  return c.group == 64 ? launch_tile<128, 2>(ctx, c, a) : launch_tile<128, 1>(ctx, c, a);
+}
+
+}  // namespace mnb
