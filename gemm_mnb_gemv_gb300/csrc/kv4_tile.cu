@@ -203,16 +203,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every copy lands before the CTA can retire
       for (int i = max(0, issued - L::kStages); i < issued; ++i)
         (void)mbar_wait_bounded(&raw_full[i % L::kStages], (uint32_t)(i / L::kStages) & 1u);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------ MMA issuer ----------------------------------
+      // The warp stays together and one elected lane issues: a product's descriptors are formed before its
+      // first MMA, since the tensor pipe queues little and idles while addresses are made.
+      const bool leader = tc::elect_one();
       const uint32_t idesc_s = tc::idesc_f16_f32(128, 128);
       const uint32_t idesc_o = tc::idesc_f16_f32(128, D) | tc::kIdescBMajorN;
       int item = 0;                       // K and V operands in order
       uint32_t kv_phase = 0, p_phase = 0, q_phase = 0;  // a bit for each barrier
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t ph) {
-        if (mbar_spin_bounded(bar, ph)) return true;
-        give_up(kStatusMmaWait);
+        if (__all_sync(kFull, mbar_spin_bounded(bar, ph))) return true;
+        if (leader) give_up(kStatusMmaWait);
         ok = false;
         return false;
       };
@@ -222,22 +225,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return r;
       };
+      const uint64_t dq0 = tc::smem_desc_k_sw128(q_at), dk0 = tc::smem_desc_k_sw128(buf_at);
+      const uint64_t dv0 = tc::smem_desc_mn_sw128(buf_at, kKeys * 128);
       auto mma_s = [&](int x, int buf) {
-        const uint64_t dq = tc::smem_desc_k_sw128(q_at + x * (L::kQ / 2));
-        const uint64_t dk = tc::smem_desc_k_sw128(buf_at + buf * L::kOperand);
+        const uint64_t dq = dq0 + (uint32_t)(x * (L::kQ / 2) >> 4), dk = dk0 + (uint32_t)(buf * L::kOperand >> 4);
+        const uint32_t d = tmem + kColS + x * 128;
+        uint64_t qa[D / 16], ka[D / 16];
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t step = (uint64_t)((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
-          tc::mma_f16(tmem + kColS + x * 128, dq + step, dk + step, idesc_s, kk > 0);
+          const uint32_t step = ((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
+          qa[kk] = dq + step, ka[kk] = dk + step;
         }
-        tc::mma_commit(&s_full[x]);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) tc::mma_f16(d, qa[kk], ka[kk], idesc_s, kk > 0);
+          tc::mma_commit(&s_full[x]);
+        }
+        __syncwarp();
       };
       auto mma_o = [&](int x, int buf, bool first) {
-        const uint64_t dv = tc::smem_desc_mn_sw128(buf_at + buf * L::kOperand, kKeys * 128);
+        const uint64_t dv = dv0 + (uint32_t)(buf * L::kOperand >> 4);
+        const uint32_t d = tmem + kColO + x * 128, p = tmem + kColS + x * 128;
+        uint64_t va[kKeys / 16];
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_f16_ts(tmem + kColO + x * 128, tmem + kColS + x * 128 + kk * 8, dv + (uint64_t)(kk * 2048 >> 4), idesc_o,
-                         !(first && kk == 0));
+        for (int kk = 0; kk < kKeys / 16; ++kk) va[kk] = dv + (uint32_t)(kk * 2048 >> 4);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_f16_ts(d, p + kk * 8, va[kk], idesc_o, kk > 0 ? 1u : !first);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) tc::mma_commit(bar);
+        __syncwarp();
       };
       while (left > 0 && ok) {
         const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
@@ -254,10 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_phase ^= 2u;
             tc::fence_after_sync();
             mma_o(1, vbuf, j == 1);
-            tc::mma_commit(&kv_empty[vbuf]);
+            commit(&kv_empty[vbuf]);
           }
           mma_s(1, kb);
-          tc::mma_commit(&kv_empty[kb]);
+          commit(&kv_empty[kb]);
           if (!wait_kv(vb)) break;
           if (!wait(&p_full[0], p_phase & 1u)) break;
           p_phase ^= 1u;
@@ -271,13 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         p_phase ^= 2u;
         tc::fence_after_sync();
         mma_o(1, vbuf, here == 1);
-        tc::mma_commit(&kv_empty[vbuf]);
-        tc::mma_commit(&o_full);
+        commit(&kv_empty[vbuf]);
+        commit(&o_full);
         if (!next_piece(here)) break;
       }
       if (!ok) {
         // the tensor memory is given back only after the products in flight are done
-        tc::mma_commit(&o_full);
+        commit(&o_full);
         (void)mbar_wait_bounded(&o_full, 0);
         (void)mbar_wait_bounded(&o_full, 1);
       }
@@ -633,7 +654,7 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the joining kernel waits for this one on the device
-  e = launch_kernel(ctx, kv4_join_kernel<D, kRows / 8, false>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
+  e = launch_kernel(ctx, kv4_join_kernel<D, kRows / 8, 1, false>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
   ctx.pdl = pdl;
   return e;
 }

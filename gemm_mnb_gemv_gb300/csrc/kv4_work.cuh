@@ -199,12 +199,12 @@ __device__ __forceinline__ bool find_range(const Walk<RT, kTile, kPieceCost>& wa
 }
 
 // Joins the pieces of cut sequences: o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order. Each
-// block lists the cut sequences from the CTAs' entries; teams of four warps take their rows
-// in turn, each warp every fourth piece, ten of them in flight.
-constexpr int kJoinWarps = 16, kTeam = 4;
-template <int D, int NT, bool F32>
+// block lists the cut sequences from the CTAs' entries; teams of kTeam warps take their rows
+// in turn, each warp every kTeam-th piece, several of them in flight.
+constexpr int kJoinWarps = 16;
+template <int D, int NT, int kTeam, bool F32>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a, int ctas) {
-  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = 10;
+  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = kTeam == 1 ? 4 : 10;
   __shared__ float part[kJoinWarps][D + 4];  // o, then l and m
   __shared__ int list[kMaxCtas];
   __shared__ int count[kJoinWarps + 1];
