@@ -16,8 +16,8 @@
 // fp16 stays inside fp16; both factors are undone in fp32. A key tile whose values are all below 2^-7 has
 // V at 2^12 times its value and P at 2^-14 times, or V's scales would be fp16 subnormals.  A row's reference m moves as in the
 // streaming kernel, and only then is O rescaled in tensor memory.
-// A non-finite V value enters as 0 and is kept as a flag of its key: rows that see the key get NaN in
-// its group at the end (0 * NaN would reach every row of the tile).
+// A non-finite V value enters as 0 (0 * NaN would reach every row of the tile) and marks its piece: at the piece's
+// end the rows look for such keys among those that they see, and get NaN in the groups.
 // Element order: the nibbles of a word convert to elements (n0, n4), (n1, n5), ..; q is permuted
 // alike, and O's columns are put back when they are stored.
 // Work is cut and joined as in the streaming kernel (kv4_work.cuh), so a few rows over a long context
@@ -35,7 +35,7 @@ using namespace kv4;
 constexpr int kRows = 256, kKeys = 128, kCost = 2, kThreads = 512;
 constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
-constexpr int kTinySize = 0x2000;  // fp16 bits of 2^-7
+constexpr uint32_t kTinySize = 0x2000u;  // fp16 bits of 2^-7
 
 template <int D, int NG>
 struct TileSmem {
@@ -95,15 +95,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int KW = D / 32, VW = D / 64;
   constexpr uint32_t kColS = 0, kColO = 256;  // tensor memory columns: S_A, S_B, O_A, O_B
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t raw_full[4], raw_empty[4], kv_full[kBufs], kv_empty[kBufs], q_full[2], s_full[2], p_full[2], o_full;
+  __shared__ uint64_t raw_full[4], raw_empty[4], kv_full[kBufs], kv_empty[kBufs], q_full[2], s_full[2], p_full[2][2], o_full;
   __shared__ int64_t scan[10];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int raw_have[4];                 // blocks of a raw tile that were read
-  __shared__ int tile_have[kMeta];            // the same, for the softmax
-  __shared__ int v_size[kMeta][4];            // fp16 bits of the largest V parameters, by dequantiser warp
-  __shared__ int odd_any[kMeta][4];           // a dequantiser warp saw a V value that is not finite
-  __shared__ uint8_t odd[kMeta][kKeys];       // its groups, by key
+  __shared__ uint32_t tile_info[kMeta];       // what the softmax needs to know: bits 0-7 blocks read, bit 8 V scaled up
+  __shared__ int odd_piece[kMeta];            // 1 + the last piece (modulo kMeta) with a V value that is not finite
+  __shared__ uint32_t v_size[2][4];           // fp16 bits of the largest V parameter, by dequantiser warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = smem_u32(smem_raw);
@@ -113,9 +112,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     abort_flag = 0;
+    for (int i = 0; i < kMeta; ++i) odd_piece[i] = 0;
     for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < kBufs; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&p_full[i][0], 4), mbar_init(&p_full[i][1], 4);
     mbar_init(&o_full, 1);
     fence_mbar_init();
   }
@@ -243,18 +243,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      auto mma_o = [&](int x, int buf, bool first) {
+      auto mma_o = [&](int x, int buf, bool first) {  // in the two halves in which P comes
         const uint64_t dv = dv0 + (uint32_t)(buf * L::kOperand >> 4);
         const uint32_t d = tmem + kColO + x * 128, p = tmem + kColS + x * 128;
         uint64_t va[kKeys / 16];
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk) va[kk] = dv + (uint32_t)(kk * 2048 >> 4);
-        if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_f16_ts(d, p + kk * 8, va[kk], idesc_o, kk > 0 ? 1u : !first);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(&p_full[x][half], p_phase >> x & 1u)) return false;
+          tc::fence_after_sync();
+          if (leader) {
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              tc::mma_f16_ts(d, p + kk * 8, va[kk], idesc_o, kk > 0 ? 1u : !first);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        p_phase ^= 1u << x;
+        return true;
       };
       auto commit = [&](uint64_t* bar) {
         if (leader) tc::mma_commit(bar);
@@ -271,27 +278,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait_kv(kb)) break;
           mma_s(0, kb);
           if (j > 0) {
-            if (!wait(&p_full[1], p_phase >> 1)) break;
-            p_phase ^= 2u;
-            tc::fence_after_sync();
-            mma_o(1, vbuf, j == 1);
+            if (!mma_o(1, vbuf, j == 1)) break;
             commit(&kv_empty[vbuf]);
           }
           mma_s(1, kb);
           commit(&kv_empty[kb]);
           if (!wait_kv(vb)) break;
-          if (!wait(&p_full[0], p_phase & 1u)) break;
-          p_phase ^= 1u;
-          tc::fence_after_sync();
-          mma_o(0, vb, j == 0);
+          if (!mma_o(0, vb, j == 0)) break;
           vbuf = vb;
           item += 2;
         }
         if (!ok) break;
-        if (!wait(&p_full[1], p_phase >> 1)) break;
-        p_phase ^= 2u;
-        tc::fence_after_sync();
-        mma_o(1, vbuf, here == 1);
+        if (!mma_o(1, vbuf, here == 1)) break;
         commit(&kv_empty[vbuf]);
         commit(&o_full);
         if (!next_piece(here)) break;
@@ -308,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------ dequantisers -------------------------------------
     const int r = tid - 128;  // key of the tile
     const int row = r & 15;   // in its block
-    int stage = 0, item = 0, tiles = 0;
+    int stage = 0, item = 0, tiles = 0, piece = 0;
     uint32_t phase = 0, e_phase = 0;  // e_phase: a bit for each buffer
     bool ok = true;
     while (left > 0 && ok) {
@@ -321,6 +319,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int have = raw_have[stage];
         const uint32_t blk = smem_u32(raw_ring + stage * L::kRaw + (r >> 4) * L::kBlock);
         const uint32_t par = blk + 16 * D + row * 4;
+        // ---- V's parameters, zeros for keys that are not there; the four warps agree on the tile's factor ----
+        uint32_t vpar[NG], bad = 0, size = 0;  // size: the larger of |offset| and 16 |scale|
+        const bool there = tile * kKeys + r < cur.n && (have >> (r >> 4) & 1);
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          uint32_t p = there ? lds_u32_a(par + (NG + gi) * 64) : 0u;
+          if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) bad = 1u, p = 0u;
+          vpar[gi] = p;
+          size = max(size, max((p & 0x7fffu) + 0x1000u, p >> 16 & 0x7fffu));
+        }
+        size = __reduce_max_sync(kFull, size);
+        if (lane == 0) v_size[tiles & 1][warp - 4] = size;
+        if (bad) odd_piece[piece % kMeta] = piece + 1;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const uint32_t* vs = v_size[tiles & 1];
+        const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
+        if (r == 0) tile_info[tiles % kMeta] = (uint32_t)have | (tiny ? 256u : 0u);
         // ---- K: halves of the values; keys that are not there hold anything, their scores are masked ----
         int buf = item % kBufs;
         if (item >= kBufs) {
@@ -357,25 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        uint32_t vpar[NG], bad = 0, size = 0;  // V parameters; size: the larger of |offset| and 16 |scale|
-        {
-          const bool there = tile * kKeys + r < cur.n && (have >> (r >> 4) & 1);
-#pragma unroll
-          for (int gi = 0; gi < NG; ++gi) {
-            uint32_t p = there ? lds_u32_a(par + (NG + gi) * 64) : 0u;
-            if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) bad |= 1u << gi, p = 0u;
-            vpar[gi] = p;
-            size = max(size, max((p & 0x7fffu) + 0x1000u, p >> 16 & 0x7fffu));
-          }
-          size = __reduce_max_sync(kFull, size);
-        }
-        if (r == 0) tile_have[tiles % kMeta] = have;
-        if (lane == 0) v_size[tiles % kMeta][warp - 4] = (int)size;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_full[buf]);
         ++item;
-        // ---- V: quarters of the values, zeros for keys that are not there ----
+        // ---- V: quarters of the values ----
         buf = item % kBufs;
         if (item >= kBufs) {
           if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
@@ -385,10 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           e_phase ^= 1u << buf;
         }
         {
-          // the four warps agree on the tile's factor
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          const int* vs = v_size[tiles % kMeta];
-          const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
           const __half2 factor = __half2half2(__ushort_as_half(tiny ? 0x6c00 : 0x3400));  // 2^12 or 1/4
           uint32_t scale2[NG], offset2[NG];
 #pragma unroll
@@ -417,9 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               sts128(dst + w * (kKeys * 128) + ((g ^ (r & 7)) << 4), convert(w4[w], s2, o2));
             }
           }
-          const bool any = __any_sync(kFull, bad != 0);
-          if (lane == 0) odd_any[tiles % kMeta][warp - 4] = any;
-          if (any) odd[tiles % kMeta][r] = (uint8_t)bad;
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -432,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == L::kStages) stage = 0, phase ^= 1u;
       }
       if (!ok || !next_piece(here)) break;
+      ++piece;
     }
     if (!ok && lane == 0) give_up(kStatusFullWait);
   } else {
@@ -444,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c1 = fmaxf(fabsf(a.scale) * (2.0f * kLog2e), FLT_MIN);  // K holds half values
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     uint32_t s_phase = 0, o_phase = 0;
-    int tiles = 0;
+    int tiles = 0, piece = 0;
     bool ok = true;
     if (tid == 256) pieces[blockIdx.x].first = -1;
     while (left > 0) {
@@ -473,17 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_hi = a.causal ? min(cur.n, pos + 1) : cur.n;
       const int lim_lo = a.window > 0 ? pos - a.window + 1 : 0;
       float m = -FLT_MAX, l0 = 0.0f, l1 = 0.0f;
-      uint32_t nan_groups = 0;
-      // V values that are not finite, seen by this row: of the tile before, whose flags the products waited for
-      auto odd_keys = [&](int t, int base) {
-        const int* any = odd_any[t % kMeta];
-        if ((any[0] | any[1] | any[2] | any[3]) == 0) return;
-        for (int w = 0; w < 4; ++w) {
-          if (!any[w]) continue;
-          for (int k = 32 * w; k < 32 * w + 32; ++k)
-            if (base + k >= lim_lo && base + k < lim_hi) nan_groups |= odd[t % kMeta][k];
-        }
-      };
       for (int j = 0; j < here; ++j) {
         const int base = (cur.tile + j) * kKeys;
         if (ok && !__all_sync(kFull, mbar_wait_bounded(&s_full[x], s_phase))) {
@@ -493,25 +477,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1u;
         if (!ok) break;
         tc::fence_after_sync();
-        if (j > 0) odd_keys(tiles - 1, base - kKeys);
         // The second half of the scores is read twice, for its maximum and for its probabilities: the whole row
         // would not leave registers for the rest.
         float v[64];
         auto load_half = [&](int half) {
           tc::tmem_ld32(s_at + 64 * half, *reinterpret_cast<float(*)[32]>(&v[0]));
           tc::tmem_ld32(s_at + 64 * half + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
-          tc::tmem_wait_ld();
         };
-        const int have = tile_have[tiles % kMeta];
-        const int* vs = v_size[tiles % kMeta];
-        const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
+        load_half(1);
+        const uint32_t in = tile_info[tiles % kMeta], have = in & 0xffu;
+        const bool tiny = in >> 8 != 0;
+        const bool masked = __any_sync(kFull, base < lim_lo || base + kKeys > lim_hi || have != 0xffu);
         ++tiles;
-        const bool masked = __any_sync(kFull, base < lim_lo || base + kKeys > lim_hi || have != 0xff);
         auto mask_half = [&](int half) {
-          const int lo = lim_lo - base - 64 * half, hi = lim_hi - base - 64 * half, in = have >> (4 * half);
+          const int lo = lim_lo - base - 64 * half, hi = lim_hi - base - 64 * half;
+          const uint32_t blocks = have >> (4 * half);
 #pragma unroll
           for (int i = 0; i < 64; ++i)
-            if (i < lo || i >= hi || !(in >> (i >> 4) & 1)) v[i] = -INFINITY;
+            if (i < lo || i >= hi || !(blocks >> (i >> 4) & 1)) v[i] = -INFINITY;
         };
         auto top_half = [&]() {
           float t0 = v[0], t1 = v[1];
@@ -519,10 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 2; i < 62; i += 4) t0 = max3(t0, v[i], v[i + 1]), t1 = max3(t1, v[i + 2], v[i + 3]);
           return fmaxf(max3(t0, v[62], v[63]), t1);
         };
-        load_half(1);
+        tc::tmem_wait_ld();
         if (masked) mask_half(1);
         float top = top_half();
         load_half(0);
+        tc::tmem_wait_ld();
         if (masked) mask_half(0);
         top = fmaxf(top, top_half()) * c1;
         if (__any_sync(kFull, top > m + kRise)) {
@@ -546,11 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float shift = -m - (tiny ? 14.0f : 0.0f);
         float t0 = 0.0f, t1 = 0.0f;
         // P overlays S: keys 64 h .. 64 h + 63 go to columns 32 h .. 32 h + 31, whose scores are in registers
-        // or used up
+        // or used up. The products start on the first half while the second is made.
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (half == 1) {
             load_half(1);
+            tc::tmem_wait_ld();
             if (masked) mask_half(1);
           }
           uint32_t p[32];
@@ -562,12 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             p[i / 2] = pack_half2(v[i], v[i + 1]);
           }
           tc::tmem_st32(s_at + 32 * half, p);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x][half]);
         }
         l0 = fmaf(t0, tiny ? 16384.0f : 1.0f, l0), l1 = fmaf(t1, tiny ? 16384.0f : 1.0f, l1);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       // ---- the end of this piece ----
       if (ok && !__all_sync(kFull, mbar_wait_bounded(&o_full, o_phase))) {
@@ -576,7 +561,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       o_phase ^= 1u;
       tc::fence_after_sync();
-      if (ok) odd_keys(tiles - 1, (cur.tile + here - 1) * kKeys);
+      // V values that are not finite: look for them again in the cache, 32 keys at a time
+      uint32_t nan_groups = 0;
+      if (odd_piece[piece % kMeta] == piece + 1) {
+        const int ppb = c.page_size / 16, end = min((cur.tile + here) * kKeys, cur.n);
+        for (int k0 = cur.tile * kKeys; k0 < end; k0 += 32) {
+          uint32_t bad = 0;
+          if (k0 + lane < end) {
+            const uint32_t blk = (uint32_t)(k0 + lane) / 16, pi = (uint32_t)((uint64_t)blk * page_magic >> 36);
+            const int page = a.page_table[(int64_t)cur.b * a.table_stride + pi];
+            if (page >= 0 && page < c.num_pages) {
+              const uint8_t* at = c.pages + (((uint64_t)page * c.kv_heads + cur.kvh) * ppb + (blk - pi * ppb)) * L::kBlock;
+              for (int gi = 0; gi < NG; ++gi) {
+                const uint32_t p = *reinterpret_cast<const uint32_t*>(at + 16 * D + ((NG + gi) * 16 + (k0 + lane) % 16) * 4);
+                if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) bad |= 1u << gi;
+              }
+            }
+          }
+          if (__any_sync(kFull, bad != 0))
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t w = __shfl_sync(kFull, bad, k);
+              if (k0 + k >= lim_lo && k0 + k < lim_hi) nan_groups |= w;
+            }
+        }
+      }
       const bool ends = cur.tile + here == cur.t1;
       const bool whole = from_start && ends;
       const float l = ok ? l0 + l1 : NAN;
@@ -635,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_before_sync();
       if (!next_piece(here)) break;
+      ++piece;
     }
   }
   tc::fence_before_sync();
