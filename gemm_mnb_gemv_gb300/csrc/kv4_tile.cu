@@ -12,9 +12,11 @@
 //                both row tiles read a buffer, which halves the conversion per product;
 //   warps 8-11, 12-15  softmax of row tile A, B: a row a thread, no shuffles.
 // The issuer alternates S_A, P_B V, S_B, P_A V, so each softmax has the other tile's products to hide behind.
-// K is held at half and V at a quarter of its value, so that offset + 15 scale of any cache filled from
-// fp16 stays inside fp16; both factors are undone in fp32. A key tile whose values are all below 2^-7 has
-// V at 2^12 times its value and P at 2^-14 times, or V's scales would be fp16 subnormals.  A row's reference m moves as in the
+// Conversion: a nibble as it lies is the fp16 subnormal c * 2^-24 (or c * 2^-20), so with the scale times 2^24 one FMA
+// gives offset + code * scale, rounded once. The scale has to stay below 2^16 then, so each key tile of K and of V is held at a
+// power of two of its value that puts its largest below 2^-4 and leaves fp16 its precision
+// whatever the values' size: the power goes into the softmax's factor (K) and, as a difference to the largest
+// tile so far, into P (V). A row's reference m moves as in the
 // streaming kernel, and only then is O rescaled in tensor memory.
 // A non-finite V value enters as 0 (0 * NaN would reach every row of the tile) and marks its piece: at the piece's
 // end the rows look for such keys among those that they see, and get NaN in the groups.
@@ -35,7 +37,9 @@ using namespace kv4;
 constexpr int kRows = 256, kKeys = 128, kCost = 2, kThreads = 512;
 constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
-constexpr uint32_t kTinySize = 0x2000u;  // fp16 bits of 2^-7
+
+// The power of two e for a tile whose largest parameter has the fp16 bits `size` (of |offset|, 16 |scale|): size * 2^e is in [2^-5, 2^-4).
+__device__ __forceinline__ int tile_power(uint32_t size) { return 10 - max((int)(size >> 10), 1); }
 
 template <int D, int NG>
 struct TileSmem {
@@ -76,12 +80,23 @@ __device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Scale and offset of a group, times 2^e, as pairs for convert().
+struct Group {
+  uint32_t lower, upper, offset;
+};
+__device__ __forceinline__ Group group_of(uint32_t param, int e) {
+  const float2 so = unpack_half2(param);
+  const float f = pow2(e), s = so.x * f * 16777216.0f;
+  return {pack_half2(s, s), pack_half2(s * 0.0625f, s * 0.0625f), pack_half2(so.y * f, so.y * f)};
+}
+
 // A word's 8 codes to offset + code * scale, in the order (n0, n4), (n1, n5), (n2, n6), (n3, n7).
-__device__ __forceinline__ uint4 convert(uint32_t w, uint32_t scale2, uint32_t offset2) {
-  uint32_t d[4];
-  nibbles_to_centered_half2(w, zp_lo_const(0), zp_hi_const(0), d);
-  return make_uint4(hfma2_bits(d[0], scale2, offset2), hfma2_bits(d[1], scale2, offset2),
-                    hfma2_bits(d[2], scale2, offset2), hfma2_bits(d[3], scale2, offset2));
+__device__ __forceinline__ uint4 convert(uint32_t w, const Group& g) {
+  const uint32_t t = w >> 8;
+  return make_uint4(hfma2_bits(w & 0x000f000fu, g.lower, g.offset), hfma2_bits(w & 0x00f000f0u, g.upper, g.offset),
+                    hfma2_bits(t & 0x000f000fu, g.lower, g.offset), hfma2_bits(t & 0x00f000f0u, g.upper, g.offset));
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
@@ -100,9 +115,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ int raw_have[4];                 // blocks of a raw tile that were read
-  __shared__ uint32_t tile_info[kMeta];       // what the softmax needs to know: bits 0-7 blocks read, bit 8 V scaled up
+  __shared__ uint32_t tile_info[kMeta];       // for the softmax: bits 0-7 blocks read, 8-15 and 16-23 powers of K and V + 64
   __shared__ int odd_piece[kMeta];            // 1 + the last piece (modulo kMeta) with a V value that is not finite
-  __shared__ uint32_t v_size[2][4];           // fp16 bits of the largest V parameter, by dequantiser warp
+  __shared__ uint2 sizes[2][4];               // fp16 bits of the largest K and V parameters, by dequantiser warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = smem_u32(smem_raw);
@@ -214,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kv_phase = 0, p_phase = 0, q_phase = 0;  // a bit for each barrier
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t ph) {
-        if (__all_sync(kFull, mbar_spin_bounded(bar, ph))) return true;
+        if (__all_sync(kFull, mbar_wait_bounded(bar, ph))) return true;
         if (leader) give_up(kStatusMmaWait);
         ok = false;
         return false;
@@ -319,24 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int have = raw_have[stage];
         const uint32_t blk = smem_u32(raw_ring + stage * L::kRaw + (r >> 4) * L::kBlock);
         const uint32_t par = blk + 16 * D + row * 4;
-        // ---- V's parameters, zeros for keys that are not there; the four warps agree on the tile's factor ----
-        uint32_t vpar[NG], bad = 0, size = 0;  // size: the larger of |offset| and 16 |scale|
+        // ---- parameters, zeros for keys that are not there; the four warps agree on the tile's powers ----
+        uint32_t kpar[NG], vpar[NG], bad = 0, ksize = 0, vsize = 0;  // sizes: the larger of |offset| and 16 |scale|
         const bool there = tile * kKeys + r < cur.n && (have >> (r >> 4) & 1);
+        auto finite = [](uint32_t p) { return (p & 0x7c00u) != 0x7c00u && (p & 0x7c000000u) != 0x7c000000u; };
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
-          uint32_t p = there ? lds_u32_a(par + (NG + gi) * 64) : 0u;
-          if ((p & 0x7c00u) == 0x7c00u || (p & 0x7c000000u) == 0x7c000000u) bad = 1u, p = 0u;
-          vpar[gi] = p;
-          size = max(size, max((p & 0x7fffu) + 0x1000u, p >> 16 & 0x7fffu));
+          kpar[gi] = there ? lds_u32_a(par + gi * 64) : 0u;
+          vpar[gi] = there ? lds_u32_a(par + (NG + gi) * 64) : 0u;
+          if (!finite(vpar[gi])) bad = 1u, vpar[gi] = 0u;
+          if (finite(kpar[gi])) ksize = max(ksize, max((kpar[gi] & 0x7fffu) + 0x1000u, kpar[gi] >> 16 & 0x7fffu));
+          vsize = max(vsize, max((vpar[gi] & 0x7fffu) + 0x1000u, vpar[gi] >> 16 & 0x7fffu));
         }
-        size = __reduce_max_sync(kFull, size);
-        if (lane == 0) v_size[tiles & 1][warp - 4] = size;
+        ksize = __reduce_max_sync(kFull, ksize);
+        vsize = __reduce_max_sync(kFull, vsize);
+        if (lane == 0) sizes[tiles & 1][warp - 4] = make_uint2(ksize, vsize);
         if (bad) odd_piece[piece % kMeta] = piece + 1;
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        const uint32_t* vs = v_size[tiles & 1];
-        const bool tiny = max(max(vs[0], vs[1]), max(vs[2], vs[3])) < kTinySize;
-        if (r == 0) tile_info[tiles % kMeta] = (uint32_t)have | (tiny ? 256u : 0u);
-        // ---- K: halves of the values; keys that are not there hold anything, their scores are masked ----
+        for (int w = 0; w < 4; ++w) ksize = max(ksize, sizes[tiles & 1][w].x), vsize = max(vsize, sizes[tiles & 1][w].y);
+        const int ke = tile_power(ksize), ve = tile_power(vsize);
+        if (r == 0) tile_info[tiles % kMeta] = (uint32_t)have | (uint32_t)(ke + 64) << 8 | (uint32_t)(ve + 64) << 16;
+        // ---- K ----
         int buf = item % kBufs;
         if (item >= kBufs) {
           if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
@@ -346,29 +364,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           e_phase ^= 1u << buf;
         }
         {
-          uint32_t scale2[NG], offset2[NG];
+          Group gr[NG];
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi) {
-            const uint32_t p = lds_u32_a(par + gi * 64);
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&p), __half2half2(__ushort_as_half(0x3800)));  // 1/2
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-            scale2[gi] = __byte_perm(u, 0, 0x1010), offset2[gi] = __byte_perm(u, 0, 0x3232);
-          }
-          const uint32_t dst = buf_at + buf * L::kOperand + r * 128;
+          for (int gi = 0; gi < NG; ++gi) gr[gi] = group_of(kpar[gi], ke);
+          const uint32_t dst = buf_at + buf * L::kOperand + r * 128 + ((r & 7) << 4);  // chunk c: dst ^ c << 4 (swizzled)
+          // 16 bytes: words p = 4 ch .. of the row, word (t, w) = p / KW, p % KW; the starting chunk follows the
+          // lane, so that eight rows are read from distinct banks. All loads come before the first store.
+          uint4 v4[KW];
+#pragma unroll
+          for (int j = 0; j < KW; ++j) v4[j] = lds128_a(blk + row * (D / 2) + ((j + (lane >> 1)) & (KW - 1)) * 16);
 #pragma unroll
           for (int j = 0; j < KW; ++j) {
-            // 16 bytes: words p = 4 ch .. of the row, word (t, w) = p / KW, p % KW; the starting chunk follows the
-            // lane, so that eight rows are read from distinct banks
-            const int ch = KW == 8 ? j : (j + (lane >> 1)) & (KW - 1);
-            const uint4 v = lds128_a(blk + row * (D / 2) + ch * 16);
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+            const int ch = (j + (lane >> 1)) & (KW - 1);
+            const uint32_t w4[4] = {v4[j].x, v4[j].y, v4[j].z, v4[j].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int t = KW == 4 ? ch : ch * 2 + i / 2, w = KW == 4 ? i : i % 2;
-              const int gi = w * NG / KW;
-              const uint4 y = convert(w4[i], scale2[gi], offset2[gi]);
               const int chunk = 4 * w + t;  // 16-byte chunk of the row
-              sts128(dst + (chunk >> 3) * (kKeys * 128) + (((chunk & 7) ^ (r & 7)) << 4), y);
+              sts128((dst ^ ((chunk & 7) << 4)) + (chunk >> 3) * (kKeys * 128), convert(w4[i], gr[w * NG / KW]));
             }
           }
         }
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&kv_full[buf]);
         ++item;
-        // ---- V: quarters of the values ----
+        // ---- V ----
         buf = item % kBufs;
         if (item >= kBufs) {
           if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
@@ -386,32 +399,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           e_phase ^= 1u << buf;
         }
         {
-          const __half2 factor = __half2half2(__ushort_as_half(tiny ? 0x6c00 : 0x3400));  // 2^12 or 1/4
-          uint32_t scale2[NG], offset2[NG];
+          Group gr[KW];  // of each 32 elements
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&vpar[gi]), factor);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
-            scale2[gi] = __byte_perm(u, 0, 0x1010), offset2[gi] = __byte_perm(u, 0, 0x3232);
+            const Group y = group_of(vpar[gi], ve);
+#pragma unroll
+            for (int i = gi * (KW / NG); i < (gi + 1) * (KW / NG); ++i) gr[i] = y;
           }
-          const uint32_t dst = buf_at + buf * L::kOperand + r * 128;
+          const uint32_t dst = buf_at + buf * L::kOperand + r * 128 + ((r & 7) << 4);
+          uint32_t vw[8][VW];
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            uint32_t w4[VW];
             const uint32_t at = blk + 8 * D + v_word_byte<D>(g, row, 0);
             if constexpr (VW == 1) {
-              w4[0] = lds_u32_a(at);
+              vw[g][0] = lds_u32_a(at);
             } else {
               const uint2 v = lds_u64_a(at);
-              w4[0] = v.x, w4[1] = v.y;
+              vw[g][0] = v.x, vw[g][1] = v.y;
             }
+          }
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
               // nibbles (n, n + 4): elements 32 apart, of two groups when groups have 32
-              const int g0 = 2 * w * NG / KW, g1 = (2 * w + 1) * NG / KW;
-              const uint32_t s2 = g0 == g1 ? scale2[g0] : __byte_perm(scale2[g0], scale2[g1], 0x5410);
-              const uint32_t o2 = g0 == g1 ? offset2[g0] : __byte_perm(offset2[g0], offset2[g1], 0x5410);
-              sts128(dst + w * (kKeys * 128) + ((g ^ (r & 7)) << 4), convert(w4[w], s2, o2));
+              Group y = gr[2 * w];
+              if constexpr (NG == KW)
+                y = {__byte_perm(y.lower, gr[2 * w + 1].lower, 0x5410), __byte_perm(y.upper, gr[2 * w + 1].upper, 0x5410),
+                     __byte_perm(y.offset, gr[2 * w + 1].offset, 0x5410)};
+              sts128((dst ^ (g << 4)) + w * (kKeys * 128), convert(vw[g][w], y));
             }
           }
         }
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid & 127;  // row of the row tile, tensor memory lane
     const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_at + kColS + x * 128, o_at = lane_at + kColO + x * 128;
-    const float c1 = fmaxf(fabsf(a.scale) * (2.0f * kLog2e), FLT_MIN);  // K holds half values
+    const float c0 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     uint32_t s_phase = 0, o_phase = 0;
     int tiles = 0, piece = 0;
@@ -468,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_hi = a.causal ? min(cur.n, pos + 1) : cur.n;
       const int lim_lo = a.window > 0 ? pos - a.window + 1 : 0;
       float m = -FLT_MAX, l0 = 0.0f, l1 = 0.0f;
+      int v_power = 0;  // O is held at 2^v_power, the power of the piece's largest V tile so far
       for (int j = 0; j < here; ++j) {
         const int base = (cur.tile + j) * kKeys;
         if (ok && !__all_sync(kFull, mbar_wait_bounded(&s_full[x], s_phase))) {
@@ -486,7 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         load_half(1);
         const uint32_t in = tile_info[tiles % kMeta], have = in & 0xffu;
-        const bool tiny = in >> 8 != 0;
+        const float c1 = c0 * pow2(64 - (int)(in >> 8 & 0xffu));
+        const int ve = (int)(in >> 16) - 64;
         const bool masked = __any_sync(kFull, base < lim_lo || base + kKeys > lim_hi || have != 0xffu);
         ++tiles;
         auto mask_half = [&](int half) {
@@ -509,11 +527,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         if (masked) mask_half(0);
         top = fmaxf(top, top_half()) * c1;
-        if (__any_sync(kFull, top > m + kRise)) {
+        if (j == 0) v_power = ve;
+        if (__any_sync(kFull, top > m + kRise) || ve < v_power) {
           const float m2 = top > m + kRise ? top - kLift : m;
-          const float al = ex2(m - m2);
+          float al = ex2(m - m2);
           m = m2;
           l0 *= al, l1 *= al;
+          al *= pow2(min(ve - v_power, 0));
+          v_power = min(v_power, ve);
           if (j > 0) {
 #pragma unroll 1
             for (int i = 0; i < D / 32; ++i) {
@@ -527,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float shift = -m - (tiny ? 14.0f : 0.0f);
+        const float shift = -m - (float)(ve - v_power);
         float t0 = 0.0f, t1 = 0.0f;
         // P overlays S: keys 64 h .. 64 h + 63 go to columns 32 h .. 32 h + 31, whose scores are in registers
         // or used up. The products start on the first half while the second is made.
@@ -552,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[x][half]);
         }
-        l0 = fmaf(t0, tiny ? 16384.0f : 1.0f, l0), l1 = fmaf(t1, tiny ? 16384.0f : 1.0f, l1);
+        const float back = pow2(ve - v_power);
+        l0 = fmaf(t0, back, l0), l1 = fmaf(t1, back, l1);
       }
       // ---- the end of this piece ----
       if (ok && !__all_sync(kFull, mbar_wait_bounded(&o_full, o_phase))) {
@@ -589,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = from_start && ends;
       const float l = ok ? l0 + l1 : NAN;
       const bool none = l == 0.0f;
-      const float f = whole ? (none ? 0.0f : 4.0f / l) : 4.0f;  // V holds quarters
+      const float f = (whole ? (none ? 0.0f : 1.0f / l) : 1.0f) * pow2(-v_power);
       float* slot = slots + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kSlot;
       const int64_t out_row = (int64_t)(cur.q0 + tok) * a.q_heads + (int64_t)cur.kvh * G + head;
 #pragma unroll
