@@ -111,9 +111,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream=None):
@@ -494,27 +500,41 @@ def mnb_kv4_cache_alloc(num_pages: int, page_size: int, kv_heads: int, head_dim:
     return MnbKv4Cache(pages, page_size, head_dim, group_size)
 
 
+_ACT = {}  # torch dtype -> MNB_F16 / MNB_F32, filled on first use
+
+
 def _act_dtype(name, t):
+    if not _ACT:
+        torch = _torch()
+        _ACT.update({torch.float16: MNB_F16, torch.float32: MNB_F32})
+    code = _ACT.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
+    return code
+
+
+def _raw_stream(t, stream):
+    """Handle of ``stream``, or of the current stream of ``t``'s device."""
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    if t.dtype == torch.float16:
-        return MNB_F16
-    if t.dtype == torch.float32:
-        return MNB_F32
-    raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object: 3 us of a call
+    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _token_rows(name, t, heads, D, dtype):
     """Elements between the tokens of ``[T, heads, D]``, whose heads must lie one after the other."""
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype != dtype or not t.is_cuda:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {list(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {list(shape)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError(f"{name}: the heads of a token must lie one after the other")
-    return s0 if t.shape[0] > 1 else heads * D
+    return s0 if shape[0] > 1 else heads * D
 
 
 def _new(shape, dtype, device, stream):
@@ -527,8 +547,9 @@ def _new(shape, dtype, device, stream):
 
 
 def _index(name, t, dtype, shape):
-    _check_dev(name, t, dtype)
-    if tuple(t.shape) != shape:
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _check_dev(name, t, dtype)
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
@@ -539,8 +560,9 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
     ``q`` (or None).  ``cos`` and ``sin`` are fp32 ``[rows, rot_dim / 2]``, None for no rotation."""
     torch = _torch()
     dtype = k.dtype
-    dt, T, Hk, D = _act_dtype("k", k), k.shape[0], cache.kv_heads, cache.head_dim
+    dt, Hk, D = _act_dtype("k", k), cache.kv_heads, cache.head_dim
     ks, vs = _token_rows("k", k, Hk, D, dtype), _token_rows("v", v, Hk, D, dtype)
+    T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"v has {v.shape[0]} tokens, k has {T}")
     qs = Hq = 0
@@ -553,16 +575,17 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
         if q_out is None:
             q_out = _new((T, Hq, D), dtype, q.device, stream)
         qp, op = q.data_ptr(), _index("q_out", q_out, dtype, (T, Hq, D))
-    rope = MnbRope(None, None, 0, 0, 0)
-    pp = None
     if cos is not None:
         rows, half = cos.shape
         rope = MnbRope(_index("cos", cos, torch.float32, (rows, half)), _index("sin", sin, torch.float32, (rows, half)),
                        rows, 2 * half, 1 if interleaved else 0)
         pp = _index("positions", positions, torch.int32, (T,))
-    sp = _index("slots", slots, torch.int64, (T,))
-    _raise(load_library().mnb_kv4_append(qp, k.data_ptr(), v.data_ptr(), dt, T, Hq, qs, ks, vs, pp, rope, sp, cache.arg,
-                                         op, _stream_handle(stream)))
+    else:
+        rope, pp = MnbRope(None, None, 0, 0, 0), None
+    st = load_library().mnb_kv4_append(qp, k.data_ptr(), v.data_ptr(), dt, T, Hq, qs, ks, vs, pp, rope,
+                                       _index("slots", slots, torch.int64, (T,)), cache.arg, op, _raw_stream(k, stream))
+    if st != MNB_OK:
+        _raise(st)
     return q_out
 
 
@@ -577,9 +600,11 @@ def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, 
         k_out = _new(shape, dtype, slots.device, stream)
     if v_out is None:
         v_out = _new(shape, dtype, slots.device, stream)
-    kp, vp = _index("k_out", k_out, dtype, shape), _index("v_out", v_out, dtype, shape)
-    _raise(load_library().mnb_kv4_read(cache.arg, _index("slots", slots, torch.int64, (T,)), T,
-                                       _act_dtype("k_out", k_out), kp, vp, _stream_handle(stream)))
+    st = load_library().mnb_kv4_read(cache.arg, _index("slots", slots, torch.int64, (T,)), T,
+                                     _act_dtype("k_out", k_out), _index("k_out", k_out, dtype, shape),
+                                     _index("v_out", v_out, dtype, shape), _raw_stream(slots, stream))
+    if st != MNB_OK:
+        _raise(st)
     return k_out, v_out
 
 
@@ -601,20 +626,26 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     dtype, dt = q.dtype, _act_dtype("q", q)
     qs = _token_rows("q", q, Hq, cache.head_dim, dtype)
     B = kv_len.shape[0]
-    need = mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
-    if workspace is None and need > 0:
-        workspace = _new(need, torch.uint8, q.device, stream)
-    _check_dev("workspace", workspace)
+    lib = load_library()
+    if workspace is None:
+        need = lib.mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
+        workspace = _new(need, torch.uint8, q.device, stream) if need else None
+    else:
+        _check_dev("workspace", workspace)
     if out is None:
         out = _new((T, Hq, D), dtype, q.device, stream)
-    op = _index("out", out, dtype, (T, Hq, D))
+        op = out.data_ptr()
+    else:
+        op = _index("out", out, dtype, (T, Hq, D))
     lp = None if lse is None else _index("lse", lse, torch.float32, (T, Hq))
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [{B}, pages], got {list(page_table.shape)}")
     stride = page_table.shape[1]
-    _raise(load_library().mnb_kv4_attention(
+    st = lib.mnb_kv4_attention(
         q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
         _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
         stride, scale, 1 if causal else 0, window, None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), op, lp, _stream_handle(stream)))
+        0 if workspace is None else workspace.nbytes, op, lp, _raw_stream(q, stream))
+    if st != MNB_OK:
+        _raise(st)
     return out

@@ -5,6 +5,7 @@
 // >= 16; marlin_gemm.rs, launch_marlin_gemm: K a multiple of 16 and of the group size,
 // sizes that fit 32-bit indices), with every failure returned as a status code and a
 // message instead of an exception (the EpError::KernelFailed strings of matmul_nbits.rs).
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -90,12 +91,17 @@ mnb_status make_ctx(const char* fn, mnb_stream stream, mnb::LaunchCtx* ctx) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(fn, e);
-  int sms = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(fn, e);
+  static std::atomic<int> known[128];  // SMs of each device, asked for once
+  int sms = dev < 128 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(fn, e);
+    if (dev < 128) known[dev].store(sms, std::memory_order_relaxed);
+  }
   ctx->stream = reinterpret_cast<cudaStream_t>(stream);
   ctx->pdl = g_pdl;
   ctx->num_sms = sms;
+  ctx->device = dev;
   ctx->status = device_status_ptr(dev);
   ctx->variant = nullptr;
   return MNB_OK;

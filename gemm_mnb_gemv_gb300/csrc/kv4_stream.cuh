@@ -731,7 +731,8 @@ cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention&
   using L = Layout<D, NG, NT, PB, F32>;
   constexpr int smem = L::kFixed + kWarps * L::stages(227 * 1024 / per_sm - 1024) * PB * L::kBlock;
   auto kern = kv4_stream_kernel<D, NG, NT, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, smem, ctx.device, done);
   if (e != cudaSuccess) return e;
   const int grid = per_sm * (ctx.num_sms < 160 ? ctx.num_sms : 160);
   // n / ppb = n * magic >> 36 for n < 2^26 (2^30 tokens), ppb <= 256: n * ppb < 2^36

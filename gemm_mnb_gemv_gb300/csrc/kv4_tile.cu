@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int NG>
 cudaError_t launch_tile(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a) {
   auto kern = kv4_tile_kernel<D, NG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D, NG>::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, TileSmem<D, NG>::kBytes, ctx.device, done);
   if (e != cudaSuccess) return e;
   const int grid = ctx.num_sms < 160 ? ctx.num_sms : 160;
   const uint64_t ppb = (uint64_t)(c.page_size / 16), magic = ((1ull << 36) + ppb - 1) / ppb;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -18,6 +19,7 @@ struct LaunchCtx {
   cudaStream_t stream;
   bool pdl;         // launch with programmatic stream serialisation
   int num_sms;
+  int device = 0;
   uint32_t* status = nullptr;     // device status word for bounded waits
   const void* bias = nullptr;     // fp16 [N] or null
   int bias_mode = 0;              // 0 none, 1 fp16(acc + b), 2 fp16(fp16(acc) + b)
@@ -139,6 +141,17 @@ cudaError_t launch_kv4_read(LaunchCtx& ctx, const Kv4Cache& c, const int64_t* sl
                             void* v_out);
 cudaError_t launch_kv4_attention(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a);
 size_t kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim, int f32);
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device: `done` is a static of the caller,
+// a bit for each device.
+template <typename Kern>
+cudaError_t allow_smem(Kern kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch helper: cudaLaunchKernelEx with the programmatic-serialisation attribute when
 // ctx.pdl is set.
