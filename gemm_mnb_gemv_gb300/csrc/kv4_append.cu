@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
   using P = Passes<D>;
   constexpr int kLanes = P::kLanes;
   const P passes(a.q_heads, c.kv_heads);
-  const int t = blockIdx.x, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const int gl = c.group / 8;  // lanes of a group: 4, 8 or 16
   // q: the lane's two chunks of 8 elements. Rotated elements come first, half-split pairs as one chunk of each side.
   const int qj = tid % P::kQLanes, half = a.rot / 2;
@@ -141,6 +141,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
   const int sub = tid % kLanes, d = 8 * sub;
   const bool k_turns = d < a.rot;
   const int partner = d < half ? d + half : d - half;
+  const int64_t capacity = (int64_t)c.num_pages * c.page_size;
+  int64_t slot = a.slots[blockIdx.x];
+  int pos = a.rot ? a.positions[blockIdx.x] : 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  const int64_t slot_now = slot;
+  const int pos_now = pos;
+  if (t + gridDim.x < a.T) {  // the next token's numbers are on their way while this one is worked on
+    slot = a.slots[t + gridDim.x];
+    if (a.rot) pos = a.positions[t + gridDim.x];
+  }
   bool known = false, store = false, pos_ok = true;
   int r = 0;
   uint8_t* blk0 = nullptr;  // the token's block of key head 0
@@ -169,14 +179,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
     }
     if (!known) {  // the token's own numbers
       known = true;
-      const int64_t slot = a.slots[t];
-      const int64_t capacity = (int64_t)c.num_pages * c.page_size;
-      const int pos = a.rot ? a.positions[t] : 0;
-      pos_ok = a.rot == 0 || (pos >= 0 && pos < a.rows);
-      store = slot >= 0 && slot < capacity && pos_ok;
-      if (tid == 0 && blockIdx.y == 0 && (slot >= capacity || !pos_ok)) report_status(status, kStatusBadIndex);
+      pos_ok = a.rot == 0 || (pos_now >= 0 && pos_now < a.rows);
+      store = slot_now >= 0 && slot_now < capacity && pos_ok;
+      if (tid == 0 && blockIdx.y == 0 && (slot_now >= capacity || !pos_ok)) report_status(status, kStatusBadIndex);
       if (a.rot && pos_ok) {
-        const float *cos = a.cos + (int64_t)pos * half, *sin = a.sin + (int64_t)pos * half;
+        const float *cos = a.cos + (int64_t)pos_now * half, *sin = a.sin + (int64_t)pos_now * half;
         if (q_turns) qc = load8<true>(cos, 8 * qj), qs = load8<true>(sin, 8 * qj);
         if (k_turns) {
           // interleaved: pairs d / 2 .. d / 2 + 3, the first four values
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
       if (store) {
         int64_t page;
         int in_page;
-        split_slot(slot, c.page_size, page, in_page);
+        split_slot(slot_now, c.page_size, page, in_page);
         r = in_page % 16;
         blk0 = c.pages + (page * c.kv_heads * (c.page_size / 16) + in_page / 16) * c.block_bytes();
       }
@@ -287,6 +294,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
             __halves2half2(scale, offset);
     }
   }
+  }
 }
 
 constexpr int kReadThreads = 256;
@@ -354,14 +362,15 @@ __global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const Kv4Cache c
 
 // Few tokens: their passes are spread over the SMs. Many: a block takes a token's passes, four (fp32: two) in flight
 // (append), or four tokens (read).
-constexpr int kFewTokens = 304;
+constexpr int kFewTokens = 304, kManyBlocks = 4;  // blocks an SM holds: by registers
 
 cudaError_t launch_kv4_append(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Append& a) {
   ctx.variant = "kv4_append";
   const bool few = a.T <= kFewTokens;
   auto pick = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    const dim3 grid(a.T, few ? Passes<D>(a.q_heads, c.kv_heads).count() : 1);
+    const int blocks = kManyBlocks * ctx.num_sms;
+    const dim3 grid(few || a.T < blocks ? a.T : blocks, few ? Passes<D>(a.q_heads, c.kv_heads).count() : 1);
     auto go = [&](auto kern) { return launch_kernel(ctx, kern, grid, dim3(kAppendThreads), 0, c, a, ctx.status); };
     if (a.f32) return few ? go(kv4_append_kernel<D, true, 1>) : go(kv4_append_kernel<D, true, 2>);
     return few ? go(kv4_append_kernel<D, false, 1>) : go(kv4_append_kernel<D, false, 4>);
