@@ -464,17 +464,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = cur.qlen * G, row = cur.rt * kRows + x * 128 + r;
       const bool live = row < rows;
       const int tok = live ? row / G : 0, head = live ? row - tok * G : 0;
+      const int wrow = r & ~31;  // first row of this warp
       {
-        const __half* q = static_cast<const __half*>(a.q) + (int64_t)(cur.q0 + tok) * a.q_stride +
-                          ((int64_t)cur.kvh * G + head) * D;
-        const uint32_t dst = q_at + x * (L::kQ / 2) + r * 128;
+        // whole rows of q by neighbouring lanes: a lane that reads its own row takes a line for every 16 bytes
+        const int64_t own = (int64_t)(cur.q0 + tok) * a.q_stride + ((int64_t)cur.kvh * G + head) * D;
+        constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;  // 16-byte chunks of a row, rows an instruction
+        const int ch = lane % kChunks;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 8 * kAtOnce) {
+          uint4 v[8];
 #pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
-          uint4 v = live ? *reinterpret_cast<const uint4*>(q + ch * 8) : make_uint4(0, 0, 0, 0);
-          uint32_t p[4];
-          pair_halves_stride4(v, p);
-          sts128(dst + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (r & 7)) << 4),
-                 make_uint4(p[0] ^ flip, p[1] ^ flip, p[2] ^ flip, p[3] ^ flip));
+          for (int i = 0; i < 8; ++i) {
+            const int from = i0 + i * kAtOnce + lane / kChunks;
+            const int64_t at = __shfl_sync(kFull, own, from);
+            const bool there = __shfl_sync(kFull, (int)live, from) != 0;
+            v[i] = there ? *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at + ch * 8) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int to = wrow + i0 + i * kAtOnce + lane / kChunks;
+            uint32_t p[4];
+            pair_halves_stride4(v[i], p);
+            sts128(q_at + x * (L::kQ / 2) + (ch >> 3) * (128 * 128) + to * 128 + (((ch ^ to) & 7) << 4),
+                   make_uint4(p[0] ^ flip, p[1] ^ flip, p[2] ^ flip, p[3] ^ flip));
+          }
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -507,12 +520,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ve = (int)(in >> 16) - 64;
         const bool masked = __any_sync(kFull, base < lim_lo || base + kKeys > lim_hi || have != 0xffu);
         ++tiles;
+        // keys of a half that this row does not see, as bits (a block's 16 keys together when it was not read)
         auto mask_half = [&](int half) {
-          const int lo = lim_lo - base - 64 * half, hi = lim_hi - base - 64 * half;
-          const uint32_t blocks = have >> (4 * half);
+          const int lo = min(max(lim_lo - base - 64 * half, 0), 64), hi = min(max(lim_hi - base - 64 * half, 0), 64);
+          uint64_t see = hi == 64 ? ~0ull : (1ull << hi) - 1;
+          see = lo == 64 ? 0 : see >> lo << lo;
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i < lo || i >= hi || !(blocks >> (i >> 4) & 1)) v[i] = -INFINITY;
+          for (int i = 0; i < 4; ++i)
+            if (!(have >> (4 * half + i) & 1)) see &= ~(0xffffull << (16 * i));
+          const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (!(s0 >> i & 1)) v[i] = -INFINITY;
+            if (!(s1 >> i & 1)) v[32 + i] = -INFINITY;
+          }
         };
         auto top_half = [&]() {
           float t0 = v[0], t1 = v[1];
@@ -520,14 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 2; i < 62; i += 4) t0 = max3(t0, v[i], v[i + 1]), t1 = max3(t1, v[i + 2], v[i + 3]);
           return fmaxf(max3(t0, v[62], v[63]), t1);
         };
-        tc::tmem_wait_ld();
-        if (masked) mask_half(1);
-        float top = top_half();
-        load_half(0);
-        tc::tmem_wait_ld();
-        if (masked) mask_half(0);
-        top = fmaxf(top, top_half()) * c1;
-        if (j == 0) v_power = ve;
+        // Loops that could be unrolled are not: the four roles' code has to stay in the instruction cache together.
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int half = 1; half >= 0; --half) {
+          if (half == 0) load_half(0);
+          tc::tmem_wait_ld();
+          if (masked) mask_half(half);
+          top = fmaxf(top, top_half());
+        }
+        top *= c1;
         if (__any_sync(kFull, top > m + kRise) || ve < v_power) {
           const float m2 = top > m + kRise ? top - kLift : m;
           float al = ex2(m - m2);
@@ -552,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float t0 = 0.0f, t1 = 0.0f;
         // P overlays S: keys 64 h .. 64 h + 63 go to columns 32 h .. 32 h + 31, whose scores are in registers
         // or used up. The products start on the first half while the second is made.
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           if (half == 1) {
             load_half(1);
@@ -614,43 +637,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = (whole ? (none ? 0.0f : 1.0f / l) : 1.0f) * pow2(-v_power);
       float* slot = slots + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kSlot;
       const int64_t out_row = (int64_t)(cur.q0 + tok) * a.q_heads + (int64_t)cur.kvh * G + head;
-#pragma unroll
+      // 64 elements of 32 rows at a time through this warp's part of q's room (nothing reads q any more), so that
+      // neighbouring lanes store whole lines
+      uint8_t* room = smem + x * (L::kQ / 2) + wrow * (L::kQ / 256);
+      constexpr int kRoom = 32 * (L::kQ / 256);
+#pragma unroll 1
       for (int w = 0; w < VW; ++w) {
         // columns 64 w + 8 g + i hold element 64 w + 32 (i & 1) + 4 g + i / 2
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {  // g of 4 half ..
           float o[32];
           if (ok) {
             tc::tmem_ld32(o_at + 64 * w + 32 * half, o);
             tc::tmem_wait_ld();
           }
+          // 0 of a row that sees nothing (its l is 0 and so is f), NaN of groups that have one and of a call that gave up
+          const float f0 = (nan_groups >> (2 * w * NG / KW) & 1) || !ok ? NAN : f;
+          const float f1 = (nan_groups >> ((2 * w + 1) * NG / KW) & 1) || !ok ? NAN : f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int gi = (2 * w + (i & 1)) * NG / KW;
-            o[i] = none && whole ? 0.0f : o[i] * f;
-            if ((nan_groups >> gi & 1) || !ok) o[i] = NAN;
-          }
-          if (live) {
+          for (int i = 0; i < 32; ++i) o[i] = none && whole ? 0.0f : o[i] * (i & 1 ? f1 : f0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-              for (int g2 = 0; g2 < 4; g2 += 2) {  // elements 64 w + 32 h + 16 half + 4 g2 .. + 7
-                float y[8];
+            for (int g2 = 0; g2 < 4; g2 += 2) {  // elements 32 h + 16 half + 4 g2 .. + 7 of the 64
+              float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 2 * (k % 4) + h];
-                const int d = 64 * w + 32 * h + 16 * half + 4 * g2;
-                if (whole) {
-                  *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + out_row * D + d) = make_uint4(
-                      pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
-                } else {
-                  float4* s4 = reinterpret_cast<float4*>(slot + (x * 128 + r) * D + d);
-                  s4[0] = make_float4(y[0], y[1], y[2], y[3]);
-                  s4[1] = make_float4(y[4], y[5], y[6], y[7]);
-                }
+              for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 2 * (k % 4) + h];
+              const int d8 = 4 * h + 2 * half + g2 / 2;  // eight elements
+              if (whole) {
+                *reinterpret_cast<uint4*>(room + lane * 128 + ((d8 ^ lane) & 7) * 16) = make_uint4(
+                    pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+              } else if (kRoom >= 8192) {
+                float4* s4 = reinterpret_cast<float4*>(room + lane * 256);
+                s4[(2 * d8) ^ (lane & 15)] = make_float4(y[0], y[1], y[2], y[3]);
+                s4[(2 * d8 + 1) ^ (lane & 15)] = make_float4(y[4], y[5], y[6], y[7]);
+              } else if (live) {
+                float4* s4 = reinterpret_cast<float4*>(slot + (x * 128 + r) * D + 64 * w + 8 * d8);
+                s4[0] = make_float4(y[0], y[1], y[2], y[3]);
+                s4[1] = make_float4(y[4], y[5], y[6], y[7]);
               }
             }
           }
         }
+        __syncwarp();
+        if (whole) {
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            const int from = 4 * i + lane / 8, ch = lane % 8;
+            const int64_t to = __shfl_sync(kFull, out_row, from);
+            const bool there = __shfl_sync(kFull, (int)live, from) != 0;
+            const uint4 y = *reinterpret_cast<const uint4*>(room + from * 128 + ((ch ^ from) & 7) * 16);
+            if (there) *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + to * D + 64 * w + 8 * ch) = y;
+          }
+        } else if (kRoom >= 8192) {
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int from = 2 * i + lane / 16, ch = lane % 16;
+            const bool there = __shfl_sync(kFull, (int)live, from) != 0;
+            const float4 y = *reinterpret_cast<const float4*>(room + from * 256 + (ch ^ (from & 15)) * 16);
+            if (there) *reinterpret_cast<float4*>(slot + (x * 128 + wrow + from) * D + 64 * w + 4 * ch) = y;
+          }
+        }
+        __syncwarp();
       }
       if (live) {
         if (whole) {
