@@ -541,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 2; i < 62; i += 4) t0 = max3(t0, v[i], v[i + 1]), t1 = max3(t1, v[i + 2], v[i + 3]);
           return fmaxf(max3(t0, v[62], v[63]), t1);
         };
-        // Loops that could be unrolled are not: the four roles' code has to stay in the instruction cache together.
+        // Most loops that could be unrolled are not: the four roles' code has to stay in the instruction cache together (a chunk
+        // of 2048 over 32768 keys: 805 us; with this loop unrolled too 878, with the one below rolled 921).
         float top = -INFINITY;
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float t0 = 0.0f, t1 = 0.0f;
         // P overlays S: keys 64 h .. 64 h + 63 go to columns 32 h .. 32 h + 31, whose scores are in registers
         // or used up. The products start on the first half while the second is made.
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (half == 1) {
             load_half(1);
