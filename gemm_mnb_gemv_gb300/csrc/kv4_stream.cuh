@@ -741,7 +741,7 @@ cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention&
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the joining kernel waits for the streaming kernel on the device
-  e = launch_kernel(ctx, kv4_join_kernel<D, NT, 4, F32>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
+  e = launch_kernel(ctx, kv4_join_kernel<D, NT, F32>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
   ctx.pdl = pdl;
   return e;
 }

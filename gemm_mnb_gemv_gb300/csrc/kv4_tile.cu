@@ -34,7 +34,8 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kRows = 256, kKeys = 128, kCost = 2, kThreads = 512;
+constexpr int kRows = 256, kKeys = 128, kThreads = 512;
+constexpr int kCost = 3;   // tiles that a piece's start and end cost: 2: 50 and 86 us (16 drafted tokens over 32768 keys; prompts), 3: 47 and 85
 constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
 
@@ -735,7 +736,7 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the joining kernel waits for this one on the device
-  e = launch_kernel(ctx, kv4_join_kernel<D, kRows / 8, 1, false>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
+  e = launch_kernel(ctx, kv4_join_kernel<D, kRows / 8, false>, dim3(ctx.num_sms), dim3(kJoinWarps * 32), 0, c, a, grid);
   ctx.pdl = pdl;
   return e;
 }

@@ -199,19 +199,20 @@ __device__ __forceinline__ bool find_range(const Walk<RT, kTile, kPieceCost>& wa
 }
 
 // Joins the pieces of cut sequences: o = sum_p e^(m_p - m) o_p / sum_p e^(m_p - m) l_p, in a fixed order. Each
-// block lists the cut sequences from the CTAs' entries; teams of kTeam warps take their rows
-// in turn, each warp every kTeam-th piece, several of them in flight.
+// block lists the cut sequences from the CTAs' entries; teams of warps take their rows in turn, each warp its share of
+// the pieces, several of them in flight. With few rows a team is four warps (many pieces each), with more rows than such
+// teams it is one.
 constexpr int kJoinWarps = 16;
-template <int D, int NT, int kTeam, bool F32>
+template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a, int ctas) {
-  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = kTeam == 1 ? 4 : 10;
+  constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = NT > 4 ? 4 : D > 128 ? 5 : 10;
   __shared__ float part[kJoinWarps][D + 4];  // o, then l and m
   __shared__ int list[kMaxCtas];
   __shared__ int count[kJoinWarps + 1];
   pdl_wait();
   const Piece* pieces = reinterpret_cast<const Piece*>(a.workspace);
   const float* slots = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % kTeam;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int n_list = 0;
   for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
     const int i = i0 + threadIdx.x;
@@ -229,22 +230,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cach
     __syncthreads();
   }
   const int G = a.q_heads / c.kv_heads;
-  const int teams = kJoinWarps / kTeam;
   const int items = n_list * RT;
+  const int team = items > (int)gridDim.x * (kJoinWarps / 4) ? 1 : 4;
+  const int teams = kJoinWarps / team, sub = warp % team;
   for (int item0 = blockIdx.x * teams; item0 < items; item0 += gridDim.x * teams) {
-    const int item = item0 + warp / kTeam;
+    const int item = item0 + warp / team;
     const int last = item < items ? list[item / RT] : 0, col = item % RT;
     Piece p = {};
     if (item < items) p = pieces[last];
     const bool live = item < items && p.row0 + col < p.rows;
     const int n = live ? last - p.first + 1 : 0;
     float m = -FLT_MAX, l = 0.0f, acc[E] = {};
-    for (int i0 = sub; i0 < n; i0 += kTeam * kFlight) {
+    for (int i0 = sub; i0 < n; i0 += team * kFlight) {
       float2 ml[kFlight];
       float v[kFlight][E];
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
-        const int i = i0 + k * kTeam;
+        const int i = i0 + k * team;
         ml[k] = make_float2(-FLT_MAX, 0.0f);
         if (i < n) {
           const float* s = slots + ((int64_t)(p.first + i) * 2 + (i == 0 ? 1 : 0)) * kSlot;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cach
       for (int e = 0; e < E; ++e) acc[e] *= al;
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
-        if (i0 + k * kTeam < n) {
+        if (i0 + k * team < n) {
           const float f = ex2(ml[k].x - top);
           l = fmaf(ml[k].y, f, l);
 #pragma unroll
@@ -278,12 +280,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cach
     __syncthreads();
     if (live && sub == 0) {
       float top = part[warp][D + 1];
-      for (int w = 1; w < kTeam; ++w) top = fmaxf(top, part[warp + w][D + 1]);
-      float den = 0.0f, f[kTeam];
-      for (int w = 0; w < kTeam; ++w) {
-        f[w] = ex2(part[warp + w][D + 1] - top);
-        den = fmaf(part[warp + w][D], f[w], den);
-      }
+      for (int w = 1; w < team; ++w) top = fmaxf(top, part[warp + w][D + 1]);
+      float den = 0.0f, f[4] = {};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (w < team) {
+          f[w] = ex2(part[warp + w][D + 1] - top);
+          den = fmaf(part[warp + w][D], f[w], den);
+        }
       const int r = p.row0 + col;
       const int64_t row = (int64_t)(p.q0 + r / G) * a.q_heads + (int64_t)p.kvh * G + r % G;
       const bool none = den == 0.0f;
@@ -292,7 +296,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cach
       for (int e = 0; e < E; e += 2) {
         const int d = e * 32 + lane * 2;
         float2 v = make_float2(0.0f, 0.0f);
-        for (int w = 0; w < kTeam; ++w) v.x = fmaf(part[warp + w][d], f[w], v.x), v.y = fmaf(part[warp + w][d + 1], f[w], v.y);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w < team) v.x = fmaf(part[warp + w][d], f[w], v.x), v.y = fmaf(part[warp + w][d + 1], f[w], v.y);
         v.x *= inv, v.y *= inv;
         if (none) v = make_float2(0.0f, 0.0f);
         if constexpr (F32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + d) = v;
