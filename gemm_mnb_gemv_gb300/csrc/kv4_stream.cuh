@@ -9,7 +9,8 @@
 //     added in fp32.
 //   * V: codes become c - 8 (exact), probabilities become fp16(p * scale_g * 2^x) per group, and
 //     sum_j p_j (offset + 8 scale) is kept in fp32.  Centring keeps the rounding of p * scale from being
-//     multiplied by |offset| / |v|.  The power 2^x follows the largest scale seen, so values of any size use
+//     multiplied by |offset| / |v| (fp32 activations centre K too: fp32 sums of uncentred products would lose
+//     two bits).  The power 2^x follows the largest scale seen, so values of any size use
 //     fp16's whole range.
 // A row's reference m moves only when a score passes it by 14 (in powers of two; one vote a
 // block instead of shuffles) and is then set 8 below the largest: p = 2^(s - m) <= 2^14, so
@@ -42,13 +43,13 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   return d;
 }
 
-// Two V code pairs to fp16 c - 8: the lower and the upper nibble of each byte pair position.
-__device__ __forceinline__ uint32_t v_lower(uint32_t x) {
+// Codes to fp16 c - 8, exact, two at a time: the lower and the upper nibbles of two byte positions.
+__device__ __forceinline__ uint32_t c_lower(uint32_t x) {
   uint32_t r = lop3_and_or(x, 0x000f000fu, 0x64006400u);  // 1024 + c
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0xE408E408u));
   return r;
 }
-__device__ __forceinline__ uint32_t v_upper(uint32_t x) {
+__device__ __forceinline__ uint32_t c_upper(uint32_t x) {
   uint32_t r = lop3_and_or(x, 0x00f000f0u, 0x64006400u);  // 1024 + 16 c
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(r), "r"(0x2C002C00u), "r"(0xD480D480u));
   return r;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
         if ((i + 1) % GR == 0) {
           acc += __shfl_xor_sync(kFull, acc, 1);
           acc += __shfl_xor_sync(kFull, acc, 2);
-          acc *= 5.9604644775390625e-8f;  // 2^-24, as the codes
+          if (!F32) acc *= 5.9604644775390625e-8f;  // 2^-24, as the codes
           if constexpr (NT == 1)
             qsreg[i / GR] = make_float2(__shfl_sync(kFull, acc, 8 * t), __shfl_sync(kFull, acc, 8 * t + 4));
           else if (t == 0)
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const float x0 = q[i][2 * s], x1 = q[i][2 * s + 4];
-          const float y0 = q[i][2 * s + 1] * 0.0625f, y1 = q[i][2 * s + 5] * 0.0625f;
+          const float y0 = q[i][2 * s + 1] * (F32 ? 1.0f : 0.0625f), y1 = q[i][2 * s + 5] * (F32 ? 1.0f : 0.0625f);
           const uint2 hi = make_uint2(pack_half2(x0, x1), pack_half2(y0, y1));
           if constexpr (kQreg) qreg[2 * i + s] = hi;
           else qf[((2 * i + s) * NT + my_nt) * 32 + lane] = hi;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
           }
         }
       }
-      const float fac = scalbnf(a.scale * kLog2e, e + 24);
+      const float fac = scalbnf(a.scale * kLog2e, F32 ? e : e + 24);
       if constexpr (NT == 1)
         cf[0][0] = __shfl_sync(kFull, fac, 8 * t), cf[0][1] = __shfl_sync(kFull, fac, 8 * t + 4);
       else if (t == 0)
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
 #pragma unroll
                   for (int p = 0; p < PB; ++p) {
                     const uint32_t x = kw[p][0][i] >> (8 * st), y = kw[p][1][i] >> (8 * st);
-                    const uint32_t a0 = x & 0x000f000fu, a2 = x & 0x00f000f0u, a1 = y & 0x000f000fu, a3 = y & 0x00f000f0u;
+                    const uint32_t a0 = F32 ? c_lower(x) : x & 0x000f000fu, a2 = F32 ? c_upper(x) : x & 0x00f000f0u;
+                    const uint32_t a1 = F32 ? c_lower(y) : y & 0x000f000fu, a3 = F32 ? c_upper(y) : y & 0x00f000f0u;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                       uint2 b;
@@ -423,15 +425,16 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
               for (int nt = 0; nt < NT; ++nt) {
                 float* sp = s[p][nt];
                 if (gi * SG % GR == 0) {
+                  const float z0 = F32 ? fmaf(8.0f, p0.x, p0.y) : p0.y, z1 = F32 ? fmaf(8.0f, p1.x, p1.y) : p1.y;
                   float2 qs;
                   if constexpr (kQsReg) qs = qsreg[grp * NT + nt];
                   else qs = *reinterpret_cast<const float2*>(&qsf[(grp * NT + nt) * 8 + 2 * t]);
                   if (gi == 0) {
-                    sp[0] = p0.y * qs.x, sp[1] = p0.y * qs.y;
-                    sp[2] = p1.y * qs.x, sp[3] = p1.y * qs.y;
+                    sp[0] = z0 * qs.x, sp[1] = z0 * qs.y;
+                    sp[2] = z1 * qs.x, sp[3] = z1 * qs.y;
                   } else {
-                    sp[0] = fmaf(p0.y, qs.x, sp[0]), sp[1] = fmaf(p0.y, qs.y, sp[1]);
-                    sp[2] = fmaf(p1.y, qs.x, sp[2]), sp[3] = fmaf(p1.y, qs.y, sp[3]);
+                    sp[0] = fmaf(z0, qs.x, sp[0]), sp[1] = fmaf(z0, qs.y, sp[1]);
+                    sp[2] = fmaf(z1, qs.x, sp[2]), sp[3] = fmaf(z1, qs.y, sp[3]);
                   }
                 }
                 sp[0] = fmaf(acc[p][nt][0], p0.x, sp[0]), sp[1] = fmaf(acc[p][nt][1], p0.x, sp[1]);
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
             uint32_t x = __byte_perm(vw[0][i / 2], vw[1][i / 2], sel), y = __byte_perm(vw[2][i / 2], vw[3][i / 2], sel);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t a0 = v_lower(x), a1 = v_upper(x), a2 = v_lower(y), a3 = v_upper(y);
+              const uint32_t a0 = c_lower(x), a1 = c_upper(x), a2 = c_lower(y), a3 = c_upper(y);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 if constexpr (F32) {  // added outside the tensor cores, with rounding
