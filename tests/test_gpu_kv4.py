@@ -479,3 +479,59 @@ def test_binding_refusals(env):
         mnb.MnbKv4Cache(cache.pages, 16, 96, 64)
     with pytest.raises(mnb.MnbError):
         mnb.mnb_kv4_cache_alloc(2, 10, 2, 128, 64, dev)
+
+
+def test_more_sequences_than_threads_look_at(env):
+    """More than 128 sequences: the work list is scanned in turns."""
+    rng = np.random.default_rng(14)
+    lens = [(int(rng.integers(0, 3)), int(rng.integers(0, 60))) for _ in range(300)] + [(1, 400)]
+    _run(env, rng, 64, 64, 16, 1, 2, lens, "f16")
+    lens = [(int(rng.integers(0, 60)), int(rng.integers(1, 90))) for _ in range(140)]
+    assert _run(env, rng, 64, 32, 16, 1, 2, lens, "f16") == "kv4_tile_tcgen05"
+
+
+@pytest.mark.parametrize("G,tokens,variant", [(4, 1, "kv4_stream_f16_rows8"), (4, 3, "kv4_stream_f16_rows16"),
+                                              (4, 8, "kv4_stream_f16_rows32"), (4, 9, "kv4_tile_tcgen05")])
+def test_variant_by_rows(env, G, tokens, variant):
+    assert _run(env, np.random.default_rng(15), 128, 128, 16, 1, G, [(tokens, 70), (tokens, 200)], "f16") == variant
+
+
+def test_programmatic_launch_and_workspace_reuse(env):
+    """Append, attention and append again back to back, one workspace, each launched before the last has ended."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(16)
+    D, ps, Hk, G, B = 128, 16, 2, 4, 4
+    cos, sin = (torch.from_numpy(t).to(dev) for t in _tables(rng, 64, D))
+    start = torch.arange(B + 1, dtype=torch.int32, device=dev)
+    table = torch.arange(B * 4, dtype=torch.int32, device=dev).view(B, 4)
+    x = [torch.from_numpy(rng.standard_normal((B, (G + 2) * Hk, D)).astype(np.float16)).to(dev) for _ in range(30)]
+    results = []
+    for pdl in (False, True):
+        cache = mnb.mnb_kv4_cache_alloc(B * 4, ps, Hk, D, 64, dev)
+        ws = torch.empty(mnb.mnb_kv4_attention_workspace_bytes(B, B, G * Hk, Hk, D), dtype=torch.uint8, device=dev)
+        pos = [torch.full((B,), i, dtype=torch.int32, device=dev) for i in range(30)]
+        slots = [table[:, i // ps].long() * ps + i % ps for i in range(30)]
+        kv = [p + 1 for p in pos]
+        outs = [torch.empty((B, G * Hk, D), dtype=torch.float16, device=dev) for _ in range(30)]
+        torch.cuda.synchronize()
+        mnb.mnb_set_programmatic_launch(pdl)
+        try:
+            for i in range(30):
+                q = mnb.mnb_kv4_append(cache, x[i][:, G * Hk:(G + 1) * Hk], x[i][:, (G + 1) * Hk:], slots[i],
+                                       q=x[i][:, : G * Hk], positions=pos[i], cos=cos, sin=sin)
+                mnb.mnb_kv4_attention(q, cache, start, kv[i], table, 0.1, workspace=ws, out=outs[i])
+        finally:
+            mnb.mnb_set_programmatic_launch(False)
+        torch.cuda.synchronize()
+        results.append(outs + [cache.pages])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    mnb.mnb_check_device_status()
+
+
+def test_layer_example(env):
+    """The example's layer: 4-bit products, append, attention, from prompts to captured decode steps. Its check is
+    against fp32 torch rounded to fp16, so the fp16 norm bound holds."""
+    from examples import decode_layer
+    _, _, error = decode_layer.run(batch=3, prompt=90, steps=5, q_heads=8, kv_heads=2, head_dim=128, hidden=512, page_size=16)
+    assert error <= 2.0 ** -10
