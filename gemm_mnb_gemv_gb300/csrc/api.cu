@@ -662,7 +662,7 @@ mnb_status check_kv4(const char* fn, const mnb_kv4_cache& c, mnb::Kv4Cache* out)
                 c.group_size);
   mnb_status st = check_ptr(fn, "pages", c.pages);
   if (st != MNB_OK) return st;
-  *out = {c.pages, c.num_pages, c.page_size, c.kv_heads, c.head_dim, c.group_size};
+  *out = mnb::Kv4Cache(c.pages, c.num_pages, c.page_size, c.kv_heads, c.head_dim, c.group_size);
   return MNB_OK;
 }
 
@@ -688,7 +688,7 @@ extern "C" {
 
 size_t mnb_kv4_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim, int group_size) {
   if (!kv4_geometry_ok(num_pages, page_size, kv_heads, head_dim, group_size)) return 0;
-  const mnb::Kv4Cache c = {nullptr, num_pages, page_size, kv_heads, head_dim, group_size};
+  const mnb::Kv4Cache c(nullptr, num_pages, page_size, kv_heads, head_dim, group_size);
   return (size_t)num_pages * kv_heads * (page_size / 16) * c.block_bytes();
 }
 

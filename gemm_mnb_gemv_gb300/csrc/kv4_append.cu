@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
         int in_page;
         split_slot(slot_now, c.page_size, page, in_page);
         r = in_page % 16;
-        blk0 = c.pages + (page * c.kv_heads * (c.page_size / 16) + in_page / 16) * c.block_bytes();
+        blk0 = c.pages + page * c.kv_heads * c.head_bytes() + (in_page / 16) * c.block_bytes();
       }
     }
 #pragma unroll
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
                                   : __ushort_as_half(0x7fff);
       const float sf = __half2float(scale);
       const float of = finite ? __half2float(offset) : 0.0f;
-      const float inv = sf > 0.0f ? __fdiv_rn(1.0f, sf) : 0.0f;
+      const float inv = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
       // 1.5 2^23 + x has the integer nearest to x, ties to even, in its low bits; what lies above a code's
       // 4 bits is the same for every element and goes with one subtraction. fmaxf turns a NaN into 0.
       uint32_t word = 0;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv4_append_kernel(const Kv4Cac
         word = (word << 4) + __float_as_uint(__fadd_rn(f, 12582912.0f));
       }
       word -= 0x4B400000u * 0x11111111u;
-      uint8_t* blk = blk0 + (int64_t)h * (c.page_size / 16) * c.block_bytes();
+      uint8_t* blk = blk0 + h * c.head_bytes();
       if (is_k) {
         *reinterpret_cast<uint32_t*>(blk + kv4::k_word_byte<D>(r, sub % 4, sub / 4)) = word;
       } else {
@@ -322,13 +322,13 @@ __global__ void __launch_bounds__(kReadThreads) kv4_read_kernel(const Kv4Cache c
       int in_page;
       split_slot(slot, c.page_size, page, in_page);
       r[u] = in_page % 16;
-      at0[u] = (page * c.kv_heads * (c.page_size / 16) + in_page / 16) * c.block_bytes();
+      at0[u] = page * c.kv_heads * c.head_bytes() + (in_page / 16) * c.block_bytes();
     }
   }
   for (int h = blockIdx.y * per + threadIdx.x / kLanes; h < 2 * c.kv_heads; h += gridDim.y * per) {
     const bool is_k = h < c.kv_heads;
     const int kvh = is_k ? h : h - c.kv_heads;
-    const int64_t head = (int64_t)kvh * (c.page_size / 16) * c.block_bytes();
+    const int64_t head = kvh * c.head_bytes();
     uint32_t word[kU], par[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {

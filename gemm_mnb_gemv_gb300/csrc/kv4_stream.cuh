@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
   // Block numbers come in batches, lane i holding the i-th next; the page indices of the batch
   // after are on their way meanwhile.
   constexpr uint32_t kNone = 0xfffffffeu;  // nothing to read: past the end, or not in the cache
-  const int ppb = c.page_size / 16;
+  const int ppb = c.page_blocks;
   Cursor pro = cur;
   int64_t pro_left = u1 - u0 + skipped;  // units, those of pro's piece cost included
   int pro_stage = 0, issued = 0;         // issued: steps of the batch that are used up

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::setmaxnreg_dec<72>();
     if (warp == 0) {
       // ------------------------------ producer ------------------------------------
-      const int ppb = c.page_size / 16;
+      const int ppb = c.page_blocks;
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V values that are not finite: look for them again in the cache, 32 keys at a time
       uint32_t nan_groups = 0;
       if (odd_piece[piece % kMeta] == piece + 1) {
-        const int ppb = c.page_size / 16, end = min((cur.tile + here) * kKeys, cur.n);
+        const int ppb = c.page_blocks, end = min((cur.tile + here) * kKeys, cur.n);
         for (int k0 = cur.tile * kKeys; k0 < end; k0 += 32) {
           uint32_t bad = 0;
           if (k0 + lane < end) {

@@ -110,8 +110,15 @@ cudaError_t launch_generic_pair_swiglu(LaunchCtx& ctx, const void* A, const QWei
 struct Kv4Cache {
   uint8_t* pages;
   int num_pages, page_size, kv_heads, head_dim, group;
-  __host__ __device__ int ng() const { return head_dim / group; }
-  __host__ __device__ int block_bytes() const { return 16 * head_dim + 128 * ng(); }
+  // derived once on the host: kernels would divide for them
+  int groups, block_size, page_blocks;
+  Kv4Cache() = default;
+  Kv4Cache(uint8_t* pages_, int num_pages_, int page_size_, int kv_heads_, int head_dim_, int group_)
+      : pages(pages_), num_pages(num_pages_), page_size(page_size_), kv_heads(kv_heads_), head_dim(head_dim_), group(group_),
+        groups(head_dim_ / group_), block_size(16 * head_dim_ + 128 * (head_dim_ / group_)), page_blocks(page_size_ / 16) {}
+  __host__ __device__ int ng() const { return groups; }
+  __host__ __device__ int block_bytes() const { return block_size; }
+  __host__ __device__ int64_t head_bytes() const { return (int64_t)page_blocks * block_size; }  // of a page's key head
 };
 struct Kv4Append {
   const void *q, *k, *v;
