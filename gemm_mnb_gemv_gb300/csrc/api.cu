@@ -799,6 +799,7 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
   if (need > 0 && (st = check_ptr(fn, "workspace", workspace)) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  if (window >= 1 << 30) window = 0;  // no position reaches 2^30: such a window leaves nothing out
   const mnb::Kv4Attention a = {q,     dtype == MNB_F32, T,           q_heads, q_stride,  q_start,  kv_len, page_table, batch,
                                table_stride, scale, causal != 0, window, workspace, ws_bytes, out,   lse};
   return finish(fn, mnb::launch_kv4_attention(ctx, c, a), ctx);

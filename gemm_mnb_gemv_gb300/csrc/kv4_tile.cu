@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t raw_full[4], raw_empty[4], kv_full[kBufs], kv_empty[kBufs], q_full[2], s_full[2], p_full[2][2], o_full;
   __shared__ int64_t scan[10];
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag;
   __shared__ int raw_have[4];                 // blocks of a raw tile that were read
   __shared__ uint32_t tile_info[kMeta];       // for the softmax: bits 0-7 blocks read, 8-15 and 16-23 powers of K and V + 64
   __shared__ int odd_piece[kMeta];            // 1 + the last piece (modulo kMeta) with a V value that is not finite
@@ -127,7 +126,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* raw_ring = smem + L::kQ + kBufs * L::kOperand;
 
   if (tid == 0) {
-    abort_flag = 0;
     for (int i = 0; i < kMeta; ++i) odd_piece[i] = 0;
     for (int i = 0; i < 4; ++i) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < kBufs; ++i) mbar_init(&kv_full[i], 4), mbar_init(&kv_empty[i], 1);
@@ -166,10 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     walk.next_part(cur);
     return true;
   };
-  auto give_up = [&](uint32_t what) {
-    report_status(status, what);
-    atomicExch(&abort_flag, 1);
-  };
+  // a role whose wait gave up says so and stops; the others run into their own limits, and rows get NaN
+  auto give_up = [&](uint32_t what) { report_status(status, what); };
 
   const int wg = warp >> 2;
   if (wg == 0) {

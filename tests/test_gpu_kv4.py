@@ -333,6 +333,15 @@ def test_bad_pages_and_lengths(env):
     mnb.mnb_check_device_status()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1])
+def test_a_window_beyond_every_key(env, window, dtype):
+    """It leaves nothing out, for tokens at negative positions (more tokens than keys) either."""
+    lens = [(5, 3), (1, 40), (60, 20)]
+    for causal in (False, True):
+        _run(env, np.random.default_rng(17), 64, 64, 16, 1, 2, lens, dtype, causal=causal, window=window)
+
+
 def test_query_ranges_are_clamped(env):
     """q_start that runs past T or backwards reads and writes nothing outside q and out."""
     mnb, torch, dev = env
