@@ -485,6 +485,7 @@ class MnbKv4Cache:
             raise ValueError(f"pages has records of {record} bytes, {need // (num_pages * kv_heads)} needed")
         self.pages, self.page_size, self.head_dim, self.group_size = pages, page_size, head_dim, group_size
         self.num_pages, self.kv_heads = num_pages, kv_heads
+        self.workspace_bytes = {}  # by (tokens, batch, q_heads, dtype)
         self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
 
 
@@ -628,7 +629,11 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     B = kv_len.shape[0]
     lib = load_library()
     if workspace is None:
-        need = lib.mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
+        need = cache.workspace_bytes.get((T, B, Hq, dt))
+        if need is None:
+            need = lib.mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
+            if len(cache.workspace_bytes) < 4096:
+                cache.workspace_bytes[(T, B, Hq, dt)] = need
         workspace = _new(need, torch.uint8, q.device, stream) if need else None
     else:
         _check_dev("workspace", workspace)

@@ -34,7 +34,7 @@ namespace mnb {
 namespace kv4 {
 
 constexpr int kWarps = 4;      // warps of a CTA
-constexpr int kPieceCost = 4;  // 2: 85.9 us for 64 ragged contexts, 1: 97.0, 4: 81.6
+constexpr int kPieceCost = 3;  // 64 ragged contexts: 1: 83.5 us, 2: 78.6, 3: 77.3, 4: 78.0, 6: 80.7, 8: 84.0
 
 // 8 x 8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {

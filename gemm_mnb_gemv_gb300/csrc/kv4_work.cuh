@@ -202,42 +202,54 @@ __device__ __forceinline__ bool find_range(const Walk<RT, kTile, kPieceCost>& wa
 // block lists the cut sequences from the CTAs' entries; teams of warps take their rows in turn, each warp its share of
 // the pieces, several of them in flight. With few rows a team is four warps (many pieces each), with more rows than such
 // teams it is one.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 16, kRounds = (kMaxCtas + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const Kv4Cache c, const Kv4Attention a, int ctas) {
   constexpr int RT = 8 * NT, kSlot = RT * (D + 2), E = D / 32, kFlight = NT > 4 ? 4 : D > 128 ? 5 : 10;
   __shared__ float part[kJoinWarps][D + 4];  // o, then l and m
-  __shared__ int list[kMaxCtas];
-  __shared__ int count[kJoinWarps + 1];
+  __shared__ Piece list[kMaxCtas];
+  __shared__ int list_last[kMaxCtas];  // the CTA that wrote the entry
+  __shared__ int count[kRounds][kJoinWarps];
   pdl_wait();
   const Piece* pieces = reinterpret_cast<const Piece*>(a.workspace);
   const float* slots = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.workspace) + kMaxCtas * sizeof(Piece));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int n_list = 0;
-  for (int i0 = 0; i0 < ctas; i0 += kJoinWarps * 32) {
-    const int i = i0 + threadIdx.x;
-    const bool has = i < ctas && pieces[i].first >= 0;
-    const uint32_t vote = __ballot_sync(kFull, has);
-    if (lane == 0) count[warp] = __popc(vote);
-    __syncthreads();
-    int at = n_list, all = 0;
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (w < warp) at += count[w];
-      all += count[w];
-    }
-    if (has) list[at + __popc(vote & ((1u << lane) - 1))] = i;
-    n_list += all;
-    __syncthreads();
+  Piece own[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int i = k * kJoinWarps * 32 + threadIdx.x;
+    own[k].first = -1;
+    if (i < ctas) own[k] = pieces[i];
   }
+  uint32_t vote[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    vote[k] = __ballot_sync(kFull, own[k].first >= 0);
+    if (lane == 0) count[k][warp] = __popc(vote[k]);
+  }
+  __syncthreads();
+  int n_list = 0;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    int at = n_list;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) at += count[k][w];
+      n_list += count[k][w];
+    }
+    at += __popc(vote[k] & ((1u << lane) - 1));
+    if (own[k].first >= 0) list[at] = own[k], list_last[at] = k * kJoinWarps * 32 + threadIdx.x;
+  }
+  __syncthreads();
   const int G = a.q_heads / c.kv_heads;
   const int items = n_list * RT;
   const int team = items > (int)gridDim.x * (kJoinWarps / 4) ? 1 : 4;
   const int teams = kJoinWarps / team, sub = warp % team;
   for (int item0 = blockIdx.x * teams; item0 < items; item0 += gridDim.x * teams) {
     const int item = item0 + warp / team;
-    const int last = item < items ? list[item / RT] : 0, col = item % RT;
+    const int col = item % RT;
+    int last = 0;
     Piece p = {};
-    if (item < items) p = pieces[last];
+    if (item < items) p = list[item / RT], last = list_last[item / RT];
     const bool live = item < items && p.row0 + col < p.rows;
     const int n = live ? last - p.first + 1 : 0;
     float m = -FLT_MAX, l = 0.0f, acc[E] = {};
