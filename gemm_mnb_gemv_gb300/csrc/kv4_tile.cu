@@ -465,20 +465,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         // whole rows of q by neighbouring lanes: a lane that reads its own row takes a line for every 16 bytes
         const int64_t own = (int64_t)(cur.q0 + tok) * a.q_stride + ((int64_t)cur.kvh * G + head) * D;
-        constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;  // 16-byte chunks of a row, rows an instruction
+        constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks, kLoads = 32 / kAtOnce;  // 16-byte chunks of a row, rows an instruction
         const int ch = lane % kChunks;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32; i0 += 8 * kAtOnce) {
-          uint4 v[8];
+        for (int i0 = 0; i0 < 32; i0 += kLoads * kAtOnce) {
+          uint4 v[kLoads];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kLoads; ++i) {
             const int from = i0 + i * kAtOnce + lane / kChunks;
             const int64_t at = __shfl_sync(kFull, own, from);
             const bool there = __shfl_sync(kFull, (int)live, from) != 0;
             v[i] = there ? *reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at + ch * 8) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kLoads; ++i) {
             const int to = wrow + i0 + i * kAtOnce + lane / kChunks;
             uint32_t p[4];
             pair_halves_stride4(v[i], p);
