@@ -486,6 +486,7 @@ class MnbKv4Cache:
         self.pages, self.page_size, self.head_dim, self.group_size = pages, page_size, head_dim, group_size
         self.num_pages, self.kv_heads = num_pages, kv_heads
         self.workspace_bytes = {}  # by (tokens, batch, q_heads, dtype)
+        self.workspace = None      # of the attention calls on the default stream
         self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
 
 
@@ -619,6 +620,8 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     """``[T, q_heads, head_dim]``: attention of ``q`` over the cached keys of ``batch`` sequences.
 
     ``q_start`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]``, ``page_table`` int32 ``[batch, pages]``.
+    Without ``workspace``, calls on the default stream share one that the cache keeps (the largest asked for so far), and
+    calls on other streams allocate theirs.
     """
     torch = _torch()
     if q.dim() != 3:
@@ -628,13 +631,20 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     qs = _token_rows("q", q, Hq, cache.head_dim, dtype)
     B = kv_len.shape[0]
     lib = load_library()
+    raw_stream = _raw_stream(q, stream)
     if workspace is None:
         need = cache.workspace_bytes.get((T, B, Hq, dt))
         if need is None:
             need = lib.mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
             if len(cache.workspace_bytes) < 4096:
                 cache.workspace_bytes[(T, B, Hq, dt)] = need
-        workspace = _new(need, torch.uint8, q.device, stream) if need else None
+        workspace = cache.workspace
+        if stream is not None or raw_stream != 0:
+            workspace = _new(need, torch.uint8, q.device, stream)
+        elif workspace is None or workspace.numel() < need:
+            # The default stream is never destroyed, orders all its calls and can't be captured, so one workspace serves
+            # them in turn: 16 us a call of one token over 1000 keys against 20 us with one allocated in each.
+            workspace = cache.workspace = _new(need, torch.uint8, q.device, None)
     else:
         _check_dev("workspace", workspace)
     if out is None:
@@ -649,8 +659,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     st = lib.mnb_kv4_attention(
         q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
         _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
-        stride, scale, 1 if causal else 0, window, None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.nbytes, op, lp, _raw_stream(q, stream))
+        stride, scale, 1 if causal else 0, window, workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
     if st != MNB_OK:
         _raise(st)
     return out

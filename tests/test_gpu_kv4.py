@@ -395,6 +395,42 @@ def test_strided_q_other_stream_and_graph(env):
     mnb.mnb_check_device_status()
 
 
+def test_kept_workspaces(env):
+    """Calls without a workspace: the default stream's is kept and grows, others allocate theirs; shapes in turn, three
+    streams at once and a captured call beside eager ones give what calls with a workspace of their own give."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(18)
+    D, ps, Hk, G = 128, 16, 1, 4
+    _, cache = _cache(env, rng, D, 128, ps, Hk, 130)
+    table = torch.arange(120, dtype=torch.int32, device=dev).view(2, 60)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    calls = []
+    for n in (1, 3, 8, 90):
+        q = torch.from_numpy(rng.standard_normal((2 * n, Hk * G, D)).astype(np.float16)).to(dev)
+        args = (q, cache, i32(0, n, 2 * n), i32(900, 333), table, 0.09)
+        ws = torch.empty(mnb.mnb_kv4_attention_workspace_bytes(2 * n, 2, Hk * G, Hk, D), dtype=torch.uint8, device=dev)
+        calls.append((args, mnb.mnb_kv4_attention(*args, workspace=ws)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = mnb.mnb_kv4_attention(*calls[1][0])
+    assert cache.workspace is None
+    streams = [torch.cuda.default_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for turn in range(10):
+        outs = []
+        with torch.cuda.stream(streams[1]):
+            graph.replay()
+        for s in streams:
+            with torch.cuda.stream(s):
+                for k in range(4):
+                    outs.append((k, mnb.mnb_kv4_attention(*calls[(k + turn) % 4][0]), turn))
+        torch.cuda.synchronize()
+        for k, o, t in outs:
+            assert torch.equal(o, calls[(k + t) % 4][1])
+        assert torch.equal(captured, calls[1][1])
+    assert cache.workspace is not None
+
+
 def test_offsets_beyond_32_bits(env):
     """A cache of more than 4 GiB: append, read and attention in its last pages."""
     mnb, torch, dev = env
