@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmnb.so")
@@ -487,6 +488,7 @@ class MnbKv4Cache:
         self.num_pages, self.kv_heads = num_pages, kv_heads
         self.workspace_bytes = {}  # by (tokens, batch, q_heads, dtype)
         self.workspace = None      # of the attention calls on the default stream
+        self.workspace_lock = threading.Lock()  # between two threads' launches that use it
         self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
 
 
@@ -632,19 +634,21 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     B = kv_len.shape[0]
     lib = load_library()
     raw_stream = _raw_stream(q, stream)
+    kept = workspace is None and stream is None and raw_stream == 0
     if workspace is None:
         need = cache.workspace_bytes.get((T, B, Hq, dt))
         if need is None:
             need = lib.mnb_kv4_attention_workspace_bytes(T, B, Hq, cache.kv_heads, D, dt)
             if len(cache.workspace_bytes) < 4096:
                 cache.workspace_bytes[(T, B, Hq, dt)] = need
-        workspace = cache.workspace
-        if stream is not None or raw_stream != 0:
-            workspace = _new(need, torch.uint8, q.device, stream)
-        elif workspace is None or workspace.numel() < need:
+        if kept:
             # The default stream is never destroyed, orders all its calls and can't be captured, so one workspace serves
-            # them in turn: 16 us a call of one token over 1000 keys against 20 us with one allocated in each.
-            workspace = cache.workspace = _new(need, torch.uint8, q.device, None)
+            # them in turn: 15 us a call of one token over 1000 keys against 20 us with one allocated in each.
+            workspace = cache.workspace
+            if workspace is None or workspace.numel() < need:
+                workspace = cache.workspace = _new(need, torch.uint8, q.device, None)
+        else:
+            workspace = _new(need, torch.uint8, q.device, stream)
     else:
         _check_dev("workspace", workspace)
     if out is None:
@@ -656,10 +660,15 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [{B}, pages], got {list(page_table.shape)}")
     stride = page_table.shape[1]
-    st = lib.mnb_kv4_attention(
-        q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
-        _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
-        stride, scale, 1 if causal else 0, window, workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
+    args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
+            _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
+            stride, scale, 1 if causal else 0, window, workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
+    if kept:
+        # A call is two launches, and its workspace is theirs from the first to the second.
+        with cache.workspace_lock:
+            st = lib.mnb_kv4_attention(*args)
+    else:
+        st = lib.mnb_kv4_attention(*args)
     if st != MNB_OK:
         _raise(st)
     return out

@@ -9,6 +9,8 @@ As a norm, independent roundings add up as squares: at most 2 u of the result (f
 """
 from __future__ import annotations
 
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 
@@ -429,6 +431,14 @@ def test_kept_workspaces(env):
             assert torch.equal(o, calls[(k + t) % 4][1])
         assert torch.equal(captured, calls[1][1])
     assert cache.workspace is not None
+
+    def thread(k):
+        for _ in range(300):
+            out = mnb.mnb_kv4_attention(*calls[k][0])
+        return torch.equal(out, calls[k][1])
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(thread, range(4)))
 
 
 def test_offsets_beyond_32_bits(env):
