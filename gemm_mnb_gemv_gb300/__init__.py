@@ -643,7 +643,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
                 cache.workspace_bytes[(T, B, Hq, dt)] = need
         if kept:
             # The default stream is never destroyed, orders all its calls and can't be captured, so one workspace serves
-            # them in turn: 15 us a call of one token over 1000 keys against 20 us with one allocated in each.
+            # them in turn: 16 us a call of one token over 1000 keys against 20 us with one allocated in each.
             workspace = cache.workspace
             if workspace is None or workspace.numel() < need:
                 workspace = cache.workspace = _new(need, torch.uint8, q.device, None)

@@ -8,7 +8,8 @@
 // partners by a second load that hits L1, extrema by shuffles over a group's 4-16 lanes. The
 // passes' loads are all issued before the token's position is waited for.
 // Bound: HBM bytes of q, k, v, q_out, and close behind them the instructions of the conversion (the
-// first form, one pass shape for q, k and v, took twice the time at the same bytes).
+// first form, one pass shape for q, k and v, took 177 us for appending and reading 16381 tokens of 32 / 8 heads of
+// 128, this one 130 us; the bytes alone would be 66 us). Append alone is 104 us at 3.1 TB/s, 4490 warp instructions a token.
 #include <type_traits>
 
 #include "kv4.cuh"

@@ -546,7 +546,7 @@ def test_more_sequences_than_threads_look_at(env):
 
 
 @pytest.mark.parametrize("G,tokens,variant", [(4, 1, "kv4_stream_f16_rows8"), (4, 3, "kv4_stream_f16_rows16"),
-                                              (4, 8, "kv4_stream_f16_rows32"), (4, 9, "kv4_tile_tcgen05")])
+                                              (4, 12, "kv4_stream_f16_rows16"), (4, 13, "kv4_tile_tcgen05")])
 def test_variant_by_rows(env, G, tokens, variant):
     assert _run(env, np.random.default_rng(15), 128, 128, 16, 1, G, [(tokens, 70), (tokens, 200)], "f16") == variant
 
