@@ -487,8 +487,6 @@ class MnbKv4Cache:
         self.pages, self.page_size, self.head_dim, self.group_size = pages, page_size, head_dim, group_size
         self.num_pages, self.kv_heads = num_pages, kv_heads
         self.workspace_bytes = {}  # by (tokens, batch, q_heads, dtype)
-        self.workspace = None      # of the attention calls on the default stream
-        self.workspace_lock = threading.Lock()  # between two threads' launches that use it
         self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
 
 
@@ -617,13 +615,17 @@ def mnb_kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads
     return int(load_library().mnb_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, dtype))
 
 
+_default_workspace = {}  # by device: of mnb_kv4_attention's calls on its default stream, 43 MB at most
+_default_workspace_lock = threading.Lock()
+
+
 def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale: float, causal: bool = True,
                       window: int = 0, workspace=None, out=None, lse=None, stream=None):
     """``[T, q_heads, head_dim]``: attention of ``q`` over the cached keys of ``batch`` sequences.
 
     ``q_start`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]``, ``page_table`` int32 ``[batch, pages]``.
-    Without ``workspace``, calls on the default stream share one that the cache keeps (the largest asked for so far), and
-    calls on other streams allocate theirs.
+    Without ``workspace``, calls on the device's default stream share one that is kept (the largest asked for so far, 43 MB
+    at most), and calls on other streams allocate theirs.
     """
     torch = _torch()
     if q.dim() != 3:
@@ -644,9 +646,9 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
         if kept:
             # The default stream is never destroyed, orders all its calls and can't be captured, so one workspace serves
             # them in turn: 16 us a call of one token over 1000 keys against 20 us with one allocated in each.
-            workspace = cache.workspace
+            workspace = _default_workspace.get(q.get_device())
             if workspace is None or workspace.numel() < need:
-                workspace = cache.workspace = _new(need, torch.uint8, q.device, None)
+                workspace = _default_workspace[q.get_device()] = _new(need, torch.uint8, q.device, None)
         else:
             workspace = _new(need, torch.uint8, q.device, stream)
     else:
@@ -665,7 +667,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
             stride, scale, 1 if causal else 0, window, workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
     if kept:
         # A call is two launches, and its workspace is theirs from the first to the second.
-        with cache.workspace_lock:
+        with _default_workspace_lock:
             st = lib.mnb_kv4_attention(*args)
     else:
         st = lib.mnb_kv4_attention(*args)

@@ -411,11 +411,11 @@ def test_kept_workspaces(env):
         q = torch.from_numpy(rng.standard_normal((2 * n, Hk * G, D)).astype(np.float16)).to(dev)
         args = (q, cache, i32(0, n, 2 * n), i32(900, 333), table, 0.09)
         ws = torch.empty(mnb.mnb_kv4_attention_workspace_bytes(2 * n, 2, Hk * G, Hk, D), dtype=torch.uint8, device=dev)
-        calls.append((args, mnb.mnb_kv4_attention(*args, workspace=ws)))
+        calls.append((args, mnb.mnb_kv4_attention(*args, workspace=ws), ws.numel()))
+    mnb._default_workspace.clear()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         captured = mnb.mnb_kv4_attention(*calls[1][0])
-    assert cache.workspace is None
     streams = [torch.cuda.default_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     for turn in range(10):
@@ -430,7 +430,7 @@ def test_kept_workspaces(env):
         for k, o, t in outs:
             assert torch.equal(o, calls[(k + t) % 4][1])
         assert torch.equal(captured, calls[1][1])
-    assert cache.workspace is not None
+    assert mnb._default_workspace[0].numel() >= calls[3][2]
 
     def thread(k):
         for _ in range(300):
