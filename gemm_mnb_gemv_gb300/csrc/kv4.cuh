@@ -1,7 +1,6 @@
 // Addressing inside a paged 4-bit key/value cache (layout: mnb.h, "Paged 4-bit key/value cache").
 #pragma once
 
-#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace mnb {
@@ -26,6 +25,14 @@ __host__ __device__ constexpr int v_place(int r, int g) {
 template <int D>
 __host__ __device__ constexpr int v_word_byte(int g, int r, int w) {
   return (g * 16 + v_place<D>(r, g)) * (D / 16) + w * 4;
+}
+
+// Byte of 16-byte chunk `chunk` of row `row` (of 128) in the tcgen05 kernel's shared memory of one row tile: 64 fp16
+// elements of a row are 128 bytes, swizzled, and the next 64 follow after those of all rows. q lies so, and
+// results pass through the same places on their way out: a row's bytes belong to its own warp from the
+// start of a piece to its end, so the warps need no barrier between one piece's results and the next one's q.
+__host__ __device__ constexpr int tile_row_byte(int row, int chunk) {
+  return (chunk >> 3) * (128 * 128) + row * 128 + ((chunk ^ row) & 7) * 16;
 }
 
 }  // namespace kv4

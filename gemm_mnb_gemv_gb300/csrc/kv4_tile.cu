@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int to = wrow + i0 + i * kAtOnce + lane / kChunks;
             uint32_t p[4];
             pair_halves_stride4(v[i], p);
-            sts128(q_at + x * (L::kQ / 2) + (ch >> 3) * (128 * 128) + to * 128 + (((ch ^ to) & 7) << 4),
+            sts128(q_at + x * (L::kQ / 2) + tile_row_byte(to, ch),
                    make_uint4(p[0] ^ flip, p[1] ^ flip, p[2] ^ flip, p[3] ^ flip));
           }
         }
@@ -640,10 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = (whole ? (none ? 0.0f : 1.0f / l) : 1.0f) * pow2(-v_power);
       float* slot = slots + ((int64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kSlot;
       const int64_t out_row = (int64_t)(cur.q0 + tok) * a.q_heads + (int64_t)cur.kvh * G + head;
-      // 64 elements of 32 rows at a time through this warp's part of q's room (nothing reads q any more), so that
-      // neighbouring lanes store whole lines
-      uint8_t* room = smem + x * (L::kQ / 2) + wrow * (L::kQ / 256);
-      constexpr int kRoom = 32 * (L::kQ / 256);
+      // 64 elements of 32 rows at a time through the bytes of these rows' own q (the products have read it, and only this
+      // warp writes it), so that neighbouring lanes store whole lines
+      uint8_t* room = smem + x * (L::kQ / 2);
+      constexpr bool kCutRoom = D == 128;  // 64 elements of a row in fp32 fit
 #pragma unroll 1
       for (int w = 0; w < VW; ++w) {
         // columns 64 w + 8 g + i hold element 64 w + 32 (i & 1) + 4 g + i / 2
@@ -668,12 +668,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 2 * (k % 4) + h];
               const int d8 = 4 * h + 2 * half + g2 / 2;  // eight elements
               if (whole) {
-                *reinterpret_cast<uint4*>(room + lane * 128 + ((d8 ^ lane) & 7) * 16) = make_uint4(
+                *reinterpret_cast<uint4*>(room + tile_row_byte(wrow + lane, d8)) = make_uint4(
                     pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
-              } else if (kRoom >= 8192) {
-                float4* s4 = reinterpret_cast<float4*>(room + lane * 256);
-                s4[(2 * d8) ^ (lane & 15)] = make_float4(y[0], y[1], y[2], y[3]);
-                s4[(2 * d8 + 1) ^ (lane & 15)] = make_float4(y[4], y[5], y[6], y[7]);
+              } else if (kCutRoom) {
+                *reinterpret_cast<float4*>(room + tile_row_byte(wrow + lane, 2 * d8)) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(room + tile_row_byte(wrow + lane, 2 * d8 + 1)) =
+                    make_float4(y[4], y[5], y[6], y[7]);
               } else if (live) {
                 float4* s4 = reinterpret_cast<float4*>(slot + (x * 128 + r) * D + 64 * w + 8 * d8);
                 s4[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -689,15 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int from = 4 * i + lane / 8, ch = lane % 8;
             const int64_t to = __shfl_sync(kFull, out_row, from);
             const bool there = __shfl_sync(kFull, (int)live, from) != 0;
-            const uint4 y = *reinterpret_cast<const uint4*>(room + from * 128 + ((ch ^ from) & 7) * 16);
+            const uint4 y = *reinterpret_cast<const uint4*>(room + tile_row_byte(wrow + from, ch));
             if (there) *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + to * D + 64 * w + 8 * ch) = y;
           }
-        } else if (kRoom >= 8192) {
+        } else if (kCutRoom) {
 #pragma unroll 4
           for (int i = 0; i < 16; ++i) {
             const int from = 2 * i + lane / 16, ch = lane % 16;
             const bool there = __shfl_sync(kFull, (int)live, from) != 0;
-            const float4 y = *reinterpret_cast<const float4*>(room + from * 256 + (ch ^ (from & 15)) * 16);
+            const float4 y = *reinterpret_cast<const float4*>(room + tile_row_byte(wrow + from, ch));
             if (there) *reinterpret_cast<float4*>(slot + (x * 128 + wrow + from) * D + 64 * w + 4 * ch) = y;
           }
         }

@@ -1,0 +1,163 @@
+"""Attention over the paged 4-bit cache where a CTA takes many key tiles and several pieces of work.
+
+The kernels cut all key tiles of a call into one range for each CTA, so short calls give a CTA one tile. Here the
+shares are worked out first and each test asserts that its shape reaches the loops: later tiles of a piece,
+reuse of every ring, the change from one piece to the next. Results are compared with fp64 on the GPU, from the values
+that the cache holds (which the append and read tests compare bit for bit), within the tolerances of
+``test_gpu_kv4``, and with a second run bit for bit.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv4 import _check, env  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+STREAM_CTAS = 4  # an SM, at most
+
+
+def _shares(lens, Hk, G, rows, keys, cost, ctas, causal=True, window=0):
+    """Key tiles of each piece of each CTA: [[tiles, ..], ..]; `rows` and `keys` of a tile, `cost` of a piece in tiles."""
+    pieces = []
+    for q_len, n in lens:
+        for rt in range(-(-q_len * G // rows)):
+            first, last = rt * rows // G, min(q_len - 1, (rt * rows + rows - 1) // G)
+            hi = min(n, n - q_len + last + 1) if causal else n
+            lo = max(0, n - q_len + first - window + 1) if window else 0
+            t0 = lo // keys
+            pieces += [max(t0 + 1, -(-max(hi, 0) // keys)) - t0] * Hk
+    total = sum(p + cost for p in pieces)
+    ctas = min(ctas, total)
+    out, at, used = [], 0, 0  # piece, units of it that are taken
+    for i in range(ctas):
+        left = total // ctas + (1 if i < total % ctas else 0)
+        own = []
+        while left:
+            take = min(left, pieces[at] + cost - used)
+            tiles = max(0, used + take - cost) - max(0, used - cost)
+            if tiles:
+                own.append(tiles)
+            left -= take
+            used += take
+            if used == pieces[at] + cost:
+                at, used = at + 1, 0
+        out.append(own)
+    return out
+
+
+def _reaches(shares, tiles, pieces):
+    """Most CTAs have `tiles` key tiles in all, and many at least `pieces` pieces."""
+    assert np.median([sum(s) for s in shares]) >= tiles, np.median([sum(s) for s in shares])
+    assert np.mean([len(s) >= pieces for s in shares]) >= 0.3, np.mean([len(s) >= pieces for s in shares])
+    assert max(max(s, default=0) for s in shares) >= 3
+
+
+class Filled:
+    """A cache with `lens` sequences of random keys and values, pages in random order, times ksize(j) and vsize(j)."""
+
+    def __init__(self, env, seed, D, group, ps, Hk, lens, ksize=None, vsize=None):
+        mnb, torch, dev = env
+        self.env, self.D, self.Hk, self.lens = env, D, Hk, lens
+        gen = torch.Generator(device=dev)
+        gen.manual_seed(seed)
+        need = [-(-n // ps) for _, n in lens]
+        self.cache = mnb.mnb_kv4_cache_alloc(sum(need) + 2, ps, Hk, D, group, dev)
+        order = torch.randperm(sum(need) + 2, generator=gen, device=dev)
+        table = torch.zeros((len(lens), max(need)), dtype=torch.int64, device=dev)
+        self.slots, at = [], 0
+        for b, (_, n) in enumerate(lens):
+            table[b, : need[b]] = order[at: at + need[b]]
+            at += need[b]
+            j = torch.arange(n, device=dev)
+            self.slots.append(table[b, j // ps] * ps + j % ps)
+            kv = [torch.randn((n, Hk, D), generator=gen, device=dev) for _ in range(2)]
+            for x, size in zip(kv, (ksize, vsize)):
+                if size is not None:
+                    x *= size(j.float())[:, None, None]
+            kv = [x.float() for x in kv]
+            if n:
+                mnb.mnb_kv4_append(self.cache, kv[0], kv[1], self.slots[b])
+        self.table = table.int()
+        self.kv_len = torch.tensor([n for _, n in lens], dtype=torch.int32, device=dev)
+        self.start = torch.tensor(np.cumsum([0] + [a for a, _ in lens]), dtype=torch.int32, device=dev)
+        self.gen = gen
+
+    def queries(self, G, dtype, size=1.0):
+        _, torch, dev = self.env
+        T = sum(a for a, _ in self.lens)
+        q = torch.randn((T, self.Hk * G, self.D), generator=self.gen, device=dev) * size
+        return q.to(torch.float16 if dtype == "f16" else torch.float32)
+
+    def attend(self, q, scale, causal=True, window=0, lse=None):
+        return self.env[0].mnb_kv4_attention(q, self.cache, self.start, self.kv_len, self.table, scale, causal=causal,
+                                             window=window, lse=lse)
+
+    def want(self, q, scale, causal=True, window=0):
+        """As the oracle's `attention`: out, lse, sum_j p_j |v_j|, largest scale * sum_d |q_d k_jd|, fp64."""
+        mnb, torch, dev = self.env
+        T, Hq, D = q.shape
+        G = Hq // self.Hk
+        f64 = torch.float64
+        out, mag = torch.zeros((T, Hq, D), dtype=f64, device=dev), torch.zeros((T, Hq, D), dtype=f64, device=dev)
+        lse = torch.full((T, Hq), float("-inf"), dtype=f64, device=dev)
+        reach = torch.zeros((T, Hq), dtype=f64, device=dev)
+        for b, (q_len, n) in enumerate(self.lens):
+            if not q_len or not n:
+                continue
+            a = int(self.start[b])
+            K, V = (x.double() for x in mnb.mnb_kv4_read(self.cache, self.slots[b], dtype=torch.float32))
+            j, pos = torch.arange(n, device=dev), n - q_len + torch.arange(q_len, device=dev)
+            hide = torch.zeros((q_len, n), dtype=torch.bool, device=dev)
+            if causal:
+                hide |= j[None] > pos[:, None]
+            if window:
+                hide |= j[None] <= pos[:, None] - window
+            for h in range(Hq):
+                x, k, v = q[a: a + q_len, h].double(), K[:, h // G], V[:, h // G]
+                s = (x @ k.T * scale).masked_fill(hide, float("-inf"))
+                l = s.logsumexp(-1)
+                p = torch.exp(s - torch.where(torch.isinf(l), torch.zeros_like(l), l)[:, None])
+                out[a: a + q_len, h], mag[a: a + q_len, h] = p @ v, p @ v.abs()
+                lse[a: a + q_len, h] = l
+                reach[a: a + q_len, h] = (x.abs() @ k.abs().T * abs(scale)).masked_fill(hide, 0.0).amax(-1)
+        return tuple(t.cpu().numpy() for t in (out, lse, mag, reach))
+
+    def check(self, q, dtype, scale, causal=True, window=0):
+        mnb, torch, dev = self.env
+        lse = torch.full(q.shape[:2], 7.0, device=dev)
+        scale = float(np.float32(scale))
+        out = self.attend(q, scale, causal, window, lse)
+        variant = mnb.mnb_last_variant()
+        for _ in range(3):
+            assert torch.equal(out, self.attend(q, scale, causal, window)), variant
+        mnb.mnb_check_device_status()
+        _check(out, lse, self.want(q, scale, causal, window), dtype, variant)
+        return out, variant
+
+
+def _sms(env):
+    return env[1].cuda.get_device_properties(0).multi_processor_count
+
+
+PROMPTS = [(700, 3000), (900, 3000)]
+DRAFTS = [(16 - i % 5, 500 + 137 * i) for i in range(24)]
+
+
+@pytest.mark.parametrize("D,group,ps,Hk,G,lens,causal,window", [
+    (128, 128, 16, 8, 4, PROMPTS, True, 0),
+    (128, 32, 64, 8, 4, PROMPTS, True, 700),
+    (128, 64, 16, 4, 7, [(511, 511), (700, 1900), (40, 2500), (900, 901)], True, 0),
+    (128, 128, 32, 8, 4, [(300, 1500), (420, 900), (256, 2000)], False, 0),
+    (64, 64, 16, 8, 4, PROMPTS, True, 0),
+    (64, 32, 128, 6, 5, [(650, 2222), (800, 3100)], True, 0),
+    (128, 64, 16, 8, 4, DRAFTS, True, 0),
+])
+def test_prompts_of_several_pieces(env, D, group, ps, Hk, G, lens, causal, window):  # noqa: F811
+    """tcgen05 kernel: a row tile's four warps leave a piece and enter the next one each in its own time."""
+    shares = _shares(lens, Hk, G, 256, 128, 3, min(160, _sms(env)), causal, window)
+    _reaches(shares, 8, 2)
+    f = Filled(env, D + G, D, group, ps, Hk, lens)
+    _, variant = f.check(f.queries(G, "f16"), "f16", D ** -0.5, causal, window)
+    assert variant == "kv4_tile_tcgen05"

@@ -186,3 +186,30 @@ def test_read_refusals(lib, change, expect, word):
     a.update(change)
     st = lib.mnb_kv4_read(_cache(mnb), P(a["slots"]), a["T"], a["dtype"], P(a["k"]), P(a["v"]), None)
     assert st == expect and word in mnb.mnb_last_error()
+
+
+def test_rows_of_the_tcgen05_kernel_own_their_bytes(tmp_path):
+    """A row's chunks lie in bytes of that row alone: q and the results that pass through the same places belong to the
+    warp of the row, whichever piece of work each warp is at."""
+    import os
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "places.cpp"
+    src.write_text('#define __host__\n#define __device__\n#include "kv4.cuh"\n#include <cstdio>\nint main() {\n'
+                   '  for (int r = 0; r < 128; ++r)\n    for (int c = 0; c < 16; ++c)\n'
+                   '      std::printf("%d\\n", mnb::kv4::tile_row_byte(r, c));\n}\n')
+    exe = tmp_path / "places"
+    subprocess.run([gxx, "-std=c++17", "-I", os.path.join(root, "gemm_mnb_gemv_gb300", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    at = np.array(subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split(), int).reshape(128, 16)
+    assert sorted(at.reshape(-1)) == list(range(0, 128 * 256, 16))
+    np.testing.assert_array_equal(at % 16384 // 128, np.repeat(np.arange(128)[:, None], 16, 1))
+    np.testing.assert_array_equal(at // 16384, np.repeat(np.arange(16)[None] // 8, 128, 0))
+    # the kernel keeps q and stages its results through these places alone
+    kernel = open(os.path.join(root, "gemm_mnb_gemv_gb300", "csrc", "kv4_tile.cu")).read()
+    used = [line for line in kernel.splitlines() if "room +" in line]
+    assert used and all("room + tile_row_byte(" in line for line in used)
