@@ -43,6 +43,7 @@ constexpr int kRows = 256, kKeys = 128, kThreads = 512;
 constexpr int kCost = 3;   // tiles that a piece's start and end cost: 2: 50 and 86 us (16 drafted tokens over 32768 keys; prompts), 3: 47 and 85 (now 45 and 78)
 constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
+constexpr uint32_t kLate = 0xffffffffu;  // in a size's place: this warp's wait gave up
 
 // The power of two e for a tile whose largest parameter has the fp16 bits `size` (of |offset|, 16 |scale|): size * 2^e is in [2^-5, 2^-4).
 __device__ __forceinline__ int tile_power(uint32_t size) { return 10 - max((int)(size >> 10), 1); }
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int raw_have[4];                 // blocks of a raw tile that were read
   __shared__ uint32_t tile_info[kMeta];       // for the softmax: bits 0-7 blocks read, 8-15 and 16-23 powers of K and V + 64
   __shared__ int odd_piece[kMeta];            // 1 + the last piece (modulo kMeta) with a V value that is not finite
-  __shared__ uint2 sizes[2][4];               // fp16 bits of the largest K and V parameters, by dequantiser warp
+  __shared__ uint2 sizes[2][4];               // fp16 bits of the largest K and V parameters, by dequantiser warp; kLate
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t raw = smem_u32(smem_raw);
@@ -325,14 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = r & 15;   // in its block
     int stage = 0, item = 0, tiles = 0, piece = 0;
     uint32_t phase = 0, e_phase = 0;  // e_phase: a bit for each buffer
-    bool ok = true;
+    // A warp whose wait gave up is late: it does no more work but comes to the next tile's barrier, where all four see it and
+    // stop together. Left alone, the others would wait there without a limit.
+    bool ok = true, late = false;
     while (left > 0 && ok) {
       const int here = (int)min(left, (int64_t)(cur.t1 - cur.tile));
       for (int tile = cur.tile; tile < cur.tile + here; ++tile) {
-        if (!__all_sync(kFull, mbar_wait_bounded(&raw_full[stage], phase))) {
-          ok = false;
-          break;
-        }
+        if (!late) late = !__all_sync(kFull, mbar_wait_bounded(&raw_full[stage], phase));
         const int have = raw_have[stage];
         const uint32_t blk = smem_u32(raw_ring + stage * L::kRaw + (r >> 4) * L::kBlock);
         const uint32_t par = blk + 16 * D + row * 4;
@@ -350,22 +350,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ksize = __reduce_max_sync(kFull, ksize);
         vsize = __reduce_max_sync(kFull, vsize);
-        if (lane == 0) sizes[tiles & 1][warp - 4] = make_uint2(ksize, vsize);
+        if (lane == 0) sizes[tiles & 1][warp - 4] = make_uint2(late ? kLate : ksize, vsize);
         if (bad) odd_piece[piece % kMeta] = piece + 1;
         asm volatile("bar.sync 1, 128;" ::: "memory");
         for (int w = 0; w < 4; ++w) ksize = max(ksize, sizes[tiles & 1][w].x), vsize = max(vsize, sizes[tiles & 1][w].y);
+        if (ksize == kLate) {
+          ok = false;
+          break;
+        }
         const int ke = tile_power(ksize), ve = tile_power(vsize);
         if (r == 0) tile_info[tiles % kMeta] = (uint32_t)have | (uint32_t)(ke + 64) << 8 | (uint32_t)(ve + 64) << 16;
         // ---- K ----
         int buf = item % kBufs;
         if (item >= kBufs) {
-          if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
-            ok = false;
-            break;
-          }
+          if (!late) late = !__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u));
           e_phase ^= 1u << buf;
         }
-        {
+        if (!late) {
           Group gr[NG];
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi) gr[gi] = group_of(kpar[gi], ke);
@@ -389,18 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kv_full[buf]);
+        if (lane == 0 && !late) mbar_arrive(&kv_full[buf]);
         ++item;
         // ---- V ----
         buf = item % kBufs;
         if (item >= kBufs) {
-          if (!__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u))) {
-            ok = false;
-            break;
-          }
+          if (!late) late = !__all_sync(kFull, mbar_wait_bounded(&kv_empty[buf], e_phase >> buf & 1u));
           e_phase ^= 1u << buf;
         }
-        {
+        if (!late) {
           Group gr[KW];  // of each 32 elements
 #pragma unroll
           for (int gi = 0; gi < NG; ++gi) {
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && !late) {
           mbar_arrive(&kv_full[buf]);
           mbar_arrive(&raw_empty[stage]);
         }
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || !next_piece(here)) break;
       ++piece;
     }
-    if (!ok && lane == 0) give_up(kStatusFullWait);
+    if ((!ok || late) && lane == 0) give_up(kStatusFullWait);
   } else {
     tc::setmaxnreg_inc<168>();
     // ------------------------------ softmax -------------------------------------

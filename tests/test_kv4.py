@@ -213,3 +213,20 @@ def test_rows_of_the_tcgen05_kernel_own_their_bytes(tmp_path):
     kernel = open(os.path.join(root, "gemm_mnb_gemv_gb300", "csrc", "kv4_tile.cu")).read()
     used = [line for line in kernel.splitlines() if "room +" in line]
     assert used and all("room + tile_row_byte(" in line for line in used)
+
+
+def test_dequantisers_stop_together():
+    """They meet at a named barrier, which has no limit: a warp whose wait gave up has to come to it, so the only way out of
+    the loop over tiles is behind the barrier, on what all four were told there."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    kernel = open(os.path.join(root, "gemm_mnb_gemv_gb300", "csrc", "kv4_tile.cu")).read()
+    assert len(re.findall(r"bar\.sync|barrier\.(?:cta\.)?sync", kernel)) == 1
+    role = kernel[kernel.index("- dequantisers -"):kernel.index("- softmax -")]
+    loop = role[role.index("for (int tile = "):role.index("next_piece(here)")]
+    loop = re.sub(r"\[\]\([^)]*\) \{[^}]*\}", "", loop)  # lambdas
+    before, after = loop.split("bar.sync 1, 128;")
+    assert not re.search(r"\b(break|return|goto)\b", before)
+    outs = re.findall(r"(if \([^;{]*\) \{\s*ok = false;\s*)?\b(?:break|return|goto)\b", after)
+    assert len(outs) == 1 and outs[0].startswith("if (ksize == kLate)")
