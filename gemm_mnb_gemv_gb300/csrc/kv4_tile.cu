@@ -12,15 +12,19 @@
 //                both row tiles read a buffer, which halves the conversion per product;
 //   warps 8-11, 12-15  softmax of row tile A, B: a row a thread, no shuffles.
 // The issuer alternates S_A, P_B V, S_B, P_A V, so each softmax has the other tile's products to hide behind.
-// Conversion: a nibble as it lies is the fp16 subnormal c * 2^-24 (or c * 2^-20), so with the scale times 2^24 one FMA
-// gives offset + code * scale, rounded once. The scale has to stay below 2^16 then, so each key tile of K and of V is held at a
-// power of two of its value that puts its largest below 2^-4 and leaves fp16 its precision
-// whatever the values' size: the power goes into the softmax's factor (K) and, as a difference to the largest
-// tile so far, into P (V). A row's reference m moves as in the
-// streaming kernel, and only then is O rescaled in tensor memory.
+// Conversion: a code's byte is the 8-bit float (4 exponent bits) of c * 2^-9, two of which one instruction turns into fp16, exactly;
+// with the scale times 2^9 one FMA gives offset + code * scale, rounded once. The scale has to stay below 2^7 then. K is
+// held, a key tile at a time, at the power of two of its value that puts its largest just below 2^11: parts of 2^-24 of
+// the largest still have all of fp16's bits, whether their rows see the largest or not. The power goes into the softmax's factor. V is
+// held as it is (what mnb_kv4_read gives in fp16); a tile beyond 2^11 is held at the power that brings it there, which goes, as a
+// difference to the largest tile so far, into P (2^-9 at the least, where P's last place is 2^-23 of its largest).
+// Other ways: the nibbles as they lie, fp16 subnormals c * 2^-24, save two operations in eleven a word, but the scale times 2^24 stays
+// inside fp16 only where a tile's largest is held below 2^-4, and parts of 2^-10 of it are subnormals then (chunk and prompts below
+// 825 and 75.8 us in the same run in which this form took 845 and 76.3); codes as 1024 + c, less 1024: 852 and 78.0.
+// A row's reference m moves as in the streaming kernel, and only then is O rescaled in tensor memory.
 // A non-finite V value enters as 0 (0 * NaN would reach every row of the tile) and marks its piece: at the piece's
 // end the rows look for such keys among those that they see, and get NaN in the groups.
-// Element order: the nibbles of a word convert to elements (n0, n4), (n1, n5), ..; q is permuted
+// Element order: the nibbles of a word convert to elements n0, n2, n4, n6, n1, n3, n5, n7; q is permuted
 // alike, and O's columns are put back when they are stored.
 // Fewer bits: K, V and P are each rounded once to fp16, as the result is; the error (norm, against fp64) is 3.8e-4 to 4.5e-4,
 // of which the result's own rounding is 2.1e-4. Keeping the codes exact would take a multiplication of each score and each
@@ -45,8 +49,9 @@ constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
 constexpr uint32_t kLate = 0xffffffffu;  // in a size's place: this warp's wait gave up
 
-// The power of two e for a tile whose largest parameter has the fp16 bits `size` (of |offset|, 16 |scale|): size * 2^e is in [2^-5, 2^-4).
-__device__ __forceinline__ int tile_power(uint32_t size) { return 10 - max((int)(size >> 10), 1); }
+// The power of two e for a tile whose largest parameter has the fp16 bits `size` (of |offset|, 16 |scale|): size * 2^e is in
+// [2^10, 2^11).
+__device__ __forceinline__ int tile_power(uint32_t size) { return 25 - max((int)(size >> 10), 1); }
 
 template <int D, int NG>
 struct TileSmem {
@@ -91,19 +96,34 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 
 // Scale and offset of a group, times 2^e, as pairs for convert().
 struct Group {
-  uint32_t lower, upper, offset;
+  uint32_t scale, offset;
 };
 __device__ __forceinline__ Group group_of(uint32_t param, int e) {
   const float2 so = unpack_half2(param);
-  const float f = pow2(e), s = so.x * f * 16777216.0f;
-  return {pack_half2(s, s), pack_half2(s * 0.0625f, s * 0.0625f), pack_half2(so.y * f, so.y * f)};
+  const float f = pow2(e), s = so.x * f * 512.0f;
+  return {pack_half2(s, s), pack_half2(so.y * f, so.y * f)};
 }
 
-// A word's 8 codes to offset + code * scale, in the order (n0, n4), (n1, n5), (n2, n6), (n3, n7).
-__device__ __forceinline__ uint4 convert(uint32_t w, const Group& g) {
-  const uint32_t t = w >> 8;
-  return make_uint4(hfma2_bits(w & 0x000f000fu, g.lower, g.offset), hfma2_bits(w & 0x00f000f0u, g.upper, g.offset),
-                    hfma2_bits(t & 0x000f000fu, g.lower, g.offset), hfma2_bits(t & 0x00f000f0u, g.upper, g.offset));
+// Bytes 0 and 1, and 2 and 3, of codes 0..15 to fp16 c * 2^-9.
+__device__ __forceinline__ uint2 codes_to_half(uint32_t x) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(x));
+  return r;
+}
+
+// A word's 8 codes to offset + code * scale, in the order n0, n2, n4, n6, n1, n3, n5, n7; n0..n3 are of group `a`, n4..n7 of `b`.
+__device__ __forceinline__ uint4 convert(uint32_t w, const Group& a, const Group& b) {
+  const uint2 even = codes_to_half(w & 0x0f0f0f0fu), odd = codes_to_half(w >> 4 & 0x0f0f0f0fu);
+  return make_uint4(hfma2_bits(even.x, a.scale, a.offset), hfma2_bits(even.y, b.scale, b.offset),
+                    hfma2_bits(odd.x, a.scale, a.offset), hfma2_bits(odd.y, b.scale, b.offset));
+}
+// Elements of q in the same order.
+__device__ __forceinline__ uint4 in_code_order(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                    __byte_perm(v.z, v.w, 0x7632));
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
@@ -358,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const int ke = tile_power(ksize), ve = tile_power(vsize);
+        const int ke = tile_power(ksize), ve = min(tile_power(vsize), 0);
         if (r == 0) tile_info[tiles % kMeta] = (uint32_t)have | (uint32_t)(ke + 64) << 8 | (uint32_t)(ve + 64) << 16;
         // ---- K ----
         int buf = item % kBufs;
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const int t = KW == 4 ? ch : ch * 2 + i / 2, w = KW == 4 ? i : i % 2;
               const int chunk = 4 * w + t;  // 16-byte chunk of the row
-              sts128((dst ^ ((chunk & 7) << 4)) + (chunk >> 3) * (kKeys * 128), convert(w4[i], gr[w * NG / KW]));
+              sts128((dst ^ ((chunk & 7) << 4)) + (chunk >> 3) * (kKeys * 128), convert(w4[i], gr[w * NG / KW], gr[w * NG / KW]));
             }
           }
         }
@@ -422,12 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < 8; ++g) {
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
-              // nibbles (n, n + 4): elements 32 apart, of two groups when groups have 32
-              Group y = gr[2 * w];
-              if constexpr (NG == KW)
-                y = {__byte_perm(y.lower, gr[2 * w + 1].lower, 0x5410), __byte_perm(y.upper, gr[2 * w + 1].upper, 0x5410),
-                     __byte_perm(y.offset, gr[2 * w + 1].offset, 0x5410)};
-              sts128((dst ^ (g << 4)) + w * (kKeys * 128), convert(vw[g][w], y));
+              // nibbles 0..3 and 4..7: elements 32 apart, of two groups when groups have 32
+              sts128((dst ^ (g << 4)) + w * (kKeys * 128), convert(vw[g][w], gr[2 * w], gr[2 * w + 1]));
             }
           }
         }
@@ -483,10 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
             const int to = wrow + i0 + i * kAtOnce + lane / kChunks;
-            uint32_t p[4];
-            pair_halves_stride4(v[i], p);
+            const uint4 p = in_code_order(v[i]);
             sts128(q_at + x * (L::kQ / 2) + tile_row_byte(to, ch),
-                   make_uint4(p[0] ^ flip, p[1] ^ flip, p[2] ^ flip, p[3] ^ flip));
+                   make_uint4(p.x ^ flip, p.y ^ flip, p.z ^ flip, p.w ^ flip));
           }
         }
         tc::fence_proxy_async_smem();
@@ -644,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr bool kCutRoom = D == 128;  // 64 elements of a row in fp32 fit
 #pragma unroll 1
       for (int w = 0; w < VW; ++w) {
-        // columns 64 w + 8 g + i hold element 64 w + 32 (i & 1) + 4 g + i / 2
+        // column 64 w + 8 g + 4 (n & 1) + 2 h + n / 2 holds element 64 w + 32 h + 4 g + n
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {  // g of 4 half ..
           float o[32];
@@ -656,14 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f0 = (nan_groups >> (2 * w * NG / KW) & 1) || !ok ? NAN : f;
           const float f1 = (nan_groups >> ((2 * w + 1) * NG / KW) & 1) || !ok ? NAN : f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = none && whole ? 0.0f : o[i] * (i & 1 ? f1 : f0);
+          for (int i = 0; i < 32; ++i) o[i] = none && whole ? 0.0f : o[i] * (i & 2 ? f1 : f0);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int g2 = 0; g2 < 4; g2 += 2) {  // elements 32 h + 16 half + 4 g2 .. + 7 of the 64
               float y[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 2 * (k % 4) + h];
+              for (int k = 0; k < 8; ++k) y[k] = o[8 * (g2 + k / 4) + 4 * (k & 1) + 2 * h + k % 4 / 2];
               const int d8 = 4 * h + 2 * half + g2 / 2;  // eight elements
               if (whole) {
                 *reinterpret_cast<uint4*>(room + tile_row_byte(wrow + lane, d8)) = make_uint4(

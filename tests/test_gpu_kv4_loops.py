@@ -66,7 +66,7 @@ class Filled:
         self.cache = mnb.mnb_kv4_cache_alloc(sum(need) + 2, ps, Hk, D, group, dev)
         order = torch.randperm(sum(need) + 2, generator=gen, device=dev)
         table = torch.zeros((len(lens), max(need)), dtype=torch.int64, device=dev)
-        self.slots, at = [], 0
+        self.slots, self.kv, at = [], [], 0
         for b, (_, n) in enumerate(lens):
             table[b, : need[b]] = order[at: at + need[b]]
             at += need[b]
@@ -76,9 +76,9 @@ class Filled:
             for x, size in zip(kv, (ksize, vsize)):
                 if size is not None:
                     x *= size(j.float())[:, None, None]
-            kv = [x.float() for x in kv]
             if n:
                 mnb.mnb_kv4_append(self.cache, kv[0], kv[1], self.slots[b])
+            self.kv.append(kv)
         self.table = table.int()
         self.kv_len = torch.tensor([n for _, n in lens], dtype=torch.int32, device=dev)
         self.start = torch.tensor(np.cumsum([0] + [a for a, _ in lens]), dtype=torch.int32, device=dev)
@@ -89,6 +89,10 @@ class Filled:
         T = sum(a for a, _ in self.lens)
         q = torch.randn((T, self.Hk * G, self.D), generator=self.gen, device=dev) * size
         return q.to(torch.float16 if dtype == "f16" else torch.float32)
+
+    def store(self, b):
+        """Appends sequence b again, after changes of kv[b]."""
+        self.env[0].mnb_kv4_append(self.cache, *self.kv[b], self.slots[b])
 
     def attend(self, q, scale, causal=True, window=0, lse=None):
         return self.env[0].mnb_kv4_attention(q, self.cache, self.start, self.kv_len, self.table, scale, causal=causal,
@@ -161,3 +165,62 @@ def test_prompts_of_several_pieces(env, D, group, ps, Hk, G, lens, causal, windo
     f = Filled(env, D + G, D, group, ps, Hk, lens)
     _, variant = f.check(f.queries(G, "f16"), "f16", D ** -0.5, causal, window)
     assert variant == "kv4_tile_tcgen05"
+
+
+def _check_parts(out, want, dtype, rows, parts, what):
+    """The norm bound of `test_gpu_kv4` for these rows' elements of each part of the head by itself (their scores must
+    be ordinary), and its bound for each element."""
+    ref, _, mag, reach = (x[rows] for x in want)
+    got = out.double().cpu().numpy()[rows]
+    assert reach.max() < 40
+    _check(out[rows], None, (ref, None, mag, reach), dtype, what)
+    u = 2.0 ** -11 if dtype == "f16" else 2.0 ** -20
+    for part in np.split(np.arange(ref.shape[-1]), parts):
+        a, b = got[..., part], ref[..., part]
+        bound = 2 * u * np.linalg.norm(b) + 2.0 ** -25 * np.sqrt(b.size) if dtype == "f16" else 4 * u * np.linalg.norm(b)
+        assert np.linalg.norm(a - b) <= bound, (what, part[0], np.linalg.norm(a - b) / np.linalg.norm(b))
+
+
+# (query tokens, keys), window, the odd token: the tcgen05 kernel, then the streaming one
+UNEVEN = [((300, 300), 0, 220), ((200, 450), 100, 340), ((3, 300), 0, 298), ((1, 300), 100, 190)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("factor", [100, 1000, 10000])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 128)])
+@pytest.mark.parametrize("lens,window,odd", UNEVEN)
+def test_a_token_of_another_size(env, D, group, lens, window, odd, factor, dtype):  # noqa: F811
+    """One token's key or value is larger than all others of its tile: rows that don't see it are as exact as without it."""
+    q_len, n = lens
+    pos = n - q_len + np.arange(q_len)
+    hidden = (pos < odd) | ((window > 0) & (pos - window >= odd))
+    for which in (0, 1):
+        f = Filled(env, D + group, D, group, 16, 2, [lens], None, lambda j: 0.05 + 0 * j)
+        f.kv[0][which][odd] *= factor
+        f.store(0)
+        q, scale = f.queries(4, dtype), float(np.float32(D ** -0.5))
+        out = f.attend(q, scale, True, window)
+        assert env[0].mnb_last_variant() == ("kv4_tile_tcgen05" if q_len > 100 and dtype == "f16" else env[0].mnb_last_variant())
+        want = f.want(q, scale, True, window)
+        _check_parts(out, want, dtype, hidden, 1, (which, factor))
+        if which == 1:  # with a key of ordinary size the rows that do see it are ordinary too
+            _check(out, None, want, dtype, "all rows")
+    env[0].mnb_check_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f16"])
+@pytest.mark.parametrize("factor", [100, 1000, 10000])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 64)])
+@pytest.mark.parametrize("lens,window,odd", UNEVEN)
+def test_groups_of_another_size(env, D, group, lens, window, odd, factor, dtype):  # noqa: F811
+    """The first group of every key and value is larger than the others, and q has zeros there: scores are ordinary, and
+    the other groups' results are as exact as without it."""
+    f = Filled(env, D + group, D, group, 16, 2, [lens], None, lambda j: 0.05 + 0 * j)
+    for x in f.kv[0]:
+        x[..., :group] *= factor
+    f.store(0)
+    q, scale = f.queries(4, dtype), float(np.float32(D ** -0.5))
+    q[..., :group] = 0
+    out = f.attend(q, scale, True, window)
+    _check_parts(out, f.want(q, scale, True, window), dtype, np.ones(lens[0], bool), D // group, factor)
+    env[0].mnb_check_device_status()
