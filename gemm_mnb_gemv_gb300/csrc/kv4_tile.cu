@@ -356,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int have = raw_have[stage];
         const uint32_t blk = smem_u32(raw_ring + stage * L::kRaw + (r >> 4) * L::kBlock);
         const uint32_t par = blk + 16 * D + row * 4;
-        // ---- parameters, zeros for keys that are not there; the four warps agree on the tile's powers ----
+        // ---- parameters, zeros for keys that are not there or that no row sees; the four warps agree on the tile's powers ----
         uint32_t kpar[NG], vpar[NG], bad = 0, ksize = 0, vsize = 0;  // sizes: the larger of |offset| and 16 |scale|
-        const bool there = tile * kKeys + r < cur.n && (have >> (r >> 4) & 1);
+        const bool there = tile * kKeys + r >= cur.lo && tile * kKeys + r < cur.hi && (have >> (r >> 4) & 1);
         auto finite = [](uint32_t p) { return (p & 0x7c00u) != 0x7c00u && (p & 0x7c000000u) != 0x7c000000u; };
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {

@@ -62,7 +62,8 @@ struct Cursor {
   int b, rt, kvh, tile;
   int q0, qlen, n;    // query rows and keys of sequence b
   int R;              // row tiles of sequence b
-  int t0, t1;         // key tiles of row tile rt
+  int lo, hi;         // keys that some row of row tile rt sees: 32 bits hold them (2^30 keys, 2^20 tokens, a window of 2^30)
+  int t0, t1;         // their tiles
 };
 
 // kPieceCost: what starting and ending a piece of a sequence costs, in tiles; counted where the work is
@@ -82,14 +83,13 @@ struct Walk {
     s.n = min(max(a.kv_len[s.b], 0), capacity);
     s.R = (int)(((int64_t)s.qlen * G + RT - 1) / RT);
   }
-  // key tiles that some row of row tile rt sees
+  // of row tile rt
   __device__ __forceinline__ void range(Cursor& s) const {
     const int first = s.rt * RT / G, last = min(s.qlen - 1, (s.rt * RT + RT - 1) / G);
-    const int64_t pos0 = (int64_t)s.n - s.qlen + first, pos1 = (int64_t)s.n - s.qlen + last;
-    const int64_t hi = a.causal ? min((int64_t)s.n, pos1 + 1) : s.n;
-    const int64_t lo = a.window > 0 ? max((int64_t)0, pos0 - a.window + 1) : 0;
-    s.t0 = (int)(lo / kTile);
-    s.t1 = max(s.t0 + 1, (int)((max(hi, (int64_t)0) + kTile - 1) / kTile));  // a row tile without keys still has a unit: it writes zeros
+    s.hi = a.causal ? max(0, min(s.n, s.n - s.qlen + last + 1)) : s.n;
+    s.lo = a.window > 0 ? max(0, s.n - s.qlen + first - a.window + 1) : 0;
+    s.t0 = s.lo / kTile;
+    s.t1 = max(s.t0 + 1, (s.hi + kTile - 1) / kTile);  // a row tile without keys still has a unit: it writes zeros
   }
   __device__ __forceinline__ int64_t units(Cursor s) const {  // of sequence s.b, loaded
     int64_t u = 0;

@@ -208,7 +208,7 @@ def test_a_token_of_another_size(env, D, group, lens, window, odd, factor, dtype
     env[0].mnb_check_device_status()
 
 
-@pytest.mark.parametrize("dtype", ["f16"])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("factor", [100, 1000, 10000])
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 64)])
 @pytest.mark.parametrize("lens,window,odd", UNEVEN)
@@ -223,4 +223,22 @@ def test_groups_of_another_size(env, D, group, lens, window, odd, factor, dtype)
     q[..., :group] = 0
     out = f.attend(q, scale, True, window)
     _check_parts(out, f.want(q, scale, True, window), dtype, np.ones(lens[0], bool), D // group, factor)
+    env[0].mnb_check_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("D,group,lens,window", [(64, 64, (1, 300), 100), (128, 128, (1, 300), 100), (128, 64, (3, 300), 100),
+                                                 (256, 128, (1, 300), 100), (128, 64, (90, 300), 100)])
+def test_a_value_that_no_row_sees(env, D, group, lens, window, dtype):  # noqa: F811
+    """It lies in a key tile that is read, below the window, and is larger than the others by almost all of fp16's range."""
+    f = Filled(env, D, D, group, 16, 2, [lens], None, lambda j: 0.001 + 0 * j)
+    q, scale = f.queries(4, dtype), float(np.float32(D ** -0.5))
+    clean = f.attend(q, scale, True, window)
+    first = lens[1] - lens[0] - window + 1
+    f.kv[0][1][first - 3] = 40000.0 * f.kv[0][1][first - 3].sign()
+    f.store(0)
+    out = f.attend(q, scale, True, window)
+    _check(out, None, f.want(q, scale, True, window), dtype, env[0].mnb_last_variant())
+    if env[0].mnb_last_variant() != "kv4_tile_tcgen05":
+        assert env[1].equal(out, clean)
     env[0].mnb_check_device_status()
