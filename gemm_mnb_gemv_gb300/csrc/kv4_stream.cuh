@@ -10,10 +10,10 @@
 //   * V: codes become c - 8 (exact), probabilities become fp16(p * scale_g * 2^x) per group, and
 //     sum_j p_j (offset + 8 scale) is kept in fp32.  Centring keeps the rounding of p * scale from being
 //     multiplied by |offset| / |v| (fp32 activations centre K too: fp32 sums of uncentred products would lose
-//     two bits).  The power 2^x follows the largest scale among the keys that some row of the tile sees, so values of any
-//     size use fp16's whole range. A scale 2^-y of that largest leaves p * scale 2^(y - 33) of the row's
-//     largest p as its step: with fp16 activations one power serves all groups (2^-13 at y = 20), with fp32 each group has
-//     its own, and tokens 2^13 apart stay within 2^-20.
+//     two bits).  With fp16 activations the power 2^x follows the largest scale among the keys that some row of the
+//     tile sees, which then is 1 to 2; a scale 2^-y of it leaves its products a step of 2^(y - 33) of a row's largest
+//     (2^-13 at y = 20).  With fp32 each group of each 16 keys has its own power, as their sums are added outside the
+//     tensor cores anyway.
 // A row's reference m moves only when a score passes it by 14 (in powers of two; one vote a
 // block instead of shuffles) and is then set 8 below the largest: p = 2^(s - m) <= 2^14, so
 // fp16 keeps probabilities down to 2^-22 of the largest normal.
@@ -59,6 +59,10 @@ __device__ __forceinline__ uint32_t c_upper(uint32_t x) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(r), "r"(0x2C002C00u), "r"(0xD480D480u));
   return r;
 }
+
+// Power of two of an fp16 magnitude's bits: 2^e <= size < 2^(e + 1) for normal ones, smaller ones count as 2^-14.
+__device__ __forceinline__ int half_exponent(uint32_t bits) { return max((int)(bits >> 10), 1) - 15; }
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Shared memory of a CTA.
 template <int D, int NG, int NT, int PB, bool F32>
@@ -336,11 +340,9 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
       return key < cur.n && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
     };
     float m[NT][2], l[NT][2], o[D / 16][NT][4], oo[NG][NT][2];
-    constexpr int VG = F32 ? NG : 1;  // groups with a power of their own
-    float vmul[VG], vinv[VG];
-    uint32_t vlim[VG];  // fp16 pair: V scales stay up to this (offsets: any finite)
-#pragma unroll
-    for (int k = 0; k < VG; ++k) vmul[k] = vinv[k] = 1.0f, vlim[k] = 0x7bff0000u;
+    // fp16: V scales are held times vmul, o times vmul too
+    float vmul = 1.0f, vinv = 1.0f;
+    uint32_t vlim = F32 ? 0x7bff7bffu : 0x7bff0000u;  // fp16 pair: V scales stay up to this (offsets, and all of fp32's: any finite)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
           }
         }
         // ---- references: rise when a score passes its row's, or a V scale its limit ----
-        uint32_t vtop[VG];  // fp16 pairs of largest magnitudes, NaN if there is one
+        uint32_t vtop = 0;  // fp16 pair of largest magnitudes, NaN if there is one
 #pragma unroll
         for (int p = 0; p < PB; ++p)
 #pragma unroll
@@ -495,14 +497,10 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t v = vp[p][gi][h] & 0x7fff7fffu;
-              uint32_t& top = vtop[F32 ? gi : 0];
-              if (p == 0 && (F32 || gi == 0) && h == 0) top = v;
-              else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(top) : "r"(top), "r"(v));
+              if (p == 0 && gi == 0 && h == 0) vtop = v;
+              else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(vtop) : "r"(vtop), "r"(v));
             }
-        bool rise = false;
-#pragma unroll
-        for (int k = 0; k < VG; ++k)
-          rise |= !__hble2(*reinterpret_cast<const __half2*>(&vtop[k]), *reinterpret_cast<const __half2*>(&vlim[k]));
+        bool rise = !__hble2(*reinterpret_cast<const __half2*>(&vtop), *reinterpret_cast<const __half2*>(&vlim));
         float tops[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -515,12 +513,9 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
         if (__any_sync(kFull, rise)) {
           // inf or NaN among the V parameters: rows that see such a key get NaN in its group, the others
           // go on without the key's value (0 * NaN would reach them in the products)
-          bool odd = false;
-#pragma unroll
-          for (int k = 0; k < VG; ++k) odd |= (vtop[k] & 0x7c00u) == 0x7c00u || (vtop[k] & 0x7c000000u) == 0x7c000000u;
+          const bool odd = (vtop & 0x7c00u) == 0x7c00u || (vtop & 0x7c000000u) == 0x7c000000u;
           if (__any_sync(kFull, odd)) {
-#pragma unroll
-            for (int k = 0; k < VG; ++k) vtop[k] = 0;
+            vtop = 0;
 #pragma unroll
             for (int p = 0; p < PB; ++p)
 #pragma unroll
@@ -536,23 +531,21 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
                       for (int j = 0; j < 2; ++j)
                         if (sees(base + 16 * p + g + 8 * h, nt * 8 + 2 * t + j)) oo[gi][nt][j] = NAN;
                   } else {
-                    vtop[F32 ? gi : 0] = __vmaxu2(vtop[F32 ? gi : 0], v & 0x7fff7fffu);
+                    vtop = __vmaxu2(vtop, v & 0x7fff7fffu);
                   }
                 }
           }
-          float grow[VG];
-#pragma unroll
-          for (int k = 0; k < VG; ++k) {
-            const uint32_t need = __reduce_max_sync(kFull, vtop[k] & 0xffffu);
-            grow[k] = 1.0f;
-            if (need > (vlim[k] & 0xffffu)) {
-              const int ex = (int)(__float_as_uint(half_bits_to_float(need)) >> 23) - 127;
-              const float mul = __uint_as_float((uint32_t)(127 - 2 - ex) << 23);  // scales up to vlim become at most 1
-              grow[k] = vinv[k] * mul;
-              vmul[k] = mul;
-              vinv[k] = __uint_as_float((uint32_t)(127 + 2 + ex) << 23);
-              const __half lim = __float2half_rn(fminf(scalbnf(1.0f, ex + 2), 65504.0f));
-              vlim[k] = (uint32_t)__half_as_ushort(lim) | 0x7bff0000u;
+          float grow = 1.0f;
+          if constexpr (!F32) {
+            const uint32_t need = __reduce_max_sync(kFull, vtop & 0xffffu);
+            if (need > (vlim & 0xffffu)) {
+              const int ex = half_exponent(need);
+              const float mul = pow2f(-ex);  // scales up to vlim = 2^(ex + 1) become at most 2
+              grow = vinv * mul;
+              vmul = mul;
+              vinv = pow2f(ex);
+              const __half lim = __float2half_rn(fminf(pow2f(ex + 1), 65504.0f));
+              vlim = (uint32_t)__half_as_ushort(lim) | 0x7bff0000u;
             }
           }
 #pragma unroll
@@ -568,11 +561,9 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
               l[nt][j] *= al;
 #pragma unroll
               for (int gi = 0; gi < NG; ++gi) oo[gi][nt][j] *= al;
+              const float ag = al * grow;
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const float ag = al * grow[F32 ? i / 2 / GR : 0];
-                o[i][nt][j] *= ag, o[i][nt][j + 2] *= ag;
-              }
+              for (int i = 0; i < D / 16; ++i) o[i][nt][j] *= ag, o[i][nt][j + 2] *= ag;
             }
         }
         // ---- probabilities ----
@@ -608,13 +599,20 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
             }
           }
           uint32_t bh[NT][2], bl[F32 ? NT : 1][2];
+          float back = 1.0f;  // fp32: undoes the group's power
 #pragma unroll
           for (int i = 0; i < KW; ++i) {  // granule of 32 elements: word i / 2, half i % 2
             if (i % GR == 0) {
               const int gi = i / GR;
               const float2 p0 = unpack_half2(vp[p][gi][0]), p1 = unpack_half2(vp[p][gi][1]);
               const float x0 = fmaf(p0.x, 8.0f, p0.y), x1 = fmaf(p1.x, 8.0f, p1.y);
-              const float f0 = p0.x * vmul[F32 ? gi : 0], f1 = p1.x * vmul[F32 ? gi : 0];
+              float mul = vmul;
+              if constexpr (F32) {
+                const uint32_t need = __reduce_max_sync(kFull, max(vp[p][gi][0] & 0x7fffu, vp[p][gi][1] & 0x7fffu));
+                const int ex = half_exponent(need);
+                mul = pow2f(-ex), back = pow2f(ex);
+              }
+              const float f0 = p0.x * mul, f1 = p1.x * mul;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const float* sp = s[p][nt];
@@ -645,7 +643,7 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
                   mma16816_zero(acc, a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
                   mma16816(acc, a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) o[2 * i + j][nt][k] += acc[k];
+                  for (int k = 0; k < 4; ++k) o[2 * i + j][nt][k] = fmaf(acc[k], back, o[2 * i + j][nt][k]);
                 } else {
                   mma16816(o[2 * i + j][nt], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
                 }
@@ -697,8 +695,8 @@ __global__ void __launch_bounds__(kWarps * 32, stream_ctas<D, NT, F32>())
             const int d = (i % 4 / 2) * 32 + 4 * g + (i % 2) * 2;  // within the 64 elements
             const int col = 2 * t + j;
             float2 v;
-            v.x = fmaf(o[i][nt][j], vinv[F32 ? i / 2 / GR : 0], base_sum) * fac[j];
-            v.y = fmaf(o[i][nt][j + 2], vinv[F32 ? i / 2 / GR : 0], base_sum) * fac[j];
+            v.x = fmaf(o[i][nt][j], vinv, base_sum) * fac[j];
+            v.y = fmaf(o[i][nt][j + 2], vinv, base_sum) * fac[j];
             *reinterpret_cast<float2*>(&exch[(warp * 8 + col) * 64 + d]) = v;
           }
         }

@@ -47,10 +47,10 @@ def _shares(lens, Hk, G, rows, keys, cost, ctas, causal=True, window=0):
     return out
 
 
-def _reaches(shares, tiles, pieces):
-    """Most CTAs have `tiles` key tiles in all, and many at least `pieces` pieces."""
+def _reaches(shares, tiles, pieces, part=0.3):
+    """Most CTAs have `tiles` key tiles in all, and this part of them at least `pieces` pieces."""
     assert np.median([sum(s) for s in shares]) >= tiles, np.median([sum(s) for s in shares])
-    assert np.mean([len(s) >= pieces for s in shares]) >= 0.3, np.mean([len(s) >= pieces for s in shares])
+    assert np.mean([len(s) >= pieces for s in shares]) >= part, np.mean([len(s) >= pieces for s in shares])
     assert max(max(s, default=0) for s in shares) >= 3
 
 
@@ -98,8 +98,10 @@ class Filled:
         return self.env[0].mnb_kv4_attention(q, self.cache, self.start, self.kv_len, self.table, scale, causal=causal,
                                              window=window, lse=lse)
 
-    def want(self, q, scale, causal=True, window=0):
-        """As the oracle's `attention`: out, lse, sum_j p_j |v_j|, largest scale * sum_d |q_d k_jd|, fp64."""
+    def want(self, q, scale, causal=True, window=0, held=None):
+        """As the oracle's `attention`: out, lse, sum_j p_j |v_j|, largest scale * sum_d |q_d k_jd|, fp64.  With held =
+        (half step, smallest half step of p relative to the row's largest, whether groups share it, largest |code| in a
+        product) also the bound of what holding p_j * V scale in fewer bits does to each element."""
         mnb, torch, dev = self.env
         T, Hq, D = q.shape
         G = Hq // self.Hk
@@ -107,6 +109,7 @@ class Filled:
         out, mag = torch.zeros((T, Hq, D), dtype=f64, device=dev), torch.zeros((T, Hq, D), dtype=f64, device=dev)
         lse = torch.full((T, Hq), float("-inf"), dtype=f64, device=dev)
         reach = torch.zeros((T, Hq), dtype=f64, device=dev)
+        bound = torch.zeros((T, Hq, D), dtype=f64, device=dev)
         for b, (q_len, n) in enumerate(self.lens):
             if not q_len or not n:
                 continue
@@ -126,7 +129,16 @@ class Filled:
                 out[a: a + q_len, h], mag[a: a + q_len, h] = p @ v, p @ v.abs()
                 lse[a: a + q_len, h] = l
                 reach[a: a + q_len, h] = (x.abs() @ k.abs().T * abs(scale)).masked_fill(hide, 0.0).amax(-1)
-        return tuple(t.cpu().numpy() for t in (out, lse, mag, reach))
+                if held:
+                    half, least, shared, code = held
+                    g = self.cache.group_size
+                    step = (v.view(n, -1, g).amax(-1) - v.view(n, -1, g).amin(-1)) / 15  # V scales, up to their rounding
+                    for i in range(D // g):
+                        product = p * step[:, i]
+                        floor = p.amax(-1, keepdim=True) * least * (step.max() if shared else step[:, i])
+                        lost = torch.maximum(half * product, torch.minimum(product, floor))
+                        bound[a: a + q_len, h, i * g: (i + 1) * g] = code * lost.sum(-1, keepdim=True)
+        return tuple(t.cpu().numpy() for t in (out, lse, mag, reach) + ((bound,) if held else ()))
 
     def check(self, q, dtype, scale, causal=True, window=0):
         mnb, torch, dev = self.env
@@ -241,4 +253,39 @@ def test_a_value_that_no_row_sees(env, D, group, lens, window, dtype):  # noqa: 
     _check(out, None, f.want(q, scale, True, window), dtype, env[0].mnb_last_variant())
     if env[0].mnb_last_variant() != "kv4_tile_tcgen05":
         assert env[1].equal(out, clean)
+    env[0].mnb_check_device_status()
+
+
+# keys that grow make every row's reference rise over sums that it has; values of 0.003 to 3000 in waves of a few tiles
+LONG = {"decode": [(1, 8000), (1, 8192), (1, 5000)] * 6, "verify": [(4, 8000), (3, 8192), (4, 6000)] * 6,
+        "prompts": [(700, 3000), (900, 2900)]}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("form", LONG)
+def test_one_key_takes_all_among_values_of_many_sizes(env, form, D, group, dtype):  # noqa: F811
+    """Scores so far apart that a row is one or two keys, whose elements may be near zero while the parts that make them up
+    are not.  The bound of an element is `_check`'s and what the held probabilities add to it:
+
+    * streaming, fp16: p * V scale is rounded to fp16, to 2^-12 of it or, among the subnormals, to 2^-25 where the row's largest
+      p times the largest scale is 2^8 at least; it multiplies |c - 8| <= 8;
+    * streaming, fp32: two fp16 make it 2^-23, and the scale is that of its own 16 keys (within 2 here);
+    * tcgen05: p itself, where values beyond 2^11 (16 V scales; up to 2^15 here) take up to 2^5 from it; it multiplies up to 16 scales.
+    """
+    lens, Hk, G = LONG[form], 8, 4
+    tiles = form == "prompts" and dtype == "f16" and D <= 128
+    f = Filled(env, D, D, group, 16, Hk, lens, lambda j: 0.05 + 15 * (j / 8192) ** 0.5,
+               lambda j: 3 * 10 ** (3 * env[1].sin(j / 150)))
+    q, scale = f.queries(G, dtype), float(np.float32(D ** -0.5))
+    held = (2.0 ** -12, 2.0 ** -28, True, 16) if tiles else (2.0 ** -12, 2.0 ** -33, True, 8) if dtype == "f16" else (
+        2.0 ** -23, 2.0 ** -32, False, 8)
+    out = f.attend(q, scale).double().cpu().numpy()
+    ref, _, mag, reach, bound = f.want(q, scale, held=held)
+    u = 2.0 ** -11 if dtype == "f16" else 2.0 ** -20
+    tol = 4 * u * (np.abs(ref) + mag) + np.expm1(2 * u * reach[..., None]) * (mag + bound) + bound
+    if dtype == "f16":
+        tol = tol + 2.0 ** -24
+    assert reach.max() > 60 and np.isfinite(out).all()
+    assert (np.abs(out - ref) <= tol).all(), np.max(np.abs(out - ref) / tol)
     env[0].mnb_check_device_status()
