@@ -256,9 +256,44 @@ def test_a_value_that_no_row_sees(env, D, group, lens, window, dtype):  # noqa: 
     env[0].mnb_check_device_status()
 
 
+RAGGED = [8192, 1, 7000, 0, 3333, 17, 5000, 8191, 128, 129, 6100, 2049, 4096, 7777, 900, 8000, 6500, 30, 5555, 7123, 4444,
+          8188, 2500, 6001, 7400, 3000, 8100]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 4])
+@pytest.mark.parametrize("D,group,ps,Hk,G,window", [
+    (64, 32, 16, 8, 4, 0), (64, 64, 64, 7, 3, 5000), (128, 32, 32, 8, 4, 0), (128, 64, 128, 8, 4, 6000), (128, 128, 16, 8, 4, 0),
+    (256, 32, 16, 8, 4, 0), (256, 64, 48, 7, 2, 0), (256, 128, 16, 8, 4, 4500)])
+def test_decode_and_verify_of_many_tiles(env, D, group, ps, Hk, G, window, tokens, dtype):  # noqa: F811
+    """Streaming kernel: several steps of every warp, rings in use again, one piece after the other, ragged."""
+    lens = [(min(n, 1 + i % tokens), n) if n else (1, 0) for i, n in enumerate(RAGGED)]
+    average = -(-sum(a for a, _ in lens) // len(lens)) * G
+    rows = 8 if average <= 8 else 16
+    keys = 64 if D == 256 and rows == 16 else 128
+    _reaches(_shares(lens, Hk, G, rows, keys, 3, STREAM_CTAS * _sms(env), True, window), 7, 2, 0.15)
+    f = Filled(env, D + G + tokens, D, group, ps, Hk, lens)
+    _, variant = f.check(f.queries(G, dtype), dtype, D ** -0.5, True, window)
+    assert variant == f"kv4_stream_{dtype}_rows{rows}"
+
+
 # keys that grow make every row's reference rise over sums that it has; values of 0.003 to 3000 in waves of a few tiles
 LONG = {"decode": [(1, 8000), (1, 8192), (1, 5000)] * 6, "verify": [(4, 8000), (3, 8192), (4, 6000)] * 6,
         "prompts": [(700, 3000), (900, 2900)]}
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("form", LONG)
+def test_sizes_that_change_along_a_sequence(env, form, D, group, dtype):  # noqa: F811
+    lens, Hk, G = LONG[form], 8, 4
+    tiles = form == "prompts" and dtype == "f16" and D <= 128
+    rows, keys, ctas = (256, 128, _sms(env)) if tiles else (8 if form == "decode" else 16, 128, STREAM_CTAS * _sms(env))
+    _reaches(_shares(lens, Hk, G, rows, keys, 3, ctas), 5, 2, 0.15)
+    f = Filled(env, D, D, group, 16, Hk, lens, lambda j: 0.05 + 3.5 * (j / 8192) ** 0.5,
+               lambda j: 3 * 10 ** (3 * env[1].sin(j / 150)))
+    _, variant = f.check(f.queries(G, dtype), dtype, D ** -0.5)
+    assert (variant == "kv4_tile_tcgen05") == tiles
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
@@ -289,3 +324,39 @@ def test_one_key_takes_all_among_values_of_many_sizes(env, form, D, group, dtype
     assert reach.max() > 60 and np.isfinite(out).all()
     assert (np.abs(out - ref) <= tol).all(), np.max(np.abs(out - ref) / tol)
     env[0].mnb_check_device_status()
+
+
+@pytest.mark.parametrize("form,dtype", [(form, dtype) for form in LONG for dtype in ("f16", "f32")])
+def test_a_nan_deep_in_a_long_sequence(env, form, dtype):  # noqa: F811
+    """A value of sequence 1 that is not finite: rows that see it get NaN in its group, all others what they had; a row of q
+    with NaN harms itself alone."""
+    _, torch, dev = env
+    lens, Hk, G, D, group = LONG[form], 8, 4, 128, 32
+    f = Filled(env, 5, D, group, 16, Hk, lens)
+    q, scale = f.queries(G, dtype), float(np.float32(D ** -0.5))
+    clean = f.attend(q, scale)
+    at = lens[1][1] - (400 if form == "prompts" else 2 if form == "verify" else 3000)
+    f.kv[1][1][at, 3, 40] = float("inf")
+    f.store(1)
+    q2 = q.clone()
+    q2[0, 5, 7] = float("nan")
+    got = f.attend(q2, scale)
+    a, (q_len, n) = int(f.start[1]), lens[1]
+    sees = torch.arange(n - q_len, n, device=dev) >= at
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    hit[a: a + q_len, 3 * G: 4 * G, 32:64] = sees[:, None, None]
+    assert 0 < int(sees.sum()) and (form == "decode" or int(sees.sum()) < q_len)
+    hit[0, 5] = True
+    assert torch.isnan(got[hit]).all()
+    assert torch.equal(got[~hit], clean[~hit])
+    env[0].mnb_check_device_status()
+
+
+@pytest.mark.parametrize("dtype,D", [("f16", 128), ("f16", 256), ("f32", 128)])
+@pytest.mark.parametrize("chunk", [40, 512, 1500])
+def test_a_chunk_beside_decode_tokens(env, chunk, dtype, D):  # noqa: F811
+    """A serving batch: one kernel takes all of it, by the average of rows."""
+    lens = [(1, 300 + 61 * i) for i in range(31)] + [(chunk, 3000)] + [(1, 4000 - 77 * i) for i in range(32)]
+    f = Filled(env, D + chunk, D, 128, 16, 4, lens)
+    _, variant = f.check(f.queries(4, dtype), dtype, D ** -0.5)
+    assert (variant == "kv4_tile_tcgen05") == (chunk == 1500 and dtype == "f16" and D == 128)
