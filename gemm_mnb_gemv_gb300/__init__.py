@@ -23,7 +23,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmnb.so")
@@ -616,7 +615,6 @@ def mnb_kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads
 
 
 _default_workspace = {}  # by device: of mnb_kv4_attention's calls on its default stream, 43 MB at most
-_default_workspace_lock = threading.Lock()
 
 
 def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale: float, causal: bool = True,
@@ -625,7 +623,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
 
     ``q_start`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]``, ``page_table`` int32 ``[batch, pages]``.
     Without ``workspace``, calls on the device's default stream share one that is kept (the largest asked for so far, 43 MB
-    at most), and calls on other streams allocate theirs.
+    at most), and calls on other streams allocate theirs. One workspace may serve calls of several threads on one stream.
     """
     torch = _torch()
     if q.dim() != 3:
@@ -665,12 +663,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
             _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
             stride, scale, 1 if causal else 0, window, workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
-    if kept:
-        # A call is two launches, and its workspace is theirs from the first to the second.
-        with _default_workspace_lock:
-            st = lib.mnb_kv4_attention(*args)
-    else:
-        st = lib.mnb_kv4_attention(*args)
+    st = lib.mnb_kv4_attention(*args)
     if st != MNB_OK:
         _raise(st)
     return out

@@ -802,6 +802,10 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
   if (window >= 1 << 30) window = 0;  // no position reaches 2^30: such a window leaves nothing out
   const mnb::Kv4Attention a = {q,     dtype == MNB_F32, T,           q_heads, q_stride,  q_start,  kv_len, page_table, batch,
                                table_stride, scale, causal != 0, window, workspace, ws_bytes, out,   lse};
+  // A call is two launches, and its workspace is theirs from the first to the second: calls of several host threads on
+  // one stream with one workspace have to come one after the other.
+  static std::mutex two_launches;
+  std::lock_guard<std::mutex> lock(two_launches);
   return finish(fn, mnb::launch_kv4_attention(ctx, c, a), ctx);
 }
 

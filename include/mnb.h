@@ -398,7 +398,8 @@ MNB_API mnb_status mnb_kv4_read(mnb_kv4_cache cache, const int64_t *slots, int T
 /*
  * Scratch bytes of mnb_kv4_attention for these shapes (0 for arguments outside its ranges).
  * The size covers GPUs of up to 160 SMs; contents need no initialisation, each call
- * overwrites them, so calls sharing one workspace must be ordered on one stream.
+ * overwrites them, so calls sharing one workspace must be ordered on one stream (from any host
+ * threads: a call's launches are issued together).
  */
 MNB_API size_t mnb_kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim,
                                                  int dtype);

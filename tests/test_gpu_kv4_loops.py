@@ -8,6 +8,8 @@ that the cache holds (which the append and read tests compare bit for bit), with
 """
 from __future__ import annotations
 
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 
@@ -360,3 +362,26 @@ def test_a_chunk_beside_decode_tokens(env, chunk, dtype, D):  # noqa: F811
     f = Filled(env, D + chunk, D, 128, 16, 4, lens)
     _, variant = f.check(f.queries(4, dtype), dtype, D ** -0.5)
     assert (variant == "kv4_tile_tcgen05") == (chunk == 1500 and dtype == "f16" and D == 128)
+
+
+@pytest.mark.parametrize("kept", [True, False])
+def test_threads_share_a_workspace(env, kept):  # noqa: F811
+    """Calls of four host threads on one stream with one workspace: each is two launches, which stay together."""
+    mnb, torch, dev = env
+    need, forms = 0, []
+    for i, lens in enumerate(([(1, 3000), (1, 700)], [(4, 2500)], [(90, 1500)], [(1, 4000)])):
+        f = Filled(env, i, 128, 64, 16, 2, lens)
+        q = f.queries(4, "f16")
+        forms.append((f, q, f.attend(q, 0.09)))
+        need = max(need, mnb.mnb_kv4_attention_workspace_bytes(q.shape[0], len(lens), 8, 2, 128))
+    torch.cuda.synchronize()
+    shared = None if kept else torch.empty(need, dtype=torch.uint8, device=dev)
+
+    def calls(i):
+        f, q, want = forms[i]
+        outs = [mnb.mnb_kv4_attention(q, f.cache, f.start, f.kv_len, f.table, 0.09, workspace=shared) for _ in range(200)]
+        return all(torch.equal(o, want) for o in outs)
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(calls, range(4)))
+    mnb.mnb_check_device_status()
