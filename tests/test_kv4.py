@@ -230,3 +230,85 @@ def test_dequantisers_stop_together():
     assert not re.search(r"\b(break|return|goto)\b", before)
     outs = re.findall(r"(if \([^;{]*\) \{\s*ok = false;\s*)?\b(?:break|return|goto)\b", after)
     assert len(outs) == 1 and outs[0].startswith("if (ksize == kLate)")
+
+
+class _Recorder:
+    """Stands for the library: keeps what the binding hands to an entry point."""
+
+    def __init__(self, lib):
+        self.lib, self.calls = lib, []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.lib, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def binding(lib, monkeypatch):
+    """The binding on tensors that say they lie on GPU `dev`, and a library that keeps the calls."""
+    import torch
+
+    import gemm_mnb_gemv_gb300 as mnb
+
+    class OnGpu(torch.Tensor):
+        dev = 0
+        is_cuda = property(lambda self: True)
+
+        def get_device(self):
+            return self.dev
+
+    def tensor(*shape, dtype=torch.float16, dev=0):
+        t = torch.zeros(shape, dtype=dtype).as_subclass(OnGpu)
+        t.dev = dev
+        return t
+
+    recorder = _Recorder(lib)
+    monkeypatch.setattr(mnb, "load_library", lambda *a: recorder)
+    monkeypatch.setattr(mnb, "_raw_stream", lambda *a, **k: 77)
+    monkeypatch.setattr(mnb, "_new", lambda shape, dtype, device, stream: tensor(*(shape if isinstance(shape, tuple) else (shape,)),
+                                                                                 dtype=dtype))
+    if hasattr(mnb, "_current_device"):
+        monkeypatch.setattr(mnb, "_current_device", lambda: 0)
+    return mnb, torch, tensor, recorder
+
+
+def _binding_cache(binding, **kw):
+    mnb, torch, tensor, _ = binding
+    return mnb.MnbKv4Cache(tensor(4, 2, 1280, dtype=torch.uint8, **kw), 16, 64, 32)
+
+
+def _binding_attention(binding, cache=None, **kw):
+    mnb, torch, tensor, _ = binding
+    i32 = torch.int32
+    a = dict(q=tensor(3, 4, 64), cache=cache or _binding_cache(binding), q_start=tensor(3, dtype=i32), kv_len=tensor(2, dtype=i32),
+             page_table=tensor(2, 5, dtype=i32), scale=0.1)
+    a.update(kw)
+    return mnb.mnb_kv4_attention(**a)
+
+
+@pytest.mark.parametrize("window,handed_on", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                              (2 ** 32, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1)])
+def test_a_window_beyond_32_bits_is_not_cut(binding, window, handed_on):
+    _binding_attention(binding, window=window)
+    name, args = binding[3].calls[-1]
+    assert name == "mnb_kv4_attention" and args[13] == handed_on
+
+
+@pytest.mark.parametrize("window", [-1, -2 ** 32, -2 ** 32 + 9, -2 ** 40])
+def test_a_negative_window_stays_negative(binding, window):
+    _binding_attention(binding, window=window)
+    assert binding[3].calls[-1][1][13] < 0  # the library refuses it
+
+
+def test_sizes_beyond_32_bits_are_refused(binding):
+    mnb, torch, tensor, _ = binding
+    for bad in [(2 ** 32 + 4, 16, 2, 64, 32), (4, 2 ** 32 + 16, 2, 64, 32), (4, 16, 2, 2 ** 32 + 64, 32), (4, 16, 2, 64, 32 - 2 ** 32)]:
+        assert mnb.mnb_kv4_cache_bytes(*bad) == 0
+    with pytest.raises(mnb.MnbError):
+        mnb.MnbKv4Cache(tensor(4, 2, 1280, dtype=torch.uint8), 2 ** 32 + 16, 64, 32)
+    assert mnb.mnb_kv4_attention_workspace_bytes(2 ** 32 + 3, 2, 4, 2, 64) == 0
