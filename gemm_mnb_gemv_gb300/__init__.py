@@ -467,13 +467,18 @@ def mnb_gemm_act_order_noalloc(A, packed, scales, zero_points, perm, K: int, K_p
 _INT_MAX = 2 ** 31 - 1
 
 
-def _int32(n: int) -> int:
+def _nearest(n: int) -> int:
     """``n``, or the C int nearest to it: ctypes would hand on its low 32 bits."""
     return max(-_INT_MAX, min(n, _INT_MAX))
 
 
+def _size(n: int) -> int:
+    """``n`` as a C int, -1 (which every entry point refuses) where it is none."""
+    return n if -_INT_MAX <= n <= _INT_MAX else -1
+
+
 def mnb_kv4_cache_bytes(num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int) -> int:
-    num_pages, page_size, kv_heads, head_dim, group_size = map(_int32, (num_pages, page_size, kv_heads, head_dim, group_size))
+    num_pages, page_size, kv_heads, head_dim, group_size = map(_size, (num_pages, page_size, kv_heads, head_dim, group_size))
     return int(load_library().mnb_kv4_cache_bytes(num_pages, page_size, kv_heads, head_dim, group_size))
 
 
@@ -588,7 +593,7 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
     if cos is not None:
         rows, half = cos.shape
         rope = MnbRope(_index("cos", cos, torch.float32, (rows, half)), _index("sin", sin, torch.float32, (rows, half)),
-                       _int32(rows), _int32(2 * half), 1 if interleaved else 0)
+                       _nearest(rows), _size(2 * half), 1 if interleaved else 0)
         pp = _index("positions", positions, torch.int32, (T,))
     else:
         rope, pp = MnbRope(None, None, 0, 0, 0), None
@@ -620,7 +625,7 @@ def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, 
 
 def mnb_kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads: int, head_dim: int,
                                       dtype: int = MNB_F16) -> int:
-    T, batch, q_heads, kv_heads, head_dim, dtype = map(_int32, (T, batch, q_heads, kv_heads, head_dim, dtype))
+    T, batch, q_heads, kv_heads, head_dim, dtype = map(_size, (T, batch, q_heads, kv_heads, head_dim, dtype))
     return int(load_library().mnb_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, dtype))
 
 
@@ -672,7 +677,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     stride = page_table.shape[1]
     args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
             _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
-            _int32(stride), scale, 1 if causal else 0, _int32(window), workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
+            _size(stride), scale, 1 if causal else 0, _nearest(window), workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
     st = lib.mnb_kv4_attention(*args)
     if st != MNB_OK:
         _raise(st)

@@ -302,7 +302,7 @@ def test_a_window_beyond_32_bits_is_not_cut(binding, window, handed_on):
 @pytest.mark.parametrize("window", [-1, -2 ** 32, -2 ** 32 + 9, -2 ** 40])
 def test_a_negative_window_stays_negative(binding, window):
     _binding_attention(binding, window=window)
-    assert binding[3].calls[-1][1][13] < 0  # the library refuses it
+    assert -2 ** 31 <= binding[3].calls[-1][1][13] < 0  # the library refuses it
 
 
 def test_sizes_beyond_32_bits_are_refused(binding):
