@@ -522,6 +522,8 @@ def _act_dtype(name, t):
     if not _ACT:
         torch = _torch()
         _ACT.update({torch.float16: MNB_F16, torch.float32: MNB_F32})
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor, got None")
     code = _ACT.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
@@ -539,6 +541,8 @@ def _raw_stream(t, stream):
 
 def _token_rows(name, t, heads, D, dtype):
     """Elements between the tokens of ``[T, heads, D]``, whose heads must lie one after the other."""
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor, got None")
     if t.dtype != dtype or not t.is_cuda:
         if not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
@@ -563,6 +567,8 @@ def _new(shape, dtype, device, stream):
 
 def _index(name, t, dtype, shape):
     """Address of a contiguous CUDA tensor of this type and shape."""
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor, got None")
     if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         _check_dev(name, t, dtype)
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -574,8 +580,8 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
     """Rotates, quantises and stores ``k`` and ``v`` (``[T, kv_heads, head_dim]``) at ``slots``; returns the rotated
     ``q`` (or None).  ``cos`` and ``sin`` are fp32 ``[rows, rot_dim / 2]``, None for no rotation."""
     torch = _torch()
-    dtype = k.dtype
     dt, Hk, D = _act_dtype("k", k), cache.kv_heads, cache.head_dim
+    dtype = k.dtype
     ks, vs = _token_rows("k", k, Hk, D, dtype), _token_rows("v", v, Hk, D, dtype)
     T = k.shape[0]
     if v.shape[0] != T:
@@ -590,7 +596,11 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
         if q_out is None:
             q_out = _new((T, Hq, D), dtype, q.device, stream)
         qp, op = q.data_ptr(), _index("q_out", q_out, dtype, (T, Hq, D))
+    if cos is None and sin is not None:
+        raise TypeError("sin without cos")
     if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError(f"cos must be [rows, rot_dim / 2], got {list(cos.shape)}")
         rows, half = cos.shape
         rope = MnbRope(_index("cos", cos, torch.float32, (rows, half)), _index("sin", sin, torch.float32, (rows, half)),
                        _nearest(rows), _size(2 * half), 1 if interleaved else 0)
@@ -607,6 +617,8 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
 def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, stream=None):
     """``(k, v)``, ``[T, kv_heads, head_dim]`` of ``dtype`` (float16 by default): what ``slots`` hold."""
     torch = _torch()
+    if slots is None or slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
     T = slots.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
     if dtype is None:
@@ -641,8 +653,9 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     at most), and calls on other streams allocate theirs. One workspace may serve calls of several threads on one stream.
     """
     torch = _torch()
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, q_heads, head_dim], got {list(q.shape)}")
+    for name, t, dims in (("q", q, 3), ("kv_len", kv_len, 1), ("page_table", page_table, 2)):
+        if t is None or t.dim() != dims:
+            raise ValueError(f"{name} must have {dims} dimensions, got {None if t is None else list(t.shape)}")
     T, Hq, D = q.shape
     dtype, dt = q.dtype, _act_dtype("q", q)
     qs = _token_rows("q", q, Hq, cache.head_dim, dtype)
@@ -672,8 +685,6 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     else:
         op = _index("out", out, dtype, (T, Hq, D))
     lp = None if lse is None else _index("lse", lse, torch.float32, (T, Hq))
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [{B}, pages], got {list(page_table.shape)}")
     stride = page_table.shape[1]
     args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
             _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,

@@ -312,3 +312,43 @@ def test_sizes_beyond_32_bits_are_refused(binding):
     with pytest.raises(mnb.MnbError):
         mnb.MnbKv4Cache(tensor(4, 2, 1280, dtype=torch.uint8), 2 ** 32 + 16, 64, 32)
     assert mnb.mnb_kv4_attention_workspace_bytes(2 ** 32 + 3, 2, 4, 2, 64) == 0
+
+
+def _binding_append(binding, cache=None, **kw):
+    mnb, torch, tensor, _ = binding
+    a = dict(cache=cache or _binding_cache(binding), k=tensor(3, 2, 64), v=tensor(3, 2, 64), slots=tensor(3, dtype=torch.int64),
+             q=tensor(3, 4, 64), positions=tensor(3, dtype=torch.int32), cos=tensor(9, 32, dtype=torch.float32),
+             sin=tensor(9, 32, dtype=torch.float32))
+    a.update(kw)
+    return mnb.mnb_kv4_append(**a)
+
+
+@pytest.mark.parametrize("missing", ["k", "v", "slots", "positions", "sin", "cos"])
+def test_append_says_what_is_missing(binding, missing):
+    _binding_append(binding)
+    calls = len(binding[3].calls)
+    with pytest.raises(TypeError, match=missing):
+        _binding_append(binding, **{missing: None})
+    assert len(binding[3].calls) == calls
+
+
+@pytest.mark.parametrize("missing", ["q", "q_start", "kv_len", "page_table"])
+def test_attention_says_what_is_missing(binding, missing):
+    with pytest.raises((TypeError, ValueError), match=missing):
+        _binding_attention(binding, **{missing: None})
+    assert not binding[3].calls
+
+
+def test_wrong_dimensions_are_named(binding):
+    mnb, torch, tensor, _ = binding
+    with pytest.raises(ValueError, match="cos"):
+        _binding_append(binding, cos=tensor(9, dtype=torch.float32))
+    with pytest.raises(ValueError, match="kv_len"):
+        _binding_attention(binding, kv_len=tensor(2, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="kv_len"):
+        _binding_attention(binding, kv_len=torch.tensor(3))
+    with pytest.raises(ValueError, match="page_table"):
+        _binding_attention(binding, page_table=tensor(5, dtype=torch.int32))
+    with pytest.raises(ValueError, match="slots"):
+        mnb.mnb_kv4_read(_binding_cache(binding), None)
+    assert not binding[3].calls
