@@ -498,7 +498,9 @@ class MnbKv4Cache:
         if need != num_pages * kv_heads * record:
             raise ValueError(f"pages has records of {record} bytes, {need // (num_pages * kv_heads)} needed")
         self.pages, self.page_size, self.head_dim, self.group_size = pages, page_size, head_dim, group_size
-        self.num_pages, self.kv_heads = num_pages, kv_heads
+        self.num_pages, self.kv_heads, self.device = num_pages, kv_heads, pages.get_device()
+        # what tensors and the current device are compared with in each call: 1 to 2 us, for nothing where there is one GPU
+        self.guard = self.device if _gpu_count() > 1 else None
         self.workspace_bytes = {}  # by (tokens, batch, q_heads, dtype)
         self.arg = MnbKv4CacheArg(pages.data_ptr(), num_pages, page_size, kv_heads, head_dim, group_size)
 
@@ -530,23 +532,46 @@ def _act_dtype(name, t):
     return code
 
 
-def _raw_stream(t, stream):
-    """Handle of ``stream``, or of the current stream of ``t``'s device."""
+def _raw_stream(device: int, stream):
+    """Handle of ``stream``, or of the current stream of the device."""
     if stream is not None:
+        if stream.device.index != device:
+            raise ValueError(f"stream is of {stream.device}, the cache on cuda:{device}")
         return stream.cuda_stream
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object: 3 us of a call
-    return raw(t.get_device()) if raw is not None else torch.cuda.current_stream(t.device).cuda_stream
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _token_rows(name, t, heads, D, dtype):
-    """Elements between the tokens of ``[T, heads, D]``, whose heads must lie one after the other."""
-    if t is None:
-        raise TypeError(f"{name} must be a CUDA tensor, got None")
-    if t.dtype != dtype or not t.is_cuda:
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
+def _gpu_count() -> int:
+    return _torch().cuda.device_count()
+
+
+def _current_device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _call_on(device: int, fn, args) -> int:
+    """Calls an entry point, which launches on the current device, with this device as that."""
+    with _torch().cuda.device(device):
+        return fn(*args)
+
+
+def _refuse(name, t, dtype, guard):
+    """Raises for a tensor that is missing, of another type or elsewhere."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if guard is not None and t.get_device() != guard:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{guard}")
+
+
+def _token_rows(name, t, heads, D, dtype, guard):
+    """Elements between the tokens of ``[T, heads, D]``, whose heads must lie one after the other."""
+    if t is None or t.dtype != dtype or not t.is_cuda or guard is not None:
+        _refuse(name, t, dtype, guard)
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {list(shape)}")
@@ -565,13 +590,14 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _index(name, t, dtype, shape):
+def _index(name, t, dtype, shape, guard):
     """Address of a contiguous CUDA tensor of this type and shape."""
-    if t is None:
-        raise TypeError(f"{name} must be a CUDA tensor, got None")
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _check_dev(name, t, dtype)
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or guard is not None:
+        _refuse(name, t, dtype, guard)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
@@ -582,7 +608,8 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
     torch = _torch()
     dt, Hk, D = _act_dtype("k", k), cache.kv_heads, cache.head_dim
     dtype = k.dtype
-    ks, vs = _token_rows("k", k, Hk, D, dtype), _token_rows("v", v, Hk, D, dtype)
+    dev, guard = cache.device, cache.guard
+    ks, vs = _token_rows("k", k, Hk, D, dtype, guard), _token_rows("v", v, Hk, D, dtype, guard)
     T = k.shape[0]
     if v.shape[0] != T:
         raise ValueError(f"v has {v.shape[0]} tokens, k has {T}")
@@ -592,23 +619,25 @@ def mnb_kv4_append(cache: MnbKv4Cache, k, v, slots, q=None, positions=None, cos=
         if q.dim() != 3 or q.shape[0] != T:
             raise ValueError(f"q must be [{T}, q_heads, {D}], got {list(q.shape)}")
         Hq = q.shape[1]
-        qs = _token_rows("q", q, Hq, D, dtype)
+        qs = _token_rows("q", q, Hq, D, dtype, guard)
         if q_out is None:
             q_out = _new((T, Hq, D), dtype, q.device, stream)
-        qp, op = q.data_ptr(), _index("q_out", q_out, dtype, (T, Hq, D))
+        qp, op = q.data_ptr(), _index("q_out", q_out, dtype, (T, Hq, D), guard)
     if cos is None and sin is not None:
         raise TypeError("sin without cos")
     if cos is not None:
         if cos.dim() != 2:
             raise ValueError(f"cos must be [rows, rot_dim / 2], got {list(cos.shape)}")
         rows, half = cos.shape
-        rope = MnbRope(_index("cos", cos, torch.float32, (rows, half)), _index("sin", sin, torch.float32, (rows, half)),
-                       _nearest(rows), _size(2 * half), 1 if interleaved else 0)
-        pp = _index("positions", positions, torch.int32, (T,))
+        rope = MnbRope(_index("cos", cos, torch.float32, (rows, half), guard),
+                       _index("sin", sin, torch.float32, (rows, half), guard), _nearest(rows), _size(2 * half), 1 if interleaved else 0)
+        pp = _index("positions", positions, torch.int32, (T,), guard)
     else:
         rope, pp = MnbRope(None, None, 0, 0, 0), None
-    st = load_library().mnb_kv4_append(qp, k.data_ptr(), v.data_ptr(), dt, T, Hq, qs, ks, vs, pp, rope,
-                                       _index("slots", slots, torch.int64, (T,)), cache.arg, op, _raw_stream(k, stream))
+    args = (qp, k.data_ptr(), v.data_ptr(), dt, T, Hq, qs, ks, vs, pp, rope, _index("slots", slots, torch.int64, (T,), guard),
+            cache.arg, op, _raw_stream(dev, stream))
+    fn = load_library().mnb_kv4_append
+    st = fn(*args) if guard is None or _current_device() == dev else _call_on(dev, fn, args)
     if st != MNB_OK:
         _raise(st)
     return q_out
@@ -620,6 +649,8 @@ def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, 
     if slots is None or slots.dim() != 1:
         raise ValueError("slots must be [tokens]")
     T = slots.shape[0]
+    dev, guard = cache.device, cache.guard
+    slots_at = _index("slots", slots, torch.int64, (T,), guard)
     shape = (T, cache.kv_heads, cache.head_dim)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else torch.float16
@@ -627,9 +658,10 @@ def mnb_kv4_read(cache: MnbKv4Cache, slots, dtype=None, k_out=None, v_out=None, 
         k_out = _new(shape, dtype, slots.device, stream)
     if v_out is None:
         v_out = _new(shape, dtype, slots.device, stream)
-    st = load_library().mnb_kv4_read(cache.arg, _index("slots", slots, torch.int64, (T,)), T,
-                                     _act_dtype("k_out", k_out), _index("k_out", k_out, dtype, shape),
-                                     _index("v_out", v_out, dtype, shape), _raw_stream(slots, stream))
+    args = (cache.arg, slots_at, T, _act_dtype("k_out", k_out), _index("k_out", k_out, dtype, shape, guard),
+            _index("v_out", v_out, dtype, shape, guard), _raw_stream(dev, stream))
+    fn = load_library().mnb_kv4_read
+    st = fn(*args) if guard is None or _current_device() == dev else _call_on(dev, fn, args)
     if st != MNB_OK:
         _raise(st)
     return k_out, v_out
@@ -653,15 +685,16 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     at most), and calls on other streams allocate theirs. One workspace may serve calls of several threads on one stream.
     """
     torch = _torch()
-    for name, t, dims in (("q", q, 3), ("kv_len", kv_len, 1), ("page_table", page_table, 2)):
-        if t is None or t.dim() != dims:
-            raise ValueError(f"{name} must have {dims} dimensions, got {None if t is None else list(t.shape)}")
+    if q is None or kv_len is None or page_table is None or q.dim() != 3 or kv_len.dim() != 1 or page_table.dim() != 2:
+        raise ValueError("q, kv_len and page_table must be [tokens, q_heads, head_dim], [batch] and [batch, pages], got "
+                         + ", ".join("None" if t is None else str(list(t.shape)) for t in (q, kv_len, page_table)))
     T, Hq, D = q.shape
     dtype, dt = q.dtype, _act_dtype("q", q)
-    qs = _token_rows("q", q, Hq, cache.head_dim, dtype)
+    dev, guard = cache.device, cache.guard
+    qs = _token_rows("q", q, Hq, cache.head_dim, dtype, guard)
     B = kv_len.shape[0]
     lib = load_library()
-    raw_stream = _raw_stream(q, stream)
+    raw_stream = _raw_stream(dev, stream)
     kept = workspace is None and stream is None and raw_stream == 0
     if workspace is None:
         need = cache.workspace_bytes.get((T, B, Hq, dt))
@@ -672,24 +705,28 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
         if kept:
             # The default stream is never destroyed, orders all its calls and can't be captured, so one workspace serves
             # them in turn: 16 us a call of one token over 1000 keys against 20 us with one allocated in each.
-            workspace = _default_workspace.get(q.get_device())
+            workspace = _default_workspace.get(dev)
             if workspace is None or workspace.numel() < need:
-                workspace = _default_workspace[q.get_device()] = _new(need, torch.uint8, q.device, None)
+                workspace = _default_workspace[dev] = _new(need, torch.uint8, q.device, None)
         else:
             workspace = _new(need, torch.uint8, q.device, stream)
     else:
         _check_dev("workspace", workspace)
+        if guard is not None:
+            _refuse("workspace", workspace, workspace.dtype, guard)
     if out is None:
         out = _new((T, Hq, D), dtype, q.device, stream)
         op = out.data_ptr()
     else:
-        op = _index("out", out, dtype, (T, Hq, D))
-    lp = None if lse is None else _index("lse", lse, torch.float32, (T, Hq))
+        op = _index("out", out, dtype, (T, Hq, D), guard)
+    lp = None if lse is None else _index("lse", lse, torch.float32, (T, Hq), guard)
     stride = page_table.shape[1]
-    args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,)),
-            _index("kv_len", kv_len, torch.int32, (B,)), _index("page_table", page_table, torch.int32, (B, stride)), B,
-            _size(stride), scale, 1 if causal else 0, _nearest(window), workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
-    st = lib.mnb_kv4_attention(*args)
+    args = (q.data_ptr(), dt, T, Hq, qs, cache.arg, _index("q_start", q_start, torch.int32, (B + 1,), guard),
+            _index("kv_len", kv_len, torch.int32, (B,), guard),
+            _index("page_table", page_table, torch.int32, (B, stride), guard), B, _size(stride), scale, 1 if causal else 0,
+            _nearest(window), workspace.data_ptr(), workspace.nbytes, op, lp, raw_stream)
+    fn = lib.mnb_kv4_attention
+    st = fn(*args) if guard is None or _current_device() == dev else _call_on(dev, fn, args)
     if st != MNB_OK:
         _raise(st)
     return out

@@ -272,8 +272,8 @@ def binding(lib, monkeypatch):
     monkeypatch.setattr(mnb, "_raw_stream", lambda *a, **k: 77)
     monkeypatch.setattr(mnb, "_new", lambda shape, dtype, device, stream: tensor(*(shape if isinstance(shape, tuple) else (shape,)),
                                                                                  dtype=dtype))
-    if hasattr(mnb, "_current_device"):
-        monkeypatch.setattr(mnb, "_current_device", lambda: 0)
+    monkeypatch.setattr(mnb, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(mnb, "_gpu_count", lambda: 2, raising=False)
     return mnb, torch, tensor, recorder
 
 
@@ -352,3 +352,66 @@ def test_wrong_dimensions_are_named(binding):
     with pytest.raises(ValueError, match="slots"):
         mnb.mnb_kv4_read(_binding_cache(binding), None)
     assert not binding[3].calls
+
+
+APPEND = ["k", "v", "slots", "q", "positions", "cos", "sin", "q_out"]
+ATTENTION = ["q", "q_start", "kv_len", "page_table", "out", "lse", "workspace"]
+READ = ["slots", "k_out", "v_out"]
+
+
+def _tensors(binding, dev):
+    """Arguments of the three entry points on GPU `dev`."""
+    _, torch, tensor, _ = binding
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    t = lambda *s, d=torch.float16: tensor(*s, dtype=d, dev=dev)  # noqa: E731
+    return (dict(k=t(3, 2, 64), v=t(3, 2, 64), slots=t(3, d=i64), q=t(3, 4, 64), positions=t(3, d=i32), cos=t(9, 32, d=f32),
+                 sin=t(9, 32, d=f32), q_out=t(3, 4, 64)),
+            dict(q=t(3, 4, 64), q_start=t(3, d=i32), kv_len=t(2, d=i32), page_table=t(2, 5, d=i32), out=t(3, 4, 64),
+                 lse=t(3, 4, d=f32), workspace=t(1 << 20, d=torch.uint8)),
+            dict(slots=t(3, d=i64), k_out=t(3, 2, 64), v_out=t(3, 2, 64)))
+
+
+@pytest.mark.parametrize("call,name", [(i, n) for i, names in enumerate((APPEND, ATTENTION, READ)) for n in names])
+def test_tensors_of_another_gpu_are_refused(binding, call, name):
+    mnb, torch, tensor, recorder = binding
+    cache = _binding_cache(binding)
+    fn = (mnb.mnb_kv4_append, mnb.mnb_kv4_attention, mnb.mnb_kv4_read)[call]
+    own, other = _tensors(binding, 0)[call], _tensors(binding, 1)[call]
+    more = dict(scale=0.1) if call == 1 else {}
+    fn(cache=cache, **own, **more)
+    assert len(recorder.calls) == 1
+    with pytest.raises(ValueError, match=f"{name} is on .*the cache on cuda:0"):
+        fn(cache=cache, **{**own, name: other[name]}, **more)
+    assert len(recorder.calls) == 1
+
+
+@pytest.mark.parametrize("call", [0, 1, 2])
+def test_calls_run_on_the_gpu_of_their_cache(binding, call, monkeypatch):
+    """The library launches on the current device: it is the cache's during the call, and no other call changes it."""
+    import contextlib
+    mnb, torch, tensor, recorder = binding
+    entered = []
+
+    @contextlib.contextmanager
+    def device(index):
+        entered.append((index, len(recorder.calls)))
+        yield
+        entered.append(("left", len(recorder.calls)))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    fn = (mnb.mnb_kv4_append, mnb.mnb_kv4_attention, mnb.mnb_kv4_read)[call]
+    more = dict(scale=0.1) if call == 1 else {}
+    fn(cache=_binding_cache(binding, dev=1), **_tensors(binding, 1)[call], **more)
+    assert entered == [(1, 0), ("left", 1)]
+    fn(cache=_binding_cache(binding), **_tensors(binding, 0)[call], **more)
+    assert len(entered) == 2 and len(recorder.calls) == 2
+
+
+def test_a_stream_of_another_gpu_is_refused(lib):
+    from types import SimpleNamespace
+
+    import gemm_mnb_gemv_gb300 as mnb
+    stream = SimpleNamespace(device=SimpleNamespace(index=1), cuda_stream=5)
+    assert mnb._raw_stream(1, stream) == 5
+    with pytest.raises(ValueError, match="stream"):
+        mnb._raw_stream(0, stream)
