@@ -80,11 +80,11 @@ struct Layout {
   }
 };
 
-// CTAs an SM holds: by registers (128, 168 or 255 a thread).
+// CTAs an SM holds: by registers (128, 168 or 255 a thread), and with heads of 256 by two stages of shared memory.
 template <int D, int NT, bool F32>
 constexpr int stream_ctas() {
   constexpr int o_regs = D / 4 * NT;
-  return o_regs <= 32 ? (F32 ? 3 : 4) : o_regs <= 64 ? 3 : 2;
+  return o_regs <= 32 ? (F32 ? 3 : 4) : o_regs <= 64 && D < 256 ? 3 : 2;
 }
 
 // Cache blocks (of 16 keys) that a warp takes at a time: two where registers hold their scores, for
@@ -755,6 +755,7 @@ cudaError_t launch_stream(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention&
   constexpr int PB = step_blocks<D, NT>();
   using L = Layout<D, NG, NT, PB, F32>;
   constexpr int smem = L::kFixed + kWarps * L::stages(227 * 1024 / per_sm - 1024) * PB * L::kBlock;
+  static_assert((smem + 1024) * per_sm <= 228 * 1024, "the SM holds so many CTAs (each with 1 KB of the system's)");
   auto kern = kv4_stream_kernel<D, NG, NT, F32>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kern, smem, ctx.device, done);
