@@ -7,9 +7,11 @@
 // elements a lane, which are one 32-bit K word (or two 16-bit halves of V words), the rotation's
 // partners by a second load that hits L1, extrema by shuffles over a group's 4-16 lanes. The
 // passes' loads are all issued before the token's position is waited for.
-// Bound: HBM bytes of q, k, v, q_out, and close behind them the instructions of the conversion (the
-// first form, one pass shape for q, k and v, took 177 us for appending and reading 16381 tokens of 32 / 8 heads of
-// 128, this one 130 us; the bytes alone would be 66 us). Append alone is 104 us at 3.1 TB/s, 4490 warp instructions a token.
+// Measured, 16381 tokens of 32 / 8 heads of 128, graph replays: fp16 append 95.6 us, read 29.3 (their bytes alone 53.2 and 12.5); fp32
+// 121 and 35.5 (103 and 22.4). The first form, one pass shape for q, k and v, took 177 us for both in fp16.
+// Bound, fp16 append: neither bytes (3.4 TB/s) nor issue alone: 67.8 M warp instructions (4140 a token) fill 58% of the issue slots,
+// and 16 warps an SM (128 registers) leave the rest to fixed latencies and loads. The fp32 append is bound by its bytes.
+// Read: one block for four tokens; slot, code and store one after the other, without a second round to hide behind.
 #include <type_traits>
 
 #include "kv4.cuh"

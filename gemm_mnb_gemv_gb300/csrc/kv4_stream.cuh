@@ -25,9 +25,12 @@
 // ring of bulk copies (16 D + 128 ng bytes a block) that runs ahead across the ends of sequences; the
 // warps meet only at a sequence's end.  Pieces of a sequence cut by a range's end go to the workspace
 // as (m, l, o) and a second, dependent launch joins them in order.
-// Bound: issue (about 320 instructions a block of 16 keys, ALU pipe 48%, four warps a scheduler). Measured at 32 / 8 heads of
-// 128: 64 ragged contexts of up to 8192 keys 77 us (3.8 TB/s; the bytes alone 43 us), one of 131071 keys 47 us, one of
-// 1000 keys 14.5 us (launch, lengths, page, block and join one after the other).
+// Bound: issue with four warps a scheduler (0.56 instructions a cycle, about 320 a block of 16 keys, ALU pipe 49%); at 128 registers
+// 132 to 400 bytes a thread are spilled, 0.6% of the instructions. Measured at 32 / 8 heads of 128, graph replays: 64 ragged contexts of
+// up to 8192 keys 74 us (3.9 TB/s; the bytes alone 43 us), one of 131071 keys 44 us, one of 1000 keys 11 us (launch,
+// lengths, page, block and join one after the other); with heads of 256 64 contexts 119 us (86), fp32 101 us (heads of 128) and 186 (256).
+// Every 16 rows read and convert the visible cache again: prompts of heads of 256 and of fp32, which no other kernel takes, are slow here
+// (two prompts of up to 2048: 530 and 423 us; their products alone 34 and 17).
 #pragma once
 
 #include <type_traits>

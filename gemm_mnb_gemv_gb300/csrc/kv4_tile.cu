@@ -29,8 +29,9 @@
 // Fewer bits: K, V and P are each rounded once to fp16, as the result is; the error (norm, against fp64) is 3.8e-4 to 4.5e-4,
 // of which the result's own rounding is 2.1e-4. Keeping the codes exact would take a multiplication of each score and each
 // probability by its key's scale, in the softmax, whose instructions the kernel has least to spare of.
-// Measured: 2048 tokens over 32768 keys, 32 / 8 heads of 128: 805 to 817 us, 1.3 PFLOP/s, 67% of the measured peak; without
-// the conversion 704 us, without the softmax 685 us, without either 637 us. Two prompts of up to 2048: 78 us.
+// Measured, graph replays: 2048 tokens over 32768 keys, 32 / 8 heads of 128: 850 us, 1.25 PFLOP/s, 64% of the measured peak (an earlier
+// conversion: 817; without it 704 us, without the softmax 685 us, without either 637 us). Two prompts of up to 2048: 77 us.
+// Where the compiler places the roles' code alone moves the chunk by up to 10%.
 // Work is cut and joined as in the streaming kernel (kv4_work.cuh), so a few rows over a long context
 // use every SM too.
 #include <type_traits>
@@ -44,7 +45,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kRows = 256, kKeys = 128, kThreads = 512;
-constexpr int kCost = 3;   // tiles that a piece's start and end cost: 2: 50 and 86 us (16 drafted tokens over 32768 keys; prompts), 3: 47 and 85 (now 45 and 78)
+constexpr int kCost = 3;   // tiles that a piece's start and end cost: 2: 50 and 86 us (16 drafted tokens over 32768 keys; prompts), 3: 47 and 85 (now 43 and 77)
 constexpr int kBufs = 3;   // K / V operand buffers
 constexpr int kMeta = 4;   // tiles whose flags are kept
 constexpr uint32_t kLate = 0xffffffffu;  // in a size's place: this warp's wait gave up
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return fmaxf(max3(t0, v[62], v[63]), t1);
         };
         // Most loops that could be unrolled are not: the four roles' code has to stay in the instruction cache together (a chunk
-        // of 2048 over 32768 keys: 805 us; with this loop unrolled too 878, with the one below rolled 921).
+        // of 2048 over 32768 keys, when this was chosen: 805 us; with this loop unrolled too 878, with the one below rolled 921).
         float top = -INFINITY;
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
