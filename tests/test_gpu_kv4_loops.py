@@ -385,3 +385,28 @@ def test_threads_share_a_workspace(env, kept):  # noqa: F811
     with ThreadPoolExecutor(4) as pool:
         assert all(pool.map(calls, range(4)))
     mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", LONG)
+def test_strided_q_and_programmatic_launch_of_several_pieces(env, form, D, dtype):  # noqa: F811
+    """q as a view of a fused product whose other columns are NaN, calls launched before the last has ended: as with q by
+    itself, one call after the other."""
+    mnb, torch, dev = env
+    f = Filled(env, D, D, 64, 16, 4, LONG[form])
+    q = f.queries(5, dtype)
+    T = q.shape[0]
+    plain = f.attend(q, 0.07)
+    torch.cuda.synchronize()
+    fused = torch.full((T, 28 * D), float("nan"), dtype=q.dtype, device=dev)
+    view = fused[:, 4 * D: 24 * D].view(T, 20, D)
+    mnb.mnb_set_programmatic_launch(True)
+    try:
+        view.copy_(q)
+        outs = [f.attend(view, 0.07) for _ in range(6)]
+    finally:
+        mnb.mnb_set_programmatic_launch(False)
+    torch.cuda.synchronize()
+    assert torch.isfinite(plain).all() and all(torch.equal(o, plain) for o in outs)
+    mnb.mnb_check_device_status()
