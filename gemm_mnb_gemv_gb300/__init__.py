@@ -14,6 +14,7 @@ The names match the C entry points: ``mnb_dequant``, ``mnb_repacked_bytes``,
 ``mnb_act_order_workspace_bytes``, ``mnb_gemm_act_order``, ``mnb_gemm_act_order_noalloc``,
 ``mnb_kv4_cache_bytes``, ``mnb_kv4_append``, ``mnb_kv4_read``, ``mnb_kv4_attention_workspace_bytes``,
 ``mnb_kv4_attention`` (with ``MnbKv4Cache``, the handle of a cache, and ``mnb_kv4_cache_alloc``),
+``mnb_lora`` (with ``MnbLoraPool``, the handle of a layer's adapters), ``mnb_softmax``, ``mnb_verify``,
 ``mnb_set_programmatic_launch``,
 ``mnb_check_device_status``,
 ``mnb_last_error``,
@@ -56,6 +57,11 @@ class MnbRope(ctypes.Structure):
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class MnbLoraPoolArg(ctypes.Structure):
+    _fields_ = [("down", ctypes.c_void_p), ("up", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -96,6 +102,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mnb_kv4_attention_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int, c_int, c_int]),
         "mnb_kv4_attention": (c_int, [vp, c_int, c_int, c_int, i64, MnbKv4CacheArg, vp, vp, vp, c_int, c_int,
                                       ctypes.c_float, c_int, c_int, vp, c_size, vp, vp, vp]),
+        "mnb_lora": (c_int, [vp, c_int, c_int, c_int, i64, MnbLoraPoolArg, vp, vp, i64, c_int, vp, i64, vp]),
+        "mnb_softmax": (c_int, [vp, c_int, c_int, c_int, i64, vp, vp, vp]),
+        "mnb_verify": (c_int, [vp, i64, vp, i64, vp, vp, vp, vp, c_int, c_int, c_int, vp, vp, vp]),
         "mnb_set_programmatic_launch": (None, [c_int]),
         "mnb_check_device_status": (c_int, []),
         "mnb_selftest_wait_timeout": (c_int, [ctypes.c_uint, vp]),
@@ -730,3 +739,147 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
     if st != MNB_OK:
         _raise(st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# What each request of a shared step has of its own: adapters, probabilities, drafted tokens
+# ---------------------------------------------------------------------------
+
+
+def _device_of(name, t):
+    """``(device, guard)`` of the tensor that a call goes by: the guard is None where there is one GPU."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
+    dev = t.get_device()
+    return dev, dev if _gpu_count() > 1 else None
+
+
+def _on(name, t, dtype, guard):
+    """Raises for a tensor that is missing, of another type or on another GPU than the call's."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if guard is not None and t.get_device() != guard:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{guard}")
+
+
+def _matrix(name, t, rows, cols, dtype, guard):
+    """Elements between the rows of a CUDA tensor ``[rows, cols]`` whose rows are contiguous."""
+    _on(name, t, dtype, guard)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {[rows, cols]}, got {list(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must lie one after the other")
+    return s0 if rows > 1 else cols
+
+
+def _vector(name, t, dtype, shape, guard):
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    _on(name, t, dtype, guard)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_of(dev, stream):
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream is of {stream.device}, the tensors on cuda:{dev}")
+    return _raw_stream(dev, stream)
+
+
+def _launch(fn, args, dev, guard):
+    st = fn(*args) if guard is None or _current_device() == dev else _call_on(dev, fn, args)
+    if st != MNB_OK:
+        _raise(st)
+
+
+class MnbLoraPool:
+    """Handle of a layer's low-rank adapters: ``down`` fp16 ``[count, max_rank, K]``, ``up`` fp16 ``[count, N, max_rank]``,
+    ``ranks`` int32 ``[count]`` (None: all ``max_rank``), ``scales`` fp32 ``[count]`` (None: 1)."""
+
+    def __init__(self, down, up, ranks=None, scales=None):
+        torch = _torch()
+        self.device, self.guard = _device_of("down", down)
+        if down.dim() != 3 or not isinstance(up, torch.Tensor) or up.dim() != 3:
+            raise ValueError("down and up must be [count, max_rank, K] and [count, N, max_rank]")
+        count, max_rank, self.K = down.shape
+        self.N = up.shape[1]
+        if count < 1 or count > 1 << 20 or max_rank % 8 or not 8 <= max_rank <= 128:
+            raise MnbError(MNB_ERR_INVALID_ARG, f"MnbLoraPool: count={count} max_rank={max_rank} (count 1..2^20, max_rank a "
+                           "multiple of 8 in 8..128)")
+        self.down, self.up, self.ranks, self.scales = down, up, ranks, scales
+        self.arg = MnbLoraPoolArg(
+            _vector("down", down, torch.float16, (count, max_rank, self.K), self.guard),
+            _vector("up", up, torch.float16, (count, self.N, max_rank), self.guard),
+            None if ranks is None else _vector("ranks", ranks, torch.int32, (count,), self.guard),
+            None if scales is None else _vector("scales", scales, torch.float32, (count,), self.guard), count, max_rank)
+
+
+def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, out=None, stream=None):
+    """``[M, N]`` = ``base`` (None: zeros) + each row's adapter on ``x`` ``[M, K]``; ``adapter`` int32 ``[M]``, -1 for none.
+    ``out`` may be ``base``."""
+    torch = _torch()
+    dev, guard = pool.device, pool.guard
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"x must be [M, {pool.K}]")
+    M, K, N, dtype, dt = x.shape[0], pool.K, pool.N, x.dtype, _act_dtype("x", x)
+    xs = _matrix("x", x, M, K, dtype, guard)
+    bs = 0 if base is None else _matrix("base", base, M, N, dtype, guard)
+    if out is None:
+        out = _new((M, N), dtype, x.device, stream)
+    os_ = _matrix("out", out, M, N, dtype, guard)
+    args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard),
+            None if base is None else base.data_ptr(), bs, _size(N), out.data_ptr(), os_, _stream_of(dev, stream))
+    _launch(load_library().mnb_lora, args, dev, guard)
+    return out
+
+
+def mnb_softmax(logits, temperature=None, out=None, stream=None):
+    """fp32 ``[rows, V]``: softmax of ``logits / temperature`` (fp32 ``[rows]``, None: 1; 0: 1 at the largest logit)."""
+    torch = _torch()
+    dev, guard = _device_of("logits", logits)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, V], got {list(logits.shape)}")
+    (rows, V), dt = logits.shape, _act_dtype("logits", logits)
+    stride = _matrix("logits", logits, rows, V, logits.dtype, guard)
+    if out is None:
+        out = _new((rows, V), torch.float32, logits.device, stream)
+    args = (logits.data_ptr(), dt, _size(rows), _size(V), stride,
+            None if temperature is None else _vector("temperature", temperature, torch.float32, (rows,), guard),
+            _vector("out", out, torch.float32, (rows, V), guard), _stream_of(dev, stream))
+    _launch(load_library().mnb_softmax, args, dev, guard)
+    return out
+
+
+def mnb_verify(target, draft, draft_tokens, draft_start, u_accept, u_next, tokens=None, accepted=None, stream=None):
+    """``(tokens, accepted)``: int32 ``[drafted + batch]`` in the order of ``target``'s rows (a sequence's accepted tokens, the
+    next one, then -1) and int32 ``[batch]``.
+
+    ``target`` fp32 ``[drafted + batch, V]``, ``draft`` fp32 ``[drafted, V]`` or None (each row 1 at its token),
+    ``draft_tokens`` int32 and ``u_accept`` fp32 ``[drafted]``, ``draft_start`` int32 ``[batch + 1]``, ``u_next`` fp32 ``[batch]``.
+    """
+    torch = _torch()
+    dev, guard = _device_of("target", target)
+    if target.dim() != 2 or any(not isinstance(t, torch.Tensor) or t.dim() != 1 for t in (draft_tokens, u_next)):
+        raise ValueError("target, draft_tokens and u_next must be [drafted + batch, V], [drafted] and [batch]")
+    D, B, V = draft_tokens.shape[0], u_next.shape[0], target.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    ts = _matrix("target", target, D + B, V, f32, guard)
+    ds = 0 if draft is None else _matrix("draft", draft, D, V, f32, guard)
+    if tokens is None:
+        tokens = _new((D + B,), i32, target.device, stream)
+    if accepted is None:
+        accepted = _new((B,), i32, target.device, stream)
+    args = (target.data_ptr(), ts, None if draft is None else draft.data_ptr(), ds,
+            _vector("draft_tokens", draft_tokens, i32, (D,), guard), _vector("draft_start", draft_start, i32, (B + 1,), guard),
+            _vector("u_accept", u_accept, f32, (D,), guard), _vector("u_next", u_next, f32, (B,), guard), _size(B), _size(D),
+            _size(V), _vector("tokens", tokens, i32, (D + B,), guard), _vector("accepted", accepted, i32, (B,), guard),
+            _stream_of(dev, stream))
+    _launch(load_library().mnb_verify, args, dev, guard)
+    return tokens, accepted

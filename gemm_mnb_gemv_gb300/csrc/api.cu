@@ -810,3 +810,119 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------------------------
+// What each request has of its own: adapters, probabilities, drafted tokens.
+// ------------------------------------------------------------------------------------
+
+namespace {
+
+// Rows of `cols` elements that lie `stride` elements apart; each at 16 bytes when `whole` is set.
+mnb_status check_rows(const char* fn, const char* name, int64_t stride, int cols, int bytes, bool whole) {
+  if (stride < cols || stride > (int64_t)1 << 40)
+    return fail(MNB_ERR_INVALID_ARG, "%s: %s=%lld is below rows of %d elements", fn, name, (long long)stride, cols);
+  if (whole && stride * bytes % 16 != 0)
+    return fail(MNB_ERR_MISALIGNED, "%s: %s=%lld elements is not a multiple of 16 bytes", fn, name, (long long)stride);
+  return MNB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mnb_status mnb_lora(const void* x, int dtype, int M, int K, int64_t x_stride, mnb_lora_pool pool, const int32_t* adapter,
+                    const void* base, int64_t base_stride, int N, void* out, int64_t out_stride, mnb_stream stream) {
+  const char* fn = "mnb_lora";
+  mnb_status st;
+  if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
+  if (M < 0 || M > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: M=%d must be in [0, 2^20]", fn, M);
+  if (K < 16 || K > kMaxKN || K % 16 != 0)
+    return fail(MNB_ERR_INVALID_ARG, "%s: K=%d must be a multiple of 16 in [16, 2^24]", fn, K);
+  if (N < 1 || N > kMaxKN) return fail(MNB_ERR_INVALID_ARG, "%s: N=%d must be in [1, 2^24]", fn, N);
+  if (pool.count < 1 || pool.count > kMaxM)
+    return fail(MNB_ERR_INVALID_ARG, "%s: pool.count=%d must be in [1, 2^20]", fn, pool.count);
+  if (pool.max_rank < 8 || pool.max_rank > 128 || pool.max_rank % 8 != 0)
+    return fail(MNB_ERR_INVALID_ARG, "%s: pool.max_rank=%d must be a multiple of 8 in [8, 128]", fn, pool.max_rank);
+  if (M == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  const int e = dtype == MNB_F16 ? 2 : 4;
+  if ((st = check_ptr(fn, "x", x)) != MNB_OK) return st;
+  if ((st = check_rows(fn, "x_stride", x_stride, K, e, true)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "pool.down", pool.down)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "pool.up", pool.up)) != MNB_OK) return st;
+  if (pool.ranks && (st = check_ptr(fn, "pool.ranks", pool.ranks)) != MNB_OK) return st;
+  if (pool.scales && (st = check_ptr(fn, "pool.scales", pool.scales)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "adapter", adapter)) != MNB_OK) return st;
+  if (base) {
+    if ((st = check_ptr(fn, "base", base)) != MNB_OK) return st;
+    if ((st = check_rows(fn, "base_stride", base_stride, N, e, false)) != MNB_OK) return st;
+    if (base == out && base_stride != out_stride)
+      return fail(MNB_ERR_INVALID_ARG, "%s: base is out, so base_stride=%lld must be out_stride=%lld", fn,
+                  (long long)base_stride, (long long)out_stride);
+  }
+  if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
+  if ((st = check_rows(fn, "out_stride", out_stride, N, e, false)) != MNB_OK) return st;
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  const mnb::Lora a = {x,       dtype == MNB_F32, M,           K,          x_stride, pool.down,     pool.up,
+                       pool.ranks, pool.scales,   pool.count,  pool.max_rank, adapter, base,     base_stride,
+                       N,       out,              out_stride};
+  return finish(fn, mnb::launch_lora(ctx, a), ctx);
+}
+
+mnb_status mnb_softmax(const void* logits, int dtype, int rows, int V, int64_t stride, const float* temperature, float* out,
+                       mnb_stream stream) {
+  const char* fn = "mnb_softmax";
+  mnb_status st;
+  if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
+  if (rows < 0 || rows > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: rows=%d must be in [0, 2^20]", fn, rows);
+  if (V < 1 || V > kMaxKN) return fail(MNB_ERR_INVALID_ARG, "%s: V=%d must be in [1, 2^24]", fn, V);
+  if (rows == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  if ((st = check_ptr(fn, "logits", logits)) != MNB_OK) return st;
+  if ((st = check_rows(fn, "stride", stride, V, 4, false)) != MNB_OK) return st;
+  if (temperature && (st = check_ptr(fn, "temperature", temperature)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  const mnb::Softmax a = {logits, dtype == MNB_F32, rows, V, stride, temperature, out};
+  return finish(fn, mnb::launch_softmax(ctx, a), ctx);
+}
+
+mnb_status mnb_verify(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                      const int32_t* draft_tokens, const int32_t* draft_start, const float* u_accept, const float* u_next,
+                      int batch, int drafted, int V, int32_t* tokens, int32_t* accepted, mnb_stream stream) {
+  const char* fn = "mnb_verify";
+  mnb_status st;
+  if (batch < 0 || batch > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: batch=%d must be in [0, 2^20]", fn, batch);
+  if (drafted < 0 || drafted > kMaxM || (drafted > 0 && batch == 0))
+    return fail(MNB_ERR_INVALID_ARG, "%s: drafted=%d must be in [0, 2^20], and 0 without sequences", fn, drafted);
+  if (V < 1 || V > kMaxKN) return fail(MNB_ERR_INVALID_ARG, "%s: V=%d must be in [1, 2^24]", fn, V);
+  if (batch == 0) {
+    g_last_error.clear();
+    return MNB_OK;
+  }
+  if ((st = check_ptr(fn, "target", target)) != MNB_OK) return st;
+  if ((st = check_rows(fn, "target_stride", target_stride, V, 4, false)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "draft_start", draft_start)) != MNB_OK) return st;
+  if (drafted > 0) {
+    if (draft && (st = check_ptr(fn, "draft", draft)) != MNB_OK) return st;
+    if (draft && (st = check_rows(fn, "draft_stride", draft_stride, V, 4, false)) != MNB_OK) return st;
+    if ((st = check_ptr(fn, "draft_tokens", draft_tokens)) != MNB_OK) return st;
+    if ((st = check_ptr(fn, "u_accept", u_accept)) != MNB_OK) return st;
+  }
+  if ((st = check_ptr(fn, "u_next", u_next)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "tokens", tokens)) != MNB_OK) return st;
+  if ((st = check_ptr(fn, "accepted", accepted)) != MNB_OK) return st;
+  mnb::LaunchCtx ctx;
+  if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
+  const mnb::Verify a = {target, target_stride, draft, draft_stride, draft_tokens, draft_start, u_accept,
+                         u_next, batch,         drafted, V,          tokens,       accepted};
+  return finish(fn, mnb::launch_verify(ctx, a), ctx);
+}
+
+}  // extern "C"

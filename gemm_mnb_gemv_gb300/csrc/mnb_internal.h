@@ -149,6 +149,45 @@ cudaError_t launch_kv4_read(LaunchCtx& ctx, const Kv4Cache& c, const int64_t* sl
 cudaError_t launch_kv4_attention(LaunchCtx& ctx, const Kv4Cache& c, const Kv4Attention& a);
 size_t kv4_attention_workspace_bytes(int T, int batch, int q_heads, int kv_heads, int head_dim, int f32);
 
+// Low-rank adapters beside a product (mnb.h).
+struct Lora {
+  const void* x;
+  int f32, M, K;
+  int64_t x_stride;
+  const void *down, *up;
+  const int32_t* ranks;
+  const float* scales;
+  int count, max_rank;
+  const int32_t* adapter;
+  const void* base;
+  int64_t base_stride;
+  int N;
+  void* out;
+  int64_t out_stride;
+};
+cudaError_t launch_lora(LaunchCtx& ctx, const Lora& a);
+
+// Probabilities and verification of drafted tokens (mnb.h).
+struct Softmax {
+  const void* logits;
+  int f32, rows, V;
+  int64_t stride;
+  const float* temperature;
+  float* out;
+};
+struct Verify {
+  const float* target;
+  int64_t target_stride;
+  const float* draft;
+  int64_t draft_stride;
+  const int32_t *tokens, *start;
+  const float *u_accept, *u_next;
+  int batch, drafted, V;
+  int32_t *out, *accepted;
+};
+cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a);
+cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a);
+
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device: `done` is a static of the caller,
 // a bit for each device.
 template <typename Kern>
@@ -176,6 +215,36 @@ cudaError_t launch_kernel(LaunchCtx& ctx, Kern kernel, dim3 grid, dim3 block, si
   cfg.attrs = attr;
   cfg.numAttrs = ctx.pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The same for a grid of thread-block clusters of `cluster` CTAs.  Sizes above 8 need the kernel's
+// NonPortableClusterSizeAllowed attribute (allow_wide_clusters).
+template <typename Kern, typename... Args>
+cudaError_t launch_clusters(LaunchCtx& ctx, Kern kernel, int cluster, dim3 grid, dim3 block, size_t smem, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctx.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename Kern>
+cudaError_t allow_wide_clusters(Kern kernel, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace mnb

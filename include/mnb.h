@@ -431,6 +431,68 @@ MNB_API mnb_status mnb_kv4_attention(const void *q, int dtype, int T, int q_head
                                      float *lse, mnb_stream stream);
 
 /*
+ * ---- What each request of a shared step has of its own ----
+ *
+ * Requests that share the 4-bit products of a decode, verify or prefill step may each have a low-rank adapter, a
+ * temperature and drafted tokens. The pages have no counterpart: these entry points are this library's own.
+ */
+
+/* Low-rank adapters of one layer, in one pool: adapter i is down[i] (fp16 [max_rank, K]) and up[i] (fp16 [N, max_rank]), of
+ * which the first ranks[i] rows of down and columns of up count (the rest is not used, whatever it holds). */
+typedef struct {
+    const void *down;      /* fp16 [count, max_rank, K]                                  */
+    const void *up;        /* fp16 [count, N, max_rank]                                  */
+    const int32_t *ranks;  /* int32 [count], held to 0..max_rank; NULL: all max_rank      */
+    const float *scales;   /* fp32 [count]; NULL: 1                                      */
+    int32_t count;         /* 1 .. 2^20                                                  */
+    int32_t max_rank;      /* a multiple of 8 in 8 .. 128                                */
+} mnb_lora_pool;
+
+/*
+ * out[m] = base[m] + scales[a] * up[a] . (down[a] . x[m]), a = adapter[m], for M rows of any adapters in any order (rows of one
+ * adapter that lie near each other share its loads). Beside a product of this section's kind, base is that product's Y.
+ * x [M, K], base and out [M, N] are of `dtype` (MNB_F16 or MNB_F32), rows *_stride elements apart (views of one fused
+ * product do); x_stride is a multiple of 16 bytes (else MNB_ERR_MISALIGNED), K of 16 elements. base may be out
+ * (with the same stride; it may not overlap it otherwise) or NULL, which counts as zeros. adapter is int32 [M]: a negative one
+ * leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
+ * Products and sums are fp32. MNB_F16: down . x is rounded to fp16 relative to the row's largest (2^-11), as the result is;
+ * MNB_F32: x and down . x enter the products with 22 bits or more. A row of x with inf or NaN gives non-finite outputs in that row.
+ * M = 0 is valid and does nothing.
+ */
+MNB_API mnb_status mnb_lora(const void *x, int dtype, int M, int K, int64_t x_stride, mnb_lora_pool pool,
+                            const int32_t *adapter, const void *base, int64_t base_stride, int N, void *out,
+                            int64_t out_stride, mnb_stream stream);
+
+/*
+ * Probabilities: out[r, j] = e^((x[r, j] - max_j x) / temperature[r]) / sum_j, fp32 [rows, V], contiguous. logits x [rows, V]
+ * are of `dtype` (MNB_F16 or MNB_F32), rows `stride` elements apart. temperature is fp32 [rows], NULL for 1; a row of
+ * temperature 0 gets 1 at its largest logit (the first of equal ones) and 0 elsewhere. Masked logits are -inf: a row of
+ * nothing else gets zeros. A NaN or (unless the temperature is 0) +inf logit, and a temperature that is negative or NaN, make the row
+ * NaN. rows = 0 is valid and does nothing.
+ */
+MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, int64_t stride, const float *temperature,
+                               float *out, mnb_stream stream);
+
+/*
+ * Verification of drafted tokens from given random numbers (speculative sampling). Sequence b of `batch` has the drafted tokens
+ * draft_start[b] .. draft_start[b+1]-1 of draft_tokens (int32 [drafted]; draft_start int32 [batch + 1], not decreasing,
+ * from 0 to drafted; there may be none). target holds drafted + batch rows of V fp32 probabilities, rows target_stride
+ * elements apart: token i of sequence b has row draft_start[b] + b + i, and one more row follows after the sequence's
+ * last. draft holds `drafted` rows, those that the tokens were drawn from; NULL: each is 1 at its token.
+ *   Token d_i is accepted while u_accept[.] * q_i(d_i) < p_i(d_i). The token after the last accepted one is the first j with
+ *   sum_{k <= j} w_k > u_next[b] * sum_k w_k, w = max(p - q, 0) at the rejected token's rows, w = p of the last row
+ *   when all are accepted. Where nothing is left of p - q it is drawn from p; where p is all 0, it is -1.
+ * u_accept fp32 [drafted], u_next fp32 [batch], in [0, 1) (others are held to it). tokens int32 [drafted + batch], laid out as
+ * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
+ * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0), weights and sums are whole numbers of 2^-60 (a row adds
+ * up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
+ */
+MNB_API mnb_status mnb_verify(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
+                              const int32_t *draft_tokens, const int32_t *draft_start, const float *u_accept,
+                              const float *u_next, int batch, int drafted, int V, int32_t *tokens, int32_t *accepted,
+                              mnb_stream stream);
+
+/*
  * Programmatic dependent launch. With `enable` != 0, later calls on this host thread
  * launch their kernels with programmatic stream serialisation: a kernel may start while
  * the previous kernel on the stream is still running, and it streams its weight, scale
@@ -444,7 +506,7 @@ MNB_API void mnb_set_programmatic_launch(int enable);
 /*
  * Reads and clears the device status word. Kernels that wait on shared-memory barriers
  * bound every wait; one that gives up sets a bit in this word, writes NaN outputs and
- * returns instead of hanging. The act-order and key/value cache kernels set another bit for
+ * returns instead of hanging. The act-order, key/value cache, adapter and verification kernels set another bit for
  * an index input out of range. Returns MNB_ERR_TIMEOUT (with the bits in the message) if a wait gave
  * up, MNB_ERR_INVALID_ARG if only the index bit is set, else MNB_OK. Synchronises the
  * current device, so it must not be called while a stream is being captured.
