@@ -10,96 +10,166 @@ namespace mnb {
 namespace {
 
 // ---------------------------------------------------------------------------------
-// Softmax: p = e^((x - max) / temperature) / sum.  A cluster has a row, its CTAs a part each.
+// Softmax: p = e^((x - max) / temperature) / sum.  A cluster has a row, its CTAs a part each: read once, kept in registers
+// (parts of up to 32 elements a thread; of rows beyond 16 such parts, read three times), largest and sum of the parts exchanged once.
+// Elements go in chunks of 8 that begin at 16-byte boundaries of the logits, whatever the row's own start.
 // ---------------------------------------------------------------------------------
-constexpr int kSoftThreads = 512;
-
-struct MaxSum {
-  float m, s;
-};
-
-template <bool F32>
-__device__ __forceinline__ float logit(const void* row, int j) {
-  if constexpr (F32) return static_cast<const float*>(row)[j];
-  else return __half2float(static_cast<const __half*>(row)[j]);
-}
+constexpr int kHeld = 4;  // chunks that a thread keeps
 
 __device__ __forceinline__ float nan_max(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-template <bool F32>
-__global__ void __launch_bounds__(kSoftThreads) softmax_kernel(const Softmax a, int cluster) {
-  __shared__ float red[kSoftThreads / 32];
-  __shared__ int red_at[kSoftThreads / 32];
+template <bool F32, int kThreads, bool kHold>
+__global__ void __launch_bounds__(kThreads) softmax_kernel(const Softmax a, int cluster) {
+  constexpr int kWarps = kThreads / 32, kNone = 0x7fffffff;
+  __shared__ float red[2][kWarps];
+  __shared__ int red_at[kWarps];
   __shared__ float2 mine;
   __shared__ int mine_at;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int part = cluster_ctarank(), r = blockIdx.x / cluster;
   pdl_launch_dependents();
   pdl_wait();
-  const void* row = static_cast<const uint8_t*>(a.logits) + (int64_t)r * a.stride * (F32 ? 4 : 2);
-  float* out = a.out + (int64_t)r * a.V;
-  const int j0 = (int)((int64_t)a.V * part / cluster), j1 = (int)((int64_t)a.V * (part + 1) / cluster);
+  const int64_t in_at = (int64_t)r * a.stride, out_at = (int64_t)r * a.V;
+  const int skew = (int)(in_at % (F32 ? 4 : 8));  // chunk i is the elements 8 i - skew ..
+  const int chunks = (a.V + skew + 7) / 8;
+  const int c0 = (int)((int64_t)chunks * part / cluster), c1 = (int)((int64_t)chunks * (part + 1) / cluster);
+  const bool out_vec = ((out_at - skew) & 3) == 0;
   const float temp = a.temperature ? a.temperature[r] : 1.0f;
-  // ---- the largest, and the first place that has it ----
-  float m = -INFINITY;
-  int at = 0x7fffffff;
-  for (int j = j0 + tid; j < j1; j += kSoftThreads) {
-    const float x = logit<F32>(row, j);
-    if (x > m) at = j;
-    m = nan_max(m, x);
+  auto load = [&](int c, float (&v)[8]) {
+    const int j = 8 * c - skew;
+    if (j >= 0 && j + 8 <= a.V) {
+      if constexpr (F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + in_at + j);
+        const float4 x = __ldg(p), y = __ldg(p + 1);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+      } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.logits) + in_at + j));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = half2_floats(u[i]);
+          v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = -INFINITY;
+        if (j + i >= 0 && j + i < a.V) {
+          if constexpr (F32) v[i] = static_cast<const float*>(a.logits)[in_at + j + i];
+          else v[i] = __half2float(static_cast<const __half*>(a.logits)[in_at + j + i]);
+        }
+      }
+    }
+  };
+  float held[kHold ? kHeld : 1][8];
+  // f(first element, values) of each of this thread's chunks
+  auto each = [&](auto f) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (c0 + tid + i * kThreads < c1) f(8 * (c0 + tid + i * kThreads) - skew, held[i]);
+    } else {
+      for (int c = c0 + tid; c < c1; c += kThreads) {
+        load(c, held[0]);
+        f(8 * c - skew, held[0]);
+      }
+    }
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (c0 + tid + i * kThreads < c1) load(c0 + tid + i * kThreads, held[i]);
   }
-  float top = m;
+  float top = -INFINITY;
+  each([&](int, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = nan_max(top, v[i]);
+  });
   for (int o = 16; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
-  if (m != top) at = 0x7fffffff;
-  for (int o = 16; o; o >>= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
-  if (lane == 0) red[warp] = top, red_at[warp] = at;
+  if (lane == 0) red[0][warp] = top;
   __syncthreads();
-  top = red[0];
-  for (int w = 1; w < kSoftThreads / 32; ++w) top = nan_max(top, red[w]);
-  at = 0x7fffffff;
-  for (int w = 0; w < kSoftThreads / 32; ++w)
-    if (red[w] == top) at = min(at, red_at[w]);
-  __syncthreads();
-  const float inv_t = temp > 0.0f ? fminf(1.0f / temp, FLT_MAX) : temp == 0.0f ? 1.0f : NAN;
+  top = red[0][lane % kWarps];
+  for (int o = kWarps / 2; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
+  const float c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
+  const float ref = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
-  if (top != -INFINITY)
-    for (int j = j0 + tid; j < j1; j += kSoftThreads) sum += expf((logit<F32>(row, j) - top) * inv_t);
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    sum = 0.0f;
-    for (int w = 0; w < kSoftThreads / 32; ++w) sum += red[w];
-    mine = make_float2(top, sum);
-    mine_at = at;
+  int at = kNone;
+  if (temp == 0.0f) {
+    each([&](int j, const float (&v)[8]) {
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (v[i] == top) at = min(at, j + i);
+    });
+    at = __reduce_min_sync(kFull, at);
+    if (lane == 0) red_at[warp] = at;
+  } else {
+    each([&](int, float (&v)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = ex2((v[i] - ref) * c);
+        if constexpr (kHold) v[i] = e;
+        sum += e;
+      }
+    });
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) red[1][warp] = sum;
   }
-  // ---- over the cluster ----
+  __syncthreads();
+  if (warp == 0) {
+    sum = red[1][lane % kWarps];
+    for (int o = kWarps / 2; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    at = __reduce_min_sync(kFull, red_at[lane % kWarps]);
+    if (lane == 0) mine = make_float2(top, sum), mine_at = top == -INFINITY ? kNone : at;
+  }
+  // ---- over the cluster: lane i reads part i ----
   cluster_arrive();
   cluster_wait();
-  float all_top = -INFINITY;
-  for (int c = 0; c < cluster; ++c) all_top = nan_max(all_top, cluster_ld_f2(cluster_map(smem_u32(&mine), c)).x);
-  float all = 0.0f;
-  int first = 0x7fffffff;
-  for (int c = 0; c < cluster; ++c) {
-    const float2 v = cluster_ld_f2(cluster_map(smem_u32(&mine), c));
-    if (v.x != -INFINITY) all += v.y * expf((v.x - all_top) * inv_t);
-    int f;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(f) : "r"(cluster_map(smem_u32(&mine_at), c)));
-    if (v.x == all_top) first = min(first, f);
+  float2 other = make_float2(-INFINITY, 0.0f);
+  int first = kNone;
+  if (lane < cluster) {
+    other = cluster_ld_f2(cluster_map(smem_u32(&mine), lane));
+    if (temp == 0.0f) first = cluster_ld_s32(cluster_map(smem_u32(&mine_at), lane));
   }
   cluster_arrive();
+  float all_top = other.x;
+  for (int o = 8; o; o >>= 1) all_top = nan_max(all_top, __shfl_xor_sync(kFull, all_top, o));
+  all_top = __shfl_sync(kFull, all_top, 0);
+  float all = other.x == -INFINITY ? 0.0f : other.y * ex2((other.x - all_top) * c);
+  for (int o = 8; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+  all = __shfl_sync(kFull, all, 0);
+  first = __reduce_min_sync(kFull, other.x == all_top ? first : kNone);
   const bool none = all_top == -INFINITY;  // no logit above -inf
-  const float inv = none ? 0.0f : 1.0f / all;
-  for (int j = j0 + tid; j < j1; j += kSoftThreads) {
-    float p;
-    if (temp == 0.0f) p = all_top != all_top ? NAN : j == first ? 1.0f : 0.0f;
-    else p = none ? 0.0f : expf((logit<F32>(row, j) - all_top) * inv_t) * inv;
-    out[j] = p;
-  }
+  const float all_ref = none ? 0.0f : all_top;
+  // what a held exponential is off by, and 1 / sum
+  const float factor = none ? 0.0f : kHold ? ex2((top - all_top) * c) / all : 1.0f / all;
+  each([&](int j, const float (&v)[8]) {
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (temp == 0.0f) p[i] = all_top != all_top ? NAN : j + i == first ? 1.0f : 0.0f;
+      else p[i] = (kHold ? v[i] : ex2((v[i] - all_ref) * c)) * factor;
+    }
+    float* out = a.out + out_at + j;
+    if (out_vec && j >= 0 && j + 8 <= a.V) {
+      *reinterpret_cast<float4*>(out) = make_float4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(p[4], p[5], p[6], p[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j + i >= 0 && j + i < a.V) out[i] = p[i];
+    }
+  });
   cluster_wait();
 }
 
@@ -170,19 +240,51 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const Verify 
   const float* q = rejected && a.draft ? a.draft + (int64_t)(s0 + accepted) * a.draft_stride : nullptr;
   const int not_this = rejected && !a.draft ? a.tokens[s0 + accepted] : -1;
   // ---- sums of this warp's part of the row ----
+  // Chunks of 4 elements that begin at 16-byte boundaries of p (and of q, where its row lies alike).
+  const int skew = (int)((int64_t)(s0 + b + accepted) * a.target_stride & 3);
+  const bool alike = q && ((int64_t)(s0 + accepted) * a.draft_stride & 3) == skew;
+  const int chunks = (a.V + skew + 3) / 4;
   const int parts = cluster * kVerifyWarps, own = part * kVerifyWarps + warp;
-  const int len = ((a.V + parts - 1) / parts + 127) / 128 * 128;
-  const int j0 = (int)min((int64_t)own * len, (int64_t)a.V), j1 = min(j0 + len, a.V);
-  auto weight = [&](int j, bool residual) -> uint64_t {
-    const uint64_t f = fixed60(p[j]);
+  const int each = ((chunks + parts - 1) / parts + 31) / 32 * 32;
+  const int c0 = (int)min((int64_t)own * each, (int64_t)chunks), c1 = min(c0 + each, chunks);
+  auto load = [&](const float* row, int c, bool whole, float (&v)[4]) {
+    const int j = 4 * c - skew;
+    if (whole && j >= 0 && j + 4 <= a.V) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(row + j));
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < a.V ? __ldg(row + j + i) : 0.0f;
+    }
+  };
+  auto weight = [&](float pj, float qj, int j, bool residual) -> uint64_t {
+    const uint64_t f = fixed60(pj);
     if (!residual) return f;
-    if (q) return sub_clamped(f, fixed60(q[j]));
+    if (q) return sub_clamped(f, fixed60(qj));
     return j == not_this ? 0 : f;
   };
+  constexpr int kFlight = 4;
   uint64_t sum_w = 0, sum_p = 0;
-  for (int j = j0 + lane; j < j1; j += 32) {
-    sum_p += weight(j, false);
-    if (rejected) sum_w += weight(j, true);
+  for (int c = c0 + lane; c < c1; c += 32 * kFlight) {
+    float pv[kFlight][4], qv[kFlight][4];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
+      if (c + 32 * k < c1) {
+        load(p, c + 32 * k, true, pv[k]);
+        if (q) load(q, c + 32 * k, alike, qv[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t f = fixed60(pv[k][i]);
+        sum_p += f;
+        if (q) sum_w += sub_clamped(f, fixed60(qv[k][i]));
+        else if (4 * (c + 32 * k) - skew + i != not_this) sum_w += f;
+      }
   }
   sum_p = warp_sum(sum_p), sum_w = warp_sum(sum_w);
   if (lane == 0) sums[0][warp] = sum_w, sums[1][warp] = sum_p;
@@ -208,16 +310,34 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const Verify 
   const int64_t at = (int64_t)s0 + b;
   if (all > 0 && head <= limit && head + here > limit) {
     uint64_t run = head;
-    for (int j = j0; j < j1; j += 32) {
-      const uint64_t w = j + lane < j1 ? weight(j + lane, residual) : 0;
-      uint64_t inc = w;
+    for (int c = c0; c < c1; c += 32) {
+      float pv[4] = {}, qv[4] = {};
+      uint64_t w[4], inc = 0;
+      if (c + lane < c1) {
+        load(p, c + lane, true, pv);
+        if (q) load(q, c + lane, alike, qv);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = weight(pv[i], qv[i], 4 * (c + lane) - skew + i, residual);
+        inc += w[i];
+      }
+      const uint64_t mine = inc;
       for (int o = 1; o < 32; o <<= 1) {
         const uint64_t v = shfl_up_u64(inc, o);
         if (lane >= o) inc += v;
       }
       const uint32_t past = __ballot_sync(kFull, run + inc > limit);
       if (past) {
-        if (lane == 0) a.out[at + accepted] = j + __ffs(past) - 1;
+        if (lane == __ffs(past) - 1) {
+          uint64_t s = run + inc - mine;
+          int i = 0;
+          for (; i < 3; ++i) {
+            s += w[i];
+            if (s > limit) break;
+          }
+          a.out[at + accepted] = 4 * (c + lane) - skew + i;
+        }
         break;
       }
       run += __shfl_sync(kFull, (unsigned long long)inc, 31);
@@ -244,14 +364,18 @@ int cluster_for(int rows, int V, int least, int num_sms) {
 }  // namespace
 
 cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a) {
-  const int c = cluster_for(a.rows, a.V, 2048, ctx.num_sms);
+  int c = cluster_for(a.rows, a.V, 2048, ctx.num_sms);
+  while (c < 16 && a.V + 7 > c * 512 * kHeld * 8) c *= 2;
+  const bool hold = a.V + 7 <= c * 512 * kHeld * 8, few = (a.V + 7) / 8 <= c * 128 * kHeld - c;
   ctx.variant = a.f32 ? "softmax_f32" : "softmax_f16";
-  auto go = [&](auto kern, std::atomic<uint64_t>& wide) {
+  auto go = [&](auto kern, int threads, std::atomic<uint64_t>& wide) {
     const cudaError_t e = c > 8 ? allow_wide_clusters(kern, ctx.device, wide) : cudaSuccess;
-    return e != cudaSuccess ? e : launch_clusters(ctx, kern, c, dim3((unsigned)a.rows * c), dim3(kSoftThreads), 0, a, c);
+    return e != cudaSuccess ? e : launch_clusters(ctx, kern, c, dim3((unsigned)a.rows * c), dim3(threads), 0, a, c);
   };
-  static std::atomic<uint64_t> wide[2];
-  return a.f32 ? go(softmax_kernel<true>, wide[1]) : go(softmax_kernel<false>, wide[0]);
+  static std::atomic<uint64_t> wide[6];
+  if (!hold) return a.f32 ? go(softmax_kernel<true, 512, false>, 512, wide[0]) : go(softmax_kernel<false, 512, false>, 512, wide[1]);
+  if (few) return a.f32 ? go(softmax_kernel<true, 128, true>, 128, wide[2]) : go(softmax_kernel<false, 128, true>, 128, wide[3]);
+  return a.f32 ? go(softmax_kernel<true, 512, true>, 512, wide[4]) : go(softmax_kernel<false, 512, true>, 512, wide[5]);
 }
 
 cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a) {
