@@ -14,7 +14,7 @@ The names match the C entry points: ``mnb_dequant``, ``mnb_repacked_bytes``,
 ``mnb_act_order_workspace_bytes``, ``mnb_gemm_act_order``, ``mnb_gemm_act_order_noalloc``,
 ``mnb_kv4_cache_bytes``, ``mnb_kv4_append``, ``mnb_kv4_read``, ``mnb_kv4_attention_workspace_bytes``,
 ``mnb_kv4_attention`` (with ``MnbKv4Cache``, the handle of a cache, and ``mnb_kv4_cache_alloc``),
-``mnb_lora`` (with ``MnbLoraPool``, the handle of a layer's adapters), ``mnb_softmax``, ``mnb_verify``,
+``mnb_lora_workspace_bytes``, ``mnb_lora`` (with ``MnbLoraPool``, the handle of a layer's adapters), ``mnb_softmax``, ``mnb_verify``,
 ``mnb_set_programmatic_launch``,
 ``mnb_check_device_status``,
 ``mnb_last_error``,
@@ -102,7 +102,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "mnb_kv4_attention_workspace_bytes": (c_size, [c_int, c_int, c_int, c_int, c_int, c_int]),
         "mnb_kv4_attention": (c_int, [vp, c_int, c_int, c_int, i64, MnbKv4CacheArg, vp, vp, vp, c_int, c_int,
                                       ctypes.c_float, c_int, c_int, vp, c_size, vp, vp, vp]),
-        "mnb_lora": (c_int, [vp, c_int, c_int, c_int, i64, MnbLoraPoolArg, vp, vp, i64, c_int, vp, i64, vp]),
+        "mnb_lora_workspace_bytes": (c_size, [c_int]),
+        "mnb_lora": (c_int, [vp, c_int, c_int, c_int, i64, MnbLoraPoolArg, vp, vp, i64, c_int, vp, c_size, vp, i64, vp]),
         "mnb_softmax": (c_int, [vp, c_int, c_int, c_int, i64, vp, vp, vp]),
         "mnb_verify": (c_int, [vp, i64, vp, i64, vp, vp, vp, vp, c_int, c_int, c_int, vp, vp, vp]),
         "mnb_set_programmatic_launch": (None, [c_int]),
@@ -821,7 +822,11 @@ class MnbLoraPool:
             None if scales is None else _vector("scales", scales, torch.float32, (count,), self.guard), count, max_rank)
 
 
-def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, out=None, stream=None):
+def mnb_lora_workspace_bytes(M: int) -> int:
+    return int(load_library().mnb_lora_workspace_bytes(_size(M)))
+
+
+def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, workspace=None, out=None, stream=None):
     """``[M, N]`` = ``base`` (None: zeros) + each row's adapter on ``x`` ``[M, K]``; ``adapter`` int32 ``[M]``, -1 for none.
     ``out`` may be ``base``."""
     torch = _torch()
@@ -834,9 +839,18 @@ def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, out=None, stream=None):
     if out is None:
         out = _new((M, N), dtype, x.device, stream)
     os_ = _matrix("out", out, M, N, dtype, guard)
+    lib = load_library()
+    if workspace is None:
+        need = lib.mnb_lora_workspace_bytes(_size(M))
+        if need:
+            workspace = _new(need, torch.uint8, x.device, stream)
+    else:
+        _check_dev("workspace", workspace)
+        _on("workspace", workspace, workspace.dtype, guard)
+    wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard),
-            None if base is None else base.data_ptr(), bs, _size(N), out.data_ptr(), os_, _stream_of(dev, stream))
-    _launch(load_library().mnb_lora, args, dev, guard)
+            None if base is None else base.data_ptr(), bs, _size(N), wp, ws_bytes, out.data_ptr(), os_, _stream_of(dev, stream))
+    _launch(lib.mnb_lora, args, dev, guard)
     return out
 
 

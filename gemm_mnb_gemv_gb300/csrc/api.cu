@@ -830,8 +830,11 @@ mnb_status check_rows(const char* fn, const char* name, int64_t stride, int cols
 
 extern "C" {
 
+size_t mnb_lora_workspace_bytes(int M) { return M < 1 || M > kMaxM ? 0 : mnb::lora_workspace_bytes(M); }
+
 mnb_status mnb_lora(const void* x, int dtype, int M, int K, int64_t x_stride, mnb_lora_pool pool, const int32_t* adapter,
-                    const void* base, int64_t base_stride, int N, void* out, int64_t out_stride, mnb_stream stream) {
+                    const void* base, int64_t base_stride, int N, void* workspace, size_t ws_bytes, void* out,
+                    int64_t out_stride, mnb_stream stream) {
   const char* fn = "mnb_lora";
   mnb_status st;
   if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
@@ -864,11 +867,19 @@ mnb_status mnb_lora(const void* x, int dtype, int M, int K, int64_t x_stride, mn
   }
   if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
   if ((st = check_rows(fn, "out_stride", out_stride, N, e, false)) != MNB_OK) return st;
+  const size_t need = mnb_lora_workspace_bytes(M);
+  if (ws_bytes < need)
+    return fail(MNB_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  if (need > 0 && (st = check_ptr(fn, "workspace", workspace)) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
   const mnb::Lora a = {x,       dtype == MNB_F32, M,           K,          x_stride, pool.down,     pool.up,
                        pool.ranks, pool.scales,   pool.count,  pool.max_rank, adapter, base,     base_stride,
-                       N,       out,              out_stride};
+                       N,       out,              out_stride,  workspace};
+  if (need == 0) return finish(fn, mnb::launch_lora(ctx, a), ctx);
+  // As in the attention: a call's launches come one after the other, whatever other host threads do on the stream.
+  static std::mutex two_launches;
+  std::lock_guard<std::mutex> lock(two_launches);
   return finish(fn, mnb::launch_lora(ctx, a), ctx);
 }
 

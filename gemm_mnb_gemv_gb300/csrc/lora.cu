@@ -1,15 +1,17 @@
 // Low-rank adapters of many requests beside a shared product:
 //   out[m] = base[m] + scale[a] * up[a] (down[a] x[m]),  a = adapter[m].
 //
-// A cluster of CTAs takes the rows of one adapter among a tile of consecutive rows, in one launch for both products:
-//   1. s = down x: the CTAs split K, the warps of a CTA split it further; partial sums meet in shared memory, then over
-//      the cluster;
-//   2. up s: the CTAs split N, each with all of s.
-// Rows are the M side of the warp's matrix instructions and ranks (then output columns) the N side; a lane loads 8 consecutive
-// elements of K (or of the rank), and both operands number the products' inner index alike, so neither passes
-// through shared memory.
+// A cluster of CTAs takes the rows of one adapter among a tile of 16 or 64 consecutive rows, in one launch for both products:
+//   1. s = down x: the CTAs split K; partial sums meet in shared memory, over the warps and then over the cluster;
+//   2. out = base + up s: the CTAs split N, each with all of s.
+// One ring of asynchronous copies feeds both: a stage is 32 WN of K (x and down) or 32 WN columns of N (base and up), and
+// the first stages of the second product are on their way while the first one's sums are joined.
+// Rows are the M side of the warp's matrix instructions, ranks (then output columns) the N side; a lane takes 8 consecutive
+// elements of the inner index, which both operands number alike.
 // fp16 activations: s is rounded to fp16 after its row was scaled by a power of two to [2^13, 2^14), as the result is
-// rounded. fp32: x and s are split into two tf32 parts (2^-23 together), the weights are exact in tf32.
+// rounded. fp32: x and s are split into two tf32 parts (2^-22 together), the weights are exact in tf32.
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "mma_sync.cuh"
 #include "mnb_device.cuh"
@@ -27,10 +29,18 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 __device__ __forceinline__ float2 half2_floats(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
+// x as two tf32
+struct Split {
+  uint32_t hi, lo;
+};
 __device__ __forceinline__ uint32_t tf32(float x) {
   uint32_t r;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
   return r;
+}
+__device__ __forceinline__ Split split(float x) {
+  const uint32_t h = tf32(x);
+  return {h, tf32(x - __uint_as_float(h))};
 }
 // c += A . B, m16n8k8: lane 4g + t holds A rows g, g + 8 and B column g at k = t, t + 4
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -40,210 +50,314 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// E halves from p, zeros from element `have` on.
-template <int E>
-__device__ __forceinline__ void load_weights(uint32_t (&w)[E / 2], const __half* p, int have) {
+// 16 bytes global -> shared; the first `bytes` (0..16) are read, the rest is zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// RB: ranks in eights; WM: row tiles of 16.
+template <int RB, int WM, bool F32>
+struct Geo {
+  static constexpr int RP = RB * 8, TM = 16 * WM, WN = kWarps / WM;
+  static constexpr int kSpan = 32 * WN;                       // of K or N in a stage
+  static constexpr int kElem = F32 ? 4 : 2;
+  static constexpr int kRow = kSpan * kElem;                  // bytes of a row of x or base in a stage
+  static constexpr int kDownRow = kSpan * 2, kUpRow = RP * 2;  // of down, up
+  static constexpr int kAct = TM * kRow, kWeight = RP * kSpan * 2;
+  static constexpr int kStage = kAct + kWeight;
+  static constexpr int kPart = (WN - 1) * TM * RP * 4;        // partial sums of the warps; the CTA's own in the first
+  static constexpr int kSRow = F32 ? RP * 4 + 8 : RP >= 64 ? RP * 2 + 64 : RP * 2;  // bytes of a row of s
+  static constexpr int kS = (TM * kSRow + 127) / 128 * 128;
+  // Two CTAs an SM where two stages fit (113 KB each), else as many as one CTA can have.
+  static constexpr int fit(int budget) {
+    const int n = (budget - kPart - kS) / kStage;
+    return n > 4 ? 4 : n;
+  }
+  static constexpr int kStages = fit(115200) >= 2 ? fit(115200) : fit(230400);
+  static constexpr int kBytes = kStages * kStage + kPart + kS;
+  static_assert(kStages >= 2, "one stage is read while the next one lands");
+  // With two stages a slot is filled again behind a second barrier, as soon as it is free; with more, behind the next stage's.
+  static constexpr bool kTwo = kStages == 2;
+  static constexpr int kAhead = kTwo ? 2 : kStages - 1;
+};
+
+// Where 16-byte chunk `chunk` of a row lies in it: the chunks that a quarter warp reads of two neighbouring rows come from
+// distinct banks. fp16: chunks 4 i + t of each; fp32: 2 (4 i + t) and its neighbour.
+template <bool F32>
+__device__ __forceinline__ int place(int row, int chunk) {
+  return (chunk ^ ((row & 1) * (F32 ? 1 : 4))) * 16;
+}
+template <int RP>
+__device__ __forceinline__ int up_place(int row, int chunk) {  // rows of 64 bytes and less are neighbours without conflicts
+  return (chunk ^ (RP >= 64 ? (row & 1) * 4 : 0)) * 16;
+}
+
+// The rows of one adapter in a tile.
+struct Item {
+  int m0, adapter;
+  uint64_t rows;  // bit i: row m0 + i
+};
+
+// A call's items, largest first: those with more than half a tile's rows from the front of `list`, the others from its
+// back. Counters first, in 16 bytes.
+template <int TM>
+__global__ void __launch_bounds__(1024) lora_list_kernel(const Lora a, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
+  __shared__ uint32_t count[2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x < 2) count[threadIdx.x] = 0;
+  __syncthreads();
+  for (int m0 = warp * TM; m0 < a.M; m0 += 32 * TM) {
+    int v[2];
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) w[i] = 0;
-  if (have > 0) {
-    if constexpr (E == 8) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (E == 4) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = v.x, w[1] = v.y;
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    for (int h = 0; h < 2; ++h) {
+      const int i = 32 * h + lane;
+      v[h] = -2;
+      if (i < TM && m0 + i < a.M) {
+        v[h] = max(a.adapter[m0 + i], -1);
+        if (v[h] >= a.count) {
+          report_status(status, kStatusBadIndex);
+          v[h] = -1;
+        }
+      }
     }
-    if (have < E) {
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) w[i] &= have >= 2 * i + 2 ? 0xffffffffu : have == 2 * i + 1 ? 0xffffu : 0u;
+    uint32_t left[2] = {__ballot_sync(kFull, v[0] != -2), __ballot_sync(kFull, v[1] != -2)};
+    while (left[0] | left[1]) {
+      const int value = left[0] ? __shfl_sync(kFull, v[0], __ffs(left[0]) - 1) : __shfl_sync(kFull, v[1], __ffs(left[1]) - 1);
+      const uint32_t lo = __ballot_sync(kFull, v[0] == value), hi = __ballot_sync(kFull, v[1] == value);
+      left[0] &= ~lo, left[1] &= ~hi;
+      if (lane == 0) {
+        const int small = __popc(lo) + __popc(hi) <= TM / 2;
+        const int at = (int)atomicAdd(&count[small], 1u);
+        list[small ? capacity - 1 - at : at] = {m0, value, (uint64_t)hi << 32 | lo};
+      }
     }
   }
+  __syncthreads();
+  if (threadIdx.x < 2) counts[threadIdx.x] = count[threadIdx.x];
 }
 
-// One tile's products with 4 inner elements a lane for each row (fp32 activations): a[part][row][element].
-struct Split {
-  uint32_t hi, lo;
-};
-__device__ __forceinline__ Split split(float x) {
-  const uint32_t h = tf32(x);
-  return {h, tf32(x - __uint_as_float(h))};
-}
-
-template <int RB, int MT, bool F32>
-struct LoraSmem {
-  static constexpr int RP = RB * 8;                              // ranks, padded
-  static constexpr int kPart = kWarps * 16 * RP * 4;             // partial sums of s
-  static constexpr int kS = F32 ? 16 * MT * (RP + 4) * 4 : 16 * MT * (RP + 8) * 2;  // s, rows apart by an odd number of 16 bytes
-  static constexpr int kBytes = kPart + kS;
-};
-
-template <int RB, int MT, bool F32>
-__global__ void __launch_bounds__(kThreads) lora_kernel(const Lora a, int tiles, int subs, int cluster, uint32_t* status) {
+template <int RB, int WM, bool F32>
+__global__ void __launch_bounds__(kThreads, 2)
+    lora_kernel(const Lora a, int cluster, int subs, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
   using T = std::conditional_t<F32, float, __half>;
-  using L = LoraSmem<RB, MT, F32>;
-  constexpr int RP = L::RP, TM = 16 * MT;
-  constexpr int E = RB >= 4 ? 8 : RB == 2 ? 4 : 2;  // elements of the rank that a lane has of a chunk
-  constexpr int KC = RP / (4 * E);                  // chunks of the rank
-  constexpr int kSRow = F32 ? RP + 4 : RP + 8;      // elements between the rows of s
+  using L = Geo<RB, WM, F32>;
+  constexpr int RP = L::RP, TM = L::TM, WN = L::WN, S = L::kStages;
+  constexpr int E = RB >= 4 ? 8 : RB == 2 ? 4 : 2;  // elements of the rank that a lane has of a chunk of 4 E
+  constexpr int KC = RP / (4 * E);
   extern __shared__ __align__(128) uint8_t smem[];
-  float* part = reinterpret_cast<float*>(smem);
-  T* s_mem = reinterpret_cast<T*>(smem + L::kPart);
-  __shared__ int index[TM], rows[TM];
+  float* part = reinterpret_cast<float*>(smem + S * L::kStage);
+  uint8_t* s_mem = smem + S * L::kStage + L::kPart;
+  __shared__ int rows[TM];
   __shared__ float factors[TM];
-  __shared__ uint32_t firsts[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
-  const int rank_of_cta = cluster_ctarank(), id = blockIdx.x / cluster;
-  const int tile = id % tiles, sub = id / tiles;
-  const int m0 = tile * TM;
+  const int wm = warp % WM, wn = warp / WM;
+  const int cta = cluster_ctarank(), id = blockIdx.x / cluster;
+  const uint32_t ring = smem_u32(smem);
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the tile's distinct adapters ----
-  if (tid < TM) {
-    int v = -2;  // no row
-    if (m0 + tid < a.M) {
-      v = a.adapter[m0 + tid];
-      if (v >= a.count) {
-        if (rank_of_cta == 0 && sub == 0) report_status(status, kStatusBadIndex);
-        v = -1;
-      }
-      v = max(v, -1);
-    }
-    index[tid] = v;
-  }
-  if (tid < 2) firsts[tid] = 0;
-  __syncthreads();
-  if (tid < TM) {
-    const int v = index[tid];
-    bool first = v != -2;
-    for (int j = 0; j < tid; ++j) first = first && index[j] != v;
-    if (first) atomicOr(&firsts[tid / 32], 1u << (tid % 32));
-  }
-  __syncthreads();
-  uint64_t left = (uint64_t)firsts[1] << 32 | firsts[0];
-  for (int i = 0; i < sub && left; ++i) left &= left - 1;
+  const int granules = (a.K + 31) / 32, blocks = (a.N + 31) / 32;
+  const int g0 = (int)((int64_t)granules * cta / cluster), g1 = (int)((int64_t)granules * (cta + 1) / cluster);
+  const int b0 = (int)((int64_t)blocks * cta / cluster), b1 = (int)((int64_t)blocks * (cta + 1) / cluster);
+  constexpr int kVec = 16 / sizeof(T);
+  const bool base_vec = a.base && a.base_stride % kVec == 0, out_vec = a.out_stride % kVec == 0;
+  const bool in_place = a.base == a.out;
 
-  while (left) {
-    const int value = index[__ffsll(left) - 1];
-    for (int i = 0; i < subs && left; ++i) left &= left - 1;
-    // ---- this adapter's rows ----
-    uint64_t mine = 0;
-#pragma unroll
-    for (int h = 0; h < (TM + 31) / 32; ++h) {
-      const int i = 32 * h + lane;
-      mine |= (uint64_t)__ballot_sync(kFull, i < TM && index[i < TM ? i : 0] == value) << (32 * h);
-    }
-    const int n_rows = __popcll(mine);
-    if (tid < TM && (mine >> tid & 1)) rows[__popcll(mine & ((1ull << tid) - 1))] = m0 + tid;
-    __syncthreads();
-    const int rank = value < 0 ? 0 : a.ranks ? min(max(a.ranks[value], 0), a.max_rank) : a.max_rank;
-    if (rank == 0 && a.base == a.out && a.base_stride == a.out_stride) {
-      __syncthreads();
-      continue;
-    }
-    const int mt_all = (n_rows + 15) / 16;
-    if (rank > 0) {
-      // ---- s = down x over this CTA's part of K ----
-      const int groups = mt_all > 2 ? 4 : mt_all;      // warps side by side over the rows,
-      const int splits = kWarps / groups;              // and over K
-      const int mg = warp % groups, kg = warp / groups;
-      const int granules = (a.K + 31) / 32;
-      const int g0 = (int)((int64_t)granules * rank_of_cta / cluster), g1 = (int)((int64_t)granules * (rank_of_cta + 1) / cluster);
-      float acc[RB][4];
-#pragma unroll
-      for (int j = 0; j < RB; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-      const T* xr[2];
-      bool live[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = mg * 16 + g + 8 * h;
-        live[h] = r < n_rows;
-        xr[h] = static_cast<const T*>(a.x) + (int64_t)rows[live[h] ? r : 0] * a.x_stride;
+  // Without a list (one tile's adapters are found by each cluster itself): cluster `id` takes tile id / subs and its adapter id % subs,
+  // in the order of their first rows.
+  const int big = list ? (int)counts[0] : 0, items = list ? big + (int)counts[1] : 1;
+  const int step = list ? gridDim.x / cluster : 1;
+  for (int it = list ? id : 0; it < items; it += step) {
+    Item item;
+    if (list) {
+      item = list[it < big ? it : capacity - 1 - (it - big)];
+    } else {
+      item.m0 = id / subs * TM;
+      const int i = lane, want = id % subs;
+      int v = -2;
+      if (i < TM && item.m0 + i < a.M) {
+        v = max(a.adapter[item.m0 + i], -1);
+        if (v >= a.count) {
+          if (want == 0 && cta == 0 && warp == 0) report_status(status, kStatusBadIndex);
+          v = -1;
+        }
       }
-      const __half* down = static_cast<const __half*>(a.down) + ((int64_t)value * a.max_rank + g) * a.K;
-      if (mg < mt_all) {
-        for (int i = g0 + kg; i < g1; i += splits) {
-          const int k = i * 32 + 8 * t;
-          const bool in = k < a.K;
-          uint4 w[RB];
+      const uint32_t same = __match_any_sync(kFull, v);
+      uint32_t firsts = __ballot_sync(kFull, v != -2 && __ffs(same) - 1 == lane);
+      if (__popc(firsts) <= want) return;  // all CTAs of the cluster alike
+      for (int k = 0; k < want; ++k) firsts &= firsts - 1;
+      const int from = __ffs(firsts) - 1;
+      item.adapter = __shfl_sync(kFull, v, from);
+      item.rows = __shfl_sync(kFull, same, from);
+    }
+    const int n_rows = __popcll(item.rows), value = item.adapter;
+    const int rank = value < 0 ? 0 : a.ranks ? min(max(a.ranks[value], 0), a.max_rank) : a.max_rank;
+    if (rank == 0 && in_place) continue;
+    __syncthreads();  // the item before is done with rows, s and the ring
+    if (tid < TM && (item.rows >> tid & 1)) rows[__popcll(item.rows & ((1ull << tid) - 1))] = item.m0 + tid;
+    __syncthreads();
+
+    const int down_stages = rank > 0 ? (g1 - g0 + WN - 1) / WN : 0;
+    const int stages = down_stages + (b1 - b0 + WN - 1) / WN;
+    const __half* down = static_cast<const __half*>(a.down) + (int64_t)value * a.max_rank * a.K;
+    const __half* up = static_cast<const __half*>(a.up) + (int64_t)value * a.N * a.max_rank;
+    auto issue = [&](int q) {
+      if (q < stages) {
+        const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
+        constexpr int kChunks = L::kRow / 16;  // of a row of x or base
+        if (q < down_stages) {
+          const int k0 = (g0 + q * WN) * 32, k1 = min(a.K, g1 * 32);
+          for (int i = tid; i < n_rows * kChunks; i += kThreads) {
+            const int r = i / kChunks, c = i % kChunks, k = k0 + c * kVec;
+            const T* src = static_cast<const T*>(a.x) + (int64_t)rows[r] * a.x_stride + k;
+            copy16(act + r * L::kRow + place<F32>(r, c), k < k1 ? src : static_cast<const T*>(a.x), k < k1 ? 16 : 0);
+          }
+          constexpr int kDownChunks = L::kDownRow / 16;
+          const int padded = min((rank + 7) / 8 * 8, RP);
+          for (int i = tid; i < padded * kDownChunks; i += kThreads) {
+            const int r = i / kDownChunks, c = i % kDownChunks, k = k0 + c * 8;
+            const bool there = r < rank && k < k1;
+            copy16(weight + r * L::kDownRow + place<false>(r, c), there ? down + (int64_t)r * a.K + k : down, there ? 16 : 0);
+          }
+        } else {
+          const int n0 = (b0 + (q - down_stages) * WN) * 32, n1 = min(a.N, b1 * 32);
+          if (base_vec) {
+            for (int i = tid; i < n_rows * kChunks; i += kThreads) {
+              const int r = i / kChunks, c = i % kChunks, n = n0 + c * kVec;
+              const int bytes = min(max(n1 - n, 0) * (int)sizeof(T), 16);
+              const T* src = static_cast<const T*>(a.base);
+              copy16(act + r * L::kRow + place<F32>(r, c), bytes ? src + (int64_t)rows[r] * a.base_stride + n : src, bytes);
+            }
+          }
+          if (rank > 0) {
+            constexpr int kUpChunks = L::kUpRow / 16;
+            for (int i = tid; i < L::kSpan * kUpChunks; i += kThreads) {
+              const int r = i / kUpChunks, c = i % kUpChunks;
+              const int bytes = n0 + r < n1 ? min(max(rank - 8 * c, 0) * 2, 16) : 0;
+              copy16(weight + r * L::kUpRow + up_place<RP>(r, c), bytes ? up + (int64_t)(n0 + r) * a.max_rank + 8 * c : up, bytes);
+            }
+          }
+        }
+      }
+      copy_commit();
+    };
+    for (int q = 0; q < L::kAhead; ++q) issue(q);
+
+    const bool live = wm * 16 < n_rows;
+    float acc[RB][4];
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+    int q = 0;
+    // ---- s = down x over this CTA's part of K ----
+    for (; q < down_stages; ++q) {
+      copy_wait<L::kAhead - 1>();
+      __syncthreads();
+      if (!L::kTwo) issue(q + L::kAhead);
+      if (live) {
+        const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
+        const int r0 = wm * 16 + g;
+        // Rows beyond the last hold what was there: they do not reach the others' sums.
+        if constexpr (F32) {
+          float x[2][8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = r0 + 8 * h;
+              const uint4 v = lds128_a(act + r * L::kRow + place<true>(r, 2 * (4 * wn + t) + i));
+              x[h][4 * i] = __uint_as_float(v.x), x[h][4 * i + 1] = __uint_as_float(v.y);
+              x[h][4 * i + 2] = __uint_as_float(v.z), x[h][4 * i + 3] = __uint_as_float(v.w);
+            }
+          uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const Split v = split(x[i & 1][2 * s + i / 2]);
+              hi[s][i] = v.hi, lo[s][i] = v.lo;
+            }
 #pragma unroll
           for (int j = 0; j < RB; ++j) {
-            w[j] = make_uint4(0, 0, 0, 0);
-            if (in && j * 8 + g < rank) w[j] = __ldg(reinterpret_cast<const uint4*>(down + (int64_t)j * 8 * a.K + k));
+            if (j * 8 < rank) {
+              const uint4 w = lds128_a(weight + (j * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
+              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                const float2 b = half2_floats(u[s]);
+                mma1688(acc[j], lo[s], __float_as_uint(b.x), __float_as_uint(b.y));
+                mma1688(acc[j], hi[s], __float_as_uint(b.x), __float_as_uint(b.y));
+              }
+            }
           }
-          if constexpr (F32) {
-            float x[2][8];
+        } else {
+          uint4 x[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) x[h] = lds128_a(act + (r0 + 8 * h) * L::kRow + place<false>(g, 4 * wn + t));
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                float4 v = make_float4(0, 0, 0, 0);
-                if (in && live[h]) v = *reinterpret_cast<const float4*>(xr[h] + k + 4 * q);
-                x[h][4 * q] = v.x, x[h][4 * q + 1] = v.y, x[h][4 * q + 2] = v.z, x[h][4 * q + 3] = v.w;
-              }
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const Split x0 = split(x[0][2 * s]), x1 = split(x[1][2 * s]), x2 = split(x[0][2 * s + 1]), x3 = split(x[1][2 * s + 1]);
-              const uint32_t hi[4] = {x0.hi, x1.hi, x2.hi, x3.hi}, lo[4] = {x0.lo, x1.lo, x2.lo, x3.lo};
-#pragma unroll
-              for (int j = 0; j < RB; ++j) {
-                if (j * 8 < rank) {
-                  const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-                  const float2 b = half2_floats(u[s]);
-                  mma1688(acc[j], lo, __float_as_uint(b.x), __float_as_uint(b.y));
-                  mma1688(acc[j], hi, __float_as_uint(b.x), __float_as_uint(b.y));
-                }
-              }
-            }
-          } else {
-            uint4 x[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              x[h] = make_uint4(0, 0, 0, 0);
-              if (in && live[h]) x[h] = *reinterpret_cast<const uint4*>(xr[h] + k);
-            }
-#pragma unroll
-            for (int j = 0; j < RB; ++j) {
-              if (j * 8 < rank) {
-                mma16816(acc[j], x[0].x, x[1].x, x[0].y, x[1].y, w[j].x, w[j].y);
-                mma16816(acc[j], x[0].z, x[1].z, x[0].w, x[1].w, w[j].z, w[j].w);
-              }
+          for (int j = 0; j < RB; ++j) {
+            if (j * 8 < rank) {
+              const uint4 w = lds128_a(weight + (j * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
+              mma16816(acc[j], x[0].x, x[1].x, x[0].y, x[1].y, w.x, w.y);
+              mma16816(acc[j], x[0].z, x[1].z, x[0].w, x[1].w, w.z, w.w);
             }
           }
         }
+      }
+      if (L::kTwo) {
+        __syncthreads();
+        issue(q + L::kAhead);
+      }
+    }
+    if (rank > 0) {
+      // ---- over the warps ----
+      auto at = [&](int w, int r, int col) { return part + ((w * TM + r) * RP + col); };
+      const int r0 = wm * 16 + g;
+      if (live && wn > 0) {
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
-          float* p = part + ((kg * groups + mg) * 16 + g) * RP + j * 8 + 2 * t;
-          *reinterpret_cast<float2*>(p) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(p + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
+          *reinterpret_cast<float2*>(at(wn - 1, r0, j * 8 + 2 * t)) = make_float2(acc[j][0], acc[j][1]);
+          *reinterpret_cast<float2*>(at(wn - 1, r0 + 8, j * 8 + 2 * t)) = make_float2(acc[j][2], acc[j][3]);
         }
       }
       __syncthreads();
-      // ---- over the warps, then over the cluster; every CTA gets all of s ----
-      for (int e = tid * 4; e < mt_all * 16 * RP; e += kThreads * 4) {
-        float4 v = *reinterpret_cast<float4*>(part + e);
-        for (int i = 1; i < splits; ++i) {
-          const float4 o = *reinterpret_cast<float4*>(part + i * groups * 16 * RP + e);
-          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
-        *reinterpret_cast<float4*>(part + e) = v;
+      if (live && wn == 0) {
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float2 v = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+#pragma unroll
+            for (int w = 0; w < WN - 1; ++w) {
+              const float2 o = *reinterpret_cast<float2*>(at(w, r0 + 8 * h, j * 8 + 2 * t));
+              v.x += o.x, v.y += o.y;
+            }
+            *reinterpret_cast<float2*>(at(0, r0 + 8 * h, j * 8 + 2 * t)) = v;
+          }
       }
+      // ---- over the cluster; every CTA gets all of s. RP / 4 neighbouring lanes have a row ----
       cluster_arrive();
       cluster_wait();
       const float scale = a.scales ? a.scales[value] : 1.0f;
-      for (int e = tid * 4; e < mt_all * 16 * RP; e += kThreads * 4) {  // RP / 4 neighbouring lanes have a row
+      for (int e0 = warp * 128; e0 < n_rows * RP; e0 += kThreads * 4) {
+        const int e = e0 + lane * 4, r = e / RP, col = e % RP;
         float4 v = make_float4(0, 0, 0, 0);
         for (int c = 0; c < cluster; ++c) {
           const float4 o = cluster_ld_f4(cluster_map(smem_u32(part + e), c));
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
-        const int r = e / RP, col = e % RP;
+        uint8_t* row = s_mem + r * L::kSRow;
         if constexpr (F32) {
-          *reinterpret_cast<float4*>(s_mem + r * kSRow + col) = v;
+          *reinterpret_cast<float2*>(row + col * 4) = make_float2(v.x, v.y);
+          *reinterpret_cast<float2*>(row + col * 4 + 8) = make_float2(v.z, v.w);
           if (col == 0) factors[r] = scale;
         } else {
           float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -252,108 +366,84 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Lora a, int tiles,
           const int ex = (int)(__float_as_uint(top) >> 23) - 127;
           const int p = top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
           const float f = __uint_as_float((uint32_t)(127 - p) << 23);
-          *reinterpret_cast<uint2*>(s_mem + r * kSRow + col) = make_uint2(half2_bits(v.x * f, v.y * f), half2_bits(v.z * f, v.w * f));
+          *reinterpret_cast<uint2*>(row + col * 2) = make_uint2(half2_bits(v.x * f, v.y * f), half2_bits(v.z * f, v.w * f));
           if (col == 0) factors[r] = scalbnf(scale, p);
         }
       }
-      __syncthreads();
       cluster_arrive();  // no more reads of the others' sums
     }
 
-    // ---- out = base + up s over this CTA's part of N, 32 columns at a time ----
-    // Column c of the product's 8-column tile j is output column 8 (c / 2) + 2 j + c % 2 of the 32: a lane then has
+    // ---- out = base + up s over this CTA's part of N ----
+    // Column c of the product's 8-column tile j is output column 8 (c / 2) + 2 j + c % 2 of the warp's 32: a lane then has
     // 8 consecutive ones, of four tiles.
-    const int blocks = (a.N + 31) / 32;
-    const int n0 = (int)((int64_t)blocks * rank_of_cta / cluster), n1 = (int)((int64_t)blocks * (rank_of_cta + 1) / cluster);
-    constexpr int kVec = 16 / sizeof(T);
-    const bool base_vec = a.base_stride % kVec == 0, out_vec = a.out_stride % kVec == 0;
-    for (int nb = n0 + warp; nb < n1; nb += kWarps) {
-      uint32_t w[4][KC][E / 2];
-      if (rank > 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = nb * 32 + 8 * (g / 2) + 2 * j + g % 2;
-          const __half* up = static_cast<const __half*>(a.up) + ((int64_t)value * a.N + n) * a.max_rank + E * t;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) load_weights<E>(w[j][c], up + 4 * E * c, n < a.N ? rank - 4 * E * c - E * t : 0);
-        }
-      }
-      const int n = nb * 32 + 8 * t, width = min(8, a.N - n);
-      for (int mt = 0; mt < mt_all; ++mt) {
-        float acc[4][4];
+    for (; q < stages; ++q) {
+      copy_wait<L::kAhead - 1>();
+      __syncthreads();
+      if (!L::kTwo) issue(q + L::kAhead);
+      if (live) {
+        const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
+        const int r0 = wm * 16 + g;
+        const int n = (b0 + (q - down_stages) * WN + wn) * 32 + 8 * t, width = min(8, min(a.N, b1 * 32) - n);
+        float d[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-        float b[2][8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + g + 8 * h;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[h][i] = 0.0f;
-          if (a.base && r < n_rows && width > 0) {
-            const T* p = static_cast<const T*>(a.base) + (int64_t)rows[r] * a.base_stride + n;
-            if (base_vec && width == 8) {
-              if constexpr (F32) {
-                const float4 v0 = *reinterpret_cast<const float4*>(p), v1 = *reinterpret_cast<const float4*>(p + 4);
-                b[h][0] = v0.x, b[h][1] = v0.y, b[h][2] = v0.z, b[h][3] = v0.w;
-                b[h][4] = v1.x, b[h][5] = v1.y, b[h][6] = v1.z, b[h][7] = v1.w;
-              } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 f = half2_floats(u[i]);
-                  b[h][2 * i] = f.x, b[h][2 * i + 1] = f.y;
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i < width) b[h][i] = (float)p[i];
-            }
-          }
-        }
+          for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
         if (rank > 0) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             if (4 * E * c < rank) {
-              const T* sr = s_mem + (mt * 16 + g) * kSRow + 4 * E * c + E * t;
+              uint32_t w[4][E / 2];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = 32 * wn + 8 * (g / 2) + 2 * j + g % 2;
+                const uint32_t p = weight + r * L::kUpRow;
+                if constexpr (E == 8) {
+                  const uint4 v = lds128_a(p + up_place<RP>(r, 4 * c + t));
+                  w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+                } else if constexpr (E == 4) {
+                  const uint2 v = lds_u64_a(p + 8 * t);
+                  w[j][0] = v.x, w[j][1] = v.y;
+                } else {
+                  w[j][0] = lds_u32_a(p + 4 * t);
+                }
+              }
               if constexpr (F32) {
 #pragma unroll
                 for (int s = 0; s < E / 2; ++s) {
-                  const float2 v0 = *reinterpret_cast<const float2*>(sr + 2 * s);
-                  const float2 v1 = *reinterpret_cast<const float2*>(sr + 8 * kSRow + 2 * s);
+                  const float* p = reinterpret_cast<const float*>(s_mem + r0 * L::kSRow) + 4 * E * c + E * t + 2 * s;
+                  const float2 v0 = *reinterpret_cast<const float2*>(p);
+                  const float2 v1 = *reinterpret_cast<const float2*>(reinterpret_cast<const uint8_t*>(p) + 8 * L::kSRow);
                   const Split x0 = split(v0.x), x1 = split(v1.x), x2 = split(v0.y), x3 = split(v1.y);
                   const uint32_t hi[4] = {x0.hi, x1.hi, x2.hi, x3.hi}, lo[4] = {x0.lo, x1.lo, x2.lo, x3.lo};
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
-                    const float2 f = half2_floats(w[j][c][s]);
-                    mma1688(acc[j], lo, __float_as_uint(f.x), __float_as_uint(f.y));
-                    mma1688(acc[j], hi, __float_as_uint(f.x), __float_as_uint(f.y));
+                    const float2 f = half2_floats(w[j][s]);
+                    mma1688(d[j], lo, __float_as_uint(f.x), __float_as_uint(f.y));
+                    mma1688(d[j], hi, __float_as_uint(f.x), __float_as_uint(f.y));
                   }
                 }
               } else {
                 uint32_t x[2][E / 2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const T* p = sr + 8 * h * kSRow;
+                  const uint32_t p = smem_u32(s_mem + (r0 + 8 * h) * L::kSRow) + (4 * E * c + E * t) * 2;
                   if constexpr (E == 8) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    const uint4 v = lds128_a(p);
                     x[h][0] = v.x, x[h][1] = v.y, x[h][2] = v.z, x[h][3] = v.w;
                   } else if constexpr (E == 4) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    const uint2 v = lds_u64_a(p);
                     x[h][0] = v.x, x[h][1] = v.y;
                   } else {
-                    x[h][0] = *reinterpret_cast<const uint32_t*>(p);
+                    x[h][0] = lds_u32_a(p);
                   }
                 }
 #pragma unroll
                 for (int s = 0; s < (E + 3) / 4; ++s)
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
-                    if constexpr (E == 2) mma16816(acc[j], x[0][0], x[1][0], 0u, 0u, w[j][c][0], 0u);
-                    else mma16816(acc[j], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1], w[j][c][2 * s], w[j][c][2 * s + 1]);
+                    if constexpr (E == 2) mma16816(d[j], x[0][0], x[1][0], 0u, 0u, w[j][0], 0u);
+                    else mma16816(d[j], x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1], w[j][2 * s], w[j][2 * s + 1]);
                   }
               }
             }
@@ -361,13 +451,37 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Lora a, int tiles,
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = mt * 16 + g + 8 * h;
+          const int r = r0 + 8 * h;
           if (r < n_rows && width > 0) {
-            const float f = rank > 0 ? factors[r] : 0.0f;
-            T* p = static_cast<T*>(a.out) + (int64_t)rows[r] * a.out_stride + n;
             float y[8];
+            if (base_vec) {
+              if constexpr (F32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = rank > 0 ? fmaf(acc[i / 2][2 * h + i % 2], f, b[h][i]) : b[h][i];
+                for (int i = 0; i < 2; ++i) {
+                  const uint4 v = lds128_a(act + r * L::kRow + place<true>(r, 2 * (4 * wn + t) + i));
+                  y[4 * i] = __uint_as_float(v.x), y[4 * i + 1] = __uint_as_float(v.y);
+                  y[4 * i + 2] = __uint_as_float(v.z), y[4 * i + 3] = __uint_as_float(v.w);
+                }
+              } else {
+                const uint4 v = lds128_a(act + r * L::kRow + place<false>(r, 4 * wn + t));
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 f = half2_floats(u[i]);
+                  y[2 * i] = f.x, y[2 * i + 1] = f.y;
+                }
+              }
+            } else {
+              const T* p = static_cast<const T*>(a.base) + (int64_t)rows[r] * a.base_stride + n;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = a.base && i < width ? (float)p[i] : 0.0f;
+            }
+            if (rank > 0) {
+              const float f = factors[r];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = fmaf(d[i / 2][2 * h + i % 2], f, y[i]);
+            }
+            T* p = static_cast<T*>(a.out) + (int64_t)rows[r] * a.out_stride + n;
             if (out_vec && width == 8) {
               if constexpr (F32) {
                 *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
@@ -384,47 +498,61 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Lora a, int tiles,
           }
         }
       }
+      if (L::kTwo) {
+        __syncthreads();
+        issue(q + L::kAhead);
+      }
     }
     if (rank > 0) cluster_wait();
-    __syncthreads();
   }
 }
 
-template <int RB, int MT, bool F32>
-cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a, int subs, int cluster) {
-  using L = LoraSmem<RB, MT, F32>;
-  auto kern = lora_kernel<RB, MT, F32>;
+// Rows from which on tiles have 64 rows, and up to which a cluster finds its tile's adapters itself.
+constexpr int kManyRows = 1024, kFewRows = 64;
+
+template <int RB, int WM, bool F32>
+cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
+  using L = Geo<RB, WM, F32>;
+  auto kern = lora_kernel<RB, WM, F32>;
   static std::atomic<uint64_t> sized{0}, wide{0};
+  const int tiles = (a.M + L::TM - 1) / L::TM;
+  const bool listed = a.M > kFewRows;
+  const int cluster = a.M <= 16 ? 16 : 8, subs = a.M < 16 ? a.M : 16;
   cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
   if (e == cudaSuccess && cluster > 8) e = allow_wide_clusters(kern, ctx.device, wide);
   if (e != cudaSuccess) return e;
-  const int tiles = (a.M + 16 * MT - 1) / (16 * MT);
-  return launch_clusters(ctx, kern, cluster, dim3((unsigned)tiles * subs * cluster), dim3(kThreads), L::kBytes, a, tiles, subs, cluster,
-                         ctx.status);
-}
-
-template <int RB, int MT>
-cudaError_t launch_lora_rb(LaunchCtx& ctx, const Lora& a, int subs, int cluster) {
-  return a.f32 ? launch_lora_t<RB, MT, true>(ctx, a, subs, cluster) : launch_lora_t<RB, MT, false>(ctx, a, subs, cluster);
+  if (!listed)
+    return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(kThreads), L::kBytes, a, cluster, subs,
+                           (const uint32_t*)nullptr, (const Item*)nullptr, 0, ctx.status);
+  uint32_t* counts = static_cast<uint32_t*>(a.workspace);
+  Item* list = reinterpret_cast<Item*>(counts + 4);
+  e = launch_kernel(ctx, lora_list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, counts, list, a.M, ctx.status);
+  if (e != cudaSuccess) return e;
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;  // it waits for the list on the device
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(2 * ctx.num_sms / cluster * cluster)), dim3(kThreads), L::kBytes, a, cluster, 1,
+                      (const uint32_t*)counts, (const Item*)list, a.M, ctx.status);
+  ctx.pdl = pdl;
+  return e;
 }
 
 template <int RB>
-cudaError_t launch_lora_mt(LaunchCtx& ctx, const Lora& a) {
-  // Few rows: tiles of 16 and a cluster for each adapter that a tile can have; many: tiles of 64, whose adapters four
-  // clusters take in turn.
-  if (a.M <= 1024) return launch_lora_rb<RB, 1>(ctx, a, a.M < 16 ? a.M : 16, a.M <= 16 ? 16 : 8);
-  return launch_lora_rb<RB, 4>(ctx, a, 4, 8);
+cudaError_t launch_lora_r(LaunchCtx& ctx, const Lora& a) {
+  if (a.M <= kManyRows) return a.f32 ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 1, false>(ctx, a);
+  return a.f32 ? launch_lora_t<RB, 4, true>(ctx, a) : launch_lora_t<RB, 4, false>(ctx, a);
 }
 
 }  // namespace
 
+size_t lora_workspace_bytes(int M) { return M > kFewRows ? 16 + (size_t)M * sizeof(Item) : 0; }
+
 cudaError_t launch_lora(LaunchCtx& ctx, const Lora& a) {
   ctx.variant = a.f32 ? "lora_f32" : "lora_f16";
-  if (a.max_rank <= 8) return launch_lora_mt<1>(ctx, a);
-  if (a.max_rank <= 16) return launch_lora_mt<2>(ctx, a);
-  if (a.max_rank <= 32) return launch_lora_mt<4>(ctx, a);
-  if (a.max_rank <= 64) return launch_lora_mt<8>(ctx, a);
-  return launch_lora_mt<16>(ctx, a);
+  if (a.max_rank <= 8) return launch_lora_r<1>(ctx, a);
+  if (a.max_rank <= 16) return launch_lora_r<2>(ctx, a);
+  if (a.max_rank <= 32) return launch_lora_r<4>(ctx, a);
+  if (a.max_rank <= 64) return launch_lora_r<8>(ctx, a);
+  return launch_lora_r<16>(ctx, a);
 }
 
 }  // namespace mnb

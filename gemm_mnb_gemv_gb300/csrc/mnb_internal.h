@@ -164,8 +164,10 @@ struct Lora {
   int N;
   void* out;
   int64_t out_stride;
+  void* workspace;
 };
 cudaError_t launch_lora(LaunchCtx& ctx, const Lora& a);
+size_t lora_workspace_bytes(int M);
 
 // Probabilities and verification of drafted tokens (mnb.h).
 struct Softmax {

@@ -457,11 +457,14 @@ typedef struct {
  * leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
  * Products and sums are fp32. MNB_F16: down . x is rounded to fp16 relative to the row's largest (2^-11), as the result is;
  * MNB_F32: x and down . x enter the products with 22 bits or more. A row of x with inf or NaN gives non-finite outputs in that row.
- * M = 0 is valid and does nothing.
+ * `workspace` holds mnb_lora_workspace_bytes(M) bytes (0 up to 64 rows); its contents need no initialisation and are overwritten by
+ * each call, so calls sharing one workspace must be ordered on one stream (from any host threads). M = 0 is valid and does
+ * nothing.
  */
+MNB_API size_t mnb_lora_workspace_bytes(int M);
 MNB_API mnb_status mnb_lora(const void *x, int dtype, int M, int K, int64_t x_stride, mnb_lora_pool pool,
-                            const int32_t *adapter, const void *base, int64_t base_stride, int N, void *out,
-                            int64_t out_stride, mnb_stream stream);
+                            const int32_t *adapter, const void *base, int64_t base_stride, int N, void *workspace,
+                            size_t ws_bytes, void *out, int64_t out_stride, mnb_stream stream);
 
 /*
  * Probabilities: out[r, j] = e^((x[r, j] - max_j x) / temperature[r]) / sum_j, fp32 [rows, V], contiguous. logits x [rows, V]

@@ -72,15 +72,18 @@ def test_oracle_lora_against_dense_products():
     (dict(base=96, out=96, base_stride=9), 1, "out_stride"),
     (dict(out=None), 1, "out is NULL"),
     (dict(out_stride=6), 1, "out_stride"),
+    (dict(M=300, ws_bytes=300 * 16 + 15), 1, "workspace"),
+    (dict(M=300, workspace=None), 1, "workspace"),
+    (dict(M=300, workspace=72), 3, "workspace"),
 ])
 def test_lora_refusals(lib, change, expect, word):
     import gemm_mnb_gemv_gb300 as mnb
     a = dict(x=64, dtype=0, M=3, K=48, x_stride=48, down=64, up=64, ranks=None, scales=None, count=2, rank=16, adapter=64, base=64,
-             base_stride=7, N=7, out=128, out_stride=7)
+             base_stride=7, N=7, workspace=64, ws_bytes=1 << 40, out=128, out_stride=7)
     a.update(change)
     pool = mnb.MnbLoraPoolArg(a["down"], a["up"], a["ranks"], a["scales"], a["count"], a["rank"])
     st = lib.mnb_lora(P(a["x"]), a["dtype"], a["M"], a["K"], a["x_stride"], pool, P(a["adapter"]), P(a["base"]), a["base_stride"],
-                      a["N"], P(a["out"]), a["out_stride"], None)
+                      a["N"], P(a["workspace"]), a["ws_bytes"], P(a["out"]), a["out_stride"], None)
     assert st == expect, mnb.mnb_last_error()
     assert mnb.mnb_last_error().startswith("mnb_lora") and word in mnb.mnb_last_error()
 
@@ -133,10 +136,15 @@ def test_verify_refusals(lib, change, expect, word):
     assert mnb.mnb_last_error().startswith("mnb_verify") and word in mnb.mnb_last_error()
 
 
+def test_lora_workspace_bytes(lib):
+    assert [lib.mnb_lora_workspace_bytes(M) for M in (-1, 0, 1, 64, 65, 1 << 20, (1 << 20) + 1)] == [
+        0, 0, 0, 0, 16 * 66, 16 * ((1 << 20) + 1), 0]
+
+
 def test_no_rows_is_valid(lib):
     import gemm_mnb_gemv_gb300 as mnb
     pool = mnb.MnbLoraPoolArg(None, None, None, None, 1, 8)
-    assert lib.mnb_lora(None, 0, 0, 16, 16, pool, None, None, 0, 1, None, 1, None) == 0
+    assert lib.mnb_lora(None, 0, 0, 16, 16, pool, None, None, 0, 1, None, 0, None, 1, None) == 0
     assert lib.mnb_softmax(None, 0, 0, 1, 1, None, None, None) == 0
     assert lib.mnb_verify(None, 0, None, 0, None, None, None, None, 0, 0, 1, None, None, None) == 0
 
