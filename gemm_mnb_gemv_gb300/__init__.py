@@ -14,7 +14,8 @@ The names match the C entry points: ``mnb_dequant``, ``mnb_repacked_bytes``,
 ``mnb_act_order_workspace_bytes``, ``mnb_gemm_act_order``, ``mnb_gemm_act_order_noalloc``,
 ``mnb_kv4_cache_bytes``, ``mnb_kv4_append``, ``mnb_kv4_read``, ``mnb_kv4_attention_workspace_bytes``,
 ``mnb_kv4_attention`` (with ``MnbKv4Cache``, the handle of a cache, and ``mnb_kv4_cache_alloc``),
-``mnb_lora_workspace_bytes``, ``mnb_lora`` (with ``MnbLoraPool``, the handle of a layer's adapters), ``mnb_softmax``, ``mnb_verify``,
+``mnb_lora_workspace_bytes``, ``mnb_lora`` (with ``MnbLoraPool``, the handle of a layer's adapters), ``mnb_softmax_workspace_bytes``,
+``mnb_softmax``, ``mnb_verify_workspace_bytes``, ``mnb_verify``,
 ``mnb_set_programmatic_launch``,
 ``mnb_check_device_status``,
 ``mnb_last_error``,
@@ -104,8 +105,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                       ctypes.c_float, c_int, c_int, vp, c_size, vp, vp, vp]),
         "mnb_lora_workspace_bytes": (c_size, [c_int]),
         "mnb_lora": (c_int, [vp, c_int, c_int, c_int, i64, MnbLoraPoolArg, vp, vp, i64, c_int, vp, c_size, vp, i64, vp]),
-        "mnb_softmax": (c_int, [vp, c_int, c_int, c_int, i64, vp, vp, vp]),
-        "mnb_verify": (c_int, [vp, i64, vp, i64, vp, vp, vp, vp, c_int, c_int, c_int, vp, vp, vp]),
+        "mnb_softmax_workspace_bytes": (c_size, [c_int, c_int]),
+        "mnb_softmax": (c_int, [vp, c_int, c_int, c_int, i64, vp, vp, c_size, vp, vp]),
+        "mnb_verify_workspace_bytes": (c_size, [c_int, c_int]),
+        "mnb_verify": (c_int, [vp, i64, vp, i64, vp, vp, vp, vp, c_int, c_int, c_int, vp, c_size, vp, vp, vp]),
         "mnb_set_programmatic_launch": (None, [c_int]),
         "mnb_check_device_status": (c_int, []),
         "mnb_selftest_wait_timeout": (c_int, [ctypes.c_uint, vp]),
@@ -683,7 +686,7 @@ def mnb_kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads
     return int(load_library().mnb_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, dtype))
 
 
-_default_workspace = {}  # by device: of mnb_kv4_attention's calls on its default stream, 43 MB at most
+_default_workspace = {}  # by device: of the calls on its default stream that want one
 
 
 def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale: float, causal: bool = True,
@@ -692,7 +695,7 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
 
     ``q_start`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]``, ``page_table`` int32 ``[batch, pages]``.
     Without ``workspace``, calls on the device's default stream share one that is kept (the largest asked for so far, 43 MB
-    at most), and calls on other streams allocate theirs. One workspace may serve calls of several threads on one stream.
+    at most for attention), and calls on other streams allocate theirs. One workspace may serve calls of several threads on one stream.
     """
     torch = _torch()
     if q is None or kv_len is None or page_table is None or q.dim() != 3 or kv_len.dim() != 1 or page_table.dim() != 2:
@@ -747,13 +750,15 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
 # ---------------------------------------------------------------------------
 
 
-def _device_of(name, t):
-    """``(device, guard)`` of the tensor that a call goes by: the guard is None where there is one GPU."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
-    dev = t.get_device()
-    return dev, dev if _gpu_count() > 1 else None
+_gpus = None  # asked for once: 1 to 2 us of a call
+
+
+def _guard_of(dev: int):
+    """What tensors and the current device are compared with in each call: None where there is one GPU."""
+    global _gpus
+    if _gpus is None:
+        _gpus = _gpu_count()
+    return dev if _gpus > 1 else None
 
 
 def _on(name, t, dtype, guard):
@@ -767,20 +772,31 @@ def _on(name, t, dtype, guard):
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{guard}")
 
 
-def _matrix(name, t, rows, cols, dtype, guard):
-    """Elements between the rows of a CUDA tensor ``[rows, cols]`` whose rows are contiguous."""
-    _on(name, t, dtype, guard)
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} must be {[rows, cols]}, got {list(t.shape)}")
+def _two_dims(name, t, what):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be {what}, got {list(t.shape)}")
+    return t.shape
+
+
+def _matrix(name, t, shape, dtype, guard):
+    """Elements between the rows of a CUDA tensor of this type and shape whose rows are contiguous."""
+    if t is None or t.dtype != dtype or not t.is_cuda or guard is not None:
+        _on(name, t, dtype, guard)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     s0, s1 = t.stride()
-    if s1 != 1 and cols > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must lie one after the other")
-    return s0 if rows > 1 else cols
+    return s0 if shape[0] > 1 else shape[1]
 
 
 def _vector(name, t, dtype, shape, guard):
     """Address of a contiguous CUDA tensor of this type and shape."""
-    _on(name, t, dtype, guard)
+    if t is None or t.dtype != dtype or not t.is_cuda or guard is not None:
+        _on(name, t, dtype, guard)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
@@ -792,6 +808,28 @@ def _stream_of(dev, stream):
     if stream is not None and stream.device.index != dev:
         raise ValueError(f"stream is of {stream.device}, the tensors on cuda:{dev}")
     return _raw_stream(dev, stream)
+
+
+def _room(workspace, need, device, dev, stream, raw_stream, guard):
+    """The workspace, or one of ``need`` bytes: the kept one on the default stream, as in the attention, else a new one of the
+    stream's pool.  The caller holds it until the launch, so that no other allocation of the call gets its bytes."""
+    torch = _torch()
+    if workspace is not None:
+        _check_dev("workspace", workspace)
+        _on("workspace", workspace, workspace.dtype, guard)
+        return workspace
+    if need == 0:
+        return None
+    if stream is None and raw_stream == 0:
+        workspace = _default_workspace.get(dev)
+        if workspace is None or workspace.numel() < need:
+            workspace = _default_workspace[dev] = _new(need, torch.uint8, device, None)
+        return workspace
+    return _new(need, torch.uint8, device, stream)
+
+
+def _room_args(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
 
 
 def _launch(fn, args, dev, guard):
@@ -806,9 +844,13 @@ class MnbLoraPool:
 
     def __init__(self, down, up, ranks=None, scales=None):
         torch = _torch()
-        self.device, self.guard = _device_of("down", down)
-        if down.dim() != 3 or not isinstance(up, torch.Tensor) or up.dim() != 3:
+        for name, t in (("down", down), ("up", up)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor, got {None if t is None else type(t).__name__}")
+        if down.dim() != 3 or up.dim() != 3:
             raise ValueError("down and up must be [count, max_rank, K] and [count, N, max_rank]")
+        self.device = down.get_device()
+        self.guard = guard = _guard_of(self.device)
         count, max_rank, self.K = down.shape
         self.N = up.shape[1]
         if count < 1 or count > 1 << 20 or max_rank % 8 or not 8 <= max_rank <= 128:
@@ -816,10 +858,10 @@ class MnbLoraPool:
                            "multiple of 8 in 8..128)")
         self.down, self.up, self.ranks, self.scales = down, up, ranks, scales
         self.arg = MnbLoraPoolArg(
-            _vector("down", down, torch.float16, (count, max_rank, self.K), self.guard),
-            _vector("up", up, torch.float16, (count, self.N, max_rank), self.guard),
-            None if ranks is None else _vector("ranks", ranks, torch.int32, (count,), self.guard),
-            None if scales is None else _vector("scales", scales, torch.float32, (count,), self.guard), count, max_rank)
+            _vector("down", down, torch.float16, (count, max_rank, self.K), guard),
+            _vector("up", up, torch.float16, (count, self.N, max_rank), guard),
+            None if ranks is None else _vector("ranks", ranks, torch.int32, (count,), guard),
+            None if scales is None else _vector("scales", scales, torch.float32, (count,), guard), count, max_rank)
 
 
 def mnb_lora_workspace_bytes(M: int) -> int:
@@ -828,72 +870,87 @@ def mnb_lora_workspace_bytes(M: int) -> int:
 
 def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, workspace=None, out=None, stream=None):
     """``[M, N]`` = ``base`` (None: zeros) + each row's adapter on ``x`` ``[M, K]``; ``adapter`` int32 ``[M]``, -1 for none.
-    ``out`` may be ``base``."""
+    ``out`` may be ``base``.  A workspace is shared or allocated as in ``mnb_kv4_attention``."""
     torch = _torch()
-    dev, guard = pool.device, pool.guard
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError(f"x must be [M, {pool.K}]")
-    M, K, N, dtype, dt = x.shape[0], pool.K, pool.N, x.dtype, _act_dtype("x", x)
-    xs = _matrix("x", x, M, K, dtype, guard)
-    bs = 0 if base is None else _matrix("base", base, M, N, dtype, guard)
+    dev, guard, K, N = pool.device, pool.guard, pool.K, pool.N
+    M = _two_dims("x", x, f"[M, {K}]")[0]
+    dtype, dt = x.dtype, _act_dtype("x", x)
+    xs = _matrix("x", x, (M, K), dtype, guard)
+    shape = (M, N)
+    bs = bp = None
+    if base is not None:
+        bs, bp = _matrix("base", base, shape, dtype, guard), base.data_ptr()
     if out is None:
-        out = _new((M, N), dtype, x.device, stream)
-    os_ = _matrix("out", out, M, N, dtype, guard)
-    lib = load_library()
-    if workspace is None:
-        need = lib.mnb_lora_workspace_bytes(_size(M))
-        if need:
-            workspace = _new(need, torch.uint8, x.device, stream)
+        out, os_ = _new(shape, dtype, x.device, stream), N
     else:
-        _check_dev("workspace", workspace)
-        _on("workspace", workspace, workspace.dtype, guard)
-    wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard),
-            None if base is None else base.data_ptr(), bs, _size(N), wp, ws_bytes, out.data_ptr(), os_, _stream_of(dev, stream))
+        os_ = _matrix("out", out, shape, dtype, guard)
+    lib, raw_stream = load_library(), _stream_of(dev, stream)
+    need = 0 if M <= 64 and workspace is None else lib.mnb_lora_workspace_bytes(_size(M))
+    workspace = _room(workspace, need, x.device, dev, stream, raw_stream, guard)
+    args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard), bp, bs or 0,
+            _size(N), *_room_args(workspace), out.data_ptr(), os_, raw_stream)
     _launch(lib.mnb_lora, args, dev, guard)
     return out
 
 
-def mnb_softmax(logits, temperature=None, out=None, stream=None):
-    """fp32 ``[rows, V]``: softmax of ``logits / temperature`` (fp32 ``[rows]``, None: 1; 0: 1 at the largest logit)."""
+def mnb_softmax_workspace_bytes(rows: int, V: int) -> int:
+    return int(load_library().mnb_softmax_workspace_bytes(_size(rows), _size(V)))
+
+
+def mnb_softmax(logits, temperature=None, workspace=None, out=None, stream=None):
+    """fp32 ``[rows, V]``: softmax of ``logits / temperature`` (fp32 ``[rows]``, None: 1; 0: 1 at the largest logit).  A
+    workspace is shared or allocated as in ``mnb_kv4_attention``."""
     torch = _torch()
-    dev, guard = _device_of("logits", logits)
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [rows, V], got {list(logits.shape)}")
-    (rows, V), dt = logits.shape, _act_dtype("logits", logits)
-    stride = _matrix("logits", logits, rows, V, logits.dtype, guard)
+    shape = rows, V = _two_dims("logits", logits, "[rows, V]")
+    dev = logits.get_device()
+    guard = _guard_of(dev)
+    dt = _act_dtype("logits", logits)
+    stride = _matrix("logits", logits, shape, logits.dtype, guard)
+    tp = None if temperature is None else _vector("temperature", temperature, torch.float32, (rows,), guard)
+    lib, raw_stream = load_library(), _stream_of(dev, stream)
     if out is None:
-        out = _new((rows, V), torch.float32, logits.device, stream)
-    args = (logits.data_ptr(), dt, _size(rows), _size(V), stride,
-            None if temperature is None else _vector("temperature", temperature, torch.float32, (rows,), guard),
-            _vector("out", out, torch.float32, (rows, V), guard), _stream_of(dev, stream))
-    _launch(load_library().mnb_softmax, args, dev, guard)
+        out = _new(shape, torch.float32, logits.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _vector("out", out, torch.float32, shape, guard)
+    workspace = _room(workspace, lib.mnb_softmax_workspace_bytes(_size(rows), _size(V)), logits.device, dev, stream, raw_stream, guard)
+    args = (logits.data_ptr(), dt, _size(rows), _size(V), stride, tp, *_room_args(workspace), op, raw_stream)
+    _launch(lib.mnb_softmax, args, dev, guard)
     return out
 
 
-def mnb_verify(target, draft, draft_tokens, draft_start, u_accept, u_next, tokens=None, accepted=None, stream=None):
+def mnb_verify_workspace_bytes(batch: int, V: int) -> int:
+    return int(load_library().mnb_verify_workspace_bytes(_size(batch), _size(V)))
+
+
+def mnb_verify(target, draft, draft_tokens, draft_start, u_accept, u_next, workspace=None, tokens=None, accepted=None, stream=None):
     """``(tokens, accepted)``: int32 ``[drafted + batch]`` in the order of ``target``'s rows (a sequence's accepted tokens, the
     next one, then -1) and int32 ``[batch]``.
 
     ``target`` fp32 ``[drafted + batch, V]``, ``draft`` fp32 ``[drafted, V]`` or None (each row 1 at its token),
     ``draft_tokens`` int32 and ``u_accept`` fp32 ``[drafted]``, ``draft_start`` int32 ``[batch + 1]``, ``u_next`` fp32 ``[batch]``.
+    A workspace is shared or allocated as in ``mnb_kv4_attention``.
     """
     torch = _torch()
-    dev, guard = _device_of("target", target)
-    if target.dim() != 2 or any(not isinstance(t, torch.Tensor) or t.dim() != 1 for t in (draft_tokens, u_next)):
+    rows, V = _two_dims("target", target, "[drafted + batch, V]")
+    if any(not isinstance(t, torch.Tensor) or t.dim() != 1 for t in (draft_tokens, u_next)):
         raise ValueError("target, draft_tokens and u_next must be [drafted + batch, V], [drafted] and [batch]")
-    D, B, V = draft_tokens.shape[0], u_next.shape[0], target.shape[1]
-    f32, i32 = torch.float32, torch.int32
-    ts = _matrix("target", target, D + B, V, f32, guard)
-    ds = 0 if draft is None else _matrix("draft", draft, D, V, f32, guard)
+    D, B = draft_tokens.shape[0], u_next.shape[0]
+    dev = target.get_device()
+    guard, f32, i32 = _guard_of(dev), torch.float32, torch.int32
+    ts = _matrix("target", target, (D + B, V), f32, guard)
+    ds, dp = 0, None
+    if draft is not None:
+        ds, dp = _matrix("draft", draft, (D, V), f32, guard), draft.data_ptr()
+    given = [_vector("draft_tokens", draft_tokens, i32, (D,), guard), _vector("draft_start", draft_start, i32, (B + 1,), guard),
+             _vector("u_accept", u_accept, f32, (D,), guard), _vector("u_next", u_next, f32, (B,), guard)]
+    lib, raw_stream = load_library(), _stream_of(dev, stream)
+    workspace = _room(workspace, lib.mnb_verify_workspace_bytes(_size(B), _size(V)), target.device, dev, stream, raw_stream, guard)
     if tokens is None:
         tokens = _new((D + B,), i32, target.device, stream)
     if accepted is None:
         accepted = _new((B,), i32, target.device, stream)
-    args = (target.data_ptr(), ts, None if draft is None else draft.data_ptr(), ds,
-            _vector("draft_tokens", draft_tokens, i32, (D,), guard), _vector("draft_start", draft_start, i32, (B + 1,), guard),
-            _vector("u_accept", u_accept, f32, (D,), guard), _vector("u_next", u_next, f32, (B,), guard), _size(B), _size(D),
-            _size(V), _vector("tokens", tokens, i32, (D + B,), guard), _vector("accepted", accepted, i32, (B,), guard),
-            _stream_of(dev, stream))
-    _launch(load_library().mnb_verify, args, dev, guard)
+    args = (target.data_ptr(), ts, dp, ds, *given, _size(B), _size(D), _size(V), *_room_args(workspace),
+            _vector("tokens", tokens, i32, (D + B,), guard), _vector("accepted", accepted, i32, (B,), guard), raw_stream)
+    _launch(lib.mnb_verify, args, dev, guard)
     return tokens, accepted

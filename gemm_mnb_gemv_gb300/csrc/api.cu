@@ -817,6 +817,16 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
 
 namespace {
 
+// As in the attention: the launches of a call that has a workspace come one after the other, whatever other host threads do
+// on the stream.
+std::mutex g_two_launches;
+
+mnb_status check_workspace(const char* fn, const void* workspace, size_t ws_bytes, size_t need) {
+  if (ws_bytes < need)
+    return fail(MNB_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  return need > 0 ? check_ptr(fn, "workspace", workspace) : MNB_OK;
+}
+
 // Rows of `cols` elements that lie `stride` elements apart; each at 16 bytes when `whole` is set.
 mnb_status check_rows(const char* fn, const char* name, int64_t stride, int cols, int bytes, bool whole) {
   if (stride < cols || stride > (int64_t)1 << 40)
@@ -868,23 +878,23 @@ mnb_status mnb_lora(const void* x, int dtype, int M, int K, int64_t x_stride, mn
   if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
   if ((st = check_rows(fn, "out_stride", out_stride, N, e, false)) != MNB_OK) return st;
   const size_t need = mnb_lora_workspace_bytes(M);
-  if (ws_bytes < need)
-    return fail(MNB_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
-  if (need > 0 && (st = check_ptr(fn, "workspace", workspace)) != MNB_OK) return st;
+  if ((st = check_workspace(fn, workspace, ws_bytes, need)) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
   const mnb::Lora a = {x,       dtype == MNB_F32, M,           K,          x_stride, pool.down,     pool.up,
                        pool.ranks, pool.scales,   pool.count,  pool.max_rank, adapter, base,     base_stride,
                        N,       out,              out_stride,  workspace};
-  if (need == 0) return finish(fn, mnb::launch_lora(ctx, a), ctx);
-  // As in the attention: a call's launches come one after the other, whatever other host threads do on the stream.
-  static std::mutex two_launches;
-  std::lock_guard<std::mutex> lock(two_launches);
+  std::unique_lock<std::mutex> lock(g_two_launches, std::defer_lock);
+  if (need > 0) lock.lock();
   return finish(fn, mnb::launch_lora(ctx, a), ctx);
 }
 
-mnb_status mnb_softmax(const void* logits, int dtype, int rows, int V, int64_t stride, const float* temperature, float* out,
-                       mnb_stream stream) {
+size_t mnb_softmax_workspace_bytes(int rows, int V) {
+  return rows < 1 || rows > kMaxM || V < 1 || V > kMaxKN ? 0 : mnb::softmax_workspace_bytes(rows, V);
+}
+
+mnb_status mnb_softmax(const void* logits, int dtype, int rows, int V, int64_t stride, const float* temperature,
+                       void* workspace, size_t ws_bytes, float* out, mnb_stream stream) {
   const char* fn = "mnb_softmax";
   mnb_status st;
   if ((st = check_dtype(fn, dtype)) != MNB_OK) return st;
@@ -898,15 +908,26 @@ mnb_status mnb_softmax(const void* logits, int dtype, int rows, int V, int64_t s
   if ((st = check_rows(fn, "stride", stride, V, 4, false)) != MNB_OK) return st;
   if (temperature && (st = check_ptr(fn, "temperature", temperature)) != MNB_OK) return st;
   if ((st = check_ptr(fn, "out", out)) != MNB_OK) return st;
+  if ((int64_t)rows * V > (int64_t)1 << 42)
+    return fail(MNB_ERR_UNSUPPORTED, "%s: rows=%d of V=%d are more than one launch takes", fn, rows, V);
+  const size_t need = mnb_softmax_workspace_bytes(rows, V);
+  if ((st = check_workspace(fn, workspace, ws_bytes, need)) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
-  const mnb::Softmax a = {logits, dtype == MNB_F32, rows, V, stride, temperature, out};
+  const mnb::Softmax a = {logits, dtype == MNB_F32, rows, V, stride, temperature, out, workspace};
+  std::unique_lock<std::mutex> lock(g_two_launches, std::defer_lock);
+  if (need > 0) lock.lock();
   return finish(fn, mnb::launch_softmax(ctx, a), ctx);
+}
+
+size_t mnb_verify_workspace_bytes(int batch, int V) {
+  return batch < 1 || batch > kMaxM || V < 1 || V > kMaxKN ? 0 : mnb::verify_workspace_bytes(batch, V);
 }
 
 mnb_status mnb_verify(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
                       const int32_t* draft_tokens, const int32_t* draft_start, const float* u_accept, const float* u_next,
-                      int batch, int drafted, int V, int32_t* tokens, int32_t* accepted, mnb_stream stream) {
+                      int batch, int drafted, int V, void* workspace, size_t ws_bytes, int32_t* tokens, int32_t* accepted,
+                      mnb_stream stream) {
   const char* fn = "mnb_verify";
   mnb_status st;
   if (batch < 0 || batch > kMaxM) return fail(MNB_ERR_INVALID_ARG, "%s: batch=%d must be in [0, 2^20]", fn, batch);
@@ -929,10 +950,14 @@ mnb_status mnb_verify(const float* target, int64_t target_stride, const float* d
   if ((st = check_ptr(fn, "u_next", u_next)) != MNB_OK) return st;
   if ((st = check_ptr(fn, "tokens", tokens)) != MNB_OK) return st;
   if ((st = check_ptr(fn, "accepted", accepted)) != MNB_OK) return st;
+  if ((int64_t)batch * V > (int64_t)1 << 42)
+    return fail(MNB_ERR_UNSUPPORTED, "%s: batch=%d rows of V=%d are more than one launch takes", fn, batch, V);
+  if ((st = check_workspace(fn, workspace, ws_bytes, mnb_verify_workspace_bytes(batch, V))) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
   const mnb::Verify a = {target, target_stride, draft, draft_stride, draft_tokens, draft_start, u_accept,
-                         u_next, batch,         drafted, V,          tokens,       accepted};
+                         u_next, batch,         drafted, V,          tokens,       accepted, workspace};
+  std::lock_guard<std::mutex> lock(g_two_launches);
   return finish(fn, mnb::launch_verify(ctx, a), ctx);
 }
 

@@ -1,8 +1,9 @@
 // From logits to verified tokens: probabilities at each row's temperature, and the verification of drafted tokens from
-// given random numbers.
+// given random numbers.  Rows that one CTA would be long at are cut into segments: a first launch takes every segment's
+// numbers, a second one, which depends on it, joins them.  (A cluster for each row in one launch was slower beyond a few rows: 16 CTAs that have to
+// start and meet together; 320 rows of 128256 took 67 us at its best size, one row the same.)
 #include <float.h>
 
-#include "cluster.cuh"
 #include "mnb_device.cuh"
 #include "mnb_internal.h"
 
@@ -10,11 +11,17 @@ namespace mnb {
 namespace {
 
 // ---------------------------------------------------------------------------------
-// Softmax: p = e^((x - max) / temperature) / sum.  A cluster has a row, its CTAs a part each: read once, kept in registers
-// (parts of up to 32 elements a thread; of rows beyond 16 such parts, read three times), largest and sum of the parts exchanged once.
-// Elements go in chunks of 8 that begin at 16-byte boundaries of the logits, whatever the row's own start.
+// Softmax: p = e^((x - max) / temperature) / sum.  Elements go in chunks of 8 that begin at 16-byte boundaries of the logits,
+// whatever the row's own start; a thread keeps its chunks in registers.
 // ---------------------------------------------------------------------------------
-constexpr int kHeld = 4;  // chunks that a thread keeps
+constexpr int kHeld = 4;           // chunks of a thread
+constexpr int kSegThreads = 256;   // of a segment: 8192 elements
+constexpr int kNone = 0x7fffffff;
+
+struct SoftPart {  // of a segment: largest, sum of the exponentials relative to it, first place of the largest
+  float m, s;
+  int at, pad;
+};
 
 __device__ __forceinline__ float nan_max(float a, float b) {
   float r;
@@ -28,32 +35,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-template <bool F32, int kThreads, bool kHold>
-__global__ void __launch_bounds__(kThreads) softmax_kernel(const Softmax a, int cluster) {
-  constexpr int kWarps = kThreads / 32, kNone = 0x7fffffff;
-  __shared__ float red[2][kWarps];
-  __shared__ int red_at[kWarps];
-  __shared__ float2 mine;
-  __shared__ int mine_at;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int part = cluster_ctarank(), r = blockIdx.x / cluster;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t in_at = (int64_t)r * a.stride, out_at = (int64_t)r * a.V;
-  const int skew = (int)(in_at % (F32 ? 4 : 8));  // chunk i is the elements 8 i - skew ..
-  const int chunks = (a.V + skew + 7) / 8;
-  const int c0 = (int)((int64_t)chunks * part / cluster), c1 = (int)((int64_t)chunks * (part + 1) / cluster);
-  const bool out_vec = ((out_at - skew) & 3) == 0;
-  const float temp = a.temperature ? a.temperature[r] : 1.0f;
-  auto load = [&](int c, float (&v)[8]) {
+// One row's place, temperature and chunks.
+template <bool F32>
+struct SoftRow {
+  const Softmax& a;
+  int64_t in_at, out_at;
+  int skew, chunks;  // chunk i is the elements 8 i - skew ..
+  __device__ __forceinline__ SoftRow(const Softmax& a_, int r) : a(a_), in_at((int64_t)r * a_.stride), out_at((int64_t)r * a_.V) {
+    skew = (int)(in_at % (F32 ? 4 : 8));
+    chunks = (a.V + skew + 7) / 8;
+  }
+  __device__ __forceinline__ void load(int c, float (&v)[8]) const {
     const int j = 8 * c - skew;
     if (j >= 0 && j + 8 <= a.V) {
       if constexpr (F32) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + in_at + j);
-        const float4 x = __ldg(p), y = __ldg(p + 1);
+        const float4 x = __ldcg(p), y = __ldcg(p + 1);
         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
       } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.logits) + in_at + j));
+        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.logits) + in_at + j));
         const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -66,102 +66,16 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(const Softmax a, int 
       for (int i = 0; i < 8; ++i) {
         v[i] = -INFINITY;
         if (j + i >= 0 && j + i < a.V) {
-          if constexpr (F32) v[i] = static_cast<const float*>(a.logits)[in_at + j + i];
-          else v[i] = __half2float(static_cast<const __half*>(a.logits)[in_at + j + i]);
+          if constexpr (F32) v[i] = __ldcg(static_cast<const float*>(a.logits) + in_at + j + i);
+          else v[i] = __half2float(__ldcg(static_cast<const __half*>(a.logits) + in_at + j + i));
         }
       }
     }
-  };
-  float held[kHold ? kHeld : 1][8];
-  // f(first element, values) of each of this thread's chunks
-  auto each = [&](auto f) {
-    if constexpr (kHold) {
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (c0 + tid + i * kThreads < c1) f(8 * (c0 + tid + i * kThreads) - skew, held[i]);
-    } else {
-      for (int c = c0 + tid; c < c1; c += kThreads) {
-        load(c, held[0]);
-        f(8 * c - skew, held[0]);
-      }
-    }
-  };
-  if constexpr (kHold) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (c0 + tid + i * kThreads < c1) load(c0 + tid + i * kThreads, held[i]);
   }
-  float top = -INFINITY;
-  each([&](int, const float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = nan_max(top, v[i]);
-  });
-  for (int o = 16; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  top = red[0][lane % kWarps];
-  for (int o = kWarps / 2; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
-  const float c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  int at = kNone;
-  if (temp == 0.0f) {
-    each([&](int j, const float (&v)[8]) {
-#pragma unroll
-      for (int i = 7; i >= 0; --i)
-        if (v[i] == top) at = min(at, j + i);
-    });
-    at = __reduce_min_sync(kFull, at);
-    if (lane == 0) red_at[warp] = at;
-  } else {
-    each([&](int, float (&v)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = ex2((v[i] - ref) * c);
-        if constexpr (kHold) v[i] = e;
-        sum += e;
-      }
-    });
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    if (lane == 0) red[1][warp] = sum;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    sum = red[1][lane % kWarps];
-    for (int o = kWarps / 2; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    at = __reduce_min_sync(kFull, red_at[lane % kWarps]);
-    if (lane == 0) mine = make_float2(top, sum), mine_at = top == -INFINITY ? kNone : at;
-  }
-  // ---- over the cluster: lane i reads part i ----
-  cluster_arrive();
-  cluster_wait();
-  float2 other = make_float2(-INFINITY, 0.0f);
-  int first = kNone;
-  if (lane < cluster) {
-    other = cluster_ld_f2(cluster_map(smem_u32(&mine), lane));
-    if (temp == 0.0f) first = cluster_ld_s32(cluster_map(smem_u32(&mine_at), lane));
-  }
-  cluster_arrive();
-  float all_top = other.x;
-  for (int o = 8; o; o >>= 1) all_top = nan_max(all_top, __shfl_xor_sync(kFull, all_top, o));
-  all_top = __shfl_sync(kFull, all_top, 0);
-  float all = other.x == -INFINITY ? 0.0f : other.y * ex2((other.x - all_top) * c);
-  for (int o = 8; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
-  all = __shfl_sync(kFull, all, 0);
-  first = __reduce_min_sync(kFull, other.x == all_top ? first : kNone);
-  const bool none = all_top == -INFINITY;  // no logit above -inf
-  const float all_ref = none ? 0.0f : all_top;
-  // what a held exponential is off by, and 1 / sum
-  const float factor = none ? 0.0f : kHold ? ex2((top - all_top) * c) / all : 1.0f / all;
-  each([&](int j, const float (&v)[8]) {
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (temp == 0.0f) p[i] = all_top != all_top ? NAN : j + i == first ? 1.0f : 0.0f;
-      else p[i] = (kHold ? v[i] : ex2((v[i] - all_ref) * c)) * factor;
-    }
+  __device__ __forceinline__ void store(int c, const float (&p)[8]) const {
+    const int j = 8 * c - skew;
     float* out = a.out + out_at + j;
-    if (out_vec && j >= 0 && j + 8 <= a.V) {
+    if (((out_at - skew) & 3) == 0 && j >= 0 && j + 8 <= a.V) {
       *reinterpret_cast<float4*>(out) = make_float4(p[0], p[1], p[2], p[3]);
       *reinterpret_cast<float4*>(out + 4) = make_float4(p[4], p[5], p[6], p[7]);
     } else {
@@ -169,18 +83,177 @@ __global__ void __launch_bounds__(kThreads) softmax_kernel(const Softmax a, int 
       for (int i = 0; i < 8; ++i)
         if (j + i >= 0 && j + i < a.V) out[i] = p[i];
     }
-  });
-  cluster_wait();
+  }
+};
+
+// 1 / temperature in powers of two, within what keeps 0 * it at 0 and -inf * it at -inf; NaN for what is no temperature.
+__device__ __forceinline__ float cold_factor(float temp) {
+  return temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
+}
+
+// Largest, its first place (temperature 0) or the sum of exponentials (else) of a CTA's chunks, for all its threads; the
+// exponentials replace the values.
+template <int kThreads>
+__device__ __forceinline__ SoftPart soft_part(float (&v)[kHeld][8], int n, int first, float temp, float c) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float red[2][kWarps];
+  __shared__ int red_at[kWarps];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  SoftPart r = {-INFINITY, 0.0f, kNone, 0};
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * kThreads < n)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r.m = nan_max(r.m, v[i][k]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) r.m = nan_max(r.m, __shfl_xor_sync(kFull, r.m, o));
+  if (lane == 0) red[0][warp] = r.m;
+  __syncthreads();
+  r.m = red[0][lane % kWarps];
+#pragma unroll
+  for (int o = kWarps / 2; o; o >>= 1) r.m = nan_max(r.m, __shfl_xor_sync(kFull, r.m, o));
+  if (temp == 0.0f) {
+#pragma unroll
+    for (int i = kHeld - 1; i >= 0; --i)
+      if (tid + i * kThreads < n)
+#pragma unroll
+        for (int k = 7; k >= 0; --k)
+          if (v[i][k] == r.m) r.at = first + 8 * (tid + i * kThreads) + k;
+    r.at = __reduce_min_sync(kFull, r.at);
+    if (lane == 0) red_at[warp] = r.at;
+    __syncthreads();
+    r.at = r.m == -INFINITY ? kNone : __reduce_min_sync(kFull, red_at[lane % kWarps]);
+  } else {
+    const float ref = r.m == -INFINITY ? 0.0f : r.m;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (tid + i * kThreads < n)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          v[i][k] = ex2((v[i][k] - ref) * c);
+          r.s += v[i][k];
+        }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
+    if (lane == 0) red[1][warp] = r.s;
+    __syncthreads();
+    r.s = red[1][lane % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
+  }
+  return r;
+}
+
+// Rows of up to kThreads * kHeld chunks: a CTA has one, and reads it once.
+template <bool F32, int kThreads>
+__global__ void __launch_bounds__(kThreads) softmax_row_kernel(const Softmax a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const SoftRow<F32> row(a, blockIdx.x);
+  const float temp = a.temperature ? a.temperature[blockIdx.x] : 1.0f;
+  float v[kHeld][8];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if ((int)threadIdx.x + i * kThreads < row.chunks) row.load(threadIdx.x + i * kThreads, v[i]);
+  const SoftPart all = soft_part<kThreads>(v, row.chunks, -row.skew, temp, cold_factor(temp));
+  const float inv = all.m == -INFINITY ? 0.0f : 1.0f / all.s;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = threadIdx.x + i * kThreads;
+    if (c < row.chunks) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (temp == 0.0f) v[i][k] = all.m != all.m ? NAN : 8 * c - row.skew + k == all.at ? 1.0f : 0.0f;
+        else v[i][k] *= inv;
+      }
+      row.store(c, v[i]);
+    }
+  }
+}
+
+// Longer rows: a CTA has a segment, in both launches.
+template <bool F32>
+__global__ void __launch_bounds__(kSegThreads) softmax_part_kernel(const Softmax a, int segs) {
+  pdl_wait();
+  pdl_launch_dependents();  // behind the wait: the next launch reads logits (past L1) before its own
+  const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
+  const SoftRow<F32> row(a, r);
+  const float temp = a.temperature ? a.temperature[r] : 1.0f;
+  const int c0 = (int)((int64_t)row.chunks * seg / segs), n = (int)((int64_t)row.chunks * (seg + 1) / segs) - c0;
+  float v[kHeld][8];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if ((int)threadIdx.x + i * kSegThreads < n) row.load(c0 + threadIdx.x + i * kSegThreads, v[i]);
+  const SoftPart part = soft_part<kSegThreads>(v, n, 8 * c0 - row.skew, temp, cold_factor(temp));
+  if (threadIdx.x == 0) static_cast<SoftPart*>(a.workspace)[blockIdx.x] = part;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kSegThreads) softmax_join_kernel(const Softmax a, int segs) {
+  pdl_launch_dependents();
+  const int r = blockIdx.x / segs, seg = blockIdx.x % segs, lane = threadIdx.x % 32;
+  const SoftRow<F32> row(a, r);
+  const float temp = a.temperature ? a.temperature[r] : 1.0f, c = cold_factor(temp);
+  const int c0 = (int)((int64_t)row.chunks * seg / segs), n = (int)((int64_t)row.chunks * (seg + 1) / segs) - c0;
+  float v[kHeld][8];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if ((int)threadIdx.x + i * kSegThreads < n) row.load(c0 + threadIdx.x + i * kSegThreads, v[i]);
+  pdl_wait();
+  const SoftPart* parts = static_cast<const SoftPart*>(a.workspace) + (int64_t)r * segs;
+  SoftPart all = {-INFINITY, 0.0f, kNone, 0};
+  for (int s = lane; s < segs; s += 32) {
+    const int4 u = *reinterpret_cast<const int4*>(parts + s);
+    const float m = __int_as_float(u.x), top = nan_max(all.m, m), ref = top == -INFINITY ? 0.0f : top;
+    if (m > all.m) all.at = u.z;
+    all.s = all.s * ex2((all.m - ref) * c) + __int_as_float(u.y) * ex2((m - ref) * c);
+    all.m = top;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float m = __shfl_xor_sync(kFull, all.m, o), s = __shfl_xor_sync(kFull, all.s, o);
+    const int at = __shfl_xor_sync(kFull, all.at, o);
+    const float top = nan_max(all.m, m), ref = top == -INFINITY ? 0.0f : top;
+    all.at = m > all.m ? at : m == all.m ? min(all.at, at) : all.at;
+    all.s = all.s * ex2((all.m - ref) * c) + s * ex2((m - ref) * c);
+    all.m = top;
+  }
+  const float ref = all.m == -INFINITY ? 0.0f : all.m, inv = all.m == -INFINITY ? 0.0f : 1.0f / all.s;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int k0 = threadIdx.x + i * kSegThreads;
+    if (k0 < n) {
+      const int ch = c0 + k0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (temp == 0.0f) v[i][k] = all.m != all.m ? NAN : 8 * ch - row.skew + k == all.at ? 1.0f : 0.0f;
+        else v[i][k] = ex2((v[i][k] - ref) * c) * inv;
+      }
+      row.store(ch, v[i]);
+    }
+  }
+}
+
+// Chunks of a row that one CTA takes, and segments of longer rows (0: one CTA).
+int soft_segments(int V) {
+  const int chunks = (V + 14) / 8;
+  return chunks <= 512 * kHeld ? 0 : (chunks + kSegThreads * kHeld - 1) / (kSegThreads * kHeld);
 }
 
 // ---------------------------------------------------------------------------------
-// Verification.  A cluster has a sequence.  Every warp finds the first rejected token by itself; then the warps of the
-// cluster share the row to draw from.
+// Verification.  Every CTA of a sequence's segments finds the first rejected token by itself and sums its segment of the
+// row to draw from; the second launch has a CTA for each sequence, which finds the segment, then the element.
 //
 // Weights are whole numbers of 2^-60 (probabilities are held to 0..1; what is below 2^-60 counts as 0): sums are exact in any
 // order, and the drawn token does not hang on how the row was cut. A row may add up to just below 16.
 // ---------------------------------------------------------------------------------
-constexpr int kVerifyWarps = 8;
+constexpr int kVerifyWarps = 8, kVerifyThreads = kVerifyWarps * 32;
+constexpr int kRun = 4;                                // chunks of 4 elements of a thread
+constexpr int kSegChunks = kVerifyThreads * kRun;      // of a segment: 4096 elements
+
+struct VerifyPart {  // of a segment: sums of max(p - q, 0) and of p
+  uint64_t w, p;
+};
 
 __device__ __forceinline__ uint64_t fixed60(float p) {
   const uint32_t b = __float_as_uint(__saturatef(p));  // NaN: 0
@@ -200,19 +273,62 @@ __device__ __forceinline__ uint64_t scaled(uint64_t total, float u) {
   return s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0;
 }
 
-__device__ __forceinline__ uint64_t shfl_up_u64(uint64_t v, int o) { return __shfl_up_sync(kFull, (unsigned long long)v, o); }
+__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int from) { return __shfl_sync(kFull, (unsigned long long)v, from); }
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, (unsigned long long)v, o);
   return v;
 }
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // of the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(kFull, (unsigned long long)v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
 
-__global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const Verify a, int cluster, uint32_t* status) {
+// The row to draw from, in chunks of 4 elements that begin at 16-byte boundaries of p (and of q, where its row lies alike).
+struct DrawRow {
+  const float *p, *q;  // q: null when all were accepted, or without draft rows
+  int V, not_this;     // not_this: the rejected token without draft rows, -1 else
+  int skew, chunks;
+  bool rejected, alike;
+  __device__ __forceinline__ DrawRow(const Verify& a, int b, int s0, int n, int accepted) : V(a.V) {
+    rejected = accepted < n;
+    const int64_t p_at = (int64_t)(s0 + b + accepted) * a.target_stride, q_at = (int64_t)(s0 + accepted) * a.draft_stride;
+    p = a.target + p_at;
+    q = rejected && a.draft ? a.draft + q_at : nullptr;
+    not_this = rejected && !a.draft ? a.tokens[s0 + accepted] : -1;
+    skew = (int)(p_at & 3);
+    alike = (q_at & 3) == skew;
+    chunks = (V + skew + 3) / 4;
+  }
+  __device__ __forceinline__ void load4(const float* row, int c, bool whole, float (&v)[4]) const {
+    const int j = 4 * c - skew;
+    if (whole && j >= 0 && j + 4 <= V) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(row + j));
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < V ? __ldg(row + j + i) : 0.0f;
+    }
+  }
+};
+
+__device__ __forceinline__ void sequence(const Verify& a, int b, int& s0, int& n) {
+  s0 = min(max(a.start[b], 0), a.drafted);
+  n = min(max(a.start[b + 1], s0), a.drafted) - s0;
+}
+
+__global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verify a, int segs, uint32_t* status) {
   __shared__ uint64_t sums[2][kVerifyWarps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int part = cluster_ctarank(), b = blockIdx.x / cluster;
+  const int b = blockIdx.x / segs, seg = blockIdx.x % segs;
   pdl_launch_dependents();
   pdl_wait();
-  const int s0 = min(max(a.start[b], 0), a.drafted), s1 = min(max(a.start[b + 1], s0), a.drafted), n = s1 - s0;
+  int s0, n;
+  sequence(a, b, s0, n);
   // ---- the first rejected token ----
   int accepted = n;
   for (int i0 = 0; i0 < n; i0 += 32) {
@@ -220,12 +336,13 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const Verify 
     bool bad = false;
     if (i < n) {
       const int tok = a.tokens[s0 + i];
+      const float u = __saturatef(a.u_accept[s0 + i]);
       bad = true;
       if (tok >= 0 && tok < a.V) {
         const float pt = __saturatef(a.target[(int64_t)(s0 + b + i) * a.target_stride + tok]);
         const float qt = a.draft ? __saturatef(a.draft[(int64_t)(s0 + i) * a.draft_stride + tok]) : 1.0f;
-        bad = !((double)__saturatef(a.u_accept[s0 + i]) * (double)qt < (double)pt);
-      } else if (part == 0 && warp == 0) {
+        bad = !((double)u * (double)qt < (double)pt);
+      } else if (seg == 0 && warp == 0) {
         report_status(status, kStatusBadIndex);
       }
     }
@@ -235,156 +352,177 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const Verify 
       break;
     }
   }
-  const bool rejected = accepted < n;
-  const float* p = a.target + (int64_t)(s0 + b + accepted) * a.target_stride;
-  const float* q = rejected && a.draft ? a.draft + (int64_t)(s0 + accepted) * a.draft_stride : nullptr;
-  const int not_this = rejected && !a.draft ? a.tokens[s0 + accepted] : -1;
-  // ---- sums of this warp's part of the row ----
-  // Chunks of 4 elements that begin at 16-byte boundaries of p (and of q, where its row lies alike).
-  const int skew = (int)((int64_t)(s0 + b + accepted) * a.target_stride & 3);
-  const bool alike = q && ((int64_t)(s0 + accepted) * a.draft_stride & 3) == skew;
-  const int chunks = (a.V + skew + 3) / 4;
-  const int parts = cluster * kVerifyWarps, own = part * kVerifyWarps + warp;
-  const int each = ((chunks + parts - 1) / parts + 31) / 32 * 32;
-  const int c0 = (int)min((int64_t)own * each, (int64_t)chunks), c1 = min(c0 + each, chunks);
-  auto load = [&](const float* row, int c, bool whole, float (&v)[4]) {
-    const int j = 4 * c - skew;
-    if (whole && j >= 0 && j + 4 <= a.V) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row + j));
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
+  // ---- sums of this segment ----
+  const DrawRow row(a, b, s0, n, accepted);
+  const int c0 = seg * kSegChunks + tid;
+  float pv[kRun][4], qv[kRun][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < a.V ? __ldg(row + j + i) : 0.0f;
+  for (int k = 0; k < kRun; ++k) {
+    const int c = c0 + k * kVerifyThreads;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
+    if (c < row.chunks) {
+      row.load4(row.p, c, true, pv[k]);
+      if (row.q) row.load4(row.q, c, row.alike, qv[k]);
     }
-  };
-  auto weight = [&](float pj, float qj, int j, bool residual) -> uint64_t {
-    const uint64_t f = fixed60(pj);
-    if (!residual) return f;
-    if (q) return sub_clamped(f, fixed60(qj));
-    return j == not_this ? 0 : f;
-  };
-  constexpr int kFlight = 4;
+  }
   uint64_t sum_w = 0, sum_p = 0;
-  for (int c = c0 + lane; c < c1; c += 32 * kFlight) {
-    float pv[kFlight][4], qv[kFlight][4];
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
+  for (int k = 0; k < kRun; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
-      if (c + 32 * k < c1) {
-        load(p, c + 32 * k, true, pv[k]);
-        if (q) load(q, c + 32 * k, alike, qv[k]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t f = fixed60(pv[k][i]);
+      sum_p += f;
+      if (row.q) sum_w += sub_clamped(f, fixed60(qv[k][i]));
+      else if (4 * (c0 + k * kVerifyThreads) - row.skew + i != row.not_this) sum_w += f;
     }
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t f = fixed60(pv[k][i]);
-        sum_p += f;
-        if (q) sum_w += sub_clamped(f, fixed60(qv[k][i]));
-        else if (4 * (c + 32 * k) - skew + i != not_this) sum_w += f;
-      }
-  }
-  sum_p = warp_sum(sum_p), sum_w = warp_sum(sum_w);
+  sum_w = warp_sum(sum_w), sum_p = warp_sum(sum_p);
   if (lane == 0) sums[0][warp] = sum_w, sums[1][warp] = sum_p;
-  cluster_arrive();
-  cluster_wait();
-  // ---- all parts' sums; the part that the drawn one is in ----
-  uint64_t total[2] = {0, 0}, before[2] = {0, 0};
-  for (int i = lane; i < parts; i += 32) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint64_t v = cluster_ld_u64(cluster_map(smem_u32(&sums[k][i % kVerifyWarps]), i / kVerifyWarps));
-      total[k] += v;
-      if (i < own) before[k] += v;
-    }
+  __syncthreads();
+  if (tid == 0) {
+    VerifyPart r = {0, 0};
+    for (int w = 0; w < kVerifyWarps; ++w) r.w += sums[0][w], r.p += sums[1][w];
+    static_cast<VerifyPart*>(a.workspace)[blockIdx.x] = r;
+    if (seg == 0) a.accepted[b] = accepted;
   }
-  cluster_arrive();
-#pragma unroll
-  for (int k = 0; k < 2; ++k) total[k] = warp_sum(total[k]), before[k] = warp_sum(before[k]);
-  const bool residual = rejected && total[0] > 0;  // nothing left of p - q: drawn from p
-  const uint64_t all = residual ? total[0] : total[1], head = residual ? before[0] : before[1];
-  const uint64_t here = residual ? sum_w : sum_p;
-  const uint64_t limit = scaled(all, a.u_next[b]);
-  const int64_t at = (int64_t)s0 + b;
-  if (all > 0 && head <= limit && head + here > limit) {
-    uint64_t run = head;
-    for (int c = c0; c < c1; c += 32) {
-      float pv[4] = {}, qv[4] = {};
-      uint64_t w[4], inc = 0;
-      if (c + lane < c1) {
-        load(p, c + lane, true, pv);
-        if (q) load(q, c + lane, alike, qv);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = weight(pv[i], qv[i], 4 * (c + lane) - skew + i, residual);
-        inc += w[i];
-      }
-      const uint64_t mine = inc;
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t v = shfl_up_u64(inc, o);
-        if (lane >= o) inc += v;
-      }
-      const uint32_t past = __ballot_sync(kFull, run + inc > limit);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          uint64_t s = run + inc - mine;
-          int i = 0;
-          for (; i < 3; ++i) {
-            s += w[i];
-            if (s > limit) break;
-          }
-          a.out[at + accepted] = 4 * (c + lane) - skew + i;
-        }
-        break;
-      }
-      run += __shfl_sync(kFull, (unsigned long long)inc, 31);
-    }
-  }
-  if (own == 0) {
-    if (lane == 0) {
-      a.accepted[b] = accepted;
-      if (all == 0) a.out[at + accepted] = -1;
-    }
-    for (int i = lane; i <= n; i += 32)
-      if (i != accepted) a.out[at + i] = i < accepted ? a.tokens[s0 + i] : -1;
-  }
-  cluster_wait();
 }
 
-// CTAs of a cluster: enough of them for every SM, parts of at least `least` elements.
-int cluster_for(int rows, int V, int least, int num_sms) {
-  int c = 16;
-  while (c > 1 && ((int64_t)rows * (c / 2) >= 2 * num_sms || V / c < least)) c /= 2;
-  return c;
+__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verify a, int segs) {
+  __shared__ uint64_t runs[kVerifyWarps];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  int s0, n;
+  sequence(a, b, s0, n);
+  const int accepted = min(max(a.accepted[b], 0), n);  // the first launch's: in range unless the caller's buffers overlap
+  const float u = a.u_next[b];
+  const VerifyPart* parts = static_cast<const VerifyPart*>(a.workspace) + (int64_t)b * segs;
+  int32_t* out = a.out + s0 + b;
+  // ---- the row's total, then the segment that the drawn one is in; every warp finds it by itself ----
+  VerifyPart total = {0, 0}, first = {0, 0};
+  for (int s = lane; s < segs; s += 32) {
+    const VerifyPart v = parts[s];
+    if (s == lane) first = v;
+    total.w += v.w, total.p += v.p;
+  }
+  const DrawRow row(a, b, s0, n, accepted);
+  total.w = row.rejected ? warp_sum(total.w) : 0;
+  const bool residual = total.w > 0;  // nothing left of p - q: drawn from p
+  const uint64_t all = residual ? total.w : warp_sum(total.p);
+  const uint64_t limit = scaled(all, u);
+  uint64_t head = 0;
+  int seg = -1;
+  for (int i = 0; i < segs; i += 32) {
+    VerifyPart v = first;
+    if (i > 0 && i + lane < segs) v = parts[i + lane];
+    const uint64_t x = i + lane < segs ? residual ? v.w : v.p : 0, to = head + warp_scan(x, lane);
+    const uint32_t past = __ballot_sync(kFull, to > limit);
+    if (past) {
+      seg = i + __ffs(past) - 1;
+      head = shfl_u64(to - x, __ffs(past) - 1);
+      break;
+    }
+    head = shfl_u64(to, 31);
+  }
+  for (int i = tid; i <= n; i += kVerifyThreads)
+    if (i != accepted || all == 0) out[i] = i < accepted ? a.tokens[s0 + i] : -1;
+  if (seg < 0) return;
+  // ---- the element: each warp a run of the segment ----
+  const int c0 = seg * kSegChunks + warp * (32 * kRun);
+  uint64_t w[kRun][4], sum[kRun], mine = 0;
+  float pv[kRun][4], qv[kRun][4];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int c = c0 + 32 * k + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
+    if (c < row.chunks) {
+      row.load4(row.p, c, true, pv[k]);
+      if (row.q && residual) row.load4(row.q, c, row.alike, qv[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    sum[k] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[k][i] = fixed60(pv[k][i]);
+      if (residual && row.q) w[k][i] = sub_clamped(w[k][i], fixed60(qv[k][i]));
+      if (residual && 4 * (c0 + 32 * k + lane) - row.skew + i == row.not_this) w[k][i] = 0;
+      sum[k] += w[k][i];
+    }
+    mine += sum[k];
+  }
+  mine = warp_sum(mine);
+  if (lane == 0) runs[warp] = mine;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) head += runs[i];
+  if (head <= limit && head + mine > limit) {
+    bool done = false;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      if (!done) {
+        const uint64_t to = head + warp_scan(sum[k], lane);
+        const uint32_t past = __ballot_sync(kFull, to > limit);
+        if (past) {
+          done = true;
+          if (lane == __ffs(past) - 1) {
+            uint64_t s = to - sum[k];
+            int at = 3;
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {
+              uint64_t upto = s;
+#pragma unroll
+              for (int j = 0; j <= i; ++j) upto += w[k][j];
+              if (upto > limit) at = i;
+            }
+            out[accepted] = 4 * (c0 + 32 * k + lane) - row.skew + at;
+          }
+        }
+        head = shfl_u64(to, 31);
+      }
+    }
+  }
 }
+
+int verify_segments(int V) { return ((V + 6) / 4 + kSegChunks - 1) / kSegChunks; }
 
 }  // namespace
 
+size_t softmax_workspace_bytes(int rows, int V) { return (size_t)rows * soft_segments(V) * sizeof(SoftPart); }
+size_t verify_workspace_bytes(int batch, int V) { return (size_t)batch * verify_segments(V) * sizeof(VerifyPart); }
+
 cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a) {
-  int c = cluster_for(a.rows, a.V, 2048, ctx.num_sms);
-  while (c < 16 && a.V + 7 > c * 512 * kHeld * 8) c *= 2;
-  const bool hold = a.V + 7 <= c * 512 * kHeld * 8, few = (a.V + 7) / 8 <= c * 128 * kHeld - c;
   ctx.variant = a.f32 ? "softmax_f32" : "softmax_f16";
-  auto go = [&](auto kern, int threads, std::atomic<uint64_t>& wide) {
-    const cudaError_t e = c > 8 ? allow_wide_clusters(kern, ctx.device, wide) : cudaSuccess;
-    return e != cudaSuccess ? e : launch_clusters(ctx, kern, c, dim3((unsigned)a.rows * c), dim3(threads), 0, a, c);
-  };
-  static std::atomic<uint64_t> wide[6];
-  if (!hold) return a.f32 ? go(softmax_kernel<true, 512, false>, 512, wide[0]) : go(softmax_kernel<false, 512, false>, 512, wide[1]);
-  if (few) return a.f32 ? go(softmax_kernel<true, 128, true>, 128, wide[2]) : go(softmax_kernel<false, 128, true>, 128, wide[3]);
-  return a.f32 ? go(softmax_kernel<true, 512, true>, 512, wide[4]) : go(softmax_kernel<false, 512, true>, 512, wide[5]);
+  const int segs = soft_segments(a.V);
+  if (segs == 0) {
+    const bool few = (a.V + 14) / 8 <= 128 * kHeld;
+    auto go = [&](auto kern, int threads) { return launch_kernel(ctx, kern, dim3(a.rows), dim3(threads), 0, a); };
+    if (few) return a.f32 ? go(softmax_row_kernel<true, 128>, 128) : go(softmax_row_kernel<false, 128>, 128);
+    return a.f32 ? go(softmax_row_kernel<true, 512>, 512) : go(softmax_row_kernel<false, 512>, 512);
+  }
+  const dim3 grid((unsigned)a.rows * segs);
+  cudaError_t e = a.f32 ? launch_kernel(ctx, softmax_part_kernel<true>, grid, dim3(kSegThreads), 0, a, segs)
+                        : launch_kernel(ctx, softmax_part_kernel<false>, grid, dim3(kSegThreads), 0, a, segs);
+  if (e != cudaSuccess) return e;
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;  // the second launch waits for the first one on the device
+  e = a.f32 ? launch_kernel(ctx, softmax_join_kernel<true>, grid, dim3(kSegThreads), 0, a, segs)
+            : launch_kernel(ctx, softmax_join_kernel<false>, grid, dim3(kSegThreads), 0, a, segs);
+  ctx.pdl = pdl;
+  return e;
 }
 
 cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a) {
-  const int c = cluster_for(a.batch, a.V, 1024, ctx.num_sms);
   ctx.variant = "verify";
-  static std::atomic<uint64_t> wide{0};
-  const cudaError_t e = c > 8 ? allow_wide_clusters(verify_kernel, ctx.device, wide) : cudaSuccess;
+  const int segs = verify_segments(a.V);
+  cudaError_t e = launch_kernel(ctx, verify_part_kernel, dim3((unsigned)a.batch * segs), dim3(kVerifyThreads), 0, a, segs, ctx.status);
   if (e != cudaSuccess) return e;
-  return launch_clusters(ctx, verify_kernel, c, dim3((unsigned)a.batch * c), dim3(kVerifyWarps * 32), 0, a, c, ctx.status);
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;
+  e = launch_kernel(ctx, verify_draw_kernel, dim3(a.batch), dim3(kVerifyThreads), 0, a, segs);
+  ctx.pdl = pdl;
+  return e;
 }
 
 }  // namespace mnb

@@ -20,8 +20,6 @@
 namespace mnb {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -63,6 +61,7 @@ __device__ __forceinline__ void copy_wait() {
 // RB: ranks in eights; WM: row tiles of 16.
 template <int RB, int WM, bool F32>
 struct Geo {
+  static constexpr int kWarps = WM == 1 ? 4 : 8, kThreads = kWarps * 32;
   static constexpr int RP = RB * 8, TM = 16 * WM, WN = kWarps / WM;
   static constexpr int kSpan = 32 * WN;                       // of K or N in a stage
   static constexpr int kElem = F32 ? 4 : 2;
@@ -73,12 +72,14 @@ struct Geo {
   static constexpr int kPart = (WN - 1) * TM * RP * 4;        // partial sums of the warps; the CTA's own in the first
   static constexpr int kSRow = F32 ? RP * 4 + 8 : RP >= 64 ? RP * 2 + 64 : RP * 2;  // bytes of a row of s
   static constexpr int kS = (TM * kSRow + 127) / 128 * 128;
-  // Two CTAs an SM where two stages fit (113 KB each), else as many as one CTA can have.
-  static constexpr int fit(int budget) {
-    const int n = (budget - kPart - kS) / kStage;
-    return n > 4 ? 4 : n;
+  // Stages that fit when an SM holds n CTAs; as many CTAs as can have two (16 warps an SM are what registers allow).
+  static constexpr int fit(int n) {
+    const int stages = (228 * 1024 / n - 1024 - 768 - kPart - kS) / kStage;
+    return stages > 4 ? 4 : stages;
   }
-  static constexpr int kStages = fit(115200) >= 2 ? fit(115200) : fit(230400);
+  static constexpr int kMost = 16 / kWarps;
+  static constexpr int kCtas = fit(kMost) >= 2 ? kMost : kMost > 2 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;
+  static constexpr int kStages = fit(kCtas);
   static constexpr int kBytes = kStages * kStage + kPart + kS;
   static_assert(kStages >= 2, "one stage is read while the next one lands");
   // With two stages a slot is filled again behind a second barrier, as soon as it is free; with more, behind the next stage's.
@@ -144,11 +145,11 @@ __global__ void __launch_bounds__(1024) lora_list_kernel(const Lora a, uint32_t*
 }
 
 template <int RB, int WM, bool F32>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::kCtas)
     lora_kernel(const Lora a, int cluster, int subs, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
   using T = std::conditional_t<F32, float, __half>;
   using L = Geo<RB, WM, F32>;
-  constexpr int RP = L::RP, TM = L::TM, WN = L::WN, S = L::kStages;
+  constexpr int RP = L::RP, TM = L::TM, WN = L::WN, S = L::kStages, kThreads = L::kThreads;
   constexpr int E = RB >= 4 ? 8 : RB == 2 ? 4 : 2;  // elements of the rank that a lane has of a chunk of 4 E
   constexpr int KC = RP / (4 * E);
   extern __shared__ __align__(128) uint8_t smem[];
@@ -522,7 +523,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   if (e == cudaSuccess && cluster > 8) e = allow_wide_clusters(kern, ctx.device, wide);
   if (e != cudaSuccess) return e;
   if (!listed)
-    return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(kThreads), L::kBytes, a, cluster, subs,
+    return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, subs,
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, ctx.status);
   uint32_t* counts = static_cast<uint32_t*>(a.workspace);
   Item* list = reinterpret_cast<Item*>(counts + 4);
@@ -530,7 +531,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
-  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(2 * ctx.num_sms / cluster * cluster)), dim3(kThreads), L::kBytes, a, cluster, 1,
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(L::kCtas * ctx.num_sms / cluster * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
                       (const uint32_t*)counts, (const Item*)list, a.M, ctx.status);
   ctx.pdl = pdl;
   return e;

@@ -176,6 +176,7 @@ struct Softmax {
   int64_t stride;
   const float* temperature;
   float* out;
+  void* workspace;
 };
 struct Verify {
   const float* target;
@@ -186,9 +187,12 @@ struct Verify {
   const float *u_accept, *u_next;
   int batch, drafted, V;
   int32_t *out, *accepted;
+  void* workspace;
 };
 cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a);
 cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a);
+size_t softmax_workspace_bytes(int rows, int V);
+size_t verify_workspace_bytes(int batch, int V);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device: `done` is a static of the caller,
 // a bit for each device.

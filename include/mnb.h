@@ -471,10 +471,12 @@ MNB_API mnb_status mnb_lora(const void *x, int dtype, int M, int K, int64_t x_st
  * are of `dtype` (MNB_F16 or MNB_F32), rows `stride` elements apart. temperature is fp32 [rows], NULL for 1; a row of
  * temperature 0 gets 1 at its largest logit (the first of equal ones) and 0 elsewhere. Masked logits are -inf: a row of
  * nothing else gets zeros. A NaN or (unless the temperature is 0) +inf logit, and a temperature that is negative or NaN, make the row
- * NaN. rows = 0 is valid and does nothing.
+ * NaN. `workspace` holds mnb_softmax_workspace_bytes(rows, V) bytes (0 for V up to 16377), under the rules of mnb_lora's; more than
+ * 2^42 elements give MNB_ERR_UNSUPPORTED. rows = 0 is valid and does nothing.
  */
+MNB_API size_t mnb_softmax_workspace_bytes(int rows, int V);
 MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, int64_t stride, const float *temperature,
-                               float *out, mnb_stream stream);
+                               void *workspace, size_t ws_bytes, float *out, mnb_stream stream);
 
 /*
  * Verification of drafted tokens from given random numbers (speculative sampling). Sequence b of `batch` has the drafted tokens
@@ -489,11 +491,14 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
  * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
  * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0), weights and sums are whole numbers of 2^-60 (a row adds
  * up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
+ * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes, under the rules of mnb_lora's; more than 2^42 elements in the batch's rows
+ * give MNB_ERR_UNSUPPORTED. batch = 0 is valid and does nothing.
  */
+MNB_API size_t mnb_verify_workspace_bytes(int batch, int V);
 MNB_API mnb_status mnb_verify(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
                               const int32_t *draft_tokens, const int32_t *draft_start, const float *u_accept,
-                              const float *u_next, int batch, int drafted, int V, int32_t *tokens, int32_t *accepted,
-                              mnb_stream stream);
+                              const float *u_next, int batch, int drafted, int V, void *workspace, size_t ws_bytes,
+                              int32_t *tokens, int32_t *accepted, mnb_stream stream);
 
 /*
  * Programmatic dependent launch. With `enable` != 0, later calls on this host thread

@@ -442,7 +442,7 @@ def test_bindings_refuse(env):
         (TypeError, "adapter must be torch.int32", lambda: mnb.mnb_lora(x, pool, idx.long())),
         (ValueError, "adapter must be", lambda: mnb.mnb_lora(x, pool, idx[:2].clone())),
         (ValueError, "x must be", lambda: mnb.mnb_lora(x[:, :16], pool, idx)),
-        (ValueError, "x must be", lambda: mnb.mnb_lora(None, pool, idx)),
+        (TypeError, "x must be", lambda: mnb.mnb_lora(None, pool, idx)),
         (TypeError, "x must be float16 or float32", lambda: mnb.mnb_lora(x.bfloat16(), pool, idx)),
         (TypeError, "base must be torch.float16", lambda: mnb.mnb_lora(x, pool, idx, base=torch.zeros(3, 12, device=dev))),
         (ValueError, "base must be", lambda: mnb.mnb_lora(x, pool, idx, base=torch.zeros(3, 11, **h))),
@@ -482,3 +482,21 @@ def test_no_rows(env):
     none = torch.zeros(0, device=dev)
     tokens, accepted = mnb.mnb_verify(torch.zeros(0, 5, device=dev), None, torch.zeros(0, **i32), torch.zeros(1, **i32), none, none)
     assert tokens.shape == (0,) and accepted.shape == (0,)
+
+
+def test_workspaces_of_other_streams_are_held(env):
+    """On a stream of their own, calls allocate their workspaces: no output of the call may get the same bytes."""
+    mnb, torch, dev = env
+    case = _draft_case(np.random.default_rng(13), 40, 9000, 3, False)
+    want, want_n = orc.verify(*case)
+    args = _up(torch, dev, *case)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            room = torch.empty(mnb.mnb_verify_workspace_bytes(40, 9000), dtype=torch.uint8, device=dev)
+            del room  # what the next allocation of these bytes gets
+            tokens, accepted = mnb.mnb_verify(*args)
+    side.synchronize()
+    np.testing.assert_array_equal(tokens.cpu().numpy(), want)
+    np.testing.assert_array_equal(accepted.cpu().numpy(), want_n)

@@ -98,12 +98,16 @@ def test_lora_refusals(lib, change, expect, word):
     (dict(stride=9), 1, "stride"),
     (dict(temperature=4), 3, "temperature"),
     (dict(out=None), 1, "out"),
+    (dict(V=16378, stride=16378, ws_bytes=2 * 3 * 16 - 1, workspace=64), 1, "workspace"),
+    (dict(V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
+    (dict(rows=1 << 20, V=1 << 23, stride=1 << 23, ws_bytes=1 << 50, workspace=64), 2, "more than"),
 ])
 def test_softmax_refusals(lib, change, expect, word):
     import gemm_mnb_gemv_gb300 as mnb
-    a = dict(logits=64, dtype=0, rows=2, V=10, stride=10, temperature=None, out=64)
+    a = dict(logits=64, dtype=0, rows=2, V=10, stride=10, temperature=None, workspace=None, ws_bytes=0, out=64)
     a.update(change)
-    st = lib.mnb_softmax(P(a["logits"]), a["dtype"], a["rows"], a["V"], a["stride"], P(a["temperature"]), P(a["out"]), None)
+    st = lib.mnb_softmax(P(a["logits"]), a["dtype"], a["rows"], a["V"], a["stride"], P(a["temperature"]),
+                         P(a["workspace"]), a["ws_bytes"], P(a["out"]), None)
     assert st == expect, mnb.mnb_last_error()
     assert mnb.mnb_last_error().startswith("mnb_softmax") and word in mnb.mnb_last_error()
 
@@ -124,14 +128,18 @@ def test_softmax_refusals(lib, change, expect, word):
     (dict(v=None), 1, "u_next"),
     (dict(tokens=None), 1, "tokens"),
     (dict(accepted=8), 3, "accepted"),
+    (dict(ws_bytes=2 * 16 - 1), 1, "workspace"),
+    (dict(workspace=None), 1, "workspace"),
+    (dict(batch=1 << 20, V=1 << 23, target_stride=1 << 23, draft_stride=1 << 23), 2, "more than"),
 ])
 def test_verify_refusals(lib, change, expect, word):
     import gemm_mnb_gemv_gb300 as mnb
     a = dict(target=64, target_stride=10, draft=64, draft_stride=10, tokens_in=64, start=64, u=64, v=64, batch=2, drafted=3, V=10,
-             tokens=64, accepted=64)
+             workspace=64, ws_bytes=1 << 50, tokens=64, accepted=64)
     a.update(change)
     st = lib.mnb_verify(P(a["target"]), a["target_stride"], P(a["draft"]), a["draft_stride"], P(a["tokens_in"]), P(a["start"]),
-                        P(a["u"]), P(a["v"]), a["batch"], a["drafted"], a["V"], P(a["tokens"]), P(a["accepted"]), None)
+                        P(a["u"]), P(a["v"]), a["batch"], a["drafted"], a["V"], P(a["workspace"]),
+                        a["ws_bytes"], P(a["tokens"]), P(a["accepted"]), None)
     assert st == expect, mnb.mnb_last_error()
     assert mnb.mnb_last_error().startswith("mnb_verify") and word in mnb.mnb_last_error()
 
@@ -141,12 +149,20 @@ def test_lora_workspace_bytes(lib):
         0, 0, 0, 0, 16 * 66, 16 * ((1 << 20) + 1), 0]
 
 
+def test_draft_workspace_bytes(lib):
+    soft, ver = lib.mnb_softmax_workspace_bytes, lib.mnb_verify_workspace_bytes
+    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (3, 16378), (3, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 0, 3 * 3 * 16, 3 * 16 * 16, 0]
+    assert [ver(*a) for a in [(0, 9), (3, 0), (3, 1), (3, 4096), (3, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 3 * 16, 3 * 2 * 16, 3 * 32 * 16, 0]
+
+
 def test_no_rows_is_valid(lib):
     import gemm_mnb_gemv_gb300 as mnb
     pool = mnb.MnbLoraPoolArg(None, None, None, None, 1, 8)
     assert lib.mnb_lora(None, 0, 0, 16, 16, pool, None, None, 0, 1, None, 0, None, 1, None) == 0
-    assert lib.mnb_softmax(None, 0, 0, 1, 1, None, None, None) == 0
-    assert lib.mnb_verify(None, 0, None, 0, None, None, None, None, 0, 0, 1, None, None, None) == 0
+    assert lib.mnb_softmax(None, 0, 0, 1, 1, None, None, 0, None, None) == 0
+    assert lib.mnb_verify(None, 0, None, 0, None, None, None, None, 0, 0, 1, None, 0, None, None, None) == 0
 
 
 def test_host_tensors_are_refused():
