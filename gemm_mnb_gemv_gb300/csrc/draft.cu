@@ -10,15 +10,22 @@
 namespace mnb {
 namespace {
 
+// CTAs that share a row of `chunks`: four an SM together where that is possible, so that none waits for another's end, each with
+// `smallest` to `largest` chunks.
+int row_parts(int rows, int chunks, int smallest, int largest) {
+  const int most = (chunks + smallest - 1) / smallest, least = (chunks + largest - 1) / largest, want = 4 * 152 / rows;
+  return want < least ? least : want > most ? most : want;
+}
+
 // ---------------------------------------------------------------------------------
 // Softmax: p = e^((x - max) / temperature) / sum.  Elements go in chunks of 8 that begin at 16-byte boundaries of the logits,
-// whatever the row's own start; a thread keeps its chunks in registers.
+// whatever the row's own start.
 // ---------------------------------------------------------------------------------
-constexpr int kHeld = 4;           // chunks of a thread
-constexpr int kSegThreads = 256;   // of a segment: 8192 elements
+constexpr int kBatch = 4;          // chunks of a thread in flight
+constexpr int kPartThreads = 256;  // of a row's part
 constexpr int kNone = 0x7fffffff;
 
-struct SoftPart {  // of a segment: largest, sum of the exponentials relative to it, first place of the largest
+struct SoftPart {  // of a part: largest, sum of the exponentials relative to it, first place of the largest
   float m, s;
   int at, pad;
 };
@@ -34,235 +41,373 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+__device__ __forceinline__ float some(float m) { return m == -INFINITY ? 0.0f : m; }  // what logits are taken relative to
+struct Base;
 
-// One row's place, temperature and chunks.
+// Eight logits as they lie.
+template <bool F32>
+struct Chunk {
+  uint32_t u[F32 ? 8 : 4];
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (F32) return make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+    else return half2_floats(u[i]);
+  }
+  __device__ __forceinline__ float largest() const {
+    if constexpr (F32) {
+      float m = __uint_as_float(u[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = nan_max(m, __uint_as_float(u[i]));
+      return m;
+    } else {
+      uint32_t m = u[0];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(u[i]));
+      const float2 f = half2_floats(m);
+      return nan_max(f.x, f.y);
+    }
+  }
+  // e^((x - m) c) / base.factor
+  template <bool kPlain>
+  __device__ __forceinline__ void exps(const Base& base, float (&e)[8]) const;
+};
+
+// The exponent (x - m) c as one operation, x c - rc, where rc = m c is moderate: rc's rounding is the same for all and goes into
+// `factor`. Else as two (infinite logits, large ones, temperatures near 0).
+struct Base {
+  float m, c, rc, factor;
+  bool plain;
+  __device__ __forceinline__ Base(float m_, float c_) : m(some(m_)), c(c_) {
+    rc = m * c;
+    plain = fabsf(rc) < 65536.0f;  // its rounding moves the exponent by 2^-8 at most
+    factor = plain ? ex2(-fmaf(m, c, -rc)) : 1.0f;
+  }
+  template <bool kPlain>
+  __device__ __forceinline__ float exponent(float x) const {
+    return kPlain ? fmaf(x, c, -rc) : (x - m) * c;
+  }
+};
+template <bool F32>
+template <bool kPlain>
+__device__ __forceinline__ void Chunk<F32>::exps(const Base& base, float (&e)[8]) const {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = pair(i);
+    e[2 * i] = ex2(base.exponent<kPlain>(f.x)), e[2 * i + 1] = ex2(base.exponent<kPlain>(f.y));
+  }
+}
+
 template <bool F32>
 struct SoftRow {
   const Softmax& a;
   int64_t in_at, out_at;
   int skew, chunks;  // chunk i is the elements 8 i - skew ..
+  float temp, c;     // c: 1 / temperature in powers of two, within what keeps 0 * c at 0 and -inf * c at -inf; NaN for no temperature
   __device__ __forceinline__ SoftRow(const Softmax& a_, int r) : a(a_), in_at((int64_t)r * a_.stride), out_at((int64_t)r * a_.V) {
-    skew = (int)(in_at % (F32 ? 4 : 8));
+    skew = (int)(in_at % 8);
     chunks = (a.V + skew + 7) / 8;
+    temp = a.temperature ? a.temperature[r] : 1.0f;
+    c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
   }
-  __device__ __forceinline__ void load(int c, float (&v)[8]) const {
-    const int j = 8 * c - skew;
-    if (j >= 0 && j + 8 <= a.V) {
-      if constexpr (F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + in_at + j);
-        const float4 x = __ldcg(p), y = __ldcg(p + 1);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-      } else {
-        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.logits) + in_at + j));
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  // Whether chunks i0 .. i1 - 1 lie within the row, and its probabilities at 32 bytes.
+  __device__ __forceinline__ bool whole(int i0, int i1) const {
+    return 8 * i0 - skew >= 0 && 8 * i1 - skew <= a.V && ((reinterpret_cast<uintptr_t>(a.out + out_at) >> 2) - skew) % 8 == 0;
+  }
+  // Chunk i when `live`, past L1; -inf beyond the row and when not.
+  template <bool kWhole>
+  __device__ __forceinline__ void load(int i, bool live, Chunk<F32>& v) const {
+    constexpr int kWords = F32 ? 8 : 4;
+    const int j = 8 * i - skew;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = half2_floats(u[i]);
-          v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
+    for (int k = 0; k < kWords; ++k) v.u[k] = F32 ? 0xff800000u : 0xfc00fc00u;
+    if (!live) return;
+    if (kWhole || (j >= 0 && j + 8 <= a.V)) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.logits) + (in_at + j) * (F32 ? 4 : 2));
+#pragma unroll
+      for (int k = 0; k < kWords / 4; ++k) {
+        const uint4 x = __ldcg(p + k);
+        v.u[4 * k] = x.x, v.u[4 * k + 1] = x.y, v.u[4 * k + 2] = x.z, v.u[4 * k + 3] = x.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = -INFINITY;
-        if (j + i >= 0 && j + i < a.V) {
-          if constexpr (F32) v[i] = __ldcg(static_cast<const float*>(a.logits) + in_at + j + i);
-          else v[i] = __half2float(__ldcg(static_cast<const __half*>(a.logits) + in_at + j + i));
+      for (int k = 0; k < 8; ++k)
+        if (j + k >= 0 && j + k < a.V) {
+          if constexpr (F32) v.u[k] = __ldcg(static_cast<const uint32_t*>(a.logits) + in_at + j + k);
+          else v.u[k / 2] = __byte_perm(v.u[k / 2], __ldcg(static_cast<const unsigned short*>(a.logits) + in_at + j + k), k & 1 ? 0x5410 : 0x3254);
         }
-      }
     }
   }
-  __device__ __forceinline__ void store(int c, const float (&p)[8]) const {
-    const int j = 8 * c - skew;
+  // 32 bytes in one store (two of 16 would write every sector twice), streaming: the logits are to stay in L2
+  template <bool kWhole>
+  __device__ __forceinline__ void store(int i, const float (&p)[8]) const {
+    const int j = 8 * i - skew;
     float* out = a.out + out_at + j;
-    if (((out_at - skew) & 3) == 0 && j >= 0 && j + 8 <= a.V) {
-      *reinterpret_cast<float4*>(out) = make_float4(p[0], p[1], p[2], p[3]);
-      *reinterpret_cast<float4*>(out + 4) = make_float4(p[4], p[5], p[6], p[7]);
+    if (kWhole) {
+      asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(p[0]), "f"(p[1]), "f"(p[2]),
+                   "f"(p[3]), "f"(p[4]), "f"(p[5]), "f"(p[6]), "f"(p[7])
+                   : "memory");
+    } else if ((reinterpret_cast<uintptr_t>(out) & 15) == 0 && j >= 0 && j + 8 <= a.V) {
+      __stcs(reinterpret_cast<float4*>(out), make_float4(p[0], p[1], p[2], p[3]));
+      __stcs(reinterpret_cast<float4*>(out + 4), make_float4(p[4], p[5], p[6], p[7]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j + i >= 0 && j + i < a.V) out[i] = p[i];
+      for (int k = 0; k < 8; ++k)
+        if (j + k >= 0 && j + k < a.V) out[k] = p[k];
     }
+  }
+  __device__ __forceinline__ int find(int i, const Chunk<F32>& v, float m) const {  // first place of m in the chunk
+    int at = kNone;
+#pragma unroll
+    for (int k = 7; k >= 0; --k) {
+      const float2 f = v.pair(k / 2);
+      if ((k & 1 ? f.y : f.x) == m) at = 8 * i - skew + k;
+    }
+    return at;
+  }
+  template <bool kWhole>
+  __device__ __forceinline__ void one_hot(int i, const SoftPart& all) const {  // temperature 0
+    const float zero = all.m != all.m ? NAN : 0.0f;
+    const int at = all.at - (8 * i - skew);
+    float p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = at == k ? zero + 1.0f : zero;
+    store<kWhole>(i, p);
   }
 };
 
-// 1 / temperature in powers of two, within what keeps 0 * it at 0 and -inf * it at -inf; NaN for what is no temperature.
-__device__ __forceinline__ float cold_factor(float temp) {
-  return temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
+// a and b together
+__device__ __forceinline__ SoftPart join(const SoftPart& a, const SoftPart& b, float c) {
+  SoftPart r = {nan_max(a.m, b.m), 0.0f, kNone, 0};
+  const float ref = some(r.m);
+  r.s = a.s * ex2((a.m - ref) * c) + b.s * ex2((b.m - ref) * c);
+  r.at = a.m > b.m ? a.at : b.m > a.m ? b.at : min(a.at, b.at);
+  return r;
 }
-
-// Largest, its first place (temperature 0) or the sum of exponentials (else) of a CTA's chunks, for all its threads; the
-// exponentials replace the values.
-template <int kThreads>
-__device__ __forceinline__ SoftPart soft_part(float (&v)[kHeld][8], int n, int first, float temp, float c) {
-  constexpr int kWarps = kThreads / 32;
-  __shared__ float red[2][kWarps];
-  __shared__ int red_at[kWarps];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  SoftPart r = {-INFINITY, 0.0f, kNone, 0};
+__device__ __forceinline__ SoftPart warp_join(SoftPart r, float c) {
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (tid + i * kThreads < n)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r.m = nan_max(r.m, v[i][k]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) r.m = nan_max(r.m, __shfl_xor_sync(kFull, r.m, o));
-  if (lane == 0) red[0][warp] = r.m;
-  __syncthreads();
-  r.m = red[0][lane % kWarps];
-#pragma unroll
-  for (int o = kWarps / 2; o; o >>= 1) r.m = nan_max(r.m, __shfl_xor_sync(kFull, r.m, o));
-  if (temp == 0.0f) {
-#pragma unroll
-    for (int i = kHeld - 1; i >= 0; --i)
-      if (tid + i * kThreads < n)
-#pragma unroll
-        for (int k = 7; k >= 0; --k)
-          if (v[i][k] == r.m) r.at = first + 8 * (tid + i * kThreads) + k;
-    r.at = __reduce_min_sync(kFull, r.at);
-    if (lane == 0) red_at[warp] = r.at;
-    __syncthreads();
-    r.at = r.m == -INFINITY ? kNone : __reduce_min_sync(kFull, red_at[lane % kWarps]);
-  } else {
-    const float ref = r.m == -INFINITY ? 0.0f : r.m;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (tid + i * kThreads < n)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[i][k] = ex2((v[i][k] - ref) * c);
-          r.s += v[i][k];
-        }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
-    if (lane == 0) red[1][warp] = r.s;
-    __syncthreads();
-    r.s = red[1][lane % kWarps];
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
+  for (int o = 16; o; o >>= 1) {
+    const SoftPart v = {__shfl_xor_sync(kFull, r.m, o), __shfl_xor_sync(kFull, r.s, o), __shfl_xor_sync(kFull, r.at, o), 0};
+    r = join(r, v, c);
   }
   return r;
 }
+// Of the CTA's threads, for all of them: the largest first, so that a thread's sum is brought to it once.
+template <int kThreads>
+__device__ __forceinline__ SoftPart cta_join(SoftPart r, float temp, float c) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float m[kWarps], s[kWarps];
+  __shared__ int at[kWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  float top = r.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
+  if (temp == 0.0f) {
+    r.at = __reduce_min_sync(kFull, r.m == top ? r.at : kNone);
+  } else {
+    r.s *= ex2((r.m - some(top)) * c);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
+  }
+  if (lane == 0) m[warp] = top, s[warp] = r.s, at[warp] = r.at;
+  __syncthreads();
+  r.m = m[lane % kWarps];
+  top = r.m;
+#pragma unroll
+  for (int o = kWarps / 2; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(kFull, top, o));
+  if (temp == 0.0f) {
+    r.at = __reduce_min_sync(kFull, r.m == top ? at[lane % kWarps] : kNone);
+  } else {
+    r.s = s[lane % kWarps] * ex2((r.m - some(top)) * c);
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
+  }
+  r.m = top;
+  return r;
+}
 
-// Rows of up to kThreads * kHeld chunks: a CTA has one, and reads it once.
+// A batch joins r: chunks i, i + kThreads .. (-inf where there are none).
+template <bool F32, int kThreads, bool kPlain>
+__device__ __forceinline__ float batch_sum(const Chunk<F32> (&v)[kBatch], const Base& base) {
+  float sum[4] = {}, e[8];
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    v[k].template exps<kPlain>(base, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j % 4] += e[j];
+  }
+  return ((sum[0] + sum[1]) + (sum[2] + sum[3])) * base.factor;
+}
+template <bool F32, int kThreads>
+__device__ __forceinline__ void take(const SoftRow<F32>& row, const Chunk<F32> (&v)[kBatch], int i, SoftPart& r) {
+  float m = r.m;
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) m = nan_max(m, v[k].largest());
+  if (row.temp == 0.0f) {
+    if (m > r.m) {
+      r.at = kNone;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r.at = min(r.at, row.find(i + k * kThreads, v[k], m));
+    }
+  } else {
+    const Base base(m, row.c);
+    const float sum = base.plain ? batch_sum<F32, kThreads, true>(v, base) : batch_sum<F32, kThreads, false>(v, base);
+    r.s = r.s * ex2((r.m - base.m) * row.c) + sum;
+  }
+  r.m = m;
+}
+template <bool F32, int kThreads, bool kWhole>
+__device__ __forceinline__ void load_batch(const SoftRow<F32>& row, int i, int end, Chunk<F32> (&v)[kBatch]) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) row.template load<kWhole>(i + k * kThreads, i + k * kThreads < end, v[k]);
+}
+template <bool F32, int kThreads, bool kWhole, bool kPlain>
+__device__ __forceinline__ void store_batch(const SoftRow<F32>& row, int i, int end, const Chunk<F32> (&v)[kBatch], const Base& base, float inv) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    float e[8];
+    v[k].template exps<kPlain>(base, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] *= inv;
+    if (i + k * kThreads < end) row.template store<kWhole>(i + k * kThreads, e);
+  }
+}
+
+// Rows of up to kThreads * kBatch chunks: a CTA has one, and reads it once.
 template <bool F32, int kThreads>
 __global__ void __launch_bounds__(kThreads) softmax_row_kernel(const Softmax a) {
   pdl_launch_dependents();
   pdl_wait();
   const SoftRow<F32> row(a, blockIdx.x);
-  const float temp = a.temperature ? a.temperature[blockIdx.x] : 1.0f;
-  float v[kHeld][8];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if ((int)threadIdx.x + i * kThreads < row.chunks) row.load(threadIdx.x + i * kThreads, v[i]);
-  const SoftPart all = soft_part<kThreads>(v, row.chunks, -row.skew, temp, cold_factor(temp));
-  const float inv = all.m == -INFINITY ? 0.0f : 1.0f / all.s;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int c = threadIdx.x + i * kThreads;
-    if (c < row.chunks) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (temp == 0.0f) v[i][k] = all.m != all.m ? NAN : 8 * c - row.skew + k == all.at ? 1.0f : 0.0f;
-        else v[i][k] *= inv;
-      }
-      row.store(c, v[i]);
-    }
+  const int tid = threadIdx.x, end = row.chunks;
+  Chunk<F32> v[kBatch];
+  const bool whole = row.whole(0, end);
+  if (whole) load_batch<F32, kThreads, true>(row, tid, end, v);
+  else load_batch<F32, kThreads, false>(row, tid, end, v);
+  SoftPart all = {-INFINITY, 0.0f, kNone, 0};
+  take<F32, kThreads>(row, v, tid, all);
+  all = cta_join<kThreads>(all, row.temp, row.c);
+  if (row.temp == 0.0f) {
+    for (int i = tid; i < end; i += kThreads) row.template one_hot<false>(i, all);
+    return;
   }
+  const Base base(all.m, row.c);
+  const float inv = all.m == -INFINITY ? 0.0f : base.factor / all.s;
+  if (whole && base.plain) store_batch<F32, kThreads, true, true>(row, tid, end, v, base, inv);
+  else if (base.plain) store_batch<F32, kThreads, false, true>(row, tid, end, v, base, inv);
+  else store_batch<F32, kThreads, false, false>(row, tid, end, v, base, inv);
 }
 
-// Longer rows: a CTA has a segment, in both launches.
+// Longer rows: a CTA has a part, the same one in both launches.
+template <bool F32, bool kWhole>
+__device__ __forceinline__ SoftPart part_of(const SoftRow<F32>& row, int i0, int i1) {
+  SoftPart mine = {-INFINITY, 0.0f, kNone, 0};
+  for (int i = i0 + threadIdx.x; i < i1; i += kPartThreads * kBatch) {
+    Chunk<F32> v[kBatch];
+    load_batch<F32, kPartThreads, kWhole>(row, i, i1, v);
+    take<F32, kPartThreads>(row, v, i, mine);
+  }
+  return mine;
+}
 template <bool F32>
-__global__ void __launch_bounds__(kSegThreads) softmax_part_kernel(const Softmax a, int segs) {
+__global__ void __launch_bounds__(kPartThreads) softmax_part_kernel(const Softmax a, int parts) {
   pdl_wait();
   pdl_launch_dependents();  // behind the wait: the next launch reads logits (past L1) before its own
-  const int r = blockIdx.x / segs, seg = blockIdx.x % segs;
+  const int r = blockIdx.x / parts, part = blockIdx.x % parts;
   const SoftRow<F32> row(a, r);
-  const float temp = a.temperature ? a.temperature[r] : 1.0f;
-  const int c0 = (int)((int64_t)row.chunks * seg / segs), n = (int)((int64_t)row.chunks * (seg + 1) / segs) - c0;
-  float v[kHeld][8];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if ((int)threadIdx.x + i * kSegThreads < n) row.load(c0 + threadIdx.x + i * kSegThreads, v[i]);
-  const SoftPart part = soft_part<kSegThreads>(v, n, 8 * c0 - row.skew, temp, cold_factor(temp));
-  if (threadIdx.x == 0) static_cast<SoftPart*>(a.workspace)[blockIdx.x] = part;
+  const int i0 = (int)((int64_t)row.chunks * part / parts), i1 = (int)((int64_t)row.chunks * (part + 1) / parts);
+  SoftPart mine = row.whole(i0, i1) ? part_of<F32, true>(row, i0, i1) : part_of<F32, false>(row, i0, i1);
+  mine = cta_join<kPartThreads>(mine, row.temp, row.c);
+  if (threadIdx.x == 0) static_cast<SoftPart*>(a.workspace)[blockIdx.x] = mine;
 }
 
+// v: the first batch.
+template <bool F32, bool kWhole, bool kPlain>
+__device__ __forceinline__ void put(const SoftRow<F32>& row, int i0, int i1, Chunk<F32> (&v)[kBatch], const Base& base, float inv) {
+  for (int i = i0 + threadIdx.x; i < i1; i += kPartThreads * kBatch) {
+    store_batch<F32, kPartThreads, kWhole, kPlain>(row, i, i1, v, base, inv);
+    load_batch<F32, kPartThreads, kWhole>(row, i + kPartThreads * kBatch, i1, v);
+  }
+}
 template <bool F32>
-__global__ void __launch_bounds__(kSegThreads) softmax_join_kernel(const Softmax a, int segs) {
+__global__ void __launch_bounds__(kPartThreads) softmax_join_kernel(const Softmax a, int parts) {
+  __shared__ SoftPart joined;
   pdl_launch_dependents();
-  const int r = blockIdx.x / segs, seg = blockIdx.x % segs, lane = threadIdx.x % 32;
+  // From the last part to the first: what the first launch read last is in L2.
+  const int id = gridDim.x - 1 - blockIdx.x, r = id / parts, part = id % parts, lane = threadIdx.x % 32;
   const SoftRow<F32> row(a, r);
-  const float temp = a.temperature ? a.temperature[r] : 1.0f, c = cold_factor(temp);
-  const int c0 = (int)((int64_t)row.chunks * seg / segs), n = (int)((int64_t)row.chunks * (seg + 1) / segs) - c0;
-  float v[kHeld][8];
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if ((int)threadIdx.x + i * kSegThreads < n) row.load(c0 + threadIdx.x + i * kSegThreads, v[i]);
+  const int i0 = (int)((int64_t)row.chunks * part / parts), i1 = (int)((int64_t)row.chunks * (part + 1) / parts);
+  const bool whole = row.whole(i0, i1);
+  Chunk<F32> v[kBatch];
+  if (row.temp != 0.0f) {
+    if (whole) load_batch<F32, kPartThreads, true>(row, i0 + threadIdx.x, i1, v);
+    else load_batch<F32, kPartThreads, false>(row, i0 + threadIdx.x, i1, v);
+  }
   pdl_wait();
-  const SoftPart* parts = static_cast<const SoftPart*>(a.workspace) + (int64_t)r * segs;
-  SoftPart all = {-INFINITY, 0.0f, kNone, 0};
-  for (int s = lane; s < segs; s += 32) {
-    const int4 u = *reinterpret_cast<const int4*>(parts + s);
-    const float m = __int_as_float(u.x), top = nan_max(all.m, m), ref = top == -INFINITY ? 0.0f : top;
-    if (m > all.m) all.at = u.z;
-    all.s = all.s * ex2((all.m - ref) * c) + __int_as_float(u.y) * ex2((m - ref) * c);
-    all.m = top;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float m = __shfl_xor_sync(kFull, all.m, o), s = __shfl_xor_sync(kFull, all.s, o);
-    const int at = __shfl_xor_sync(kFull, all.at, o);
-    const float top = nan_max(all.m, m), ref = top == -INFINITY ? 0.0f : top;
-    all.at = m > all.m ? at : m == all.m ? min(all.at, at) : all.at;
-    all.s = all.s * ex2((all.m - ref) * c) + s * ex2((m - ref) * c);
-    all.m = top;
-  }
-  const float ref = all.m == -INFINITY ? 0.0f : all.m, inv = all.m == -INFINITY ? 0.0f : 1.0f / all.s;
-#pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int k0 = threadIdx.x + i * kSegThreads;
-    if (k0 < n) {
-      const int ch = c0 + k0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (temp == 0.0f) v[i][k] = all.m != all.m ? NAN : 8 * ch - row.skew + k == all.at ? 1.0f : 0.0f;
-        else v[i][k] = ex2((v[i][k] - ref) * c) * inv;
-      }
-      row.store(ch, v[i]);
+  if (threadIdx.x < 32) {
+    const int4* of = static_cast<const int4*>(a.workspace) + (int64_t)r * parts;
+    SoftPart all = {-INFINITY, 0.0f, kNone, 0};
+    for (int p = lane; p < parts; p += 32) {
+      const int4 u = of[p];
+      all = join(all, {__int_as_float(u.x), __int_as_float(u.y), u.z, 0}, row.c);
     }
+    all = warp_join(all, row.c);
+    if (lane == 0) joined = all;
+  }
+  __syncthreads();
+  const SoftPart all = joined;
+  const Base base(all.m, row.c);
+  const float inv = all.m == -INFINITY ? 0.0f : base.factor / all.s;
+  if (row.temp == 0.0f) {
+    for (int i = i0 + threadIdx.x; i < i1; i += kPartThreads)
+      if (whole) row.template one_hot<true>(i, all);
+      else row.template one_hot<false>(i, all);
+  } else if (whole && base.plain) {
+    put<F32, true, true>(row, i0, i1, v, base, inv);
+  } else if (base.plain) {
+    put<F32, false, true>(row, i0, i1, v, base, inv);
+  } else {
+    put<F32, false, false>(row, i0, i1, v, base, inv);
   }
 }
 
-// Chunks of a row that one CTA takes, and segments of longer rows (0: one CTA).
-int soft_segments(int V) {
+// Parts of a row, 0: one CTA has a whole one.
+int soft_parts(int rows, int V) {
   const int chunks = (V + 14) / 8;
-  return chunks <= 512 * kHeld ? 0 : (chunks + kSegThreads * kHeld - 1) / (kSegThreads * kHeld);
+  return chunks <= 512 * kBatch ? 0 : row_parts(rows, chunks, 256, 2048);
 }
 
 // ---------------------------------------------------------------------------------
-// Verification.  Every CTA of a sequence's segments finds the first rejected token by itself and sums its segment of the
-// row to draw from; the second launch has a CTA for each sequence, which finds the segment, then the element.
+// Verification.  Every CTA of a sequence finds the first rejected token by itself and sums its part of the row to draw
+// from, each warp a run of it; the second launch has a CTA for each sequence, which finds the run, then the element.
 //
-// Weights are whole numbers of 2^-60 (probabilities are held to 0..1; what is below 2^-60 counts as 0): sums are exact in any
-// order, and the drawn token does not hang on how the row was cut. A row may add up to just below 16.
+// Probabilities are whole numbers of 2^-60 (held to 0..1, rounded to nearest): sums are exact in any order, and the drawn
+// token does not hang on how the row was cut. A row may add up to just below 16. A number is taken apart by fp32
+// additions: x + 8 has its last place at 2^-20, and what that leaves of x goes on to 1.5 * 2^-17 (2^-40) and 1.5 * 2^-37 (2^-60);
+// the sums' bits, less those of the constants, count the places. (Shifts of the mantissa take half as many instructions again.)
 // ---------------------------------------------------------------------------------
 constexpr int kVerifyWarps = 8, kVerifyThreads = kVerifyWarps * 32;
-constexpr int kRun = 4;                                // chunks of 4 elements of a thread
-constexpr int kSegChunks = kVerifyThreads * kRun;      // of a segment: 4096 elements
+constexpr int kMostSteps = 16;  // of 32 chunks, in the longest run
 
-struct VerifyPart {  // of a segment: sums of max(p - q, 0) and of p
-  uint64_t w, p;
+struct Places {  // bits of the three sums
+  uint32_t at[3];
 };
-
-__device__ __forceinline__ uint64_t fixed60(float p) {
-  const uint32_t b = __float_as_uint(__saturatef(p));  // NaN: 0
-  const uint64_t m = (uint64_t)((b & 0x7fffffu) | 0x800000u) << 37;
-  uint64_t r;
-  asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(m), "r"(127u - (b >> 23)));  // shifts of 64 and more give 0
+__device__ __forceinline__ Places places(float v) {
+  const float c[3] = {8.0f, 1.5f / 131072.0f, 1.5f / 137438953472.0f};
+  Places r;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float s = v + c[i];
+    r.at[i] = __float_as_uint(s);
+    v -= s - c[i];
+  }
   return r;
 }
-__device__ __forceinline__ uint64_t sub_clamped(uint64_t a, uint64_t b) { return a > b ? a - b : 0; }
+__device__ __forceinline__ Places zero_places() {
+  return {{__float_as_uint(8.0f), __float_as_uint(1.5f / 131072.0f), __float_as_uint(1.5f / 137438953472.0f)}};
+}
+// The number that counts of the three places stand for (the constants' bits taken off, or cancelled).
+__device__ __forceinline__ int64_t placed(int32_t a, int32_t b, int32_t c) {
+  return ((int64_t)a << 40) + ((int64_t)b << 20) + (int64_t)c;
+}
 
 // floor(total * u), u in [0, 1)
 __device__ __forceinline__ uint64_t scaled(uint64_t total, float u) {
@@ -291,7 +436,7 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // of the
 // The row to draw from, in chunks of 4 elements that begin at 16-byte boundaries of p (and of q, where its row lies alike).
 struct DrawRow {
   const float *p, *q;  // q: null when all were accepted, or without draft rows
-  int V, not_this;     // not_this: the rejected token without draft rows, -1 else
+  int V, not_this;     // not_this: the rejected token without draft rows, else no element
   int skew, chunks;
   bool rejected, alike;
   __device__ __forceinline__ DrawRow(const Verify& a, int b, int s0, int n, int accepted) : V(a.V) {
@@ -299,11 +444,12 @@ struct DrawRow {
     const int64_t p_at = (int64_t)(s0 + b + accepted) * a.target_stride, q_at = (int64_t)(s0 + accepted) * a.draft_stride;
     p = a.target + p_at;
     q = rejected && a.draft ? a.draft + q_at : nullptr;
-    not_this = rejected && !a.draft ? a.tokens[s0 + accepted] : -1;
+    not_this = rejected && !a.draft ? a.tokens[s0 + accepted] : -100;
     skew = (int)(p_at & 3);
     alike = (q_at & 3) == skew;
     chunks = (V + skew + 3) / 4;
   }
+  __device__ __forceinline__ void without_draft() { q = nullptr, not_this = -100; }
   __device__ __forceinline__ void load4(const float* row, int c, bool whole, float (&v)[4]) const {
     const int j = 4 * c - skew;
     if (whole && j >= 0 && j + 4 <= V) {
@@ -314,6 +460,39 @@ struct DrawRow {
       for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < V ? __ldg(row + j + i) : 0.0f;
     }
   }
+  // p and q of chunk c, zeros when not `live`. kAny: any row; kPair: the chunk lies within the row, and q alike; kAlone: the same,
+  // without q.
+  enum Mode { kAny, kPair, kAlone };
+  template <int kMode>
+  __device__ __forceinline__ void load(int c, bool live, float (&pv)[4], float (&qv)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pv[i] = qv[i] = 0.0f;
+    if (!live) return;
+    if constexpr (kMode != kAny) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p + 4 * c - skew));
+      pv[0] = x.x, pv[1] = x.y, pv[2] = x.z, pv[3] = x.w;
+      if constexpr (kMode == kPair) {
+        const float4 y = __ldg(reinterpret_cast<const float4*>(q + 4 * c - skew));
+        qv[0] = y.x, qv[1] = y.y, qv[2] = y.z, qv[3] = y.w;
+      }
+    } else {
+      load4(p, c, true, pv);
+      if (q) load4(q, c, alike, qv);
+    }
+  }
+  // s += the places of max(p - q, 0): those of p less those of q, or of 0, where p is the larger
+  template <int kMode>
+  static __device__ __forceinline__ void add(float pj, float qj, uint32_t (&s)[3]) {
+    pj = __saturatef(pj);  // NaN: 0
+    const Places x = places(pj), y = kMode == kAlone ? zero_places() : places(fminf(pj, __saturatef(qj)));
+#pragma unroll
+    for (int j = 0; j < 3; ++j) s[j] += x.at[j] - y.at[j];
+  }
+  __device__ __forceinline__ uint64_t weight64(int c, int i, float pj, float qj) const {
+    uint32_t s[3] = {0, 0, 0};
+    if (4 * c - skew + i != not_this) add<kAny>(pj, qj, s);
+    return (uint64_t)placed((int32_t)s[0], (int32_t)s[1], (int32_t)s[2]);
+  }
 };
 
 __device__ __forceinline__ void sequence(const Verify& a, int b, int& s0, int& n) {
@@ -321,10 +500,46 @@ __device__ __forceinline__ void sequence(const Verify& a, int b, int& s0, int& n
   n = min(max(a.start[b + 1], s0), a.drafted) - s0;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verify a, int segs, uint32_t* status) {
-  __shared__ uint64_t sums[2][kVerifyWarps];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int b = blockIdx.x / segs, seg = blockIdx.x % segs;
+// Chunks of a warp's run of a part.
+__host__ __device__ __forceinline__ int run_chunks(int chunks, int parts) {
+  const int each = (chunks + parts - 1) / parts;
+  return (each + kVerifyWarps * 32 - 1) / (kVerifyWarps * 32) * 32;
+}
+
+// This warp's sum of the run c0 .. c1 - 1, in all lanes.
+template <int kMode>
+__device__ __forceinline__ uint64_t run_sum_of(const DrawRow& row, int c0, int c1) {
+  int64_t sum = 0;
+  for (int c = c0 + threadIdx.x % 32; c < c1; c += 32 * 4) {
+    float pv[4][4], qv[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) row.load<kMode>(c + k * 32, c + k * 32 < c1, pv[k], qv[k]);
+    uint32_t s[3] = {0, 0, 0};  // 16 numbers of up to 2^20 places
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) DrawRow::add<kMode>(pv[k][i], qv[k][i], s);
+    sum += placed((int32_t)s[0], (int32_t)s[1], (int32_t)s[2]);
+  }
+  return warp_sum((uint64_t)sum);
+}
+__device__ __forceinline__ uint64_t run_sum(const DrawRow& row, int c0, int c1) {
+  const bool whole = 4 * c0 - row.skew >= 0 && 4 * c1 - row.skew <= row.V;
+  uint64_t sum = whole && !row.q      ? run_sum_of<DrawRow::kAlone>(row, c0, c1)
+                 : whole && row.alike ? run_sum_of<DrawRow::kPair>(row, c0, c1)
+                                      : run_sum_of<DrawRow::kAny>(row, c0, c1);
+  // the rejected token without draft rows
+  const int c = (row.not_this + row.skew) / 4, i = (row.not_this + row.skew) % 4;
+  if (row.not_this >= 0 && row.not_this < row.V && c >= c0 && c < c1) {
+    DrawRow all = row;
+    all.without_draft();
+    sum -= all.weight64(c, i, __ldg(row.p + row.not_this), 0.0f);
+  }
+  return sum;
+}
+
+__global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verify a, int parts, int run, uint32_t* status) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, b = blockIdx.x / parts, part = blockIdx.x % parts;
   pdl_launch_dependents();
   pdl_wait();
   int s0, n;
@@ -342,7 +557,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verif
         const float pt = __saturatef(a.target[(int64_t)(s0 + b + i) * a.target_stride + tok]);
         const float qt = a.draft ? __saturatef(a.draft[(int64_t)(s0 + i) * a.draft_stride + tok]) : 1.0f;
         bad = !((double)u * (double)qt < (double)pt);
-      } else if (seg == 0 && warp == 0) {
+      } else if (part == 0 && warp == 0) {
         report_status(status, kStatusBadIndex);
       }
     }
@@ -352,43 +567,16 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verif
       break;
     }
   }
-  // ---- sums of this segment ----
+  // ---- the sum of this warp's run ----
   const DrawRow row(a, b, s0, n, accepted);
-  const int c0 = seg * kSegChunks + tid;
-  float pv[kRun][4], qv[kRun][4];
-#pragma unroll
-  for (int k = 0; k < kRun; ++k) {
-    const int c = c0 + k * kVerifyThreads;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
-    if (c < row.chunks) {
-      row.load4(row.p, c, true, pv[k]);
-      if (row.q) row.load4(row.q, c, row.alike, qv[k]);
-    }
-  }
-  uint64_t sum_w = 0, sum_p = 0;
-#pragma unroll
-  for (int k = 0; k < kRun; ++k)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t f = fixed60(pv[k][i]);
-      sum_p += f;
-      if (row.q) sum_w += sub_clamped(f, fixed60(qv[k][i]));
-      else if (4 * (c0 + k * kVerifyThreads) - row.skew + i != row.not_this) sum_w += f;
-    }
-  sum_w = warp_sum(sum_w), sum_p = warp_sum(sum_p);
-  if (lane == 0) sums[0][warp] = sum_w, sums[1][warp] = sum_p;
-  __syncthreads();
-  if (tid == 0) {
-    VerifyPart r = {0, 0};
-    for (int w = 0; w < kVerifyWarps; ++w) r.w += sums[0][w], r.p += sums[1][w];
-    static_cast<VerifyPart*>(a.workspace)[blockIdx.x] = r;
-    if (seg == 0) a.accepted[b] = accepted;
-  }
+  const int c0 = (part * kVerifyWarps + warp) * run;
+  const uint64_t sum = run_sum(row, c0, min(c0 + run, row.chunks));
+  if (lane == 0) static_cast<uint64_t*>(a.workspace)[blockIdx.x * kVerifyWarps + warp] = sum;
+  if (part == 0 && threadIdx.x == 0) a.accepted[b] = accepted;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verify a, int segs) {
-  __shared__ uint64_t runs[kVerifyWarps];
+__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verify a, int parts, int run) {
+  __shared__ uint64_t of_step[kMostSteps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
@@ -396,131 +584,125 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
   sequence(a, b, s0, n);
   const int accepted = min(max(a.accepted[b], 0), n);  // the first launch's: in range unless the caller's buffers overlap
   const float u = a.u_next[b];
-  const VerifyPart* parts = static_cast<const VerifyPart*>(a.workspace) + (int64_t)b * segs;
+  const int runs = parts * kVerifyWarps, per = (runs + 31) / 32;
+  const uint64_t* sums = static_cast<const uint64_t*>(a.workspace) + (int64_t)b * runs;
   int32_t* out = a.out + s0 + b;
-  // ---- the row's total, then the segment that the drawn one is in; every warp finds it by itself ----
-  VerifyPart total = {0, 0}, first = {0, 0};
-  for (int s = lane; s < segs; s += 32) {
-    const VerifyPart v = parts[s];
-    if (s == lane) first = v;
-    total.w += v.w, total.p += v.p;
-  }
-  const DrawRow row(a, b, s0, n, accepted);
-  total.w = row.rejected ? warp_sum(total.w) : 0;
-  const bool residual = total.w > 0;  // nothing left of p - q: drawn from p
-  const uint64_t all = residual ? total.w : warp_sum(total.p);
-  const uint64_t limit = scaled(all, u);
-  uint64_t head = 0;
-  int seg = -1;
-  for (int i = 0; i < segs; i += 32) {
-    VerifyPart v = first;
-    if (i > 0 && i + lane < segs) v = parts[i + lane];
-    const uint64_t x = i + lane < segs ? residual ? v.w : v.p : 0, to = head + warp_scan(x, lane);
-    const uint32_t past = __ballot_sync(kFull, to > limit);
-    if (past) {
-      seg = i + __ffs(past) - 1;
-      head = shfl_u64(to - x, __ffs(past) - 1);
-      break;
+  // ---- the row's total, then the run that the drawn one is in: a lane has `per` neighbouring ones. Every warp finds it by itself ----
+  uint64_t mine = 0;
+#pragma unroll 16
+  for (int i = 0; i < per; ++i) mine += lane * per + i < runs ? sums[lane * per + i] : 0;
+  DrawRow row(a, b, s0, n, accepted);
+  uint64_t to = warp_scan(mine, lane), all = shfl_u64(to, 31), limit = scaled(all, u), head = 0;
+  int found = -1;
+  if (all > 0) {
+    const int from = __ffs(__ballot_sync(kFull, to > limit)) - 1;  // there is one: limit < all
+    head = shfl_u64(to - mine, from);
+    for (int i = 0; i < per && found < 0; i += 32) {
+      const int at = from * per + i + lane;
+      const uint64_t x = i + lane < per && at < runs ? sums[at] : 0;
+      to = head + warp_scan(x, lane);
+      const uint32_t past = __ballot_sync(kFull, to > limit);
+      if (past) {
+        found = from * per + i + __ffs(past) - 1;
+        head = shfl_u64(to - x, __ffs(past) - 1);
+      } else {
+        head = shfl_u64(to, 31);
+      }
     }
-    head = shfl_u64(to, 31);
+  } else if (row.rejected) {  // nothing left of p - q: drawn from p, whose sums are taken here, by every warp alike
+    row.without_draft();
+    for (int i = 0; i < runs; ++i) all += run_sum(row, i * run, min((i + 1) * run, row.chunks));
+    limit = scaled(all, u);
+    for (int i = 0; i < runs && all > 0 && found < 0; ++i) {
+      const uint64_t x = run_sum(row, i * run, min((i + 1) * run, row.chunks));
+      if (head + x > limit) found = i;
+      else head += x;
+    }
   }
   for (int i = tid; i <= n; i += kVerifyThreads)
-    if (i != accepted || all == 0) out[i] = i < accepted ? a.tokens[s0 + i] : -1;
-  if (seg < 0) return;
-  // ---- the element: each warp a run of the segment ----
-  const int c0 = seg * kSegChunks + warp * (32 * kRun);
-  uint64_t w[kRun][4], sum[kRun], mine = 0;
-  float pv[kRun][4], qv[kRun][4];
+    if (i != accepted || found < 0) out[i] = i < accepted ? a.tokens[s0 + i] : -1;
+  if (found < 0) return;
+  // ---- the element: the warps take the run's steps of 32 chunks in turn ----
+  constexpr int kMine = kMostSteps / kVerifyWarps;
+  const int steps = run / 32;
+  float pv[kMine][4], qv[kMine][4];
+  uint64_t sum[kMine];
 #pragma unroll
-  for (int k = 0; k < kRun; ++k) {
-    const int c = c0 + 32 * k + lane;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) pv[k][i] = qv[k][i] = 0.0f;
-    if (c < row.chunks) {
-      row.load4(row.p, c, true, pv[k]);
-      if (row.q && residual) row.load4(row.q, c, row.alike, qv[k]);
-    }
+  for (int k = 0; k < kMine; ++k) {
+    const int s = k * kVerifyWarps + warp, c = found * run + 32 * s + lane;
+    row.load<DrawRow::kAny>(c, s < steps && c < row.chunks, pv[k], qv[k]);
   }
 #pragma unroll
-  for (int k = 0; k < kRun; ++k) {
+  for (int k = 0; k < kMine; ++k) {
+    const int s = k * kVerifyWarps + warp, c = found * run + 32 * s + lane;
     sum[k] = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[k][i] = fixed60(pv[k][i]);
-      if (residual && row.q) w[k][i] = sub_clamped(w[k][i], fixed60(qv[k][i]));
-      if (residual && 4 * (c0 + 32 * k + lane) - row.skew + i == row.not_this) w[k][i] = 0;
-      sum[k] += w[k][i];
-    }
-    mine += sum[k];
+    for (int i = 0; i < 4; ++i) sum[k] += row.weight64(c, i, pv[k][i], qv[k][i]);
+    const uint64_t total = warp_sum(sum[k]);
+    if (lane == 0) of_step[s] = total;
   }
-  mine = warp_sum(mine);
-  if (lane == 0) runs[warp] = mine;
   __syncthreads();
-  for (int i = 0; i < warp; ++i) head += runs[i];
-  if (head <= limit && head + mine > limit) {
-    bool done = false;
+  const uint64_t x = lane < kMostSteps ? of_step[lane] : 0;
+  to = head + warp_scan(x, lane);
+  const int step = __ffs(__ballot_sync(kFull, to > limit)) - 1;
+  head = shfl_u64(to - x, max(step, 0));
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-      if (!done) {
-        const uint64_t to = head + warp_scan(sum[k], lane);
-        const uint32_t past = __ballot_sync(kFull, to > limit);
-        if (past) {
-          done = true;
-          if (lane == __ffs(past) - 1) {
-            uint64_t s = to - sum[k];
-            int at = 3;
+  for (int k = 0; k < kMine; ++k) {
+    if (step == k * kVerifyWarps + warp) {
+      const int c = found * run + 32 * step + lane;
+      to = head + warp_scan(sum[k], lane);
+      const uint32_t past = __ballot_sync(kFull, to > limit);
+      if (past && lane == __ffs(past) - 1) {
+        uint64_t s = to - sum[k];
+        int at = -1;
 #pragma unroll
-            for (int i = 2; i >= 0; --i) {
-              uint64_t upto = s;
-#pragma unroll
-              for (int j = 0; j <= i; ++j) upto += w[k][j];
-              if (upto > limit) at = i;
-            }
-            out[accepted] = 4 * (c0 + 32 * k + lane) - row.skew + at;
-          }
+        for (int i = 0; i < 4; ++i) {
+          s += row.weight64(c, i, pv[k][i], qv[k][i]);
+          if (at < 0 && s > limit) at = i;
         }
-        head = shfl_u64(to, 31);
+        out[accepted] = 4 * c - row.skew + at;
       }
     }
   }
 }
 
-int verify_segments(int V) { return ((V + 6) / 4 + kSegChunks - 1) / kSegChunks; }
+int verify_parts(int batch, int V) { return row_parts(batch, (V + 6) / 4, 512, kVerifyThreads * kMostSteps); }
 
 }  // namespace
 
-size_t softmax_workspace_bytes(int rows, int V) { return (size_t)rows * soft_segments(V) * sizeof(SoftPart); }
-size_t verify_workspace_bytes(int batch, int V) { return (size_t)batch * verify_segments(V) * sizeof(VerifyPart); }
+size_t softmax_workspace_bytes(int rows, int V) { return (size_t)rows * soft_parts(rows, V) * sizeof(SoftPart); }
+size_t verify_workspace_bytes(int batch, int V) { return (size_t)batch * verify_parts(batch, V) * kVerifyWarps * sizeof(uint64_t); }
 
 cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a) {
   ctx.variant = a.f32 ? "softmax_f32" : "softmax_f16";
-  const int segs = soft_segments(a.V);
-  if (segs == 0) {
-    const bool few = (a.V + 14) / 8 <= 128 * kHeld;
+  const int parts = soft_parts(a.rows, a.V);
+  if (parts == 0) {
+    const bool few = (a.V + 14) / 8 <= 128 * kBatch;
     auto go = [&](auto kern, int threads) { return launch_kernel(ctx, kern, dim3(a.rows), dim3(threads), 0, a); };
     if (few) return a.f32 ? go(softmax_row_kernel<true, 128>, 128) : go(softmax_row_kernel<false, 128>, 128);
     return a.f32 ? go(softmax_row_kernel<true, 512>, 512) : go(softmax_row_kernel<false, 512>, 512);
   }
-  const dim3 grid((unsigned)a.rows * segs);
-  cudaError_t e = a.f32 ? launch_kernel(ctx, softmax_part_kernel<true>, grid, dim3(kSegThreads), 0, a, segs)
-                        : launch_kernel(ctx, softmax_part_kernel<false>, grid, dim3(kSegThreads), 0, a, segs);
+  const dim3 grid((unsigned)a.rows * parts);
+  cudaError_t e = a.f32 ? launch_kernel(ctx, softmax_part_kernel<true>, grid, dim3(kPartThreads), 0, a, parts)
+                        : launch_kernel(ctx, softmax_part_kernel<false>, grid, dim3(kPartThreads), 0, a, parts);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // the second launch waits for the first one on the device
-  e = a.f32 ? launch_kernel(ctx, softmax_join_kernel<true>, grid, dim3(kSegThreads), 0, a, segs)
-            : launch_kernel(ctx, softmax_join_kernel<false>, grid, dim3(kSegThreads), 0, a, segs);
+  e = a.f32 ? launch_kernel(ctx, softmax_join_kernel<true>, grid, dim3(kPartThreads), 0, a, parts)
+            : launch_kernel(ctx, softmax_join_kernel<false>, grid, dim3(kPartThreads), 0, a, parts);
   ctx.pdl = pdl;
   return e;
 }
 
 cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a) {
   ctx.variant = "verify";
-  const int segs = verify_segments(a.V);
-  cudaError_t e = launch_kernel(ctx, verify_part_kernel, dim3((unsigned)a.batch * segs), dim3(kVerifyThreads), 0, a, segs, ctx.status);
+  const int parts = verify_parts(a.batch, a.V), run = run_chunks((a.V + 6) / 4, parts);
+  cudaError_t e = launch_kernel(ctx, verify_part_kernel, dim3((unsigned)a.batch * parts), dim3(kVerifyThreads), 0, a, parts, run,
+                                ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;
-  e = launch_kernel(ctx, verify_draw_kernel, dim3(a.batch), dim3(kVerifyThreads), 0, a, segs);
+  e = launch_kernel(ctx, verify_draw_kernel, dim3(a.batch), dim3(kVerifyThreads), 0, a, parts, run);
   ctx.pdl = pdl;
   return e;
 }

@@ -489,8 +489,8 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
  *   when all are accepted. Where nothing is left of p - q it is drawn from p; where p is all 0, it is -1.
  * u_accept fp32 [drafted], u_next fp32 [batch], in [0, 1) (others are held to it). tokens int32 [drafted + batch], laid out as
  * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
- * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0), weights and sums are whole numbers of 2^-60 (a row adds
- * up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
+ * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0) and rounded to whole numbers of 2^-60, in which weights and
+ * sums are taken (a row adds up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
  * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes, under the rules of mnb_lora's; more than 2^42 elements in the batch's rows
  * give MNB_ERR_UNSUPPORTED. batch = 0 is valid and does nothing.
  */

@@ -49,7 +49,7 @@ def softmax(x, temperature):
 def _held(p):
     """Probabilities held to 0..1, as whole numbers of 2^-60."""
     p = np.nan_to_num(np.asarray(p, np.float64), nan=0.0, posinf=1.0, neginf=0.0).clip(0, 1)
-    return [int(v) for v in np.ldexp(p, 60)]  # 24 significant bits: exact until int() cuts them off
+    return [int(v) for v in np.rint(np.ldexp(p, 60))]
 
 
 def verify(target, draft, draft_tokens, draft_start, u_accept, u_next):

@@ -98,7 +98,7 @@ def test_lora_refusals(lib, change, expect, word):
     (dict(stride=9), 1, "stride"),
     (dict(temperature=4), 3, "temperature"),
     (dict(out=None), 1, "out"),
-    (dict(V=16378, stride=16378, ws_bytes=2 * 3 * 16 - 1, workspace=64), 1, "workspace"),
+    (dict(V=16378, stride=16378, ws_bytes=2 * 9 * 16 - 1, workspace=64), 1, "workspace"),
     (dict(V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
     (dict(rows=1 << 20, V=1 << 23, stride=1 << 23, ws_bytes=1 << 50, workspace=64), 2, "more than"),
 ])
@@ -128,7 +128,7 @@ def test_softmax_refusals(lib, change, expect, word):
     (dict(v=None), 1, "u_next"),
     (dict(tokens=None), 1, "tokens"),
     (dict(accepted=8), 3, "accepted"),
-    (dict(ws_bytes=2 * 16 - 1), 1, "workspace"),
+    (dict(ws_bytes=2 * 64 - 1), 1, "workspace"),
     (dict(workspace=None), 1, "workspace"),
     (dict(batch=1 << 20, V=1 << 23, target_stride=1 << 23, draft_stride=1 << 23), 2, "more than"),
 ])
@@ -150,11 +150,13 @@ def test_lora_workspace_bytes(lib):
 
 
 def test_draft_workspace_bytes(lib):
+    """16 and 64 bytes for each part of a row; a part has 256 to 2048 chunks of 8 elements, or
+    512 to 4096 of 4, and the rows have 608 where possible."""
     soft, ver = lib.mnb_softmax_workspace_bytes, lib.mnb_verify_workspace_bytes
-    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (3, 16378), (3, 128256), (1, (1 << 24) + 1)]] == [
-        0, 0, 0, 3 * 3 * 16, 3 * 16 * 16, 0]
-    assert [ver(*a) for a in [(0, 9), (3, 0), (3, 1), (3, 4096), (3, 128256), (1, (1 << 24) + 1)]] == [
-        0, 0, 3 * 16, 3 * 2 * 16, 3 * 32 * 16, 0]
+    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (3, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 0, 3 * 9 * 16, 320 * 8 * 16, 0]
+    assert [ver(*a) for a in [(0, 9), (3, 0), (3, 1), (3, 4096), (64, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 3 * 64, 3 * 3 * 64, 64 * 9 * 64, 0]
 
 
 def test_no_rows_is_valid(lib):
