@@ -13,20 +13,14 @@
 #include <type_traits>
 
 #include "cluster.cuh"
+#include "lora.cuh"
 #include "mma_sync.cuh"
-#include "mnb_device.cuh"
-#include "mnb_internal.h"
 
 namespace mnb {
 namespace {
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 half2_floats(uint32_t u) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
+using namespace lora;
+
 // x as two tf32
 struct Split {
   uint32_t hi, lo;
@@ -46,16 +40,6 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// 16 bytes global -> shared; the first `bytes` (0..16) are read, the rest is zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // RB: ranks in eights; WM: row tiles of 16.
@@ -96,52 +80,6 @@ __device__ __forceinline__ int place(int row, int chunk) {
 template <int RP>
 __device__ __forceinline__ int up_place(int row, int chunk) {  // rows of 64 bytes and less are neighbours without conflicts
   return (chunk ^ (RP >= 64 ? (row & 1) * 4 : 0)) * 16;
-}
-
-// The rows of one adapter in a tile.
-struct Item {
-  int m0, adapter;
-  uint64_t rows;  // bit i: row m0 + i
-};
-
-// A call's items, largest first: those with more than half a tile's rows from the front of `list`, the others from its
-// back. Counters first, in 16 bytes.
-template <int TM>
-__global__ void __launch_bounds__(1024) lora_list_kernel(const Lora a, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
-  __shared__ uint32_t count[2];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x < 2) count[threadIdx.x] = 0;
-  __syncthreads();
-  for (int m0 = warp * TM; m0 < a.M; m0 += 32 * TM) {
-    int v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 32 * h + lane;
-      v[h] = -2;
-      if (i < TM && m0 + i < a.M) {
-        v[h] = max(a.adapter[m0 + i], -1);
-        if (v[h] >= a.count) {
-          report_status(status, kStatusBadIndex);
-          v[h] = -1;
-        }
-      }
-    }
-    uint32_t left[2] = {__ballot_sync(kFull, v[0] != -2), __ballot_sync(kFull, v[1] != -2)};
-    while (left[0] | left[1]) {
-      const int value = left[0] ? __shfl_sync(kFull, v[0], __ffs(left[0]) - 1) : __shfl_sync(kFull, v[1], __ffs(left[1]) - 1);
-      const uint32_t lo = __ballot_sync(kFull, v[0] == value), hi = __ballot_sync(kFull, v[1] == value);
-      left[0] &= ~lo, left[1] &= ~hi;
-      if (lane == 0) {
-        const int small = __popc(lo) + __popc(hi) <= TM / 2;
-        const int at = (int)atomicAdd(&count[small], 1u);
-        list[small ? capacity - 1 - at : at] = {m0, value, (uint64_t)hi << 32 | lo};
-      }
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) counts[threadIdx.x] = count[threadIdx.x];
 }
 
 template <int RB, int WM, bool F32>
@@ -196,13 +134,13 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       for (int k = 0; k < want; ++k) firsts &= firsts - 1;
       const int from = __ffs(firsts) - 1;
       item.adapter = __shfl_sync(kFull, v, from);
-      item.rows = __shfl_sync(kFull, same, from);
+      item.rows[0] = __shfl_sync(kFull, same, from);
     }
-    const int n_rows = __popcll(item.rows), value = item.adapter;
+    const int n_rows = __popcll(item.rows[0]), value = item.adapter;
     const int rank = value < 0 ? 0 : a.ranks ? min(max(a.ranks[value], 0), a.max_rank) : a.max_rank;
     if (rank == 0 && in_place) continue;
     __syncthreads();  // the item before is done with rows, s and the ring
-    if (tid < TM && (item.rows >> tid & 1)) rows[__popcll(item.rows & ((1ull << tid) - 1))] = item.m0 + tid;
+    if (tid < TM && (item.rows[0] >> tid & 1)) rows[__popcll(item.rows[0] & ((1ull << tid) - 1))] = item.m0 + tid;
     __syncthreads();
 
     const int down_stages = rank > 0 ? (g1 - g0 + WN - 1) / WN : 0;
@@ -364,8 +302,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
           for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-          const int ex = (int)(__float_as_uint(top) >> 23) - 127;
-          const int p = top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
+          const int p = row_power(top);
           const float f = __uint_as_float((uint32_t)(127 - p) << 23);
           *reinterpret_cast<uint2*>(row + col * 2) = make_uint2(half2_bits(v.x * f, v.y * f), half2_bits(v.z * f, v.w * f));
           if (col == 0) factors[r] = scalbnf(scale, p);
@@ -508,8 +445,9 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   }
 }
 
-// Rows from which on tiles have 64 rows, and up to which a cluster finds its tile's adapters itself.
-constexpr int kManyRows = 1024, kFewRows = 64;
+// Rows up to which a cluster finds its tile's adapters itself, from which on tiles have 64 rows, and (fp16) from which on the tcgen05
+// kernel takes the call.
+constexpr int kFewRows = 64, kManyRows = 1024, kTileRows = 1024;
 
 template <int RB, int WM, bool F32>
 cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
@@ -525,29 +463,36 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   if (!listed)
     return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, subs,
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, ctx.status);
-  uint32_t* counts = static_cast<uint32_t*>(a.workspace);
-  Item* list = reinterpret_cast<Item*>(counts + 4);
-  e = launch_kernel(ctx, lora_list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, counts, list, a.M, ctx.status);
+  const List list(a.workspace);
+  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
-  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(L::kCtas * ctx.num_sms / cluster * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
-                      (const uint32_t*)counts, (const Item*)list, a.M, ctx.status);
+  static std::atomic<int> known[64];
+  const int room = clusters_held(ctx, kern, cluster, L::kThreads, L::kBytes, known);
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)((room > 0 ? room : 1) * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
+                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
   ctx.pdl = pdl;
   return e;
 }
 
 template <int RB>
 cudaError_t launch_lora_r(LaunchCtx& ctx, const Lora& a) {
-  if (a.M <= kManyRows) return a.f32 ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 1, false>(ctx, a);
-  return a.f32 ? launch_lora_t<RB, 4, true>(ctx, a) : launch_lora_t<RB, 4, false>(ctx, a);
+  if (!a.f32) return launch_lora_t<RB, 1, false>(ctx, a);
+  return a.M <= kManyRows ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
 }
 
 }  // namespace
 
+cudaError_t launch_lora_tile(LaunchCtx& ctx, const Lora& a);
+
 size_t lora_workspace_bytes(int M) { return M > kFewRows ? 16 + (size_t)M * sizeof(Item) : 0; }
 
 cudaError_t launch_lora(LaunchCtx& ctx, const Lora& a) {
+  if (!a.f32 && a.M > kTileRows) {
+    ctx.variant = "lora_tile_tcgen05";
+    return launch_lora_tile(ctx, a);
+  }
   ctx.variant = a.f32 ? "lora_f32" : "lora_f16";
   if (a.max_rank <= 8) return launch_lora_r<1>(ctx, a);
   if (a.max_rank <= 16) return launch_lora_r<2>(ctx, a);

@@ -1,0 +1,102 @@
+// What the adapter kernels share: copies, and the list of a call's items.
+#pragma once
+
+#include "mnb_device.cuh"
+#include "mnb_internal.h"
+
+namespace mnb {
+namespace lora {
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// 16 bytes global -> shared; the first `bytes` (0..16) are read, the rest is zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The rows of one adapter (negative: none) in a tile.
+struct Item {
+  int m0, adapter;
+  uint64_t rows[2];  // bit i: row m0 + i
+};
+
+// Power of two that brings a row whose largest magnitude is `top` to [2^13, 2^14): the row is held times 2^-power.
+__device__ __forceinline__ int row_power(float top) {
+  const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+  return top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
+}
+
+// A call's items, largest first: those with more than half a tile's rows from the front of `list`, the others from its
+// back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
+template <int TM>
+__global__ void __launch_bounds__(1024) list_kernel(const Lora a, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
+  constexpr int H = (TM + 31) / 32;
+  __shared__ uint32_t count[2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x < 2) count[threadIdx.x] = 0;
+  __syncthreads();
+  for (int m0 = warp * TM; m0 < a.M; m0 += 32 * TM) {
+    int v[H];
+    uint32_t left[H], any = 0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int i = 32 * h + lane;
+      v[h] = -2;
+      if (i < TM && m0 + i < a.M) {
+        v[h] = max(a.adapter[m0 + i], -1);
+        if (v[h] >= a.count) {
+          report_status(status, kStatusBadIndex);
+          v[h] = -1;
+        }
+      }
+      left[h] = __ballot_sync(kFull, v[h] != -2);
+      any |= left[h];
+    }
+    while (any) {
+      int value = -2;
+#pragma unroll
+      for (int h = H - 1; h >= 0; --h)
+        if (left[h]) value = __shfl_sync(kFull, v[h], __ffs(left[h]) - 1);
+      uint32_t same[4] = {0, 0, 0, 0};
+      int n = 0;
+      any = 0;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        same[h] = __ballot_sync(kFull, v[h] == value);
+        left[h] &= ~same[h];
+        any |= left[h];
+        n += __popc(same[h]);
+      }
+      if (lane == 0) {
+        const int small = n <= TM / 2;
+        const int at = (int)atomicAdd(&count[small], 1u);
+        list[small ? capacity - 1 - at : at] = {m0, value, {(uint64_t)same[1] << 32 | same[0], (uint64_t)same[3] << 32 | same[2]}};
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) counts[threadIdx.x] = count[threadIdx.x];
+}
+
+// The list's places in a call's workspace.
+struct List {
+  uint32_t* counts;
+  Item* items;
+  explicit List(void* workspace) : counts(static_cast<uint32_t*>(workspace)), items(reinterpret_cast<Item*>(counts + 4)) {}
+};
+
+}  // namespace lora
+}  // namespace mnb

@@ -1,0 +1,546 @@
+// Low-rank adapters of many rows (prompts) on the tcgen05 tensor cores, fp16: the products of lora.cu for tiles of 128
+// rows.
+//
+// A cluster of 1 to 8 CTAs (one an SM) takes an item, the rows of one adapter in a tile:
+//   1. partial s = down x over the CTA's part of K, 128 a stage (M 128 rows, N the rank), in tensor memory;
+//   2. the CTAs exchange: CTA c adds up the rows c 128 / C .. of all partial sums, rounds them to fp16 (scaled by the row's power of two)
+//      and writes them into every CTA's operand s;
+//   3. out = base + s up over the CTA's part of N, 128 columns a stage, accumulated in two tensor memory buffers in turn.
+// Roles in 512 threads:
+//   warps 0-3    producers: rows of x, down, base and up by 16-byte asynchronous copies (rows of an item need not be
+//                neighbours, ranks not whole swizzle rows) into one ring that runs on from product to product and item to item;
+//   warp 4       MMA issuer (one lane) and tensor memory;
+//   warps 8-15   exchange and epilogue: a row a thread; a stage's results replace its base in shared memory and leave it
+//                as whole lines.
+// Every wait is bounded: a role whose wait gave up reports it and stops, the others run into their own limits, and the
+// rows left get NaN.
+#include "cluster.cuh"
+#include "lora.cuh"
+#include "tcgen05.cuh"
+
+namespace mnb {
+namespace {
+
+using namespace lora;
+
+constexpr int kRows = 128, kSpan = 128, kThreads = 512, kEpiWarps = 8, kProducers = 128;
+
+template <int RP>
+struct TileGeo {
+  static constexpr int kAct = kRows * kSpan * 2;                 // x or base: two halves of 64 columns, 128-byte rows
+  static constexpr int kWeight = kSpan * 128 * (RP > 64 ? 2 : 1);  // down: two halves of K; up: halves of the rank
+  static constexpr int kSlot = kAct + kWeight;
+  static constexpr int kS = kRows * 128 * (RP > 64 ? 2 : 1);
+  static constexpr int kPart = kRows * RP * 4;
+  static constexpr int kFit = (227 * 1024 - 2048 - kS - kPart) / kSlot;
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kBytes = kStages * kSlot + kS + kPart + 1024;
+  static_assert(kStages >= 2, "two stages in flight");
+};
+
+// Byte of 16-byte chunk `chunk` of a row of 128 bytes, in the 128-byte swizzle of the tensor cores' operands.
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return (uint32_t)(row * 128 + ((chunk ^ row) & 7) * 16); }
+
+// Place of float4 `chunk` of a row of partial sums: eight neighbouring rows' chunks in distinct banks.
+template <int RP>
+__device__ __forceinline__ uint32_t part_place(int row, int chunk) {
+  constexpr int kChunks = RP / 4;
+  return (uint32_t)(row * RP * 4 + (chunk ^ (kChunks >= 8 ? row & 7 : row >> 1 & 3)) * 16);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void cluster_st_u64(uint32_t addr, uint32_t lo, uint32_t hi) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(lo), "r"(hi) : "memory");
+}
+__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// Arrives at the barrier of CTA `rank`; what this thread wrote before, and saw, is visible to those that wait there.
+__device__ __forceinline__ void cluster_mbar_arrive(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(smem_u32(bar), rank)) : "memory");
+}
+__device__ __forceinline__ bool cluster_mbar_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity) {
+  if (cluster_mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (cluster_mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return false;
+}
+// The barrier is arrived at once this thread's copies have landed (it counts the threads).
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Place of the n-th set bit.
+__device__ __forceinline__ int nth_bit(const uint64_t (&m)[2], int n) {
+  int at = 0;
+  uint64_t w = m[0];
+  const int c0 = __popcll(w);
+  if (n >= c0) n -= c0, w = m[1], at = 64;
+#pragma unroll
+  for (int s = 32; s; s >>= 1) {
+    const int c = __popcll(w & ((1ull << s) - 1));
+    if (n >= c) n -= c, w >>= s, at += s;
+  }
+  return at;
+}
+
+// An item as every role sees it.
+struct Work {
+  Item item;
+  int n_rows, rank, cols;          // cols: the rank, in whole steps of 16
+  int down_stages, stages;
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 1)
+    lora_tile_kernel(const Lora a, int cluster, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
+  using L = TileGeo<RP>;
+  constexpr int S = L::kStages;
+  constexpr uint32_t kColD1 = 0, kColD2 = 128;  // tensor memory columns: partial s, two buffers of results
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[4], empty_mma[4], empty_epi[4], d1_full, d2_full[2], d2_empty[2], part_ready, s_ready, drained;
+  __shared__ float factors[kRows];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t cta = cluster_ctarank();
+  const int id = blockIdx.x / cluster;
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, s_at = ring + S * L::kSlot, part_at = s_at + L::kS;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], kProducers), mbar_init(&empty_mma[i], 1), mbar_init(&empty_epi[i], kEpiWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kEpiWarps);
+    mbar_init(&d1_full, 1);
+    mbar_init(&drained, 1);
+    mbar_init(&part_ready, kEpiWarps * cluster);
+    mbar_init(&s_ready, kEpiWarps * cluster);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tc::tmem_alloc(&tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  cluster_arrive();  // the others' barriers are there before anything arrives at them
+  cluster_wait();
+  const uint32_t tmem = tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int units = (a.K + 63) / 64, blocks = (a.N + 31) / 32;
+  const int k0 = 64 * (int)((int64_t)units * cta / cluster), k1 = min(a.K, 64 * (int)((int64_t)units * (cta + 1) / cluster));
+  const int n0 = 32 * (int)((int64_t)blocks * cta / cluster), n1 = min(a.N, 32 * (int)((int64_t)blocks * (cta + 1) / cluster));
+  const bool base_vec = a.base && a.base_stride % 8 == 0, out_vec = a.out_stride % 8 == 0;
+  const int big = (int)counts[0], items = big + (int)counts[1], step = gridDim.x / cluster;
+  const bool in_place = a.base == a.out;
+  auto work_of = [&](int it) {
+    Work w;
+    w.item = list[it < big ? it : capacity - 1 - (it - big)];
+    w.n_rows = __popcll(w.item.rows[0]) + __popcll(w.item.rows[1]);
+    const int v = w.item.adapter;
+    w.rank = v < 0 ? 0 : a.ranks ? min(max(a.ranks[v], 0), a.max_rank) : a.max_rank;
+    w.cols = (w.rank + 15) / 16 * 16;
+    w.down_stages = w.rank > 0 ? (max(k1 - k0, 0) + kSpan - 1) / kSpan : 0;
+    w.stages = w.rank == 0 && in_place ? 0 : w.down_stages + (max(n1 - n0, 0) + kSpan - 1) / kSpan;
+    return w;
+  };
+  bool ok = true;
+  auto give_up = [&](uint32_t what) {
+    if (lane == 0) report_status(status, what);
+    ok = false;
+  };
+
+  if (warp < 4) {
+    // ------------------------------ producers ------------------------------------
+    int slot = 0, used = 0;
+    uint32_t by_epi = 0, mma_phase = 0, epi_phase = 0;  // a bit for each slot: who frees it, and the phases of both
+    const int c8 = tid & 7, r8 = tid >> 3;               // chunk of 8, first row of this thread's (16 apart)
+    for (int it = id; it < items && ok; it += step) {
+      const Work w = work_of(it);
+      int rows[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows[i] = r8 + 16 * i < w.n_rows ? w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i) : -1;
+      const __half* down = static_cast<const __half*>(a.down) + (int64_t)w.item.adapter * a.max_rank * a.K;
+      const __half* up = static_cast<const __half*>(a.up) + (int64_t)w.item.adapter * a.N * a.max_rank;
+      for (int q = 0; q < w.stages; ++q) {
+        if (used >= S) {
+          const bool epi = by_epi >> slot & 1;
+          uint64_t* bar = epi ? &empty_epi[slot] : &empty_mma[slot];
+          uint32_t& phase = epi ? epi_phase : mma_phase;
+          if (!__all_sync(kFull, mbar_wait_bounded(bar, phase >> slot & 1))) {
+            give_up(kStatusEmptyWait);
+            break;
+          }
+          phase ^= 1u << slot;
+        }
+        const uint32_t act = ring + slot * L::kSlot, weight = act + L::kAct;
+        if (q < w.down_stages) {
+          const int k = k0 + q * kSpan;
+          const __half* x = static_cast<const __half*>(a.x);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int kk = k + 64 * h + 8 * c8;
+            if (k + 64 * h < k1) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (rows[i] >= 0) {
+                  const int r = r8 + 16 * i;
+                  copy16(act + h * (kRows * 128) + swizzled(r, c8), kk < k1 ? x + (int64_t)rows[i] * a.x_stride + kk : x, kk < k1 ? 16 : 0);
+                }
+              for (int r = r8; r < w.cols; r += 16) {
+                const bool there = r < w.rank && kk < k1;
+                copy16(weight + h * (RP * 128) + swizzled(r, c8), there ? down + (int64_t)r * a.K + kk : down, there ? 16 : 0);
+              }
+            }
+          }
+          by_epi &= ~(1u << slot);
+        } else {
+          const int n = n0 + (q - w.down_stages) * kSpan;
+          if (base_vec) {
+            const __half* base = static_cast<const __half*>(a.base);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int nn = n + 64 * h + 8 * c8, bytes = min(max(n1 - nn, 0) * 2, 16);
+              if (bytes > 0)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (rows[i] >= 0)
+                    copy16(act + h * (kRows * 128) + swizzled(r8 + 16 * i, c8), base + (int64_t)rows[i] * a.base_stride + nn, bytes);
+            }
+          }
+          if (w.rank > 0) {
+#pragma unroll
+            for (int h = 0; h < (RP > 64 ? 2 : 1); ++h) {
+              const int col = 64 * h + 8 * c8, bytes = min(max(w.rank - col, 0) * 2, 16);
+              if (col < w.cols)
+                for (int r = r8; r < kSpan; r += 16)
+                  if (n + r < n1)
+                    copy16(weight + h * (kSpan * 128) + swizzled(r, c8), bytes ? up + (int64_t)(n + r) * a.max_rank + col : up, bytes);
+            }
+          }
+          by_epi |= 1u << slot;
+        }
+        copies_arrive(&full[slot]);
+        ++used;
+        if (++slot == S) slot = 0;
+      }
+    }
+    copy_commit();
+    copy_wait<0>();  // every copy has landed before the CTA can retire
+  } else if (warp == 4) {
+    // ------------------------------ MMA issuer ----------------------------------
+    const bool leader = tc::elect_one();
+    int slot = 0, results = 0;
+    uint32_t full_phase = 0, d2_phase = 0, s_phase = 0;
+    auto wait_full = [&]() {
+      if (!__all_sync(kFull, mbar_wait_bounded(&full[slot], full_phase >> slot & 1))) give_up(kStatusMmaWait);
+      full_phase ^= 1u << slot;
+      tc::fence_proxy_async_smem();  // the copies are generic writes, the products read through the async proxy
+      tc::fence_after_sync();
+      return ok;
+    };
+    auto next_slot = [&]() {
+      if (++slot == S) slot = 0;
+    };
+    for (int it = id; it < items && ok; it += step) {
+      const Work w = work_of(it);
+      int q = 0;
+      for (; q < w.down_stages && ok; ++q) {
+        if (!wait_full()) break;
+        const uint32_t act = ring + slot * L::kSlot;
+        const uint64_t da = tc::smem_desc_k_sw128(act), db = tc::smem_desc_k_sw128(act + L::kAct);
+        const uint32_t idesc = tc::idesc_f16_f32(kRows, w.cols);
+        const int steps = (min(kSpan, k1 - k0 - q * kSpan) + 15) / 16;
+        if (leader) {
+          for (int kk = 0; kk < steps; ++kk)
+            tc::mma_f16(tmem + kColD1, da + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
+                        db + (((kk / 4) * (RP * 128) + (kk % 4) * 32) >> 4), idesc, q > 0 || kk > 0);
+          tc::mma_commit(&empty_mma[slot]);
+          if (q == w.down_stages - 1) tc::mma_commit(&d1_full);
+        }
+        __syncwarp();
+        next_slot();
+      }
+      if (ok && w.rank > 0) {
+        if (!__all_sync(kFull, cluster_mbar_wait(&s_ready, s_phase))) give_up(kStatusMmaWait);
+        s_phase ^= 1u;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tc::fence_after_sync();
+      }
+      for (; q < w.stages && ok; ++q) {
+        if (!wait_full()) break;
+        if (w.rank > 0) {
+          const int b = results & 1;
+          if (results >= 2) {
+            if (!__all_sync(kFull, mbar_wait_bounded(&d2_empty[b], d2_phase >> b & 1))) {
+              give_up(kStatusMmaWait);
+              break;
+            }
+            d2_phase ^= 1u << b;
+            tc::fence_after_sync();
+          }
+          const uint64_t da = tc::smem_desc_k_sw128(s_at), db = tc::smem_desc_k_sw128(ring + slot * L::kSlot + L::kAct);
+          const uint32_t idesc = tc::idesc_f16_f32(kRows, kSpan);
+          if (leader) {
+            for (int kk = 0; kk < w.cols / 16; ++kk)
+              tc::mma_f16(tmem + kColD2 + 128 * b, da + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
+                          db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, kk > 0);
+            tc::mma_commit(&d2_full[b]);
+          }
+          __syncwarp();
+          ++results;
+        }
+        next_slot();
+      }
+    }
+    // the tensor memory is given back only after the products in flight are done
+    if (leader) tc::mma_commit(&drained);
+    __syncwarp();
+    (void)mbar_wait_bounded(&drained, 0);
+  } else if (warp >= 8) {
+    // ------------------------------ exchange and epilogue -------------------------------
+    const int e = warp - 8, quarter = warp & 3, half = e >> 2;  // rows 32 quarter .., columns 64 half ..
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_at = tmem + ((uint32_t)(quarter * 32) << 16);
+    int slot = 0, results = 0;
+    uint32_t full_phase = 0, d1_phase = 0, d2_phase = 0, s_phase = 0;
+    for (int it = id; it < items; it += step) {
+      const Work w = work_of(it);
+      const int row = r < w.n_rows ? w.item.m0 + nth_bit(w.item.rows, r) : -1;
+      if (w.rank > 0) {
+        // ---- this CTA's partial sums to shared memory ----
+        constexpr int kOwn = RP >= 32 ? RP / 2 : 16;  // columns of a warp; of the smallest rank half the warps have none
+        const int col0 = half * kOwn;
+        if (w.down_stages > 0) {
+          if (ok && !__all_sync(kFull, mbar_wait_bounded(&d1_full, d1_phase))) give_up(kStatusMmaWait);
+          d1_phase ^= 1u;
+          tc::fence_after_sync();
+          for (int i = 0; i < w.down_stages; ++i) {  // their slots are the MMA issuer's to free
+            full_phase ^= 1u << slot;
+            if (++slot == S) slot = 0;
+          }
+        }
+        if (ok) {
+          if (col0 < RP) {
+#pragma unroll
+            for (int c = 0; c < kOwn; c += 16) {
+              float v[16];
+              if (w.down_stages > 0 && col0 + c < w.cols) {
+                tmem_ld16(lane_at + kColD1 + col0 + c, v);
+                tc::tmem_wait_ld();
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) sts128(part_at + part_place<RP>(r, (col0 + c + i) / 4), v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0)
+            for (int c = 0; c < cluster; ++c) cluster_mbar_arrive(&part_ready, c);
+          if (!__all_sync(kFull, cluster_mbar_wait(&part_ready, s_phase))) give_up(kStatusMmaWait);
+        }
+        if (ok) {
+          // ---- rows of this CTA's share: over the cluster, to fp16, into every CTA's operand ----
+          const float scale = a.scales ? a.scales[w.item.adapter] : 1.0f;
+          const int share = kRows / cluster;
+          for (int u0 = e * 32; u0 < share * (RP / 4); u0 += kEpiWarps * 32) {  // whole warps: 16 rows of 16 are 64 chunks
+            const int u = u0 + lane, sr = (int)cta * share + u / (RP / 4), ch = u % (RP / 4);
+            float4 v = make_float4(0, 0, 0, 0);
+            for (int c = 0; c < cluster; ++c) {
+              const float4 o = cluster_ld_f4(cluster_map(part_at + part_place<RP>(sr, ch), c));
+              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+            for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            const int p = row_power(top);
+            const float f = __uint_as_float((uint32_t)(127 - p) << 23);
+            const uint32_t lo = half2_bits(v.x * f, v.y * f), hi = half2_bits(v.z * f, v.w * f);
+            const uint32_t to = s_at + (ch / 16) * (kRows * 128) + swizzled(sr, ch / 2 % 8) + (ch & 1) * 8;
+            for (int c = 0; c < cluster; ++c) {
+              cluster_st_u64(cluster_map(to, c), lo, hi);
+              if (ch == 0) cluster_st_f32(cluster_map(smem_u32(&factors[sr]), c), scalbnf(scale, p));
+            }
+          }
+          asm volatile("fence.proxy.async;" ::: "memory");  // the products read s through the async proxy
+          __syncwarp();
+          if (lane == 0)
+            for (int c = 0; c < cluster; ++c) cluster_mbar_arrive(&s_ready, c);
+          if (!__all_sync(kFull, cluster_mbar_wait(&s_ready, s_phase))) give_up(kStatusMmaWait);  // for the rows' factors
+        }
+        s_phase ^= 1u;
+      }
+      const float factor = ok && w.rank > 0 ? factors[r] : 0.0f;
+      // ---- out = base + s up, 128 columns at a time ----
+      for (int q = w.down_stages; q < w.stages; ++q) {
+        const int n = n0 + (q - w.down_stages) * kSpan + 64 * half, width = min(64, n1 - n);
+        const uint32_t tile = ring + slot * L::kSlot + half * (kRows * 128);
+        const int b = results & 1;
+        if (ok && w.rank > 0) {
+          if (!__all_sync(kFull, mbar_wait_bounded(&d2_full[b], d2_phase >> b & 1))) give_up(kStatusMmaWait);
+          d2_phase ^= 1u << b;
+          tc::fence_after_sync();
+        }
+        if (ok && !__all_sync(kFull, mbar_wait_bounded(&full[slot], full_phase >> slot & 1))) give_up(kStatusFullWait);
+        full_phase ^= 1u << slot;
+        if (!ok) {
+          if (row >= 0)
+            for (int i = 0; i < width; ++i) static_cast<__half*>(a.out)[(int64_t)row * a.out_stride + n + i] = __float2half(NAN);
+        } else if (width > 0) {
+          if (!base_vec) {  // rows that lie anywhere, or zeros: put where the copies would have
+            for (int i = 0; i < 32; ++i) {
+              const int from = __shfl_sync(kFull, row, i);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int c = lane + 32 * h;
+                __half v = __float2half(0.0f);
+                if (a.base && from >= 0 && c < width) v = static_cast<const __half*>(a.base)[(int64_t)from * a.base_stride + n + c];
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + swizzled(quarter * 32 + i, c / 8) + (c & 7) * 2), "h"(__half_as_ushort(v))
+                             : "memory");
+              }
+            }
+            __syncwarp();
+          }
+          if (w.rank > 0) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // 32 columns
+              float d[32];
+              tc::tmem_ld32(lane_at + kColD2 + 128 * b + 64 * half + 32 * g, d);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t at = tile + swizzled(r, 4 * g + c);
+                const uint4 v = lds128_a(at);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 x = half2_floats(u[i]);
+                  o[i] = half2_bits(fmaf(d[8 * c + 2 * i], factor, x.x), fmaf(d[8 * c + 2 * i + 1], factor, x.y));
+                }
+                sts128(at, make_uint4(o[0], o[1], o[2], o[3]));
+              }
+            }
+            __syncwarp();
+          }
+          // whole lines: 8 lanes have a row's 64 columns
+          if (out_vec && width == 64) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int from = 4 * i + lane / 8, ch = lane % 8;
+              const int to = __shfl_sync(kFull, row, from);
+              const uint4 y = lds128_a(tile + swizzled(quarter * 32 + from, ch));
+              if (to >= 0) *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + (int64_t)to * a.out_stride + n + 8 * ch) = y;
+            }
+          } else {
+            for (int i = 0; i < 32; ++i) {
+              const int to = __shfl_sync(kFull, row, i);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int c = lane + 32 * h;
+                if (to >= 0 && c < width)
+                  static_cast<__half*>(a.out)[(int64_t)to * a.out_stride + n + c] =
+                      __ushort_as_half((unsigned short)lds_u16_a(tile + swizzled(quarter * 32 + i, c / 8) + (c & 7) * 2));
+              }
+            }
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && ok) {
+          if (w.rank > 0) mbar_arrive(&d2_empty[b]);
+          mbar_arrive(&empty_epi[slot]);
+        }
+        if (w.rank > 0) ++results;
+        if (++slot == S) slot = 0;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  cluster_arrive();  // nobody reads or writes this CTA's memory any more
+  cluster_wait();
+  if (warp == 4) tc::tmem_dealloc(tmem, 512);
+}
+
+// CTAs of a cluster: of 1, 2, 4 and 8 the one with the shortest longest queue, an item's time being its part of a tile and
+// a fixed sixteenth of one (start, exchange). room: how many clusters of each size the GPU holds.
+int tile_cluster(int tiles, const int (&room)[4]) {
+  int best = 0;
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    if (room[i] < 1) continue;
+    const int rounds = (tiles + room[i] - 1) / room[i];
+    const double time = rounds * (1.0 / (1 << i) + 1.0 / 16);
+    if (time < least) least = time, best = i;
+  }
+  return best;
+}
+
+template <int RP>
+cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
+  using L = TileGeo<RP>;
+  auto kern = lora_tile_kernel<RP>;
+  static std::atomic<uint64_t> sized{0};
+  cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
+  if (e != cudaSuccess) return e;
+  const List list(a.workspace);
+  e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, list.counts, list.items, a.M, ctx.status);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> known[4][64];
+  int room[4];
+  for (int i = 0; i < 4; ++i) room[i] = clusters_held(ctx, kern, 1 << i, kThreads, L::kBytes, known[i]);
+  const int pick = tile_cluster((a.M + kRows - 1) / kRows, room), cluster = 1 << pick;
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;  // it waits for the list on the device
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, cluster,
+                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
+  ctx.pdl = pdl;
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_lora_tile(LaunchCtx& ctx, const Lora& a) {
+  if (a.max_rank <= 16) return launch_tile<16>(ctx, a);
+  if (a.max_rank <= 32) return launch_tile<32>(ctx, a);
+  if (a.max_rank <= 64) return launch_tile<64>(ctx, a);
+  return launch_tile<128>(ctx, a);
+}
+
+}  // namespace mnb

@@ -253,4 +253,25 @@ cudaError_t allow_wide_clusters(Kern kernel, int device, std::atomic<uint64_t>& 
   return e;
 }
 
+// Clusters of this kernel that the GPU holds at a time (0: none), asked for once a device: `known` is a static of the caller.
+template <typename Kern>
+int clusters_held(const LaunchCtx& ctx, Kern kernel, int cluster, int threads, size_t smem, std::atomic<int> (&known)[64]) {
+  int n = ctx.device < 64 ? known[ctx.device].load(std::memory_order_relaxed) : 0;
+  if (n != 0) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  if (ctx.device < 64) known[ctx.device].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace mnb

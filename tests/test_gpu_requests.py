@@ -106,6 +106,36 @@ def test_lora(env, M, K, N, R, count, ranks, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("M,K,N,R,run", [
+    (1030, 2048, 1000, 16, 515),     # clusters of 8
+    (2048, 16, 32, 32, 683),         # most CTAs have no part of K and N
+    (3000, 1104, 521, 64, 2999),
+    (5000, 528, 648, 40, 1500),
+    (9000, 384, 320, 128, 4000),
+    (20000, 144, 200, 64, 7000),     # one CTA takes several tiles
+    (20000, 64, 72, 8, 20000),
+    (1700, 8192, 136, 128, 1600),    # a prompt and 100 rows of their own
+])
+def test_lora_prompts(env, M, K, N, R, run, dtype):
+    """Runs of rows with one adapter, as prompts have them, and rows that change with every one at the end."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(M + R)
+    x, base, down, up, r, scales, adapter = _lora_inputs(rng, M, K, N, R, 6, dtype, "uneven" if R == 40 else "all", without=0)
+    tail = min(M % run, 100)
+    adapter[:M - tail] = (np.arange(M - tail) // run) % 6
+    if M == 5000:
+        adapter[1500:3000] = -1
+    xd, bd, dd, ud, rd, sd, ad = _up(torch, dev, x, base, down, up, r, scales, adapter)
+    pool = mnb.MnbLoraPool(dd, ud, ranks=rd, scales=sd)
+    got = mnb.mnb_lora(xd, pool, ad, base=bd)
+    _check_lora(got, x, base, down, up, r, scales, adapter, dtype)
+    again = bd.clone()
+    mnb.mnb_lora(xd, pool, ad, base=again, out=again)
+    assert torch.equal(again, got)
+    mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("M", [3, 300, 1600])
 def test_lora_views_of_fused_products(env, M, dtype):
     """x, base and out as column ranges of wider matrices; what lies beside out stays as it was."""
