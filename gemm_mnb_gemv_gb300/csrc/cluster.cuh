@@ -27,20 +27,19 @@ __device__ __forceinline__ float4 cluster_ld_f4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ float2 cluster_ld_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+// Sum over the CTAs, in their order, of the float4 at this CTA's address; eight loads in flight.
+__device__ __forceinline__ float4 cluster_sum_f4(uint32_t addr, int cluster) {
+  float4 v = make_float4(0, 0, 0, 0);
+  for (int c0 = 0; c0 < cluster; c0 += 8) {
+    float4 o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      o[c] = make_float4(0, 0, 0, 0);
+      if (c0 + c < cluster) o[c] = cluster_ld_f4(cluster_map(addr, c0 + c));
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v.x += o[c].x, v.y += o[c].y, v.z += o[c].z, v.w += o[c].w;
+  }
   return v;
 }
-__device__ __forceinline__ int cluster_ld_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint64_t cluster_ld_u64(uint32_t addr) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr));
-  return v;
-}
-
 }  // namespace mnb

@@ -288,11 +288,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       const float scale = a.scales ? a.scales[value] : 1.0f;
       for (int e0 = warp * 128; e0 < n_rows * RP; e0 += kThreads * 4) {
         const int e = e0 + lane * 4, r = e / RP, col = e % RP;
-        float4 v = make_float4(0, 0, 0, 0);
-        for (int c = 0; c < cluster; ++c) {
-          const float4 o = cluster_ld_f4(cluster_map(smem_u32(part + e), c));
-          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
+        const float4 v = cluster_sum_f4(smem_u32(part + e), cluster);
         uint8_t* row = s_mem + r * L::kSRow;
         if constexpr (F32) {
           *reinterpret_cast<float2*>(row + col * 4) = make_float2(v.x, v.y);

@@ -7,13 +7,17 @@
 //      and writes them into every CTA's operand s;
 //   3. out = base + s up over the CTA's part of N, 128 columns a stage, accumulated in two tensor memory buffers in turn.
 // Roles in 512 threads:
-//   warps 0-3    producers: rows of x, down, base and up by 16-byte asynchronous copies (rows of an item need not be
-//                neighbours, ranks not whole swizzle rows) into one ring that runs on from product to product and item to item;
+//   warps 0-3    producers, into one ring that runs on from product to product and item to item: x and base by tensor copies where
+//                the item's rows are neighbours (as a prompt's are), else row by row in 16-byte asynchronous copies; down and up by
+//                those (ranks end anywhere; a whole stage takes the four warps 0.75 us, more than its share of the bandwidth);
 //   warp 4       MMA issuer (one lane) and tensor memory;
 //   warps 8-15   exchange and epilogue: a row a thread; a stage's results replace its base in shared memory and leave it
 //                as whole lines.
 // Every wait is bounded: a role whose wait gave up reports it and stops, the others run into their own limits, and the
 // rows left get NaN.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "cluster.cuh"
 #include "lora.cuh"
 #include "tcgen05.cuh"
@@ -60,9 +64,13 @@ __device__ __forceinline__ void cluster_st_u64(uint32_t addr, uint32_t lo, uint3
 __device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// Arrives at the barrier of CTA `rank`; what this thread wrote before, and saw, is visible to those that wait there.
-__device__ __forceinline__ void cluster_mbar_arrive(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(smem_u32(bar), rank)) : "memory");
+// A warp arrives once at the barrier of each CTA, lane i at CTA i's: one after the other each would wait for the writes before
+// it again (0.7 us). What the warp wrote before, and saw, is visible to those that wait there.
+__device__ __forceinline__ void cluster_mbar_arrive(uint64_t* bar, int cluster) {
+  __syncwarp();
+  const int lane = threadIdx.x & 31;
+  if (lane < cluster)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(smem_u32(bar), lane)) : "memory");
 }
 __device__ __forceinline__ bool cluster_mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -123,7 +131,8 @@ struct Work {
 
 template <int RP>
 __global__ void __launch_bounds__(kThreads, 1)
-    lora_tile_kernel(const Lora a, int cluster, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
+    lora_tile_kernel(const Lora a, const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap base_map, int maps,
+                     int cluster, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
   using L = TileGeo<RP>;
   constexpr int S = L::kStages;
   constexpr uint32_t kColD1 = 0, kColD2 = 128;  // tensor memory columns: partial s, two buffers of results
@@ -137,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, s_at = ring + S * L::kSlot, part_at = s_at + L::kS;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], kProducers), mbar_init(&empty_mma[i], 1), mbar_init(&empty_epi[i], kEpiWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], kProducers + 1), mbar_init(&empty_mma[i], 1), mbar_init(&empty_epi[i], kEpiWarps);
     for (int i = 0; i < 2; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kEpiWarps);
     mbar_init(&d1_full, 1);
     mbar_init(&drained, 1);
@@ -188,6 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c8 = tid & 7, r8 = tid >> 3;               // chunk of 8, first row of this thread's (16 apart)
     for (int it = id; it < items && ok; it += step) {
       const Work w = work_of(it);
+      // Neighbouring rows, and enough of them that a whole box is no waste.
+      const uint64_t *m = w.item.rows;
+      const int first = m[0] ? __ffsll(m[0]) - 1 : 63 + __ffsll(m[1]), last = m[1] ? 127 - __clzll(m[1]) : 63 - __clzll(m[0]);
+      const bool run = last - first + 1 == w.n_rows && w.n_rows > 32;
+      const bool x_box = run && (maps & 1), base_box = run && (maps & 2);
       int rows[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) rows[i] = r8 + 16 * i < w.n_rows ? w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i) : -1;
@@ -205,6 +219,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u << slot;
         }
         const uint32_t act = ring + slot * L::kSlot, weight = act + L::kAct;
+        if (tid == 0) {
+          const bool down_q = q < w.down_stages;
+          if (down_q ? x_box : base_box) {
+            const int at = down_q ? k0 + q * kSpan : n0 + (q - w.down_stages) * kSpan, end = down_q ? k1 : n1;
+            const int boxes = at + 64 < end ? 2 : 1;
+            mbar_arrive_expect_tx(&full[slot], boxes * kRows * 128);
+            for (int h = 0; h < boxes; ++h)
+              tc::tma_load_2d(smem_raw + (act + h * (kRows * 128) - smem_u32(smem_raw)), down_q ? &x_map : &base_map, at + 64 * h,
+                              w.item.m0 + first, &full[slot]);
+          } else {
+            mbar_arrive(&full[slot]);
+          }
+        }
         if (q < w.down_stages) {
           const int k = k0 + q * kSpan;
           const __half* x = static_cast<const __half*>(a.x);
@@ -214,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k + 64 * h < k1) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (rows[i] >= 0) {
+                if (rows[i] >= 0 && !x_box) {
                   const int r = r8 + 16 * i;
                   copy16(act + h * (kRows * 128) + swizzled(r, c8), kk < k1 ? x + (int64_t)rows[i] * a.x_stride + kk : x, kk < k1 ? 16 : 0);
                 }
@@ -227,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           by_epi &= ~(1u << slot);
         } else {
           const int n = n0 + (q - w.down_stages) * kSpan;
-          if (base_vec) {
+          if (base_vec && !base_box) {
             const __half* base = static_cast<const __half*>(a.base);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -368,9 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0)
-            for (int c = 0; c < cluster; ++c) cluster_mbar_arrive(&part_ready, c);
+          cluster_mbar_arrive(&part_ready, cluster);
           if (!__all_sync(kFull, cluster_mbar_wait(&part_ready, s_phase))) give_up(kStatusMmaWait);
         }
         if (ok) {
@@ -379,11 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int share = kRows / cluster;
           for (int u0 = e * 32; u0 < share * (RP / 4); u0 += kEpiWarps * 32) {  // whole warps: 16 rows of 16 are 64 chunks
             const int u = u0 + lane, sr = (int)cta * share + u / (RP / 4), ch = u % (RP / 4);
-            float4 v = make_float4(0, 0, 0, 0);
-            for (int c = 0; c < cluster; ++c) {
-              const float4 o = cluster_ld_f4(cluster_map(part_at + part_place<RP>(sr, ch), c));
-              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
+            const float4 v = cluster_sum_f4(part_at + part_place<RP>(sr, ch), cluster);
             float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
             for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -397,9 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           asm volatile("fence.proxy.async;" ::: "memory");  // the products read s through the async proxy
-          __syncwarp();
-          if (lane == 0)
-            for (int c = 0; c < cluster; ++c) cluster_mbar_arrive(&s_ready, c);
+          cluster_mbar_arrive(&s_ready, cluster);
           if (!__all_sync(kFull, cluster_mbar_wait(&s_ready, s_phase))) give_up(kStatusMmaWait);  // for the rows' factors
         }
         s_phase ^= 1u;
@@ -480,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc::fence_before_sync();
+        tc::fence_proxy_async_smem();  // a tensor copy may write these bytes next
         __syncwarp();
         if (lane == 0 && ok) {
           if (w.rank > 0) mbar_arrive(&d2_empty[b]);
@@ -512,6 +532,16 @@ int tile_cluster(int tiles, const int (&room)[4]) {
   return best;
 }
 
+// Boxes of 128 rows and 64 columns of a [M, cols] matrix; false where it can't be one (rows then come one by one).
+bool make_map(CUtensorMap* map, const void* p, int M, int cols, int64_t stride) {
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+  if (!encode || !p || stride % 8 != 0 || stride >= (int64_t)1 << 38) return false;
+  const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)M}, pitch[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)kRows}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p), dim, pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int RP>
 cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   using L = TileGeo<RP>;
@@ -519,6 +549,8 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   static std::atomic<uint64_t> sized{0};
   cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
   if (e != cudaSuccess) return e;
+  CUtensorMap x_map = {}, base_map = {};
+  const int maps = (make_map(&x_map, a.x, a.M, a.K, a.x_stride) ? 1 : 0) | (make_map(&base_map, a.base, a.M, a.N, a.base_stride) ? 2 : 0);
   const List list(a.workspace);
   e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
@@ -528,8 +560,8 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   const int pick = tile_cluster((a.M + kRows - 1) / kRows, room), cluster = 1 << pick;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
-  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, cluster,
-                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, x_map, base_map, maps,
+                      cluster, (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
   ctx.pdl = pdl;
   return e;
 }
