@@ -145,43 +145,67 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
 
     const int down_stages = rank > 0 ? (g1 - g0 + WN - 1) / WN : 0;
     const int stages = down_stages + (b1 - b0 + WN - 1) / WN;
-    const __half* down = static_cast<const __half*>(a.down) + (int64_t)value * a.max_rank * a.K;
-    const __half* up = static_cast<const __half*>(a.up) + (int64_t)value * a.N * a.max_rank;
+    // What a copy needs is worked out ahead, as every operation is on the way of the copies behind it: a thread has one chunk of
+    // rows that lie whole passes apart, of x and base, of down and of up.
+    constexpr int kChunks = L::kRow / 16, kPass = kThreads / kChunks, kPasses = TM / kPass;
+    constexpr int kDownChunks = L::kDownRow / 16, kDownPass = kThreads / kDownChunks, kDownPasses = (RP + kDownPass - 1) / kDownPass;
+    constexpr int kUpChunks = L::kUpRow / 16, kUpPass = kThreads / kUpChunks, kUpPasses = (L::kSpan + kUpPass - 1) / kUpPass;
+    static_assert(kPass % 2 == 0 && kDownPass % 2 == 0 && kUpPass % 2 == 0, "a chunk's place depends on its row's parity");
+    const int xr = tid / kChunks, xc = tid % kChunks, dr = tid / kDownChunks, dc = tid % kDownChunks, ur = tid / kUpChunks, uc = tid % kUpChunks;
+    const uint32_t x_to = xr * L::kRow + place<F32>(xr, xc), d_to = L::kAct + dr * L::kDownRow + place<false>(dr, dc);
+    const uint32_t u_to = L::kAct + ur * L::kUpRow + up_place<RP>(ur, uc);
+    const T *x_at[kPasses], *base_at[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t row = xr + i * kPass < n_rows ? rows[xr + i * kPass] : 0;
+      x_at[i] = static_cast<const T*>(a.x) + row * a.x_stride + xc * kVec;
+      base_at[i] = static_cast<const T*>(a.base) + row * a.base_stride + xc * kVec;
+    }
+    const __half* down = static_cast<const __half*>(a.down) + ((int64_t)value * a.max_rank + dr) * a.K + dc * 8;
+    const __half* up = static_cast<const __half*>(a.up) + ((int64_t)value * a.N + ur) * a.max_rank + uc * 8;
+    const int64_t down_step = (int64_t)kDownPass * a.K, up_step = (int64_t)kUpPass * a.max_rank;
+    const int up_have = min(rank - 8 * uc, 8);  // of this thread's chunk of the rank
     auto issue = [&](int q) {
       if (q < stages) {
-        const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
-        constexpr int kChunks = L::kRow / 16;  // of a row of x or base
+        const uint32_t at = ring + q % S * L::kStage;
         if (q < down_stages) {
           const int k0 = (g0 + q * WN) * 32, k1 = min(a.K, g1 * 32);
-          for (int i = tid; i < n_rows * kChunks; i += kThreads) {
-            const int r = i / kChunks, c = i % kChunks, k = k0 + c * kVec;
-            const T* src = static_cast<const T*>(a.x) + (int64_t)rows[r] * a.x_stride + k;
-            copy16(act + r * L::kRow + place<F32>(r, c), k < k1 ? src : static_cast<const T*>(a.x), k < k1 ? 16 : 0);
-          }
-          constexpr int kDownChunks = L::kDownRow / 16;
-          const int padded = min((rank + 7) / 8 * 8, RP);
-          for (int i = tid; i < padded * kDownChunks; i += kThreads) {
-            const int r = i / kDownChunks, c = i % kDownChunks, k = k0 + c * 8;
-            const bool there = r < rank && k < k1;
-            copy16(weight + r * L::kDownRow + place<false>(r, c), there ? down + (int64_t)r * a.K + k : down, there ? 16 : 0);
-          }
+          const bool x_in = k0 + xc * kVec < k1, d_in = k0 + dc * 8 < k1;
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i)
+            if (xr + i * kPass < n_rows) {
+              if (x_in) copy16(at + x_to + i * (kPass * L::kRow), x_at[i] + k0);
+              else store_zeros(at + x_to + i * (kPass * L::kRow));
+            }
+#pragma unroll
+          for (int i = 0; i < kDownPasses; ++i)
+            if (dr + i * kDownPass < rank) {  // columns of s beyond the rank are not used
+              if (d_in) copy16(at + d_to + i * (kDownPass * L::kDownRow), down + i * down_step + k0);
+              else store_zeros(at + d_to + i * (kDownPass * L::kDownRow));
+            }
         } else {
           const int n0 = (b0 + (q - down_stages) * WN) * 32, n1 = min(a.N, b1 * 32);
           if (base_vec) {
-            for (int i = tid; i < n_rows * kChunks; i += kThreads) {
-              const int r = i / kChunks, c = i % kChunks, n = n0 + c * kVec;
-              const int bytes = min(max(n1 - n, 0) * (int)sizeof(T), 16);
-              const T* src = static_cast<const T*>(a.base);
-              copy16(act + r * L::kRow + place<F32>(r, c), bytes ? src + (int64_t)rows[r] * a.base_stride + n : src, bytes);
-            }
+            const int bytes = (n1 - n0 - xc * kVec) * (int)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i)
+              if (xr + i * kPass < n_rows && bytes > 0) {
+                if (bytes >= 16) copy16(at + x_to + i * (kPass * L::kRow), base_at[i] + n0);
+                else copy_some(at + x_to + i * (kPass * L::kRow), base_at[i] + n0, bytes);
+              }
           }
-          if (rank > 0) {
-            constexpr int kUpChunks = L::kUpRow / 16;
-            for (int i = tid; i < L::kSpan * kUpChunks; i += kThreads) {
-              const int r = i / kUpChunks, c = i % kUpChunks;
-              const int bytes = n0 + r < n1 ? min(max(rank - 8 * c, 0) * 2, 16) : 0;
-              copy16(weight + r * L::kUpRow + up_place<RP>(r, c), bytes ? up + (int64_t)(n0 + r) * a.max_rank + 8 * c : up, bytes);
-            }
+          const __half* p = up + (int64_t)n0 * a.max_rank;
+          if (up_have == 8) {
+#pragma unroll
+            for (int i = 0; i < kUpPasses; ++i)
+              if (ur + i * kUpPass < min(L::kSpan, n1 - n0)) copy16(at + u_to + i * (kUpPass * L::kUpRow), p + i * up_step);
+          } else if (up_have > 0) {
+            for (int i = 0; i < kUpPasses; ++i)
+              if (ur + i * kUpPass < min(L::kSpan, n1 - n0)) copy_some(at + u_to + i * (kUpPass * L::kUpRow), p + i * up_step, 2 * up_have);
+          } else if (8 * uc < (rank + 4 * E - 1) / (4 * E) * (4 * E)) {  // zeros behind the rank, as far as the products read
+#pragma unroll
+            for (int i = 0; i < kUpPasses; ++i)
+              if (ur + i * kUpPass < L::kSpan) store_zeros(at + u_to + i * (kUpPass * L::kUpRow));
           }
         }
       }
@@ -288,7 +312,13 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       const float scale = a.scales ? a.scales[value] : 1.0f;
       for (int e0 = warp * 128; e0 < n_rows * RP; e0 += kThreads * 4) {
         const int e = e0 + lane * 4, r = e / RP, col = e % RP;
-        const float4 v = cluster_sum_f4(smem_u32(part + e), cluster);
+        float4 v = cluster_sum_f4(smem_u32(part + e), cluster);
+        if (col + 4 > rank) {
+          if (col >= rank) v.x = 0.0f;
+          if (col + 1 >= rank) v.y = 0.0f;
+          if (col + 2 >= rank) v.z = 0.0f;
+          v.w = 0.0f;
+        }
         uint8_t* row = s_mem + r * L::kSRow;
         if constexpr (F32) {
           *reinterpret_cast<float2*>(row + col * 4) = make_float2(v.x, v.y);

@@ -202,11 +202,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = m[0] ? __ffsll(m[0]) - 1 : 63 + __ffsll(m[1]), last = m[1] ? 127 - __clzll(m[1]) : 63 - __clzll(m[0]);
       const bool run = last - first + 1 == w.n_rows && w.n_rows > 32;
       const bool x_box = run && (maps & 1), base_box = run && (maps & 2);
-      int rows[8];
+      // What a copy needs is worked out ahead: four warps issue all of them, and every operation is on their way. This thread has chunk
+      // c8 of rows r8 + 16 i, which lie 2 KB apart in shared memory.
+      const int mine = w.n_rows > r8 ? (w.n_rows - r8 + 15) / 16 : 0;
+      const __half* at[8];  // this thread's rows of x, then of base
+      auto find_rows = [&](const void* p, int64_t stride) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rows[i] = r8 + 16 * i < w.n_rows ? w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i) : -1;
-      const __half* down = static_cast<const __half*>(a.down) + (int64_t)w.item.adapter * a.max_rank * a.K;
-      const __half* up = static_cast<const __half*>(a.up) + (int64_t)w.item.adapter * a.N * a.max_rank;
+        for (int i = 0; i < 8; ++i)
+          at[i] = static_cast<const __half*>(p) + (i < mine ? w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i) : 0) * stride + 8 * c8;
+      };
+      if (!x_box && w.down_stages > 0) find_rows(a.x, a.x_stride);
+      const uint32_t to = swizzled(r8, c8);
+      const __half* down = static_cast<const __half*>(a.down) + ((int64_t)w.item.adapter * a.max_rank + r8) * a.K + 8 * c8;
+      const __half* up = static_cast<const __half*>(a.up) + ((int64_t)w.item.adapter * a.N + r8) * a.max_rank + 8 * c8;
+      const int64_t down_step = 16 * (int64_t)a.K;
+      const int up_step = 16 * a.max_rank;
       for (int q = 0; q < w.stages; ++q) {
         if (used >= S) {
           const bool epi = by_epi >> slot & 1;
@@ -219,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase ^= 1u << slot;
         }
         const uint32_t act = ring + slot * L::kSlot, weight = act + L::kAct;
+        bool stored = false;  // by this thread itself, not by an asynchronous copy
         if (tid == 0) {
           const bool down_q = q < w.down_stages;
           if (down_q ? x_box : base_box) {
@@ -234,51 +245,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (q < w.down_stages) {
           const int k = k0 + q * kSpan;
-          const __half* x = static_cast<const __half*>(a.x);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int kk = k + 64 * h + 8 * c8;
-            if (k + 64 * h < k1) {
+            const int kk = k + 64 * h;
+            if (kk + 8 * c8 < k1) {  // steps beyond k1 are not made, nor are columns of s beyond the rank used
+              if (!x_box) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (rows[i] >= 0 && !x_box) {
-                  const int r = r8 + 16 * i;
-                  copy16(act + h * (kRows * 128) + swizzled(r, c8), kk < k1 ? x + (int64_t)rows[i] * a.x_stride + kk : x, kk < k1 ? 16 : 0);
-                }
-              for (int r = r8; r < w.cols; r += 16) {
-                const bool there = r < w.rank && kk < k1;
-                copy16(weight + h * (RP * 128) + swizzled(r, c8), there ? down + (int64_t)r * a.K + kk : down, there ? 16 : 0);
+                for (int i = 0; i < 8; ++i)
+                  if (i < mine) copy16(act + h * (kRows * 128) + to + i * 2048, at[i] + kk);
               }
+#pragma unroll
+              for (int i = 0; i < RP / 16; ++i)
+                if (r8 + 16 * i < w.rank) copy16(weight + h * (RP * 128) + to + i * 2048, down + i * down_step + kk);
             }
           }
           by_epi &= ~(1u << slot);
         } else {
           const int n = n0 + (q - w.down_stages) * kSpan;
           if (base_vec && !base_box) {
-            const __half* base = static_cast<const __half*>(a.base);
+            if (q == w.down_stages) find_rows(a.base, a.base_stride);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int nn = n + 64 * h + 8 * c8, bytes = min(max(n1 - nn, 0) * 2, 16);
-              if (bytes > 0)
+              const int nn = n + 64 * h + 8 * c8;
+              if (nn + 8 <= n1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (rows[i] >= 0)
-                    copy16(act + h * (kRows * 128) + swizzled(r8 + 16 * i, c8), base + (int64_t)rows[i] * a.base_stride + nn, bytes);
+                  if (i < mine) copy16(act + h * (kRows * 128) + to + i * 2048, at[i] + n + 64 * h);
+              } else if (nn < n1) {
+                stored = true;
+                for (int i = 0; i < mine; ++i) {
+                  const __half* row = static_cast<const __half*>(a.base) + (int64_t)(w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i)) * a.base_stride;
+                  copy_some(act + h * (kRows * 128) + to + i * 2048, row + nn, 2 * (n1 - nn));
+                }
+              }
             }
           }
-          if (w.rank > 0) {
 #pragma unroll
-            for (int h = 0; h < (RP > 64 ? 2 : 1); ++h) {
-              const int col = 64 * h + 8 * c8, bytes = min(max(w.rank - col, 0) * 2, 16);
-              if (col < w.cols)
-                for (int r = r8; r < kSpan; r += 16)
-                  if (n + r < n1)
-                    copy16(weight + h * (kSpan * 128) + swizzled(r, c8), bytes ? up + (int64_t)(n + r) * a.max_rank + col : up, bytes);
+          for (int h = 0; h < (RP > 64 ? 2 : 1); ++h) {
+            const int col = 64 * h + 8 * c8, have = w.rank - col;
+            const __half* p = up + (int64_t)n * a.max_rank + 64 * h;
+            if (have >= 8) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (n + r8 + 16 * i < n1) copy16(weight + h * (kSpan * 128) + to + i * 2048, p + i * up_step);
+            } else if (col < w.cols) {  // zeros behind the rank, up to whole steps
+              stored = true;
+              if (have <= 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) store_zeros(weight + h * (kSpan * 128) + to + i * 2048);
+              } else {
+                for (int i = 0; i < 8; ++i)
+                  if (n + r8 + 16 * i < n1) copy_some(weight + h * (kSpan * 128) + to + i * 2048, p + i * up_step, 2 * have);
+              }
             }
           }
           by_epi |= 1u << slot;
         }
-        copies_arrive(&full[slot]);
+        if (stored) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          tc::fence_proxy_async_smem();
+          mbar_arrive(&full[slot]);
+        } else {
+          copies_arrive(&full[slot]);
+        }
         ++used;
         if (++slot == S) slot = 0;
       }
@@ -383,13 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kOwn; c += 16) {
               float v[16];
-              if (w.down_stages > 0 && col0 + c < w.cols) {
+              const bool some = w.down_stages > 0 && col0 + c < w.cols;
+              if (some) {
                 tmem_ld16(lane_at + kColD1 + col0 + c, v);
                 tc::tmem_wait_ld();
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
               }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!some || col0 + c + i >= w.rank) v[i] = 0.0f;
 #pragma unroll
               for (int i = 0; i < 16; i += 4) sts128(part_at + part_place<RP>(r, (col0 + c + i) / 4), v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
