@@ -84,7 +84,7 @@ __device__ __forceinline__ int up_place(int row, int chunk) {  // rows of 64 byt
 
 template <int RB, int WM, bool F32>
 __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::kCtas)
-    lora_kernel(const Lora a, int cluster, int subs, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
+    lora_kernel(const Lora a, int cluster, int subs, const uint32_t* counts, const Item* list, int capacity, int small_only, uint32_t* status) {
   using T = std::conditional_t<F32, float, __half>;
   using L = Geo<RB, WM, F32>;
   constexpr int RP = L::RP, TM = L::TM, WN = L::WN, S = L::kStages, kThreads = L::kThreads;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   const int cta = cluster_ctarank(), id = blockIdx.x / cluster;
   const uint32_t ring = smem_u32(smem);
   pdl_launch_dependents();
-  pdl_wait();
+  if (!small_only) pdl_wait();
 
   const int granules = (a.K + 31) / 32, blocks = (a.N + 31) / 32;
   const int g0 = (int)((int64_t)granules * cta / cluster), g1 = (int)((int64_t)granules * (cta + 1) / cluster);
@@ -111,12 +111,15 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
 
   // Without a list (one tile's adapters are found by each cluster itself): cluster `id` takes tile id / subs and its adapter id % subs,
   // in the order of their first rows.
-  const int big = list ? (int)counts[0] : 0, items = list ? big + (int)counts[1] : 1;
+  // With one: all its items, or the small ones alone.
+  const int big = list && !small_only ? (int)__ldcg(counts) : 0, items = list ? big + (int)__ldcg(counts + 1) : 1;
   const int step = list ? gridDim.x / cluster : 1;
   for (int it = list ? id : 0; it < items; it += step) {
     Item item;
     if (list) {
-      item = list[it < big ? it : capacity - 1 - (it - big)];
+      const uint64_t* p = reinterpret_cast<const uint64_t*>(list + (it < big ? it : capacity - 1 - (it - big)));
+      const uint64_t head = __ldcg(p);
+      item = {(int)(uint32_t)head, (int)(head >> 32), {__ldcg(p + 1), __ldcg(p + 2)}};
     } else {
       item.m0 = id / subs * TM;
       const int i = lane, want = id % subs;
@@ -135,12 +138,14 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       const int from = __ffs(firsts) - 1;
       item.adapter = __shfl_sync(kFull, v, from);
       item.rows[0] = __shfl_sync(kFull, same, from);
+      item.rows[1] = 0;
     }
-    const int n_rows = __popcll(item.rows[0]), value = item.adapter;
-    const int rank = value < 0 ? 0 : a.ranks ? min(max(a.ranks[value], 0), a.max_rank) : a.max_rank;
+    const int n_rows = __popcll(item.rows[0]) + __popcll(item.rows[1]), value = item.adapter;
+    const int rank = value < 0 ? 0 : a.ranks ? min(max(__ldcg(a.ranks + value), 0), a.max_rank) : a.max_rank;
     if (rank == 0 && in_place) continue;
     __syncthreads();  // the item before is done with rows, s and the ring
-    if (tid < TM && (item.rows[0] >> tid & 1)) rows[__popcll(item.rows[0] & ((1ull << tid) - 1))] = item.m0 + tid;
+    if (tid < 128 && (item.rows[tid / 64] >> (tid % 64) & 1))
+      rows[(tid < 64 ? 0 : __popcll(item.rows[0])) + __popcll(item.rows[tid / 64] & ((1ull << (tid % 64)) - 1))] = item.m0 + tid;
     __syncthreads();
 
     const int down_stages = rank > 0 ? (g1 - g0 + WN - 1) / WN : 0;
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       // ---- over the cluster; every CTA gets all of s. RP / 4 neighbouring lanes have a row ----
       cluster_arrive();
       cluster_wait();
-      const float scale = a.scales ? a.scales[value] : 1.0f;
+      const float scale = a.scales ? __ldcg(a.scales + value) : 1.0f;
       for (int e0 = warp * 128; e0 < n_rows * RP; e0 += kThreads * 4) {
         const int e = e0 + lane * 4, r = e / RP, col = e % RP;
         float4 v = cluster_sum_f4(smem_u32(part + e), cluster);
@@ -469,6 +474,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     }
     if (rank > 0) cluster_wait();
   }
+  if (small_only) pdl_wait();  // who waits for this kernel waits for the one beside it too
 }
 
 // Rows up to which a cluster finds its tile's adapters itself, from which on tiles have 64 rows, and (fp16) from which on the tcgen05
@@ -488,16 +494,16 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   if (e != cudaSuccess) return e;
   if (!listed)
     return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, subs,
-                           (const uint32_t*)nullptr, (const Item*)nullptr, 0, ctx.status);
+                           (const uint32_t*)nullptr, (const Item*)nullptr, 0, 0, ctx.status);
   const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, list.counts, list.items, a.M, ctx.status);
+  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
   static std::atomic<int> known[64];
   const int room = clusters_held(ctx, kern, cluster, L::kThreads, L::kBytes, known);
   e = launch_clusters(ctx, kern, cluster, dim3((unsigned)((room > 0 ? room : 1) * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
-                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
+                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, 0, ctx.status);
   ctx.pdl = pdl;
   return e;
 }
@@ -508,7 +514,34 @@ cudaError_t launch_lora_r(LaunchCtx& ctx, const Lora& a) {
   return a.M <= kManyRows ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
 }
 
+template <int RB>
+cudaError_t launch_small_r(LaunchCtx& ctx, const Lora& a) {
+  using L = Geo<RB, 1, false>;
+  auto kern = lora_kernel<RB, 1, false>;
+  static std::atomic<uint64_t> sized{0};
+  static std::atomic<int> known[64];
+  const cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
+  if (e != cudaSuccess) return e;
+  constexpr int cluster = 8;
+  const int room = clusters_held(ctx, kern, cluster, L::kThreads, L::kBytes, known);
+  const List list(a.workspace);
+  const bool pdl = ctx.pdl;
+  ctx.pdl = true;
+  const cudaError_t r = launch_clusters(ctx, kern, cluster, dim3((unsigned)((room > 0 ? room : 1) * cluster)), dim3(L::kThreads), L::kBytes, a,
+                                        cluster, 1, (const uint32_t*)list.counts, (const Item*)list.items, a.M, 1, ctx.status);
+  ctx.pdl = pdl;
+  return r;
+}
+
 }  // namespace
+
+cudaError_t launch_lora_small(LaunchCtx& ctx, const Lora& a) {
+  if (a.max_rank <= 8) return launch_small_r<1>(ctx, a);
+  if (a.max_rank <= 16) return launch_small_r<2>(ctx, a);
+  if (a.max_rank <= 32) return launch_small_r<4>(ctx, a);
+  if (a.max_rank <= 64) return launch_small_r<8>(ctx, a);
+  return launch_small_r<16>(ctx, a);
+}
 
 cudaError_t launch_lora_tile(LaunchCtx& ctx, const Lora& a);
 

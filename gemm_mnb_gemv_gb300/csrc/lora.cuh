@@ -48,10 +48,9 @@ __device__ __forceinline__ int row_power(float top) {
   return top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
 }
 
-// A call's items, largest first: those with more than half a tile's rows from the front of `list`, the others from its
-// back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
+// A call's items: those with more than `few` rows from the front of `list`, the others from its back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
 template <int TM>
-__global__ void __launch_bounds__(1024) list_kernel(const Lora a, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
+__global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
   constexpr int H = (TM + 31) / 32;
   __shared__ uint32_t count[2];
   pdl_launch_dependents();
@@ -59,23 +58,30 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, uint32_t* coun
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x < 2) count[threadIdx.x] = 0;
   __syncthreads();
+  auto fetch = [&](int m0, int (&v)[H]) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int i = 32 * h + lane;
+      v[h] = -2;  // no row
+      if (i < TM && m0 + i < a.M) v[h] = max(a.adapter[m0 + i], -1);
+    }
+  };
+  int next[H];
+  fetch(warp * TM, next);
   for (int m0 = warp * TM; m0 < a.M; m0 += 32 * TM) {
     int v[H];
     uint32_t left[H], any = 0;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const int i = 32 * h + lane;
-      v[h] = -2;
-      if (i < TM && m0 + i < a.M) {
-        v[h] = max(a.adapter[m0 + i], -1);
-        if (v[h] >= a.count) {
-          report_status(status, kStatusBadIndex);
-          v[h] = -1;
-        }
+      v[h] = next[h];
+      if (v[h] >= a.count) {
+        report_status(status, kStatusBadIndex);
+        v[h] = -1;
       }
       left[h] = __ballot_sync(kFull, v[h] != -2);
       any |= left[h];
     }
+    fetch(m0 + 32 * TM, next);
     while (any) {
       int value = -2;
 #pragma unroll
@@ -92,7 +98,7 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, uint32_t* coun
         n += __popc(same[h]);
       }
       if (lane == 0) {
-        const int small = n <= TM / 2;
+        const int small = n <= few;
         const int at = (int)atomicAdd(&count[small], 1u);
         list[small ? capacity - 1 - at : at] = {m0, value, {(uint64_t)same[1] << 32 | same[0], (uint64_t)same[3] << 32 | same[2]}};
       }
@@ -102,6 +108,8 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, uint32_t* coun
   if (threadIdx.x < 2) counts[threadIdx.x] = count[threadIdx.x];
 }
 
+constexpr int kSmallItem = 16;  // rows of the items that the tcgen05 kernel leaves to the other one
+
 // The list's places in a call's workspace.
 struct List {
   uint32_t* counts;
@@ -110,4 +118,8 @@ struct List {
 };
 
 }  // namespace lora
+
+// The small items of a list that is there already, beside the kernel before, whose end it waits for at its own.
+cudaError_t launch_lora_small(LaunchCtx& ctx, const Lora& a);
+
 }  // namespace mnb

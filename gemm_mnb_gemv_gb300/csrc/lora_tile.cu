@@ -11,8 +11,9 @@
 //                the item's rows are neighbours (as a prompt's are), else row by row in 16-byte asynchronous copies; down and up by
 //                those (ranks end anywhere; a whole stage takes the four warps 0.75 us, more than its share of the bandwidth);
 //   warp 4       MMA issuer (one lane) and tensor memory;
-//   warps 8-15   exchange and epilogue: a row a thread; a stage's results replace its base in shared memory and leave it
-//                as whole lines.
+//   warps 8-15   exchange and epilogue: a row and 64 columns of a stage a thread, stored as whole sectors.
+// Items of up to 16 rows (other requests' single tokens) are left to the kernel of lora.cu, launched behind: it starts on the SMs
+// that this one leaves free. (A row alone takes a cluster 15 us here: 1500 rows of a prompt with 63 such rows 88 us.)
 // Every wait is bounded: a role whose wait gave up reports it and stops, the others run into their own limits, and the
 // rows left get NaN.
 #include <cuda.h>
@@ -27,7 +28,8 @@ namespace {
 
 using namespace lora;
 
-constexpr int kRows = 128, kSpan = 128, kThreads = 512, kEpiWarps = 8, kProducers = 128;
+constexpr int kRows = 128, kSpan = 128, kEpiWarps = 8, kThreads = 256 + 32 * kEpiWarps, kProducers = 128;
+constexpr int kPieces = kEpiWarps / 4, kOwnCols = kSpan / kPieces;  // of an epilogue warp in a stage
 
 template <int RP>
 struct TileGeo {
@@ -52,9 +54,6 @@ __device__ __forceinline__ uint32_t part_place(int row, int chunk) {
   return (uint32_t)(row * RP * 4 + (chunk ^ (kChunks >= 8 ? row & 7 : row >> 1 & 3)) * 16);
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
@@ -83,7 +82,12 @@ __device__ __forceinline__ bool cluster_mbar_try_wait(uint64_t* bar, uint32_t pa
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity) {
+// Waits, for a whole warp; what goes beyond the first try is kept out of line: the roles' code has to stay in the instruction cache together.
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait_bounded(bar, parity)); }
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, mbar_try_wait(bar, parity)) || wait_more(bar, parity);
+}
+__device__ __noinline__ bool cluster_mbar_wait(uint64_t* bar, uint32_t parity) {
   if (cluster_mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 0; i < kSpinLimit; ++i) {
@@ -109,11 +113,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 }
 
 // Place of the n-th set bit.
-__device__ __forceinline__ int nth_bit(const uint64_t (&m)[2], int n) {
+__device__ __noinline__ int nth_bit(uint64_t m0, uint64_t m1, int n) {
   int at = 0;
-  uint64_t w = m[0];
+  uint64_t w = m0;
   const int c0 = __popcll(w);
-  if (n >= c0) n -= c0, w = m[1], at = 64;
+  if (n >= c0) n -= c0, w = m1, at = 64;
 #pragma unroll
   for (int s = 32; s; s >>= 1) {
     const int c = __popcll(w & ((1ull << s) - 1));
@@ -132,7 +136,7 @@ struct Work {
 template <int RP>
 __global__ void __launch_bounds__(kThreads, 1)
     lora_tile_kernel(const Lora a, const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap base_map, int maps,
-                     int cluster, const uint32_t* counts, const Item* list, int capacity, uint32_t* status) {
+                     int cluster, const uint32_t* counts, const Item* list, uint32_t* status) {
   using L = TileGeo<RP>;
   constexpr int S = L::kStages;
   constexpr uint32_t kColD1 = 0, kColD2 = 128;  // tensor memory columns: partial s, two buffers of results
@@ -164,18 +168,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_arrive();  // the others' barriers are there before anything arrives at them
   cluster_wait();
   const uint32_t tmem = tmem_base;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // behind the wait: the launch for the small items reads the list before its own
 
   const int units = (a.K + 63) / 64, blocks = (a.N + 31) / 32;
   const int k0 = 64 * (int)((int64_t)units * cta / cluster), k1 = min(a.K, 64 * (int)((int64_t)units * (cta + 1) / cluster));
   const int n0 = 32 * (int)((int64_t)blocks * cta / cluster), n1 = min(a.N, 32 * (int)((int64_t)blocks * (cta + 1) / cluster));
-  const bool base_vec = a.base && a.base_stride % 8 == 0, out_vec = a.out_stride % 8 == 0;
-  const int big = (int)counts[0], items = big + (int)counts[1], step = gridDim.x / cluster;
+  const bool base_vec = a.base && a.base_stride % 8 == 0, out_vec = a.out_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  const int items = (int)counts[0], step = gridDim.x / cluster;  // the small ones are another kernel's
   const bool in_place = a.base == a.out;
   auto work_of = [&](int it) {
     Work w;
-    w.item = list[it < big ? it : capacity - 1 - (it - big)];
+    w.item = list[it];
     w.n_rows = __popcll(w.item.rows[0]) + __popcll(w.item.rows[1]);
     const int v = w.item.adapter;
     w.rank = v < 0 ? 0 : a.ranks ? min(max(a.ranks[v], 0), a.max_rank) : a.max_rank;
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto find_rows = [&](const void* p, int64_t stride) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          at[i] = static_cast<const __half*>(p) + (i < mine ? w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i) : 0) * stride + 8 * c8;
+          at[i] = static_cast<const __half*>(p) + (i < mine ? w.item.m0 + nth_bit(w.item.rows[0], w.item.rows[1], r8 + 16 * i) : 0) * stride + 8 * c8;
       };
       if (!x_box && w.down_stages > 0) find_rows(a.x, a.x_stride);
       const uint32_t to = swizzled(r8, c8);
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool epi = by_epi >> slot & 1;
           uint64_t* bar = epi ? &empty_epi[slot] : &empty_mma[slot];
           uint32_t& phase = epi ? epi_phase : mma_phase;
-          if (!__all_sync(kFull, mbar_wait_bounded(bar, phase >> slot & 1))) {
+          if (!wait_warp(bar, phase >> slot & 1)) {
             give_up(kStatusEmptyWait);
             break;
           }
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (q < w.down_stages) {
           const int k = k0 + q * kSpan;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int kk = k + 64 * h;
             if (kk + 8 * c8 < k1) {  // steps beyond k1 are not made, nor are columns of s beyond the rank used
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n = n0 + (q - w.down_stages) * kSpan;
           if (base_vec && !base_box) {
             if (q == w.down_stages) find_rows(a.base, a.base_stride);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               const int nn = n + 64 * h + 8 * c8;
               if (nn + 8 <= n1) {
@@ -274,13 +278,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if (nn < n1) {
                 stored = true;
                 for (int i = 0; i < mine; ++i) {
-                  const __half* row = static_cast<const __half*>(a.base) + (int64_t)(w.item.m0 + nth_bit(w.item.rows, r8 + 16 * i)) * a.base_stride;
+                  const __half* row = static_cast<const __half*>(a.base) + (int64_t)(w.item.m0 + nth_bit(w.item.rows[0], w.item.rows[1], r8 + 16 * i)) * a.base_stride;
                   copy_some(act + h * (kRows * 128) + to + i * 2048, row + nn, 2 * (n1 - nn));
                 }
               }
             }
           }
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < (RP > 64 ? 2 : 1); ++h) {
             const int col = 64 * h + 8 * c8, have = w.rank - col;
             const __half* p = up + (int64_t)n * a.max_rank + 64 * h;
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot = 0, results = 0;
     uint32_t full_phase = 0, d2_phase = 0, s_phase = 0;
     auto wait_full = [&]() {
-      if (!__all_sync(kFull, mbar_wait_bounded(&full[slot], full_phase >> slot & 1))) give_up(kStatusMmaWait);
+      if (!wait_warp(&full[slot], full_phase >> slot & 1)) give_up(kStatusMmaWait);
       full_phase ^= 1u << slot;
       tc::fence_proxy_async_smem();  // the copies are generic writes, the products read through the async proxy
       tc::fence_after_sync();
@@ -339,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = tc::idesc_f16_f32(kRows, w.cols);
         const int steps = (min(kSpan, k1 - k0 - q * kSpan) + 15) / 16;
         if (leader) {
+#pragma unroll 1
           for (int kk = 0; kk < steps; ++kk)
             tc::mma_f16(tmem + kColD1, da + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
                         db + (((kk / 4) * (RP * 128) + (kk % 4) * 32) >> 4), idesc, q > 0 || kk > 0);
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.rank > 0) {
           const int b = results & 1;
           if (results >= 2) {
-            if (!__all_sync(kFull, mbar_wait_bounded(&d2_empty[b], d2_phase >> b & 1))) {
+            if (!wait_warp(&d2_empty[b], d2_phase >> b & 1)) {
               give_up(kStatusMmaWait);
               break;
             }
@@ -369,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t da = tc::smem_desc_k_sw128(s_at), db = tc::smem_desc_k_sw128(ring + slot * L::kSlot + L::kAct);
           const uint32_t idesc = tc::idesc_f16_f32(kRows, kSpan);
           if (leader) {
+#pragma unroll 1
             for (int kk = 0; kk < w.cols / 16; ++kk)
               tc::mma_f16(tmem + kColD2 + 128 * b, da + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
                           db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, kk > 0);
@@ -386,20 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     (void)mbar_wait_bounded(&drained, 0);
   } else if (warp >= 8) {
     // ------------------------------ exchange and epilogue -------------------------------
-    const int e = warp - 8, quarter = warp & 3, half = e >> 2;  // rows 32 quarter .., columns 64 half ..
+    const int e = warp - 8, quarter = warp & 3, piece = e >> 2;  // rows 32 quarter .., columns kOwnCols piece ..
     const int r = quarter * 32 + lane;
     const uint32_t lane_at = tmem + ((uint32_t)(quarter * 32) << 16);
     int slot = 0, results = 0;
     uint32_t full_phase = 0, d1_phase = 0, d2_phase = 0, s_phase = 0;
     for (int it = id; it < items; it += step) {
       const Work w = work_of(it);
-      const int row = r < w.n_rows ? w.item.m0 + nth_bit(w.item.rows, r) : -1;
+      const int row = r < w.n_rows ? w.item.m0 + nth_bit(w.item.rows[0], w.item.rows[1], r) : -1;
       if (w.rank > 0) {
         // ---- this CTA's partial sums to shared memory ----
-        constexpr int kOwn = RP >= 32 ? RP / 2 : 16;  // columns of a warp; of the smallest rank half the warps have none
-        const int col0 = half * kOwn;
+        constexpr int kOwn = RP >= 16 * kPieces ? RP / kPieces : 16;  // columns of a warp; of the smaller ranks some warps have none
+        const int col0 = piece * kOwn;
         if (w.down_stages > 0) {
-          if (ok && !__all_sync(kFull, mbar_wait_bounded(&d1_full, d1_phase))) give_up(kStatusMmaWait);
+          if (ok && !wait_warp(&d1_full, d1_phase)) give_up(kStatusMmaWait);
           d1_phase ^= 1u;
           tc::fence_after_sync();
           for (int i = 0; i < w.down_stages; ++i) {  // their slots are the MMA issuer's to free
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
           if (col0 < RP) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kOwn; c += 16) {
               float v[16];
               const bool some = w.down_stages > 0 && col0 + c < w.cols;
@@ -456,80 +462,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float factor = ok && w.rank > 0 ? factors[r] : 0.0f;
       // ---- out = base + s up, 128 columns at a time ----
       for (int q = w.down_stages; q < w.stages; ++q) {
-        const int n = n0 + (q - w.down_stages) * kSpan + 64 * half, width = min(64, n1 - n);
-        const uint32_t tile = ring + slot * L::kSlot + half * (kRows * 128);
         const int b = results & 1;
         if (ok && w.rank > 0) {
-          if (!__all_sync(kFull, mbar_wait_bounded(&d2_full[b], d2_phase >> b & 1))) give_up(kStatusMmaWait);
+          if (!wait_warp(&d2_full[b], d2_phase >> b & 1)) give_up(kStatusMmaWait);
           d2_phase ^= 1u << b;
           tc::fence_after_sync();
         }
-        if (ok && !__all_sync(kFull, mbar_wait_bounded(&full[slot], full_phase >> slot & 1))) give_up(kStatusFullWait);
+        if (ok && !wait_warp(&full[slot], full_phase >> slot & 1)) give_up(kStatusFullWait);
         full_phase ^= 1u << slot;
-        if (!ok) {
-          if (row >= 0)
-            for (int i = 0; i < width; ++i) static_cast<__half*>(a.out)[(int64_t)row * a.out_stride + n + i] = __float2half(NAN);
-        } else if (width > 0) {
-          if (!base_vec) {  // rows that lie anywhere, or zeros: put where the copies would have
-            for (int i = 0; i < 32; ++i) {
-              const int from = __shfl_sync(kFull, row, i);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c = lane + 32 * h;
-                __half v = __float2half(0.0f);
-                if (a.base && from >= 0 && c < width) v = static_cast<const __half*>(a.base)[(int64_t)from * a.base_stride + n + c];
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + swizzled(quarter * 32 + i, c / 8) + (c & 7) * 2), "h"(__half_as_ushort(v))
-                             : "memory");
-              }
-            }
-            __syncwarp();
-          }
-          if (w.rank > 0) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {  // 32 columns
-              float d[32];
-              tc::tmem_ld32(lane_at + kColD2 + 128 * b + 64 * half + 32 * g, d);
-              tc::tmem_wait_ld();
+        if (quarter * 32 < w.n_rows) {
+#pragma unroll 1
+          for (int g = 0; g < kOwnCols; g += 32) {
+            const int col = piece * kOwnCols + g;  // of the stage
+            const int n = n0 + (q - w.down_stages) * kSpan + col, width = min(32, n1 - n);
+            if (width <= 0) break;
+            const uint32_t tile = ring + slot * L::kSlot + col / 64 * (kRows * 128);
+            const int ch0 = col % 64 / 8;  // first 16-byte chunk of the 32 columns
+            uint32_t y[16];
+            if (base_vec) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const uint32_t at = tile + swizzled(r, 4 * g + c);
-                const uint4 v = lds128_a(at);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[4];
+                const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
+                y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
+              }
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 x = half2_floats(u[i]);
-                  o[i] = half2_bits(fmaf(d[8 * c + 2 * i], factor, x.x), fmaf(d[8 * c + 2 * i + 1], factor, x.y));
-                }
-                sts128(at, make_uint4(o[0], o[1], o[2], o[3]));
+              for (int i = 0; i < 16; ++i) y[i] = 0;
+              if (a.base && row >= 0) {
+                const unsigned short* p = static_cast<const unsigned short*>(a.base) + (int64_t)row * a.base_stride + n;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i < width) y[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
               }
             }
-            __syncwarp();
-          }
-          // whole lines: 8 lanes have a row's 64 columns
-          if (out_vec && width == 64) {
+            if (w.rank > 0) {
+              float d[32];
+              tc::tmem_ld32(lane_at + kColD2 + 128 * b + col, d);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int from = 4 * i + lane / 8, ch = lane % 8;
-              const int to = __shfl_sync(kFull, row, from);
-              const uint4 y = lds128_a(tile + swizzled(quarter * 32 + from, ch));
-              if (to >= 0) *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + (int64_t)to * a.out_stride + n + 8 * ch) = y;
+              for (int i = 0; i < 16; ++i) {
+                const float2 x = half2_floats(y[i]);
+                y[i] = half2_bits(fmaf(d[2 * i], factor, x.x), fmaf(d[2 * i + 1], factor, x.y));
+              }
             }
-          } else {
-            for (int i = 0; i < 32; ++i) {
-              const int to = __shfl_sync(kFull, row, i);
+            if (!ok) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c = lane + 32 * h;
-                if (to >= 0 && c < width)
-                  static_cast<__half*>(a.out)[(int64_t)to * a.out_stride + n + c] =
-                      __ushort_as_half((unsigned short)lds_u16_a(tile + swizzled(quarter * 32 + i, c / 8) + (c & 7) * 2));
+              for (int i = 0; i < 16; ++i) y[i] = 0x7fff7fffu;
+            }
+            if (row >= 0) {
+              __half* p = static_cast<__half*>(a.out) + (int64_t)row * a.out_stride + n;
+              if (out_vec && width == 32) {  // whole sectors
+#pragma unroll
+                for (int c = 0; c < 16; c += 8)
+                  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * c), "r"(y[c]), "r"(y[c + 1]),
+                               "r"(y[c + 2]), "r"(y[c + 3]), "r"(y[c + 4]), "r"(y[c + 5]), "r"(y[c + 6]), "r"(y[c + 7])
+                               : "memory");
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i < width) p[i] = __ushort_as_half((unsigned short)(y[i / 2] >> (16 * (i & 1))));
               }
             }
           }
         }
         tc::fence_before_sync();
-        tc::fence_proxy_async_smem();  // a tensor copy may write these bytes next
         __syncwarp();
         if (lane == 0 && ok) {
           if (w.rank > 0) mbar_arrive(&d2_empty[b]);
@@ -582,7 +578,7 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   CUtensorMap x_map = {}, base_map = {};
   const int maps = (make_map(&x_map, a.x, a.M, a.K, a.x_stride) ? 1 : 0) | (make_map(&base_map, a.base, a.M, a.N, a.base_stride) ? 2 : 0);
   const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, list.counts, list.items, a.M, ctx.status);
+  e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, kSmallItem, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   static std::atomic<int> known[4][64];
   int room[4];
@@ -591,7 +587,8 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
   e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, x_map, base_map, maps,
-                      cluster, (const uint32_t*)list.counts, (const Item*)list.items, a.M, ctx.status);
+                      cluster, (const uint32_t*)list.counts, (const Item*)list.items, ctx.status);
+  if (e == cudaSuccess) e = launch_lora_small(ctx, a);
   ctx.pdl = pdl;
   return e;
 }
