@@ -885,7 +885,7 @@ def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, workspace=None, out=None,
     else:
         os_ = _matrix("out", out, shape, dtype, guard)
     lib, raw_stream = load_library(), _stream_of(dev, stream)
-    need = 0 if M <= 64 and workspace is None else lib.mnb_lora_workspace_bytes(_size(M))
+    need = 0 if M <= 256 and workspace is None else lib.mnb_lora_workspace_bytes(_size(M))
     workspace = _room(workspace, need, x.device, dev, stream, raw_stream, guard)
     args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard), bp, bs or 0,
             _size(N), *_room_args(workspace), out.data_ptr(), os_, raw_stream)

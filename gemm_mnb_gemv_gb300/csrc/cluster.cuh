@@ -27,6 +27,12 @@ __device__ __forceinline__ float4 cluster_ld_f4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void cluster_st_u64(uint32_t addr, uint32_t lo, uint32_t hi) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(lo), "r"(hi) : "memory");
+}
+__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 // Sum over the CTAs, in their order, of the float4 at this CTA's address; eight loads in flight.
 __device__ __forceinline__ float4 cluster_sum_f4(uint32_t addr, int cluster) {
   float4 v = make_float4(0, 0, 0, 0);

@@ -9,7 +9,9 @@
 // Rows are the M side of the warp's matrix instructions, ranks (then output columns) the N side; a lane takes 8 consecutive
 // elements of the inner index, which both operands number alike.
 // fp16 activations: s is rounded to fp16 after its row was scaled by a power of two to [2^13, 2^14), as the result is
-// rounded. fp32: x and s are split into two tf32 parts (2^-22 together), the weights are exact in tf32.
+// rounded. fp32: s is held as two fp16 of that scale, and x as two of the scale of the 32 elements that a granule of K has of a row;
+// each is multiplied on its own and the granule's scale put back in fp32 (2^-22; two tf32 parts took twice the instructions at half
+// their rate).
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -21,26 +23,16 @@ namespace {
 
 using namespace lora;
 
-// x as two tf32
+// Two fp32 as fp16 pairs: hi + lo is within 2^-22 of them.
 struct Split {
   uint32_t hi, lo;
 };
-__device__ __forceinline__ uint32_t tf32(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
+__device__ __forceinline__ Split split(float x, float y) {
+  const uint32_t h = half2_bits(x, y);
+  const float2 f = half2_floats(h);
+  return {h, half2_bits(x - f.x, y - f.y)};
 }
-__device__ __forceinline__ Split split(float x) {
-  const uint32_t h = tf32(x);
-  return {h, tf32(x - __uint_as_float(h))};
-}
-// c += A . B, m16n8k8: lane 4g + t holds A rows g, g + 8 and B column g at k = t, t + 4
-__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // RB: ranks in eights; WM: row tiles of 16.
 template <int RB, int WM, bool F32>
@@ -54,21 +46,25 @@ struct Geo {
   static constexpr int kAct = TM * kRow, kWeight = RP * kSpan * 2;
   static constexpr int kStage = kAct + kWeight;
   static constexpr int kPart = (WN - 1) * TM * RP * 4;        // partial sums of the warps; the CTA's own in the first
-  static constexpr int kSRow = F32 ? RP * 4 + 8 : RP >= 64 ? RP * 2 + 64 : RP * 2;  // bytes of a row of s
-  static constexpr int kS = (TM * kSRow + 127) / 128 * 128;
-  // Stages that fit when an SM holds n CTAs; as many CTAs as can have two (16 warps an SM are what registers allow).
+  static constexpr int kSRow = RP >= 64 ? RP * 2 + 64 : RP * 2;  // bytes of a row of s
+  static constexpr int kSHalf = (TM * kSRow + 127) / 128 * 128, kS = kSHalf * (F32 ? 2 : 1);  // fp32: the low parts behind the high ones
+  // Stages that fit when an SM holds n CTAs. As many CTAs as can have three, or else two (16 warps an SM are what registers allow).
   static constexpr int fit(int n) {
     const int stages = (228 * 1024 / n - 1024 - 768 - kPart - kS) / kStage;
     return stages > 4 ? 4 : stages;
   }
-  static constexpr int kMost = 16 / kWarps;
-  static constexpr int kCtas = fit(kMost) >= 2 ? kMost : kMost > 2 && fit(3) >= 2 ? 3 : fit(2) >= 2 ? 2 : 1;
+  static constexpr int most(int stages) {
+    int n = 16 / kWarps;
+    while (n > 1 && fit(n) < stages) --n;
+    return n;
+  }
+  static constexpr int kCtas = fit(most(3)) >= 3 && most(3) + 1 >= most(2) ? most(3) : most(2);
   static constexpr int kStages = fit(kCtas);
   static constexpr int kBytes = kStages * kStage + kPart + kS;
   static_assert(kStages >= 2, "one stage is read while the next one lands");
-  // With two stages a slot is filled again behind a second barrier, as soon as it is free; with more, behind the next stage's.
-  static constexpr bool kTwo = kStages == 2;
-  static constexpr int kAhead = kTwo ? 2 : kStages - 1;
+  // With few stages a slot is filled again behind a second barrier, as soon as it is free; with more, behind the next stage's.
+  static constexpr bool kFew = kStages <= 3;
+  static constexpr int kAhead = kFew ? kStages : kStages - 1;
 };
 
 // Where 16-byte chunk `chunk` of a row lies in it: the chunks that a quarter warp reads of two neighbouring rows come from
@@ -109,36 +105,38 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   const bool base_vec = a.base && a.base_stride % kVec == 0, out_vec = a.out_stride % kVec == 0;
   const bool in_place = a.base == a.out;
 
-  // Without a list (one tile's adapters are found by each cluster itself): cluster `id` takes tile id / subs and its adapter id % subs,
-  // in the order of their first rows.
-  // With one: all its items, or the small ones alone.
-  const int big = list && !small_only ? (int)__ldcg(counts) : 0, items = list ? big + (int)__ldcg(counts + 1) : 1;
-  const int step = list ? gridDim.x / cluster : 1;
-  for (int it = list ? id : 0; it < items; it += step) {
+  // With a list: all its items, or the small ones alone. Without one each cluster finds its tile's adapters itself: cluster `id` takes
+  // tile id / subs and every subs-th of its adapters, in the order of their first rows.
+  const int big = list && !small_only ? (int)__ldcg(counts) : 0;
+  int items, first, step, of_row = -2;
+  uint32_t same = 0, firsts = 0;
+  const int m0 = id / subs * TM;
+  if (list) {
+    items = big + (int)__ldcg(counts + 1), first = id, step = gridDim.x / cluster;
+  } else {
+    first = id % subs, step = subs;
+    if (lane < TM && m0 + lane < a.M) {
+      of_row = max(a.adapter[m0 + lane], -1);
+      if (of_row >= a.count) {
+        if (first == 0 && cta == 0 && warp == 0) report_status(status, kStatusBadIndex);
+        of_row = -1;
+      }
+    }
+    same = __match_any_sync(kFull, of_row);
+    firsts = __ballot_sync(kFull, of_row != -2 && __ffs(same) - 1 == lane);
+    items = __popc(firsts);
+    for (int k = 0; k < first; ++k) firsts &= firsts - 1;
+  }
+  for (int it = first; it < items; it += step) {
     Item item;
     if (list) {
       const uint64_t* p = reinterpret_cast<const uint64_t*>(list + (it < big ? it : capacity - 1 - (it - big)));
       const uint64_t head = __ldcg(p);
       item = {(int)(uint32_t)head, (int)(head >> 32), {__ldcg(p + 1), __ldcg(p + 2)}};
     } else {
-      item.m0 = id / subs * TM;
-      const int i = lane, want = id % subs;
-      int v = -2;
-      if (i < TM && item.m0 + i < a.M) {
-        v = max(a.adapter[item.m0 + i], -1);
-        if (v >= a.count) {
-          if (want == 0 && cta == 0 && warp == 0) report_status(status, kStatusBadIndex);
-          v = -1;
-        }
-      }
-      const uint32_t same = __match_any_sync(kFull, v);
-      uint32_t firsts = __ballot_sync(kFull, v != -2 && __ffs(same) - 1 == lane);
-      if (__popc(firsts) <= want) return;  // all CTAs of the cluster alike
-      for (int k = 0; k < want; ++k) firsts &= firsts - 1;
       const int from = __ffs(firsts) - 1;
-      item.adapter = __shfl_sync(kFull, v, from);
-      item.rows[0] = __shfl_sync(kFull, same, from);
-      item.rows[1] = 0;
+      item = {m0, __shfl_sync(kFull, of_row, from), {__shfl_sync(kFull, same, from), 0}};
+      for (int k = 0; k < step; ++k) firsts &= firsts - 1;
     }
     const int n_rows = __popcll(item.rows[0]) + __popcll(item.rows[1]), value = item.adapter;
     const int rank = value < 0 ? 0 : a.ranks ? min(max(__ldcg(a.ranks + value), 0), a.max_rank) : a.max_rank;
@@ -229,7 +227,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     for (; q < down_stages; ++q) {
       copy_wait<L::kAhead - 1>();
       __syncthreads();
-      if (!L::kTwo) issue(q + L::kAhead);
+      if (!L::kFew) issue(q + L::kAhead);
       if (live) {
         const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
         const int r0 = wm * 16 + g;
@@ -245,25 +243,32 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
               x[h][4 * i] = __uint_as_float(v.x), x[h][4 * i + 1] = __uint_as_float(v.y);
               x[h][4 * i + 2] = __uint_as_float(v.z), x[h][4 * i + 3] = __uint_as_float(v.w);
             }
-          uint32_t hi[4][4], lo[4][4];
+          Split v[2][4];
+          float back[2];
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
+          for (int h = 0; h < 2; ++h) {
+            float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const Split v = split(x[i & 1][2 * s + i / 2]);
-              hi[s][i] = v.hi, lo[s][i] = v.lo;
-            }
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[h][i]));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));  // four lanes have the granule's 32 elements of a row
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            const int p = row_power(top);
+            const float f = pow2(-p);
+            back[h] = pow2(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = split(x[h][2 * i] * f, x[h][2 * i + 1] * f);
+          }
 #pragma unroll
           for (int j = 0; j < RB; ++j) {
             if (j * 8 < rank) {
               const uint4 w = lds128_a(weight + (j * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+              float d[4];
+              mma16816_zero(d, v[0][0].lo, v[1][0].lo, v[0][1].lo, v[1][1].lo, w.x, w.y);
+              mma16816(d, v[0][2].lo, v[1][2].lo, v[0][3].lo, v[1][3].lo, w.z, w.w);
+              mma16816(d, v[0][0].hi, v[1][0].hi, v[0][1].hi, v[1][1].hi, w.x, w.y);
+              mma16816(d, v[0][2].hi, v[1][2].hi, v[0][3].hi, v[1][3].hi, w.z, w.w);
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                const float2 b = half2_floats(u[s]);
-                mma1688(acc[j], lo[s], __float_as_uint(b.x), __float_as_uint(b.y));
-                mma1688(acc[j], hi[s], __float_as_uint(b.x), __float_as_uint(b.y));
-              }
+              for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(d[i], back[i / 2], acc[j][i]);
             }
           }
         } else {
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           }
         }
       }
-      if (L::kTwo) {
+      if (L::kFew) {
         __syncthreads();
         issue(q + L::kAhead);
       }
@@ -311,12 +316,17 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
             *reinterpret_cast<float2*>(at(0, r0 + 8 * h, j * 8 + 2 * t)) = v;
           }
       }
-      // ---- over the cluster; every CTA gets all of s. RP / 4 neighbouring lanes have a row ----
+      // ---- over the cluster; every CTA gets all of s. RP / 4 neighbouring lanes have a row. Few rows: each CTA reads all of them; many: it
+      // reads its share and hands the result to the others (an eighth of the reads, one barrier more) ----
+      constexpr bool kShare = WM > 1;
       cluster_arrive();
       cluster_wait();
       const float scale = a.scales ? __ldcg(a.scales + value) : 1.0f;
-      for (int e0 = warp * 128; e0 < n_rows * RP; e0 += kThreads * 4) {
-        const int e = e0 + lane * 4, r = e / RP, col = e % RP;
+      const int e_first = kShare ? TM * cta / cluster * RP : 0, e_end = kShare ? min(TM * (cta + 1) / cluster, n_rows) * RP : n_rows * RP;
+      for (int e0 = e_first + warp * 128; e0 < e_end; e0 += kThreads * 4) {
+        // a warp may reach beyond the last row, in a tile or a share that is less than 128 elements
+        const bool mine = e0 + lane * 4 < e_end;
+        const int e = mine ? e0 + lane * 4 : e_first, r = e / RP, col = e % RP;
         float4 v = cluster_sum_f4(smem_u32(part + e), cluster);
         if (col + 4 > rank) {
           if (col >= rank) v.x = 0.0f;
@@ -325,21 +335,27 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           v.w = 0.0f;
         }
         uint8_t* row = s_mem + r * L::kSRow;
-        if constexpr (F32) {
-          *reinterpret_cast<float2*>(row + col * 4) = make_float2(v.x, v.y);
-          *reinterpret_cast<float2*>(row + col * 4 + 8) = make_float2(v.z, v.w);
-          if (col == 0) factors[r] = scale;
-        } else {
-          float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+        float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-          for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-          const int p = row_power(top);
-          const float f = __uint_as_float((uint32_t)(127 - p) << 23);
-          *reinterpret_cast<uint2*>(row + col * 2) = make_uint2(half2_bits(v.x * f, v.y * f), half2_bits(v.z * f, v.w * f));
+        for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        const int p = row_power(top);
+        const float f = pow2(-p);
+        const Split x = split(v.x * f, v.y * f), y = split(v.z * f, v.w * f);
+        if constexpr (kShare) {
+          const uint32_t to = smem_u32(row + col * 2);
+          for (int c = 0; mine && c < cluster; ++c) {
+            cluster_st_u64(cluster_map(to, c), x.hi, y.hi);
+            if constexpr (F32) cluster_st_u64(cluster_map(to + L::kSHalf, c), x.lo, y.lo);
+            if (col == 0) cluster_st_f32(cluster_map(smem_u32(&factors[r]), c), scalbnf(scale, p));
+          }
+        } else if (mine) {
+          *reinterpret_cast<uint2*>(row + col * 2) = make_uint2(x.hi, y.hi);
+          if constexpr (F32) *reinterpret_cast<uint2*>(row + L::kSHalf + col * 2) = make_uint2(x.lo, y.lo);
           if (col == 0) factors[r] = scalbnf(scale, p);
         }
       }
       cluster_arrive();  // no more reads of the others' sums
+      if (kShare) cluster_wait();
     }
 
     // ---- out = base + up s over this CTA's part of N ----
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     for (; q < stages; ++q) {
       copy_wait<L::kAhead - 1>();
       __syncthreads();
-      if (!L::kTwo) issue(q + L::kAhead);
+      if (!L::kFew) issue(q + L::kAhead);
       if (live) {
         const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
         const int r0 = wm * 16 + g;
@@ -377,26 +393,12 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
                   w[j][0] = lds_u32_a(p + 4 * t);
                 }
               }
-              if constexpr (F32) {
 #pragma unroll
-                for (int s = 0; s < E / 2; ++s) {
-                  const float* p = reinterpret_cast<const float*>(s_mem + r0 * L::kSRow) + 4 * E * c + E * t + 2 * s;
-                  const float2 v0 = *reinterpret_cast<const float2*>(p);
-                  const float2 v1 = *reinterpret_cast<const float2*>(reinterpret_cast<const uint8_t*>(p) + 8 * L::kSRow);
-                  const Split x0 = split(v0.x), x1 = split(v1.x), x2 = split(v0.y), x3 = split(v1.y);
-                  const uint32_t hi[4] = {x0.hi, x1.hi, x2.hi, x3.hi}, lo[4] = {x0.lo, x1.lo, x2.lo, x3.lo};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float2 f = half2_floats(w[j][s]);
-                    mma1688(d[j], lo, __float_as_uint(f.x), __float_as_uint(f.y));
-                    mma1688(d[j], hi, __float_as_uint(f.x), __float_as_uint(f.y));
-                  }
-                }
-              } else {
+              for (int part = F32 ? 1 : 0; part >= 0; --part) {  // the low parts first
                 uint32_t x[2][E / 2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const uint32_t p = smem_u32(s_mem + (r0 + 8 * h) * L::kSRow) + (4 * E * c + E * t) * 2;
+                  const uint32_t p = smem_u32(s_mem + part * L::kSHalf + (r0 + 8 * h) * L::kSRow) + (4 * E * c + E * t) * 2;
                   if constexpr (E == 8) {
                     const uint4 v = lds128_a(p);
                     x[h][0] = v.x, x[h][1] = v.y, x[h][2] = v.z, x[h][3] = v.w;
@@ -467,19 +469,20 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           }
         }
       }
-      if (L::kTwo) {
+      if (L::kFew) {
         __syncthreads();
         issue(q + L::kAhead);
       }
     }
-    if (rank > 0) cluster_wait();
+    if (WM == 1 && rank > 0) cluster_wait();
   }
   if (small_only) pdl_wait();  // who waits for this kernel waits for the one beside it too
 }
 
-// Rows up to which a cluster finds its tile's adapters itself, from which on tiles have 64 rows, and (fp16) from which on the tcgen05
-// kernel takes the call.
-constexpr int kFewRows = 64, kManyRows = 1024, kTileRows = 1024;
+// Rows up to which each cluster finds its tile's adapters itself. Beyond, a launch of 4 us makes a list of all items first (132 rows
+// of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 9.2). Rows up to which tiles have 16 rows; more
+// come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel).
+constexpr int kFewRows = 256, kTileRows = 1024;
 
 template <int RB, int WM, bool F32>
 cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
@@ -487,14 +490,18 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   auto kern = lora_kernel<RB, WM, F32>;
   static std::atomic<uint64_t> sized{0}, wide{0};
   const int tiles = (a.M + L::TM - 1) / L::TM;
-  const bool listed = a.M > kFewRows;
-  const int cluster = a.M <= 16 ? 16 : 8, subs = a.M < 16 ? a.M : 16;
+  const int cluster = a.M <= 16 ? 16 : 8;
   cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
   if (e == cudaSuccess && cluster > 8) e = allow_wide_clusters(kern, ctx.device, wide);
   if (e != cudaSuccess) return e;
-  if (!listed)
+  if (WM == 1 && a.M <= kFewRows) {
+    // A cluster for each adapter that a tile can have, as long as the GPU holds about that many: clusters without one cost their
+    // start, adapters that share one come after each other.
+    const int most = a.M < 16 ? a.M : 16, some = 8 * 16 / tiles;
+    const int subs = some > most ? most : some < 2 ? 2 : some;
     return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, subs,
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, 0, ctx.status);
+  }
   const List list(a.workspace);
   e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
@@ -511,7 +518,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
 template <int RB>
 cudaError_t launch_lora_r(LaunchCtx& ctx, const Lora& a) {
   if (!a.f32) return launch_lora_t<RB, 1, false>(ctx, a);
-  return a.M <= kManyRows ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
+  return a.M <= kTileRows ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
 }
 
 template <int RB>

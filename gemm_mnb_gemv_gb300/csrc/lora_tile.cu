@@ -57,12 +57,6 @@ __device__ __forceinline__ uint32_t part_place(int row, int chunk) {
 __device__ __forceinline__ void sts128(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
-__device__ __forceinline__ void cluster_st_u64(uint32_t addr, uint32_t lo, uint32_t hi) {
-  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(lo), "r"(hi) : "memory");
-}
-__device__ __forceinline__ void cluster_st_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 // A warp arrives once at the barrier of each CTA, lane i at CTA i's: one after the other each would wait for the writes before
 // it again (0.7 us). What the warp wrote before, and saw, is visible to those that wait there.
 __device__ __forceinline__ void cluster_mbar_arrive(uint64_t* bar, int cluster) {
@@ -437,9 +431,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           // ---- rows of this CTA's share: over the cluster, to fp16, into every CTA's operand ----
           const float scale = a.scales ? a.scales[w.item.adapter] : 1.0f;
-          const int share = kRows / cluster;
-          for (int u0 = e * 32; u0 < share * (RP / 4); u0 += kEpiWarps * 32) {  // whole warps: 16 rows of 16 are 64 chunks
-            const int u = u0 + lane, sr = (int)cta * share + u / (RP / 4), ch = u % (RP / 4);
+          const int sr0 = kRows * (int)cta / cluster, chunks = (kRows * ((int)cta + 1) / cluster - sr0) * (RP / 4);
+          for (int u0 = e * 32; u0 < chunks; u0 += kEpiWarps * 32) {
+            const bool mine = u0 + lane < chunks;
+            const int u = mine ? u0 + lane : 0, sr = sr0 + u / (RP / 4), ch = u % (RP / 4);
             const float4 v = cluster_sum_f4(part_at + part_place<RP>(sr, ch), cluster);
             float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
@@ -448,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = __uint_as_float((uint32_t)(127 - p) << 23);
             const uint32_t lo = half2_bits(v.x * f, v.y * f), hi = half2_bits(v.z * f, v.w * f);
             const uint32_t to = s_at + (ch / 16) * (kRows * 128) + swizzled(sr, ch / 2 % 8) + (ch & 1) * 8;
-            for (int c = 0; c < cluster; ++c) {
+            for (int c = 0; mine && c < cluster; ++c) {
               cluster_st_u64(cluster_map(to, c), lo, hi);
               if (ch == 0) cluster_st_f32(cluster_map(smem_u32(&factors[sr]), c), scalbnf(scale, p));
             }
@@ -544,15 +539,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 4) tc::tmem_dealloc(tmem, 512);
 }
 
-// CTAs of a cluster: of 1, 2, 4 and 8 the one with the shortest longest queue, an item's time being its part of a tile and
-// a fixed sixteenth of one (start, exchange). room: how many clusters of each size the GPU holds.
-int tile_cluster(int tiles, const int (&room)[4]) {
+// CTAs of a cluster: the number with the shortest longest queue, an item's time being its part of a tile and a fixed sixteenth
+// of one (start, exchange). room: how many clusters of each size the GPU holds.
+constexpr int kMostCtas = 8;
+int tile_cluster(int items, const int (&room)[kMostCtas]) {
   int best = 0;
   double least = 1e30;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kMostCtas; ++i) {
     if (room[i] < 1) continue;
-    const int rounds = (tiles + room[i] - 1) / room[i];
-    const double time = rounds * (1.0 / (1 << i) + 1.0 / 16);
+    const int rounds = (items + room[i] - 1) / room[i];
+    const double time = rounds * (1.0 / (i + 1) + 1.0 / 16);
     if (time < least) least = time, best = i;
   }
   return best;
@@ -580,10 +576,11 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   const List list(a.workspace);
   e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, kSmallItem, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> known[4][64];
-  int room[4];
-  for (int i = 0; i < 4; ++i) room[i] = clusters_held(ctx, kern, 1 << i, kThreads, L::kBytes, known[i]);
-  const int pick = tile_cluster((a.M + kRows - 1) / kRows, room), cluster = 1 << pick;
+  static std::atomic<int> known[kMostCtas][64];
+  int room[kMostCtas];
+  for (int i = 0; i < kMostCtas; ++i) room[i] = clusters_held(ctx, kern, i + 1, kThreads, L::kBytes, known[i]);
+  const int tiles = (a.M + kRows - 1) / kRows;  // a tile in which one prompt ends and the next begins is two items
+  const int pick = tile_cluster(tiles + tiles / 8, room), cluster = pick + 1;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
   e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, x_map, base_map, maps,

@@ -456,8 +456,9 @@ typedef struct {
  * (with the same stride; it may not overlap it otherwise) or NULL, which counts as zeros. adapter is int32 [M]: a negative one
  * leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
  * Products and sums are fp32. MNB_F16: down . x is rounded to fp16 relative to the row's largest (2^-11), as the result is;
- * MNB_F32: x and down . x enter the products with 22 bits or more. A row of x with inf or NaN gives non-finite outputs in that row.
- * `workspace` holds mnb_lora_workspace_bytes(M) bytes (0 up to 64 rows); its contents need no initialisation and are overwritten by
+ * MNB_F32: x and down . x enter the products with 22 bits, relative
+ * to the largest of 32 neighbours and of the row. A row of x with inf or NaN gives non-finite outputs in that row.
+ * `workspace` holds mnb_lora_workspace_bytes(M) bytes (0 up to 256 rows); its contents need no initialisation and are overwritten by
  * each call, so calls sharing one workspace must be ordered on one stream (from any host threads). M = 0 is valid and does
  * nothing.
  */

@@ -3,7 +3,7 @@
 Tolerances, with a = sum_r |up s| and b = sum_r |up| sum_k |down x| of the oracle:
 * lora, fp16: the result's rounding 2^-11 |out| (2^-25 where it is subnormal), s rounded once: 2^-11 a, and fp32 sums of K
   products and then R, each step of which may cut off one last place: (K / 8 + R + 64) 2^-23 b.
-* lora, fp32: the result's rounding 2^-24 |out|, x and s as two tf32 parts: 2^-22 b each, the sums as above with steps of 4: (K / 4 + R + 64)
+* lora, fp32: the result's rounding 2^-24 |out|, x and s as two fp16 parts: 2^-22 b each, the sums as above with steps of 4: (K / 4 + R + 64)
   2^-23 b.
 * softmax: z = (x - max) / T has three roundings, 3 |z| 2^-24 of p; the exponential 2 last places, 2^-22; the sum of V terms by
   threads that add at most V / 512 + 64 of them in turn, the same again for the factors that follow: (V / 512 + 80) 2^-24;

@@ -72,9 +72,9 @@ def test_oracle_lora_against_dense_products():
     (dict(base=96, out=96, base_stride=9), 1, "out_stride"),
     (dict(out=None), 1, "out is NULL"),
     (dict(out_stride=6), 1, "out_stride"),
-    (dict(M=300, ws_bytes=300 * 24 + 15), 1, "workspace"),
-    (dict(M=300, workspace=None), 1, "workspace"),
-    (dict(M=300, workspace=72), 3, "workspace"),
+    (dict(M=1300, ws_bytes=1300 * 24 + 15), 1, "workspace"),
+    (dict(M=1300, workspace=None), 1, "workspace"),
+    (dict(M=1300, workspace=72), 3, "workspace"),
 ])
 def test_lora_refusals(lib, change, expect, word):
     import gemm_mnb_gemv_gb300 as mnb
@@ -145,8 +145,8 @@ def test_verify_refusals(lib, change, expect, word):
 
 
 def test_lora_workspace_bytes(lib):
-    assert [lib.mnb_lora_workspace_bytes(M) for M in (-1, 0, 1, 64, 65, 1 << 20, (1 << 20) + 1)] == [
-        0, 0, 0, 0, 16 + 24 * 65, 16 + 24 * (1 << 20), 0]
+    assert [lib.mnb_lora_workspace_bytes(M) for M in (-1, 0, 1, 256, 257, 1 << 20, (1 << 20) + 1)] == [
+        0, 0, 0, 0, 16 + 24 * 257, 16 + 24 * (1 << 20), 0]
 
 
 def test_draft_workspace_bytes(lib):
