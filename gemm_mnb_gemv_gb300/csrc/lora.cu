@@ -480,9 +480,12 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
 }
 
 // Rows up to which each cluster finds its tile's adapters itself. Beyond, a launch of 4 us makes a list of all items first (132 rows
-// of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 9.2). Rows up to which tiles have 16 rows; more
-// come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel).
-constexpr int kFewRows = 256, kTileRows = 1024;
+// of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 9.2).
+constexpr int kFewRows = 256;
+// Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that much less often but
+// fill the GPU later. fp16, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 15.9 / 18.0 at 1000 rows, 22.5 / 18.2 at 1400; rank 64
+// 18.3 / 19.3 at 700 and 21.5 / 19.4 at 1000; rank 128 29.7 / 23.3 at 272 and 69 / 24 at 1000.
+int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
 
 template <int RB, int WM, bool F32>
 cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
@@ -518,7 +521,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
 template <int RB>
 cudaError_t launch_lora_r(LaunchCtx& ctx, const Lora& a) {
   if (!a.f32) return launch_lora_t<RB, 1, false>(ctx, a);
-  return a.M <= kTileRows ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
+  return a.M <= tile_rows(a.max_rank) ? launch_lora_t<RB, 1, true>(ctx, a) : launch_lora_t<RB, 4, true>(ctx, a);
 }
 
 template <int RB>
@@ -555,7 +558,7 @@ cudaError_t launch_lora_tile(LaunchCtx& ctx, const Lora& a);
 size_t lora_workspace_bytes(int M) { return M > kFewRows ? 16 + (size_t)M * sizeof(Item) : 0; }
 
 cudaError_t launch_lora(LaunchCtx& ctx, const Lora& a) {
-  if (!a.f32 && a.M > kTileRows) {
+  if (!a.f32 && a.M > tile_rows(a.max_rank)) {
     ctx.variant = "lora_tile_tcgen05";
     return launch_lora_tile(ctx, a);
   }

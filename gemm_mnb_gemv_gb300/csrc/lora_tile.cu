@@ -474,21 +474,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tile = ring + slot * L::kSlot + col / 64 * (kRows * 128);
             const int ch0 = col % 64 / 8;  // first 16-byte chunk of the 32 columns
             uint32_t y[16];
-            if (base_vec) {
+            if (!base_vec) {  // rows that lie anywhere, or zeros: put where the copies would have
+#pragma unroll 1
+              for (int i0 = 0; i0 < 32; i0 += 16) {
+                unsigned short v[16];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
-                y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
+                for (int i = 0; i < 16; ++i) {
+                  const int from = __shfl_sync(kFull, row, i0 + i);
+                  v[i] = 0;
+                  if (a.base && from >= 0 && lane < width)
+                    v[i] = static_cast<const unsigned short*>(a.base)[(int64_t)from * a.base_stride + n + lane];
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + swizzled(quarter * 32 + i0 + i, ch0 + lane / 8) + (lane & 7) * 2), "h"(v[i])
+                               : "memory");
               }
-            } else {
+              __syncwarp();
+            }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = 0;
-              if (a.base && row >= 0) {
-                const unsigned short* p = static_cast<const unsigned short*>(a.base) + (int64_t)row * a.base_stride + n;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i < width) y[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
-              }
+            for (int c = 0; c < 4; ++c) {
+              const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
+              y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
             }
             if (w.rank > 0) {
               float d[32];
@@ -504,21 +511,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) y[i] = 0x7fff7fffu;
             }
-            if (row >= 0) {
-              __half* p = static_cast<__half*>(a.out) + (int64_t)row * a.out_stride + n;
-              if (out_vec && width == 32) {  // whole sectors
+            if (out_vec && width == 32) {  // whole sectors
+              if (row >= 0) {
+                __half* p = static_cast<__half*>(a.out) + (int64_t)row * a.out_stride + n;
 #pragma unroll
                 for (int c = 0; c < 16; c += 8)
                   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * c), "r"(y[c]), "r"(y[c + 1]),
                                "r"(y[c + 2]), "r"(y[c + 3]), "r"(y[c + 4]), "r"(y[c + 5]), "r"(y[c + 6]), "r"(y[c + 7])
                                : "memory");
-              } else {
+              }
+            } else {  // through the base's place, a row after the other
+              __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i < width) p[i] = __ushort_as_half((unsigned short)(y[i / 2] >> (16 * (i & 1))));
+              for (int c = 0; c < 4; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + swizzled(r, ch0 + c)), "r"(y[4 * c]), "r"(y[4 * c + 1]),
+                             "r"(y[4 * c + 2]), "r"(y[4 * c + 3])
+                             : "memory");
+              __syncwarp();
+#pragma unroll 8
+              for (int i = 0; i < 32; ++i) {
+                const int to = __shfl_sync(kFull, row, i);
+                const uint32_t v = lds_u16_a(tile + swizzled(quarter * 32 + i, ch0 + lane / 8) + (lane & 7) * 2);
+                if (to >= 0 && lane < width)
+                  static_cast<unsigned short*>(a.out)[(int64_t)to * a.out_stride + n + lane] = (unsigned short)v;
               }
             }
           }
+          // where results or bases went through these bytes, a tensor copy may write them next
+          if (!base_vec || !out_vec || n1 - n0 < (q - w.down_stages + 1) * kSpan) tc::fence_proxy_async_smem();
         }
         tc::fence_before_sync();
         __syncwarp();
