@@ -750,7 +750,11 @@ def mnb_kv4_attention(q, cache: MnbKv4Cache, q_start, kv_len, page_table, scale:
 # ---------------------------------------------------------------------------
 
 
+# A call's host time is most of a small one (13 us of softmax over 30 rows, whose kernel takes 3): what the checks look at is
+# looked at in place, and only what is wrong goes through the functions that say so.
+
 _gpus = None  # asked for once: 1 to 2 us of a call
+_raw_stream_of = None  # handle of a device's current stream, without building a Stream object
 
 
 def _guard_of(dev: int):
@@ -805,12 +809,19 @@ def _vector(name, t, dtype, shape, guard):
 
 
 def _stream_of(dev, stream):
-    if stream is not None and stream.device.index != dev:
+    global _raw_stream_of
+    if stream is None:
+        if _raw_stream_of is None:
+            torch = _torch()
+            _raw_stream_of = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                              or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+        return _raw_stream_of(dev)
+    if stream.device.index != dev:
         raise ValueError(f"stream is of {stream.device}, the tensors on cuda:{dev}")
-    return _raw_stream(dev, stream)
+    return stream.cuda_stream
 
 
-def _room(workspace, need, device, dev, stream, raw_stream, guard):
+def _room(workspace, need, like, dev, stream, raw_stream, guard):
     """The workspace, or one of ``need`` bytes: the kept one on the default stream, as in the attention, else a new one of the
     stream's pool.  The caller holds it until the launch, so that no other allocation of the call gets its bytes."""
     torch = _torch()
@@ -823,13 +834,22 @@ def _room(workspace, need, device, dev, stream, raw_stream, guard):
     if stream is None and raw_stream == 0:
         workspace = _default_workspace.get(dev)
         if workspace is None or workspace.numel() < need:
-            workspace = _default_workspace[dev] = _new(need, torch.uint8, device, None)
+            workspace = _default_workspace[dev] = _new(need, torch.uint8, like.device, None)
         return workspace
-    return _new(need, torch.uint8, device, stream)
+    return _new(need, torch.uint8, like.device, stream)
 
 
-def _room_args(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+_room_bytes = {}  # (entry point, sizes) -> bytes
+
+
+def _bytes_of(name, *sizes):
+    key = (name, sizes)
+    need = _room_bytes.get(key)
+    if need is None:
+        need = getattr(_lib, name)(*map(_size, sizes))
+        if len(_room_bytes) < 4096:
+            _room_bytes[key] = need
+    return need
 
 
 def _launch(fn, args, dev, guard):
@@ -856,6 +876,7 @@ class MnbLoraPool:
         if count < 1 or count > 1 << 20 or max_rank % 8 or not 8 <= max_rank <= 128:
             raise MnbError(MNB_ERR_INVALID_ARG, f"MnbLoraPool: count={count} max_rank={max_rank} (count 1..2^20, max_rank a "
                            "multiple of 8 in 8..128)")
+        load_library()
         self.down, self.up, self.ranks, self.scales = down, up, ranks, scales
         self.arg = MnbLoraPoolArg(
             _vector("down", down, torch.float16, (count, max_rank, self.K), guard),
@@ -871,25 +892,43 @@ def mnb_lora_workspace_bytes(M: int) -> int:
 def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, workspace=None, out=None, stream=None):
     """``[M, N]`` = ``base`` (None: zeros) + each row's adapter on ``x`` ``[M, K]``; ``adapter`` int32 ``[M]``, -1 for none.
     ``out`` may be ``base``.  A workspace is shared or allocated as in ``mnb_kv4_attention``."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     dev, guard, K, N = pool.device, pool.guard, pool.K, pool.N
-    M = _two_dims("x", x, f"[M, {K}]")[0]
-    dtype, dt = x.dtype, _act_dtype("x", x)
-    xs = _matrix("x", x, (M, K), dtype, guard)
+    if type(x) is not torch.Tensor or not x.is_cuda or x.dim() != 2:
+        _two_dims("x", x, f"[M, {K}]")
+    M, cols = x.shape
+    dtype = x.dtype
+    dt = _ACT.get(dtype)
+    if dt is None:
+        dt = _act_dtype("x", x)
+    xs, one = x.stride()
+    if cols != K or one != 1 or M < 2 or guard is not None:
+        xs = _matrix("x", x, (M, K), dtype, guard)
     shape = (M, N)
-    bs = bp = None
+    bs, bp = 0, None
     if base is not None:
         bs, bp = _matrix("base", base, shape, dtype, guard), base.data_ptr()
     if out is None:
-        out, os_ = _new(shape, dtype, x.device, stream), N
+        out, os_ = x.new_empty(shape) if stream is None else _new(shape, dtype, x.device, stream), N
     else:
         os_ = _matrix("out", out, shape, dtype, guard)
-    lib, raw_stream = load_library(), _stream_of(dev, stream)
-    need = 0 if M <= 256 and workspace is None else lib.mnb_lora_workspace_bytes(_size(M))
-    workspace = _room(workspace, need, x.device, dev, stream, raw_stream, guard)
-    args = (x.data_ptr(), dt, _size(M), _size(K), xs, pool.arg, _vector("adapter", adapter, torch.int32, (M,), guard), bp, bs or 0,
-            _size(N), *_room_args(workspace), out.data_ptr(), os_, raw_stream)
-    _launch(lib.mnb_lora, args, dev, guard)
+    if type(adapter) is not torch.Tensor or adapter.dtype is not torch.int32 or not adapter.is_cuda or adapter.shape != (M,) or not (
+            adapter.is_contiguous()) or guard is not None:
+        _vector("adapter", adapter, torch.int32, (M,), guard)
+    lib, raw_stream = _lib, _stream_of(dev, stream)
+    wp, ws_bytes = None, 0
+    if M > 256 or workspace is not None:
+        workspace = _room(workspace, _bytes_of("mnb_lora_workspace_bytes", M), x, dev, stream, raw_stream, guard)
+        if workspace is not None:
+            wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    st = M if M <= _INT_MAX else -1
+    args = (x.data_ptr(), dt, st, K, xs, pool.arg, adapter.data_ptr(), bp, bs, N, wp, ws_bytes, out.data_ptr(), os_, raw_stream)
+    if guard is not None:
+        _launch(lib.mnb_lora, args, dev, guard)
+        return out
+    st = lib.mnb_lora(*args)
+    if st != MNB_OK:
+        _raise(st)
     return out
 
 
@@ -900,22 +939,38 @@ def mnb_softmax_workspace_bytes(rows: int, V: int) -> int:
 def mnb_softmax(logits, temperature=None, workspace=None, out=None, stream=None):
     """fp32 ``[rows, V]``: softmax of ``logits / temperature`` (fp32 ``[rows]``, None: 1; 0: 1 at the largest logit).  A
     workspace is shared or allocated as in ``mnb_kv4_attention``."""
-    torch = _torch()
-    shape = rows, V = _two_dims("logits", logits, "[rows, V]")
+    torch = _torch_module or _torch()
+    if type(logits) is not torch.Tensor or not logits.is_cuda or logits.dim() != 2:
+        _two_dims("logits", logits, "[rows, V]")
+    shape = logits.shape
+    rows, V = shape
+    dt = _ACT.get(logits.dtype)
+    if dt is None:
+        dt = _act_dtype("logits", logits)
     dev = logits.get_device()
-    guard = _guard_of(dev)
-    dt = _act_dtype("logits", logits)
-    stride = _matrix("logits", logits, shape, logits.dtype, guard)
-    tp = None if temperature is None else _vector("temperature", temperature, torch.float32, (rows,), guard)
-    lib, raw_stream = load_library(), _stream_of(dev, stream)
+    guard = _guard_of(dev) if _gpus != 1 else None
+    stride, one = logits.stride()
+    if one != 1 or rows < 2:
+        stride = _matrix("logits", logits, shape, logits.dtype, guard)
+    f32 = torch.float32
+    tp = None if temperature is None else _vector("temperature", temperature, f32, (rows,), guard)
+    lib, raw_stream = _lib or load_library(), _stream_of(dev, stream)
     if out is None:
-        out = _new(shape, torch.float32, logits.device, stream)
-        op = out.data_ptr()
+        out = logits.new_empty(shape, dtype=f32) if stream is None else _new(shape, f32, logits.device, stream)
     else:
-        op = _vector("out", out, torch.float32, shape, guard)
-    workspace = _room(workspace, lib.mnb_softmax_workspace_bytes(_size(rows), _size(V)), logits.device, dev, stream, raw_stream, guard)
-    args = (logits.data_ptr(), dt, _size(rows), _size(V), stride, tp, *_room_args(workspace), op, raw_stream)
-    _launch(lib.mnb_softmax, args, dev, guard)
+        _vector("out", out, f32, shape, guard)
+    wp, ws_bytes = None, 0
+    if V > 16377 or workspace is not None:
+        workspace = _room(workspace, _bytes_of("mnb_softmax_workspace_bytes", rows, V), logits, dev, stream, raw_stream, guard)
+        if workspace is not None:
+            wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    args = (logits.data_ptr(), dt, _size(rows), _size(V), stride, tp, wp, ws_bytes, out.data_ptr(), raw_stream)
+    if guard is not None:
+        _launch(lib.mnb_softmax, args, dev, guard)
+        return out
+    st = lib.mnb_softmax(*args)
+    if st != MNB_OK:
+        _raise(st)
     return out
 
 
@@ -931,26 +986,41 @@ def mnb_verify(target, draft, draft_tokens, draft_start, u_accept, u_next, works
     ``draft_tokens`` int32 and ``u_accept`` fp32 ``[drafted]``, ``draft_start`` int32 ``[batch + 1]``, ``u_next`` fp32 ``[batch]``.
     A workspace is shared or allocated as in ``mnb_kv4_attention``.
     """
-    torch = _torch()
-    rows, V = _two_dims("target", target, "[drafted + batch, V]")
-    if any(not isinstance(t, torch.Tensor) or t.dim() != 1 for t in (draft_tokens, u_next)):
+    torch = _torch_module or _torch()
+    tensor, f32, i32 = torch.Tensor, torch.float32, torch.int32
+    if type(target) is not tensor or not target.is_cuda or target.dim() != 2:
+        _two_dims("target", target, "[drafted + batch, V]")
+    if not isinstance(draft_tokens, tensor) or not isinstance(u_next, tensor) or draft_tokens.dim() != 1 or u_next.dim() != 1:
         raise ValueError("target, draft_tokens and u_next must be [drafted + batch, V], [drafted] and [batch]")
     D, B = draft_tokens.shape[0], u_next.shape[0]
+    rows, V = target.shape
     dev = target.get_device()
-    guard, f32, i32 = _guard_of(dev), torch.float32, torch.int32
-    ts = _matrix("target", target, (D + B, V), f32, guard)
+    guard = _guard_of(dev) if _gpus != 1 else None
+    ts, one = target.stride()
+    if rows != D + B or rows < 2 or one != 1 or target.dtype is not f32:
+        ts = _matrix("target", target, (D + B, V), f32, guard)
     ds, dp = 0, None
     if draft is not None:
         ds, dp = _matrix("draft", draft, (D, V), f32, guard), draft.data_ptr()
-    given = [_vector("draft_tokens", draft_tokens, i32, (D,), guard), _vector("draft_start", draft_start, i32, (B + 1,), guard),
-             _vector("u_accept", u_accept, f32, (D,), guard), _vector("u_next", u_next, f32, (B,), guard)]
-    lib, raw_stream = load_library(), _stream_of(dev, stream)
-    workspace = _room(workspace, lib.mnb_verify_workspace_bytes(_size(B), _size(V)), target.device, dev, stream, raw_stream, guard)
+    given = (_vector("draft_tokens", draft_tokens, i32, (D,), guard), _vector("draft_start", draft_start, i32, (B + 1,), guard),
+             _vector("u_accept", u_accept, f32, (D,), guard), _vector("u_next", u_next, f32, (B,), guard))
+    lib, raw_stream = _lib or load_library(), _stream_of(dev, stream)
+    workspace = _room(workspace, _bytes_of("mnb_verify_workspace_bytes", B, V), target, dev, stream, raw_stream, guard)
+    wp, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     if tokens is None:
-        tokens = _new((D + B,), i32, target.device, stream)
+        tokens = draft_tokens.new_empty(rows) if stream is None else _new((rows,), i32, target.device, stream)
+    else:
+        _vector("tokens", tokens, i32, (rows,), guard)
     if accepted is None:
-        accepted = _new((B,), i32, target.device, stream)
-    args = (target.data_ptr(), ts, dp, ds, *given, _size(B), _size(D), _size(V), *_room_args(workspace),
-            _vector("tokens", tokens, i32, (D + B,), guard), _vector("accepted", accepted, i32, (B,), guard), raw_stream)
-    _launch(lib.mnb_verify, args, dev, guard)
+        accepted = draft_tokens.new_empty(B) if stream is None else _new((B,), i32, target.device, stream)
+    else:
+        _vector("accepted", accepted, i32, (B,), guard)
+    args = (target.data_ptr(), ts, dp, ds, *given, _size(B), _size(D), _size(V), wp, ws_bytes, tokens.data_ptr(), accepted.data_ptr(),
+            raw_stream)
+    if guard is not None:
+        _launch(lib.mnb_verify, args, dev, guard)
+        return tokens, accepted
+    st = lib.mnb_verify(*args)
+    if st != MNB_OK:
+        _raise(st)
     return tokens, accepted
