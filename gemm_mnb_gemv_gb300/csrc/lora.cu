@@ -506,7 +506,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, 0, ctx.status);
   }
   const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, list.counts, list.items, a.M, ctx.status);
+  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, 0, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device

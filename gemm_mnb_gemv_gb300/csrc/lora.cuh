@@ -48,13 +48,13 @@ __device__ __forceinline__ int row_power(float top) {
   return top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
 }
 
-// A call's items: those with more than `few` rows from the front of `list`, the others from its back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
+// A call's items, with `rest` but the first of each tile: those with more than `few` rows from the front of `list`, the others from its back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
 template <int TM>
-__global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
+__global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int rest, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
   constexpr int H = (TM + 31) / 32;
   __shared__ uint32_t count[2];
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // behind the wait: the next launch reads its inputs without one
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x < 2) count[threadIdx.x] = 0;
   __syncthreads();
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, uint3
       any |= left[h];
     }
     fetch(m0 + 32 * TM, next);
+    bool skip = rest != 0;
     while (any) {
       int value = -2;
 #pragma unroll
@@ -97,11 +98,12 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, uint3
         any |= left[h];
         n += __popc(same[h]);
       }
-      if (lane == 0) {
+      if (lane == 0 && !skip) {
         const int small = n <= few;
         const int at = (int)atomicAdd(&count[small], 1u);
         list[small ? capacity - 1 - at : at] = {m0, value, {(uint64_t)same[1] << 32 | same[0], (uint64_t)same[3] << 32 | same[2]}};
       }
+      skip = false;
     }
   }
   __syncthreads();

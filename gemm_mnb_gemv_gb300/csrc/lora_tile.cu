@@ -10,7 +10,7 @@
 //   warps 0-3    producers, into one ring that runs on from product to product and item to item: x and base by tensor copies where
 //                the item's rows are neighbours (as a prompt's are), else row by row in 16-byte asynchronous copies; down and up by
 //                those (ranks end anywhere; a whole stage takes the four warps 0.75 us, more than its share of the bandwidth);
-//   warp 4       MMA issuer (one lane) and tensor memory;
+//   warp 4       MMA issuer (one lane) and tensor memory; warp 5 lets the launch behind start;
 //   warps 8-15   exchange and epilogue: a row and 64 columns of a stage a thread, stored as whole sectors.
 // Items of up to 16 rows (other requests' single tokens) are left to the kernel of lora.cu, launched behind: it starts on the SMs
 // that this one leaves free. (A row alone takes a cluster 15 us here: 1500 rows of a prompt with 63 such rows 88 us.)
@@ -162,21 +162,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_arrive();  // the others' barriers are there before anything arrives at them
   cluster_wait();
   const uint32_t tmem = tmem_base;
-  pdl_wait();
-  pdl_launch_dependents();  // behind the wait: the launch for the small items reads the list before its own
 
   const int units = (a.K + 63) / 64, blocks = (a.N + 31) / 32;
   const int k0 = 64 * (int)((int64_t)units * cta / cluster), k1 = min(a.K, 64 * (int)((int64_t)units * (cta + 1) / cluster));
   const int n0 = 32 * (int)((int64_t)blocks * cta / cluster), n1 = min(a.N, 32 * (int)((int64_t)blocks * (cta + 1) / cluster));
   const bool base_vec = a.base && a.base_stride % 8 == 0, out_vec = a.out_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-  const int items = (int)counts[0], step = gridDim.x / cluster;  // the small ones are another kernel's
   const bool in_place = a.base == a.out;
+  // Items come in turn: the first of each tile (the rows of its first row's adapter), which a warp finds itself while the list is being
+  // made, then the list's, on from the cluster where those end. The list's launch lets this one start when its own inputs are there.
+  const int tiles = (a.M + kRows - 1) / kRows, clusters = gridDim.x / cluster;
+  int items = 0x7fffffff;
+  auto more = [&](int it) {  // whether there is item `it`
+    if (it >= tiles && items == 0x7fffffff) {
+      pdl_wait();
+      items = tiles + (int)__ldcg(counts);
+    }
+    return it < items;
+  };
   auto work_of = [&](int it) {
     Work w;
-    w.item = list[it];
+    if (it < tiles) {
+      const int m0 = it * kRows;
+      int v[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) v[h] = m0 + 32 * h + lane < a.M ? __ldcg(a.adapter + m0 + 32 * h + lane) : -1;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) v[h] = v[h] < 0 || v[h] >= a.count ? -1 : v[h];
+      w.item = {m0, __shfl_sync(kFull, v[0], 0), {0, 0}};
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        w.item.rows[h / 2] |= (uint64_t)__ballot_sync(kFull, v[h] == w.item.adapter && m0 + 32 * h + lane < a.M) << (h % 2 * 32);
+    } else {
+      const uint64_t* p = reinterpret_cast<const uint64_t*>(list + (it - tiles));
+      const uint64_t head = __ldcg(p);
+      w.item = {(int)(uint32_t)head, (int)(head >> 32), {__ldcg(p + 1), __ldcg(p + 2)}};
+    }
     w.n_rows = __popcll(w.item.rows[0]) + __popcll(w.item.rows[1]);
     const int v = w.item.adapter;
-    w.rank = v < 0 ? 0 : a.ranks ? min(max(a.ranks[v], 0), a.max_rank) : a.max_rank;
+    w.rank = v < 0 ? 0 : a.ranks ? min(max(__ldcg(a.ranks + v), 0), a.max_rank) : a.max_rank;
     w.cols = (w.rank + 15) / 16 * 16;
     w.down_stages = w.rank > 0 ? (max(k1 - k0, 0) + kSpan - 1) / kSpan : 0;
     w.stages = w.rank == 0 && in_place ? 0 : w.down_stages + (max(n1 - n0, 0) + kSpan - 1) / kSpan;
@@ -193,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int slot = 0, used = 0;
     uint32_t by_epi = 0, mma_phase = 0, epi_phase = 0;  // a bit for each slot: who frees it, and the phases of both
     const int c8 = tid & 7, r8 = tid >> 3;               // chunk of 8, first row of this thread's (16 apart)
-    for (int it = id; it < items && ok; it += step) {
+    for (int it = id; ok && more(it); it += clusters) {
       const Work w = work_of(it);
       // Neighbouring rows, and enough of them that a whole box is no waste.
       const uint64_t *m = w.item.rows;
@@ -327,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto next_slot = [&]() {
       if (++slot == S) slot = 0;
     };
-    for (int it = id; it < items && ok; it += step) {
+    for (int it = id; ok && more(it); it += clusters) {
       const Work w = work_of(it);
       int q = 0;
       for (; q < w.down_stages && ok; ++q) {
@@ -384,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) tc::mma_commit(&drained);
     __syncwarp();
     (void)mbar_wait_bounded(&drained, 0);
+  } else if (warp == 5) {
+    pdl_wait();
+    pdl_launch_dependents();  // behind the wait: the launch for the small items reads the list without one
   } else if (warp >= 8) {
     // ------------------------------ exchange and epilogue -------------------------------
     const int e = warp - 8, quarter = warp & 3, piece = e >> 2;  // rows 32 quarter .., columns kOwnCols piece ..
@@ -391,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_at = tmem + ((uint32_t)(quarter * 32) << 16);
     int slot = 0, results = 0;
     uint32_t full_phase = 0, d1_phase = 0, d2_phase = 0, s_phase = 0;
-    for (int it = id; it < items; it += step) {
+    for (int it = id; more(it); it += clusters) {
       const Work w = work_of(it);
       const int row = r < w.n_rows ? w.item.m0 + nth_bit(w.item.rows[0], w.item.rows[1], r) : -1;
       if (w.rank > 0) {
@@ -430,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
           // ---- rows of this CTA's share: over the cluster, to fp16, into every CTA's operand ----
-          const float scale = a.scales ? a.scales[w.item.adapter] : 1.0f;
+          const float scale = a.scales ? __ldcg(a.scales + w.item.adapter) : 1.0f;
           const int sr0 = kRows * (int)cta / cluster, chunks = (kRows * ((int)cta + 1) / cluster - sr0) * (RP / 4);
           for (int u0 = e * 32; u0 < chunks; u0 += kEpiWarps * 32) {
             const bool mine = u0 + lane < chunks;
@@ -551,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  pdl_wait();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -594,7 +621,7 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   CUtensorMap x_map = {}, base_map = {};
   const int maps = (make_map(&x_map, a.x, a.M, a.K, a.x_stride) ? 1 : 0) | (make_map(&base_map, a.base, a.M, a.N, a.base_stride) ? 2 : 0);
   const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, kSmallItem, list.counts, list.items, a.M, ctx.status);
+  e = launch_kernel(ctx, list_kernel<kRows>, dim3(1), dim3(1024), 0, a, kSmallItem, 1, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   static std::atomic<int> known[kMostCtas][64];
   int room[kMostCtas];
