@@ -873,9 +873,9 @@ class MnbLoraPool:
         self.guard = guard = _guard_of(self.device)
         count, max_rank, self.K = down.shape
         self.N = up.shape[1]
-        if count < 1 or count > 1 << 20 or max_rank % 8 or not 8 <= max_rank <= 128:
-            raise MnbError(MNB_ERR_INVALID_ARG, f"MnbLoraPool: count={count} max_rank={max_rank} (count 1..2^20, max_rank a "
-                           "multiple of 8 in 8..128)")
+        if count < 1 or count > 1 << 20 or max_rank % 8 or not 8 <= max_rank <= 128 or max(self.K, self.N) > _INT_MAX:
+            raise MnbError(MNB_ERR_INVALID_ARG, f"MnbLoraPool: count={count} max_rank={max_rank} K={self.K} N={self.N} (count "
+                           "1..2^20, max_rank a multiple of 8 in 8..128, K and N below 2^31)")
         load_library()
         self.down, self.up, self.ranks, self.scales = down, up, ranks, scales
         self.arg = MnbLoraPoolArg(

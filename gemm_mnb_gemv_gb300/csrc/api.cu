@@ -647,6 +647,10 @@ mnb_status mnb_gemm_act_order_noalloc(const void* A, int M, mnb_weight w, const 
 
 namespace {
 
+// A call of several launches has its workspace from the first to the last: calls of several host threads on one stream with one
+// workspace, of whatever kind, have to come one after the other.
+std::mutex g_two_launches;
+
 bool kv4_geometry_ok(int num_pages, int page_size, int kv_heads, int head_dim, int group) {
   return num_pages >= 1 && page_size >= 16 && page_size <= 4096 && page_size % 16 == 0 && kv_heads >= 1 &&
          kv_heads <= 1024 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
@@ -802,10 +806,7 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
   if (window >= 1 << 30) window = 0;  // no position reaches 2^30: such a window leaves nothing out
   const mnb::Kv4Attention a = {q,     dtype == MNB_F32, T,           q_heads, q_stride,  q_start,  kv_len, page_table, batch,
                                table_stride, scale, causal != 0, window, workspace, ws_bytes, out,   lse};
-  // A call is two launches, and its workspace is theirs from the first to the second: calls of several host threads on
-  // one stream with one workspace have to come one after the other.
-  static std::mutex two_launches;
-  std::lock_guard<std::mutex> lock(two_launches);
+  std::lock_guard<std::mutex> lock(g_two_launches);
   return finish(fn, mnb::launch_kv4_attention(ctx, c, a), ctx);
 }
 
@@ -816,10 +817,6 @@ mnb_status mnb_kv4_attention(const void* q, int dtype, int T, int q_heads, int64
 // ------------------------------------------------------------------------------------
 
 namespace {
-
-// As in the attention: the launches of a call that has a workspace come one after the other, whatever other host threads do
-// on the stream.
-std::mutex g_two_launches;
 
 mnb_status check_workspace(const char* fn, const void* workspace, size_t ws_bytes, size_t need) {
   if (ws_bytes < need)

@@ -271,6 +271,19 @@ def test_softmax(env, rows, V, dtype):
             np.testing.assert_allclose(got[r].cpu().numpy(), top / top.sum(), rtol=1e-6)
 
 
+@pytest.mark.parametrize("rows,V", [(3, 1), (5, 999), (40, 16377), (7, 40001)])
+def test_softmax_in_place(env, rows, V):
+    mnb, torch, dev = env
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((rows, V)).astype(np.float32)
+    t = rng.choice([0.0, 0.5, 1.0], rows).astype(np.float32)
+    xd, td = _up(torch, dev, x, t)
+    want = mnb.mnb_softmax(xd, temperature=td)
+    assert mnb.mnb_softmax(xd, temperature=td, out=xd) is xd
+    assert torch.equal(xd, want)
+    _check_softmax(xd, x, t)
+
+
 def test_softmax_odd_rows_and_views(env):
     mnb, torch, dev = env
     V = 1003
@@ -480,6 +493,8 @@ def test_bindings_refuse(env):
         (mnb.MnbError, "base_stride", lambda: mnb.mnb_lora(x, pool, idx, base=torch.zeros(1, 12, **h).expand(3, 12))),
         (mnb.MnbError, "max_rank", lambda: mnb.MnbLoraPool(torch.zeros(2, 4, 32, **h), torch.zeros(2, 12, 4, **h))),
         (ValueError, "up must be", lambda: mnb.MnbLoraPool(torch.zeros(2, 8, 32, **h), torch.zeros(1, 12, 8, **h))),
+        (mnb.MnbError, "K=4294967312", lambda: mnb.MnbLoraPool(torch.zeros(2, 8, 1, **h).expand(2, 8, 2 ** 32 + 16), pool.up)),
+        (mnb.MnbError, "N=4294967297", lambda: mnb.MnbLoraPool(pool.down, torch.zeros(2, 1, 8, **h).expand(2, 2 ** 32 + 1, 8))),
         (ValueError, "contiguous", lambda: mnb.MnbLoraPool(torch.zeros(2, 8, 64, **h)[:, :, :32], torch.zeros(2, 12, 8, **h))),
         (TypeError, "scales must be torch.float32", lambda: mnb.MnbLoraPool(pool.down, pool.up, scales=torch.zeros(2, **h))),
         (ValueError, "logits must be", lambda: mnb.mnb_softmax(x[0])),
@@ -500,6 +515,37 @@ def test_bindings_refuse(env):
     for kind, word, call in cases:
         with pytest.raises(kind, match=word):
             call()
+
+
+def test_threads_share_a_workspace(env):
+    """Calls of every kind that has a workspace, of four host threads on one stream with one workspace: the launches of each
+    stay together."""
+    from concurrent.futures import ThreadPoolExecutor
+    mnb, torch, dev = env
+    rng = np.random.default_rng(14)
+    D, pages, length = 64, 20, 1200
+    cache = mnb.MnbKv4Cache(torch.zeros(mnb.mnb_kv4_cache_bytes(pages, 64, 2, D, 32), dtype=torch.uint8, device=dev).view(pages, 2, -1),
+                            64, D, 32)
+    k, q = (torch.randn(n, 2, D, device=dev).half() for n in (length, 2))
+    mnb.mnb_kv4_append(cache, k, k, torch.arange(length, device=dev))
+    start, lens, table = _up(torch, dev, np.int32([0, 2]), np.int32([length]), np.arange(pages, dtype=np.int32)[None])
+    x, base, down, up, _, scales, adapter = _up(torch, dev, *_lora_inputs(rng, 1500, 64, 96, 16, 5, "f16"))
+    pool = mnb.MnbLoraPool(down, up, scales=scales)
+    logits = torch.randn(3, 40000, device=dev)
+    drafts = _up(torch, dev, *_draft_case(rng, 9, 9000, 3, False))
+    forms = [lambda w: mnb.mnb_kv4_attention(q, cache, start, lens, table, 0.1, workspace=w),
+             lambda w: mnb.mnb_lora(x, pool, adapter, base=base, workspace=w),
+             lambda w: mnb.mnb_softmax(logits, workspace=w),
+             lambda w: mnb.mnb_verify(*drafts, workspace=w)[0]]
+    wants = [f(None) for f in forms]
+    torch.cuda.synchronize()
+    shared = torch.empty(1 << 24, dtype=torch.uint8, device=dev)
+    for workspace in (None, shared):
+        with ThreadPoolExecutor(4) as threads:
+            outs = list(threads.map(lambda f: [f(workspace) for _ in range(100)], forms))
+        for got, want in zip(outs, wants):
+            assert all(torch.equal(o, want) for o in got)
+    mnb.mnb_check_device_status()
 
 
 def test_no_rows(env):
