@@ -72,14 +72,16 @@ struct Chunk {
 };
 
 // The exponent (x - m) c as one operation, x c - rc, where rc = m c is moderate: rc's rounding is the same for all and goes into
-// `factor`. Else as two (infinite logits, large ones, temperatures near 0).
+// `factor` = 2^(rc - m c), by its series (ex2's own error, 2^-22, would be every probability's). Else as two (infinite logits, large
+// ones, temperatures near 0).
 struct Base {
   float m, c, rc, factor;
   bool plain;
   __device__ __forceinline__ Base(float m_, float c_) : m(some(m_)), c(c_) {
     rc = m * c;
-    plain = fabsf(rc) < 65536.0f;  // its rounding moves the exponent by 2^-8 at most
-    factor = plain ? ex2(-fmaf(m, c, -rc)) : 1.0f;
+    plain = fabsf(rc) < 65536.0f;  // its rounding moves the exponent by 2^-9 at most: the series' third term is below 2^-28
+    const float y = plain ? -0.693147181f * fmaf(m, c, -rc) : 0.0f;
+    factor = fmaf(y, fmaf(y, 0.5f, 1.0f), 1.0f);
   }
   template <bool kPlain>
   __device__ __forceinline__ float exponent(float x) const {
@@ -105,7 +107,7 @@ struct SoftRow {
   __device__ __forceinline__ SoftRow(const Softmax& a_, int r) : a(a_), in_at((int64_t)r * a_.stride), out_at((int64_t)r * a_.V) {
     skew = (int)(in_at % 8);
     chunks = (a.V + skew + 7) / 8;
-    temp = a.temperature ? a.temperature[r] : 1.0f;
+    temp = a.temperature ? __ldcg(a.temperature + r) : 1.0f;
     c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
   }
   // Whether chunks i0 .. i1 - 1 lie within the row, and its probabilities at 32 bytes.
@@ -453,11 +455,11 @@ struct DrawRow {
   __device__ __forceinline__ void load4(const float* row, int c, bool whole, float (&v)[4]) const {
     const int j = 4 * c - skew;
     if (whole && j >= 0 && j + 4 <= V) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row + j));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(row + j));
       v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < V ? __ldg(row + j + i) : 0.0f;
+      for (int i = 0; i < 4; ++i) v[i] = j + i >= 0 && j + i < V ? __ldcg(row + j + i) : 0.0f;
     }
   }
   // p and q of chunk c, zeros when not `live`. kAny: any row; kPair: the chunk lies within the row, and q alike; kAlone: the same,
@@ -469,10 +471,10 @@ struct DrawRow {
     for (int i = 0; i < 4; ++i) pv[i] = qv[i] = 0.0f;
     if (!live) return;
     if constexpr (kMode != kAny) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p + 4 * c - skew));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 4 * c - skew));
       pv[0] = x.x, pv[1] = x.y, pv[2] = x.z, pv[3] = x.w;
       if constexpr (kMode == kPair) {
-        const float4 y = __ldg(reinterpret_cast<const float4*>(q + 4 * c - skew));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(q + 4 * c - skew));
         qv[0] = y.x, qv[1] = y.y, qv[2] = y.z, qv[3] = y.w;
       }
     } else {
@@ -533,7 +535,7 @@ __device__ __forceinline__ uint64_t run_sum(const DrawRow& row, int c0, int c1) 
   if (row.not_this >= 0 && row.not_this < row.V && c >= c0 && c < c1) {
     DrawRow all = row;
     all.without_draft();
-    sum -= all.weight64(c, i, __ldg(row.p + row.not_this), 0.0f);
+    sum -= all.weight64(c, i, __ldcg(row.p + row.not_this), 0.0f);
   }
   return sum;
 }

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
             } else {
               const T* p = static_cast<const T*>(a.base) + (int64_t)rows[r] * a.base_stride + n;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = a.base && i < width ? (float)p[i] : 0.0f;
+              for (int i = 0; i < 8; ++i) y[i] = a.base && i < width ? (float)__ldcg(p + i) : 0.0f;
             }
             if (rank > 0) {
               const float f = factors[r];

@@ -27,7 +27,7 @@ static __device__ __noinline__ void copy_some(uint32_t dst, const void* src, int
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (2 * i < bytes) w[i / 2] |= (uint32_t) static_cast<const unsigned short*>(src)[i] << (16 * (i & 1));
+    if (2 * i < bytes) w[i / 2] |= (uint32_t)__ldcg(static_cast<const unsigned short*>(src) + i) << (16 * (i & 1));
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

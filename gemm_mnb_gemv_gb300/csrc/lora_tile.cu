@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int from = __shfl_sync(kFull, row, i0 + i);
                   v[i] = 0;
                   if (a.base && from >= 0 && lane < width)
-                    v[i] = static_cast<const unsigned short*>(a.base)[(int64_t)from * a.base_stride + n + lane];
+                    v[i] = __ldcg(static_cast<const unsigned short*>(a.base) + (int64_t)from * a.base_stride + n + lane);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
