@@ -34,6 +34,19 @@ __device__ __forceinline__ Split split(float x, float y) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// Of two rows; out of line, as the ordinary case pays for the code (2 %).
+template <int kWords>
+struct LooseRows {
+  uint32_t y[2][kWords];
+};
+template <typename T, int kWords>
+__device__ __noinline__ LooseRows<kWords> loose_rows(const T* base, int64_t at0, int64_t at1, int64_t end, int width) {
+  LooseRows<kWords> r;
+  loose_row(base, at0, end, width, r.y[0]);
+  loose_row(base, at1, end, width, r.y[1]);
+  return r;
+}
+
 // RB: ranks in eights; WM: row tiles of 16.
 template <int RB, int WM, bool F32>
 struct Geo {
@@ -362,13 +375,20 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     // Column c of the product's 8-column tile j is output column 8 (c / 2) + 2 j + c % 2 of the warp's 32: a lane then has
     // 8 consecutive ones, of four tiles.
     for (; q < stages; ++q) {
+      constexpr int kWords = F32 ? 8 : 4;
+      const int r0 = wm * 16 + g;
+      const int n_warp = (b0 + (q - down_stages) * WN + wn) * 32, n = n_warp + 8 * t, width = min(8, min(a.N, b1 * 32) - n);
+      LooseRows<kWords> base;  // as they lie
+      auto& y = base.y;
       copy_wait<L::kAhead - 1>();
       __syncthreads();
       if (!L::kFew) issue(q + L::kAhead);
       if (live) {
         const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
-        const int r0 = wm * 16 + g;
-        const int n = (b0 + (q - down_stages) * WN + wn) * 32 + 8 * t, width = min(8, min(a.N, b1 * 32) - n);
+        if (!base_vec) {
+          auto at = [&](int r) { return a.base && r < n_rows ? rows[r] * a.base_stride + n : -1; };
+          base = loose_rows<T, kWords>(static_cast<const T*>(a.base), at(r0), at(r0 + 8), base_end(a), width);
+        }
         float d[4][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -420,51 +440,56 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
             }
           }
         }
+        // places of this lane's 8 columns of row r in the stage, and of the warp's column `col`
+        auto own = [&](int r, int i) { return act + r * L::kRow + place<F32>(r, F32 ? 2 * (4 * wn + t) + i : 4 * wn + t); };
+        auto col_at = [&](int r, int col) {
+          return act + r * L::kRow + place<F32>(r, F32 ? 8 * wn + col / 4 : 4 * wn + col / 8) + (F32 ? col % 4 * 4 : col % 8 * 2);
+        };
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = r0 + 8 * h;
           if (r < n_rows && width > 0) {
-            float y[8];
             if (base_vec) {
-              if constexpr (F32) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint4 v = lds128_a(act + r * L::kRow + place<true>(r, 2 * (4 * wn + t) + i));
-                  y[4 * i] = __uint_as_float(v.x), y[4 * i + 1] = __uint_as_float(v.y);
-                  y[4 * i + 2] = __uint_as_float(v.z), y[4 * i + 3] = __uint_as_float(v.w);
-                }
-              } else {
-                const uint4 v = lds128_a(act + r * L::kRow + place<false>(r, 4 * wn + t));
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float2 f = half2_floats(u[i]);
-                  y[2 * i] = f.x, y[2 * i + 1] = f.y;
-                }
+              for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = lds128_a(own(r, i));
+                y[h][4 * i] = v.x, y[h][4 * i + 1] = v.y, y[h][4 * i + 2] = v.z, y[h][4 * i + 3] = v.w;
               }
-            } else {
-              const T* p = static_cast<const T*>(a.base) + (int64_t)rows[r] * a.base_stride + n;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = a.base && i < width ? (float)__ldcg(p + i) : 0.0f;
             }
             if (rank > 0) {
               const float f = factors[r];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = fmaf(d[i / 2][2 * h + i % 2], f, y[i]);
-            }
-            T* p = static_cast<T*>(a.out) + (int64_t)rows[r] * a.out_stride + n;
-            if (out_vec && width == 8) {
-              if constexpr (F32) {
-                *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<float4*>(p + 4) = make_float4(y[4], y[5], y[6], y[7]);
-              } else {
-                *reinterpret_cast<uint4*>(p) = make_uint4(half2_bits(y[0], y[1]), half2_bits(y[2], y[3]), half2_bits(y[4], y[5]),
-                                                          half2_bits(y[6], y[7]));
+              for (int i = 0; i < 4; ++i) {
+                const float d0 = d[i][2 * h], d1 = d[i][2 * h + 1];
+                if constexpr (F32) {
+                  y[h][2 * i] = __float_as_uint(fmaf(d0, f, __uint_as_float(y[h][2 * i])));
+                  y[h][2 * i + 1] = __float_as_uint(fmaf(d1, f, __uint_as_float(y[h][2 * i + 1])));
+                } else {
+                  const float2 v = half2_floats(y[h][i]);
+                  y[h][i] = half2_bits(fmaf(d0, f, v.x), fmaf(d1, f, v.y));
+                }
               }
+            }
+            if (out_vec && width == 8) {
+              uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)rows[r] * a.out_stride + n);
+#pragma unroll
+              for (int i = 0; i < kWords / 4; ++i) p[i] = make_uint4(y[h][4 * i], y[h][4 * i + 1], y[h][4 * i + 2], y[h][4 * i + 3]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i < width) p[i] = (T)y[i];
+              for (int i = 0; i < kWords / 4; ++i) store16(own(r, i), y[h][4 * i], y[h][4 * i + 1], y[h][4 * i + 2], y[h][4 * i + 3]);
+            }
+          }
+        }
+        // what a lane can't store as it has it goes out a row after the other
+        const int whole = out_vec ? min(a.N, b1 * 32) / 8 * 8 : 0, col = n_warp + lane;
+        if (n_warp + 32 > whole) {
+          __syncwarp();
+          if (col >= whole && col < min(a.N, b1 * 32)) {
+#pragma unroll 4
+            for (int i = wm * 16; i < min(wm * 16 + 16, n_rows); ++i) {
+              T* p = static_cast<T*>(a.out) + (int64_t)rows[i] * a.out_stride + col;
+              if constexpr (F32) *p = __uint_as_float(lds_u32_a(col_at(i, lane)));
+              else *reinterpret_cast<unsigned short*>(p) = (unsigned short)lds_u16_a(col_at(i, lane));
             }
           }
         }

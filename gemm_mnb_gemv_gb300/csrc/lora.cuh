@@ -22,19 +22,63 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void store_zeros(uint32_t dst) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0u) : "memory");
 }
+__device__ __forceinline__ void store16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 // The first `bytes` (2..14, even) of 16 and zeros, by this thread itself: what the ends of rows and ranks need.
 static __device__ __noinline__ void copy_some(uint32_t dst, const void* src, int bytes) {
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (2 * i < bytes) w[i / 2] |= (uint32_t)__ldcg(static_cast<const unsigned short*>(src) + i) << (16 * (i & 1));
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+  store16(dst, w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// Elements at .. at + width - 1 of a base of `end` elements whose rows lie anywhere (at < 0: zeros): their 16-byte chunks, brought into
+// place. kWords * 4 bytes are worked on; what lies behind `width` is anything. (Element by element, and stored so too, 4096 rows of 4095
+// took 193 us instead of 78, 900 rows 34 instead of 18; rows at 16 bytes 29 and 14.)
+template <typename T, int kWords>
+__device__ __forceinline__ void loose_row(const T* base, int64_t at, int64_t end, int width, uint32_t (&y)[kWords]) {
+  constexpr int kVec = 16 / sizeof(T), kChunks = kWords / 4 + 1;
+  uint32_t w[4 * kChunks];
+#pragma unroll
+  for (int i = 0; i < 4 * kChunks; ++i) w[i] = 0;
+  int skew = 0;
+  if (at >= 0) {
+    skew = (int)(at % kVec);
+    const T* p = base + at - skew;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      if (kVec * c < skew + width) {
+        if (at - skew + kVec * (c + 1) <= end) {
+          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p) + c);
+          w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+        } else {  // behind the last row there may be nothing
+#pragma unroll
+          for (int i = 0; i < kVec; ++i)
+            if (at - skew + kVec * c + i < end) {
+              if constexpr (sizeof(T) == 4) w[4 * c + i] = __ldcg(reinterpret_cast<const uint32_t*>(p) + kVec * c + i);
+              else w[4 * c + i / 2] |= (uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p) + kVec * c + i) << (16 * (i & 1));
+            }
+        }
+      }
+    }
+  }
+  const int words = skew * (int)sizeof(T) / 4;
+#pragma unroll
+  for (int i = 0; i < kWords + 2; ++i) w[i] = words & 2 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < kWords + 1; ++i) w[i] = words & 1 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) y[i] = sizeof(T) == 2 && (skew & 1) ? __byte_perm(w[i], w[i + 1], 0x5432) : w[i];
+}
+
+__device__ __forceinline__ int64_t base_end(const Lora& a) { return (int64_t)(a.M - 1) * a.base_stride + a.N; }
 
 // The rows of one adapter (negative: none) in a tile.
 struct Item {

@@ -500,28 +500,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tile = ring + slot * L::kSlot + col / 64 * (kRows * 128);
             const int ch0 = col % 64 / 8;  // first 16-byte chunk of the 32 columns
             uint32_t y[16];
-            if (!base_vec) {  // rows that lie anywhere, or zeros: put where the copies would have
-#pragma unroll 1
-              for (int i0 = 0; i0 < 32; i0 += 16) {
-                unsigned short v[16];
+            if (base_vec) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int from = __shfl_sync(kFull, row, i0 + i);
-                  v[i] = 0;
-                  if (a.base && from >= 0 && lane < width)
-                    v[i] = __ldcg(static_cast<const unsigned short*>(a.base) + (int64_t)from * a.base_stride + n + lane);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + swizzled(quarter * 32 + i0 + i, ch0 + lane / 8) + (lane & 7) * 2), "h"(v[i])
-                               : "memory");
+              for (int c = 0; c < 4; ++c) {
+                const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
+                y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
               }
-              __syncwarp();
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
-              y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
+            } else {
+              loose_row(static_cast<const __half*>(a.base), a.base && row >= 0 ? row * a.base_stride + n : -1, base_end(a), width, y);
             }
             if (w.rank > 0) {
               float d[32];
@@ -563,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // where results or bases went through these bytes, a tensor copy may write them next
-          if (!base_vec || !out_vec || n1 - n0 < (q - w.down_stages + 1) * kSpan) tc::fence_proxy_async_smem();
+          // where results went through these bytes, a tensor copy may write them next
+          if (!out_vec || n1 - n0 < (q - w.down_stages + 1) * kSpan) tc::fence_proxy_async_smem();
         }
         tc::fence_before_sync();
         __syncwarp();
