@@ -309,24 +309,28 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       const int r0 = wm * 16 + g;
       if (live && wn > 0) {
 #pragma unroll
-        for (int j = 0; j < RB; ++j) {
-          *reinterpret_cast<float2*>(at(wn - 1, r0, j * 8 + 2 * t)) = make_float2(acc[j][0], acc[j][1]);
-          *reinterpret_cast<float2*>(at(wn - 1, r0 + 8, j * 8 + 2 * t)) = make_float2(acc[j][2], acc[j][3]);
-        }
+        for (int h = 0; h < 2; ++h)
+          if (wm * 16 + 8 * h < n_rows) {
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+              *reinterpret_cast<float2*>(at(wn - 1, r0 + 8 * h, j * 8 + 2 * t)) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+          }
       }
       __syncthreads();
       if (live && wn == 0) {
 #pragma unroll
-        for (int j = 0; j < RB; ++j)
+        for (int h = 0; h < 2; ++h)
+          if (wm * 16 + 8 * h < n_rows) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2 v = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+            for (int j = 0; j < RB; ++j) {
+              float2 v = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
 #pragma unroll
-            for (int w = 0; w < WN - 1; ++w) {
-              const float2 o = *reinterpret_cast<float2*>(at(w, r0 + 8 * h, j * 8 + 2 * t));
-              v.x += o.x, v.y += o.y;
+              for (int w = 0; w < WN - 1; ++w) {
+                const float2 o = *reinterpret_cast<float2*>(at(w, r0 + 8 * h, j * 8 + 2 * t));
+                v.x += o.x, v.y += o.y;
+              }
+              *reinterpret_cast<float2*>(at(0, r0 + 8 * h, j * 8 + 2 * t)) = v;
             }
-            *reinterpret_cast<float2*>(at(0, r0 + 8 * h, j * 8 + 2 * t)) = v;
           }
       }
       // ---- over the cluster; every CTA gets all of s. RP / 4 neighbouring lanes have a row. Few rows: each CTA reads all of them; many: it
