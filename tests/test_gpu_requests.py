@@ -576,3 +576,9 @@ def test_workspaces_of_other_streams_are_held(env):
     side.synchronize()
     np.testing.assert_array_equal(tokens.cpu().numpy(), want)
     np.testing.assert_array_equal(accepted.cpu().numpy(), want_n)
+
+
+def test_example_runs(env):
+    from examples import verify_step
+    accepted, _, _ = verify_step.run(batch=5, drafts=3, steps=3, vocab=1003 * 32, hidden=256, adapters=3, rank=8)
+    assert 0 <= accepted <= 3
