@@ -244,7 +244,9 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
       if (live) {
         const uint32_t act = ring + q % S * L::kStage, weight = act + L::kAct;
         const int r0 = wm * 16 + g;
-        // Rows beyond the last hold what was there: they do not reach the others' sums.
+        // Rows beyond the last and ranks beyond the item's hold what was there: they do not reach the others' sums. Four eights of the rank
+        // at a time: their loads and products do not wait for each other.
+        constexpr int kGroup = RB < 4 ? RB : 4;
         if constexpr (F32) {
           float x[2][8];
 #pragma unroll
@@ -272,16 +274,24 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
             for (int i = 0; i < 4; ++i) v[h][i] = split(x[h][2 * i] * f, x[h][2 * i + 1] * f);
           }
 #pragma unroll
-          for (int j = 0; j < RB; ++j) {
-            if (j * 8 < rank) {
-              const uint4 w = lds128_a(weight + (j * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
-              float d[4];
-              mma16816_zero(d, v[0][0].lo, v[1][0].lo, v[0][1].lo, v[1][1].lo, w.x, w.y);
-              mma16816(d, v[0][2].lo, v[1][2].lo, v[0][3].lo, v[1][3].lo, w.z, w.w);
-              mma16816(d, v[0][0].hi, v[1][0].hi, v[0][1].hi, v[1][1].hi, w.x, w.y);
-              mma16816(d, v[0][2].hi, v[1][2].hi, v[0][3].hi, v[1][3].hi, w.z, w.w);
+          for (int j0 = 0; j0 < RB; j0 += kGroup) {
+            if (j0 * 8 < rank) {
+              uint4 w[kGroup];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(d[i], back[i / 2], acc[j][i]);
+              for (int j = 0; j < kGroup; ++j) w[j] = lds128_a(weight + ((j0 + j) * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
+              float d[kGroup][4];
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816_zero(d[j], v[0][0].lo, v[1][0].lo, v[0][1].lo, v[1][1].lo, w[j].x, w[j].y);
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816(d[j], v[0][2].lo, v[1][2].lo, v[0][3].lo, v[1][3].lo, w[j].z, w[j].w);
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816(d[j], v[0][0].hi, v[1][0].hi, v[0][1].hi, v[1][1].hi, w[j].x, w[j].y);
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816(d[j], v[0][2].hi, v[1][2].hi, v[0][3].hi, v[1][3].hi, w[j].z, w[j].w);
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j0 + j][i] = fmaf(d[j][i], back[i / 2], acc[j0 + j][i]);
             }
           }
         } else {
@@ -289,11 +299,15 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
 #pragma unroll
           for (int h = 0; h < 2; ++h) x[h] = lds128_a(act + (r0 + 8 * h) * L::kRow + place<false>(g, 4 * wn + t));
 #pragma unroll
-          for (int j = 0; j < RB; ++j) {
-            if (j * 8 < rank) {
-              const uint4 w = lds128_a(weight + (j * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
-              mma16816(acc[j], x[0].x, x[1].x, x[0].y, x[1].y, w.x, w.y);
-              mma16816(acc[j], x[0].z, x[1].z, x[0].w, x[1].w, w.z, w.w);
+          for (int j0 = 0; j0 < RB; j0 += kGroup) {
+            if (j0 * 8 < rank) {
+              uint4 w[kGroup];
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) w[j] = lds128_a(weight + ((j0 + j) * 8 + g) * L::kDownRow + place<false>(g, 4 * wn + t));
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816(acc[j0 + j], x[0].x, x[1].x, x[0].y, x[1].y, w[j].x, w[j].y);
+#pragma unroll
+              for (int j = 0; j < kGroup; ++j) mma16816(acc[j0 + j], x[0].z, x[1].z, x[0].w, x[1].w, w[j].z, w[j].w);
             }
           }
         }
