@@ -1,9 +1,11 @@
 // From logits to verified tokens: probabilities at each row's temperature, and the verification of drafted tokens from
 // given random numbers.  Rows that one CTA would be long at are cut into segments: a first launch takes every segment's
-// numbers, a second one, which depends on it, joins them.  (A cluster for each row in one launch was slower beyond a few rows: 16 CTAs that have to
-// start and meet together; 320 rows of 128256 took 67 us at its best size, one row the same.)
+// numbers, a second one, which depends on it, joins them; a few rows of probabilities have a cluster each and one launch. (For many
+// rows clusters are slower, 16 CTAs that have to start and meet together: 320 rows of 128256 took 67 us at their best size, in two
+// launches 50.)
 #include <float.h>
 
+#include "cluster.cuh"
 #include "mnb_device.cuh"
 #include "mnb_internal.h"
 
@@ -24,6 +26,7 @@ int row_parts(int rows, int chunks, int smallest, int largest) {
 constexpr int kBatch = 4;          // chunks of a thread in flight
 constexpr int kPartThreads = 256;  // of a row's part
 constexpr int kNone = 0x7fffffff;
+constexpr int kMostCluster = 16, kClusterThreads = 512;
 
 struct SoftPart {  // of a part: largest, sum of the exponentials relative to it, first place of the largest
   float m, s;
@@ -298,6 +301,46 @@ __global__ void __launch_bounds__(kThreads) softmax_row_kernel(const Softmax a) 
   else store_batch<F32, kThreads, false, false>(row, tid, end, v, base, inv);
 }
 
+// A few longer rows: a cluster of `cluster` CTAs has one, in registers.
+template <bool F32>
+__global__ void __launch_bounds__(kClusterThreads) softmax_cluster_kernel(const Softmax a, int cluster) {
+  __shared__ __align__(16) SoftPart parts[kMostCluster];
+  cluster_arrive();
+  pdl_launch_dependents();
+  pdl_wait();
+  const int r = blockIdx.x / cluster, part = cluster_ctarank(), tid = threadIdx.x, lane = tid % 32;
+  const SoftRow<F32> row(a, r);
+  const int i0 = (int)((int64_t)row.chunks * part / cluster), i1 = (int)((int64_t)row.chunks * (part + 1) / cluster);
+  Chunk<F32> v[kBatch];
+  const bool whole = row.whole(i0, i1);
+  if (whole) load_batch<F32, kClusterThreads, true>(row, i0 + tid, i1, v);
+  else load_batch<F32, kClusterThreads, false>(row, i0 + tid, i1, v);
+  SoftPart all = {-INFINITY, 0.0f, kNone, 0};
+  take<F32, kClusterThreads>(row, v, i0 + tid, all);
+  all = cta_join<kClusterThreads>(all, row.temp, row.c);
+  cluster_wait();  // the others have started
+  if (tid < cluster) {
+    const uint32_t to = cluster_map(smem_u32(&parts[part]), tid);
+    cluster_st_u64(to, __float_as_uint(all.m), __float_as_uint(all.s));
+    cluster_st_u64(to + 8, (uint32_t)all.at, 0u);
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  all = {-INFINITY, 0.0f, kNone, 0};
+  if (lane < cluster) all = parts[lane];
+  all = warp_join(all, row.c);
+  if (row.temp == 0.0f) {
+    for (int i = i0 + tid; i < i1; i += kClusterThreads) row.template one_hot<false>(i, all);
+    return;
+  }
+  const Base base(all.m, row.c);
+  const float inv = all.m == -INFINITY ? 0.0f : base.factor / all.s;
+  if (whole && base.plain) store_batch<F32, kClusterThreads, true, true>(row, i0 + tid, i1, v, base, inv);
+  else if (base.plain) store_batch<F32, kClusterThreads, false, true>(row, i0 + tid, i1, v, base, inv);
+  else store_batch<F32, kClusterThreads, false, false>(row, i0 + tid, i1, v, base, inv);
+}
+
 // Longer rows: a CTA has a part, the same one in both launches.
 template <bool F32, bool kWhole>
 __device__ __forceinline__ SoftPart part_of(const SoftRow<F32>& row, int i0, int i1) {
@@ -371,9 +414,22 @@ __global__ void __launch_bounds__(kPartThreads) softmax_join_kernel(const Softma
   }
 }
 
-// Parts of a row, 0: one CTA has a whole one.
+// CTAs of a cluster that has a row, 0: no clusters. One launch saves 3 us of host time, and a few rows GPU time too; more clusters than the
+// GPU starts at once do not. fp16, 128256 logits a row, us with clusters / in two launches: 1 row 4.8 / 4.9, 8 rows 5.5 / 7.0, 32 rows 7.8 / 8.2,
+// 40 rows 10.2 / 9.8. Of 16 CTAs instead of 8: 4 rows 5.0 / 5.4, 8 rows 6.0 / 5.6 (262000 logits: 7.0 / 7.8 in two launches).
+int soft_cluster(int rows, int V) {
+  const int chunks = (V + 14) / 8;
+  auto fits = [&](int cluster) { return chunks <= cluster * kClusterThreads * kBatch; };
+  if (fits(1)) return 0;
+  if (rows <= 4 && fits(16)) return 16;
+  if (rows <= 32 && fits(8)) return 8;
+  return rows <= 8 && fits(16) ? 16 : 0;
+}
+
+// Parts of a row, 0: one CTA or one cluster has a whole one.
 int soft_parts(int rows, int V) {
   const int chunks = (V + 14) / 8;
+  if (soft_cluster(rows, V)) return 0;
   return chunks <= 512 * kBatch ? 0 : row_parts(rows, chunks, 256, 2048);
 }
 
@@ -678,6 +734,14 @@ size_t verify_workspace_bytes(int batch, int V) { return (size_t)batch * verify_
 cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a) {
   ctx.variant = a.f32 ? "softmax_f32" : "softmax_f16";
   const int parts = soft_parts(a.rows, a.V);
+  if (const int cluster = soft_cluster(a.rows, a.V)) {
+    auto go = [&](auto kern, std::atomic<uint64_t>& wide) {
+      const cudaError_t e = cluster > 8 ? allow_wide_clusters(kern, ctx.device, wide) : cudaSuccess;
+      return e != cudaSuccess ? e : launch_clusters(ctx, kern, cluster, dim3((unsigned)(a.rows * cluster)), dim3(kClusterThreads), 0, a, cluster);
+    };
+    static std::atomic<uint64_t> wide[2] = {};
+    return a.f32 ? go(softmax_cluster_kernel<true>, wide[1]) : go(softmax_cluster_kernel<false>, wide[0]);
+  }
   if (parts == 0) {
     const bool few = (a.V + 14) / 8 <= 128 * kBatch;
     auto go = [&](auto kern, int threads) { return launch_kernel(ctx, kern, dim3(a.rows), dim3(threads), 0, a); };

@@ -98,8 +98,8 @@ def test_lora_refusals(lib, change, expect, word):
     (dict(stride=9), 1, "stride"),
     (dict(temperature=4), 3, "temperature"),
     (dict(out=None), 1, "out"),
-    (dict(V=16378, stride=16378, ws_bytes=2 * 9 * 16 - 1, workspace=64), 1, "workspace"),
-    (dict(V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
+    (dict(rows=33, V=16378, stride=16378, ws_bytes=33 * 9 * 16 - 1, workspace=64), 1, "workspace"),
+    (dict(rows=33, V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
     (dict(rows=1 << 20, V=1 << 23, stride=1 << 23, ws_bytes=1 << 50, workspace=64), 2, "more than"),
 ])
 def test_softmax_refusals(lib, change, expect, word):
@@ -151,10 +151,10 @@ def test_lora_workspace_bytes(lib):
 
 def test_draft_workspace_bytes(lib):
     """16 and 64 bytes for each part of a row; a part has 256 to 2048 chunks of 8 elements, or
-    512 to 4096 of 4, and the rows have 608 where possible."""
+    512 to 4096 of 4, and the rows have 608 where possible; few rows of probabilities need none."""
     soft, ver = lib.mnb_softmax_workspace_bytes, lib.mnb_verify_workspace_bytes
-    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (3, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
-        0, 0, 0, 3 * 9 * 16, 320 * 8 * 16, 0]
+    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (32, 16378), (33, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 0, 0, 33 * 9 * 16, 320 * 8 * 16, 0]
     assert [ver(*a) for a in [(0, 9), (3, 0), (3, 1), (3, 4096), (64, 128256), (1, (1 << 24) + 1)]] == [
         0, 0, 3 * 64, 3 * 3 * 64, 64 * 9 * 64, 0]
 
