@@ -596,14 +596,9 @@ __device__ __forceinline__ uint64_t run_sum(const DrawRow& row, int c0, int c1) 
   return sum;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verify a, int parts, int run, uint32_t* status) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, b = blockIdx.x / parts, part = blockIdx.x % parts;
-  pdl_launch_dependents();
-  pdl_wait();
-  int s0, n;
-  sequence(a, b, s0, n);
-  // ---- the first rejected token ----
-  int accepted = n;
+// How many of a sequence's tokens are accepted; a warp each finds it by itself.
+__device__ __forceinline__ int count_accepted(const Verify& a, int b, int s0, int n, bool report, uint32_t* status) {
+  const int lane = threadIdx.x % 32;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
     bool bad = false;
@@ -615,16 +610,23 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verif
         const float pt = __saturatef(a.target[(int64_t)(s0 + b + i) * a.target_stride + tok]);
         const float qt = a.draft ? __saturatef(a.draft[(int64_t)(s0 + i) * a.draft_stride + tok]) : 1.0f;
         bad = !((double)u * (double)qt < (double)pt);
-      } else if (part == 0 && warp == 0) {
+      } else if (report) {
         report_status(status, kStatusBadIndex);
       }
     }
     const uint32_t vote = __ballot_sync(kFull, bad);
-    if (vote) {
-      accepted = i0 + __ffs(vote) - 1;
-      break;
-    }
+    if (vote) return i0 + __ffs(vote) - 1;
   }
+  return n;
+}
+
+__global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verify a, int parts, int run, uint32_t* status) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, b = blockIdx.x / parts, part = blockIdx.x % parts;
+  pdl_launch_dependents();
+  pdl_wait();
+  int s0, n;
+  sequence(a, b, s0, n);
+  const int accepted = count_accepted(a, b, s0, n, part == 0 && warp == 0, status);
   // ---- the sum of this warp's run ----
   const DrawRow row(a, b, s0, n, accepted);
   const int c0 = (part * kVerifyWarps + warp) * run;
@@ -633,17 +635,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verif
   if (part == 0 && threadIdx.x == 0) a.accepted[b] = accepted;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verify a, int parts, int run) {
+// The drawn element, from the sums of `runs` runs, and the sequence's tokens. `cta` of the CTAs that call this has the runs `cta` *
+// kVerifyWarps .. when `share` is set (all of them do the same up to there), else the only one has all.
+__device__ __forceinline__ void draw(const Verify& a, int b, int s0, int n, int accepted, const uint64_t* sums, int runs, int run, int cta,
+                                     bool share, float u) {
   __shared__ uint64_t of_step[kMostSteps];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = blockIdx.x;
-  pdl_launch_dependents();
-  pdl_wait();
-  int s0, n;
-  sequence(a, b, s0, n);
-  const int accepted = min(max(a.accepted[b], 0), n);  // the first launch's: in range unless the caller's buffers overlap
-  const float u = a.u_next[b];
-  const int runs = parts * kVerifyWarps, per = (runs + 31) / 32;
-  const uint64_t* sums = static_cast<const uint64_t*>(a.workspace) + (int64_t)b * runs;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, per = (runs + 31) / 32;
   int32_t* out = a.out + s0 + b;
   // ---- the row's total, then the run that the drawn one is in: a lane has `per` neighbouring ones. Every warp finds it by itself ----
   uint64_t mine = 0;
@@ -667,7 +664,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
         head = shfl_u64(to, 31);
       }
     }
-  } else if (row.rejected) {  // nothing left of p - q: drawn from p, whose sums are taken here, by every warp alike
+  } else if (row.rejected) {  // nothing left of p - q: drawn from p, whose sums are taken here, by every warp of one CTA alike
+    if (cta != 0) return;
+    share = false;
     row.without_draft();
     for (int i = 0; i < runs; ++i) all += run_sum(row, i * run, min((i + 1) * run, row.chunks));
     limit = scaled(all, u);
@@ -677,9 +676,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
       else head += x;
     }
   }
-  for (int i = tid; i <= n; i += kVerifyThreads)
-    if (i != accepted || found < 0) out[i] = i < accepted ? a.tokens[s0 + i] : -1;
-  if (found < 0) return;
+  if (cta == 0)
+    for (int i = tid; i <= n; i += kVerifyThreads)
+      if (i != accepted || found < 0) out[i] = i < accepted ? a.tokens[s0 + i] : -1;
+  if (found < 0 || (share && found / kVerifyWarps != cta)) return;
   // ---- the element: the warps take the run's steps of 32 chunks in turn ----
   constexpr int kMine = kMostSteps / kVerifyWarps;
   const int steps = run / 32;
@@ -724,7 +724,55 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
   }
 }
 
-int verify_parts(int batch, int V) { return row_parts(batch, (V + 6) / 4, 512, kVerifyThreads * kMostSteps); }
+__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verify a, int parts, int run) {
+  const int b = blockIdx.x, runs = parts * kVerifyWarps;
+  pdl_launch_dependents();
+  pdl_wait();
+  int s0, n;
+  sequence(a, b, s0, n);
+  const int accepted = min(max(a.accepted[b], 0), n);  // the first launch's: in range unless the caller's buffers overlap
+  draw(a, b, s0, n, accepted, static_cast<const uint64_t*>(a.workspace) + (int64_t)b * runs, runs, run, 0, false, a.u_next[b]);
+}
+
+// Few sequences: a cluster of CTAs has one, whose sums they hand to each other.
+__global__ void __launch_bounds__(kVerifyThreads) verify_cluster_kernel(const Verify a, int cluster, int run, uint32_t* status) {
+  __shared__ __align__(16) uint64_t sums[kMostCluster * kVerifyWarps];
+  cluster_arrive();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, b = blockIdx.x / cluster, cta = cluster_ctarank();
+  pdl_launch_dependents();
+  pdl_wait();
+  int s0, n;
+  sequence(a, b, s0, n);
+  const float u = a.u_next[b];
+  const int accepted = count_accepted(a, b, s0, n, cta == 0 && warp == 0, status);
+  const DrawRow row(a, b, s0, n, accepted);
+  const int at = cta * kVerifyWarps + warp, c0 = at * run;
+  const uint64_t sum = run_sum(row, c0, min(c0 + run, row.chunks));
+  __syncwarp();
+  cluster_wait();  // the others have started
+  if (lane < cluster) cluster_st_u64(cluster_map(smem_u32(&sums[at]), lane), (uint32_t)sum, (uint32_t)(sum >> 32));
+  if (cta == 0 && threadIdx.x == 0) a.accepted[b] = accepted;
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  draw(a, b, s0, n, accepted, sums, cluster * kVerifyWarps, run, cta, true, u);
+}
+
+// CTAs of a cluster that has a sequence, 0: two launches. As many as give a warp a run of 64 chunks; fewer, with runs of up to 256, where
+// that is more than a CTA for each SM, and of up to 512 where it is more than 512 in all. us with clusters / in two launches, 4 drafted tokens a
+// sequence (a call takes 4 us less of host time besides): V 128256: 1 sequence 6.7 / 8.2, 16 9.2 / 9.6, 64 15.5 / 17.1, 100 24.9 / 23.4 (800 CTAs); V
+// 32003: 8 6.5 / 6.9, 100 10.5 / 12.3.
+int verify_cluster(int batch, int V) {
+  const int chunks = (V + 6) / 4;
+  int c = kMostCluster;
+  while (c > 1 && c * kVerifyWarps * 64 > chunks) c /= 2;
+  while (c > 1 && c * batch > 152 && run_chunks(chunks, c / 2) <= 256) c /= 2;
+  while (c > 1 && c * batch > 512 && run_chunks(chunks, c / 2) <= 32 * kMostSteps) c /= 2;
+  return run_chunks(chunks, c) <= 32 * kMostSteps && (int64_t)c * batch <= 512 ? c : 0;
+}
+int verify_parts(int batch, int V) {
+  return verify_cluster(batch, V) ? 0 : row_parts(batch, (V + 6) / 4, 512, kVerifyThreads * kMostSteps);
+}
 
 }  // namespace
 
@@ -762,6 +810,13 @@ cudaError_t launch_softmax(LaunchCtx& ctx, const Softmax& a) {
 
 cudaError_t launch_verify(LaunchCtx& ctx, const Verify& a) {
   ctx.variant = "verify";
+  if (const int cluster = verify_cluster(a.batch, a.V)) {
+    static std::atomic<uint64_t> wide{0};
+    const cudaError_t e = cluster > 8 ? allow_wide_clusters(verify_cluster_kernel, ctx.device, wide) : cudaSuccess;
+    return e != cudaSuccess ? e
+                            : launch_clusters(ctx, verify_cluster_kernel, cluster, dim3((unsigned)(a.batch * cluster)), dim3(kVerifyThreads), 0,
+                                              a, cluster, run_chunks((a.V + 6) / 4, cluster), ctx.status);
+  }
   const int parts = verify_parts(a.batch, a.V), run = run_chunks((a.V + 6) / 4, parts);
   cudaError_t e = launch_kernel(ctx, verify_part_kernel, dim3((unsigned)a.batch * parts), dim3(kVerifyThreads), 0, a, parts, run,
                                 ctx.status);

@@ -493,7 +493,7 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
  * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
  * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0) and rounded to whole numbers of 2^-60, in which weights and
  * sums are taken (a row adds up to less than 16). No output may overlap an input. A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
- * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes, under the rules of mnb_lora's; more than 2^42 elements in the batch's rows
+ * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes (0 for few sequences), under the rules of mnb_lora's; more than 2^42 elements in the batch's rows
  * give MNB_ERR_UNSUPPORTED. batch = 0 is valid and does nothing.
  */
 MNB_API size_t mnb_verify_workspace_bytes(int batch, int V);

@@ -329,7 +329,7 @@ def _draft_case(rng, B, V, top, lookup):
 
 @pytest.mark.parametrize("lookup", [False, True])
 @pytest.mark.parametrize("B,V,top", [(1, 1, 0), (1, 2, 1), (1, 1000, 4), (3, 33, 2), (2, 128256, 3), (20, 5003, 8), (300, 257, 5), (9, 1028, 40),
-                                     (700, 1026, 1)])
+                                     (700, 1026, 1), (3, 270001, 2), (70, 9001, 3), (40, 20001, 2), (520, 700, 1)])
 def test_verify(env, B, V, top, lookup):
     mnb, torch, dev = env
     case = _draft_case(np.random.default_rng(B + V), B, V, top, lookup)
@@ -339,7 +339,8 @@ def test_verify(env, B, V, top, lookup):
     np.testing.assert_array_equal(tokens.cpu().numpy(), want)
 
 
-def test_verify_borders(env):
+@pytest.mark.parametrize("apart,every", [(1, 1), (1, 3), (30, 16)])
+def test_verify_borders(env, apart, every):
     """Probabilities whose sums are exact, at random numbers on and next to every border."""
     mnb, torch, dev = env
     V = 300
@@ -347,10 +348,11 @@ def test_verify_borders(env):
     k = rng.integers(0, 9, V)
     k[[0, 1, 17, V - 1]] = 0
     k[100] += 1024 - k.sum()
-    p = (k / 1024).astype(np.float32)
+    p = np.zeros(V * apart, np.float32)
+    p[::apart] = k / 1024
     edges = np.unique(np.concatenate([[0], k.cumsum()]))[:-1]
     u = (edges / 1024).astype(np.float32)
-    v = np.concatenate([u, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(-1)), np.float32([1, 2, -1, np.nan, 1e-45, 1e-20])])
+    v = np.concatenate([u, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(-1)), np.float32([1, 2, -1, np.nan, 1e-45, 1e-20])])[::every]
     B = len(v)
     zero = np.zeros(0, np.float32)
     case = (np.tile(p, (B, 1)), None, zero.astype(np.int32), np.zeros(B + 1, np.int32), zero, v.astype(np.float32))
@@ -360,9 +362,9 @@ def test_verify_borders(env):
     assert (p[tokens.cpu().numpy()] > 0).all()  # nothing impossible is drawn
 
 
-def test_verify_odd_values(env):
+@pytest.mark.parametrize("V,times", [(400, 1), (400, 40), (9001, 1)])
+def test_verify_odd_values(env, V, times):
     mnb, torch, dev = env
-    V = 400
     rng = np.random.default_rng(4)
     target, draft, tokens, start, u, v = _draft_case(rng, 16, V, 2, False)
     start = np.arange(0, 33, 2).astype(np.int32)
@@ -378,7 +380,9 @@ def test_verify_odd_values(env):
     tokens[14], tokens[17] = V, -1                  # no such tokens
     target[24, 7], target[24, 9] = np.inf, -3.0
     draft[20, tokens[20]] = 0                       # drawn though the draft gave it 0
-    case = (target, draft, tokens, start, u, v[:16] if len(v) >= 16 else rng.random(16).astype(np.float32))
+    many = lambda x: np.concatenate([x] * times)  # noqa: E731
+    start = np.arange(0, 32 * times + 1, 2).astype(np.int32)
+    case = (many(target), many(draft), many(tokens), start, many(u), many(v))
     mnb.mnb_check_device_status()
     got, accepted = mnb.mnb_verify(*_up(torch, dev, *case))
     want, want_n = orc.verify(*case)
@@ -533,7 +537,7 @@ def test_threads_share_a_workspace(env):
     x, base, down, up, _, scales, adapter = _up(torch, dev, *_lora_inputs(rng, 1500, 64, 96, 16, 5, "f16"))
     pool = mnb.MnbLoraPool(down, up, scales=scales)
     logits = torch.randn(40, 40000, device=dev)
-    drafts = _up(torch, dev, *_draft_case(rng, 9, 9000, 3, False))
+    drafts = _up(torch, dev, *_draft_case(rng, 600, 2000, 1, True))
     forms = [lambda w: mnb.mnb_kv4_attention(q, cache, start, lens, table, 0.1, workspace=w),
              lambda w: mnb.mnb_lora(x, pool, adapter, base=base, workspace=w),
              lambda w: mnb.mnb_softmax(logits, workspace=w),
@@ -564,14 +568,14 @@ def test_no_rows(env):
 def test_workspaces_of_other_streams_are_held(env):
     """On a stream of their own, calls allocate their workspaces: no output of the call may get the same bytes."""
     mnb, torch, dev = env
-    case = _draft_case(np.random.default_rng(13), 40, 9000, 3, False)
+    case = _draft_case(np.random.default_rng(13), 600, 2000, 1, True)
     want, want_n = orc.verify(*case)
     args = _up(torch, dev, *case)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         for _ in range(4):
-            room = torch.empty(mnb.mnb_verify_workspace_bytes(40, 9000), dtype=torch.uint8, device=dev)
+            room = torch.empty(mnb.mnb_verify_workspace_bytes(600, 2000), dtype=torch.uint8, device=dev)
             del room  # what the next allocation of these bytes gets
             tokens, accepted = mnb.mnb_verify(*args)
     side.synchronize()

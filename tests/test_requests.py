@@ -128,8 +128,8 @@ def test_softmax_refusals(lib, change, expect, word):
     (dict(v=None), 1, "u_next"),
     (dict(tokens=None), 1, "tokens"),
     (dict(accepted=8), 3, "accepted"),
-    (dict(ws_bytes=2 * 64 - 1), 1, "workspace"),
-    (dict(workspace=None), 1, "workspace"),
+    (dict(batch=600, ws_bytes=600 * 64 - 1), 1, "workspace"),
+    (dict(batch=600, workspace=None), 1, "workspace"),
     (dict(batch=1 << 20, V=1 << 23, target_stride=1 << 23, draft_stride=1 << 23), 2, "more than"),
 ])
 def test_verify_refusals(lib, change, expect, word):
@@ -151,12 +151,12 @@ def test_lora_workspace_bytes(lib):
 
 def test_draft_workspace_bytes(lib):
     """16 and 64 bytes for each part of a row; a part has 256 to 2048 chunks of 8 elements, or
-    512 to 4096 of 4, and the rows have 608 where possible; few rows of probabilities need none."""
+    512 to 4096 of 4, and the rows have 608 where possible; few rows and few sequences need none."""
     soft, ver = lib.mnb_softmax_workspace_bytes, lib.mnb_verify_workspace_bytes
     assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (32, 16378), (33, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
         0, 0, 0, 0, 33 * 9 * 16, 320 * 8 * 16, 0]
-    assert [ver(*a) for a in [(0, 9), (3, 0), (3, 1), (3, 4096), (64, 128256), (1, (1 << 24) + 1)]] == [
-        0, 0, 3 * 64, 3 * 3 * 64, 64 * 9 * 64, 0]
+    assert [ver(*a) for a in [(0, 9), (3, 0), (512, 1), (513, 1), (513, 4096), (64, 128256), (65, 128256), (1, 262141), (1, 262142),
+                              (1, (1 << 24) + 1)]] == [0, 0, 0, 513 * 64, 513 * 64, 0, 65 * 9 * 64, 0, 129 * 64, 0]
 
 
 def test_no_rows_is_valid(lib):
