@@ -1,17 +1,22 @@
 // Low-rank adapters of many requests beside a shared product:
 //   out[m] = base[m] + scale[a] * up[a] (down[a] x[m]),  a = adapter[m].
 //
-// A cluster of CTAs takes the rows of one adapter among a tile of 16 or 64 consecutive rows, in one launch for both products:
+// A cluster of CTAs takes an item, the rows of one adapter in a tile, in one launch for both products:
 //   1. s = down x: the CTAs split K; partial sums meet in shared memory, over the warps and then over the cluster;
 //   2. out = base + up s: the CTAs split N, each with all of s.
-// One ring of asynchronous copies feeds both: a stage is 32 WN of K (x and down) or 32 WN columns of N (base and up), and
-// the first stages of the second product are on their way while the first one's sums are joined.
+// Tiles have 16 rows (decode and verify steps, and the items of up to 16 rows that the tcgen05 kernel leaves) or, for many rows in
+// fp32, 64. One ring of asynchronous copies feeds both products: a stage is 32 WN of K (x and down) or 32 WN columns of N (base
+// and up), and the first stages of the second product are on their way while the first one's sums are joined.
 // Rows are the M side of the warp's matrix instructions, ranks (then output columns) the N side; a lane takes 8 consecutive
 // elements of the inner index, which both operands number alike.
 // fp16 activations: s is rounded to fp16 after its row was scaled by a power of two to [2^13, 2^14), as the result is
 // rounded. fp32: s is held as two fp16 of that scale, and x as two of the scale of the 32 elements that a granule of K has of a row;
 // each is multiplied on its own and the granule's scale put back in fp32 (2^-22; two tf32 parts took twice the instructions at half
 // their rate).
+// Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 14.5 us, 2.7 of them
+// bytes at the copy rate: about 2150 instructions a warp at 7 cycles each, 12 warps an SM (registers allow 16). Weights straight from
+// memory to the products' registers, without the ring: 22 us (half of each line at a time, and spills); a ring for each warp,
+// without barriers: the same.  One row of rank 16: 5.9 us, the chain of launch, adapter, K, cluster, N.
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -34,7 +39,7 @@ __device__ __forceinline__ Split split(float x, float y) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// Of two rows; out of line, as the ordinary case pays for the code (2 %).
+// Of two rows; out of line: inlined, rows at 16 bytes paid 1 to 2 % for the code.
 template <int kWords>
 struct LooseRows {
   uint32_t y[2][kWords];
@@ -525,8 +530,8 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
 // Rows up to which each cluster finds its tile's adapters itself. Beyond, a launch of 4 us makes a list of all items first (132 rows
 // of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 9.2).
 constexpr int kFewRows = 256;
-// Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that much less often but
-// fill the GPU later. fp16, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 15.9 / 18.0 at 1000 rows, 22.5 / 18.2 at 1400; rank 64
+// Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
+// much less often but fill the GPU later. fp16, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 15.9 / 18.0 at 1000 rows, 22.5 / 18.2 at 1400; rank 64
 // 18.3 / 19.3 at 700 and 21.5 / 19.4 at 1000; rank 128 29.7 / 23.3 at 272 and 69 / 24 at 1000.
 int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
 

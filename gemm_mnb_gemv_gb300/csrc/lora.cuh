@@ -92,9 +92,12 @@ __device__ __forceinline__ int row_power(float top) {
   return top < INFINITY && top > 0.0f ? max(ex, -110) - 13 : 0;
 }
 
-// A call's items, with `rest` but the first of each tile: those with more than `few` rows from the front of `list`, the others from its back. One CTA; the order within the two parts hangs on its warps' pace, and nothing hangs on the order.
+// A call's items, with `rest` but the first of each tile: those with more than `few` rows from the front of `list`, the others from
+// its back. One CTA, a warp a tile: 4 us, 7 where a tile's rows have 63 adapters. The order within the two parts hangs on the warps' pace, and
+// nothing hangs on the order.
 template <int TM>
-__global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int rest, uint32_t* counts, Item* list, int capacity, uint32_t* status) {
+__global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int rest, uint32_t* counts, Item* list, int capacity,
+                                                    uint32_t* status) {
   constexpr int H = (TM + 31) / 32;
   __shared__ uint32_t count[2];
   pdl_wait();

@@ -453,8 +453,8 @@ typedef struct {
  * adapter that lie near each other share its loads). Beside a product of this section's kind, base is that product's Y.
  * x [M, K], base and out [M, N] are of `dtype` (MNB_F16 or MNB_F32), rows *_stride elements apart (views of one fused
  * product do); x_stride is a multiple of 16 bytes (else MNB_ERR_MISALIGNED), K of 16 elements. base may be out
- * (with the same stride; neither it nor x may overlap out otherwise) or NULL, which counts as zeros. adapter is int32 [M]: a negative one
- * leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
+ * (with the same stride; neither it nor x may overlap out otherwise) or NULL, which counts as zeros. adapter is int32 [M]: a
+ * negative one leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
  * Products and sums are fp32. MNB_F16: down . x is rounded to fp16 relative to the row's largest (2^-11), as the result is;
  * MNB_F32: x and down . x enter the products with 22 bits, relative
  * to the largest of 32 neighbours and of the row. A row of x with inf or NaN gives non-finite outputs in that row.
@@ -492,9 +492,10 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
  * u_accept fp32 [drafted], u_next fp32 [batch], in [0, 1) (others are held to it). tokens int32 [drafted + batch], laid out as
  * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
  * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0) and rounded to whole numbers of 2^-60, in which weights and
- * sums are taken (a row adds up to less than 16). No output may overlap an input. A drafted token outside 0..V-1 is rejected and sets the index bit of the device status word.
- * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes (0 for few sequences), under the rules of mnb_lora's; more than 2^42 elements in the batch's rows
- * give MNB_ERR_UNSUPPORTED. batch = 0 is valid and does nothing.
+ * sums are taken (a row adds up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the
+ * device status word. No output may overlap an input.
+ * `workspace` holds mnb_verify_workspace_bytes(batch, V) bytes (0 for few sequences), under the rules of mnb_lora's; more than
+ * 2^42 elements in the batch's rows give MNB_ERR_UNSUPPORTED. batch = 0 is valid and does nothing.
  */
 MNB_API size_t mnb_verify_workspace_bytes(int batch, int V);
 MNB_API mnb_status mnb_verify(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,
