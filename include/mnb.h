@@ -483,9 +483,9 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
 /*
  * Verification of drafted tokens from given random numbers (speculative sampling). Sequence b of `batch` has the drafted tokens
  * draft_start[b] .. draft_start[b+1]-1 of draft_tokens (int32 [drafted]; draft_start int32 [batch + 1], not decreasing,
- * from 0 to drafted; there may be none). target holds drafted + batch rows of V fp32 probabilities, rows target_stride
- * elements apart: token i of sequence b has row draft_start[b] + b + i, and one more row follows after the sequence's
- * last. draft holds `drafted` rows, those that the tokens were drawn from; NULL: each is 1 at its token.
+ * from 0 to drafted or, where a batch is padded, below it; there may be none). target holds drafted + batch rows of V fp32
+ * probabilities, rows target_stride elements apart: token i of sequence b has row draft_start[b] + b + i, and one more row
+ * follows after the sequence's last; what lies behind the last sequence is neither used nor written. draft holds `drafted` rows, those that the tokens were drawn from; NULL: each is 1 at its token.
  *   Token d_i is accepted while u_accept[.] * q_i(d_i) < p_i(d_i). The token after the last accepted one is the first j with
  *   sum_{k <= j} w_k > u_next[b] * sum_k w_k, w = max(p - q, 0) at the rejected token's rows, w = p of the last row
  *   when all are accepted. Where nothing is left of p - q it is drawn from p; where p is all 0, it is -1.

@@ -393,6 +393,21 @@ def test_verify_odd_values(env, V, times):
         mnb.mnb_check_device_status()
 
 
+@pytest.mark.parametrize("B", [5, 600])
+def test_verify_padded_batch(env, B):
+    """Room for more drafted tokens than the sequences have: what lies behind them is neither used nor written."""
+    mnb, torch, dev = env
+    target, draft, tokens, start, u, v = _draft_case(np.random.default_rng(15), B, 300, 3, False)
+    D, more = len(tokens), 11
+    case = (np.concatenate([target, np.full((more, 300), np.nan, np.float32)]), np.concatenate([draft, np.full((more, 300), np.nan, np.float32)]),
+            np.concatenate([tokens, np.full(more, 1 << 30, np.int32)]), start, np.concatenate([u, np.full(more, np.nan, np.float32)]), v)
+    out = torch.full((D + more + B,), -7, dtype=torch.int32, device=dev)
+    mnb.mnb_verify(*_up(torch, dev, *case), tokens=out)
+    want = orc.verify(target, draft, tokens, start, u, v)[0]
+    np.testing.assert_array_equal(out.cpu().numpy(), np.concatenate([want, np.full(more, -7)]))
+    mnb.mnb_check_device_status()
+
+
 def test_verify_views(env):
     """Rows that lie apart, at any multiple of four bytes."""
     mnb, torch, dev = env
