@@ -420,16 +420,19 @@ __global__ void __launch_bounds__(kPartThreads) softmax_join_kernel(const Softma
   }
 }
 
-// CTAs of a cluster that has a row, 0: no clusters. One launch saves 3 us of host time, and a few rows GPU time too; more clusters than the
-// GPU starts at once do not. fp16, 128256 logits a row, us with clusters / in two launches: 1 row 4.8 / 4.9, 8 rows 5.5 / 7.0, 32 rows 7.8 / 8.2,
-// 40 rows 10.2 / 9.8. Of 16 CTAs instead of 8: 4 rows 5.0 / 5.4, 8 rows 6.0 / 5.6 (262000 logits: 7.0 / 7.8 in two launches).
+// CTAs of a cluster that has a row in registers, 0: no clusters. One launch saves 3 us of host time, and up to 256 CTAs GPU time too; more
+// clusters than the GPU starts at once do not, nor pairs that are more than one CTA an SM. Fewer CTAs a row where they are more than 128. fp16, us
+// with clusters / in two launches: 128256 logits a row: 1 row 4.8 / 4.9, 8 rows 5.5 / 7.0, 32 rows 7.8 / 8.2, 40 rows 10.2 / 9.8; 65000 logits: 64 rows
+// 7.5 / 8.6; 32003 logits: 32 rows 5.7 / 6.8, 64 rows 7.0 / 7.8, 85 rows (pairs) 8.9 / 8.5. Of 16 CTAs instead of 8: 4 rows of 128256 5.0 / 5.4, 8
+// rows 6.0 / 5.6.
 int soft_cluster(int rows, int V) {
   const int chunks = (V + 14) / 8;
   auto fits = [&](int cluster) { return chunks <= cluster * kClusterThreads * kBatch; };
   if (fits(1)) return 0;
-  if (rows <= 4 && fits(16)) return 16;
-  if (rows <= 32 && fits(8)) return 8;
-  return rows <= 8 && fits(16) ? 16 : 0;
+  int c = rows <= 4 ? 16 : 8;
+  while (c > 2 && c * rows > 128 && fits(c / 2)) c /= 2;
+  if (!fits(c) && rows <= 8) c = 16;
+  return fits(c) && (int64_t)c * rows <= (c == 2 ? 152 : 256) ? c : 0;
 }
 
 // Parts of a row, 0: one CTA or one cluster has a whole one.

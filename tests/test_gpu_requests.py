@@ -251,7 +251,7 @@ def _check_softmax(got, x, temperature):
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("rows,V", [(1, 1), (2, 7), (3, 512), (1, 4099), (5, 32003), (1, 128256), (40, 5001), (700, 130), (161, 2048),
                                     (1, 300001), (330, 9000), (33, 17001), (6, 200003),
-                                    (9, 131058), (20, 131059), (40, 70003)])
+                                    (9, 131058), (20, 131059), (40, 70003), (65, 32001), (129, 16385)])
 def test_softmax(env, rows, V, dtype):
     mnb, torch, dev = env
     rng = np.random.default_rng(rows + V)
@@ -272,7 +272,7 @@ def test_softmax(env, rows, V, dtype):
             np.testing.assert_allclose(got[r].cpu().numpy(), top / top.sum(), rtol=1e-6)
 
 
-@pytest.mark.parametrize("rows,V", [(3, 1), (5, 999), (40, 16377), (7, 40001), (35, 40001)])
+@pytest.mark.parametrize("rows,V", [(3, 1), (5, 999), (40, 16377), (7, 40001), (35, 40001), (130, 17001)])
 def test_softmax_in_place(env, rows, V):
     mnb, torch, dev = env
     rng = np.random.default_rng(V)
@@ -551,7 +551,7 @@ def test_threads_share_a_workspace(env):
     start, lens, table = _up(torch, dev, np.int32([0, 2]), np.int32([length]), np.arange(pages, dtype=np.int32)[None])
     x, base, down, up, _, scales, adapter = _up(torch, dev, *_lora_inputs(rng, 1500, 64, 96, 16, 5, "f16"))
     pool = mnb.MnbLoraPool(down, up, scales=scales)
-    logits = torch.randn(40, 40000, device=dev)
+    logits = torch.randn(130, 40000, device=dev)
     drafts = _up(torch, dev, *_draft_case(rng, 600, 2000, 1, True))
     forms = [lambda w: mnb.mnb_kv4_attention(q, cache, start, lens, table, 0.1, workspace=w),
              lambda w: mnb.mnb_lora(x, pool, adapter, base=base, workspace=w),

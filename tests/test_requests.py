@@ -98,8 +98,8 @@ def test_lora_refusals(lib, change, expect, word):
     (dict(stride=9), 1, "stride"),
     (dict(temperature=4), 3, "temperature"),
     (dict(out=None), 1, "out"),
-    (dict(rows=33, V=16378, stride=16378, ws_bytes=33 * 9 * 16 - 1, workspace=64), 1, "workspace"),
-    (dict(rows=33, V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
+    (dict(rows=77, V=16378, stride=16378, ws_bytes=77 * 7 * 16 - 1, workspace=64), 1, "workspace"),
+    (dict(rows=77, V=16378, stride=16378, ws_bytes=1 << 30), 1, "workspace"),
     (dict(rows=1 << 20, V=1 << 23, stride=1 << 23, ws_bytes=1 << 50, workspace=64), 2, "more than"),
 ])
 def test_softmax_refusals(lib, change, expect, word):
@@ -153,8 +153,8 @@ def test_draft_workspace_bytes(lib):
     """16 and 64 bytes for each part of a row; a part has 256 to 2048 chunks of 8 elements, or
     512 to 4096 of 4, and the rows have 608 where possible; few rows and few sequences need none."""
     soft, ver = lib.mnb_softmax_workspace_bytes, lib.mnb_verify_workspace_bytes
-    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (32, 16378), (33, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
-        0, 0, 0, 0, 33 * 9 * 16, 320 * 8 * 16, 0]
+    assert [soft(*a) for a in [(0, 9), (3, 0), (3, 16377), (76, 16378), (77, 16378), (320, 128256), (1, (1 << 24) + 1)]] == [
+        0, 0, 0, 0, 77 * 7 * 16, 320 * 8 * 16, 0]
     assert [ver(*a) for a in [(0, 9), (3, 0), (512, 1), (513, 1), (513, 4096), (64, 128256), (65, 128256), (1, 262141), (1, 262142),
                               (1, (1 << 24) + 1)]] == [0, 0, 0, 513 * 64, 513 * 64, 0, 65 * 9 * 64, 0, 129 * 64, 0]
 
