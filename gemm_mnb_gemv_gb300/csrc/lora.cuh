@@ -129,6 +129,16 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int r
       any |= left[h];
     }
     fetch(m0 + 32 * TM, next);
+    auto put = [&](int value, const uint32_t (&same)[4], int n) {
+      const int small = n <= few;
+      const int at = (int)atomicAdd(&count[small], 1u);
+      list[small ? capacity - 1 - at : at] = {m0, value, {(uint64_t)same[1] << 32 | same[0], (uint64_t)same[3] << 32 | same[2]}};
+    };
+    if constexpr (H == 1) {  // each adapter's first row, all at once
+      const uint32_t same[4] = {__match_any_sync(kFull, v[0]), 0, 0, 0};
+      if (v[0] != -2 && __ffs(same[0]) - 1 == lane && (lane > 0 || !rest)) put(v[0], same, __popc(same[0]));
+      continue;
+    }
     bool skip = rest != 0;
     while (any) {
       int value = -2;
@@ -145,11 +155,7 @@ __global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int r
         any |= left[h];
         n += __popc(same[h]);
       }
-      if (lane == 0 && !skip) {
-        const int small = n <= few;
-        const int at = (int)atomicAdd(&count[small], 1u);
-        list[small ? capacity - 1 - at : at] = {m0, value, {(uint64_t)same[1] << 32 | same[0], (uint64_t)same[3] << 32 | same[2]}};
-      }
+      if (lane == 0 && !skip) put(value, same, n);
       skip = false;
     }
   }
