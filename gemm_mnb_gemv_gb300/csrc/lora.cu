@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   const int cta = cluster_ctarank(), id = blockIdx.x / cluster;
   const uint32_t ring = smem_u32(smem);
   pdl_launch_dependents();
-  if (!small_only) pdl_wait();
+  if (!list) pdl_wait();  // the list's launch lets this one start when its own inputs are there
 
   const int granules = (a.K + 31) / 32, blocks = (a.N + 31) / 32;
   const int g0 = (int)((int64_t)granules * cta / cluster), g1 = (int)((int64_t)granules * (cta + 1) / cluster);
@@ -123,14 +123,16 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   const bool base_vec = a.base && a.base_stride % kVec == 0, out_vec = a.out_stride % kVec == 0;
   const bool in_place = a.base == a.out;
 
-  // With a list: all its items, or the small ones alone. Without one each cluster finds its tile's adapters itself: cluster `id` takes
+  // With a list: the first item of each tile (the rows of its first row's adapter), which the clusters find themselves while the list is
+  // being made, then its items; or its small ones alone. Without one each cluster finds its tile's adapters itself: cluster `id` takes
   // tile id / subs and every subs-th of its adapters, in the order of their first rows.
-  const int big = list && !small_only ? (int)__ldcg(counts) : 0;
-  int items, first, step, of_row = -2;
+  const int tiles = list && !small_only ? (a.M + TM - 1) / TM : 0;
+  constexpr int kUnknown = 0x7fffffff;
+  int big = 0, items, first, step, of_row = -2;
   uint32_t same = 0, firsts = 0;
   const int m0 = id / subs * TM;
   if (list) {
-    items = big + (int)__ldcg(counts + 1), first = id, step = gridDim.x / cluster;
+    items = small_only ? (int)__ldcg(counts + 1) : kUnknown, first = id, step = gridDim.x / cluster;
   } else {
     first = id % subs, step = subs;
     if (lane < TM && m0 + lane < a.M) {
@@ -145,10 +147,29 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     items = __popc(firsts);
     for (int k = 0; k < first; ++k) firsts &= firsts - 1;
   }
-  for (int it = first; it < items; it += step) {
+  for (int it = first;; it += step) {
+    if (it >= tiles && items == kUnknown) {
+      pdl_wait();
+      big = (int)__ldcg(counts), items = tiles + big + (int)__ldcg(counts + 1);
+    }
+    if (it >= items) break;
     Item item;
-    if (list) {
-      const uint64_t* p = reinterpret_cast<const uint64_t*>(list + (it < big ? it : capacity - 1 - (it - big)));
+    if (it < tiles) {
+      constexpr int H = (TM + 31) / 32;
+      int v[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const int i = 32 * h + lane;
+        const bool in = i < TM && it * TM + i < a.M;
+        v[h] = in ? __ldcg(a.adapter + it * TM + i) : 0;
+        v[h] = !in ? -2 : v[h] < 0 || v[h] >= a.count ? -1 : v[h];
+      }
+      item = {it * TM, __shfl_sync(kFull, v[0], 0), {0, 0}};
+#pragma unroll
+      for (int h = 0; h < H; ++h) item.rows[h / 2] |= (uint64_t)__ballot_sync(kFull, v[h] == item.adapter) << (h % 2 * 32);
+    } else if (list) {
+      const int at = it - tiles;
+      const uint64_t* p = reinterpret_cast<const uint64_t*>(list + (at < big ? at : capacity - 1 - (at - big)));
       const uint64_t head = __ldcg(p);
       item = {(int)(uint32_t)head, (int)(head >> 32), {__ldcg(p + 1), __ldcg(p + 2)}};
     } else {
@@ -524,7 +545,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     }
     if (WM == 1 && rank > 0) cluster_wait();
   }
-  if (small_only) pdl_wait();  // who waits for this kernel waits for the one beside it too
+  if (list) pdl_wait();  // who waits for this kernel waits for the one before it too
 }
 
 // Rows up to which each cluster finds its tile's adapters itself. Beyond, a launch of 4 us makes a list of all items first (132 rows
@@ -554,7 +575,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, 0, ctx.status);
   }
   const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, 0, list.counts, list.items, a.M, ctx.status);
+  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, 1, list.counts, list.items, a.M, ctx.status);
   if (e != cudaSuccess) return e;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
