@@ -548,12 +548,13 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   if (list) pdl_wait();  // who waits for this kernel waits for the one before it too
 }
 
-// Rows up to which each cluster finds its tile's adapters itself. Beyond, a launch of 4 us makes a list of all items first (132 rows
-// of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 9.2).
+// Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first
+// (132 rows of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 8.0).
 constexpr int kFewRows = 256;
 // Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
-// much less often but fill the GPU later. fp16, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 15.9 / 18.0 at 1000 rows, 22.5 / 18.2 at 1400; rank 64
-// 18.3 / 19.3 at 700 and 21.5 / 19.4 at 1000; rank 128 29.7 / 23.3 at 272 and 69 / 24 at 1000.
+// much less often but fill the GPU later. fp16, four prompts, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 14.8 / 18.3 at 1000 rows, 20.9 /
+// 18.4 at 1200; rank 64 17.7 / 19.9 at 700 and 20.3 / 19.8 at 1000; rank 128 29.8 / 22.1 at 272 and 56 / 23 at 800. fp32, tiles of 16 / of 64: rank 32
+// 23.7 / 24.2 at 1000 and 27.6 / 26.9 at 1400; rank 128 36.1 / 32.6 at 272.
 int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
 
 template <int RB, int WM, bool F32>

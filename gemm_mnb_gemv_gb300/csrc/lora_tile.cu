@@ -616,7 +616,9 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   static std::atomic<int> known[kMostCtas][64];
   int room[kMostCtas];
   for (int i = 0; i < kMostCtas; ++i) room[i] = clusters_held(ctx, kern, i + 1, kThreads, L::kBytes, known[i]);
-  const int tiles = (a.M + kRows - 1) / kRows;  // a tile in which one prompt ends and the next begins is two items
+  // A tile in which one prompt ends and the next begins is two items. (Where they are more than thought, a few clusters get two: 1784 rows of four
+  // prompts 27 us instead of 21.6 with clusters of 6, which take 21.6 for two prompts, too, instead of 18.8.)
+  const int tiles = (a.M + kRows - 1) / kRows;
   const int pick = tile_cluster(tiles + tiles / 8, room), cluster = pick + 1;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
