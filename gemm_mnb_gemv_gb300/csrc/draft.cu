@@ -6,9 +6,9 @@
 // rows of 128256 took 67 us with them at their best size, in two launches 50.)
 // Softmax, bound: 320 x 128256 fp16 with temperatures, 50 us (36 at the copy rate). The first launch takes 16 us, most of it
 // arithmetic (70% of the issue slots); the second reads the logits again, about half of them from L2, and writes at the memory's rate (7 TB/s).
-// One row: 4.7 us, launch and cluster.
-// Verification, bound: 64 x 4 drafted tokens x 128256, 15.3 us (8.9): three loads that follow each other to the accepted length, then one row
-// of p and q at half the copy rate, the cluster, the element. One sequence: 6.1 us.
+// One row: 4.8 us, launch and cluster.
+// Verification, bound: 64 x 4 drafted tokens x 128256, 14.9 us (8.9): three loads that follow each other to the accepted length, then one row
+// of p and q at half the copy rate, the cluster, the element. One sequence: 6.2 us.
 #include <float.h>
 
 #include "cluster.cuh"

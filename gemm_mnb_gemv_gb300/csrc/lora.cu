@@ -13,7 +13,7 @@
 // rounded. fp32: s is held as two fp16 of that scale, and x as two of the scale of the 32 elements that a granule of K has of a row;
 // each is multiplied on its own and the granule's scale put back in fp32 (2^-22; two tf32 parts took twice the instructions at half
 // their rate).
-// Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 14.5 us, 2.7 of them
+// Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 14.7 us, 2.7 of them
 // bytes at the copy rate: about 2150 instructions a warp at 7 cycles each, 12 warps an SM (registers allow 16). Weights straight from
 // memory to the products' registers, without the ring: 22 us (half of each line at a time, and spills); a ring for each warp,
 // without barriers: the same.  One row of rank 16: 5.9 us, the chain of launch, adapter, K, cluster, N.
