@@ -568,6 +568,40 @@ def test_threads_share_a_workspace(env):
     mnb.mnb_check_device_status()
 
 
+def test_graphs_replayed_at_once(env):
+    """Two captured runs of calls with workspaces, replayed on two streams at the same time, inputs changed in between."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(16)
+    graphs = []
+    for M, rows in ((1500, 130), (700, 300)):
+        x, base, down, up, _, scales, adapter = _up(torch, dev, *_lora_inputs(rng, M, 64, 96, 16, 5, "f16"))
+        pool = mnb.MnbLoraPool(down, up, scales=scales)
+        logits = torch.randn(rows, 40000, device=dev)
+        drafts = _up(torch, dev, *_draft_case(rng, 600, 2000, 1, True))
+
+        def run(x=x, base=base, pool=pool, adapter=adapter, logits=logits, drafts=drafts):
+            return mnb.mnb_lora(x, pool, adapter, base=base), mnb.mnb_softmax(logits), *mnb.mnb_verify(*drafts)
+
+        run()
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            outs = run()
+        graphs.append((side, graph, outs, run, adapter, logits))
+    for turn in range(3):
+        for _, _, _, _, adapter, logits in graphs:
+            adapter.copy_(torch.roll(adapter, 37)), logits.mul_(1.5)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for side, graph, *_ in graphs:
+                with torch.cuda.stream(side):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, _, outs, run, _, _ in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(outs, run())), turn
+    mnb.mnb_check_device_status()
+
+
 def test_no_rows(env):
     mnb, torch, dev = env
     h = dict(dtype=torch.float16, device=dev)
