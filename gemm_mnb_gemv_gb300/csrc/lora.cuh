@@ -40,8 +40,8 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // Elements at .. at + width - 1 of a base of `end` elements whose rows lie anywhere (at < 0: zeros): their 16-byte chunks, brought into
-// place. kWords * 4 bytes are worked on; what lies behind `width` is anything. (Element by element, and stored so too, 4096 rows of 4095
-// took 193 us instead of 78, 900 rows 34 instead of 18; rows at 16 bytes 29 and 14.)
+// place. kWords * 4 bytes are worked on; what lies behind `width` is anything. (Element by element, and stored so too, 900 rows of
+// 4095 took 34 us instead of 18; rows at 16 bytes 14.)
 template <typename T, int kWords>
 __device__ __forceinline__ void loose_row(const T* base, int64_t at, int64_t end, int width, uint32_t (&y)[kWords]) {
   constexpr int kVec = 16 / sizeof(T), kChunks = kWords / 4 + 1;

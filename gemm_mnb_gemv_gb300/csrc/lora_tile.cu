@@ -123,6 +123,96 @@ __device__ __noinline__ int nth_bit(uint64_t m0, uint64_t m1, int n) {
   return at;
 }
 
+// 64 columns of a warp's 32 rows of a base whose rows lie anywhere (zeros without one): 16-byte chunks, 4 rows and 8 chunks of each at a
+// time, go as they are to the rows' places in shared memory; a row's ninth stays with its lane, which brings them into place. (Each lane its own
+// row, 5 chunks for 32 columns: 4096 x 4095 of rank 16 78 us.)
+__device__ __noinline__ uint4 last_chunk(const unsigned short* p, int n) {  // behind the last row there may be nothing
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i / 2] |= (uint32_t)__ldcg(p + i) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+struct LooseBase {
+  uint4 ninth;
+  int skew;
+  __device__ __forceinline__ static uint4 chunk(const unsigned short* base, int64_t at, int64_t end, bool live) {
+    if (!live || at >= end) return make_uint4(0, 0, 0, 0);
+    return at + 8 <= end ? __ldcg(reinterpret_cast<const uint4*>(base + at)) : last_chunk(base + at, (int)(end - at));
+  }
+  // The warp's rows are `first` .. of the tile at `tile`, `row` this lane's; columns n .. (below n1).
+  __device__ __forceinline__ void fetch(const Lora& a, uint32_t tile, int first, int row, int n, int n1) {
+    const int lane = threadIdx.x & 31, c = lane % 8;
+    const unsigned short* base = static_cast<const unsigned short*>(a.base);
+    const int64_t end = base_end(a);
+    uint4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int from = __shfl_sync(kFull, row, 4 * k + lane / 8);
+      const int64_t at = from * a.base_stride + n;
+      const int off = (int)(at & 7);
+      v[k] = chunk(base, at - off + 8 * c, end, base && from >= 0 && 8 * c < off + n1 - n);
+    }
+    const int64_t at = row * a.base_stride + n;
+    skew = base && row >= 0 ? (int)(at & 7) : 0;
+    ninth = chunk(base, at - skew + 64, end, base && row >= 0 && 64 < skew + n1 - n);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store16(tile + swizzled(first + 4 * k + lane / 8, c), v[k].x, v[k].y, v[k].z, v[k].w);
+    __syncwarp();
+  }
+  // 32 columns from chunk c0 (0 or 4) on of row r.
+  __device__ __forceinline__ void take(uint32_t tile, int r, int c0, uint32_t (&y)[16]) const {
+    uint32_t w[20];
+#pragma unroll
+    for (int c = 0; c < 5; ++c) {
+      uint4 v = ninth;
+      if (c < 4 || c0 == 0) v = lds128_a(tile + swizzled(r, c0 + c));
+      w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 18; ++i) w[i] = skew & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 17; ++i) w[i] = skew & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = skew & 1 ? __byte_perm(w[i], w[i + 1], 0x5432) : w[i];
+  }
+};
+
+// A warp's 32 rows of up to 64 results, from their places in shared memory to where they lie: a row's whole 16-byte chunks, 8 of 4 rows at a
+// time, then its ends by elements. (A row after the other, 32 lanes of 2 bytes: 4096 x 4095 67 us, 54 so; rows at 32 bytes 29.)
+__device__ __noinline__ void store_loose(unsigned short* out, int64_t stride, uint32_t tile, int first, int row, int width) {
+  __syncwarp();
+  const int lane = threadIdx.x & 31, c = lane % 8;
+  const int skew_of = (int)(reinterpret_cast<uintptr_t>(out) / 2 % 8);
+#pragma unroll 2
+  for (int k = 0; k < 8; ++k) {
+    const int r = first + 4 * k + lane / 8, to = __shfl_sync(kFull, row, 4 * k + lane / 8);
+    const int off = (int)((skew_of + to * stride) & 7), s = 8 * c - off;  // the row begins `off` elements behind a chunk's start; this chunk at s
+    unsigned short* p = out + to * stride;
+    if (to >= 0) {
+      if (s >= 0 && s + 8 <= width) {
+        uint32_t w[8];
+        const uint4 u = lds128_a(tile + swizzled(r, off ? c - 1 : c)), v = lds128_a(tile + swizzled(r, c));
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+        const int shift = (8 - off) & 7;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = shift & 4 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = shift & 2 ? w[i + 1] : w[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = shift & 1 ? __byte_perm(w[i], w[i + 1], 0x5432) : w[i];
+        *reinterpret_cast<uint4*>(p + s) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      const int head = min((8 - off) & 7, width), tail = (width - head) & 7;  // elements before and behind the whole chunks
+      for (int j = c; j < head + tail; j += 8) {
+        const int e = j < head ? j : width - tail + (j - head);
+        p[e] = (unsigned short)lds_u16_a(tile + swizzled(r, e / 8) + (e & 7) * 2);
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // An item as every role sees it.
 struct Work {
   Item item;
@@ -496,13 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && !wait_warp(&full[slot], full_phase >> slot & 1)) give_up(kStatusFullWait);
         full_phase ^= 1u << slot;
         if (quarter * 32 < w.n_rows) {
+          LooseBase loose;
+          const int n_own = n0 + (q - w.down_stages) * kSpan + piece * kOwnCols;  // this warp's 64 columns
+          const bool direct = out_vec && min(kOwnCols, n1 - n_own) % 32 == 0;
+          const uint32_t tile = ring + slot * L::kSlot + piece * (kRows * 128);
+          if (a.base && !base_vec && n_own < n1) loose.fetch(a, tile, quarter * 32, row, n_own, n1);
 #pragma unroll 1
           for (int g = 0; g < kOwnCols; g += 32) {
-            const int col = piece * kOwnCols + g;  // of the stage
-            const int n = n0 + (q - w.down_stages) * kSpan + col, width = min(32, n1 - n);
-            if (width <= 0) break;
-            const uint32_t tile = ring + slot * L::kSlot + col / 64 * (kRows * 128);
-            const int ch0 = col % 64 / 8;  // first 16-byte chunk of the 32 columns
+            const int n = n_own + g;
+            if (n >= n1) break;
+            const int ch0 = g / 8;  // first 16-byte chunk of the 32 columns
             uint32_t y[16];
             if (base_vec) {
 #pragma unroll
@@ -510,12 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint4 v = lds128_a(tile + swizzled(r, ch0 + c));
                 y[4 * c] = v.x, y[4 * c + 1] = v.y, y[4 * c + 2] = v.z, y[4 * c + 3] = v.w;
               }
+            } else if (a.base) {
+              loose.take(tile, r, ch0, y);
             } else {
-              loose_row(static_cast<const __half*>(a.base), a.base && row >= 0 ? row * a.base_stride + n : -1, base_end(a), width, y);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = 0;
             }
             if (w.rank > 0) {
               float d[32];
-              tc::tmem_ld32(lane_at + kColD2 + 128 * b + col, d);
+              tc::tmem_ld32(lane_at + kColD2 + 128 * b + piece * kOwnCols + g, d);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -527,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) y[i] = 0x7fff7fffu;
             }
-            if (out_vec && width == 32) {  // whole sectors
+            if (direct) {  // whole sectors
               if (row >= 0) {
                 __half* p = static_cast<__half*>(a.out) + (int64_t)row * a.out_stride + n;
 #pragma unroll
@@ -536,25 +632,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                "r"(y[c + 2]), "r"(y[c + 3]), "r"(y[c + 4]), "r"(y[c + 5]), "r"(y[c + 6]), "r"(y[c + 7])
                                : "memory");
               }
-            } else {  // through the base's place, a row after the other
-              __syncwarp();
+            } else {  // through the base's place
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(tile + swizzled(r, ch0 + c)), "r"(y[4 * c]), "r"(y[4 * c + 1]),
-                             "r"(y[4 * c + 2]), "r"(y[4 * c + 3])
-                             : "memory");
-              __syncwarp();
-#pragma unroll 8
-              for (int i = 0; i < 32; ++i) {
-                const int to = __shfl_sync(kFull, row, i);
-                const uint32_t v = lds_u16_a(tile + swizzled(quarter * 32 + i, ch0 + lane / 8) + (lane & 7) * 2);
-                if (to >= 0 && lane < width)
-                  static_cast<unsigned short*>(a.out)[(int64_t)to * a.out_stride + n + lane] = (unsigned short)v;
-              }
+              for (int c = 0; c < 4; ++c) store16(tile + swizzled(r, ch0 + c), y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
             }
           }
-          // where results went through these bytes, a tensor copy may write them next
-          if (!out_vec || n1 - n0 < (q - w.down_stages + 1) * kSpan) tc::fence_proxy_async_smem();
+          if (!direct && n_own < n1)
+            store_loose(static_cast<unsigned short*>(a.out) + n_own, a.out_stride, tile, quarter * 32, row, min(kOwnCols, n1 - n_own));
+          // where bases or results went through these bytes, a tensor copy may write them next
+          if ((a.base && !base_vec) || !direct) tc::fence_proxy_async_smem();
         }
         tc::fence_before_sync();
         __syncwarp();
