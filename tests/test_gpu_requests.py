@@ -153,6 +153,30 @@ def test_lora_views_of_fused_products(env, M, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("N", [1, 31, 65, 518, 1027])
+@pytest.mark.parametrize("M", [40, 700, 1600, 2500])
+def test_lora_odd_strides(env, M, N, dtype):
+    """Rows of base and out that begin anywhere, in place and apart; what lies beside out stays as it was."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(M + N)
+    x, base, down, up, r, scales, adapter = _lora_inputs(rng, M, 96, N, 24, 3, dtype, "uneven", without=0.1)
+    adapter[M // 8: M // 2] = 1
+    xd, bd, dd, ud, rd, sd, ad = _up(torch, dev, x, base, down, up, r, scales, adapter)
+    pool = mnb.MnbLoraPool(dd, ud, ranks=rd, scales=sd)
+    for more in (9, 14):
+        wide = torch.full((M, N + 8 + more), 7.0, device=dev).to(bd.dtype)
+        wide[:, 8:8 + N] = bd
+        apart = torch.full((M, N + more), 5.0, device=dev).to(bd.dtype)
+        got = mnb.mnb_lora(xd, pool, ad, base=wide[:, 8:8 + N], out=apart[:, :N])
+        _check_lora(got, x, base, down, up, r, scales, adapter, dtype)
+        assert (apart[:, N:] == 5).all()
+        mnb.mnb_lora(xd, pool, ad, base=wide[:, 8:8 + N], out=wide[:, 8:8 + N])
+        assert torch.equal(wide[:, 8:8 + N], got) and (wide[:, :8] == 7).all() and (wide[:, 8 + N:] == 7).all()
+        none = mnb.mnb_lora(xd, pool, ad, out=apart[:, :N])
+        _check_lora(none, x, None, down, up, r, scales, adapter, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
 def test_lora_without_base_scales_and_with_bad_indices(env, dtype):
     mnb, torch, dev = env
     rng = np.random.default_rng(5)
