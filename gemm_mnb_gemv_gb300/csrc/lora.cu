@@ -9,10 +9,9 @@
 // and up), and the first stages of the second product are on their way while the first one's sums are joined.
 // Rows are the M side of the warp's matrix instructions, ranks (then output columns) the N side; a lane takes 8 consecutive
 // elements of the inner index, which both operands number alike.
-// fp16 activations: s is rounded to fp16 after its row was scaled by a power of two to [2^13, 2^14), as the result is
-// rounded. fp32: s is held as two fp16 of that scale, and x as two of the scale of the 32 elements that a granule of K has of a row;
-// each is multiplied on its own and the granule's scale put back in fp32 (2^-22; two tf32 parts took twice the instructions at half
-// their rate).
+// s is held as two fp16 after its row was scaled by a power of two to [2^13, 2^14), and up takes both: 22 bits of s. fp32: x, too, as two
+// fp16, of the scale of the 32 elements that a granule of K has of a row; each is multiplied on its own and the granule's scale put
+// back in fp32 (2^-22; two tf32 parts took twice the instructions at half their rate).
 // Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 14.7 us, 2.7 of them
 // bytes at the copy rate: about 2150 instructions a warp at 7 cycles each, 12 warps an SM (registers allow 16). Weights straight from
 // memory to the products' registers, without the ring: 22 us (half of each line at a time, and spills); a ring for each warp,
@@ -27,17 +26,6 @@ namespace mnb {
 namespace {
 
 using namespace lora;
-
-// Two fp32 as fp16 pairs: hi + lo is within 2^-22 of them.
-struct Split {
-  uint32_t hi, lo;
-};
-__device__ __forceinline__ Split split(float x, float y) {
-  const uint32_t h = half2_bits(x, y);
-  const float2 f = half2_floats(h);
-  return {h, half2_bits(x - f.x, y - f.y)};
-}
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Of two rows; out of line: inlined, rows at 16 bytes paid 1 to 2 % for the code.
 template <int kWords>
@@ -65,7 +53,11 @@ struct Geo {
   static constexpr int kStage = kAct + kWeight;
   static constexpr int kPart = (WN - 1) * TM * RP * 4;        // partial sums of the warps; the CTA's own in the first
   static constexpr int kSRow = RP >= 64 ? RP * 2 + 64 : RP * 2;  // bytes of a row of s
-  static constexpr int kSHalf = (TM * kSRow + 127) / 128 * 128, kS = kSHalf * (F32 ? 2 : 1);  // fp32: the low parts behind the high ones
+  // The low parts lie behind the high ones or, with tiles of 16 rows in fp16, over the partial sums of the other warps, which are joined by
+  // then (and which the other CTAs do not read): room for one more stage or CTA hangs on it.
+  static constexpr int kSHalf = (TM * kSRow + 127) / 128 * 128, kS = kSHalf * (F32 ? 2 : 1);
+  static constexpr int kLow = F32 ? kSHalf : TM * RP * 4 - kPart;  // from the high parts
+  static_assert(F32 || (WN > 2 && kSHalf <= (WN - 2) * TM * RP * 4), "the low parts fit over the other warps' sums");
   // Stages that fit when an SM holds n CTAs. As many CTAs as can have three, or else two (16 warps an SM are what registers allow).
   static constexpr int fit(int n) {
     const int stages = (228 * 1024 / n - 1024 - 768 - kPart - kS) / kStage;
@@ -402,12 +394,12 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           const uint32_t to = smem_u32(row + col * 2);
           for (int c = 0; mine && c < cluster; ++c) {
             cluster_st_u64(cluster_map(to, c), x.hi, y.hi);
-            if constexpr (F32) cluster_st_u64(cluster_map(to + L::kSHalf, c), x.lo, y.lo);
+            cluster_st_u64(cluster_map(to + L::kLow, c), x.lo, y.lo);
             if (col == 0) cluster_st_f32(cluster_map(smem_u32(&factors[r]), c), scalbnf(scale, p));
           }
         } else if (mine) {
           *reinterpret_cast<uint2*>(row + col * 2) = make_uint2(x.hi, y.hi);
-          if constexpr (F32) *reinterpret_cast<uint2*>(row + L::kSHalf + col * 2) = make_uint2(x.lo, y.lo);
+          *reinterpret_cast<uint2*>(row + L::kLow + col * 2) = make_uint2(x.lo, y.lo);
           if (col == 0) factors[r] = scalbnf(scale, p);
         }
       }
@@ -458,11 +450,11 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
                 }
               }
 #pragma unroll
-              for (int part = F32 ? 1 : 0; part >= 0; --part) {  // the low parts first
+              for (int part = 1; part >= 0; --part) {  // the low parts first
                 uint32_t x[2][E / 2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const uint32_t p = smem_u32(s_mem + part * L::kSHalf + (r0 + 8 * h) * L::kSRow) + (4 * E * c + E * t) * 2;
+                  const uint32_t p = smem_u32(s_mem + part * L::kLow + (r0 + 8 * h) * L::kSRow) + (4 * E * c + E * t) * 2;
                   if constexpr (E == 8) {
                     const uint4 v = lds128_a(p);
                     x[h][0] = v.x, x[h][1] = v.y, x[h][2] = v.z, x[h][3] = v.w;

@@ -15,6 +15,17 @@ __device__ __forceinline__ float2 half2_floats(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// Two fp32 as fp16 pairs: hi + lo is within 2^-22 of them.
+struct Split {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Split split(float x, float y) {
+  const uint32_t h = half2_bits(x, y);
+  const float2 f = half2_floats(h);
+  return {h, half2_bits(x - f.x, y - f.y)};
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // 16 bytes global -> shared, asynchronously.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

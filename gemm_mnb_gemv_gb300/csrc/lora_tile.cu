@@ -3,8 +3,8 @@
 //
 // A cluster of 1 to 8 CTAs (one an SM) takes an item, the rows of one adapter in a tile:
 //   1. partial s = down x over the CTA's part of K, 128 a stage (M 128 rows, N the rank), in tensor memory;
-//   2. the CTAs exchange: CTA c adds up the rows c 128 / C .. of all partial sums, rounds them to fp16 (scaled by the row's power of two)
-//      and writes them into every CTA's operand s;
+//   2. the CTAs exchange: CTA c adds up the rows c 128 / C .. of all partial sums, scales them by the row's power of two
+//      and writes them as two fp16 (22 bits) into every CTA's operands s;
 //   3. out = base + s up over the CTA's part of N, 128 columns a stage, accumulated in two tensor memory buffers in turn.
 // Roles in 512 threads:
 //   warps 0-3    producers, into one ring that runs on from product to product and item to item: x and base by tensor copies where
@@ -39,8 +39,14 @@ struct TileGeo {
   static constexpr int kAct = kRows * kSpan * 2;                 // x or base: two halves of 64 columns, 128-byte rows
   static constexpr int kWeight = kSpan * 128 * (RP > 64 ? 2 : 1);  // down: two halves of K; up: halves of the rank
   static constexpr int kSlot = kAct + kWeight;
-  static constexpr int kS = kRows * 128 * (RP > 64 ? 2 : 1);
+  // s: rows of 128 bytes. Ranks up to 32: the low parts behind the high ones in a row; up to 64: a half of their own; up to 128: two halves of
+  // high parts, and the low ones over the partial sums, which take as many bytes as both together.
+  static constexpr int kS = kRows * 128 * (RP > 32 ? 2 : 1);
+  static constexpr bool kOver = RP > 64;
   static constexpr int kPart = kRows * RP * 4;
+  static constexpr int kLowAt = kOver ? kS : RP > 32 ? kRows * 128 : RP * 2;  // from the high parts
+  static constexpr int kLowGroup = kOver ? 8 * RP * 4 : 1024;  // of eight rows: where the eight rows of partial sums are, their halves side by side
+  static constexpr int kLowHalf = 1024;
   static constexpr int kFit = (227 * 1024 - 2048 - kS - kPart) / kSlot;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr int kBytes = kStages * kSlot + kS + kPart + 1024;
@@ -474,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_full()) break;
         if (w.rank > 0) {
           const int b = results & 1;
+          static_assert(L::kLowAt % 32 == 0 && (!L::kOver || (L::kS % 1024 == 0 && L::kLowGroup == 4 * L::kLowHalf)), "places in the swizzle");
           if (results >= 2) {
             if (!wait_warp(&d2_empty[b], d2_phase >> b & 1)) {
               give_up(kStatusMmaWait);
@@ -482,13 +489,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             d2_phase ^= 1u << b;
             tc::fence_after_sync();
           }
-          const uint64_t da = tc::smem_desc_k_sw128(s_at), db = tc::smem_desc_k_sw128(ring + slot * L::kSlot + L::kAct);
+          const uint64_t db = tc::smem_desc_k_sw128(ring + slot * L::kSlot + L::kAct);
           const uint32_t idesc = tc::idesc_f16_f32(kRows, kSpan);
           if (leader) {
+            const uint64_t low = tc::smem_desc_k_sw128(s_at + L::kLowAt, L::kLowGroup), high = tc::smem_desc_k_sw128(s_at);
+#pragma unroll 1
+            for (int kk = 0; kk < w.cols / 16; ++kk)  // the low parts first
+              tc::mma_f16(tmem + kColD2 + 128 * b, low + (((kk / 4) * L::kLowHalf + (kk % 4) * 32) >> 4),
+                          db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, kk > 0);
 #pragma unroll 1
             for (int kk = 0; kk < w.cols / 16; ++kk)
-              tc::mma_f16(tmem + kColD2 + 128 * b, da + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
-                          db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, kk > 0);
+              tc::mma_f16(tmem + kColD2 + 128 * b, high + (((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4),
+                          db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, 1);
             tc::mma_commit(&d2_full[b]);
           }
           __syncwarp();
@@ -548,26 +560,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           cluster_mbar_arrive(&part_ready, cluster);
           if (!__all_sync(kFull, cluster_mbar_wait(&part_ready, s_phase))) give_up(kStatusMmaWait);
         }
-        if (ok) {
-          // ---- rows of this CTA's share: over the cluster, to fp16, into every CTA's operand ----
-          const float scale = a.scales ? __ldcg(a.scales + w.item.adapter) : 1.0f;
-          const int sr0 = kRows * (int)cta / cluster, chunks = (kRows * ((int)cta + 1) / cluster - sr0) * (RP / 4);
-          for (int u0 = e * 32; u0 < chunks; u0 += kEpiWarps * 32) {
-            const bool mine = u0 + lane < chunks;
-            const int u = mine ? u0 + lane : 0, sr = sr0 + u / (RP / 4), ch = u % (RP / 4);
+        // ---- rows of this CTA's share: over the cluster, to two fp16, into every CTA's operands ----
+        // The low parts of eight rows may lie over the sums of the same eight, which only the CTA that has them reads: shares are then whole
+        // eights, and its warps meet between reading and writing, whatever became of their waits.
+        constexpr int kRowUnit = L::kOver ? 8 : 1, kHeld = L::kOver ? 4 : 1;
+        const float scale = a.scales ? __ldcg(a.scales + w.item.adapter) : 1.0f;
+        const int sr0 = kRowUnit * (kRows / kRowUnit * (int)cta / cluster), sr1 = kRowUnit * (kRows / kRowUnit * ((int)cta + 1) / cluster);
+        const int chunks = (sr1 - sr0) * (RP / 4);
+        for (int u0 = e * 32; u0 < chunks; u0 += kHeld * kEpiWarps * 32) {
+          uint2 low[kHeld];
+          auto place_of = [&](int i, int& sr, int& ch) {  // of this lane's chunk i, and whether there is one
+            const int u = u0 + i * (kEpiWarps * 32) + lane;
+            sr = sr0 + (u < chunks ? u : 0) / (RP / 4), ch = (u < chunks ? u : 0) % (RP / 4);
+            return u < chunks;
+          };
+          auto put_low = [&](int i) {
+            int sr, ch;
+            if (!place_of(i, sr, ch)) return;
+            const uint32_t to = s_at + L::kLowAt + sr / 8 * L::kLowGroup + (ch / 16) * L::kLowHalf +
+                                (RP > 32 ? swizzled(sr % 8, ch / 2 % 8) : swizzled(sr % 8, ch / 2 + RP / 8) - RP * 2) + (ch & 1) * 8;
+            for (int c = 0; c < cluster; ++c) cluster_st_u64(cluster_map(to, c), low[i].x, low[i].y);
+          };
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            if (!ok || u0 + i * (kEpiWarps * 32) >= chunks) continue;
+            int sr, ch;
+            const bool mine = place_of(i, sr, ch);
             const float4 v = cluster_sum_f4(part_at + part_place<RP>(sr, ch), cluster);
             float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
             for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
             const int p = row_power(top);
-            const float f = __uint_as_float((uint32_t)(127 - p) << 23);
-            const uint32_t lo = half2_bits(v.x * f, v.y * f), hi = half2_bits(v.z * f, v.w * f);
+            const float f = pow2(-p);
+            const Split x = split(v.x * f, v.y * f), y = split(v.z * f, v.w * f);
+            low[i] = make_uint2(x.lo, y.lo);
             const uint32_t to = s_at + (ch / 16) * (kRows * 128) + swizzled(sr, ch / 2 % 8) + (ch & 1) * 8;
             for (int c = 0; mine && c < cluster; ++c) {
-              cluster_st_u64(cluster_map(to, c), lo, hi);
+              cluster_st_u64(cluster_map(to, c), x.hi, y.hi);
               if (ch == 0) cluster_st_f32(cluster_map(smem_u32(&factors[sr]), c), scalbnf(scale, p));
             }
+            if (!L::kOver) put_low(i);
           }
+          if constexpr (L::kOver) {
+            __syncwarp();
+            asm volatile("barrier.sync.aligned 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+              if (ok && u0 + i * (kEpiWarps * 32) < chunks) put_low(i);
+          }
+          __syncwarp();
+        }
+        if (ok) {
           asm volatile("fence.proxy.async;" ::: "memory");  // the products read s through the async proxy
           cluster_mbar_arrive(&s_ready, cluster);
           if (!__all_sync(kFull, cluster_mbar_wait(&s_ready, s_phase))) give_up(kStatusMmaWait);  // for the rows' factors

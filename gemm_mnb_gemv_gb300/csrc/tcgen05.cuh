@@ -18,11 +18,11 @@ namespace tc {
 //   bit  52     leading-dimension offset mode (0: relative)
 //   bits 61-63  swizzle mode (2: 128-byte swizzle)
 // ---------------------------------------------------------------------------------
-__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr) {
+__device__ __forceinline__ uint64_t smem_desc_k_sw128(uint32_t saddr, uint32_t sbo = 1024) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
   d |= (uint64_t)1u << 16;                    // LBO (ignored for this layout)
-  d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;  // SBO: 8 rows x 128 bytes
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;  // SBO: from 8 rows of 128 bytes to the next 8
   d |= (uint64_t)1u << 46;                    // version
   d |= (uint64_t)2u << 61;                    // 128-byte swizzle
   return d;

@@ -455,9 +455,8 @@ typedef struct {
  * product do); x_stride is a multiple of 16 bytes (else MNB_ERR_MISALIGNED), K of 16 elements. base may be out
  * (with the same stride; neither it nor x may overlap out otherwise) or NULL, which counts as zeros. adapter is int32 [M]: a
  * negative one leaves out[m] = base[m], and so does one beyond the pool, which sets the index bit of the device status word.
- * Products and sums are fp32. MNB_F16: down . x is rounded to fp16 relative to the row's largest (2^-11), as the result is;
- * MNB_F32: x and down . x enter the products with 22 bits, relative
- * to the largest of 32 neighbours and of the row. A row of x with inf or NaN gives non-finite outputs in that row.
+ * Products and sums are fp32. down . x enters the second product with 22 bits, relative to the row's largest, and with MNB_F32 x the
+ * first one, relative to the largest of 32 neighbours. A row of x with inf or NaN gives non-finite outputs in that row.
  * `workspace` holds mnb_lora_workspace_bytes(M) bytes (0 up to 256 rows); its contents need no initialisation and are overwritten by
  * each call, so calls sharing one workspace must be ordered on one stream (from any host threads). M = 0 is valid and does
  * nothing.
