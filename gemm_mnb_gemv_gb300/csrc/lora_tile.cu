@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u, s_at = ring + S * L::kSlot, part_at = s_at + L::kS;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&full[i], kProducers + 1), mbar_init(&empty_mma[i], 1), mbar_init(&empty_epi[i], kEpiWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&full[i], kProducers + 1), mbar_init(&empty_mma[i], 1), mbar_init(&empty_epi[i], kEpiWarps + 1);
     for (int i = 0; i < 2; ++i) mbar_init(&d2_full[i], 1), mbar_init(&d2_empty[i], kEpiWarps);
     mbar_init(&d1_full, 1);
     mbar_init(&drained, 1);
@@ -470,7 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         next_slot();
       }
-      if (ok && w.rank > 0) {
+      // A CTA without any part of K and N has nothing to wait for, and nothing would keep its exchange from going on to the next item before this
+      // warp has looked: with a part, the exchange waits for this warp's products.
+      if (ok && w.rank > 0 && w.stages > 0) {
         if (!__all_sync(kFull, cluster_mbar_wait(&s_ready, s_phase))) give_up(kStatusMmaWait);
         s_phase ^= 1u;
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -503,9 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                           db + (((kk / 4) * (kSpan * 128) + (kk % 4) * 32) >> 4), idesc, 1);
             tc::mma_commit(&d2_full[b]);
           }
-          __syncwarp();
           ++results;
         }
+        // A stage of the second product is also this warp's to free: without products (no adapter) the epilogue doesn't wait for it, and the slot
+        // could come round again before it has seen this turn's arrival.
+        if (leader) mbar_arrive(&empty_epi[slot]);
+        __syncwarp();
         next_slot();
       }
     }

@@ -37,3 +37,27 @@ def test_lora_fp16_keeps_the_first_products_precision(env, M, run, R):  # noqa: 
     err = np.abs(got - want)
     assert (err <= tol).all(), float((err / tol).max())
     mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("M,K,N,R", [(9000, 160, 2600, 128), (6000, 64, 4100, 64), (4000, 16, 32, 128), (20000, 96, 200, 16), (3000, 4096, 32, 72)])
+def test_lora_prompts_between_rows_without_adapter(env, M, K, N, R, in_place):  # noqa: F811
+    """Prompts without an adapter or with one of rank 0 between others: their tiles run through the tensor cores' kernel without
+    products, and where base and out are apart without anything else that its warps wait for together."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(M + K + R)
+    x, base, down, up, _, scales, _ = _lora_inputs(rng, M, K, N, R, 4, "f16")
+    ranks = np.int32([R, 0, R - 3, 1])
+    adapter = np.repeat(np.int32([-1, -1, 0, 1, -1, 2, 1, 1, -1, 3, -1]), -(-M // 11))[:M].copy()
+    adapter[rng.integers(0, M, 40)] = 2
+    xd, bd, dd, ud, rd, sd, ad = _up(torch, dev, x, base, down, up, ranks, scales, adapter)
+    pool = mnb.MnbLoraPool(dd, ud, ranks=rd, scales=sd)
+    first = None
+    for _ in range(20):
+        out = bd.clone() if in_place else torch.full_like(bd, float("nan"))
+        mnb.mnb_lora(xd, pool, ad, base=out if in_place else bd, out=out)
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    _check_lora(first, x, base, down, up, ranks, scales, adapter, "f16")
+    assert mnb.mnb_last_variant() == "lora_tile_tcgen05"
+    mnb.mnb_check_device_status()
