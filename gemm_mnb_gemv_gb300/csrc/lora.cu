@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
           if (col == 0) factors[r] = scalbnf(scale, p);
         }
       }
+      __syncwarp();      // the cluster's barriers want whole warps
       cluster_arrive();  // no more reads of the others' sums
       if (kShare) cluster_wait();
     }
@@ -535,7 +536,10 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
         issue(q + L::kAhead);
       }
     }
-    if (WM == 1 && rank > 0) cluster_wait();
+    if (WM == 1 && rank > 0) {
+      __syncwarp();
+      cluster_wait();
+    }
   }
   if (list) pdl_wait();  // who waits for this kernel waits for the one before it too
 }

@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                "r"(y[c + 2]), "r"(y[c + 3]), "r"(y[c + 4]), "r"(y[c + 5]), "r"(y[c + 6]), "r"(y[c + 7])
                                : "memory");
               }
+              __syncwarp();  // the next columns' loads from tensor memory want a whole warp
             } else {  // through the base's place
 #pragma unroll
               for (int c = 0; c < 4; ++c) store16(tile + swizzled(r, ch0 + c), y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
@@ -701,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  __syncwarp();  // lanes leave a bounded wait each at its own time
   pdl_wait();
   tc::fence_before_sync();
   __syncthreads();
