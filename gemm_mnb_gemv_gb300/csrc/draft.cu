@@ -476,9 +476,12 @@ __device__ __forceinline__ int64_t placed(int32_t a, int32_t b, int32_t c) {
   return ((int64_t)a << 40) + ((int64_t)b << 20) + (int64_t)c;
 }
 
+// A random number, held to [0, 1): the largest is 1 - 2^-24.
+__device__ __forceinline__ float unit(float u) { return fminf(__saturatef(u), 0.99999994f); }
+
 // floor(total * u), u in [0, 1)
 __device__ __forceinline__ uint64_t scaled(uint64_t total, float u) {
-  const uint32_t b = min(__float_as_uint(__saturatef(u)), 0x3f7fffffu);
+  const uint32_t b = __float_as_uint(unit(u));
   const uint64_t m = b >> 23 ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
   const int s = 150 - (int)max(b >> 23, 1u);  // u = m * 2^-s, s >= 24
   const uint64_t hi = __umul64hi(total, m), lo = total * m;
@@ -613,7 +616,7 @@ __device__ __forceinline__ int count_accepted(const Verify& a, int b, int s0, in
     bool bad = false;
     if (i < n) {
       const int tok = a.tokens[s0 + i];
-      const float u = __saturatef(a.u_accept[s0 + i]);
+      const float u = unit(a.u_accept[s0 + i]);
       bad = true;
       if (tok >= 0 && tok < a.V) {
         const float pt = __saturatef(a.target[(int64_t)(s0 + b + i) * a.target_stride + tok]);

@@ -488,7 +488,7 @@ MNB_API mnb_status mnb_softmax(const void *logits, int dtype, int rows, int V, i
  *   Token d_i is accepted while u_accept[.] * q_i(d_i) < p_i(d_i). The token after the last accepted one is the first j with
  *   sum_{k <= j} w_k > u_next[b] * sum_k w_k, w = max(p - q, 0) at the rejected token's rows, w = p of the last row
  *   when all are accepted. Where nothing is left of p - q it is drawn from p; where p is all 0, it is -1.
- * u_accept fp32 [drafted], u_next fp32 [batch], in [0, 1) (others are held to it). tokens int32 [drafted + batch], laid out as
+ * u_accept fp32 [drafted], u_next fp32 [batch], in [0, 1) (others are held to 0 .. 1 - 2^-24, NaN counts as 0). tokens int32 [drafted + batch], laid out as
  * target's rows: a sequence's accepted tokens, the next one, then -1. accepted int32 [batch]: how many were accepted.
  * Arithmetic is exact: probabilities are held to 0..1 (NaN counts as 0) and rounded to whole numbers of 2^-60, in which weights and
  * sums are taken (a row adds up to less than 16). A drafted token outside 0..V-1 is rejected and sets the index bit of the

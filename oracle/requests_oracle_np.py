@@ -57,13 +57,14 @@ def verify(target, draft, draft_tokens, draft_start, u_accept, u_next):
     B, V = len(draft_start) - 1, target.shape[1]
     tokens, accepted = np.full(len(target), -1, np.int32), np.zeros(B, np.int32)
     unit = lambda v: float(np.clip(np.nan_to_num(np.float64(v), nan=0.0), 0, 1))  # noqa: E731
+    number = lambda v: min(unit(v), 1 - 2.0 ** -24)  # noqa: E731  a random number: below 1
     for b in range(B):
         s0, s1 = int(draft_start[b]), int(draft_start[b + 1])
         w = None
         for k in range(s0, s1):
             d = int(draft_tokens[k])
             p = target[k + b]
-            if 0 <= d < V and unit(u_accept[k]) * (1.0 if draft is None else unit(draft[k, d])) < unit(p[d]):
+            if 0 <= d < V and number(u_accept[k]) * (1.0 if draft is None else unit(draft[k, d])) < unit(p[d]):
                 tokens[k + b] = d
                 accepted[b] += 1
                 continue
@@ -81,8 +82,7 @@ def verify(target, draft, draft_tokens, draft_start, u_accept, u_next):
         at = s0 + b + accepted[b]
         if total == 0:
             continue
-        u = min(unit(u_next[b]), 1 - 2.0 ** -24)
-        num, den = u.as_integer_ratio()
+        num, den = number(u_next[b]).as_integer_ratio()
         run = 0
         for j, v in enumerate(w):
             run += v

@@ -61,3 +61,29 @@ def test_lora_prompts_between_rows_without_adapter(env, M, K, N, R, in_place):  
     _check_lora(first, x, base, down, up, ranks, scales, adapter, "f16")
     assert mnb.mnb_last_variant() == "lora_tile_tcgen05"
     mnb.mnb_check_device_status()
+
+
+# What stands for u_accept below 0, at 1 and above, or is not a number, and the probabilities of a token that is accepted, or not, with it:
+# u is held to 0 .. 1 - 2^-24.
+HELD = [(1.0, 0.25, 0.25, True), (2.0, 0.25, 0.25, True), (np.inf, 1.0, 1.0, True), (1.0, 0.25, 0.5, False), (-1.0, 2.0 ** -30, 1.0, True),
+        (np.nan, 2.0 ** -30, 1.0, True), (0.0, 0.0, 0.5, False), (1.0, 1 - 2.0 ** -24, 1.0, False), (-np.inf, 0.0, 0.5, False)]
+
+
+@pytest.mark.parametrize("lookup", [False, True])
+@pytest.mark.parametrize("times", [1, 80])
+def test_verify_holds_u_accept_below_one(env, times, lookup):  # noqa: F811
+    mnb, torch, dev = env
+    held = [h for h in HELD if not lookup or h[2] == 1.0] * times
+    B, V = len(held), 40
+    target, draft = np.zeros((2 * B, V), np.float32), np.zeros((B, V), np.float32)
+    for b, (_, p, q, _) in enumerate(held):
+        target[2 * b, [7, 9]] = p, 1 - p
+        target[2 * b + 1, 11] = 1
+        draft[b, [7, 9]] = q, 1 - q
+    case = (target, None if lookup else draft, np.full(B, 7, np.int32), np.arange(B + 1, dtype=np.int32),
+            np.float32([h[0] for h in held]), np.zeros(B, np.float32))
+    tokens, accepted = (t.cpu().numpy() for t in mnb.mnb_verify(*_up(torch, dev, *case)))
+    np.testing.assert_array_equal(accepted, [h[3] for h in held])
+    want, want_n = orc.verify(*case)
+    np.testing.assert_array_equal(accepted, want_n)
+    np.testing.assert_array_equal(tokens, want)
