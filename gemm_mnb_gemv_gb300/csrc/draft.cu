@@ -648,9 +648,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_part_kernel(const Verif
 }
 
 // The drawn element, from the sums of `runs` runs, and the sequence's tokens. `cta` of the CTAs that call this has the runs `cta` *
-// kVerifyWarps .. when `share` is set (all of them do the same up to there), else the only one has all.
-__device__ __forceinline__ void draw(const Verify& a, int b, int s0, int n, int accepted, const uint64_t* sums, int runs, int run, int cta,
-                                     bool share, float u) {
+// kVerifyWarps .. when `share` is set (all of them do the same up to there), else the only one has all. `sums` are this CTA's alone.
+__device__ __forceinline__ void draw(const Verify& a, int b, int s0, int n, int accepted, uint64_t* sums, int runs, int run, int cta, bool share,
+                                     float u) {
   __shared__ uint64_t of_step[kMostSteps];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, per = (runs + 31) / 32;
   int32_t* out = a.out + s0 + b;
@@ -661,32 +661,37 @@ __device__ __forceinline__ void draw(const Verify& a, int b, int s0, int n, int 
   DrawRow row(a, b, s0, n, accepted);
   uint64_t to = warp_scan(mine, lane), all = shfl_u64(to, 31), limit = scaled(all, u), head = 0;
   int found = -1;
-  if (all > 0) {
-    const int from = __ffs(__ballot_sync(kFull, to > limit)) - 1;  // there is one: limit < all
-    head = shfl_u64(to - mine, from);
-    for (int i = 0; i < per && found < 0; i += 32) {
-      const int at = from * per + i + lane;
-      const uint64_t x = i + lane < per && at < runs ? sums[at] : 0;
+  auto find = [&](int first, int end) {  // among these runs, of which `head` is the sum before
+    for (int i = first; i < end && found < 0; i += 32) {
+      const uint64_t x = i + lane < end ? sums[i + lane] : 0;
       to = head + warp_scan(x, lane);
       const uint32_t past = __ballot_sync(kFull, to > limit);
       if (past) {
-        found = from * per + i + __ffs(past) - 1;
+        found = i + __ffs(past) - 1;
         head = shfl_u64(to - x, __ffs(past) - 1);
       } else {
         head = shfl_u64(to, 31);
       }
     }
-  } else if (row.rejected) {  // nothing left of p - q: drawn from p, whose sums are taken here, by every warp of one CTA alike
+  };
+  if (all > 0) {
+    const int from = __ffs(__ballot_sync(kFull, to > limit)) - 1;  // there is one: limit < all
+    head = shfl_u64(to - mine, from);
+    find(from * per, min((from + 1) * per, runs));
+  } else if (row.rejected) {  // nothing left of p - q: drawn from p, whose sums one CTA takes here
     if (cta != 0) return;
     share = false;
     row.without_draft();
-    for (int i = 0; i < runs; ++i) all += run_sum(row, i * run, min((i + 1) * run, row.chunks));
-    limit = scaled(all, u);
-    for (int i = 0; i < runs && all > 0 && found < 0; ++i) {
+    __syncthreads();  // every warp has read the sums, which are 0
+    for (int i = warp; i < runs; i += kVerifyWarps) {
       const uint64_t x = run_sum(row, i * run, min((i + 1) * run, row.chunks));
-      if (head + x > limit) found = i;
-      else head += x;
+      if (lane == 0) sums[i] = x;
     }
+    __syncthreads();
+    for (int i = lane; i < runs; i += 32) all += sums[i];
+    all = warp_sum(all);
+    limit = scaled(all, u);
+    if (all > 0) find(0, runs);
   }
   if (cta == 0)
     for (int i = tid; i <= n; i += kVerifyThreads)
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
   int s0, n;
   sequence(a, b, s0, n);
   const int accepted = min(max(a.accepted[b], 0), n);  // the first launch's: in range unless the caller's buffers overlap
-  draw(a, b, s0, n, accepted, static_cast<const uint64_t*>(a.workspace) + (int64_t)b * runs, runs, run, 0, false, a.u_next[b]);
+  draw(a, b, s0, n, accepted, static_cast<uint64_t*>(a.workspace) + (int64_t)b * runs, runs, run, 0, false, a.u_next[b]);
 }
 
 // Few sequences: a cluster of CTAs has one, whose sums they hand to each other.

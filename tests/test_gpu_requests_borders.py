@@ -87,3 +87,34 @@ def test_verify_holds_u_accept_below_one(env, times, lookup):  # noqa: F811
     want, want_n = orc.verify(*case)
     np.testing.assert_array_equal(accepted, want_n)
     np.testing.assert_array_equal(tokens, want)
+
+
+@pytest.mark.parametrize("B,V", [(1, 700), (3, 128256), (30, 9001), (70, 33003), (600, 1500), (2, 270001)])
+def test_verify_draws_from_the_target_where_nothing_is_left(env, B, V):  # noqa: F811
+    """A rejected token whose row of the draft is nowhere below the target's: as one with a probability of 0 whose two rows are the same.
+    Rows of zeros among them, from which nothing can be drawn, and rejections with something left."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(B + V)
+    p = rng.random((2 * B, V), dtype=np.float32)
+    p[rng.random((2 * B, V)) < 0.5] = 0
+    p[:, 5] = 0
+    p[:, 6] += 0.1
+    p = (p / p.sum(-1, keepdims=True)).astype(np.float32)
+    draft = p[::2].copy()
+    kinds = np.arange(B) % 5
+    for b in range(B):
+        if kinds[b] == 1:
+            draft[b] *= 1.0 + rng.random(V, dtype=np.float32)     # above the target wherever that is not 0
+        elif kinds[b] == 2:
+            p[2 * b] = 0
+        elif kinds[b] == 3:
+            draft[b] = np.roll(draft[b], 1)
+        elif kinds[b] == 4:
+            draft[b, V - 1], p[2 * b, V - 1] = 0, 2.0 ** -50      # a last element is left
+    case = (p, draft, np.full(B, 5, np.int32), np.arange(B + 1, dtype=np.int32), np.full(B, 0.5, np.float32), rng.random(B, dtype=np.float32))
+    tokens, accepted = (t.cpu().numpy() for t in mnb.mnb_verify(*_up(torch, dev, *case)))
+    want, want_n = orc.verify(*case)
+    np.testing.assert_array_equal(tokens, want)
+    np.testing.assert_array_equal(accepted, want_n)
+    assert not accepted.any() and (tokens[::2][kinds == 2] == -1).all() and (tokens[::2][kinds == 4] == V - 1).all()
+    assert (p[2 * np.arange(B)[kinds < 2], tokens[::2][kinds < 2]] > 0).all()
