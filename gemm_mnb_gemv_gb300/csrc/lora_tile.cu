@@ -755,10 +755,10 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   // A tile in which one prompt ends and the next begins is two items. (Where they are more than thought, a few clusters get two: 1784 rows of four
   // prompts 27 us instead of 21.6 with clusters of 6, which take 21.6 for two prompts, too, instead of 18.8.)
   const int tiles = (a.M + kRows - 1) / kRows;
-  const int pick = tile_cluster(tiles + tiles / 8, room), cluster = pick + 1;
+  const int pick = tile_cluster(tiles + tiles / 8, room), cluster = pick + 1, clusters = room[pick] > 0 ? room[pick] : 1;
   const bool pdl = ctx.pdl;
   ctx.pdl = true;  // it waits for the list on the device
-  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(room[pick] * cluster)), dim3(kThreads), L::kBytes, a, x_map, base_map, maps,
+  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)(clusters * cluster)), dim3(kThreads), L::kBytes, a, x_map, base_map, maps,
                       cluster, (const uint32_t*)list.counts, (const Item*)list.items, ctx.status);
   if (e == cudaSuccess) e = launch_lora_small(ctx, a);
   ctx.pdl = pdl;

@@ -253,7 +253,8 @@ cudaError_t allow_wide_clusters(Kern kernel, int device, std::atomic<uint64_t>& 
   return e;
 }
 
-// Clusters of this kernel that the GPU holds at a time (0: none), asked for once a device: `known` is a static of the caller.
+// Clusters of this kernel that the GPU holds at a time, asked for once a device: `known` is a static of the caller. 0: it holds none, or
+// could not tell, which is asked again and leaves no error behind for the launches that follow.
 template <typename Kern>
 int clusters_held(const LaunchCtx& ctx, Kern kernel, int cluster, int threads, size_t smem, std::atomic<int> (&known)[64]) {
   int n = ctx.device < 64 ? known[ctx.device].load(std::memory_order_relaxed) : 0;
@@ -269,7 +270,10 @@ int clusters_held(const LaunchCtx& ctx, Kern kernel, int cluster, int threads, s
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
   if (ctx.device < 64) known[ctx.device].store(n + 1, std::memory_order_relaxed);
   return n;
 }
