@@ -787,7 +787,7 @@ def _two_dims(name, t, what):
 
 def _matrix(name, t, shape, dtype, guard):
     """Elements between the rows of a CUDA tensor of this type and shape whose rows are contiguous."""
-    if t is None or t.dtype != dtype or not t.is_cuda or guard is not None:
+    if getattr(t, "dtype", None) != dtype or not t.is_cuda or guard is not None:
         _on(name, t, dtype, guard)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -799,7 +799,7 @@ def _matrix(name, t, shape, dtype, guard):
 
 def _vector(name, t, dtype, shape, guard):
     """Address of a contiguous CUDA tensor of this type and shape."""
-    if t is None or t.dtype != dtype or not t.is_cuda or guard is not None:
+    if getattr(t, "dtype", None) != dtype or not t.is_cuda or guard is not None:
         _on(name, t, dtype, guard)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -893,6 +893,8 @@ def mnb_lora(x, pool: MnbLoraPool, adapter, base=None, workspace=None, out=None,
     """``[M, N]`` = ``base`` (None: zeros) + each row's adapter on ``x`` ``[M, K]``; ``adapter`` int32 ``[M]``, -1 for none.
     ``out`` may be ``base``.  A workspace is shared or allocated as in ``mnb_kv4_attention``."""
     torch = _torch_module or _torch()
+    if not isinstance(pool, MnbLoraPool):
+        raise TypeError(f"pool must be an MnbLoraPool, got {type(pool).__name__}")
     dev, guard, K, N = pool.device, pool.guard, pool.K, pool.N
     if type(x) is not torch.Tensor or not x.is_cuda or x.dim() != 2:
         _two_dims("x", x, f"[M, {K}]")

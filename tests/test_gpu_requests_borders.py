@@ -118,3 +118,33 @@ def test_verify_draws_from_the_target_where_nothing_is_left(env, B, V):  # noqa:
     np.testing.assert_array_equal(accepted, want_n)
     assert not accepted.any() and (tokens[::2][kinds == 2] == -1).all() and (tokens[::2][kinds == 4] == V - 1).all()
     assert (p[2 * np.arange(B)[kinds < 2], tokens[::2][kinds < 2]] > 0).all()
+
+
+def test_bindings_refuse_what_is_no_tensor(env):  # noqa: F811
+    mnb, torch, dev = env
+    h, i32 = dict(dtype=torch.float16, device=dev), dict(dtype=torch.int32, device=dev)
+    down, up = torch.zeros(2, 8, 32, **h), torch.zeros(2, 12, 8, **h)
+    pool, x, idx = mnb.MnbLoraPool(down, up), torch.zeros(3, 32, **h), torch.zeros(3, **i32)
+    p, q = torch.zeros(5, 9, device=dev), torch.zeros(3, 9, device=dev)
+    start, u, v = torch.zeros(3, **i32), torch.zeros(3, device=dev), torch.zeros(2, device=dev)
+    for wrong in ([0, 0, 0], (1.0,), 7, np.zeros(3, np.float32)):
+        cases = {
+            "pool": lambda: mnb.mnb_lora(x, wrong, idx),
+            "x": lambda: mnb.mnb_lora(wrong, pool, idx),
+            "adapter": lambda: mnb.mnb_lora(x, pool, wrong),
+            "base": lambda: mnb.mnb_lora(x, pool, idx, base=wrong),
+            "out": lambda: mnb.mnb_lora(x, pool, idx, out=wrong),
+            "ranks": lambda: mnb.MnbLoraPool(down, up, ranks=wrong),
+            "scales": lambda: mnb.MnbLoraPool(down, up, scales=wrong),
+            "workspace": lambda: mnb.mnb_lora(x, pool, idx, workspace=wrong),
+            "logits": lambda: mnb.mnb_softmax(wrong),
+            "temperature": lambda: mnb.mnb_softmax(x, temperature=wrong),
+            "draft": lambda: mnb.mnb_verify(p, wrong, idx, start, u, v),
+            "draft_start": lambda: mnb.mnb_verify(p, q, idx, wrong, u, v),
+            "u_accept": lambda: mnb.mnb_verify(p, q, idx, start, wrong, v),
+            "tokens": lambda: mnb.mnb_verify(p, q, idx, start, u, v, tokens=wrong),
+            "accepted": lambda: mnb.mnb_verify(p, q, idx, start, u, v, accepted=wrong),
+        }
+        for name, call in cases.items():
+            with pytest.raises(TypeError, match=f"^{name} must be a"):
+                call()

@@ -65,3 +65,17 @@ def test_unknown_occupancy_leaves_no_error(tmp_path):
     assert made.returncode == 0, made.stderr
     ran = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert ran.stdout.split() == ["0", "0", "19", "19"], ran.stdout + ran.stderr
+
+
+def test_arguments_that_are_no_tensors_are_named():
+    import torch
+
+    import gemm_mnb_gemv_gb300 as mnb
+    for pool in ((1, 2), None, torch.zeros(1)):
+        with pytest.raises(TypeError, match="pool must be an MnbLoraPool"):
+            mnb.mnb_lora(None, pool, None)
+    for wrong in ([0, 1], (0.5,), 3, "x", None, np.zeros(2, np.float32), torch.zeros(2)):
+        with pytest.raises(TypeError, match="temperature must be a CUDA tensor"):
+            mnb._vector("temperature", wrong, torch.float32, (2,), None)
+        with pytest.raises(TypeError, match="base must be a CUDA tensor"):
+            mnb._matrix("base", wrong, (2, 1), torch.float32, None)
