@@ -648,7 +648,7 @@ mnb_status mnb_gemm_act_order_noalloc(const void* A, int M, mnb_weight w, const 
 namespace {
 
 // A call of several launches has its workspace from the first to the last: calls of several host threads on one stream with one
-// workspace, of whatever kind, have to come one after the other.
+// workspace, of whatever kind, have to come one after the other. (Calls that need none go past it.)
 std::mutex g_two_launches;
 
 bool kv4_geometry_ok(int num_pages, int page_size, int kv_heads, int head_dim, int group) {
@@ -949,12 +949,14 @@ mnb_status mnb_verify(const float* target, int64_t target_stride, const float* d
   if ((st = check_ptr(fn, "accepted", accepted)) != MNB_OK) return st;
   if ((int64_t)batch * V > (int64_t)1 << 42)
     return fail(MNB_ERR_UNSUPPORTED, "%s: batch=%d rows of V=%d are more than one launch takes", fn, batch, V);
-  if ((st = check_workspace(fn, workspace, ws_bytes, mnb_verify_workspace_bytes(batch, V))) != MNB_OK) return st;
+  const size_t need = mnb_verify_workspace_bytes(batch, V);
+  if ((st = check_workspace(fn, workspace, ws_bytes, need)) != MNB_OK) return st;
   mnb::LaunchCtx ctx;
   if ((st = make_ctx(fn, stream, &ctx)) != MNB_OK) return st;
   const mnb::Verify a = {target, target_stride, draft, draft_stride, draft_tokens, draft_start, u_accept,
                          u_next, batch,         drafted, V,          tokens,       accepted, workspace};
-  std::lock_guard<std::mutex> lock(g_two_launches);
+  std::unique_lock<std::mutex> lock(g_two_launches, std::defer_lock);
+  if (need > 0) lock.lock();
   return finish(fn, mnb::launch_verify(ctx, a), ctx);
 }
 

@@ -148,3 +148,30 @@ def test_bindings_refuse_what_is_no_tensor(env):  # noqa: F811
         for name, call in cases.items():
             with pytest.raises(TypeError, match=f"^{name} must be a"):
                 call()
+
+
+def test_threads_on_streams_of_their_own(env):  # noqa: F811
+    """Calls of one launch and of several, of six host threads that each have a stream: they may overlap as they like."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    from tests.test_gpu_requests import _draft_case
+    mnb, torch, dev = env
+    rng = np.random.default_rng(17)
+    kinds = [_up(torch, dev, *_draft_case(rng, B, V, 3, lookup)) for B, V, lookup in ((2, 5003, False), (7, 2000, True), (600, 900, True))]
+    logits = [torch.randn(rows, V, device=dev) for rows, V in ((3, 1000), (2, 40000), (130, 20000))]
+    forms = [lambda c=c: mnb.mnb_verify(*c) for c in kinds] + [lambda x=x: (mnb.mnb_softmax(x),) for x in logits]
+    wants = [f() for f in forms]
+    torch.cuda.synchronize()
+
+    def work(f):
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            outs = [f() for _ in range(100)]
+        side.synchronize()
+        return outs
+
+    with ThreadPoolExecutor(len(forms)) as threads:
+        results = list(threads.map(work, forms))
+    for outs, want in zip(results, wants):
+        assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))
+    mnb.mnb_check_device_status()
