@@ -40,6 +40,18 @@ __device__ __noinline__ LooseRows<kWords> loose_rows(const T* base, int64_t at0,
   return r;
 }
 
+// Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first
+// (132 rows of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 8.0).
+constexpr int kFewRows = 256;
+// Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
+// much less often but fill the GPU later. fp16, four prompts, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 14.8 / 18.3 at 1000 rows, 20.9 /
+// 18.4 at 1200; rank 64 17.7 / 19.9 at 700 and 20.3 / 19.8 at 1000; rank 128 29.8 / 22.1 at 272 and 56 / 23 at 800. fp32, tiles of 16 / of 64: rank 32
+// 23.7 / 24.2 at 1000 and 27.6 / 26.9 at 1400; rank 128 36.1 / 32.6 at 272.
+constexpr int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
+// Whether calls of this kind of tile take a list: those of 16 rows and ranks above 64 have no more rows than need none, and in fp16 only the
+// launch for small items.
+constexpr bool takes_list(int RB, int WM) { return WM > 1 || tile_rows(8 * RB) > kFewRows; }
+
 // RB: ranks in eights; WM: row tiles of 16.
 template <int RB, int WM, bool F32>
 struct Geo {
@@ -93,6 +105,7 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
     lora_kernel(const Lora a, int cluster, int subs, const uint32_t* counts, const Item* list, int capacity, int small_only, uint32_t* status) {
   using T = std::conditional_t<F32, float, __half>;
   using L = Geo<RB, WM, F32>;
+  if constexpr (F32 && !takes_list(RB, WM)) list = nullptr;
   constexpr int RP = L::RP, TM = L::TM, WN = L::WN, S = L::kStages, kThreads = L::kThreads;
   constexpr int E = RB >= 4 ? 8 : RB == 2 ? 4 : 2;  // elements of the rank that a lane has of a chunk of 4 E
   constexpr int KC = RP / (4 * E);
@@ -544,15 +557,6 @@ __global__ void __launch_bounds__(Geo<RB, WM, F32>::kThreads, Geo<RB, WM, F32>::
   if (list) pdl_wait();  // who waits for this kernel waits for the one before it too
 }
 
-// Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first
-// (132 rows of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 8.0).
-constexpr int kFewRows = 256;
-// Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
-// much less often but fill the GPU later. fp16, four prompts, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 14.8 / 18.3 at 1000 rows, 20.9 /
-// 18.4 at 1200; rank 64 17.7 / 19.9 at 700 and 20.3 / 19.8 at 1000; rank 128 29.8 / 22.1 at 272 and 56 / 23 at 800. fp32, tiles of 16 / of 64: rank 32
-// 23.7 / 24.2 at 1000 and 27.6 / 26.9 at 1400; rank 128 36.1 / 32.6 at 272.
-int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
-
 template <int RB, int WM, bool F32>
 cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   using L = Geo<RB, WM, F32>;
@@ -563,7 +567,7 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
   cudaError_t e = allow_smem(kern, L::kBytes, ctx.device, sized);
   if (e == cudaSuccess && cluster > 8) e = allow_wide_clusters(kern, ctx.device, wide);
   if (e != cudaSuccess) return e;
-  if (WM == 1 && a.M <= kFewRows) {
+  if (!takes_list(RB, WM) || (WM == 1 && a.M <= kFewRows)) {
     // A cluster for each adapter that a tile can have, as long as the GPU holds about that many: clusters without one cost their
     // start, adapters that share one come after each other.
     const int most = a.M < 16 ? a.M : 16, some = 8 * 16 / tiles;
@@ -571,16 +575,18 @@ cudaError_t launch_lora_t(LaunchCtx& ctx, const Lora& a) {
     return launch_clusters(ctx, kern, cluster, dim3((unsigned)(tiles * subs * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, subs,
                            (const uint32_t*)nullptr, (const Item*)nullptr, 0, 0, ctx.status);
   }
-  const List list(a.workspace);
-  e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, 1, list.counts, list.items, a.M, ctx.status);
-  if (e != cudaSuccess) return e;
-  const bool pdl = ctx.pdl;
-  ctx.pdl = true;  // it waits for the list on the device
-  static std::atomic<int> known[64];
-  const int room = clusters_held(ctx, kern, cluster, L::kThreads, L::kBytes, known);
-  e = launch_clusters(ctx, kern, cluster, dim3((unsigned)((room > 0 ? room : 1) * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
-                      (const uint32_t*)list.counts, (const Item*)list.items, a.M, 0, ctx.status);
-  ctx.pdl = pdl;
+  if constexpr (takes_list(RB, WM)) {
+    const List list(a.workspace);
+    e = launch_kernel(ctx, list_kernel<L::TM>, dim3(1), dim3(1024), 0, a, L::TM / 2, 1, list.counts, list.items, a.M, ctx.status);
+    if (e != cudaSuccess) return e;
+    const bool pdl = ctx.pdl;
+    ctx.pdl = true;  // it waits for the list on the device
+    static std::atomic<int> known[64];
+    const int room = clusters_held(ctx, kern, cluster, L::kThreads, L::kBytes, known);
+    e = launch_clusters(ctx, kern, cluster, dim3((unsigned)((room > 0 ? room : 1) * cluster)), dim3(L::kThreads), L::kBytes, a, cluster, 1,
+                        (const uint32_t*)list.counts, (const Item*)list.items, a.M, 0, ctx.status);
+    ctx.pdl = pdl;
+  }
   return e;
 }
 
