@@ -33,6 +33,7 @@ constexpr int kBatch = 4;          // chunks of a thread in flight
 constexpr int kPartThreads = 256;  // of a row's part
 constexpr int kNone = 0x7fffffff;
 constexpr int kMostCluster = 16, kClusterThreads = 512;
+constexpr float kLeastC = 1.0f / (1ull << 63) / (1ull << 63) / (1 << 23);  // 2^-149: logits differ by less than 2^129, so this is no temperature at all
 
 struct SoftPart {  // of a part: largest, sum of the exponentials relative to it, first place of the largest
   float m, s;
@@ -51,6 +52,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 __device__ __forceinline__ float some(float m) { return m == -INFINITY ? 0.0f : m; }  // what logits are taken relative to
+// The factor that brings sums relative to m to `ref`; halves, as the difference of two finite ones may be none.
+__device__ __forceinline__ float rescale(float m, float ref, float c) { return ex2((0.5f * m - 0.5f * ref) * c * 2.0f); }
 struct Base;
 
 // Eight logits as they lie.
@@ -112,12 +115,13 @@ struct SoftRow {
   const Softmax& a;
   int64_t in_at, out_at;
   int skew, chunks;  // chunk i is the elements 8 i - skew ..
-  float temp, c;     // c: 1 / temperature in powers of two, within what keeps 0 * c at 0 and -inf * c at -inf; NaN for no temperature
+  float temp, c;     // c: 1 / temperature in powers of two, within what keeps 0 * c at 0 and -inf * c at -inf (subnormal for the largest
+                     // temperatures, the smallest one for an infinite one); NaN for no temperature
   __device__ __forceinline__ SoftRow(const Softmax& a_, int r) : a(a_), in_at((int64_t)r * a_.stride), out_at((int64_t)r * a_.V) {
     skew = (int)(in_at % 8);
     chunks = (a.V + skew + 7) / 8;
     temp = a.temperature ? __ldcg(a.temperature + r) : 1.0f;
-    c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), FLT_MIN) : temp == 0.0f ? 1.0f : NAN;
+    c = temp > 0.0f ? fmaxf(fminf(1.4426950408889634f / temp, FLT_MAX), kLeastC) : temp == 0.0f ? 1.0f : NAN;
   }
   // Whether chunks i0 .. i1 - 1 lie within the row, and its probabilities at 32 bytes.
   __device__ __forceinline__ bool whole(int i0, int i1) const {
@@ -189,7 +193,7 @@ struct SoftRow {
 __device__ __forceinline__ SoftPart join(const SoftPart& a, const SoftPart& b, float c) {
   SoftPart r = {nan_max(a.m, b.m), 0.0f, kNone, 0};
   const float ref = some(r.m);
-  r.s = a.s * ex2((a.m - ref) * c) + b.s * ex2((b.m - ref) * c);
+  r.s = a.s * rescale(a.m, ref, c) + b.s * rescale(b.m, ref, c);
   r.at = a.m > b.m ? a.at : b.m > a.m ? b.at : min(a.at, b.at);
   return r;
 }
@@ -214,7 +218,7 @@ __device__ __forceinline__ SoftPart cta_join(SoftPart r, float temp, float c) {
   if (temp == 0.0f) {
     r.at = __reduce_min_sync(kFull, r.m == top ? r.at : kNone);
   } else {
-    r.s *= ex2((r.m - some(top)) * c);
+    r.s *= rescale(r.m, some(top), c);
 #pragma unroll
     for (int o = 16; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
   }
@@ -227,7 +231,7 @@ __device__ __forceinline__ SoftPart cta_join(SoftPart r, float temp, float c) {
   if (temp == 0.0f) {
     r.at = __reduce_min_sync(kFull, r.m == top ? at[lane % kWarps] : kNone);
   } else {
-    r.s = s[lane % kWarps] * ex2((r.m - some(top)) * c);
+    r.s = s[lane % kWarps] * rescale(r.m, some(top), c);
 #pragma unroll
     for (int o = kWarps / 2; o; o >>= 1) r.s += __shfl_xor_sync(kFull, r.s, o);
   }
@@ -261,7 +265,7 @@ __device__ __forceinline__ void take(const SoftRow<F32>& row, const Chunk<F32> (
   } else {
     const Base base(m, row.c);
     const float sum = base.plain ? batch_sum<F32, kThreads, true>(v, base) : batch_sum<F32, kThreads, false>(v, base);
-    r.s = r.s * ex2((r.m - base.m) * row.c) + sum;
+    r.s = r.s * rescale(r.m, base.m, row.c) + sum;
   }
   r.m = m;
 }

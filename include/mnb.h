@@ -470,7 +470,7 @@ MNB_API mnb_status mnb_lora(const void *x, int dtype, int M, int K, int64_t x_st
  * Probabilities: out[r, j] = e^((x[r, j] - max_j x) / temperature[r]) / sum_j, fp32 [rows, V], contiguous. logits x [rows, V]
  * are of `dtype` (MNB_F16 or MNB_F32), rows `stride` elements apart; out may be logits (MNB_F32, stride V), and may not overlap
  * them otherwise. temperature is fp32 [rows], NULL for 1; a row of
- * temperature 0 gets 1 at its largest logit (the first of equal ones) and 0 elsewhere. Masked logits are -inf: a row of
+ * temperature 0 gets 1 at its largest logit (the first of equal ones) and 0 elsewhere, one of an infinite temperature the same for all finite ones. Masked logits are -inf: a row of
  * nothing else gets zeros. A NaN or (unless the temperature is 0) +inf logit, and a temperature that is negative or NaN, make the row
  * NaN. `workspace` holds mnb_softmax_workspace_bytes(rows, V) bytes (0 for V up to 16377, and for few
  * rows), under the rules of mnb_lora's; more than 2^42 elements give MNB_ERR_UNSUPPORTED. rows = 0 is valid and does nothing.

@@ -175,3 +175,20 @@ def test_threads_on_streams_of_their_own(env):  # noqa: F811
     for outs, want in zip(results, wants):
         assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))
     mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("rows,V", [(6, 9), (12, 1003), (6, 16377), (6, 70001), (60, 40001)])
+def test_softmax_of_the_largest_temperatures(env, rows, V):  # noqa: F811
+    """Logits as large as fp32 holds, at temperatures that bring them to an ordinary range, or beyond it to the same for all. (1 / T is
+    subnormal from 2^126 on: up to 3 more last places of z, which the tolerance's 80 cover, as z is 6 at most.)"""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(V)
+    x = (rng.uniform(-1, 1, (rows, V)) * 3.4e38).astype(np.float32)
+    x[1, :V // 2] = -3.4e38
+    x[2] = np.sort(x[2])
+    t = np.resize(np.float32([np.inf, 3.4e38, 1.5e38, 1.2e38, np.inf, 5e37]), rows)
+    xd, td = _up(torch, dev, x, t)
+    from tests.test_gpu_requests import _check_softmax
+    got = mnb.mnb_softmax(xd, temperature=td)
+    _check_softmax(got, x, t)
+    np.testing.assert_allclose(got[0].cpu().numpy() * V, 1, rtol=(V / 512 + 100) * 2.0 ** -24)
