@@ -156,7 +156,7 @@ mnb_status mnb_check_device_status(void) {
                 "call are NaN", fn, v);
   return fail(MNB_ERR_INVALID_ARG, "%s: an index input was out of range (status bits 0x%x: a g_idx, perm "
               "or block_group entry outside its range; that element was written as 0; or a slot, position, page "
-              "or kv_len of a key/value cache call: see the call)", fn, v);
+              "or kv_len of a key/value cache call, an adapter of mnb_lora or a drafted token of mnb_verify: see the call)", fn, v);
 }
 
 mnb_status mnb_selftest_wait_timeout(unsigned int limit_us, mnb_stream stream) {

@@ -192,3 +192,78 @@ def test_softmax_of_the_largest_temperatures(env, rows, V):  # noqa: F811
     got = mnb.mnb_softmax(xd, temperature=td)
     _check_softmax(got, x, t)
     np.testing.assert_allclose(got[0].cpu().numpy() * V, 1, rtol=(V / 512 + 100) * 2.0 ** -24)
+
+
+def _runs(M, count):
+    """Adapters of long runs of rows, and of single rows at the end."""
+    adapter = (np.arange(M) * 3 // M % count).astype(np.int32)
+    tail = min(M // 4, 40)
+    adapter[M - tail:] = np.arange(tail) % count
+    return adapter
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("M", [20, 300, 1600, 2500])
+def test_lora_bad_indices_wherever_they_are(env, M, dtype):  # noqa: F811
+    """At the first row of a tile, whose adapter the clusters look at themselves, within runs and among single rows."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(M)
+    x, base, down, up, _, scales, _ = _lora_inputs(rng, M, 64, 136, 16, 4, dtype)
+    adapter = _runs(M, 4)
+    for first in (0, 128, 5 * 128, 64 * 3, M - 3, 7, M // 2 + 1):
+        if first < M:
+            adapter[first] = rng.choice(np.int32([4, 2 ** 31 - 1, 1 << 20]))
+    if M > 1000:
+        adapter[1024:1152] = 5  # a whole tile
+    adapter[[3, M // 2]] = -2 ** 31, -7
+    xd, bd, dd, ud, sd, ad = _up(torch, dev, x, base, down, up, scales, adapter)
+    pool = mnb.MnbLoraPool(dd, ud, scales=sd)
+    mnb.mnb_check_device_status()
+    got = mnb.mnb_lora(xd, pool, ad, base=bd)
+    with pytest.raises(mnb.MnbError, match="INVALID_ARG.*an adapter of mnb_lora"):
+        mnb.mnb_check_device_status()
+    _check_lora(got, x, base, down, up, None, scales, adapter, dtype)
+    again = bd.clone()
+    mnb.mnb_lora(xd, pool, ad, base=again, out=again)
+    assert torch.equal(again, got)
+    with pytest.raises(mnb.MnbError, match="INVALID_ARG"):
+        mnb.mnb_check_device_status()
+    none = mnb.mnb_lora(xd, pool, ad)
+    _check_lora(none, x, None, down, up, None, scales, adapter, dtype)
+    assert not none.cpu().numpy()[(adapter < 0) | (adapter > 3)].any()
+    good = np.where(adapter > 3, -1, adapter)
+    with pytest.raises(mnb.MnbError, match="INVALID_ARG"):
+        mnb.mnb_check_device_status()
+    assert torch.equal(mnb.mnb_lora(xd, pool, torch.from_numpy(good).to(dev), base=bd), got)
+    mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("R", [16, 40, 128])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("M", [20, 300, 1600, 2500])
+def test_lora_rows_of_any_size_beside_each_other(env, M, dtype, R):  # noqa: F811
+    """Rows from the smallest to the largest keep their precision, and one with inf or NaN stays alone: in runs and among single rows."""
+    mnb, torch, dev = env
+    rng = np.random.default_rng(M + R)
+    sizes = {"f16": [1e-7, 1e-3, 1.0, 1e4], "f32": [1e-30, 1e-3, 1.0, 1e30]}[dtype]
+    x, base, down, up, _, scales, _ = _lora_inputs(rng, M, 96, 72, R, 3, dtype, without=0)
+    adapter = _runs(M, 3)
+    x = (x.astype(np.float64) * np.resize(sizes, M)[:, None]).astype(x.dtype)
+    base *= 0
+    if dtype == "f16":  # s beyond fp16
+        down[0] *= np.float16(300)
+        scales *= np.float32(1e-4)
+    xd, bd, dd, ud, sd, ad = _up(torch, dev, x, base, down, up, scales, adapter)
+    pool = mnb.MnbLoraPool(dd, ud, scales=sd)
+    got = mnb.mnb_lora(xd, pool, ad, base=bd)
+    _check_lora(got, x, base, down, up, None, scales, adapter, dtype)
+    rows = [4, 9, M // 2, M // 2 + 1, M - 9, M - 2]
+    bad = xd.clone()
+    for i, r in enumerate(rows):
+        bad[r, (3, 60, 95)[i % 3]] = (float("inf"), float("nan"), -float("inf"))[i // 2]
+    odd = mnb.mnb_lora(bad, pool, ad, base=bd)
+    keep = torch.ones(M, dtype=torch.bool, device=dev)
+    keep[rows] = False
+    assert torch.equal(odd[keep], got[keep])
+    assert not torch.isfinite(odd[rows]).any()
+    mnb.mnb_check_device_status()
