@@ -50,7 +50,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float2 half2_floats(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 __device__ __forceinline__ float some(float m) { return m == -INFINITY ? 0.0f : m; }  // what logits are taken relative to
 // The factor that brings sums relative to m to `ref`; halves, as the difference of two finite ones may be none.
 __device__ __forceinline__ float rescale(float m, float ref, float c) { return ex2((0.5f * m - 0.5f * ref) * c * 2.0f); }

@@ -11,9 +11,6 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float2 half2_floats(uint32_t u) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
 
 // Two fp32 as fp16 pairs: hi + lo is within 2^-22 of them.
 struct Split {
