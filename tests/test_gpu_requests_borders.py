@@ -267,3 +267,24 @@ def test_lora_rows_of_any_size_beside_each_other(env, M, dtype, R):  # noqa: F81
     assert torch.equal(odd[keep], got[keep])
     assert not torch.isfinite(odd[rows]).any()
     mnb.mnb_check_device_status()
+
+
+@pytest.mark.parametrize("R", [24, 64, 104, 128])
+@pytest.mark.parametrize("tiles", [10, 19, 20, 23, 28, 33, 42, 56, 70, 140])
+def test_lora_prompts_of_every_length(env, tiles, R):  # noqa: F811
+    """As many tiles as make the tensor cores' kernel take clusters of 8, 7, 6, 5, 4, 3, 2 and 1 CTAs, whose shares of the exchange differ;
+    the last tile is not full."""
+    mnb, torch, dev = env
+    M, K, N = tiles * 128 - 37, 272, 328
+    rng = np.random.default_rng(tiles + R)
+    x, base, down, up, _, scales, adapter = _lora_inputs(rng, M, K, N, R, 3, "f16", without=0)
+    adapter[:] = np.arange(M) * 3 // M
+    xd, bd, dd, ud, sd, ad = _up(torch, dev, x, base, down, up, scales, adapter)
+    got = mnb.mnb_lora(xd, mnb.MnbLoraPool(dd, ud, scales=sd), ad, base=bd)
+    assert mnb.mnb_last_variant() == "lora_tile_tcgen05"
+    # s as two parts: what _check_lora allows for one is out of the way
+    want, a, b = orc.lora(x, down, up, None, scales, adapter, base)
+    tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + 2.0 ** -22 * a + (K / 8 + 2 * R + 64) * 2.0 ** -23 * b
+    err = np.abs(got.cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
+    mnb.mnb_check_device_status()
