@@ -7,8 +7,9 @@
 // Softmax, bound: 320 x 128256 fp16 with temperatures, 50 us (36 at the copy rate). The first launch takes 16 us, most of it
 // arithmetic (70% of the issue slots); the second reads the logits again, about half of them from L2, and writes at the memory's rate (7 TB/s).
 // One row: 4.8 us, launch and cluster.
-// Verification, bound: 64 x 4 drafted tokens x 128256, 14.9 us (8.9): three loads that follow each other to the accepted length, then one row
-// of p and q at half the copy rate, the cluster, the element. One sequence: 6.2 us.
+// Verification, bound: 64 x 4 drafted tokens x 128256, 15.0 us (8.9): three loads that follow each other to the accepted length, then one row
+// of p and q at half the copy rate, the cluster, the element. One sequence: 6.2 us. Where nothing is left of p - q, one CTA reads the row again: 21 us
+// for one sequence, 50 for 64 that all do.
 #include <float.h>
 
 #include "cluster.cuh"
@@ -424,10 +425,11 @@ __global__ void __launch_bounds__(kPartThreads) softmax_join_kernel(const Softma
 }
 
 // CTAs of a cluster that has a row in registers, 0: no clusters. One launch saves 3 us of host time, and up to 256 CTAs GPU time too; more
-// clusters than the GPU starts at once do not, nor pairs that are more than one CTA an SM. Fewer CTAs a row where they are more than 128. fp16, us
-// with clusters / in two launches: 128256 logits a row: 1 row 4.8 / 4.9, 8 rows 5.5 / 7.0, 32 rows 7.8 / 8.2, 40 rows 10.2 / 9.8; 65000 logits: 64 rows
-// 7.5 / 8.6; 32003 logits: 32 rows 5.7 / 6.8, 64 rows 7.0 / 7.8, 85 rows (pairs) 8.9 / 8.5. Of 16 CTAs instead of 8: 4 rows of 128256 5.0 / 5.4, 8
-// rows 6.0 / 5.6.
+// clusters than the GPU starts at once do not, nor (up to 100 rows) pairs that are more than one CTA an SM. Fewer CTAs a row where they are more than
+// 128. fp16, us with clusters / in two launches: 128256 logits a row: 1 row 4.7 / 4.5, 4 rows 4.7 / 5.2, 8 rows 5.4 / 6.5, 32 rows 7.4 / 7.8, 40 rows
+// 9.9 / 9.4; 65000 logits: 32 rows 5.6 / 6.6, 64 rows 7.1 / 8.2, 85 rows 10.1 / 10.0; 32003 logits: 32 rows 5.5 / 6.4, 64 rows 6.6 / 7.4, 85 rows (pairs)
+// 8.7 / 8.3 and in fp32 9.3 / 7.9, 128 rows 9.0 / 11.2 and in fp32 9.7 / 10.9 (not taken: 152 CTAs are the border). Clusters of 16 / of 8: 4 rows of
+// 128256 4.7 / 5.3, 8 rows 6.0 / 5.4.
 int soft_cluster(int rows, int V) {
   const int chunks = (V + 14) / 8;
   auto fits = [&](int cluster) { return chunks <= cluster * kClusterThreads * kBatch; };
@@ -780,8 +782,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_cluster_kernel(const Ve
 
 // CTAs of a cluster that has a sequence, 0: two launches. As many as give a warp a run of 64 chunks; fewer, with runs of up to 256, where
 // that is more than a CTA for each SM, and of up to 512 where it is more than 512 in all. us with clusters / in two launches, 4 drafted tokens a
-// sequence (a call takes 4 us less of host time besides): V 128256: 1 sequence 6.7 / 8.2, 16 9.2 / 9.6, 64 15.5 / 17.1, 100 24.9 / 23.4 (800 CTAs); V
-// 32003: 8 6.5 / 6.9, 100 10.5 / 12.3.
+// sequence, all accepted (a call takes 4 us less of host time besides): V 128256: 1 sequence 6.0 / 7.7, 8 7.1 / 9.6, 32 9.3 / 9.3, 64 11.1 / 11.3, 76 (608
+// CTAs) 14.3 / 11.3, 100 16.7 / 14.3; V 151936, whose runs fit clusters of 16 alone: 8 7.7 / 8.6, 32 10.2 / 9.3; V 32003: 1 5.3 / 6.5, 64 7.8 / 8.4, 100 8.8 /
+// 9.7, 200 11.4 / 11.7. With rows of q to subtract: V 128256: 64 14.0 / 14.4, 72 14.1 / 15.5, 80 16.8 / 16.7, 96 20.5 / 18.3.
 int verify_cluster(int batch, int V) {
   const int chunks = (V + 6) / 4;
   int c = kMostCluster;

@@ -12,10 +12,12 @@
 // s is held as two fp16 after its row was scaled by a power of two to [2^13, 2^14), and up takes both: 22 bits of s. fp32: x, too, as two
 // fp16, of the scale of the 32 elements that a granule of K has of a row; each is multiplied on its own and the granule's scale put
 // back in fp32 (2^-22; two tf32 parts took twice the instructions at half their rate).
-// Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 14.7 us, 2.7 of them
-// bytes at the copy rate: about 2150 instructions a warp at 7 cycles each, 12 warps an SM (registers allow 16). Weights straight from
-// memory to the products' registers, without the ring: 22 us (half of each line at a time, and spills); a ring for each warp,
-// without barriers: the same.  One row of rank 16: 5.9 us, the chain of launch, adapter, K, cluster, N.
+// Bound: what a warp has to issue, one after the other. 64 rows of 48 adapters of up to 64 ranks, K = N = 4096, take 15.5 us, 2.7 of them
+// bytes at the copy rate. By the clock: 2 to find the adapter, 4 for the first product, 2 for its sums, 4 for the second product, the last CTAs 2.5
+// later, 1 from launch to launch; in the 10 us of its products a warp issues about 2860 instructions, 7 cycles each (12 warps an SM,
+// registers allow 16). With one part of s instead of two: 14.7. Weights straight from memory to the products' registers, without the
+// ring: 22 us against 14.7 (half of each line at a time, and spills); a ring for each warp, without barriers: the same.  One row of rank 16: 6.1
+// us, a chain: adapter 1.2, first product 1.4, its sums 1.4, second product 1.3, launch to launch 0.8.
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -40,13 +42,20 @@ __device__ __noinline__ LooseRows<kWords> loose_rows(const T* base, int64_t at0,
   return r;
 }
 
-// Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first
-// (132 rows of 33 requests: 7.9 us without, 8.1 with; 803 rows of three prompts and 8 more: 13.4 and 8.0).
+// Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first.
+// On the GPU, without a list / with one: 64 rows of 64 adapters, 4096 x 4096, rank 16 9.7 / 11.0, 132 rows of them 22.9 / 17.3; fp32, four rows a
+// request, 896 x 1152, rank 8: 64 rows 6.5 / 7.5, 132 8.2 / 7.6, 256 10.0 / 8.0; 803 rows of three prompts and 8 more, 1680 x 192: 14.1 / 7.9. A
+// call without one has one launch and no workspace, 3 us less of host time: eager calls are even up to 256, replayed ones of more than 130 rows would
+// be faster with a list.
 constexpr int kFewRows = 256;
 // Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
-// much less often but fill the GPU later. fp16, four prompts, K = N = 4096, us in tiles of 16 / on the tcgen05 kernel: rank 32 14.8 / 18.3 at 1000 rows, 20.9 /
-// 18.4 at 1200; rank 64 17.7 / 19.9 at 700 and 20.3 / 19.8 at 1000; rank 128 29.8 / 22.1 at 272 and 56 / 23 at 800. fp32, tiles of 16 / of 64: rank 32
-// 23.7 / 24.2 at 1000 and 27.6 / 26.9 at 1400; rank 128 36.1 / 32.6 at 272.
+// much less often but fill the GPU later; a GPU holds 74 clusters, the tiles of 1184 rows. Four prompts, us in tiles of 16 / in the large ones:
+//   fp16, K = N = 4096: rank 16 12.4 / 18.3 at 1152 rows, 18.7 / 18.3 at 1536; rank 32 15.4 / 18.7 and 23.0 / 18.9; rank 64 18.4 / 20.2 at 768, 21.1 / 20.2 at
+//   1024; rank 128 32 / 25 at 272, 61 / 25 at 768. 4096 x 14336: rank 32 26.8 / 31.9 at 1152, 42 / 34 at 1536; rank 64 31.5 / 34.1 at 768, 37.1 / 33.9 at 1024.
+//   1024 x 1024, where a launch counts for more: rank 64 13.7 / 14.3 at 1024, 19.4 / 14.9 at 1536.
+//   fp32, K = N = 4096: rank 32 25.5 / 26.7 at 1152, 28.0 / 26.9 at 1536; rank 64 17.5 / 24.8 at 512, 28.6 / 24.9 at 768; rank 128 35.8 / 32.2 at 272. 4096 x
+//   14336: rank 64 50.5 / 51.8 at 768, 81 / 75 at 1536; rank 128 62 / 65 at 272, 91 / 66 at 512. 1024 x 1024: rank 32 13.3 / 11.4 at 1024, rank 64 10.5 / 11.3
+//   at 512 and 15.9 / 11.5 at 768: fp32's border is too far out for small layers.
 constexpr int tile_rows(int max_rank) { return max_rank > 64 ? 256 : max_rank > 32 ? 768 : 1152; }
 // Whether calls of this kind of tile take a list: those of 16 rows and ranks above 64 have no more rows than need none, and in fp16 only the
 // launch for small items.

@@ -49,7 +49,7 @@ __device__ __forceinline__ void copy_wait() {
 
 // Elements at .. at + width - 1 of a base of `end` elements whose rows lie anywhere (at < 0: zeros): their 16-byte chunks, brought into
 // place. kWords * 4 bytes are worked on; what lies behind `width` is anything. (Element by element, and stored so too, 900 rows of
-// 4095 took 34 us instead of 18; rows at 16 bytes 14.)
+// 4095 took 34 us instead of 18; now 16, at a stride of 4096 13.)
 template <typename T, int kWords>
 __device__ __forceinline__ void loose_row(const T* base, int64_t at, int64_t end, int width, uint32_t (&y)[kWords]) {
   constexpr int kVec = 16 / sizeof(T), kChunks = kWords / 4 + 1;
@@ -101,7 +101,7 @@ __device__ __forceinline__ int row_power(float top) {
 }
 
 // A call's items, with `rest` but the first of each tile: those with more than `few` rows from the front of `list`, the others from
-// its back. One CTA, a warp a tile: 3 to 4 us, 7 where a tile of 128 rows has 63 adapters. The order within the two parts hangs on the warps' pace, and
+// its back. One CTA, a warp a tile: 1 to 3 us, 8 where a tile of 128 rows has 63 adapters. The order within the two parts hangs on the warps' pace, and
 // nothing hangs on the order.
 template <int TM>
 __global__ void __launch_bounds__(1024) list_kernel(const Lora a, int few, int rest, uint32_t* counts, Item* list, int capacity,

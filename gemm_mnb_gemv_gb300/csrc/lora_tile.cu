@@ -16,8 +16,8 @@
 // that this one leaves free. (A row alone takes a cluster 15 us here: 1500 rows of a prompt with 63 such rows 88 us.)
 // Every wait is bounded: a role whose wait gave up reports it and stops, the others run into their own limits, and the
 // rows left get NaN.
-// Bound: 8192 rows, K 4096, N 14336, rank 64: 106 us (80 at the copy rate), of which 15 go to the first product, 5 to the exchange and the rest
-// to the second product at 6.3 TB/s of reads and writes. 2048 rows, K = N = 4096, rank 32: 21 us (7.7): one item a cluster, so the chain of
+// Bound: 8192 rows, K 4096, N 14336, rank 64: 112 us (80 at the copy rate), of which 15 go to the first product, 6 to the exchange and 84
+// to the second product at 5.6 TB/s of reads and writes. 2048 rows, K = N = 4096, rank 32: 22.3 us (7.7): one item a cluster, so the chain of
 // start, first product, exchange and stages of 1.2 us of epilogue. 16 epilogue warps instead of 8 took 12 us more; waits that sleep changed nothing.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -753,7 +753,7 @@ cudaError_t launch_tile(LaunchCtx& ctx, const Lora& a) {
   int room[kMostCtas];
   for (int i = 0; i < kMostCtas; ++i) room[i] = clusters_held(ctx, kern, i + 1, kThreads, L::kBytes, known[i]);
   // A tile in which one prompt ends and the next begins is two items. (Where they are more than thought, a few clusters get two: 1784 rows of four
-  // prompts 27 us instead of 21.6 with clusters of 6, which take 21.6 for two prompts, too, instead of 18.8.)
+  // prompts 28.4 us instead of 22.3 with clusters of 6, which take 22.3 for two prompts, too, instead of 19.5.)
   const int tiles = (a.M + kRows - 1) / kRows;
   const int pick = tile_cluster(tiles + tiles / 8, room), cluster = pick + 1, clusters = room[pick] > 0 ? room[pick] : 1;
   const bool pdl = ctx.pdl;
