@@ -45,8 +45,8 @@ __device__ __noinline__ LooseRows<kWords> loose_rows(const T* base, int64_t at0,
 // Rows up to which each cluster finds its tile's adapters itself, in one launch. Beyond, a launch makes a list of all items but each tile's first.
 // On the GPU, without a list / with one: 64 rows of 64 adapters, 4096 x 4096, rank 16 9.7 / 11.0, 132 rows of them 22.9 / 17.3; fp32, four rows a
 // request, 896 x 1152, rank 8: 64 rows 6.5 / 7.5, 132 8.2 / 7.6, 256 10.0 / 8.0; 803 rows of three prompts and 8 more, 1680 x 192: 14.1 / 7.9. A
-// call without one has one launch and no workspace, 3 us less of host time: eager calls are even up to 256, replayed ones of more than 130 rows would
-// be faster with a list.
+// call without one has one launch and no workspace, 3 us less of host time, which eager calls of this size are bound by (18 us for 8 on the GPU); replayed
+// ones of more than 130 rows would be faster with a list.
 constexpr int kFewRows = 256;
 // Rows up to which tiles have 16 rows. More come in tiles of 64 (fp32) or 128 (fp16, the tcgen05 kernel), which read the weights that
 // much less often but fill the GPU later; a GPU holds 74 clusters, the tiles of 1184 rows. Four prompts, us in tiles of 16 / in the large ones:
